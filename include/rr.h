@@ -14,6 +14,9 @@
  *   rr_log_softmax_fwd, rr_softmax_bwd, rr_log_softmax_bwd   the softmax pair
  *   rr_rmsnorm_fwd, rr_rmsnorm_bwd                           RMSNorm
  *   rr_attention_fwd         causal scaled dot-product attention on the online softmax
+ *   rr_distill_fwd_bwd       distillation loss and dlogits from a teacher's top entries
+ *   rr_attention_tree_fwd    attention of a tree of new tokens over a paged cache
+ *   rr_draft_verify          acceptance of drafted tokens against the target
  *   rr_layernorm_bwd_noalloc the LayerNorm backward without a caller workspace
  *   rr_selftest_bounded_wait, rr_read_device_error   the bounded device waits
  *
@@ -299,6 +302,121 @@ rr_status rr_layernorm_bwd_noalloc(const void *dy, const void *x, const float *m
 rr_status rr_attention_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
                            int64_t bh, int64_t seq, int64_t head_dim, float scale, int causal,
                            rr_dtype dtype, cudaStream_t stream);
+
+/*
+ * Distillation from a teacher's top entries, forward and backward in one call
+ * (the cross-entropy's counterpart for soft labels given as a short list).
+ * With T = temperature, s = softmax(x / T) over the row's columns and the
+ * teacher's list (i_k, v_k), k < K:
+ *   tail = 0: t = softmax(v / T) over the list (v logits or log-probabilities);
+ *     loss = T^2 sum_k t_k (ln t_k - ln s_{i_k});
+ *   tail != 0: t_k = exp(v_k) (v log-probabilities at this temperature), and
+ *     the mass outside the list, tt = max(0, 1 - sum_k t_k), is matched with
+ *     the student's, st = the sum of s over the unlisted columns:
+ *     loss = T^2 [sum_k t_k (ln t_k - ln s_{i_k}) + tt (ln tt - ln st)];
+ *   dlogits_j = grad T [M s_j - sum_{k: i_k = j} t_k - (j unlisted) tt s_j / st],
+ *     M = sum_k t_k + tt (1 without a tail).
+ *   logits : [rows x cols] dtype.  top_index : [rows x k] int32, top_value :
+ *           [rows x k] float32, 0 <= k <= 1024 (k == 0: both may be NULL).
+ *   grad    : [rows] float32, the upstream gradient of the row's loss, or NULL (1).
+ *   loss    : [rows] float32.  dlogits : [rows x cols] dtype, may equal logits
+ *           (written in place); other overlap is an error.  NULL: loss only.
+ *   temperature : > 0 and finite.
+ *   bad_index_count : nullable device int32; each entry with index >= cols adds 1.
+ * An entry with a negative index, or one >= cols, is absent.  An entry listed
+ * twice counts with both values.  A value of -inf has weight 0 (with a tail its
+ * column still counts as listed).  A row with no entry present (without a tail:
+ * none of finite weight), or fully masked logits, gets loss 0 and dlogits 0.
+ * The tail term is left out of a row whose unlisted columns hold none of the
+ * student's mass (all below 2^-126 of its largest probability).
+ */
+rr_status rr_distill_fwd_bwd(const void *logits, const int32_t *top_index,
+                             const float *top_value, const float *grad, float *loss,
+                             void *dlogits, int64_t rows, int64_t cols, int64_t k,
+                             float temperature, int tail, int32_t *bad_index_count,
+                             rr_dtype dtype, cudaStream_t stream);
+
+/* Bytes of device workspace rr_attention_tree_fwd needs for these sizes; 0 if
+ * none, or if the arguments are invalid.  Depends on the current device. */
+size_t rr_attention_tree_workspace_size(int64_t batch, int64_t nodes, int64_t heads,
+                                        int64_t kv_heads, int64_t head_dim);
+
+/*
+ * Attention of new tokens over a paged cache: `nodes` tokens a sequence that
+ * form a tree (drafted tokens), a chain (a chunk of a prompt) or are one (plain
+ * decoding), with grouped heads.  The caller has written the keys and values of
+ * the new tokens to the cache: node j of sequence b is at position
+ * context_len[b] + j, and position p is row p % page_size of page
+ * page_table[b, p / page_size].  For node i and head h (key head
+ * h / (heads / kv_heads)), over the keys it sees -- every position below
+ * context_len[b], and of the nodes itself and its ancestors --
+ *   o = sum_j softmax(scale q . k)_j v_j,   lse = log sum_j exp(scale q . k_j).
+ *   q, o : [batch x nodes x heads x head_dim] bf16 (dtype must be RR_BF16).
+ *   k_cache, v_cache : [pages x page_size x kv_heads x head_dim] bf16, any
+ *           page_size >= 1; all four 16-byte aligned; a page size that is a
+ *           multiple of 16 takes the tensor-core path.
+ *   page_table : [batch x table_width] int32; only entries that cover
+ *           context_len[b] + nodes positions are read.  context_len : [batch]
+ *           int32 (negative counts as 0).
+ *   parents : [batch x nodes] int32, the node that each follows, -1 for the
+ *           root, a parent before its children; at most 256 nodes.  NULL: a chain
+ *           (node i follows i - 1).  A node whose chain of parents does not end
+ *           at -1 (an entry below -1, or not below the node) is absent: it sees
+ *           nothing.
+ *   lse : [batch x nodes x heads] float32, or NULL.
+ *   head_dim 64 or 128; heads a multiple of kv_heads; scale > 0 and finite.
+ *   workspace : device scratch of workspace_bytes >= the size query's answer
+ *           (16-byte aligned), owned by the caller; its contents on entry are
+ *           ignored.  Calls that may overlap on the GPU need one each.
+ * A row that sees nothing gets o = 0 and lse = -inf.  Positions beyond the
+ * table, or on a page outside [0, pages), are not seen.  What stands at unseen
+ * positions (NaN or infinities too) changes nothing.
+ */
+rr_status rr_attention_tree_fwd(const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *page_table, const int32_t *context_len,
+                                const int32_t *parents, void *o, float *lse, void *workspace,
+                                size_t workspace_bytes, int64_t batch, int64_t nodes,
+                                int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                int64_t pages, int64_t page_size, int64_t table_width,
+                                float scale, rr_dtype dtype, cudaStream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from
+ * given random numbers (speculative sampling, over a chain or a tree).  From
+ * the root, at the node reached so far (row 0 for the root, row i + 1 for node
+ * i): p = softmax(target row / T), q = softmax(draft row / T), from which the
+ * node's children were drawn.  The children are tried in the order of their
+ * index; with c = 0, W = 1 at first, child i with token x is accepted iff
+ *   uniform_i * W * q_x < p_x - c q_x;
+ * else c += W and W = sum_j max(p_j - c q_j, 0) (the residual distribution is
+ * max(p - c q, 0) / W).  An accepted child is the next node.  When none is
+ * accepted the walk ends with the token argmax_j max(p_j - c q_j, 0) / race_j,
+ * the lowest j at a tie (over p itself where W = 0): with exponential noise a
+ * draw from the residual.
+ *   target_logits : [batch x (nodes + 1) x cols] dtype.
+ *   draft_logits : [batch x nodes x cols] dtype; row r holds the distribution the
+ *           children of node r - 1 were drawn from.  nodes == 0: may be NULL, as
+ *           may tokens and uniform.
+ *   tokens : [batch x nodes] int32; a token outside [0, cols) marks an absent
+ *           node (never accepted, its siblings are tried as if it were not there).
+ *   parents : [batch x nodes] int32 as for rr_attention_tree_fwd, or NULL (a chain).
+ *   uniform : [batch x nodes] float32 in [0, 1).  race : [batch x cols] float32 > 0.
+ *   temperature : [batch] float32, or NULL (1).  <= 0: greedy, a child is
+ *           accepted iff it is the target's largest logit (the lowest index at a
+ *           tie), which is also the last token.
+ *   out_tokens : [batch x (nodes + 1)] int32, the accepted tokens, the last
+ *           token, then -1.  out_nodes : [batch x (nodes + 1)] int32, the nodes
+ *           of the accepted tokens, then -1.  out_count : [batch] int32, how many
+ *           were accepted.
+ * Rows of nodes that are not reached are not looked at.  A target row without a
+ * finite logit, or with a NaN or +inf one where it is softmaxed, ends the walk
+ * with the last token -1.
+ */
+rr_status rr_draft_verify(const void *target_logits, const void *draft_logits,
+                          const int32_t *tokens, const int32_t *parents, const float *uniform,
+                          const float *race, const float *temperature, int32_t *out_tokens,
+                          int32_t *out_nodes, int32_t *out_count, int64_t batch, int64_t nodes,
+                          int64_t cols, rr_dtype dtype, cudaStream_t stream);
 
 /*
  * Self-test of the bounded device-side waits (a diagnostic of this library;

@@ -1244,6 +1244,59 @@ rr_status check_shape(int64_t rows, int64_t cols, rr_dtype dt) {
   return RR_OK;
 }
 
+// ------------------------------------- the draft model's operators: launch ----
+
+rr_status distill_launch(rr::DistillParams p, rr_dtype dt, cudaStream_t stream) {
+  const rr::DistillKernel dk = rr::distill_kernel(dt);
+  const size_t smem = 128 + (size_t)p.k * 12 + p.filter_bits / 8;
+  int64_t grid = p.rows;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    DevInfo* di = nullptr;
+    rr_status st = device_info(&di);
+    if (st != RR_OK) return st;
+    p.err = di->err;
+    if (grid > (int64_t)di->sms * 8) grid = (int64_t)di->sms * 8;
+  }
+  void* args[] = {&p};
+  cudaError_t e = cudaLaunchKernel(dk.fn, dim3((unsigned)grid), dim3((unsigned)dk.threads), args,
+                                   smem, stream);
+  if (e != cudaSuccess) return fail(RR_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
+  const rr::VerifyKernel vk = rr::verify_kernel(dt);
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    DevInfo* di = nullptr;
+    rr_status st = device_info(&di);
+    if (st != RR_OK) return st;
+    p.err = di->err;
+  }
+  void* args[] = {&p};
+  cudaError_t e = cudaLaunchKernel(vk.fn, dim3((unsigned)p.batch), dim3((unsigned)vk.threads),
+                                   args, 0, stream);
+  if (e != cudaSuccess) return fail(RR_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+rr_status tree_launch(rr::TreeParams p, int d, cudaStream_t stream) {
+  const int64_t rows = p.batch * p.nodes * p.heads;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    DevInfo* di = nullptr;
+    rr_status st = device_info(&di);
+    if (st != RR_OK) return st;
+    p.err = di->err;
+  }
+  void* args[] = {&p};
+  cudaError_t e = cudaLaunchKernel(rr::tree_rows_kernel(d), dim3((unsigned)cdiv(rows, 4)),
+                                   dim3(128), args, 0, stream);
+  if (e != cudaSuccess) return fail(RR_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
 int* device_error_word() {
   std::lock_guard<std::mutex> lock(g_mu);
   DevInfo* di = nullptr;
@@ -1892,6 +1945,201 @@ rr_status rr_attention_fwd(const void* q, const void* k, const void* v, void* o,
     return fail(RR_ERR_CUDA, "attention: %s (%s)", why, cudaGetErrorString(e));
   }
   return ok();
+}
+
+// ---------------------------------------------------- the draft model ----
+
+rr_status rr_distill_fwd_bwd(const void* logits, const int32_t* top_index, const float* top_value,
+                             const float* grad, float* loss, void* dlogits, int64_t rows,
+                             int64_t cols, int64_t k, float temperature, int tail,
+                             int32_t* bad_index_count, rr_dtype dtype, cudaStream_t stream) {
+  rr_status st = check_shape(rows, cols, dtype);
+  if (st != RR_OK) return st;
+  if (k < 0 || k > 1024) return fail(RR_ERR_INVALID_ARG, "k=%lld outside 0..1024", (long long)k);
+  if (cols > INT32_MAX) return fail(RR_ERR_INVALID_ARG, "cols beyond an int32 index");
+  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature))
+    return fail(RR_ERR_INVALID_ARG, "temperature must be finite and > 0");
+  if (rows == 0) return ok();
+  if (rows > ((int64_t)1 << 50) / (k + 1)) return fail(RR_ERR_INVALID_ARG, "rows*k too large");
+  if (!logits || !loss || (k > 0 && (!top_index || !top_value)))
+    return fail(RR_ERR_INVALID_ARG, "null pointer");
+  const size_t E = dtype == RR_BF16 ? 2 : 4;
+  if (!aligned(logits, E) || !aligned(dlogits, E) || !aligned(top_index, 4) ||
+      !aligned(top_value, 4) || !aligned(grad, 4) || !aligned(loss, 4) ||
+      !aligned(bad_index_count, 4))
+    return fail(RR_ERR_INVALID_ARG, "misaligned pointer");
+  const size_t n = (size_t)rows * cols * E, nr = (size_t)rows * 4, nk = (size_t)rows * k * 4;
+  if (logits != dlogits && overlaps(logits, n, dlogits, n))
+    return fail(RR_ERR_ALIASING, "logits and dlogits partially overlap");
+  const std::pair<const void*, size_t> ins[] = {{top_index, nk}, {top_value, nk}, {grad, nr}};
+  for (const auto& in : ins)
+    if (overlaps(in.first, in.second, dlogits, n) || overlaps(in.first, in.second, loss, nr) ||
+        overlaps(in.first, in.second, bad_index_count, 4))
+      return fail(RR_ERR_ALIASING, "an output overlaps top_index, top_value or grad");
+  if (overlaps(loss, nr, logits, n) || overlaps(loss, nr, dlogits, n) ||
+      overlaps(bad_index_count, 4, logits, n) || overlaps(bad_index_count, 4, dlogits, n) ||
+      overlaps(bad_index_count, 4, loss, nr))
+    return fail(RR_ERR_ALIASING, "loss / bad_index_count overlap another tensor");
+  rr::DistillParams p{};
+  p.x = static_cast<const char*>(logits);
+  p.index = top_index;
+  p.value = top_value;
+  p.grad = grad;
+  p.loss = loss;
+  p.y = static_cast<char*>(dlogits);
+  p.bad = bad_index_count;
+  p.rows = rows;
+  p.cols = cols;
+  p.k = (int32_t)k;
+  p.tail = tail ? 1 : 0;
+  p.filter_bits = 32;
+  while (p.filter_bits < 65536 && p.filter_bits < cols) p.filter_bits *= 2;
+  p.temperature = temperature;
+  p.inv_t = 1.f / temperature;
+  p.c = 1.4426950408889634f / temperature;
+  return distill_launch(p, dtype, stream);
+}
+
+rr_status rr_draft_verify(const void* target_logits, const void* draft_logits,
+                          const int32_t* tokens, const int32_t* parents, const float* uniform,
+                          const float* race, const float* temperature, int32_t* out_tokens,
+                          int32_t* out_nodes, int32_t* out_count, int64_t batch, int64_t nodes,
+                          int64_t cols, rr_dtype dtype, cudaStream_t stream) {
+  rr_status st = check_shape(batch, cols, dtype);
+  if (st != RR_OK) return st;
+  if (nodes < 0 || nodes > 65535)
+    return fail(RR_ERR_INVALID_ARG, "nodes=%lld outside 0..65535", (long long)nodes);
+  if (cols > INT32_MAX) return fail(RR_ERR_INVALID_ARG, "cols beyond an int32 token");
+  if (batch > INT32_MAX || batch > ((int64_t)1 << 58) / (cols * (nodes + 1)))
+    return fail(RR_ERR_INVALID_ARG, "batch too large");
+  if (batch == 0) return ok();
+  if (!target_logits || !race || !out_tokens || !out_nodes || !out_count ||
+      (nodes > 0 && (!draft_logits || !tokens || !uniform)))
+    return fail(RR_ERR_INVALID_ARG, "null pointer");
+  const size_t E = dtype == RR_BF16 ? 2 : 4;
+  if (!aligned(target_logits, E) || !aligned(draft_logits, E) || !aligned(tokens, 4) ||
+      !aligned(parents, 4) || !aligned(uniform, 4) || !aligned(race, 4) ||
+      !aligned(temperature, 4) || !aligned(out_tokens, 4) || !aligned(out_nodes, 4) ||
+      !aligned(out_count, 4))
+    return fail(RR_ERR_INVALID_ARG, "misaligned pointer");
+  const size_t nb = (size_t)batch * 4, nn = (size_t)batch * nodes * 4,
+               no = (size_t)batch * (nodes + 1) * 4;
+  const std::pair<const void*, size_t> ins[] = {
+      {target_logits, (size_t)batch * (nodes + 1) * cols * E},
+      {draft_logits, (size_t)batch * nodes * cols * E},
+      {tokens, nn}, {parents, nn}, {uniform, nn},
+      {race, (size_t)batch * cols * 4}, {temperature, nb}};
+  for (const auto& in : ins)
+    if (overlaps(in.first, in.second, out_tokens, no) ||
+        overlaps(in.first, in.second, out_nodes, no) ||
+        overlaps(in.first, in.second, out_count, nb))
+      return fail(RR_ERR_ALIASING, "an output overlaps an input");
+  if (overlaps(out_tokens, no, out_nodes, no) || overlaps(out_tokens, no, out_count, nb) ||
+      overlaps(out_nodes, no, out_count, nb))
+    return fail(RR_ERR_ALIASING, "outputs overlap");
+  rr::VerifyParams p{};
+  p.target = static_cast<const char*>(target_logits);
+  p.draft = static_cast<const char*>(draft_logits);
+  p.tokens = tokens;
+  p.parents = parents;
+  p.uniform = uniform;
+  p.race = race;
+  p.temperature = temperature;
+  p.out_tokens = out_tokens;
+  p.out_nodes = out_nodes;
+  p.out_count = out_count;
+  p.batch = batch;
+  p.cols = cols;
+  p.nodes = (int32_t)nodes;
+  return verify_launch(p, dtype, stream);
+}
+
+// Shape checks of rr_attention_tree_fwd that its workspace size query shares.
+static rr_status tree_shape(int64_t batch, int64_t nodes, int64_t heads, int64_t kv_heads,
+                            int64_t head_dim) {
+  if (batch < 0 || nodes < 0) return fail(RR_ERR_INVALID_ARG, "negative size");
+  if (head_dim != 64 && head_dim != 128)
+    return fail(RR_ERR_INVALID_ARG, "head_dim must be 64 or 128");
+  if (heads < 1 || kv_heads < 1 || heads % kv_heads != 0)
+    return fail(RR_ERR_INVALID_ARG, "heads must be a positive multiple of kv_heads");
+  if (heads > 65535 || nodes > (1 << 20) || batch > (1 << 20) ||
+      batch * nodes > ((int64_t)1 << 31) / heads)
+    return fail(RR_ERR_INVALID_ARG, "too many query rows");
+  return RR_OK;
+}
+
+size_t rr_attention_tree_workspace_size(int64_t batch, int64_t nodes, int64_t heads,
+                                        int64_t kv_heads, int64_t head_dim) {
+  return tree_shape(batch, nodes, heads, kv_heads, head_dim) == RR_OK ? 0 : 0;
+}
+
+rr_status rr_attention_tree_fwd(const void* q, const void* k_cache, const void* v_cache,
+                                const int32_t* page_table, const int32_t* context_len,
+                                const int32_t* parents, void* o, float* lse, void* workspace,
+                                size_t workspace_bytes, int64_t batch, int64_t nodes,
+                                int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t pages,
+                                int64_t page_size, int64_t table_width, float scale,
+                                rr_dtype dtype, cudaStream_t stream) {
+  if (dtype != RR_BF16)
+    return fail(RR_ERR_UNSUPPORTED_DTYPE, "tree attention takes bf16 q and cache");
+  rr_status st = tree_shape(batch, nodes, heads, kv_heads, head_dim);
+  if (st != RR_OK) return st;
+  if (pages < 0 || page_size < 1 || table_width < 0 || pages > INT32_MAX ||
+      page_size > (1 << 24) || table_width > INT32_MAX / page_size)
+    return fail(RR_ERR_INVALID_ARG, "bad cache shape");
+  if (pages > ((int64_t)1 << 58) / (page_size * kv_heads * head_dim))
+    return fail(RR_ERR_INVALID_ARG, "cache too large");
+  if (parents && nodes > rr::kTreeMaxNodes)
+    return fail(RR_ERR_INVALID_ARG, "a tree holds at most %d nodes (a chain any number)",
+                rr::kTreeMaxNodes);
+  if (!(scale > 0.f) || !std::isfinite(scale))
+    return fail(RR_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (batch == 0 || nodes == 0) return ok();
+  if (!q || !o || !context_len || (pages > 0 && (!k_cache || !v_cache)) ||
+      (table_width > 0 && !page_table))
+    return fail(RR_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) ||
+      !aligned(workspace, 16))
+    return fail(RR_ERR_INVALID_ARG, "q, caches, o and workspace must be 16-byte aligned");
+  if (!aligned(page_table, 4) || !aligned(context_len, 4) || !aligned(parents, 4) ||
+      !aligned(lse, 4))
+    return fail(RR_ERR_INVALID_ARG, "misaligned pointer");
+  const size_t need = rr_attention_tree_workspace_size(batch, nodes, heads, kv_heads, head_dim);
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(RR_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", workspace_bytes,
+                need);
+  const size_t nq = (size_t)batch * nodes * heads * head_dim * 2, nl = nq / head_dim * 2,
+               nc = (size_t)pages * page_size * kv_heads * head_dim * 2;
+  const std::pair<const void*, size_t> ins[] = {
+      {q, nq}, {k_cache, nc}, {v_cache, nc},
+      {page_table, (size_t)batch * table_width * 4},
+      {context_len, (size_t)batch * 4}, {parents, (size_t)batch * nodes * 4}};
+  for (const auto& in : ins)
+    if (overlaps(in.first, in.second, o, nq) || overlaps(in.first, in.second, lse, nl) ||
+        overlaps(in.first, in.second, workspace, need))
+      return fail(RR_ERR_ALIASING, "an output or the workspace overlaps an input");
+  if (overlaps(o, nq, lse, nl) || overlaps(o, nq, workspace, need) ||
+      overlaps(lse, nl, workspace, need))
+    return fail(RR_ERR_ALIASING, "o, lse and the workspace overlap");
+  rr::TreeParams p{};
+  p.q = static_cast<const char*>(q);
+  p.k = static_cast<const char*>(k_cache);
+  p.v = static_cast<const char*>(v_cache);
+  p.table = page_table;
+  p.length = context_len;
+  p.parents = parents;
+  p.o = static_cast<char*>(o);
+  p.lse = lse;
+  p.ws = static_cast<float*>(workspace);
+  p.batch = batch;
+  p.pages = pages;
+  p.width = table_width;
+  p.nodes = (int32_t)nodes;
+  p.heads = (int32_t)heads;
+  p.kv_heads = (int32_t)kv_heads;
+  p.page = (int32_t)page_size;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  return tree_launch(p, (int)head_dim, stream);
 }
 
 }  // extern "C"

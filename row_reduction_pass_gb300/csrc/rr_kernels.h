@@ -198,6 +198,73 @@ AttnKernel attn_fwd_kernel_for(int d);
 // dimension d on stream (persistent: at most `sms` CTAs): null on success,
 // else a short reason (nothing launched, or the launch failed).
 const char* attn_fwd_launch(const AttnParams& p, int d, int sms, cudaStream_t stream);
+// Distillation from a teacher's top entries (k_distill.cu).
+struct DistillParams {
+  const char* x;         // [rows][cols] student logits
+  const int32_t* index;  // [rows][k] listed columns; negative: absent
+  const float* value;    // [rows][k] teacher logits, or log-probabilities (tail)
+  const float* grad;     // [rows] upstream gradient of the loss, or null (1)
+  float* loss;           // [rows]
+  char* y;               // [rows][cols] dlogits, or null (loss only)
+  int32_t* bad;          // counter of listed columns >= cols, or null
+  int* err;              // device error word (a bounded wait that gave up)
+  int64_t rows;
+  int64_t cols;
+  int32_t k;
+  int32_t tail;          // keep the mass outside the list as one bucket
+  uint32_t filter_bits;  // power of two >= 32
+  float temperature;
+  float inv_t;           // 1 / temperature
+  float c;               // log2 e / temperature
+};
+struct DistillKernel {
+  const void* fn;
+  int threads;
+};
+DistillKernel distill_kernel(int dtype);
+
+// Verification of drafted tokens (k_verify.cu).
+struct VerifyParams {
+  const char* target;        // [batch][nodes + 1][cols] logits
+  const char* draft;         // [batch][nodes][cols] logits
+  const int32_t* tokens;     // [batch][nodes]; outside [0, cols): absent
+  const int32_t* parents;    // [batch][nodes], or null (a chain)
+  const float* uniform;      // [batch][nodes]
+  const float* race;         // [batch][cols] exponential noise
+  const float* temperature;  // [batch], or null (1)
+  int32_t* out_tokens;       // [batch][nodes + 1]
+  int32_t* out_nodes;        // [batch][nodes + 1]
+  int32_t* out_count;        // [batch]
+  int* err;
+  int64_t batch;
+  int64_t cols;
+  int32_t nodes;
+};
+struct VerifyKernel {
+  const void* fn;
+  int threads;
+};
+VerifyKernel verify_kernel(int dtype);
+
+// Attention of a tree of new tokens over a paged cache (k_tree.cu): bf16.
+struct TreeParams {
+  const char* q;              // [batch][nodes][heads][d]
+  const char* k;              // [pages][page][kv_heads][d]
+  const char* v;
+  const int32_t* table;       // [batch][width] page of each page_size positions
+  const int32_t* length;      // [batch] keys before the tree
+  const int32_t* parents;     // [batch][nodes], or null (a chain)
+  char* o;                    // [batch][nodes][heads][d]
+  float* lse;                 // [batch][nodes][heads], or null
+  float* ws;                  // partial results of split sequences
+  int* err;
+  int64_t batch, pages, width;
+  int32_t nodes, heads, kv_heads, page;
+  float scale_log2;           // scale * log2 e
+};
+constexpr int kTreeMaxNodes = 256;  // with parents (one mask bit a node)
+const void* tree_rows_kernel(int d);
+
 // The column reduce's split of its 32 warps over the P partial rows: the
 // smallest power of two >= P / 16, at most 32 (the rest of the warps take
 // further columns), so each warp sums about 16 partials.  A block covers

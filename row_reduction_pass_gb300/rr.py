@@ -88,6 +88,17 @@ def load_library():
         lib.rr_attention_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ctypes.c_float,
                                          ctypes.c_int, st, vp]
         lib.rr_attention_fwd.restype = st
+        f32 = ctypes.c_float
+        lib.rr_distill_fwd_bwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, f32,
+                                           ctypes.c_int, vp, st, vp]
+        lib.rr_distill_fwd_bwd.restype = st
+        lib.rr_attention_tree_workspace_size.argtypes = [i64, i64, i64, i64, i64]
+        lib.rr_attention_tree_workspace_size.restype = ctypes.c_size_t
+        lib.rr_attention_tree_fwd.argtypes = [vp] * 9 + [ctypes.c_size_t] + [i64] * 8 + [f32, st,
+                                                                                        vp]
+        lib.rr_attention_tree_fwd.restype = st
+        lib.rr_draft_verify.argtypes = [vp] * 10 + [i64, i64, i64, st, vp]
+        lib.rr_draft_verify.restype = st
         _lib = lib
         return lib
 
@@ -257,6 +268,121 @@ def rr_rmsnorm_bwd(dy, x, rstd, gamma, dx, dgamma, workspace=None, stream=None):
     _check("rr_rmsnorm_bwd", load_library().rr_rmsnorm_bwd(
         _p(dy), _p(x), _p(rstd), _p(gamma), _p(dx), _p(dgamma), _p(workspace),
         workspace.numel() * workspace.element_size(), rows, cols, _dtype(x), _stream(stream)))
+
+
+def _args(fn, *ts):
+    """Checks (name, tensor, dtype or None, shape) tuples of one call: contiguous
+    CUDA tensors of that dtype and shape on the current device (a None tensor,
+    an absent argument, passes)."""
+    import torch
+    for name, t, dtype, shape in ts:
+        if t is None:
+            continue
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous")
+    for name, t, _, _ in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{fn}: {name} must be a CUDA tensor")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{fn}: {name} is on {t.device}, not on the current device")
+
+
+def rr_distill_fwd_bwd(logits, top_index, top_value, loss, dlogits=None, grad=None,
+                       temperature=1.0, tail=False, bad_index_count=None, stream=None):
+    """Distillation loss (fp32 [rows]) and dlogits from a teacher's top entries
+    (top_index int32, top_value fp32, [rows, k]); tail keeps the teacher's mass
+    outside the list (top_value then holds log-probabilities).  dlogits may be
+    logits, or None for the loss alone; grad [rows] scales dlogits."""
+    import torch
+    rows, cols = logits.shape
+    k = top_index.shape[1]
+    _args("rr_distill_fwd_bwd", ("logits", logits, None, (rows, cols)),
+          ("top_index", top_index, torch.int32, (rows, k)),
+          ("top_value", top_value, torch.float32, (rows, k)),
+          ("loss", loss, torch.float32, (rows,)), ("dlogits", dlogits, logits.dtype, (rows, cols)),
+          ("grad", grad, torch.float32, (rows,)),
+          ("bad_index_count", bad_index_count, torch.int32,
+           () if bad_index_count is None else bad_index_count.shape))
+    if bad_index_count is not None and bad_index_count.numel() != 1:
+        raise ValueError("rr_distill_fwd_bwd: bad_index_count must hold one value")
+    _check("rr_distill_fwd_bwd", load_library().rr_distill_fwd_bwd(
+        _p(logits), _p(top_index), _p(top_value), _p(grad), _p(loss), _p(dlogits), rows, cols, k,
+        ctypes.c_float(temperature), 1 if tail else 0, _p(bad_index_count), _dtype(logits),
+        _stream(stream)))
+
+
+def rr_attention_tree_workspace_size(batch: int, nodes: int, heads: int, kv_heads: int,
+                                     head_dim: int) -> int:
+    return int(load_library().rr_attention_tree_workspace_size(batch, nodes, heads, kv_heads,
+                                                               head_dim))
+
+
+def rr_attention_tree_fwd(q, k_cache, v_cache, page_table, context_len, o, lse=None, parents=None,
+                          scale=None, workspace=None, stream=None):
+    """Attention of the new tokens q [batch, nodes, heads, head_dim] (bf16) over
+    a paged cache [pages, page_size, kv_heads, head_dim] that already holds their
+    keys and values: node j of sequence b at position context_len[b] + j, position
+    p on page page_table[b, p // page_size].  parents [batch, nodes] makes them a
+    tree (None: a chain, node i sees the nodes up to i); lse (fp32) is optional;
+    scale defaults to 1 / sqrt(head_dim).
+
+    ``workspace`` is a uint8 CUDA tensor of at least
+    ``rr_attention_tree_workspace_size`` bytes; it is allocated here if omitted."""
+    import torch
+    b, n, h, d = q.shape
+    pages, page_size, kv, _ = k_cache.shape
+    width = page_table.shape[1]
+    i32 = torch.int32
+    fn = "rr_attention_tree_fwd"
+    _args(fn, ("q", q, None, (b, n, h, d)), ("k_cache", k_cache, q.dtype, (pages, page_size, kv, d)),
+          ("v_cache", v_cache, q.dtype, (pages, page_size, kv, d)),
+          ("page_table", page_table, i32, (b, width)), ("context_len", context_len, i32, (b,)),
+          ("o", o, q.dtype, (b, n, h, d)), ("lse", lse, torch.float32, (b, n, h)),
+          ("parents", parents, i32, (b, n)))
+    need = rr_attention_tree_workspace_size(b, n, h, kv, d)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    size = 0
+    if workspace is not None:
+        _args(fn, ("workspace", workspace, None, workspace.shape))
+        size = workspace.numel() * workspace.element_size()
+    if scale is None:
+        scale = 1.0 / float(d) ** 0.5
+    _check(fn, load_library().rr_attention_tree_fwd(
+        _p(q), _p(k_cache), _p(v_cache), _p(page_table), _p(context_len), _p(parents), _p(o),
+        _p(lse), _p(workspace), size, b, n, h, kv, d, pages, page_size, width,
+        ctypes.c_float(scale), _dtype(q), _stream(stream)))
+
+
+def rr_draft_verify(target_logits, draft_logits, tokens, uniform, race, out_tokens, out_nodes,
+                    out_count, parents=None, temperature=None, stream=None):
+    """Accepts drafted tokens against the target's probabilities, along the
+    chain or tree they form, and draws the token that follows them.
+
+    target_logits [batch, nodes + 1, cols], draft_logits [batch, nodes, cols],
+    tokens / parents (int32) and uniform (fp32) [batch, nodes], race [batch, cols]
+    exponential noise, temperature [batch] (<= 0: greedy).  Writes out_tokens and
+    out_nodes [batch, nodes + 1] and out_count [batch] (int32)."""
+    import torch
+    b, n1, v = target_logits.shape
+    n = n1 - 1
+    i32, f32 = torch.int32, torch.float32
+    _args("rr_draft_verify", ("target_logits", target_logits, None, (b, n1, v)),
+          ("draft_logits", draft_logits, target_logits.dtype, (b, n, v)),
+          ("tokens", tokens, i32, (b, n)), ("parents", parents, i32, (b, n)),
+          ("uniform", uniform, f32, (b, n)), ("race", race, f32, (b, v)),
+          ("temperature", temperature, f32, (b,)), ("out_tokens", out_tokens, i32, (b, n1)),
+          ("out_nodes", out_nodes, i32, (b, n1)), ("out_count", out_count, i32, (b,)))
+    _check("rr_draft_verify", load_library().rr_draft_verify(
+        _p(target_logits), _p(draft_logits), _p(tokens), _p(parents), _p(uniform), _p(race),
+        _p(temperature), _p(out_tokens), _p(out_nodes), _p(out_count), b, n, v,
+        _dtype(target_logits), _stream(stream)))
 
 
 def rr_read_device_error(device: int = 0, reset: bool = True) -> int:
