@@ -52,7 +52,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 template <int DT>
 __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParams p) {
   constexpr int E = DType<DT>::E;
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(128) unsigned char smem[];
   float* red = reinterpret_cast<float*>(smem);
   float* tval = red + 32;                                  // teacher values, then t_k
   float* tx = tval + p.k;                                  // the student's logits there
@@ -185,12 +185,438 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
   }
 }
 
+
+// ------------------------------------------------------- rows in registers ---
+//
+// One block (or a cluster of K blocks, each with a slice of S 16-byte chunks)
+// per row at a time, grid-stride over the rows; x and y share their address
+// modulo 16, so a chunk of one is a chunk of the other whatever the row's
+// alignment.  The block's last warp, the list warp, is set apart from the rest,
+// the row warps:
+//   list warp, per row j: waits until the row warps have published row j's
+//     statistics (their chunks are then in registers), refills the buffer of
+//     row j with row j + 2 (one bulk copy), finishes row j - 1's listed columns,
+//     writes row j's loss, and prepares row j + 2's list.
+//   row warp, per row j: waits for the row and its list, takes its chunks into
+//     registers, publishes the warp's maximum and sums to every block of the
+//     cluster, merges all the warps' when they are there, stores its chunks of
+//     dlogits.
+// So a block meets once a row (an mbarrier of the published statistics), the
+// two latencies of a list (its entries, then the student's logits there) are a
+// row ahead of their use, and two rows are in flight while one is worked on.
+// Listed columns are stored by the list warp one row later, when every row warp
+// has passed its chunk stores.
+//
+// Bits of the listed columns of a slice, by place in the slice, tell the row
+// warps which lanes of a chunk to leave out of Zt (a byte or half a byte a
+// chunk, nearly always 0), and the list warp whether a column came twice.
+struct __align__(16) DistHead {
+  float g;     // upstream gradient times T
+  float st;    // sum of t_k
+  int live;    // some entry has weight
+  int dup;     // a column of this slice may be listed twice
+};
+struct __align__(16) DistEntry {
+  float t, lt, x;
+  int j;
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  return v;
+}
+
+// The lanes of a chunk outside bytes [lo, hi) become -inf.
+template <int DT>
+__device__ __forceinline__ void dist_mask(uint4& c, int lo, int hi) {
+  constexpr int E = DType<DT>::E;
+#pragma unroll
+  for (int e = 0; e < DType<DT>::V; ++e)
+    if (e * E < lo || e * E >= hi) chunk_set_bits<DT>(c, e, DT == kBF16 ? 0xff80u : 0xff800000u);
+}
+
+template <int DT, bool TAIL, bool CL>
+__global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillParams p,
+                                                                const DistillGeo g) {
+  constexpr int E = DType<DT>::E, W = DType<DT>::V, NQ = kDistNQ;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int nw = (int)(blockDim.x >> 5) - 1;  // row warps
+  const int G = nw * 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int K = 1, rank = 0;
+  if constexpr (CL) {
+    K = (int)cluster_nrank();
+    rank = (int)cluster_rank();
+  }
+  const int64_t owner = blockIdx.x / K, owners = gridDim.x / K;
+  const int k = p.k;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);  // [2] the row has landed
+  uint64_t* mrg = full + 2;                            // [2] statistics published
+  uint64_t* ready = full + 4;                          // [2] the list is prepared
+  DistHead* heads = reinterpret_cast<DistHead*>(smem + 64);      // [4]
+  float4* slots = reinterpret_cast<float4*>(smem + 128);         // [2][K * nw]
+  DistEntry* lists = reinterpret_cast<DistEntry*>(smem + g.list_off);  // [4][k]
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + g.bits_off);     // [2][words]
+  const int nslot = K * nw;
+  const int64_t rowb = p.cols * E;
+  const int k0 = rank * g.S;
+  auto row_addr = [&](int64_t r) { return reinterpret_cast<uintptr_t>(p.x) + r * rowb; };
+  // chunks of this rank's slice of a row that starts h bytes into its first chunk
+  auto chunks = [&](int h) {
+    const int n = (int)((h + rowb + 15) >> 4) - k0;
+    return n < g.S ? n : g.S;
+  };
+  auto row_of = [&](int64_t j) { return owner + j * owners; };
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&mrg[i], nslot);
+      mbar_init(&ready[i], 1);
+    }
+    fence_mbar_init();
+  }
+  for (int i = tid; i < 2 * g.words; i += blockDim.x) bits[i] = 0;
+  if constexpr (CL) cluster_sync();  // peers arrive on this block's barriers
+  else __syncthreads();
+
+  bool dead = false;  // a wait gave up: later waits are skipped (the kernel still ends)
+  // row j's statistics, the same bits in every warp of every rank
+  auto merged = [&](int64_t j, float& M, float& d, float& dt) {
+    const int par = (int)(j & 1);
+    const uint32_t ph = (uint32_t)((j >> 1) & 1);
+    if (!dead) {
+      if constexpr (CL) dead = !mbar_wait_bounded_cluster(&mrg[par], ph, p.err);
+      else dead = !mbar_wait_bounded(&mrg[par], ph, p.err);
+    }
+    const float4* sl = slots + par * nslot;
+    M = -INFINITY;
+    for (int i = lane; i < nslot; i += 32) M = fmaxf(M, sl[i].x);
+    M = warp_max(M);
+    d = dt = 0.f;
+    for (int i = lane; i < nslot; i += 32) {
+      const float4 t = sl[i];
+      const float a = t.x == -INFINITY ? 0.f : ex2((t.x - M) * p.c);
+      d += t.y * a;
+      if (TAIL) dt += t.z * a;
+    }
+    d = warp_sum(d);
+    if (TAIL) dt = warp_sum(dt);
+  };
+  // the teacher's mass outside the list, and the weight of the student's softmax
+  auto masses = [&](const DistHead& hd, float dt, float& mass, float& tt) {
+    mass = 1.f;
+    tt = 0.f;
+    if (TAIL) {
+      if (dt > 0.f) tt = fmaxf(1.f - hd.st, 0.f);
+      mass = hd.st + tt;
+    }
+  };
+
+  if (warp == nw) {
+    // ------------------------------------------------------- the list warp
+    const uint64_t policy = policy_evict_first();
+    auto load_row = [&](int64_t j) {
+      if (row_of(j) >= p.rows || dead) return;
+      const uintptr_t a = row_addr(row_of(j));
+      const uint32_t bytes = (uint32_t)chunks((int)(a & 15)) * 16u;
+      mbar_arrive_expect_tx(&full[j & 1], bytes);
+      bulk_load(smem + g.buf_off + (j & 1) * g.S * 16,
+                reinterpret_cast<const void*>((a & ~uintptr_t(15)) + (int64_t)k0 * 16), bytes,
+                &full[j & 1], policy);
+    };
+    // the place of column c in the slice (row start h bytes into its chunk), or -1
+    auto place = [&](int c, int h) {
+      const int64_t e = (int64_t)c + h / E - (int64_t)k0 * W;
+      return e >= 0 && e < (int64_t)g.S * W ? (int)e : -1;
+    };
+    auto prepare = [&](int64_t j) {
+      const int64_t r = row_of(j);
+      if (r >= p.rows) return;
+      const int h = (int)(row_addr(r) & 15);
+      const char* x = p.x + r * rowb;
+      DistEntry* li = lists + (j & 3) * k;
+      uint32_t* bm = bits + (j & 1) * g.words;
+      float vm = -INFINITY;
+      int any = 0, dup = 0;
+#pragma unroll 4
+      for (int i = lane; i < k; i += 32) {
+        int c = __ldg(p.index + r * k + i);
+        const float v = __ldg(p.value + r * k + i);
+        const bool beyond = c >= p.cols;
+        if (beyond) c = -1;
+        if (beyond && rank == 0 && p.bad != nullptr) atomicAdd(p.bad, 1);
+        const float xv = c >= 0 ? ld_elem<DT>(x + (int64_t)c * E) : 0.f;
+        li[i] = DistEntry{0.f, v, xv, c};
+        if (c >= 0) {
+          any = 1;
+          vm = fmaxf(vm, v);
+        }
+      }
+      any = __any_sync(0xffffffffu, any);
+      vm = warp_max(vm);
+      float lnt = 0.f;
+      if (!TAIL) {
+        float z = 0.f;
+        for (int i = lane; i < k; i += 32)
+          if (li[i].j >= 0) z += expf((li[i].lt - vm) / p.temperature);
+        lnt = logf(warp_sum(z));
+      }
+      float st = 0.f;
+      for (int i = lane; i < k; i += 32) {
+        const int c = li[i].j;
+        if (c < 0) continue;
+        const float lt = TAIL ? li[i].lt : (li[i].lt - vm) / p.temperature - lnt;
+        const float t = expf(lt);
+        li[i].lt = lt;
+        li[i].t = t;
+        st += t;
+        const int e = place(c, h);
+        if (e >= 0 && ((atomicOr(&bm[e >> 5], 1u << (e & 31)) >> (e & 31)) & 1)) dup = 1;
+      }
+      st = warp_sum(st);
+      dup = __any_sync(0xffffffffu, dup);
+      if (lane == 0)
+        heads[j & 3] = DistHead{p.temperature * (p.grad != nullptr ? __ldg(p.grad + r) : 1.f), st,
+                                any && (TAIL || vm != -INFINITY), dup};
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ready[j & 1]);
+    };
+    auto clear_bits = [&](int64_t j) {
+      const int h = (int)(row_addr(row_of(j)) & 15);
+      const DistEntry* li = lists + (j & 3) * k;
+      uint32_t* bm = bits + (j & 1) * g.words;
+      for (int i = lane; i < k; i += 32) {
+        const int e = li[i].j < 0 ? -1 : place(li[i].j, h);
+        if (e >= 0) bm[e >> 5] = 0;
+      }
+      __syncwarp();
+    };
+    // dlogits at row j's listed columns of this slice
+    auto finish = [&](int64_t j, float M, float d, float dt) {
+      const int64_t r = row_of(j);
+      const DistHead hd = heads[j & 3];
+      if (p.y == nullptr || !hd.live || M == -INFINITY) return;
+      const int h = (int)(row_addr(r) & 15);
+      const DistEntry* li = lists + (j & 3) * k;
+      float mass, tt;
+      masses(hd, dt, mass, tt);
+      const float A = hd.g * (mass / d), mL = M * p.c, res = ex2(-fmaf(M, p.c, -mL));
+      for (int i = lane; i < k; i += 32) {
+        const DistEntry en = li[i];
+        if (en.j < 0 || place(en.j, h) < 0) continue;
+        float t = en.t;
+        if (hd.dup) {
+          bool first = true;
+          for (int n = 0; n < i; ++n) first = first && li[n].j != en.j;
+          if (!first) continue;
+          for (int n = i + 1; n < k; ++n) t += li[n].j == en.j ? li[n].t : 0.f;
+        }
+        st_elem<DT>(p.y + r * rowb + (int64_t)en.j * E,
+                    ex2(fmaf(en.x, p.c, -mL)) * res * A - hd.g * t);
+      }
+    };
+    if (lane == 0) {
+      load_row(0);
+      load_row(1);
+    }
+    prepare(0);
+    prepare(1);
+    float Mp = 0.f, dp = 0.f, dtp = 0.f;
+    int64_t j = 0;
+    for (; row_of(j) < p.rows; ++j) {
+      float M, d, dt;
+      merged(j, M, d, dt);
+      if (lane == 0) load_row(j + 2);
+      if (j > 0) finish(j - 1, Mp, dp, dtp);
+      if (rank == 0) {
+        const DistHead hd = heads[j & 3];
+        float l = 0.f;
+        if (hd.live && M != -INFINITY) {
+          const DistEntry* li = lists + (j & 3) * k;
+          // ln Z in two parts, hi of a few bits: the terms below are then small
+          // differences, and ln Z brings no rounding of its own size
+          const int ez = (__float_as_int(d) >> 23) - 127;
+          const float hi = ez * 0.6875f;
+          const float lo = fmaf((float)ez, 0.00564718056f,
+                                logf(__int_as_float(__float_as_int(d) - (ez << 23))));
+          for (int i = lane; i < k; i += 32) {
+            const DistEntry en = li[i];
+            if (en.j >= 0 && !(en.t <= 0.f)) l += en.t * ((en.lt + hi) - (en.x - M) / p.temperature);
+          }
+          l = warp_sum(l);
+          float mass, tt;
+          masses(hd, dt, mass, tt);
+          l += lo * (TAIL ? hd.st : 1.f);
+          if (tt > 0.f) l += tt * (logf(tt) - logf(dt / d));
+          l *= p.temperature * p.temperature;
+          if (d != d) l = d;
+        }
+        if (lane == 0) p.loss[row_of(j)] = l;
+      }
+      clear_bits(j);
+      prepare(j + 2);
+      Mp = M;
+      dp = d;
+      dtp = dt;
+    }
+    if (dead && lane == 0)  // copies of this block still in flight end before it does
+      for (int i = 0; i < 2; ++i) mbar_wait_bounded(&full[i], 0, p.err);
+    __syncthreads();
+    if (j > 0) finish(j - 1, Mp, dp, dtp);
+  } else {
+    // ------------------------------------------------------- the row warps
+    for (int64_t j = 0; row_of(j) < p.rows; ++j) {
+      const int64_t r = row_of(j);
+      const uintptr_t a = row_addr(r);
+      const int h = (int)(a & 15);
+      const int n = chunks(h);
+      const int last = (int)((h + rowb + 15) >> 4) - 1 - k0;  // place of the row's last chunk
+      const int tail_bytes = (int)(h + rowb - 16 * ((h + rowb + 15) / 16 - 1));
+      const uint32_t ph = (uint32_t)((j >> 1) & 1);
+      const uint4* buf = reinterpret_cast<const uint4*>(smem + g.buf_off + (j & 1) * g.S * 16);
+      const unsigned char* bm = reinterpret_cast<const unsigned char*>(bits + (j & 1) * g.words);
+      if (!dead) dead = !mbar_wait_bounded(&full[j & 1], ph, p.err);
+      uint4 v[NQ];
+      float m = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const int c = tid + q * G;
+        if (c >= n) break;
+        v[q] = buf[c];
+        if ((c == 0 && rank == 0 && h != 0) || c == last)
+          dist_mask<DT>(v[q], c == 0 && rank == 0 ? h : 0, c == last ? tail_bytes : 16);
+        if constexpr (DT == kBF16) {
+          const uint32_t w = bf16x2_max(bf16x2_max(v[q].x, v[q].y), bf16x2_max(v[q].z, v[q].w));
+          m = fmaxf(m, fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
+        } else {
+          m = fmaxf(fmaxf(m, fmaxf(__uint_as_float(v[q].x), __uint_as_float(v[q].y))),
+                    fmaxf(__uint_as_float(v[q].z), __uint_as_float(v[q].w)));
+        }
+      }
+      if (!dead) dead = !mbar_wait_bounded(&ready[j & 1], ph, p.err);
+      // sums of 2^(x c - fl(m c)), without and (dl) of the listed columns
+      float d = 0.f, dl = 0.f;
+      if (m != -INFINITY) {
+        const float mL = m * p.c;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          const int c = tid + q * G;
+          if (c >= n) break;
+          float e[W];
+#pragma unroll
+          for (int i = 0; i < W; i += 2) {
+            float t0, t1;
+            fma2(t0, t1, chunk_get<DT>(v[q], i), chunk_get<DT>(v[q], i + 1), p.c, p.c, -mL, -mL);
+            e[i] = ex2(t0);
+            e[i + 1] = ex2(t1);
+          }
+          if (TAIL) {
+            uint32_t b = bm[W == 8 ? c : c >> 1];
+            if (W == 4) b = (c & 1) ? b >> 4 : b & 15u;
+            if (b != 0) {
+#pragma unroll
+              for (int i = 0; i < W; ++i)
+                if ((b >> i) & 1) {
+                  dl += e[i];
+                  e[i] = 0.f;
+                }
+            }
+          }
+          if constexpr (W == 8) d += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+          else d += (e[0] + e[1]) + (e[2] + e[3]);
+        }
+        const float s = ex2(-fmaf(m, p.c, -mL));
+        d *= s;
+        dl *= s;
+      }
+      {
+        const float M = warp_max(m);
+        const float s = m == -INFINITY ? 0.f : ex2((m - M) * p.c);
+        d = warp_sum(m == -INFINITY ? 0.f : d * s);
+        if (TAIL) dl = warp_sum(m == -INFINITY ? 0.f : dl * s);
+        if (lane == 0) {
+          float4* sl = slots + (j & 1) * nslot + rank * nw + warp;
+          if constexpr (CL) {
+            for (int t = 0; t < K; ++t) {
+              st_cluster_f32x4(map_to_rank(sl, t), M, d + dl, d, 0.f);
+              mbar_arrive_cluster(map_to_rank(&mrg[j & 1], t));
+            }
+          } else {
+            *sl = make_float4(M, d + dl, d, 0.f);
+            mbar_arrive(&mrg[j & 1]);
+          }
+        }
+      }
+      float M, dt;
+      merged(j, M, d, dt);
+      if (p.y == nullptr) continue;
+      char* y = p.y + r * rowb - h + (int64_t)k0 * 16;
+      const DistHead hd = heads[j & 3];
+      float f = 0.f, mL = 0.f;
+      const bool zero = !hd.live || M == -INFINITY;
+      if (!zero) {
+        float mass, tt;
+        masses(hd, dt, mass, tt);
+        mL = M * p.c;
+        f = (hd.g * (mass / d) - (tt > 0.f ? hd.g * (tt / dt) : 0.f)) * ex2(-fmaf(M, p.c, -mL));
+      }
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const int c = tid + q * G;
+        if (c >= n) break;
+        float e[W];
+#pragma unroll
+        for (int i = 0; i < W; i += 2) {
+          float t0, t1;
+          fma2(t0, t1, chunk_get<DT>(v[q], i), chunk_get<DT>(v[q], i + 1), p.c, p.c, -mL, -mL);
+          mul2(e[i], e[i + 1], ex2(t0), ex2(t1), f, f);
+        }
+        if (zero) {
+#pragma unroll
+          for (int i = 0; i < W; ++i) e[i] = 0.f;
+        }
+        char* at = y + (int64_t)c * 16;
+        if ((c == 0 && rank == 0 && h != 0) || (c == last && tail_bytes != 16)) {
+          const int lo = c == 0 && rank == 0 ? h : 0, hi = c == last ? tail_bytes : 16;
+#pragma unroll
+          for (int i = 0; i < W; ++i)
+            if (i * E >= lo && i * E < hi) st_elem<DT>(at + i * E, e[i]);
+        } else {
+          st_chunk_stream(at, chunk_pack<DT>(e));
+        }
+      }
+    }
+    __syncthreads();  // every chunk stored: the list warp finishes the last row
+  }
+  if constexpr (CL) cluster_sync();  // no peer still writes this block's slots
+}
+
 }  // namespace
 
-DistillKernel distill_kernel(int dtype) {
-  return {dtype == kBF16 ? (const void*)distill_rows_kernel<kBF16>
-                         : (const void*)distill_rows_kernel<kF32>,
-          kDistT};
+DistillKernels distill_kernels(int dtype, bool tail) {
+  DistillKernels d{};
+  if (dtype == kBF16) {
+    d.rows = (const void*)distill_rows_kernel<kBF16>;
+    d.stream[0] = tail ? (const void*)distill_stream_kernel<kBF16, true, false>
+                       : (const void*)distill_stream_kernel<kBF16, false, false>;
+    d.stream[1] = tail ? (const void*)distill_stream_kernel<kBF16, true, true>
+                       : (const void*)distill_stream_kernel<kBF16, false, true>;
+  } else {
+    d.rows = (const void*)distill_rows_kernel<kF32>;
+    d.stream[0] = tail ? (const void*)distill_stream_kernel<kF32, true, false>
+                       : (const void*)distill_stream_kernel<kF32, false, false>;
+    d.stream[1] = tail ? (const void*)distill_stream_kernel<kF32, true, true>
+                       : (const void*)distill_stream_kernel<kF32, false, true>;
+  }
+  d.rows_threads = kDistT;
+  return d;
 }
 
 }  // namespace rr

@@ -1246,9 +1246,94 @@ rr_status check_shape(int64_t rows, int64_t cols, rr_dtype dt) {
 
 // ------------------------------------- the draft model's operators: launch ----
 
+// The streaming kernel's launch: row threads for at most kDistNQ chunks each,
+// rounded up to whole warps, plus the list warp; a cluster of K blocks where one
+// block cannot hold the row twice, or where splitting rows over more SMs ends
+// earlier (few rows).  The cost of a shape is its rounds of rows times a row's
+// share of a block (chunks, plus 1024 for what a row costs whatever its length:
+// the statistics' meeting and, in a cluster, its distance).  False where no
+// shape holds the row.
+struct DistillShape {
+  int K = 0, T = 0;
+  int64_t grid = 0;
+  size_t smem = 0;
+  rr::DistillGeo geo{};
+};
+static rr_status distill_shape(const rr::DistillKernels& dk, const rr::DistillParams& p,
+                               rr_dtype dt, DevInfo* di, DistillShape* best) {
+  const int E = dt == RR_BF16 ? 2 : 4, W = 16 / E;
+  const int64_t rowb = p.cols * E;
+  const int64_t nch_min = cdiv(rowb, 16), nch_max = cdiv(rowb + 15, 16);
+  double best_cost = 0;
+  for (int K = 1; K <= 8; ++K) {
+    const int64_t S = cdiv(nch_max, K);
+    if (K > 1 && (K - 1) * S >= nch_min) break;  // every rank gets chunks
+    const int64_t nw = std::max<int64_t>(3, cdiv(cdiv(S, rr::kDistNQ), 32));
+    if (nw > 31) continue;
+    DistillShape sh;
+    sh.K = K;
+    sh.T = (int)(nw + 1) * 32;
+    sh.geo.S = (int32_t)S;
+    sh.geo.words = (int32_t)cdiv(S * W, 32);
+    const int64_t list = round_up(128 + 2 * 16 * K * nw, 16);
+    const int64_t bits = list + 4 * 16 * (int64_t)p.k;
+    const int64_t buf = round_up(bits + 8 * (int64_t)sh.geo.words, 128);
+    const int64_t smem = buf + 2 * S * 16;
+    if (smem > di->smem_optin) continue;
+    sh.geo.list_off = (int32_t)list;
+    sh.geo.bits_off = (int32_t)bits;
+    sh.geo.buf_off = (int32_t)buf;
+    sh.smem = (size_t)smem;
+    const void* fn = dk.stream[K > 1];
+    rr_status st = set_smem(di, fn, sh.smem);
+    if (st != RR_OK) return st;
+    int64_t owners = 0;
+    if (K == 1) {
+      int& occ = di->occ[{fn, ((long long)sh.T << 32) | (long long)smem}];
+      if (occ == 0) {
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, sh.T, sh.smem);
+        if (e != cudaSuccess || occ <= 0)
+          return fail(RR_ERR_CUDA, "occupancy query: %s", cudaGetErrorString(e));
+      }
+      owners = (int64_t)di->sms * occ;
+    } else {
+      int& ncl = di->ncl[{fn, ((long long)K << 32) | (long long)smem | ((long long)sh.T << 48)}];
+      if (ncl == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = K;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3((unsigned)(K * di->sms));
+        cfg.blockDim = dim3((unsigned)sh.T);
+        cfg.dynamicSmemBytes = sh.smem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        cudaError_t e = cudaOccupancyMaxActiveClusters(&ncl, fn, &cfg);
+        if (e != cudaSuccess)
+          return fail(RR_ERR_CUDA, "cluster occupancy query (K=%d): %s", K, cudaGetErrorString(e));
+        if (ncl <= 0) ncl = -1;
+      }
+      if (ncl <= 0) continue;
+      owners = ncl;
+    }
+    owners = std::min(owners, p.rows);
+    // blocks of one SM share its bandwidth
+    const double per_sm = std::max(1.0, (double)owners * K / di->sms);
+    const double cost = (double)cdiv(p.rows, owners) * (S * per_sm + (K > 1 ? 1536 : 1024));
+    if (best->K == 0 || cost < best_cost) {
+      best_cost = cost;
+      sh.grid = owners * K;
+      *best = sh;
+    }
+  }
+  return RR_OK;
+}
+
 rr_status distill_launch(rr::DistillParams p, rr_dtype dt, cudaStream_t stream) {
-  const rr::DistillKernel dk = rr::distill_kernel(dt);
-  const size_t smem = 128 + (size_t)p.k * 12 + p.filter_bits / 8;
+  const rr::DistillKernels dk = rr::distill_kernels(dt, p.tail != 0);
+  DistillShape sh;
   int64_t grid = p.rows;
   {
     std::lock_guard<std::mutex> lock(g_mu);
@@ -1256,11 +1341,33 @@ rr_status distill_launch(rr::DistillParams p, rr_dtype dt, cudaStream_t stream) 
     rr_status st = device_info(&di);
     if (st != RR_OK) return st;
     p.err = di->err;
+    if (p.y == nullptr || ((reinterpret_cast<uintptr_t>(p.x) ^ reinterpret_cast<uintptr_t>(p.y)) &
+                           15) == 0)
+      if ((st = distill_shape(dk, p, dt, di, &sh)) != RR_OK) return st;
     if (grid > (int64_t)di->sms * 8) grid = (int64_t)di->sms * 8;
   }
-  void* args[] = {&p};
-  cudaError_t e = cudaLaunchKernel(dk.fn, dim3((unsigned)grid), dim3((unsigned)dk.threads), args,
-                                   smem, stream);
+  cudaError_t e;
+  if (sh.K > 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)sh.grid);
+    cfg.blockDim = dim3((unsigned)sh.T);
+    cfg.dynamicSmemBytes = sh.smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = sh.K;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = sh.K > 1 ? 1 : 0;
+    void* args[] = {&p, &sh.geo};
+    e = cudaLaunchKernelExC(&cfg, dk.stream[sh.K > 1], args);
+  } else {
+    const size_t smem = 128 + (size_t)p.k * 12 + p.filter_bits / 8;
+    void* args[] = {&p};
+    e = cudaLaunchKernel(dk.rows, dim3((unsigned)grid), dim3((unsigned)dk.rows_threads), args,
+                         smem, stream);
+  }
   if (e != cudaSuccess) return fail(RR_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
   return ok();
 }

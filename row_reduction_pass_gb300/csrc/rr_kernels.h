@@ -217,11 +217,23 @@ struct DistillParams {
   float inv_t;           // 1 / temperature
   float c;               // log2 e / temperature
 };
-struct DistillKernel {
-  const void* fn;
-  int threads;
+// Launch geometry of the streaming kernel: a block (one of K of a cluster)
+// holds a slice of S 16-byte chunks of a row, at most kDistNQ a row thread;
+// byte offsets into its shared memory.
+constexpr int kDistNQ = 8;
+struct DistillGeo {
+  int32_t S;
+  int32_t words;     // 32-bit words of a slice's column bits
+  int32_t list_off;  // lists: [4][k] 16-byte entries
+  int32_t bits_off;  // column bits: [2][words]
+  int32_t buf_off;   // rows: [2][S] chunks
 };
-DistillKernel distill_kernel(int dtype);
+struct DistillKernels {
+  const void* rows;       // a block per row, any alignment and length
+  int rows_threads;
+  const void* stream[2];  // [cluster]
+};
+DistillKernels distill_kernels(int dtype, bool tail);
 
 // Verification of drafted tokens (k_verify.cu).
 struct VerifyParams {
