@@ -194,12 +194,12 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
 // alignment.  The block's last warp, the list warp, is set apart from the rest,
 // the row warps:
 //   list warp, per row j: waits until the row warps have published row j's
-//     statistics (their chunks are then in registers), refills the buffer of
-//     row j with row j + 2 (one bulk copy), finishes row j - 1's listed columns,
-//     writes row j's loss, and prepares row j + 2's list.
+//     statistics, finishes row j - 1's listed columns, writes row j's loss, and
+//     prepares row j + 2's list.
 //   row warp, per row j: waits for the row and its list, takes its chunks into
 //     registers, publishes the warp's maximum and sums to every block of the
-//     cluster, merges all the warps' when they are there, stores its chunks of
+//     cluster, merges all the warps' when they are there (thread 0 then refills
+//     the row's buffer with row j + 2, one bulk copy), stores its chunks of
 //     dlogits.
 // So a block meets once a row (an mbarrier of the published statistics), the
 // two latencies of a list (its entries, then the student's logits there) are a
@@ -217,9 +217,10 @@ struct __align__(16) DistHead {
   int dup;     // a column of this slice may be listed twice
 };
 struct __align__(16) DistEntry {
-  float t, lt, x;
-  int j;
+  float t, lt, x;  // the teacher's weight (0: absent) and its logarithm, the student's logit
+  int place;       // element place in this block's slice, -1 none; + kDistAgain if listed before
 };
+constexpr int kDistAgain = 1 << 30;
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -230,6 +231,20 @@ __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
   return v;
+}
+
+// The lanes of a chunk whose bit is set become -inf.
+template <int DT>
+__device__ __forceinline__ uint4 dist_take_out(uint4 c, uint32_t b) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t m = DT == kBF16 ? ((b >> (2 * i)) & 1 ? 0xffffu : 0u) |
+                                         ((b >> (2 * i + 1)) & 1 ? 0xffff0000u : 0u)
+                                   : ((b >> i) & 1 ? 0xffffffffu : 0u);
+    w[i] = (word_of(c, i) & ~m) | ((DT == kBF16 ? 0xff80ff80u : 0xff800000u) & m);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // The lanes of a chunk outside bytes [lo, hi) become -inf.
@@ -260,10 +275,15 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
   uint64_t* mrg = full + 2;                            // [2] statistics published
   uint64_t* ready = full + 4;                          // [2] the list is prepared
   DistHead* heads = reinterpret_cast<DistHead*>(smem + 64);      // [4]
-  float4* slots = reinterpret_cast<float4*>(smem + 128);         // [2][K * nw]
+  uint4* edge = reinterpret_cast<uint4*>(smem + 128);            // [2] a row's ragged chunks
+  float4* slots = reinterpret_cast<float4*>(smem + 160);         // [2][nslot]
   DistEntry* lists = reinterpret_cast<DistEntry*>(smem + g.list_off);  // [4][k]
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + g.bits_off);     // [2][words]
-  const int nslot = K * nw;
+  // With a tail the list warps publish too (the listed columns' part of Z).  In a
+  // cluster they always do: a slot is written again two rows later, and every
+  // warp that reads it must have said, by publishing the row between, that it has.
+  constexpr bool kListPublishes = TAIL || CL;
+  const int nwp = nw + (kListPublishes ? 1 : 0), nslot = K * nwp;
   const int64_t rowb = p.cols * E;
   const int k0 = rank * g.S;
   auto row_addr = [&](int64_t r) { return reinterpret_cast<uintptr_t>(p.x) + r * rowb; };
@@ -309,6 +329,25 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     d = warp_sum(d);
     if (TAIL) dt = warp_sum(dt);
   };
+  // warp w's partial of row j, to the slots of every rank
+  auto publish = [&](int64_t j, int w, float m, float d) {
+    const float M = warp_max(m);
+    const float a = m == -INFINITY ? 0.f : ex2((m - M) * p.c);
+    d = warp_sum(d * a);
+    if (lane == 0) {
+      float4* sl = slots + (j & 1) * nslot + rank * nwp + w;
+      const float4 v = make_float4(M, d, w < nw ? d : 0.f, 0.f);
+      if constexpr (CL) {
+        for (int t = 0; t < K; ++t) {
+          st_cluster_f32x4(map_to_rank(sl, t), v.x, v.y, v.z, v.w);
+          mbar_arrive_cluster(map_to_rank(&mrg[j & 1], t));
+        }
+      } else {
+        *sl = v;
+        mbar_arrive(&mrg[j & 1]);
+      }
+    }
+  };
   // the teacher's mass outside the list, and the weight of the student's softmax
   auto masses = [&](const DistHead& hd, float dt, float& mass, float& tt) {
     mass = 1.f;
@@ -319,83 +358,122 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     }
   };
 
+  auto load_row = [&](int64_t j) {
+    if (row_of(j) >= p.rows || dead) return;
+    const uintptr_t a = row_addr(row_of(j));
+    const uint32_t bytes = (uint32_t)chunks((int)(a & 15)) * 16u;
+    mbar_arrive_expect_tx(&full[j & 1], bytes);
+    bulk_load(smem + g.buf_off + (j & 1) * g.S * 16,
+              reinterpret_cast<const void*>((a & ~uintptr_t(15)) + (int64_t)k0 * 16), bytes,
+              &full[j & 1], policy_evict_first());
+  };
+
   if (warp == nw) {
     // ------------------------------------------------------- the list warp
-    const uint64_t policy = policy_evict_first();
-    auto load_row = [&](int64_t j) {
-      if (row_of(j) >= p.rows || dead) return;
-      const uintptr_t a = row_addr(row_of(j));
-      const uint32_t bytes = (uint32_t)chunks((int)(a & 15)) * 16u;
-      mbar_arrive_expect_tx(&full[j & 1], bytes);
-      bulk_load(smem + g.buf_off + (j & 1) * g.S * 16,
-                reinterpret_cast<const void*>((a & ~uintptr_t(15)) + (int64_t)k0 * 16), bytes,
-                &full[j & 1], policy);
-    };
     // the place of column c in the slice (row start h bytes into its chunk), or -1
     auto place = [&](int c, int h) {
       const int64_t e = (int64_t)c + h / E - (int64_t)k0 * W;
       return e >= 0 && e < (int64_t)g.S * W ? (int)e : -1;
     };
+    // The list of a row passes through registers, 4 entries a lane (lists of up
+    // to 128) at a time: its entries are loaded one row before the student's
+    // logits there, and those one row's wait before they are used.
+    int ci[4];
+    float cv[4], cx[4];
+    auto load_entries = [&](int64_t j, int base) {
+      const int64_t at = row_of(j) * k;
+      const bool any = row_of(j) < p.rows;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = base + lane + 32 * q;
+        ci[q] = any && i < k ? __ldg(p.index + at + i) : -1;
+        cv[q] = any && i < k ? __ldg(p.value + at + i) : 0.f;
+      }
+    };
+    auto load_logits = [&](int64_t j) {
+      const char* x = p.x + row_of(j) * rowb;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        cx[q] = ci[q] >= 0 && ci[q] < p.cols ? ld_elem<DT>(x + (int64_t)ci[q] * E) : 0.f;
+    };
     auto prepare = [&](int64_t j) {
       const int64_t r = row_of(j);
       if (r >= p.rows) return;
       const int h = (int)(row_addr(r) & 15);
-      const char* x = p.x + r * rowb;
       DistEntry* li = lists + (j & 3) * k;
       uint32_t* bm = bits + (j & 1) * g.words;
       float vm = -INFINITY;
       int any = 0, dup = 0;
-#pragma unroll 4
-      for (int i = lane; i < k; i += 32) {
-        int c = __ldg(p.index + r * k + i);
-        const float v = __ldg(p.value + r * k + i);
-        const bool beyond = c >= p.cols;
-        if (beyond) c = -1;
-        if (beyond && rank == 0 && p.bad != nullptr) atomicAdd(p.bad, 1);
-        const float xv = c >= 0 ? ld_elem<DT>(x + (int64_t)c * E) : 0.f;
-        li[i] = DistEntry{0.f, v, xv, c};
-        if (c >= 0) {
-          any = 1;
-          vm = fmaxf(vm, v);
+      for (int base = 0;;) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int i = base + lane + 32 * q;
+          if (i >= k) break;
+          const bool beyond = ci[q] >= p.cols;
+          if (beyond && rank == 0 && p.bad != nullptr) atomicAdd(p.bad, 1);
+          const bool there = ci[q] >= 0 && !beyond;
+          int e = there ? place(ci[q], h) : -1;
+          if (e >= 0 && ((atomicOr(&bm[e >> 5], 1u << (e & 31)) >> (e & 31)) & 1)) {
+            dup = 1;
+            e |= kDistAgain;
+          }
+          li[i] = DistEntry{0.f, there ? cv[q] : -INFINITY, cx[q], e};
+          if (there) {
+            any = 1;
+            vm = fmaxf(vm, cv[q]);
+          }
         }
+        base += 128;
+        if (base >= k) break;
+        load_entries(j, base);
+        load_logits(j);
       }
       any = __any_sync(0xffffffffu, any);
       vm = warp_max(vm);
+      const bool live = any && (TAIL || vm != -INFINITY);
       float lnt = 0.f;
       if (!TAIL) {
         float z = 0.f;
-        for (int i = lane; i < k; i += 32)
-          if (li[i].j >= 0) z += expf((li[i].lt - vm) / p.temperature);
+        for (int i = lane; i < k && live; i += 32) z += expf((li[i].lt - vm) / p.temperature);
         lnt = logf(warp_sum(z));
       }
       float st = 0.f;
-      for (int i = lane; i < k; i += 32) {
-        const int c = li[i].j;
-        if (c < 0) continue;
+      for (int i = lane; i < k && live; i += 32) {
         const float lt = TAIL ? li[i].lt : (li[i].lt - vm) / p.temperature - lnt;
         const float t = expf(lt);
         li[i].lt = lt;
         li[i].t = t;
         st += t;
-        const int e = place(c, h);
-        if (e >= 0 && ((atomicOr(&bm[e >> 5], 1u << (e & 31)) >> (e & 31)) & 1)) dup = 1;
       }
       st = warp_sum(st);
       dup = __any_sync(0xffffffffu, dup);
       if (lane == 0)
         heads[j & 3] = DistHead{p.temperature * (p.grad != nullptr ? __ldg(p.grad + r) : 1.f), st,
-                                any && (TAIL || vm != -INFINITY), dup};
+                                live, dup};
       __syncwarp();
       if (lane == 0) mbar_arrive(&ready[j & 1]);
     };
+    // the maximum and sum of the slice's listed columns (each column once)
+    auto publish_list = [&](int64_t j) {
+      const DistEntry* li = lists + (j & 3) * k;
+      float m = -INFINITY, d = 0.f;
+      if (TAIL) {
+        for (int i = lane; i < k; i += 32)
+          if (li[i].place >= 0 && li[i].place < kDistAgain) m = fmaxf(m, li[i].x);
+        if (m != -INFINITY) {
+          const float mL = m * p.c;
+          for (int i = lane; i < k; i += 32)
+            if (li[i].place >= 0 && li[i].place < kDistAgain) d += ex2(fmaf(li[i].x, p.c, -mL));
+          d *= ex2(-fmaf(m, p.c, -mL));
+        }
+      }
+      publish(j, nw, m, d);
+    };
     auto clear_bits = [&](int64_t j) {
-      const int h = (int)(row_addr(row_of(j)) & 15);
       const DistEntry* li = lists + (j & 3) * k;
       uint32_t* bm = bits + (j & 1) * g.words;
-      for (int i = lane; i < k; i += 32) {
-        const int e = li[i].j < 0 ? -1 : place(li[i].j, h);
-        if (e >= 0) bm[e >> 5] = 0;
-      }
+      for (int i = lane; i < k; i += 32)
+        if (li[i].place >= 0) bm[(li[i].place & (kDistAgain - 1)) >> 5] = 0;
       __syncwarp();
     };
     // dlogits at row j's listed columns of this slice
@@ -408,32 +486,29 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       float mass, tt;
       masses(hd, dt, mass, tt);
       const float A = hd.g * (mass / d), mL = M * p.c, res = ex2(-fmaf(M, p.c, -mL));
+      char* y = p.y + r * rowb - h + (int64_t)k0 * 16;
       for (int i = lane; i < k; i += 32) {
         const DistEntry en = li[i];
-        if (en.j < 0 || place(en.j, h) < 0) continue;
+        if (en.place < 0 || en.place >= kDistAgain) continue;
         float t = en.t;
-        if (hd.dup) {
-          bool first = true;
-          for (int n = 0; n < i; ++n) first = first && li[n].j != en.j;
-          if (!first) continue;
-          for (int n = i + 1; n < k; ++n) t += li[n].j == en.j ? li[n].t : 0.f;
-        }
-        st_elem<DT>(p.y + r * rowb + (int64_t)en.j * E,
-                    ex2(fmaf(en.x, p.c, -mL)) * res * A - hd.g * t);
+        if (hd.dup)
+          for (int n = 0; n < k; ++n) t += li[n].place == (en.place | kDistAgain) ? li[n].t : 0.f;
+        st_elem<DT>(y + (int64_t)en.place * E, ex2(fmaf(en.x, p.c, -mL)) * res * A - hd.g * t);
       }
     };
-    if (lane == 0) {
-      load_row(0);
-      load_row(1);
+    for (int i = 0; i < 2; ++i) {
+      load_entries(i, 0);
+      load_logits(i);
+      prepare(i);
     }
-    prepare(0);
-    prepare(1);
+    load_entries(2, 0);
     float Mp = 0.f, dp = 0.f, dtp = 0.f;
     int64_t j = 0;
     for (; row_of(j) < p.rows; ++j) {
       float M, d, dt;
+      load_logits(j + 2);
+      if (kListPublishes) publish_list(j);
       merged(j, M, d, dt);
-      if (lane == 0) load_row(j + 2);
       if (j > 0) finish(j - 1, Mp, dp, dtp);
       if (rank == 0) {
         const DistHead hd = heads[j & 3];
@@ -448,7 +523,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
                                 logf(__int_as_float(__float_as_int(d) - (ez << 23))));
           for (int i = lane; i < k; i += 32) {
             const DistEntry en = li[i];
-            if (en.j >= 0 && !(en.t <= 0.f)) l += en.t * ((en.lt + hi) - (en.x - M) / p.temperature);
+            if (!(en.t <= 0.f)) l += en.t * ((en.lt + hi) - (en.x - M) / p.temperature);
           }
           l = warp_sum(l);
           float mass, tt;
@@ -462,36 +537,57 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       }
       clear_bits(j);
       prepare(j + 2);
+      load_entries(j + 3, 0);
       Mp = M;
       dp = d;
       dtp = dt;
     }
-    if (dead && lane == 0)  // copies of this block still in flight end before it does
-      for (int i = 0; i < 2; ++i) mbar_wait_bounded(&full[i], 0, p.err);
     __syncthreads();
     if (j > 0) finish(j - 1, Mp, dp, dtp);
   } else {
     // ------------------------------------------------------- the row warps
+    if (tid == 0) {
+      load_row(0);
+      load_row(1);
+    }
     for (int64_t j = 0; row_of(j) < p.rows; ++j) {
       const int64_t r = row_of(j);
       const uintptr_t a = row_addr(r);
       const int h = (int)(a & 15);
       const int n = chunks(h);
-      const int last = (int)((h + rowb + 15) >> 4) - 1 - k0;  // place of the row's last chunk
-      const int tail_bytes = (int)(h + rowb - 16 * ((h + rowb + 15) / 16 - 1));
+      const int64_t nch = (h + rowb + 15) >> 4;                // chunks of the row
+      const int last = (int)(nch - 1 - k0);                    // place of its last chunk
+      const int tail_bytes = (int)(h + rowb - 16 * (nch - 1));
       const uint32_t ph = (uint32_t)((j >> 1) & 1);
-      const uint4* buf = reinterpret_cast<const uint4*>(smem + g.buf_off + (j & 1) * g.S * 16);
+      uint4* buf = reinterpret_cast<uint4*>(smem + g.buf_off + (j & 1) * g.S * 16);
       const unsigned char* bm = reinterpret_cast<const unsigned char*>(bits + (j & 1) * g.words);
       if (!dead) dead = !mbar_wait_bounded(&full[j & 1], ph, p.err);
+      // the lanes of the row's first and last chunk that belong to its
+      // neighbours become -inf in the buffer, by the chunk's only reader (the
+      // proxy fence orders this before the copy that refills the buffer)
+      const int nq = n > tid ? (n - tid + G - 1) / G : 0;
+      const bool head = tid == 0 && rank == 0 && h != 0;
+      const bool end = tail_bytes != 16 && last < n && tid + (nq - 1) * G == last;
+      if (head || end) {
+        if (head) dist_mask<DT>(buf[0], h, 16);
+        if (end) dist_mask<DT>(buf[last], 0, tail_bytes);
+        if (head) edge[0] = buf[0];
+        if (end) edge[1] = buf[last];
+        fence_proxy_async_smem();
+      }
+      if (!dead) dead = !mbar_wait_bounded(&ready[j & 1], ph, p.err);
       uint4 v[NQ];
       float m = -INFINITY;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
-        const int c = tid + q * G;
-        if (c >= n) break;
-        v[q] = buf[c];
-        if ((c == 0 && rank == 0 && h != 0) || c == last)
-          dist_mask<DT>(v[q], c == 0 && rank == 0 ? h : 0, c == last ? tail_bytes : 16);
+        if (q >= nq) break;
+        v[q] = buf[tid + q * G];
+        if (TAIL) {  // listed lanes become -inf: the list warp counts them
+          const int c = tid + q * G;
+          uint32_t b = bm[W == 8 ? c : c >> 1];
+          if (W == 4) b = (c & 1) ? b >> 4 : b & 15u;
+          if (b != 0) v[q] = dist_take_out<DT>(v[q], b);
+        }
         if constexpr (DT == kBF16) {
           const uint32_t w = bf16x2_max(bf16x2_max(v[q].x, v[q].y), bf16x2_max(v[q].z, v[q].w));
           m = fmaxf(m, fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
@@ -500,62 +596,27 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
                     fmaxf(__uint_as_float(v[q].z), __uint_as_float(v[q].w)));
         }
       }
-      if (!dead) dead = !mbar_wait_bounded(&ready[j & 1], ph, p.err);
-      // sums of 2^(x c - fl(m c)), without and (dl) of the listed columns
-      float d = 0.f, dl = 0.f;
+      // sum of 2^(x c - fl(m c))
+      float d = 0.f;
       if (m != -INFINITY) {
         const float mL = m * p.c;
+        float d1 = 0.f;
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
-          const int c = tid + q * G;
-          if (c >= n) break;
-          float e[W];
+          if (q >= nq) break;
 #pragma unroll
           for (int i = 0; i < W; i += 2) {
             float t0, t1;
             fma2(t0, t1, chunk_get<DT>(v[q], i), chunk_get<DT>(v[q], i + 1), p.c, p.c, -mL, -mL);
-            e[i] = ex2(t0);
-            e[i + 1] = ex2(t1);
-          }
-          if (TAIL) {
-            uint32_t b = bm[W == 8 ? c : c >> 1];
-            if (W == 4) b = (c & 1) ? b >> 4 : b & 15u;
-            if (b != 0) {
-#pragma unroll
-              for (int i = 0; i < W; ++i)
-                if ((b >> i) & 1) {
-                  dl += e[i];
-                  e[i] = 0.f;
-                }
-            }
-          }
-          if constexpr (W == 8) d += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-          else d += (e[0] + e[1]) + (e[2] + e[3]);
-        }
-        const float s = ex2(-fmaf(m, p.c, -mL));
-        d *= s;
-        dl *= s;
-      }
-      {
-        const float M = warp_max(m);
-        const float s = m == -INFINITY ? 0.f : ex2((m - M) * p.c);
-        d = warp_sum(m == -INFINITY ? 0.f : d * s);
-        if (TAIL) dl = warp_sum(m == -INFINITY ? 0.f : dl * s);
-        if (lane == 0) {
-          float4* sl = slots + (j & 1) * nslot + rank * nw + warp;
-          if constexpr (CL) {
-            for (int t = 0; t < K; ++t) {
-              st_cluster_f32x4(map_to_rank(sl, t), M, d + dl, d, 0.f);
-              mbar_arrive_cluster(map_to_rank(&mrg[j & 1], t));
-            }
-          } else {
-            *sl = make_float4(M, d + dl, d, 0.f);
-            mbar_arrive(&mrg[j & 1]);
+            add2(d, d1, d, d1, ex2(t0), ex2(t1));
           }
         }
+        d = (d + d1) * ex2(-fmaf(m, p.c, -mL));
       }
+      publish(j, warp, m, d);
       float M, dt;
       merged(j, M, d, dt);
+      if (tid == 0) load_row(j + 2);  // every row warp has taken its chunks of row j
       if (p.y == nullptr) continue;
       char* y = p.y + r * rowb - h + (int64_t)k0 * 16;
       const DistHead hd = heads[j & 3];
@@ -567,32 +628,38 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         mL = M * p.c;
         f = (hd.g * (mass / d) - (tt > 0.f ? hd.g * (tt / dt) : 0.f)) * ex2(-fmaf(M, p.c, -mL));
       }
+      const float nmL = -mL;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
-        const int c = tid + q * G;
-        if (c >= n) break;
+        if (q >= nq || zero) break;
         float e[W];
 #pragma unroll
         for (int i = 0; i < W; i += 2) {
           float t0, t1;
-          fma2(t0, t1, chunk_get<DT>(v[q], i), chunk_get<DT>(v[q], i + 1), p.c, p.c, -mL, -mL);
+          fma2(t0, t1, chunk_get<DT>(v[q], i), chunk_get<DT>(v[q], i + 1), p.c, p.c, nmL, nmL);
           mul2(e[i], e[i + 1], ex2(t0), ex2(t1), f, f);
         }
-        if (zero) {
-#pragma unroll
-          for (int i = 0; i < W; ++i) e[i] = 0.f;
-        }
-        char* at = y + (int64_t)c * 16;
-        if ((c == 0 && rank == 0 && h != 0) || (c == last && tail_bytes != 16)) {
-          const int lo = c == 0 && rank == 0 ? h : 0, hi = c == last ? tail_bytes : 16;
-#pragma unroll
-          for (int i = 0; i < W; ++i)
-            if (i * E >= lo && i * E < hi) st_elem<DT>(at + i * E, e[i]);
-        } else {
-          st_chunk_stream(at, chunk_pack<DT>(e));
+        if (!(head && q == 0) && !(end && q == nq - 1))
+          st_chunk_stream(y + (int64_t)(tid + q * G) * 16, chunk_pack<DT>(e));
+      }
+      if (zero)
+        for (int q = head ? 1 : 0; q < nq - (end ? 1 : 0); ++q)
+          st_chunk_stream(y + (int64_t)(tid + q * G) * 16, make_uint4(0u, 0u, 0u, 0u));
+      // the first and last chunk of a row that starts or ends inside one: the
+      // row's own lanes, from the copies kept
+      for (int s = 0; s < 2; ++s) {
+        if (!(s == 0 ? head : end)) continue;
+        const int lo = s == 0 ? h : (nch == 1 ? h : 0), hi = s == 0 && nch > 1 ? 16 : tail_bytes;
+        if (s == 1 && head && nch == 1) continue;  // one chunk in all: done
+        for (int i = lo; i < hi; i += E) {
+          const float x = ld_smem_elem<DT>(reinterpret_cast<const char*>(edge + s) + i);
+          st_elem<DT>(y + (s == 0 ? 0 : (int64_t)last * 16) + i,
+                      zero ? 0.f : ex2(fmaf(x, p.c, nmL)) * f);
         }
       }
     }
+    if (dead && tid == 0)  // copies of this block still in flight end before it does
+      for (int i = 0; i < 2; ++i) mbar_wait_bounded(&full[i], 0, p.err);
     __syncthreads();  // every chunk stored: the list warp finishes the last row
   }
   if constexpr (CL) cluster_sync();  // no peer still writes this block's slots

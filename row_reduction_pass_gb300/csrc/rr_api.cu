@@ -1268,14 +1268,18 @@ static rr_status distill_shape(const rr::DistillKernels& dk, const rr::DistillPa
   for (int K = 1; K <= 8; ++K) {
     const int64_t S = cdiv(nch_max, K);
     if (K > 1 && (K - 1) * S >= nch_min) break;  // every rank gets chunks
-    const int64_t nw = std::max<int64_t>(3, cdiv(cdiv(S, rr::kDistNQ), 32));
-    if (nw > 31) continue;
+    if (const char* f = std::getenv("RR_DIST_K")) if (atoi(f) && atoi(f) != K) continue;
+    // 1, 3, 7, 15 or 31 row warps: with the list warp a block of 64 .. 1024
+    // threads, so that the 1024 threads an SM holds at 64 registers are whole blocks
+    int64_t nw = 1;
+    while (nw < 31 && 32 * nw * rr::kDistNQ < S) nw = 2 * nw + 1;
+    if (32 * nw * rr::kDistNQ < S) continue;
     DistillShape sh;
     sh.K = K;
     sh.T = (int)(nw + 1) * 32;
     sh.geo.S = (int32_t)S;
     sh.geo.words = (int32_t)cdiv(S * W, 32);
-    const int64_t list = round_up(128 + 2 * 16 * K * nw, 16);
+    const int64_t list = 160 + 2 * 16 * K * (nw + 1);
     const int64_t bits = list + 4 * 16 * (int64_t)p.k;
     const int64_t buf = round_up(bits + 8 * (int64_t)sh.geo.words, 128);
     const int64_t smem = buf + 2 * S * 16;
