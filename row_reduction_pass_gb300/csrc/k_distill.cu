@@ -191,11 +191,12 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
 // One block (or a cluster of K blocks, each with a slice of S 16-byte chunks)
 // per row at a time, grid-stride over the rows; x and y share their address
 // modulo 16, so a chunk of one is a chunk of the other whatever the row's
-// alignment.  The block's last warp, the list warp, is set apart from the rest,
-// the row warps:
-//   list warp, per row j: waits until the row warps have published row j's
-//     statistics, finishes row j - 1's listed columns, writes row j's loss, and
-//     prepares row j + 2's list.
+// alignment.  The block's last two warps, the list warps, are set apart from the
+// rest, the row warps:
+//   list warp, per row j (of its parity): waits until the row warps have
+//     published row j's statistics, prepares row j + 2's list, writes row j's
+//     loss, and, once row j + 1 is published (every chunk of row j then stored),
+//     stores row j's listed columns.
 //   row warp, per row j: waits for the row and its list, takes its chunks into
 //     registers, publishes the warp's maximum and sums to every block of the
 //     cluster, merges all the warps' when they are there (thread 0 then refills
@@ -204,8 +205,8 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
 // So a block meets once a row (an mbarrier of the published statistics), the
 // two latencies of a list (its entries, then the student's logits there) are a
 // row ahead of their use, and two rows are in flight while one is worked on.
-// Listed columns are stored by the list warp one row later, when every row warp
-// has passed its chunk stores.
+// One list warp alone was the bottleneck: 8192 x 50304 bf16 took 265 us without
+// entries, 357 us with 64 a row, 451 us with 128 (54 rows a block).
 //
 // Bits of the listed columns of a slice, by place in the slice, tell the row
 // warps which lanes of a chunk to leave out of Zt (a byte or half a byte a
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
                                                                 const DistillGeo g) {
   constexpr int E = DType<DT>::E, W = DType<DT>::V, NQ = kDistNQ;
   extern __shared__ __align__(128) unsigned char smem[];
-  const int nw = (int)(blockDim.x >> 5) - 1;  // row warps
+  const int nw = (int)(blockDim.x >> 5) - 2;  // row warps
   const int G = nw * 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int K = 1, rank = 0;
@@ -272,16 +273,16 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
   const int64_t owner = blockIdx.x / K, owners = gridDim.x / K;
   const int k = p.k;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);  // [2] the row has landed
-  uint64_t* mrg = full + 2;                            // [2] statistics published
-  uint64_t* ready = full + 4;                          // [2] the list is prepared
+  uint64_t* mrg = full + 2;                            // [4] statistics published
+  uint64_t* ready = full + 6;                          // [2] the list is prepared
   DistHead* heads = reinterpret_cast<DistHead*>(smem + 64);      // [4]
   uint4* edge = reinterpret_cast<uint4*>(smem + 128);            // [2] a row's ragged chunks
-  float4* slots = reinterpret_cast<float4*>(smem + 160);         // [2][nslot]
+  float4* slots = reinterpret_cast<float4*>(smem + 160);         // [4][nslot]
   DistEntry* lists = reinterpret_cast<DistEntry*>(smem + g.list_off);  // [4][k]
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + g.bits_off);     // [2][words]
   // With a tail the list warps publish too (the listed columns' part of Z).  In a
-  // cluster they always do: a slot is written again two rows later, and every
-  // warp that reads it must have said, by publishing the row between, that it has.
+  // cluster they always do: a slot is written again four rows later, and every
+  // warp that reads it must have said, by publishing a later row, that it has.
   constexpr bool kListPublishes = TAIL || CL;
   const int nwp = nw + (kListPublishes ? 1 : 0), nslot = K * nwp;
   const int64_t rowb = p.cols * E;
@@ -297,9 +298,9 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&mrg[i], nslot);
       mbar_init(&ready[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&mrg[i], nslot);
     fence_mbar_init();
   }
   for (int i = tid; i < 2 * g.words; i += blockDim.x) bits[i] = 0;
@@ -307,15 +308,19 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
   else __syncthreads();
 
   bool dead = false;  // a wait gave up: later waits are skipped (the kernel still ends)
+  // Row j published by every warp.  (No list warp runs so late that the barrier's
+  // next phase, row j + 4, ends before it looks: that row waits for its list.)
+  auto published = [&](int64_t j) {
+    const uint32_t ph = (uint32_t)((j >> 2) & 1);
+    if (!dead) {
+      if constexpr (CL) dead = !mbar_wait_bounded_cluster(&mrg[j & 3], ph, p.err);
+      else dead = !mbar_wait_bounded(&mrg[j & 3], ph, p.err);
+    }
+  };
   // row j's statistics, the same bits in every warp of every rank
   auto merged = [&](int64_t j, float& M, float& d, float& dt) {
-    const int par = (int)(j & 1);
-    const uint32_t ph = (uint32_t)((j >> 1) & 1);
-    if (!dead) {
-      if constexpr (CL) dead = !mbar_wait_bounded_cluster(&mrg[par], ph, p.err);
-      else dead = !mbar_wait_bounded(&mrg[par], ph, p.err);
-    }
-    const float4* sl = slots + par * nslot;
+    published(j);
+    const float4* sl = slots + (j & 3) * nslot;
     M = -INFINITY;
     for (int i = lane; i < nslot; i += 32) M = fmaxf(M, sl[i].x);
     M = warp_max(M);
@@ -335,16 +340,16 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     const float a = m == -INFINITY ? 0.f : ex2((m - M) * p.c);
     d = warp_sum(d * a);
     if (lane == 0) {
-      float4* sl = slots + (j & 1) * nslot + rank * nwp + w;
+      float4* sl = slots + (j & 3) * nslot + rank * nwp + w;
       const float4 v = make_float4(M, d, w < nw ? d : 0.f, 0.f);
       if constexpr (CL) {
         for (int t = 0; t < K; ++t) {
           st_cluster_f32x4(map_to_rank(sl, t), v.x, v.y, v.z, v.w);
-          mbar_arrive_cluster(map_to_rank(&mrg[j & 1], t));
+          mbar_arrive_cluster(map_to_rank(&mrg[j & 3], t));
         }
       } else {
         *sl = v;
-        mbar_arrive(&mrg[j & 1]);
+        mbar_arrive(&mrg[j & 3]);
       }
     }
   };
@@ -368,12 +373,16 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
               &full[j & 1], policy_evict_first());
   };
 
-  if (warp == nw) {
-    // ------------------------------------------------------- the list warp
+  if (warp >= nw) {
+    // ------------------------------------------------------ the list warps
     // the place of column c in the slice (row start h bytes into its chunk), or -1
     auto place = [&](int c, int h) {
       const int64_t e = (int64_t)c + h / E - (int64_t)k0 * W;
       return e >= 0 && e < (int64_t)g.S * W ? (int)e : -1;
+    };
+    // a / T, 1 / T in two parts
+    auto over_t = [&](float a) {
+      return isfinite(a) ? fmaf(a, p.inv_t, a * p.inv_t_lo) : a;
     };
     // The list of a row passes through registers, 4 entries a lane (lists of up
     // to 128) at a time: its entries are loaded one row before the student's
@@ -434,12 +443,12 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       float lnt = 0.f;
       if (!TAIL) {
         float z = 0.f;
-        for (int i = lane; i < k && live; i += 32) z += expf((li[i].lt - vm) / p.temperature);
+        for (int i = lane; i < k && live; i += 32) z += expf(over_t(li[i].lt - vm));
         lnt = logf(warp_sum(z));
       }
       float st = 0.f;
       for (int i = lane; i < k && live; i += 32) {
-        const float lt = TAIL ? li[i].lt : (li[i].lt - vm) / p.temperature - lnt;
+        const float lt = TAIL ? li[i].lt : over_t(li[i].lt - vm) - lnt;
         const float t = expf(lt);
         li[i].lt = lt;
         li[i].t = t;
@@ -496,54 +505,54 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         st_elem<DT>(y + (int64_t)en.place * E, ex2(fmaf(en.x, p.c, -mL)) * res * A - hd.g * t);
       }
     };
-    for (int i = 0; i < 2; ++i) {
-      load_entries(i, 0);
-      load_logits(i);
-      prepare(i);
-    }
-    load_entries(2, 0);
-    float Mp = 0.f, dp = 0.f, dtp = 0.f;
-    int64_t j = 0;
-    for (; row_of(j) < p.rows; ++j) {
-      float M, d, dt;
+    auto write_loss = [&](int64_t j, float M, float d, float dt) {
+      const DistHead hd = heads[j & 3];
+      float l = 0.f;
+      if (hd.live && M != -INFINITY) {
+        const DistEntry* li = lists + (j & 3) * k;
+        // ln Z in two parts, hi of a few bits: the terms below are then small
+        // differences, and ln Z brings no rounding of its own size
+        const int ez = (__float_as_int(d) >> 23) - 127;
+        const float hi = ez * 0.6875f;
+        const float lo = fmaf((float)ez, 0.00564718056f,
+                              logf(__int_as_float(__float_as_int(d) - (ez << 23))));
+        for (int i = lane; i < k; i += 32) {
+          const DistEntry en = li[i];
+          if (!(en.t <= 0.f)) l += en.t * ((en.lt + hi) - over_t(en.x - M));
+        }
+        l = warp_sum(l);
+        float mass, tt;
+        masses(hd, dt, mass, tt);
+        l += lo * (TAIL ? hd.st : 1.f);
+        if (tt > 0.f) l += tt * (logf(tt) - logf(dt / d));
+        l *= p.temperature * p.temperature;
+        if (d != d) l = d;
+      }
+      if (lane == 0) p.loss[row_of(j)] = l;
+    };
+    int64_t j = warp - nw;
+    load_entries(j, 0);
+    load_logits(j);
+    prepare(j);
+    load_entries(j + 2, 0);
+    float M = 0.f, d = 0.f, dt = 0.f;
+    bool open = false;  // the block's last row: listed columns still to be stored
+    for (; row_of(j) < p.rows; j += 2) {
       load_logits(j + 2);
       if (kListPublishes) publish_list(j);
       merged(j, M, d, dt);
-      if (j > 0) finish(j - 1, Mp, dp, dtp);
-      if (rank == 0) {
-        const DistHead hd = heads[j & 3];
-        float l = 0.f;
-        if (hd.live && M != -INFINITY) {
-          const DistEntry* li = lists + (j & 3) * k;
-          // ln Z in two parts, hi of a few bits: the terms below are then small
-          // differences, and ln Z brings no rounding of its own size
-          const int ez = (__float_as_int(d) >> 23) - 127;
-          const float hi = ez * 0.6875f;
-          const float lo = fmaf((float)ez, 0.00564718056f,
-                                logf(__int_as_float(__float_as_int(d) - (ez << 23))));
-          for (int i = lane; i < k; i += 32) {
-            const DistEntry en = li[i];
-            if (!(en.t <= 0.f)) l += en.t * ((en.lt + hi) - (en.x - M) / p.temperature);
-          }
-          l = warp_sum(l);
-          float mass, tt;
-          masses(hd, dt, mass, tt);
-          l += lo * (TAIL ? hd.st : 1.f);
-          if (tt > 0.f) l += tt * (logf(tt) - logf(dt / d));
-          l *= p.temperature * p.temperature;
-          if (d != d) l = d;
-        }
-        if (lane == 0) p.loss[row_of(j)] = l;
-      }
       clear_bits(j);
       prepare(j + 2);
-      load_entries(j + 3, 0);
-      Mp = M;
-      dp = d;
-      dtp = dt;
+      load_entries(j + 4, 0);
+      if (rank == 0) write_loss(j, M, d, dt);
+      open = row_of(j + 1) >= p.rows;
+      if (!open) {
+        published(j + 1);
+        finish(j, M, d, dt);
+      }
     }
     __syncthreads();
-    if (j > 0) finish(j - 1, Mp, dp, dtp);
+    if (open) finish(j - 2, M, d, dt);
   } else {
     // ------------------------------------------------------- the row warps
     if (tid == 0) {
@@ -660,7 +669,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     }
     if (dead && tid == 0)  // copies of this block still in flight end before it does
       for (int i = 0; i < 2; ++i) mbar_wait_bounded(&full[i], 0, p.err);
-    __syncthreads();  // every chunk stored: the list warp finishes the last row
+    __syncthreads();  // every chunk stored: the last row's listed columns may be
   }
   if constexpr (CL) cluster_sync();  // no peer still writes this block's slots
 }

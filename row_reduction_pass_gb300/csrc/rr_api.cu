@@ -1269,17 +1269,17 @@ static rr_status distill_shape(const rr::DistillKernels& dk, const rr::DistillPa
     const int64_t S = cdiv(nch_max, K);
     if (K > 1 && (K - 1) * S >= nch_min) break;  // every rank gets chunks
     if (const char* f = std::getenv("RR_DIST_K")) if (atoi(f) && atoi(f) != K) continue;
-    // 1, 3, 7, 15 or 31 row warps: with the list warp a block of 64 .. 1024
+    // 1, 2, 6, 14 or 30 row warps: with the list warps a block of 96 .. 1024
     // threads, so that the 1024 threads an SM holds at 64 registers are whole blocks
     int64_t nw = 1;
-    while (nw < 31 && 32 * nw * rr::kDistNQ < S) nw = 2 * nw + 1;
+    while (nw < 30 && 32 * nw * rr::kDistNQ < S) nw = nw == 1 ? 2 : 2 * nw + 2;
     if (32 * nw * rr::kDistNQ < S) continue;
     DistillShape sh;
     sh.K = K;
-    sh.T = (int)(nw + 1) * 32;
+    sh.T = (int)(nw + 2) * 32;
     sh.geo.S = (int32_t)S;
     sh.geo.words = (int32_t)cdiv(S * W, 32);
-    const int64_t list = 160 + 2 * 16 * K * (nw + 1);
+    const int64_t list = 160 + 4 * 16 * K * (nw + 1);
     const int64_t bits = list + 4 * 16 * (int64_t)p.k;
     const int64_t buf = round_up(bits + 8 * (int64_t)sh.geo.words, 128);
     const int64_t smem = buf + 2 * S * 16;
@@ -2107,6 +2107,7 @@ rr_status rr_distill_fwd_bwd(const void* logits, const int32_t* top_index, const
   while (p.filter_bits < 65536 && p.filter_bits < cols) p.filter_bits *= 2;
   p.temperature = temperature;
   p.inv_t = 1.f / temperature;
+  p.inv_t_lo = (float)(1.0 / (double)temperature - (double)p.inv_t);
   p.c = 1.4426950408889634f / temperature;
   return distill_launch(p, dtype, stream);
 }

@@ -214,7 +214,7 @@ struct DistillParams {
   int32_t tail;          // keep the mass outside the list as one bucket
   uint32_t filter_bits;  // power of two >= 32
   float temperature;
-  float inv_t;           // 1 / temperature
+  float inv_t, inv_t_lo;  // 1 / temperature in two parts
   float c;               // log2 e / temperature
 };
 // Launch geometry of the streaming kernel: a block (one of K of a cluster)
