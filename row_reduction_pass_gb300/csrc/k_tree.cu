@@ -1,10 +1,38 @@
-// k_tree.cu -- attention of a tree of new tokens over a paged cache, any page
-// size: one warp per query row, online softmax over its keys (the fallback for
-// page sizes that the tensor-core kernel cannot tile).
+// k_tree.cu -- attention of a tree of new tokens over a paged cache (the online
+// softmax of k_attn.cu, with the query rows of one key head as the tile, and the
+// keys cut into shares).
+//
+// The n * G rows (node, head of the group) of one sequence and key head share
+// its keys, so they are the rows of a tile: 128 at a time, thread t of a softmax
+// warpgroup owning row t.  The work is counted in key tiles of BN keys over all
+// (sequence, key head, row tile) items in order, and every pipeline (two per
+// SM) takes an equal run of them, whatever the lengths, which the host does not
+// know.  An item inside one run is finished there; of an item cut by runs every
+// piece leaves its unscaled output, maximum and sum in the workspace, and a
+// second kernel joins the pieces.
+//
+// Bound: a key tile is read once per row tile (HBM: 44.7 GB/s a SM, 0.73 us per
+// 32 KB tile of keys and values), its two products cost 128 rows whatever the
+// number that is alive (0.3 us), so up to 128 rows a key head are HBM-bound and
+// more are bound by the products and the softmax, as in k_attn.cu.
+//
+// The keys come through the page table as tensor-map boxes of [64 head
+// dimensions x R positions x 1 head x 1 page], R the largest power of two that
+// divides the page size, at most BN.  Tiles that reach past the context take a
+// mask of 32 bits per 32 keys: the ancestors of the row's node (bits found by
+// walking the parents once a piece), or the nodes up to it.  The rows of V at
+// positions that no row may see are cleared in shared memory before the product,
+// and so are non-finite values at nodes (0 x inf would be NaN for rows that do not
+// see the node); rows that do see such a node get the values added at the end.
+//
+// Page sizes that are not a multiple of 16 go to a kernel of one warp per query
+// row.
+#include <algorithm>
 #include <cstdint>
 
 #include "rr_device.cuh"
 #include "rr_kernels.h"
+#include "rr_tc.cuh"
 
 namespace rr {
 namespace {
@@ -75,12 +103,756 @@ __global__ void __launch_bounds__(kTreeT) tree_rows_kernel_t(const TreeParams p)
     p.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 
+
+// ------------------------------------------------------------ tensor cores ---
+
+// 4-D TMA tile load [dst] <- map at {c0, c1, c2, c3}, completing bytes on bar.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1,
+                                            int c2, int c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+
+constexpr int kTM = 128;  // rows of a tile: MMA M, TMEM lanes
+constexpr int kTreeThreads = 384;
+constexpr int kMaskStride = kTreeMaxNodes / 32 + 1;  // mask words of a row, one spare
+
+// Tiles, stages, TMEM columns (256 a pipeline: S, P buffers, O) as in k_attn.cu.
+template <int D>
+struct TreePL {
+  static constexpr int BN = D == 64 ? 128 : 64;
+  static constexpr int NS = 2;
+  static constexpr int NPB = D == 128 ? 2 : 1;
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kQBox = kTM * 128;
+  static constexpr int kQBytes = kBoxes * kQBox;
+  static constexpr int kKVBox = BN * 128;
+  static constexpr int kKVBytes = kBoxes * kKVBox;
+  static constexpr int kPipe = kQBytes + NS * 2 * kKVBytes;
+  static constexpr int kOffMask = 2 * kPipe;
+  static constexpr int kOffBar = kOffMask + 2 * kTM * kMaskStride * 4;
+  static constexpr int kOffScan = kOffBar + 512;
+  static constexpr int kSmem = kOffScan + 256 + 1024;
+  static constexpr uint32_t kColS = 0, kColP = BN, kColO = 256 - D;
+  static constexpr uint32_t kIdescS = attn_idesc(kTM, BN, false);
+  static constexpr uint32_t kIdescO = attn_idesc(kTM, D, true);
+};
+
+// A piece: the key tiles [t0, t1) of an item, t1 - t0 of its T tiles.
+struct TreeSeg {
+  int64_t left;  // tiles of the run from t0 on
+  int b, hm, t0, t1, T;
+  int ctx;    // keys before the nodes
+  int vis;    // positions below it may be seen by some row of the tile
+  int tiles;  // tiles to work on: those of [t0, t1) below vis
+};
+
+struct TreeWork {
+  int G, MT, KM;  // heads per key head, row tiles per key head, KV * MT
+  int64_t cap;    // positions of the page table
+  __device__ __forceinline__ TreeWork(const TreeParams& p) {
+    G = p.heads / p.kv_heads;
+    MT = (p.nodes * G + kTM - 1) / kTM;
+    KM = p.kv_heads * MT;
+    cap = p.width * (int64_t)p.page;
+  }
+  // keys before the nodes (nodes past the table are not seen wherever they are)
+  __device__ __forceinline__ int context(const TreeParams& p, int b) const {
+    return (int)min((int64_t)max(__ldg(p.length + b), 0), cap);
+  }
+  // key tiles of a sequence
+  __device__ __forceinline__ int tiles(const TreeParams& p, int ctx, int bn) const {
+    return (int)((min((int64_t)ctx + p.nodes, cap) + bn - 1) / bn);
+  }
+};
+
+// The run of pipeline `slot`: tiles [slot * share, (slot + 1) * share) of all.
+__device__ __forceinline__ int64_t tree_share(int64_t total, int nslots, int min_tiles) {
+  return max((total + nslots - 1) / nslots, (int64_t)min_tiles);
+}
+
+template <int D>
+__device__ __forceinline__ void tree_seg_fill(TreeSeg& s, const TreeParams& p, const TreeWork& w) {
+  constexpr int BN = TreePL<D>::BN;
+  s.t1 = (int)min((int64_t)s.T, s.t0 + s.left);
+  const int mt = s.hm % w.MT;
+  const int last = min(p.nodes - 1, (mt * kTM + kTM - 1) / w.G);  // the tile's last node
+  s.vis = (int)min((int64_t)s.ctx + (p.parents != nullptr ? p.nodes : last + 1), w.cap);
+  s.tiles = max(0, min(s.t1, (s.vis + BN - 1) / BN) - s.t0);
+}
+template <int D>
+__device__ __forceinline__ bool tree_seg_next(TreeSeg& s, const TreeParams& p, const TreeWork& w) {
+  s.left -= s.t1 - s.t0;
+  if (s.left <= 0) return false;
+  s.t0 = 0;
+  if (++s.hm == w.KM) {
+    s.hm = 0;
+    do {  // (a sequence of no tiles has no items; tiles are left, so one comes)
+      if (++s.b >= p.batch) return false;
+      s.ctx = w.context(p, s.b);
+      s.T = w.tiles(p, s.ctx, TreePL<D>::BN);
+    } while (s.T == 0);
+  }
+  tree_seg_fill<D>(s, p, w);
+  return true;
+}
+
+// The sum over the block's threads before this one, and over all (in *total);
+// scratch of 16 values.
+__device__ __forceinline__ int64_t tree_scan(int64_t v, int64_t* scratch, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  if (lane == 31) scratch[warp] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+  for (int i = 0; i < nw; ++i) {
+    if (i < warp) before += scratch[i];
+    all += scratch[i];
+  }
+  __syncthreads();
+  *total = all;
+  return before + x - v;
+}
+
+// Row r of a tile in the workspace: one piece of `slot`, 0 its first, 1 its last.
+__device__ __forceinline__ int64_t tree_part(int slot, int part, int rows, int r) {
+  return ((int64_t)slot * 2 + part) * rows + r;
+}
+
+__device__ __forceinline__ bool odd_bf16x2(uint32_t w) {  // an infinity or NaN in the pair
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                   const TreeParams p, const TreeGeo g) {
+  using C = TreePL<D>;
+  constexpr int BN = C::BN;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int w = warp < 8 ? warp >> 2 : (warp - 8) & 1;  // this thread's pipeline
+  unsigned char* pipe = smem + w * C::kPipe;
+  unsigned char* sq = pipe;
+  auto stage_k = [&](int s) { return pipe + C::kQBytes + (2 * s) * C::kKVBytes; };
+  auto stage_v = [&](int s) { return pipe + C::kQBytes + (2 * s + 1) * C::kKVBytes; };
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + C::kOffMask) + w * kTM * kMaskStride;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + w * 16;
+  uint64_t* bar_q = bars + 0;       // Q written, 128 arrivals
+  uint64_t* bar_s = bars + 1;       // S done
+  uint64_t* bar_sfree = bars + 2;   // S read, 128 arrivals
+  uint64_t* bar_ofree = bars + 3;   // O read, 128 arrivals
+  uint64_t* bar_p = bars + 4;       // [NPB] P written, 128 arrivals
+  uint64_t* bar_o = bars + 6;       // [NPB] O += P V done with the P buffer
+  uint64_t* bar_kfull = bars + 8;   // [2]
+  uint64_t* bar_vfull = bars + 10;  // [2]
+  uint64_t* bar_kempty = bars + 12; // [2] S done with the K stage
+  uint64_t* bar_vempty = bars + 14; // [2] O += P V done with the V stage
+  uint64_t* extra = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + 40;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(extra);
+  int* odd = reinterpret_cast<int*>(extra + 1) + w;  // the last piece with a non-finite V row
+  TreeSeg* firsts = reinterpret_cast<TreeSeg*>(extra + 4);  // [2]
+  int64_t* scratch = reinterpret_cast<int64_t*>(smem + C::kOffScan);
+
+  const TreeWork wk(p);
+  const int nslots = 2 * (int)gridDim.x, slot0 = 2 * (int)blockIdx.x;
+
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tslot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if ((warp == 8 || warp == 9) && lane == 0) {
+    mbar_init(bar_q, 128);
+    mbar_init(bar_s, 1);
+    mbar_init(bar_sfree, 128);
+    mbar_init(bar_ofree, 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_p[i], 128);
+      mbar_init(&bar_o[i], 1);
+      mbar_init(&bar_kfull[i], 1);
+      mbar_init(&bar_vfull[i], 1);
+      mbar_init(&bar_kempty[i], 1);
+      mbar_init(&bar_vempty[i], 1);
+    }
+    fence_mbar_init();
+    *odd = 0;
+    firsts[w].left = 0;
+  }
+  // where the two pipelines' runs begin: each thread counts the tiles of some
+  // sequences, and the one that holds a run's first tile writes it down
+  {
+    const int per = (int)((p.batch + kTreeThreads - 1) / kTreeThreads);
+    const int b0 = tid * per, b1 = (int)min((int64_t)b0 + per, p.batch);
+    int64_t mine = 0, total;
+    for (int b = b0; b < b1; ++b) mine += (int64_t)wk.tiles(p, wk.context(p, b), BN) * wk.KM;
+    int64_t at = tree_scan(mine, scratch, &total);
+    const int64_t share = tree_share(total, nslots, g.min_tiles);
+    for (int s = 0; s < 2; ++s) {
+      const int64_t start = (slot0 + s) * share;
+      if (start < at || start >= at + mine) continue;
+      int64_t off = start - at;
+      for (int b = b0; b < b1; ++b) {
+        TreeSeg sg;
+        sg.ctx = wk.context(p, b);
+        sg.T = wk.tiles(p, sg.ctx, BN);
+        const int64_t n = (int64_t)sg.T * wk.KM;
+        if (off >= n) {
+          off -= n;
+          continue;
+        }
+        sg.left = min(share, total - start);
+        sg.b = b;
+        sg.hm = (int)(off / sg.T);
+        sg.t0 = (int)(off % sg.T);
+        tree_seg_fill<D>(sg, p, wk);
+        firsts[s] = sg;
+        break;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *tslot + 256u * w;
+  const TreeSeg first = firsts[w];
+  bool dead = false;  // a wait gave up: no further waits (the kernel still ends)
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!dead) dead = !mbar_wait_bounded(bar, parity, p.err);
+  };
+
+  if (first.left <= 0) {
+    // no run for this pipeline
+  } else if (warp >= 8) {
+    // ------------------------------------------------------ the issuers
+    if (lane == 0) {
+      // the pipeline's tiles in order: tile t0 + j of a piece
+      struct Cur {
+        TreeSeg s;
+        int j;
+        bool ok;
+      };
+      auto settle = [&](Cur& c) {  // to the next piece that has tiles
+        while (c.ok && c.s.tiles == 0) c.ok = tree_seg_next<D>(c.s, p, wk);
+        c.j = 0;
+      };
+      auto begin = [&]() {
+        Cur c{first, 0, true};
+        settle(c);
+        return c;
+      };
+      auto advance = [&](Cur& c) {
+        if (++c.j < c.s.tiles) return;
+        c.ok = tree_seg_next<D>(c.s, p, wk);
+        settle(c);
+      };
+      // loads one tile of K or V through the page table
+      auto load = [&](const CUtensorMap* map, unsigned char* dst, const Cur& c, uint64_t* bar) {
+        const int key0 = (c.s.t0 + c.j) * BN, h = c.s.hm / wk.MT;
+        const int boxes = min(BN, c.s.vis - key0 + g.box - 1) / g.box;  // those that hold keys
+        mbar_arrive_expect_tx(bar, (uint32_t)(boxes * g.box * C::kBoxes * 128));
+        for (int i = 0; i < boxes; ++i) {
+          const int pos = key0 + i * g.box;
+          const int at = pos / p.page;
+          int page = __ldg(p.table + (int64_t)c.s.b * p.width + at);
+          if (page < 0 || page >= p.pages) page = (int)p.pages;  // out of range: zeros
+#pragma unroll
+          for (int b = 0; b < C::kBoxes; ++b)
+            tma_load_4d(dst + b * C::kKVBox + i * g.box * 128, map, 64 * b, h, pos - at * p.page,
+                        page, bar);
+        }
+      };
+      if (warp >= 10) {
+        // V loads and O += P V
+        Cur vc = begin(), c = vc;
+        int vt = 0;
+        auto load_v = [&]() {
+          load(&tv, stage_v(vt & 1), vc, &bar_vfull[vt & 1]);
+          ++vt;
+          advance(vc);
+        };
+        if (c.ok) {
+          load_v();
+          if (vc.ok) load_v();
+        }
+        int r = 0;  // pieces begun
+        for (int t = 0; c.ok && !dead; ++t) {
+          if (vc.ok && vt == t + 1 && t >= 1) {
+            wait_spin(&bar_vempty[(t - 1) & 1], (uint32_t)(((t - 1) >> 1) & 1), dead, p.err);
+            if (!dead) load_v();
+          }
+          if (c.j == 0 && r++ > 0) wait_spin(bar_ofree, (uint32_t)(r & 1), dead, p.err);
+          wait_spin(&bar_p[t % C::NPB], (uint32_t)((t / C::NPB) & 1), dead, p.err);
+          wait_spin(&bar_vfull[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
+          const uint32_t v_addr = smem_addr(stage_v(t & 1));
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(tm + C::kColO, tm + C::kColP + (t % C::NPB) * (BN / 2) + 8 * kk,
+                   sw128_desc(v_addr + kk * 2048, C::kKVBox, 1024), C::kIdescO,
+                   (c.j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&bar_o[t % C::NPB]);
+          mma_commit(&bar_vempty[t & 1]);
+          advance(c);
+        }
+      } else {
+        // K loads and S = Q K^T
+        Cur kc = begin(), c = kc;
+        int kt = 0;
+        auto load_k = [&]() {
+          load(&tk, stage_k(kt & 1), kc, &bar_kfull[kt & 1]);
+          ++kt;
+          advance(kc);
+        };
+        if (c.ok) {
+          load_k();
+          if (kc.ok) load_k();
+        }
+        int r = 0;
+        for (int t = 0; c.ok && !dead; ++t) {
+          // S(t) once the softmax has read S(t - 1); a new piece's Q is then there
+          if (t >= 1) wait_spin(bar_sfree, (uint32_t)((t - 1) & 1), dead, p.err);
+          if (c.j == 0) wait_spin(bar_q, (uint32_t)(r++ & 1), dead, p.err);
+          wait_spin(&bar_kfull[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
+          const uint32_t q_addr = smem_addr(sq), k_addr = smem_addr(stage_k(t & 1));
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t qo = (uint32_t)((kk >> 2) * C::kQBox + (kk & 3) * 32);
+            const uint32_t ko = (uint32_t)((kk >> 2) * C::kKVBox + (kk & 3) * 32);
+            mma_ss(tm + C::kColS, sw128_desc(q_addr + qo, 16, 1024),
+                   sw128_desc(k_addr + ko, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(bar_s);
+          mma_commit(&bar_kempty[t & 1]);
+          if (kc.ok) {  // K(t + 2) into the stage S(t) used
+            wait_spin(&bar_kempty[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
+            if (!dead) load_k();
+          }
+          advance(c);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------ softmax warpgroup
+    const int row = tid & 127;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tm + lane_base + C::kColS;
+    const uint32_t tO = tm + lane_base + C::kColO;
+    const float sc = p.scale_log2;
+    const int slot = slot0 + w;
+    const int all_rows = p.nodes * wk.G, ws_rows = min(all_rows, kTM);
+    float* ws_o = p.ws;
+    float2* ws_ml = reinterpret_cast<float2*>(p.ws + (int64_t)g.max_slots * 2 * ws_rows * D);
+    uint32_t* mask = masks + row * kMaskStride;
+    TreeSeg s = first;
+    int t = 0;        // tiles done by this pipeline
+    int piece = 0;    // pieces seen
+    bool more = true;
+    for (; more; more = tree_seg_next<D>(s, p, wk)) {
+      const bool cut0 = piece == 0 && s.t0 > 0, cut1 = s.t1 < s.T;
+      ++piece;
+      const int h = s.hm / wk.MT, mt = s.hm % wk.MT;
+      const int R = mt * kTM + row;
+      const bool live = R < all_rows;
+      const bool wlive = mt * kTM + 32 * (warp & 3) < all_rows;  // some row of this warp
+      const int node = live ? R / wk.G : 0, head = h * wk.G + (live ? R % wk.G : 0);
+      const int64_t out = ((int64_t)s.b * p.nodes + node) * p.heads + head;
+      bool present = live;
+      float m = -INFINITY, l = 0.f;
+      if (s.tiles > 0) {
+        // Q: this thread's row into its place of the swizzled tile
+        if (live) {
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + out * D * 2);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c)
+            *reinterpret_cast<uint4*>(sq + (c >> 3) * C::kQBox + row * 128 +
+                                      (((c & 7) ^ (row & 7)) << 4)) = __ldg(src + c);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar_q);
+        if (p.parents != nullptr) {
+          const int32_t* par = p.parents + (int64_t)s.b * p.nodes;
+          for (int i = 0; i < kMaskStride; ++i) mask[i] = 0;
+          for (int a = node; a >= 0 && present;) {
+            mask[a >> 5] |= 1u << (a & 31);
+            const int up = __ldg(par + a);
+            if (up < -1 || up >= a) present = false;
+            a = up;
+          }
+        }
+        // pages that do not exist: none in the pieces of a sound table
+        bool holes = false;
+        {
+          const int last = min((s.t0 + s.tiles) * BN, s.vis) - 1;
+          for (int i = s.t0 * BN / p.page + lane; i <= last / p.page; i += 32) {
+            const int page = __ldg(p.table + (int64_t)s.b * p.width + i);
+            holes = holes || page < 0 || page >= p.pages;
+          }
+          holes = __any_sync(0xffffffffu, holes);
+        }
+        bool tail_seen = false;
+        for (int j = 0; j < s.tiles; ++j, ++t) {
+          const int key0 = (s.t0 + j) * BN;
+          const bool tail = key0 + BN > min(s.ctx, s.vis);
+          wait(bar_s, (uint32_t)(t & 1));
+          tc_fence_after();
+          uint32_t v[BN / 32][32];
+          if (wlive) {
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) tmem_ld32_nowait(tS + 32 * c, v[c]);
+            tmem_ld_wait();
+          }
+          tc_fence_before();
+          mbar_arrive(bar_sfree);
+          if (tail) {
+            // V at positions nobody may see, and non-finite values at nodes: 0
+            tail_seen = true;
+            wait(&bar_vfull[t & 1], (uint32_t)((t >> 1) & 1));
+            const int vr = row % BN, pos = key0 + vr;
+            if (pos >= s.ctx || pos >= s.vis) {
+              uint4* vp = reinterpret_cast<uint4*>(stage_v(t & 1) + row / BN * C::kKVBox + vr * 128);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                if (pos >= s.vis) {
+                  vp[c] = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                  uint4 x = vp[c];
+                  if (odd_bf16x2(x.x) || odd_bf16x2(x.y) || odd_bf16x2(x.z) || odd_bf16x2(x.w)) {
+                    for (int i = 0; i < 4; ++i) {
+                      uint32_t y = word_of(x, i);
+                      if ((y & 0x7f80u) == 0x7f80u) y &= 0xffff0000u;
+                      if ((y & 0x7f800000u) == 0x7f800000u) y &= 0xffffu;
+                      set_word(x, i, y);
+                    }
+                    vp[c] = x;
+                    *odd = piece;
+                  }
+                }
+              }
+            }
+            fence_proxy_async_smem();
+          }
+          if (wlive) {
+            if (tail || holes) {
+#pragma unroll
+              for (int c = 0; c < BN / 32; ++c) {
+                const int pos = key0 + 32 * c;   // of bit 0
+                const int nb = pos - s.ctx;      // its node
+                uint32_t bits = 0xffffffffu;
+                if (p.parents != nullptr) {
+                  if (nb >= 0)
+                    bits = nb >> 5 < kMaskStride - 1
+                               ? __funnelshift_r(mask[nb >> 5], mask[(nb >> 5) + 1], nb & 31)
+                               : 0u;
+                  else if (nb > -32)
+                    bits = (mask[0] << -nb) | ((1u << -nb) - 1u);
+                }
+                const int lim = p.parents != nullptr ? s.vis : min(s.ctx + node + 1, s.vis);
+                if (lim - pos <= 0) bits = 0;
+                else if (lim - pos < 32) bits &= (1u << (lim - pos)) - 1u;
+                if (holes) {
+                  for (int i = 0; i < 32; i += 16) {
+                    if (pos + i >= s.vis) break;
+                    const int page = __ldg(p.table + (int64_t)s.b * p.width + (pos + i) / p.page);
+                    if (page < 0 || page >= p.pages) bits &= ~(0xffffu << i);
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!((bits >> i) & 1)) v[c][i] = __float_as_uint(-INFINITY);
+              }
+            }
+            float mx[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx[k] = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) mx[i & 7] = fmaxf(mx[i & 7], __uint_as_float(v[c][i]));
+            const float mx0 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const float mx1 = fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+            // m moves only by more than 8 (k_attn.cu); a row that has seen no key
+            // keeps m = -inf and takes its exponentials (all 0) from 0
+            const float mt_ = fmaxf(mx0, mx1) * sc;
+            const float m_new = mt_ > m + 8.f ? mt_ : m;
+            const float alpha = m_new == m ? 1.f : ex2(m - m_new);
+            const float mref = m_new == -INFINITY ? 0.f : m_new;
+            float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+            uint32_t pk[BN / 32][16];
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                float t0, t1, t2, t3;
+                fma2(t0, t1, __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]), sc, sc, -mref,
+                     -mref);
+                fma2(t2, t3, __uint_as_float(v[c][i + 2]), __uint_as_float(v[c][i + 3]), sc, sc,
+                     -mref, -mref);
+                const float p0 = ex2(t0), p1 = ex2(t1), p2 = ex2(t2), p3 = ex2(t3);
+                add2(l0, l1, l0, l1, p0, p1);
+                add2(l2, l3, l2, l3, p2, p3);
+                pk[c][i >> 1] = pack_bf16(p0, p1);
+                pk[c][(i >> 1) + 1] = pack_bf16(p2, p3);
+              }
+            l = l * alpha + ((l0 + l1) + (l2 + l3));
+            m = m_new;
+            if (t >= C::NPB) {
+              wait(&bar_o[t % C::NPB], (uint32_t)((t / C::NPB - 1) & 1));
+              tc_fence_after();
+            }
+            const uint32_t tP = tm + lane_base + C::kColP + (t % C::NPB) * (BN / 2);
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) tmem_st16(tP + 16 * c, pk[c]);
+            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+              if constexpr (C::NPB > 1) {
+                wait(&bar_o[(t - 1) % C::NPB], (uint32_t)(((t - 1) / C::NPB) & 1));
+                tc_fence_after();
+              }
+              uint32_t o[D / 32][32];
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) tmem_ld32_nowait(tO + 32 * c, o[c]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  float a0, a1;
+                  mul2(a0, a1, __uint_as_float(o[c][i]), __uint_as_float(o[c][i + 1]), alpha,
+                       alpha);
+                  o[c][i] = __float_as_uint(a0);
+                  o[c][i + 1] = __float_as_uint(a1);
+                }
+                tmem_st32(tO + 32 * c, o[c]);
+              }
+            }
+            tmem_st_wait();
+          } else if (t >= C::NPB) {
+            // a warp without rows keeps pace: its arrival below must not fall into
+            // the P buffer's previous phase
+            wait(&bar_o[t % C::NPB], (uint32_t)((t / C::NPB - 1) & 1));
+          }
+          tc_fence_before();
+          mbar_arrive(&bar_p[t % C::NPB]);
+        }
+        wait(&bar_o[(t - 1) % C::NPB], (uint32_t)(((t - 1) / C::NPB) & 1));
+        tc_fence_after();
+        uint32_t o[D / 32][32];
+        if (wlive) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) tmem_ld32_nowait(tO + 32 * c, o[c]);
+          tmem_ld_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(bar_ofree);
+        if (tail_seen) named_bar(1 + w, 128);  // every thread's look at V
+        if (!present) {
+          m = -INFINITY;
+          l = 0.f;
+        }
+        if (l == 0.f) {  // (nothing seen: the accumulator holds nothing of this row's)
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[c][i] = 0u;
+        }
+        if (tail_seen && *odd == piece && present) {
+          // add the non-finite values of V that this row sees
+          const int lo = max(s.ctx, s.t0 * BN), hi = min((s.t0 + s.tiles) * BN, s.vis);
+          for (int pos = lo; pos < hi; ++pos) {
+            const int j = pos - s.ctx;
+            if (p.parents != nullptr ? !((mask[j >> 5] >> (j & 31)) & 1) : j > node) continue;
+            const int page = __ldg(p.table + (int64_t)s.b * p.width + pos / p.page);
+            if (page < 0 || page >= p.pages) continue;
+            const uint4* vp = reinterpret_cast<const uint4*>(
+                p.v + (((int64_t)page * p.page + pos % p.page) * p.kv_heads + h) * D * 2);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              const uint4 x = __ldg(vp + c);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float f = chunk_get<kBF16>(x, i);
+                if (!(fabsf(f) < INFINITY)) {
+                  uint32_t& y = o[c >> 2][(c & 3) * 8 + i];
+                  y = __float_as_uint(__uint_as_float(y) + f);
+                }
+              }
+            }
+          }
+        }
+        if (live && !cut0 && !cut1) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          uint4* dst = reinterpret_cast<uint4*>(p.o + out * D * 2);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint32_t* oc = &o[c >> 2][(c & 3) * 8];
+            dst[c] = make_uint4(
+                pack_bf16(__uint_as_float(oc[0]) * inv, __uint_as_float(oc[1]) * inv),
+                pack_bf16(__uint_as_float(oc[2]) * inv, __uint_as_float(oc[3]) * inv),
+                pack_bf16(__uint_as_float(oc[4]) * inv, __uint_as_float(oc[5]) * inv),
+                pack_bf16(__uint_as_float(oc[6]) * inv, __uint_as_float(oc[7]) * inv));
+          }
+          if (p.lse != nullptr)
+            p.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
+        if (live && (cut0 || cut1)) {
+          const int64_t at = tree_part(slot, piece > 1, ws_rows, row);
+          uint4* dst = reinterpret_cast<uint4*>(ws_o + at * D);
+#pragma unroll
+          for (int c = 0; c < D / 4; ++c) {
+            const uint32_t* oc = &o[c >> 3][(c & 7) * 4];
+            dst[c] = make_uint4(oc[0], oc[1], oc[2], oc[3]);
+          }
+          ws_ml[at] = make_float2(m, l);
+        }
+      } else if (live) {
+        // nothing of these tiles is visible to the row tile
+        if (cut0 || cut1)
+          ws_ml[tree_part(slot, piece > 1, ws_rows, row)] = make_float2(-INFINITY, 0.f);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tslot), "r"(512u)
+                 : "memory");
+}
+
+// Joins the pieces of items cut by runs, and writes the rows of sequences that
+// have no tile at all.  One warp per row: a block takes 8 rows of one item.
+constexpr int kJoinT = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, const TreeGeo g) {
+  constexpr int BN = TreePL<D>::BN, V = D / 32;
+  __shared__ int64_t scratch[16], s_before;
+  const TreeWork wk(p);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t item = blockIdx.x;
+  const int b = (int)(item / wk.KM), hm = (int)(item % wk.KM);
+  // tiles before this sequence, and of all
+  const int per = (int)((p.batch + kJoinT - 1) / kJoinT);
+  const int b0 = tid * per, b1 = (int)min((int64_t)b0 + per, p.batch);
+  int64_t mine = 0, total;
+  for (int i = b0; i < b1; ++i) mine += (int64_t)wk.tiles(p, wk.context(p, i), BN) * wk.KM;
+  int64_t at = tree_scan(mine, scratch, &total);
+  if (b >= b0 && b < b1) {
+    for (int i = b0; i < b; ++i) at += (int64_t)wk.tiles(p, wk.context(p, i), BN) * wk.KM;
+    s_before = at;
+  }
+  __syncthreads();
+  const int T = wk.tiles(p, wk.context(p, b), BN);
+  const int64_t share = tree_share(total, g.max_slots, g.min_tiles);
+  const int64_t start = s_before + (int64_t)hm * T;
+  const int64_t s0 = start / share, s1 = (start + T - 1) / share;
+  if (T > 0 && s0 == s1) return;  // finished by its run
+  const int all_rows = p.nodes * wk.G, ws_rows = min(all_rows, kTM);
+  const int h = hm / wk.MT, mt = hm % wk.MT;
+  const int row = (int)blockIdx.y * (kJoinT / 32) + (tid >> 5), R = mt * kTM + row;
+  if (row >= kTM || R >= all_rows) return;
+  const int64_t out = ((int64_t)b * p.nodes + R / wk.G) * p.heads + h * wk.G + R % wk.G;
+  const float* ws_o = p.ws;
+  const float2* ws_ml =
+      reinterpret_cast<const float2*>(p.ws + (int64_t)g.max_slots * 2 * ws_rows * D);
+  // the item's piece in a run is its last if it begins inside the run
+  auto place = [&](int64_t s) { return tree_part((int)s, s * share < start ? 1 : 0, ws_rows, row); };
+  float M = -INFINITY;
+  const int64_t n = T > 0 ? s1 - s0 + 1 : 0;
+  for (int64_t i = lane; i < n; i += 32) M = fmaxf(M, ws_ml[place(s0 + i)].x);
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float L = 0.f, o[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = 0.f;
+#pragma unroll 4
+  for (int64_t i = 0; i < n; ++i) {
+    const int64_t pl = place(s0 + i);
+    const float2 ml = ws_ml[pl];
+    if (ml.y == 0.f) continue;  // a piece in which the row sees nothing
+    const float a = ml.x == M ? 1.f : ex2(ml.x - M);
+    L += ml.y * a;
+    const float* src = ws_o + pl * D + lane * V;
+#pragma unroll
+    for (int c = 0; c < V; ++c) o[c] = fmaf(src[c], a, o[c]);
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  char* dst = p.o + out * D * 2 + lane * V * 2;
+#pragma unroll
+  for (int c = 0; c < V; c += 2)
+    *reinterpret_cast<uint32_t*>(dst + 2 * c) = pack_bf16(o[c] * inv, o[c + 1] * inv);
+  if (lane == 0 && p.lse != nullptr) p.lse[out] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
 }  // namespace
 
 const void* tree_rows_kernel(int d) {
   return d == 64    ? (const void*)tree_rows_kernel_t<64>
          : d == 128 ? (const void*)tree_rows_kernel_t<128>
                     : nullptr;
+}
+
+TreeKernels tree_kernels(int d) {
+  if (d == 64)
+    return {(const void*)tree_tc_kernel<64>, (const void*)tree_join_kernel<64>, kTreeThreads,
+            TreePL<64>::kSmem, TreePL<64>::BN};
+  return {(const void*)tree_tc_kernel<128>, (const void*)tree_join_kernel<128>, kTreeThreads,
+          TreePL<128>::kSmem, TreePL<128>::BN};
+}
+
+const char* tree_tc_launch(const TreeParams& p, int d, int sms, cudaStream_t stream) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return "cuTensorMapEncodeTiled is not available from the driver";
+  const TreeKernels tk = tree_kernels(d);
+  TreeGeo g{};
+  g.box = 16;
+  while (g.box < tk.bn && p.page % (2 * g.box) == 0) g.box *= 2;
+  g.min_tiles = kTreeMinTiles;
+  CUtensorMap maps[2];
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)p.kv_heads, (cuuint64_t)p.page,
+                              (cuuint64_t)p.pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)p.kv_heads * d * 2,
+                                 (cuuint64_t)p.page * p.kv_heads * d * 2};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)g.box, 1}, es[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 2; ++i)
+    if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<char*>(i ? p.v : p.k),
+               dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return "tensor map encoding failed";
+  const int G = p.heads / p.kv_heads;
+  const int64_t rows = (int64_t)p.nodes * G, mt = (rows + kTM - 1) / kTM;
+  g.max_slots = 2 * sms;
+  TreeParams pc = p;
+  void* args[] = {&maps[0], &maps[1], &pc, &g};
+  if (cudaLaunchKernel(tk.main, dim3((unsigned)sms), dim3((unsigned)tk.threads), args,
+                       (size_t)tk.smem, stream) != cudaSuccess)
+    return "launch failed";
+  void* jargs[] = {&pc, &g};
+  const int64_t items = p.batch * p.kv_heads * mt;
+  const unsigned groups = (unsigned)((std::min<int64_t>(rows, kTM) + kJoinT / 32 - 1) / (kJoinT / 32));
+  if (cudaLaunchKernel(tk.join, dim3((unsigned)items, groups), dim3(kJoinT), jargs, 0, stream) !=
+      cudaSuccess)
+    return "join launch failed";
+  return nullptr;
+}
+
+size_t tree_ws_bytes(int64_t nodes, int heads, int kv_heads, int d, int sms) {
+  const int64_t rows = std::min<int64_t>(nodes * (heads / kv_heads), kTM);
+  return (size_t)(2 * sms) * 2 * rows * (d + 2) * sizeof(float);
 }
 
 }  // namespace rr

@@ -1394,12 +1394,26 @@ rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
 
 rr_status tree_launch(rr::TreeParams p, int d, cudaStream_t stream) {
   const int64_t rows = p.batch * p.nodes * p.heads;
+  const bool tc = p.page % 16 == 0 && p.pages > 0;
+  int sms = 0;
   {
     std::lock_guard<std::mutex> lock(g_mu);
     DevInfo* di = nullptr;
     rr_status st = device_info(&di);
     if (st != RR_OK) return st;
     p.err = di->err;
+    sms = di->sms;
+    const rr::TreeKernels tk = rr::tree_kernels(d);
+    if (tk.smem > di->smem_optin)
+      return fail(RR_ERR_INVALID_ARG, "attention tile exceeds shared memory");
+    if (tc && (st = set_smem(di, tk.main, (size_t)tk.smem)) != RR_OK) return st;
+  }
+  if (tc) {
+    if (const char* why = rr::tree_tc_launch(p, d, sms, stream)) {
+      cudaError_t e = cudaGetLastError();
+      return fail(RR_ERR_CUDA, "tree attention: %s (%s)", why, cudaGetErrorString(e));
+    }
+    return ok();
   }
   void* args[] = {&p};
   cudaError_t e = cudaLaunchKernel(rr::tree_rows_kernel(d), dim3((unsigned)cdiv(rows, 4)),
@@ -2182,7 +2196,12 @@ static rr_status tree_shape(int64_t batch, int64_t nodes, int64_t heads, int64_t
 
 size_t rr_attention_tree_workspace_size(int64_t batch, int64_t nodes, int64_t heads,
                                         int64_t kv_heads, int64_t head_dim) {
-  return tree_shape(batch, nodes, heads, kv_heads, head_dim) == RR_OK ? 0 : 0;
+  if (tree_shape(batch, nodes, heads, kv_heads, head_dim) != RR_OK) return 0;
+  if (batch == 0 || nodes == 0) return 0;
+  std::lock_guard<std::mutex> lock(g_mu);
+  DevInfo* di = nullptr;
+  if (device_info(&di) != RR_OK) return 0;
+  return rr::tree_ws_bytes(nodes, (int)heads, (int)kv_heads, (int)head_dim, di->sms);
 }
 
 rr_status rr_attention_tree_fwd(const void* q, const void* k_cache, const void* v_cache,
@@ -2197,7 +2216,7 @@ rr_status rr_attention_tree_fwd(const void* q, const void* k_cache, const void* 
   rr_status st = tree_shape(batch, nodes, heads, kv_heads, head_dim);
   if (st != RR_OK) return st;
   if (pages < 0 || page_size < 1 || table_width < 0 || pages > INT32_MAX ||
-      page_size > (1 << 24) || table_width > INT32_MAX / page_size)
+      page_size > (1 << 24) || table_width > (1 << 30) / page_size)
     return fail(RR_ERR_INVALID_ARG, "bad cache shape");
   if (pages > ((int64_t)1 << 58) / (page_size * kv_heads * head_dim))
     return fail(RR_ERR_INVALID_ARG, "cache too large");

@@ -276,6 +276,26 @@ struct TreeParams {
 };
 constexpr int kTreeMaxNodes = 256;  // with parents (one mask bit a node)
 const void* tree_rows_kernel(int d);
+struct TreeGeo {
+  int32_t box;        // positions of one tensor-map box
+  int32_t min_tiles;  // fewest key tiles of a run
+  int32_t max_slots;  // pipelines
+};
+// fewest key tiles a pipeline takes: a shorter run would cost more in its
+// piece's trip through the workspace than it saves
+constexpr int kTreeMinTiles = 4;
+struct TreeKernels {
+  const void* main;
+  const void* join;
+  int threads;
+  int smem;
+  int bn;  // keys per tile
+};
+TreeKernels tree_kernels(int d);
+// Encodes the tensor maps and launches the two kernels (`sms` blocks): null on
+// success, else a short reason.
+const char* tree_tc_launch(const TreeParams& p, int d, int sms, cudaStream_t stream);
+size_t tree_ws_bytes(int64_t nodes, int heads, int kv_heads, int d, int sms);
 
 // The column reduce's split of its 32 warps over the P partial rows: the
 // smallest power of two >= P / 16, at most 32 (the rest of the warps take
