@@ -232,10 +232,41 @@ __device__ __forceinline__ bool odd_bf16x2(uint32_t w) {  // an infinity or NaN 
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
+// Adds to columns [32 c, 32 c + 32) of a row's output the non-finite values of V
+// at the nodes of piece s that its node sees (a rare path, kept out of line).
+__device__ __noinline__ void tree_add_odd_at(const TreeParams& p, int b, int ctx, int lo, int hi,
+                                             int h, int node, const uint32_t* mask, int D, int c,
+                                             float* o) {
+  for (int pos = lo; pos < hi; ++pos) {
+    const int j = pos - ctx;
+    if (p.parents != nullptr ? !((mask[j >> 5] >> (j & 31)) & 1) : j > node) continue;
+    const int page = __ldg(p.table + (int64_t)b * p.width + pos / p.page);
+    if (page < 0 || page >= p.pages) continue;
+    const char* v = p.v + ((((int64_t)page * p.page + pos % p.page) * p.kv_heads + h) * D + 32 * c) * 2;
+    for (int i = 0; i < 32; ++i) {
+      const float f = ld_elem_cached<kBF16>(v + 2 * i);
+      if (!(fabsf(f) < INFINITY)) o[i] += f;
+    }
+  }
+}
+__device__ __forceinline__ void tree_add_odd(const TreeParams& p, const TreeSeg& s,
+                                             const TreeWork&, int h, int node,
+                                             const uint32_t* mask, int D, int BN, int c,
+                                             uint32_t (&o)[32]) {
+  float f[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = 0.f;
+  tree_add_odd_at(p, s.b, s.ctx, max(s.ctx, s.t0 * BN), min((s.t0 + s.tiles) * BN, s.vis), h,
+                  node, mask, D, c, f);
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (f[i] != 0.f) o[i] = __float_as_uint(__uint_as_float(o[i]) + f[i]);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                   const TreeParams p, const TreeGeo g) {
+                   const __grid_constant__ TreeParams p, const TreeGeo g) {
   using C = TreePL<D>;
   constexpr int BN = C::BN;
   extern __shared__ unsigned char smem_raw[];
@@ -475,12 +506,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       float m = -INFINITY, l = 0.f;
       if (s.tiles > 0) {
         // Q: this thread's row into its place of the swizzled tile
-        if (live) {
+        // (zeros for the rows of a live warp beyond the last)
+        if (wlive) {
           const uint4* src = reinterpret_cast<const uint4*>(p.q + out * D * 2);
 #pragma unroll
           for (int c = 0; c < D / 8; ++c)
             *reinterpret_cast<uint4*>(sq + (c >> 3) * C::kQBox + row * 128 +
-                                      (((c & 7) ^ (row & 7)) << 4)) = __ldg(src + c);
+                                      (((c & 7) ^ (row & 7)) << 4)) =
+                live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
         mbar_arrive(bar_q);
@@ -622,21 +655,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 wait(&bar_o[(t - 1) % C::NPB], (uint32_t)(((t - 1) / C::NPB) & 1));
                 tc_fence_after();
               }
-              uint32_t o[D / 32][32];
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) tmem_ld32_nowait(tO + 32 * c, o[c]);
-              tmem_ld_wait();
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32_nowait(tO + 32 * c, o);
+                tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
                   float a0, a1;
-                  mul2(a0, a1, __uint_as_float(o[c][i]), __uint_as_float(o[c][i + 1]), alpha,
-                       alpha);
-                  o[c][i] = __float_as_uint(a0);
-                  o[c][i + 1] = __float_as_uint(a1);
+                  mul2(a0, a1, __uint_as_float(o[i]), __uint_as_float(o[i + 1]), alpha, alpha);
+                  o[i] = __float_as_uint(a0);
+                  o[i + 1] = __float_as_uint(a1);
                 }
-                tmem_st32(tO + 32 * c, o[c]);
+                tmem_st32(tO + 32 * c, o);
               }
             }
             tmem_st_wait();
@@ -650,74 +681,48 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         wait(&bar_o[(t - 1) % C::NPB], (uint32_t)(((t - 1) / C::NPB) & 1));
         tc_fence_after();
-        uint32_t o[D / 32][32];
-        if (wlive) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) tmem_ld32_nowait(tO + 32 * c, o[c]);
-          tmem_ld_wait();
-        }
-        tc_fence_before();
-        mbar_arrive(bar_ofree);
         if (tail_seen) named_bar(1 + w, 128);  // every thread's look at V
+        const bool fix = tail_seen && *odd == piece && present;
         if (!present) {
           m = -INFINITY;
           l = 0.f;
         }
-        if (l == 0.f) {  // (nothing seen: the accumulator holds nothing of this row's)
+        const bool whole = !cut0 && !cut1;
+        const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        const int64_t at = whole ? 0 : tree_part(slot, piece > 1, ws_rows, live ? row : 0);
+        // O in 32 columns at a time (few registers: the loop above keeps the rest)
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          if (!wlive) break;
+          uint32_t o[32];
+          tmem_ld32_nowait(tO + 32 * c, o);
+          tmem_ld_wait();
+          if (l == 0.f) {  // (nothing seen: the accumulator holds nothing of this row's)
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c)
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+          }
+          if (fix) tree_add_odd(p, s, wk, h, node, mask, D, BN, c, o);
+          if (live && whole) {
+            uint4* dst = reinterpret_cast<uint4*>(p.o + (out * D + 32 * c) * 2);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[c][i] = 0u;
-        }
-        if (tail_seen && *odd == piece && present) {
-          // add the non-finite values of V that this row sees
-          const int lo = max(s.ctx, s.t0 * BN), hi = min((s.t0 + s.tiles) * BN, s.vis);
-          for (int pos = lo; pos < hi; ++pos) {
-            const int j = pos - s.ctx;
-            if (p.parents != nullptr ? !((mask[j >> 5] >> (j & 31)) & 1) : j > node) continue;
-            const int page = __ldg(p.table + (int64_t)s.b * p.width + pos / p.page);
-            if (page < 0 || page >= p.pages) continue;
-            const uint4* vp = reinterpret_cast<const uint4*>(
-                p.v + (((int64_t)page * p.page + pos % p.page) * p.kv_heads + h) * D * 2);
+            for (int i = 0; i < 32; i += 8)
+              dst[i >> 3] = make_uint4(
+                  pack_bf16(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv),
+                  pack_bf16(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv),
+                  pack_bf16(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv),
+                  pack_bf16(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv));
+          } else if (live) {
+            uint4* dst = reinterpret_cast<uint4*>(ws_o + at * D + 32 * c);
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              const uint4 x = __ldg(vp + c);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float f = chunk_get<kBF16>(x, i);
-                if (!(fabsf(f) < INFINITY)) {
-                  uint32_t& y = o[c >> 2][(c & 3) * 8 + i];
-                  y = __float_as_uint(__uint_as_float(y) + f);
-                }
-              }
-            }
+            for (int i = 0; i < 32; i += 4)
+              dst[i >> 2] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
-        if (live && !cut0 && !cut1) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          uint4* dst = reinterpret_cast<uint4*>(p.o + out * D * 2);
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint32_t* oc = &o[c >> 2][(c & 3) * 8];
-            dst[c] = make_uint4(
-                pack_bf16(__uint_as_float(oc[0]) * inv, __uint_as_float(oc[1]) * inv),
-                pack_bf16(__uint_as_float(oc[2]) * inv, __uint_as_float(oc[3]) * inv),
-                pack_bf16(__uint_as_float(oc[4]) * inv, __uint_as_float(oc[5]) * inv),
-                pack_bf16(__uint_as_float(oc[6]) * inv, __uint_as_float(oc[7]) * inv));
-          }
-          if (p.lse != nullptr)
-            p.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        }
-        if (live && (cut0 || cut1)) {
-          const int64_t at = tree_part(slot, piece > 1, ws_rows, row);
-          uint4* dst = reinterpret_cast<uint4*>(ws_o + at * D);
-#pragma unroll
-          for (int c = 0; c < D / 4; ++c) {
-            const uint32_t* oc = &o[c >> 3][(c & 7) * 4];
-            dst[c] = make_uint4(oc[0], oc[1], oc[2], oc[3]);
-          }
-          ws_ml[at] = make_float2(m, l);
-        }
+        tc_fence_before();
+        mbar_arrive(bar_ofree);
+        if (live && whole && p.lse != nullptr)
+          p.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (live && !whole) ws_ml[at] = make_float2(m, l);
       } else if (live) {
         // nothing of these tiles is visible to the row tile
         if (cut0 || cut1)
