@@ -775,24 +775,54 @@ __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, c
       reinterpret_cast<const float2*>(p.ws + (int64_t)g.max_slots * 2 * ws_rows * D);
   // the item's piece in a run is its last if it begins inside the run
   auto place = [&](int64_t s) { return tree_part((int)s, s * share < start ? 1 : 0, ws_rows, row); };
-  float M = -INFINITY;
-  const int64_t n = T > 0 ? s1 - s0 + 1 : 0;
-  for (int64_t i = lane; i < n; i += 32) M = fmaxf(M, ws_ml[place(s0 + i)].x);
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  float L = 0.f, o[V];
+  // lanes take the pieces' maxima and sums, 32 pieces at a time; their outputs
+  // then come four loads at once, a piece in which the row sees nothing (it has
+  // no output) with weight 0
+  const int n = T > 0 ? (int)(s1 - s0) + 1 : 0;
+  float M = -INFINITY, L = 0.f, o[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.f;
-#pragma unroll 4
-  for (int64_t i = 0; i < n; ++i) {
-    const int64_t pl = place(s0 + i);
-    const float2 ml = ws_ml[pl];
-    if (ml.y == 0.f) continue;  // a piece in which the row sees nothing
-    const float a = ml.x == M ? 1.f : ex2(ml.x - M);
-    L += ml.y * a;
-    const float* src = ws_o + pl * D + lane * V;
+  for (int base = 0; base < n; base += 32) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (base + lane < n) ml = ws_ml[place(s0 + base + lane)];
+    float mx = ml.x;
 #pragma unroll
-    for (int c = 0; c < V; ++c) o[c] = fmaf(src[c], a, o[c]);
+    for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    mx = fmaxf(mx, M);
+    const float keep = M == mx ? 1.f : ex2(M - mx);
+    M = mx;
+    const float a = ml.y == 0.f ? 0.f : ml.x == M ? 1.f : ex2(ml.x - M);
+    float sum = ml.y * a;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    L = L * keep + sum;
+#pragma unroll
+    for (int c = 0; c < V; ++c) o[c] *= keep;
+    const uint32_t full = __ballot_sync(0xffffffffu, ml.y != 0.f);
+    const int m = min(32, n - base);
+    for (int i = 0; i < m; i += 4) {
+      float f[4][V], wt[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        wt[q] = __shfl_sync(0xffffffffu, a, i + q);
+#pragma unroll
+        for (int c = 0; c < V; ++c) f[q][c] = 0.f;
+        if ((full >> (i + q)) & 1) {
+          const float* src = ws_o + place(s0 + base + i + q) * D + lane * V;
+          if constexpr (V == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            f[q][0] = x.x, f[q][1] = x.y, f[q][2] = x.z, f[q][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            f[q][0] = x.x, f[q][1] = x.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int c = 0; c < V; ++c) o[c] = fmaf(f[q][c], wt[q], o[c]);
+    }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
   char* dst = p.o + out * D * 2 + lane * V * 2;

@@ -40,6 +40,8 @@ def library_path() -> str:
 def load_library():
     """Load librr.so (built by ``__graft_entry__.build()``); raises if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -273,24 +275,30 @@ def rr_rmsnorm_bwd(dy, x, rstd, gamma, dx, dgamma, workspace=None, stream=None):
 def _args(fn, *ts):
     """Checks (name, tensor, dtype or None, shape) tuples of one call: contiguous
     CUDA tensors of that dtype and shape on the current device (a None tensor,
-    an absent argument, passes)."""
+    an absent argument, passes).  Returns their addresses."""
     import torch
+    out = []
     for name, t, dtype, shape in ts:
         if t is None:
+            out.append(None)
             continue
         if dtype is not None and t.dtype != dtype:
             raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{fn}: {name} must be contiguous")
+        out.append(t.data_ptr())
+    dev = -1
     for name, t, _, _ in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{fn}: {name} must be a CUDA tensor")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{fn}: {name} is on {t.device}, not on the current device")
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError(f"{fn}: {name} must be a CUDA tensor")
+            if dev < 0:
+                dev = torch.cuda.current_device()
+            if t.get_device() != dev:
+                raise ValueError(f"{fn}: {name} is on {t.device}, not on the current device")
+    return out
 
 
 def rr_distill_fwd_bwd(logits, top_index, top_value, loss, dlogits=None, grad=None,
@@ -302,19 +310,21 @@ def rr_distill_fwd_bwd(logits, top_index, top_value, loss, dlogits=None, grad=No
     import torch
     rows, cols = logits.shape
     k = top_index.shape[1]
-    _args("rr_distill_fwd_bwd", ("logits", logits, None, (rows, cols)),
-          ("top_index", top_index, torch.int32, (rows, k)),
-          ("top_value", top_value, torch.float32, (rows, k)),
-          ("loss", loss, torch.float32, (rows,)), ("dlogits", dlogits, logits.dtype, (rows, cols)),
-          ("grad", grad, torch.float32, (rows,)),
-          ("bad_index_count", bad_index_count, torch.int32,
-           () if bad_index_count is None else bad_index_count.shape))
+    i32, f32 = torch.int32, torch.float32
+    fn = "rr_distill_fwd_bwd"
     if bad_index_count is not None and bad_index_count.numel() != 1:
-        raise ValueError("rr_distill_fwd_bwd: bad_index_count must hold one value")
-    _check("rr_distill_fwd_bwd", load_library().rr_distill_fwd_bwd(
-        _p(logits), _p(top_index), _p(top_value), _p(grad), _p(loss), _p(dlogits), rows, cols, k,
-        ctypes.c_float(temperature), 1 if tail else 0, _p(bad_index_count), _dtype(logits),
-        _stream(stream)))
+        raise ValueError(f"{fn}: bad_index_count must hold one value")
+    x, i, v, l, d, g, bad = _args(
+        fn, ("logits", logits, None, (rows, cols)), ("top_index", top_index, i32, (rows, k)),
+        ("top_value", top_value, f32, (rows, k)), ("loss", loss, f32, (rows,)),
+        ("dlogits", dlogits, logits.dtype, (rows, cols)), ("grad", grad, f32, (rows,)),
+        ("bad_index_count", bad_index_count, i32,
+         None if bad_index_count is None else bad_index_count.shape))
+    st = load_library().rr_distill_fwd_bwd(x, i, v, g, l, d, rows, cols, k, temperature,
+                                           1 if tail else 0, bad, _dtype(logits),
+                                           _stream(stream))
+    if st != 0:
+        _check(fn, st)
 
 
 def rr_attention_tree_workspace_size(batch: int, nodes: int, heads: int, kv_heads: int,
@@ -338,26 +348,27 @@ def rr_attention_tree_fwd(q, k_cache, v_cache, page_table, context_len, o, lse=N
     b, n, h, d = q.shape
     pages, page_size, kv, _ = k_cache.shape
     width = page_table.shape[1]
-    i32 = torch.int32
+    i32, dt, cache = torch.int32, q.dtype, (pages, page_size, kv, d)
     fn = "rr_attention_tree_fwd"
-    _args(fn, ("q", q, None, (b, n, h, d)), ("k_cache", k_cache, q.dtype, (pages, page_size, kv, d)),
-          ("v_cache", v_cache, q.dtype, (pages, page_size, kv, d)),
-          ("page_table", page_table, i32, (b, width)), ("context_len", context_len, i32, (b,)),
-          ("o", o, q.dtype, (b, n, h, d)), ("lse", lse, torch.float32, (b, n, h)),
-          ("parents", parents, i32, (b, n)))
-    need = rr_attention_tree_workspace_size(b, n, h, kv, d)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    size = 0
-    if workspace is not None:
-        _args(fn, ("workspace", workspace, None, workspace.shape))
-        size = workspace.numel() * workspace.element_size()
+    lib = load_library()
+    pq, pk, pv, pt, pc, po, pl, pp, pw = _args(
+        fn, ("q", q, None, (b, n, h, d)), ("k_cache", k_cache, dt, cache),
+        ("v_cache", v_cache, dt, cache), ("page_table", page_table, i32, (b, width)),
+        ("context_len", context_len, i32, (b,)), ("o", o, dt, (b, n, h, d)),
+        ("lse", lse, torch.float32, (b, n, h)), ("parents", parents, i32, (b, n)),
+        ("workspace", workspace, None, None if workspace is None else workspace.shape))
+    if workspace is None:
+        need = lib.rr_attention_tree_workspace_size(b, n, h, kv, d)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            pw = workspace.data_ptr()
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if scale is None:
         scale = 1.0 / float(d) ** 0.5
-    _check(fn, load_library().rr_attention_tree_fwd(
-        _p(q), _p(k_cache), _p(v_cache), _p(page_table), _p(context_len), _p(parents), _p(o),
-        _p(lse), _p(workspace), size, b, n, h, kv, d, pages, page_size, width,
-        ctypes.c_float(scale), _dtype(q), _stream(stream)))
+    st = lib.rr_attention_tree_fwd(pq, pk, pv, pt, pc, pp, po, pl, pw, size, b, n, h, kv, d, pages,
+                                   page_size, width, scale, _dtype(q), _stream(stream))
+    if st != 0:
+        _check(fn, st)
 
 
 def rr_draft_verify(target_logits, draft_logits, tokens, uniform, race, out_tokens, out_nodes,
@@ -371,18 +382,19 @@ def rr_draft_verify(target_logits, draft_logits, tokens, uniform, race, out_toke
     out_nodes [batch, nodes + 1] and out_count [batch] (int32)."""
     import torch
     b, n1, v = target_logits.shape
-    n = n1 - 1
-    i32, f32 = torch.int32, torch.float32
-    _args("rr_draft_verify", ("target_logits", target_logits, None, (b, n1, v)),
-          ("draft_logits", draft_logits, target_logits.dtype, (b, n, v)),
-          ("tokens", tokens, i32, (b, n)), ("parents", parents, i32, (b, n)),
-          ("uniform", uniform, f32, (b, n)), ("race", race, f32, (b, v)),
-          ("temperature", temperature, f32, (b,)), ("out_tokens", out_tokens, i32, (b, n1)),
-          ("out_nodes", out_nodes, i32, (b, n1)), ("out_count", out_count, i32, (b,)))
-    _check("rr_draft_verify", load_library().rr_draft_verify(
-        _p(target_logits), _p(draft_logits), _p(tokens), _p(parents), _p(uniform), _p(race),
-        _p(temperature), _p(out_tokens), _p(out_nodes), _p(out_count), b, n, v,
-        _dtype(target_logits), _stream(stream)))
+    n, dt, i32, f32 = n1 - 1, target_logits.dtype, torch.int32, torch.float32
+    fn = "rr_draft_verify"
+    pt, pd, pk, pp, pu, pr, pT, ot, on, oc = _args(
+        fn, ("target_logits", target_logits, None, (b, n1, v)),
+        ("draft_logits", draft_logits, dt, (b, n, v)), ("tokens", tokens, i32, (b, n)),
+        ("parents", parents, i32, (b, n)), ("uniform", uniform, f32, (b, n)),
+        ("race", race, f32, (b, v)), ("temperature", temperature, f32, (b,)),
+        ("out_tokens", out_tokens, i32, (b, n1)), ("out_nodes", out_nodes, i32, (b, n1)),
+        ("out_count", out_count, i32, (b,)))
+    st = load_library().rr_draft_verify(pt, pd, pk, pp, pu, pr, pT, ot, on, oc, b, n, v,
+                                        _dtype(target_logits), _stream(stream))
+    if st != 0:
+        _check(fn, st)
 
 
 def rr_read_device_error(device: int = 0, reset: bool = True) -> int:
