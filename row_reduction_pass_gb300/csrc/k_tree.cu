@@ -144,76 +144,82 @@ struct TreePL {
 
 // A piece: the key tiles [t0, t1) of an item, t1 - t0 of its T tiles.
 struct TreeSeg {
-  int64_t left;  // tiles of the run from t0 on
+  int left;   // tiles of the run from t0 on
   int b, hm, t0, t1, T;
   int ctx;    // keys before the nodes
   int vis;    // positions below it may be seen by some row of the tile
   int tiles;  // tiles to work on: those of [t0, t1) below vis
+  int h, mt;  // hm = h * MT + mt
 };
 
-struct TreeWork {
-  int G, MT, KM;  // heads per key head, row tiles per key head, KV * MT
-  int64_t cap;    // positions of the page table
-  __device__ __forceinline__ TreeWork(const TreeParams& p) {
-    G = p.heads / p.kv_heads;
-    MT = (p.nodes * G + kTM - 1) / kTM;
-    KM = p.kv_heads * MT;
-    cap = p.width * (int64_t)p.page;
-  }
-  // keys before the nodes (nodes past the table are not seen wherever they are)
-  __device__ __forceinline__ int context(const TreeParams& p, int b) const {
-    return (int)min((int64_t)max(__ldg(p.length + b), 0), cap);
-  }
-  // key tiles of a sequence
-  __device__ __forceinline__ int tiles(const TreeParams& p, int ctx, int bn) const {
-    return (int)((min((int64_t)ctx + p.nodes, cap) + bn - 1) / bn);
-  }
-};
+// keys before the nodes (nodes past the table are not seen wherever they are)
+__device__ __forceinline__ int tree_context(const TreeParams& p, const TreeGeo& g, int b) {
+  return min(max(__ldg(p.length + b), 0), g.cap);
+}
+// key tiles of a sequence
+template <int BN>
+__device__ __forceinline__ int tree_tiles(const TreeParams& p, const TreeGeo& g, int ctx) {
+  return (min(ctx + p.nodes, g.cap) + BN - 1) / BN;
+}
+// position / page size, and the rest: a shift for the usual powers of two (a
+// division costs an issuing warp about 300 cycles a tile)
+__device__ __forceinline__ int tree_page(const TreeParams& p, const TreeGeo& g, int pos) {
+  return g.page_shift >= 0 ? pos >> g.page_shift : pos / p.page;
+}
+__device__ __forceinline__ int tree_page_row(const TreeParams& p, const TreeGeo& g, int pos) {
+  return g.page_shift >= 0 ? pos & (p.page - 1) : pos % p.page;
+}
 
 // The run of pipeline `slot`: tiles [slot * share, (slot + 1) * share) of all.
-__device__ __forceinline__ int64_t tree_share(int64_t total, int nslots, int min_tiles) {
-  return max((total + nslots - 1) / nslots, (int64_t)min_tiles);
+__device__ __forceinline__ int tree_share(int total, int nslots, int min_tiles) {
+  return max((total + nslots - 1) / nslots, min_tiles);
 }
 
 template <int D>
-__device__ __forceinline__ void tree_seg_fill(TreeSeg& s, const TreeParams& p, const TreeWork& w) {
+__device__ __forceinline__ void tree_seg_fill(TreeSeg& s, const TreeParams& p, const TreeGeo& g) {
   constexpr int BN = TreePL<D>::BN;
-  s.t1 = (int)min((int64_t)s.T, s.t0 + s.left);
-  const int mt = s.hm % w.MT;
-  const int last = min(p.nodes - 1, (mt * kTM + kTM - 1) / w.G);  // the tile's last node
-  s.vis = (int)min((int64_t)s.ctx + (p.parents != nullptr ? p.nodes : last + 1), w.cap);
+  s.t1 = min(s.T, s.t0 + s.left);
+  int last = p.nodes - 1;  // the tile's last node
+  if (p.parents == nullptr && g.MT > 1) last = min(last, (s.mt * kTM + kTM - 1) / g.G);
+  s.vis = min(s.ctx + last + 1, g.cap);
   s.tiles = max(0, min(s.t1, (s.vis + BN - 1) / BN) - s.t0);
 }
 template <int D>
-__device__ __forceinline__ bool tree_seg_next(TreeSeg& s, const TreeParams& p, const TreeWork& w) {
+__device__ __forceinline__ bool tree_seg_next(TreeSeg& s, const TreeParams& p, const TreeGeo& g) {
   s.left -= s.t1 - s.t0;
   if (s.left <= 0) return false;
   s.t0 = 0;
-  if (++s.hm == w.KM) {
-    s.hm = 0;
+  ++s.hm;
+  if (++s.mt == g.MT) {
+    s.mt = 0;
+    ++s.h;
+  }
+  if (s.hm == g.KM) {
+    s.hm = s.h = 0;
     do {  // (a sequence of no tiles has no items; tiles are left, so one comes)
       if (++s.b >= p.batch) return false;
-      s.ctx = w.context(p, s.b);
-      s.T = w.tiles(p, s.ctx, TreePL<D>::BN);
+      s.ctx = tree_context(p, g, s.b);
+      s.T = tree_tiles<TreePL<D>::BN>(p, g, s.ctx);
     } while (s.T == 0);
   }
-  tree_seg_fill<D>(s, p, w);
+  tree_seg_fill<D>(s, p, g);
   return true;
 }
 
 // The sum over the block's threads before this one, and over all (in *total);
 // scratch of 16 values.
-__device__ __forceinline__ int64_t tree_scan(int64_t v, int64_t* scratch, int64_t* total) {
+__device__ __forceinline__ int tree_scan(int v, int* scratch, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  int64_t x = v;
+  int x = v;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+    const int y = __shfl_up_sync(0xffffffffu, x, off);
     if (lane >= off) x += y;
   }
   if (lane == 31) scratch[warp] = x;
   __syncthreads();
-  int64_t before = 0, all = 0;
+  int before = 0, all = 0;
+#pragma unroll 4
   for (int i = 0; i < nw; ++i) {
     if (i < warp) before += scratch[i];
     all += scratch[i];
@@ -249,10 +255,9 @@ __device__ __noinline__ void tree_add_odd_at(const TreeParams& p, int b, int ctx
     }
   }
 }
-__device__ __forceinline__ void tree_add_odd(const TreeParams& p, const TreeSeg& s,
-                                             const TreeWork&, int h, int node,
-                                             const uint32_t* mask, int D, int BN, int c,
-                                             uint32_t (&o)[32]) {
+__device__ __forceinline__ void tree_add_odd(const TreeParams& p, const TreeSeg& s, int h,
+                                             int node, const uint32_t* mask, int D, int BN,
+                                             int c, uint32_t (&o)[32]) {
   float f[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) f[i] = 0.f;
@@ -294,9 +299,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(extra);
   int* odd = reinterpret_cast<int*>(extra + 1) + w;  // the last piece with a non-finite V row
   TreeSeg* firsts = reinterpret_cast<TreeSeg*>(extra + 4);  // [2]
-  int64_t* scratch = reinterpret_cast<int64_t*>(smem + C::kOffScan);
+  int* scratch = reinterpret_cast<int*>(smem + C::kOffScan);
 
-  const TreeWork wk(p);
   const int nslots = 2 * (int)gridDim.x, slot0 = 2 * (int)blockIdx.x;
 
   if (warp == 0) {
@@ -326,30 +330,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   // where the two pipelines' runs begin: each thread counts the tiles of some
   // sequences, and the one that holds a run's first tile writes it down
   {
-    const int per = (int)((p.batch + kTreeThreads - 1) / kTreeThreads);
-    const int b0 = tid * per, b1 = (int)min((int64_t)b0 + per, p.batch);
-    int64_t mine = 0, total;
-    for (int b = b0; b < b1; ++b) mine += (int64_t)wk.tiles(p, wk.context(p, b), BN) * wk.KM;
-    int64_t at = tree_scan(mine, scratch, &total);
-    const int64_t share = tree_share(total, nslots, g.min_tiles);
+    const int batch = (int)p.batch, per = (batch + kTreeThreads - 1) / kTreeThreads;
+    const int b0 = tid * per, b1 = min(b0 + per, batch);
+    int mine = 0, total;
+    for (int b = b0; b < b1; ++b) mine += tree_tiles<BN>(p, g, tree_context(p, g, b)) * g.KM;
+    const int at = tree_scan(mine, scratch, &total);
+    const int share = tree_share(total, nslots, g.min_tiles);
     for (int s = 0; s < 2; ++s) {
-      const int64_t start = (slot0 + s) * share;
-      if (start < at || start >= at + mine) continue;
-      int64_t off = start - at;
+      const int64_t start = (int64_t)(slot0 + s) * share;
+      if (start < at || start >= (int64_t)at + mine) continue;
+      int off = (int)start - at;
       for (int b = b0; b < b1; ++b) {
         TreeSeg sg;
-        sg.ctx = wk.context(p, b);
-        sg.T = wk.tiles(p, sg.ctx, BN);
-        const int64_t n = (int64_t)sg.T * wk.KM;
+        sg.ctx = tree_context(p, g, b);
+        sg.T = tree_tiles<BN>(p, g, sg.ctx);
+        const int n = sg.T * g.KM;
         if (off >= n) {
           off -= n;
           continue;
         }
-        sg.left = min(share, total - start);
+        sg.left = min(share, total - (int)start);
         sg.b = b;
-        sg.hm = (int)(off / sg.T);
-        sg.t0 = (int)(off % sg.T);
-        tree_seg_fill<D>(sg, p, wk);
+        sg.hm = off / sg.T;
+        sg.t0 = off - sg.hm * sg.T;
+        sg.h = sg.hm / g.MT;
+        sg.mt = sg.hm - sg.h * g.MT;
+        tree_seg_fill<D>(sg, p, g);
         firsts[s] = sg;
         break;
       }
@@ -369,65 +375,77 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // no run for this pipeline
   } else if (warp >= 8) {
     // ------------------------------------------------------ the issuers
-    if (lane == 0) {
-      // the pipeline's tiles in order: tile t0 + j of a piece
-      struct Cur {
-        TreeSeg s;
-        int j;
-        bool ok;
-      };
-      auto settle = [&](Cur& c) {  // to the next piece that has tiles
-        while (c.ok && c.s.tiles == 0) c.ok = tree_seg_next<D>(c.s, p, wk);
-        c.j = 0;
-      };
-      auto begin = [&]() {
-        Cur c{first, 0, true};
-        settle(c);
-        return c;
-      };
-      auto advance = [&](Cur& c) {
-        if (++c.j < c.s.tiles) return;
-        c.ok = tree_seg_next<D>(c.s, p, wk);
-        settle(c);
-      };
-      // loads one tile of K or V through the page table
-      auto load = [&](const CUtensorMap* map, unsigned char* dst, const Cur& c, uint64_t* bar) {
-        const int key0 = (c.s.t0 + c.j) * BN, h = c.s.hm / wk.MT;
-        const int boxes = min(BN, c.s.vis - key0 + g.box - 1) / g.box;  // those that hold keys
+    // the pipeline's tiles in order: tile t0 + j of a piece
+    struct Cur {
+      TreeSeg s;
+      int j;
+      bool ok;
+    };
+    auto settle = [&](Cur& c) {  // to the next piece that has tiles
+      while (c.ok && c.s.tiles == 0) c.ok = tree_seg_next<D>(c.s, p, g);
+      c.j = 0;
+    };
+    auto advance = [&](Cur& c) {
+      if (++c.j < c.s.tiles) return;
+      c.ok = tree_seg_next<D>(c.s, p, g);
+      settle(c);
+    };
+    // Tiles of K or V through the page table: lane i loads box i, whose page it
+    // looks up one tile ahead.
+    struct Loader {
+      Cur c;
+      int n;     // tiles loaded
+      int page;  // of this lane's box of the next tile
+    };
+    auto box_pos = [&](const Cur& c) { return (c.s.t0 + c.j) * BN + lane * g.box; };
+    auto look_up = [&](Loader& ld) {
+      if (!ld.c.ok) return;
+      const int pos = box_pos(ld.c);
+      if (lane * g.box < BN && pos < ld.c.s.vis) {
+        ld.page = __ldg(p.table + (int64_t)ld.c.s.b * p.width + tree_page(p, g, pos));
+        if (ld.page < 0 || ld.page >= p.pages) ld.page = (int)p.pages;  // out of range: zeros
+      }
+    };
+    auto load = [&](Loader& ld, const CUtensorMap* map, unsigned char* dst, uint64_t* bar) {
+      const int key0 = (ld.c.s.t0 + ld.c.j) * BN, pos = box_pos(ld.c);
+      const int boxes = min(BN, ld.c.s.vis - key0 + g.box - 1) >> g.box_shift;  // those that hold keys
+      if (lane == 0)
         mbar_arrive_expect_tx(bar, (uint32_t)(boxes * g.box * C::kBoxes * 128));
-        for (int i = 0; i < boxes; ++i) {
-          const int pos = key0 + i * g.box;
-          const int at = pos / p.page;
-          int page = __ldg(p.table + (int64_t)c.s.b * p.width + at);
-          if (page < 0 || page >= p.pages) page = (int)p.pages;  // out of range: zeros
+      __syncwarp();
+      if (lane < boxes) {
 #pragma unroll
-          for (int b = 0; b < C::kBoxes; ++b)
-            tma_load_4d(dst + b * C::kKVBox + i * g.box * 128, map, 64 * b, h, pos - at * p.page,
-                        page, bar);
+        for (int b = 0; b < C::kBoxes; ++b)
+          tma_load_4d(dst + b * C::kKVBox + lane * g.box * 128, map, 64 * b, ld.c.s.h,
+                      tree_page_row(p, g, pos), ld.page, bar);
+      }
+      ++ld.n;
+      advance(ld.c);
+      look_up(ld);
+    };
+    auto begin = [&]() {
+      Cur c{first, 0, true};
+      settle(c);
+      return c;
+    };
+    Cur c = begin();
+    Loader ld{c, 0, 0};
+    look_up(ld);
+    int r = 0;  // pieces begun
+    if (warp >= 10) {
+      // V loads and O += P V
+      for (int i = 0; i < C::NS && ld.c.ok; ++i)
+        load(ld, &tv, stage_v(ld.n & 1), &bar_vfull[ld.n & 1]);
+      for (int t = 0; c.ok && !dead; ++t) {
+        if (ld.c.ok && ld.n == t + 1 && t >= 1) {
+          wait_spin(&bar_vempty[(t - 1) & 1], (uint32_t)(((t - 1) >> 1) & 1), dead, p.err);
+          dead = __any_sync(0xffffffffu, dead);
+          if (!dead) load(ld, &tv, stage_v(ld.n & 1), &bar_vfull[ld.n & 1]);
         }
-      };
-      if (warp >= 10) {
-        // V loads and O += P V
-        Cur vc = begin(), c = vc;
-        int vt = 0;
-        auto load_v = [&]() {
-          load(&tv, stage_v(vt & 1), vc, &bar_vfull[vt & 1]);
-          ++vt;
-          advance(vc);
-        };
-        if (c.ok) {
-          load_v();
-          if (vc.ok) load_v();
-        }
-        int r = 0;  // pieces begun
-        for (int t = 0; c.ok && !dead; ++t) {
-          if (vc.ok && vt == t + 1 && t >= 1) {
-            wait_spin(&bar_vempty[(t - 1) & 1], (uint32_t)(((t - 1) >> 1) & 1), dead, p.err);
-            if (!dead) load_v();
-          }
-          if (c.j == 0 && r++ > 0) wait_spin(bar_ofree, (uint32_t)(r & 1), dead, p.err);
-          wait_spin(&bar_p[t % C::NPB], (uint32_t)((t / C::NPB) & 1), dead, p.err);
-          wait_spin(&bar_vfull[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
+        if (c.j == 0 && r++ > 0) wait_spin(bar_ofree, (uint32_t)(r & 1), dead, p.err);
+        wait_spin(&bar_p[t % C::NPB], (uint32_t)((t / C::NPB) & 1), dead, p.err);
+        wait_spin(&bar_vfull[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
+        dead = __any_sync(0xffffffffu, dead);
+        if (lane == 0) {
           const uint32_t v_addr = smem_addr(stage_v(t & 1));
           tc_fence_after();
 #pragma unroll
@@ -437,27 +455,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                    (c.j > 0 || kk > 0) ? 1u : 0u);
           mma_commit(&bar_o[t % C::NPB]);
           mma_commit(&bar_vempty[t & 1]);
-          advance(c);
         }
-      } else {
-        // K loads and S = Q K^T
-        Cur kc = begin(), c = kc;
-        int kt = 0;
-        auto load_k = [&]() {
-          load(&tk, stage_k(kt & 1), kc, &bar_kfull[kt & 1]);
-          ++kt;
-          advance(kc);
-        };
-        if (c.ok) {
-          load_k();
-          if (kc.ok) load_k();
-        }
-        int r = 0;
-        for (int t = 0; c.ok && !dead; ++t) {
-          // S(t) once the softmax has read S(t - 1); a new piece's Q is then there
-          if (t >= 1) wait_spin(bar_sfree, (uint32_t)((t - 1) & 1), dead, p.err);
-          if (c.j == 0) wait_spin(bar_q, (uint32_t)(r++ & 1), dead, p.err);
-          wait_spin(&bar_kfull[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
+        __syncwarp();
+        advance(c);
+      }
+    } else {
+      // K loads and S = Q K^T
+      for (int i = 0; i < C::NS && ld.c.ok; ++i)
+        load(ld, &tk, stage_k(ld.n & 1), &bar_kfull[ld.n & 1]);
+      for (int t = 0; c.ok && !dead; ++t) {
+        // S(t) once the softmax has read S(t - 1); a new piece's Q is then there
+        if (t >= 1) wait_spin(bar_sfree, (uint32_t)((t - 1) & 1), dead, p.err);
+        if (c.j == 0) wait_spin(bar_q, (uint32_t)(r++ & 1), dead, p.err);
+        wait_spin(&bar_kfull[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
+        if (lane == 0) {
           const uint32_t q_addr = smem_addr(sq), k_addr = smem_addr(stage_k(t & 1));
           tc_fence_after();
 #pragma unroll
@@ -469,12 +480,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           mma_commit(bar_s);
           mma_commit(&bar_kempty[t & 1]);
-          if (kc.ok) {  // K(t + 2) into the stage S(t) used
-            wait_spin(&bar_kempty[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
-            if (!dead) load_k();
-          }
-          advance(c);
         }
+        __syncwarp();
+        if (ld.c.ok) {  // K(t + 2) into the stage S(t) used
+          wait_spin(&bar_kempty[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
+          dead = __any_sync(0xffffffffu, dead);
+          if (!dead) load(ld, &tk, stage_k(ld.n & 1), &bar_kfull[ld.n & 1]);
+        }
+        dead = __any_sync(0xffffffffu, dead);
+        advance(c);
       }
     }
   } else {
@@ -485,7 +499,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const uint32_t tO = tm + lane_base + C::kColO;
     const float sc = p.scale_log2;
     const int slot = slot0 + w;
-    const int all_rows = p.nodes * wk.G, ws_rows = min(all_rows, kTM);
+    const int all_rows = p.nodes * g.G, ws_rows = min(all_rows, kTM);
     float* ws_o = p.ws;
     float2* ws_ml = reinterpret_cast<float2*>(p.ws + (int64_t)g.max_slots * 2 * ws_rows * D);
     uint32_t* mask = masks + row * kMaskStride;
@@ -493,14 +507,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     int t = 0;        // tiles done by this pipeline
     int piece = 0;    // pieces seen
     bool more = true;
-    for (; more; more = tree_seg_next<D>(s, p, wk)) {
+    for (; more; more = tree_seg_next<D>(s, p, g)) {
       const bool cut0 = piece == 0 && s.t0 > 0, cut1 = s.t1 < s.T;
       ++piece;
-      const int h = s.hm / wk.MT, mt = s.hm % wk.MT;
+      const int h = s.h, mt = s.mt;
       const int R = mt * kTM + row;
       const bool live = R < all_rows;
       const bool wlive = mt * kTM + 32 * (warp & 3) < all_rows;  // some row of this warp
-      const int node = live ? R / wk.G : 0, head = h * wk.G + (live ? R % wk.G : 0);
+      const int node = live ? R / g.G : 0, head = h * g.G + (live ? R - node * g.G : 0);
       const int64_t out = ((int64_t)s.b * p.nodes + node) * p.heads + head;
       bool present = live;
       float m = -INFINITY, l = 0.f;
@@ -531,7 +545,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         bool holes = false;
         {
           const int last = min((s.t0 + s.tiles) * BN, s.vis) - 1;
-          for (int i = s.t0 * BN / p.page + lane; i <= last / p.page; i += 32) {
+          for (int i = tree_page(p, g, s.t0 * BN) + lane; i <= tree_page(p, g, last); i += 32) {
             const int page = __ldg(p.table + (int64_t)s.b * p.width + i);
             holes = holes || page < 0 || page >= p.pages;
           }
@@ -600,7 +614,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 if (holes) {
                   for (int i = 0; i < 32; i += 16) {
                     if (pos + i >= s.vis) break;
-                    const int page = __ldg(p.table + (int64_t)s.b * p.width + (pos + i) / p.page);
+                    const int page =
+                        __ldg(p.table + (int64_t)s.b * p.width + tree_page(p, g, pos + i));
                     if (page < 0 || page >= p.pages) bits &= ~(0xffffu << i);
                   }
                 }
@@ -701,7 +716,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0u;
           }
-          if (fix) tree_add_odd(p, s, wk, h, node, mask, D, BN, c, o);
+          if (fix) tree_add_odd(p, s, h, node, mask, D, BN, c, o);
           if (live && whole) {
             uint4* dst = reinterpret_cast<uint4*>(p.o + (out * D + 32 * c) * 2);
 #pragma unroll
@@ -744,41 +759,39 @@ constexpr int kJoinT = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, const TreeGeo g) {
   constexpr int BN = TreePL<D>::BN, V = D / 32;
-  __shared__ int64_t scratch[16], s_before;
-  const TreeWork wk(p);
+  __shared__ int scratch[16], s_before;
   const int tid = threadIdx.x, lane = tid & 31;
-  const int64_t item = blockIdx.x;
-  const int b = (int)(item / wk.KM), hm = (int)(item % wk.KM);
+  const int b = (int)blockIdx.x / g.KM, hm = (int)blockIdx.x - b * g.KM;
   // tiles before this sequence, and of all
-  const int per = (int)((p.batch + kJoinT - 1) / kJoinT);
-  const int b0 = tid * per, b1 = (int)min((int64_t)b0 + per, p.batch);
-  int64_t mine = 0, total;
-  for (int i = b0; i < b1; ++i) mine += (int64_t)wk.tiles(p, wk.context(p, i), BN) * wk.KM;
-  int64_t at = tree_scan(mine, scratch, &total);
+  const int batch = (int)p.batch, per = (batch + kJoinT - 1) / kJoinT;
+  const int b0 = tid * per, b1 = min(b0 + per, batch);
+  int mine = 0, total;
+  for (int i = b0; i < b1; ++i) mine += tree_tiles<BN>(p, g, tree_context(p, g, i)) * g.KM;
+  int at = tree_scan(mine, scratch, &total);
   if (b >= b0 && b < b1) {
-    for (int i = b0; i < b; ++i) at += (int64_t)wk.tiles(p, wk.context(p, i), BN) * wk.KM;
+    for (int i = b0; i < b; ++i) at += tree_tiles<BN>(p, g, tree_context(p, g, i)) * g.KM;
     s_before = at;
   }
   __syncthreads();
-  const int T = wk.tiles(p, wk.context(p, b), BN);
-  const int64_t share = tree_share(total, g.max_slots, g.min_tiles);
-  const int64_t start = s_before + (int64_t)hm * T;
-  const int64_t s0 = start / share, s1 = (start + T - 1) / share;
+  const int T = tree_tiles<BN>(p, g, tree_context(p, g, b));
+  const int share = tree_share(total, g.max_slots, g.min_tiles);
+  const int start = s_before + hm * T;
+  const int s0 = start / share, s1 = (start + T - 1) / share;
   if (T > 0 && s0 == s1) return;  // finished by its run
-  const int all_rows = p.nodes * wk.G, ws_rows = min(all_rows, kTM);
-  const int h = hm / wk.MT, mt = hm % wk.MT;
+  const int all_rows = p.nodes * g.G, ws_rows = min(all_rows, kTM);
+  const int h = hm / g.MT, mt = hm - h * g.MT;
   const int row = (int)blockIdx.y * (kJoinT / 32) + (tid >> 5), R = mt * kTM + row;
   if (row >= kTM || R >= all_rows) return;
-  const int64_t out = ((int64_t)b * p.nodes + R / wk.G) * p.heads + h * wk.G + R % wk.G;
+  const int64_t out = ((int64_t)b * p.nodes + R / g.G) * p.heads + h * g.G + R % g.G;
   const float* ws_o = p.ws;
   const float2* ws_ml =
       reinterpret_cast<const float2*>(p.ws + (int64_t)g.max_slots * 2 * ws_rows * D);
   // the item's piece in a run is its last if it begins inside the run
-  auto place = [&](int64_t s) { return tree_part((int)s, s * share < start ? 1 : 0, ws_rows, row); };
+  auto place = [&](int s) { return tree_part(s, s * share < start ? 1 : 0, ws_rows, row); };
   // lanes take the pieces' maxima and sums, 32 pieces at a time; their outputs
   // then come four loads at once, a piece in which the row sees nothing (it has
   // no output) with weight 0
-  const int n = T > 0 ? (int)(s1 - s0) + 1 : 0;
+  const int n = T > 0 ? s1 - s0 + 1 : 0;
   float M = -INFINITY, L = 0.f, o[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.f;
@@ -855,7 +868,17 @@ const char* tree_tc_launch(const TreeParams& p, int d, int sms, cudaStream_t str
   TreeGeo g{};
   g.box = 16;
   while (g.box < tk.bn && p.page % (2 * g.box) == 0) g.box *= 2;
+  g.box_shift = 4;
+  while ((1 << g.box_shift) < g.box) ++g.box_shift;
+  g.page_shift = -1;
+  for (int i = 4; i < 31; ++i)
+    if (p.page == (1 << i)) g.page_shift = i;
   g.min_tiles = kTreeMinTiles;
+  g.G = p.heads / p.kv_heads;
+  const int64_t rows = (int64_t)p.nodes * g.G, mt = (rows + kTM - 1) / kTM;
+  g.MT = (int)mt;
+  g.KM = (int)(p.kv_heads * mt);
+  g.cap = (int)(p.width * p.page);
   CUtensorMap maps[2];
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)p.kv_heads, (cuuint64_t)p.page,
                               (cuuint64_t)p.pages};
@@ -868,8 +891,6 @@ const char* tree_tc_launch(const TreeParams& p, int d, int sms, cudaStream_t str
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return "tensor map encoding failed";
-  const int G = p.heads / p.kv_heads;
-  const int64_t rows = (int64_t)p.nodes * G, mt = (rows + kTM - 1) / kTM;
   g.max_slots = 2 * sms;
   TreeParams pc = p;
   void* args[] = {&maps[0], &maps[1], &pc, &g};

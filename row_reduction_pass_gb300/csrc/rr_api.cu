@@ -2220,6 +2220,11 @@ rr_status rr_attention_tree_fwd(const void* q, const void* k_cache, const void* 
     return fail(RR_ERR_INVALID_ARG, "bad cache shape");
   if (pages > ((int64_t)1 << 58) / (page_size * kv_heads * head_dim))
     return fail(RR_ERR_INVALID_ARG, "cache too large");
+  // key tiles of 64 positions over all sequences, key heads and row tiles are
+  // counted in 32 bits
+  if (batch * kv_heads * cdiv(nodes * (heads / kv_heads), 128) >
+      ((int64_t)1 << 30) / (cdiv(table_width * page_size, 64) + 1))
+    return fail(RR_ERR_INVALID_ARG, "too many key tiles (batch x key heads x table positions)");
   if (parents && nodes > rr::kTreeMaxNodes)
     return fail(RR_ERR_INVALID_ARG, "a tree holds at most %d nodes (a chain any number)",
                 rr::kTreeMaxNodes);

@@ -277,7 +277,12 @@ struct TreeParams {
 constexpr int kTreeMaxNodes = 256;  // with parents (one mask bit a node)
 const void* tree_rows_kernel(int d);
 struct TreeGeo {
-  int32_t box;        // positions of one tensor-map box
+  int32_t box;        // positions of one tensor-map box, a power of two
+  int32_t box_shift, page_shift;  // their logarithms (page: -1 if no power of two)
+  int32_t G;          // heads per key head
+  int32_t MT;         // row tiles per key head
+  int32_t KM;         // kv_heads * MT
+  int32_t cap;        // positions of the page table
   int32_t min_tiles;  // fewest key tiles of a run
   int32_t max_slots;  // pipelines
 };
