@@ -7,7 +7,9 @@
 // warpgroup owning row t.  The work is counted in key tiles of BN keys over all
 // (sequence, key head, row tile) items in order, and every pipeline (two per
 // SM) takes an equal run of them, whatever the lengths, which the host does not
-// know.  An item inside one run is finished there; of an item cut by runs every
+// know.  Up to 16 key heads of the same positions go to as many pipelines side by
+// side (a group), since they lie side by side in the cache: the runs are runs of
+// groups, an item being (sequence, block of heads, row tile).  An item inside one run is finished there; of an item cut by runs every
 // piece leaves its unscaled output, maximum and sum in the workspace, and a
 // second kernel joins the pieces.
 //
@@ -149,7 +151,7 @@ struct TreeSeg {
   int ctx;    // keys before the nodes
   int vis;    // positions below it may be seen by some row of the tile
   int tiles;  // tiles to work on: those of [t0, t1) below vis
-  int h, mt;  // hm = h * MT + mt
+  int h, mt;  // key head and row tile of item hm
 };
 
 // keys before the nodes (nodes past the table are not seen wherever they are)
@@ -170,9 +172,9 @@ __device__ __forceinline__ int tree_page_row(const TreeParams& p, const TreeGeo&
   return g.page_shift >= 0 ? pos & (p.page - 1) : pos % p.page;
 }
 
-// The run of pipeline `slot`: tiles [slot * share, (slot + 1) * share) of all.
-__device__ __forceinline__ int tree_share(int total, int nslots, int min_tiles) {
-  return max((total + nslots - 1) / nslots, min_tiles);
+// The run of group `grp`: tiles [grp * share, (grp + 1) * share) of all.
+__device__ __forceinline__ int tree_share(int total, int groups, int min_tiles) {
+  return max((total + groups - 1) / groups, min_tiles);
 }
 
 template <int D>
@@ -189,13 +191,13 @@ __device__ __forceinline__ bool tree_seg_next(TreeSeg& s, const TreeParams& p, c
   s.left -= s.t1 - s.t0;
   if (s.left <= 0) return false;
   s.t0 = 0;
-  ++s.hm;
   if (++s.mt == g.MT) {
     s.mt = 0;
-    ++s.h;
+    s.h += g.HB;
   }
-  if (s.hm == g.KM) {
-    s.hm = s.h = 0;
+  if (++s.hm == g.KM) {
+    s.hm = 0;
+    s.h -= p.kv_heads;
     do {  // (a sequence of no tiles has no items; tiles are left, so one comes)
       if (++s.b >= p.batch) return false;
       s.ctx = tree_context(p, g, s.b);
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   TreeSeg* firsts = reinterpret_cast<TreeSeg*>(extra + 4);  // [2]
   int* scratch = reinterpret_cast<int*>(smem + C::kOffScan);
 
-  const int nslots = 2 * (int)gridDim.x, slot0 = 2 * (int)blockIdx.x;
+  const int slot0 = 2 * (int)blockIdx.x;
 
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -335,10 +337,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     int mine = 0, total;
     for (int b = b0; b < b1; ++b) mine += tree_tiles<BN>(p, g, tree_context(p, g, b)) * g.KM;
     const int at = tree_scan(mine, scratch, &total);
-    const int share = tree_share(total, nslots, g.min_tiles);
+    const int share = tree_share(total, g.groups, g.min_tiles);
     for (int s = 0; s < 2; ++s) {
-      const int64_t start = (int64_t)(slot0 + s) * share;
-      if (start < at || start >= (int64_t)at + mine) continue;
+      const int grp = (slot0 + s) / g.HB;
+      const int64_t start = (int64_t)grp * share;
+      if (grp >= g.groups || start < at || start >= (int64_t)at + mine) continue;
       int off = (int)start - at;
       for (int b = b0; b < b1; ++b) {
         TreeSeg sg;
@@ -353,8 +356,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         sg.b = b;
         sg.hm = off / sg.T;
         sg.t0 = off - sg.hm * sg.T;
-        sg.h = sg.hm / g.MT;
-        sg.mt = sg.hm - sg.h * g.MT;
+        const int hb = sg.hm / g.MT;
+        sg.h = hb * g.HB + (slot0 + s) % g.HB;
+        sg.mt = sg.hm - hb * g.MT;
         tree_seg_fill<D>(sg, p, g);
         firsts[s] = sg;
         break;
@@ -427,69 +431,72 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       settle(c);
       return c;
     };
-    Cur c = begin();
-    Loader ld{c, 0, 0};
-    look_up(ld);
-    int r = 0;  // pieces begun
     if (warp >= 10) {
-      // V loads and O += P V
-      for (int i = 0; i < C::NS && ld.c.ok; ++i)
-        load(ld, &tv, stage_v(ld.n & 1), &bar_vfull[ld.n & 1]);
-      for (int t = 0; c.ok && !dead; ++t) {
-        if (ld.c.ok && ld.n == t + 1 && t >= 1) {
-          wait_spin(&bar_vempty[(t - 1) & 1], (uint32_t)(((t - 1) >> 1) & 1), dead, p.err);
+      // the loader: K(n) into the stage that S(n - 2) has read, V(n) into the one
+      // that O += P V of n - 2 has
+      Loader lk{begin(), 0, 0}, lv = lk;
+      look_up(lk);
+      lv.page = lk.page;
+      while (lv.c.ok && !dead) {
+        if (lk.c.ok) {
+          const int s = lk.n & 1;
+          if (lk.n >= 2) wait_spin(&bar_kempty[s], (uint32_t)((lk.n / 2 - 1) & 1), dead, p.err);
           dead = __any_sync(0xffffffffu, dead);
-          if (!dead) load(ld, &tv, stage_v(ld.n & 1), &bar_vfull[ld.n & 1]);
+          if (!dead) load(lk, &tk, stage_k(s), &bar_kfull[s]);
         }
-        if (c.j == 0 && r++ > 0) wait_spin(bar_ofree, (uint32_t)(r & 1), dead, p.err);
+        const int s = lv.n & 1;
+        if (lv.n >= 2) wait_spin(&bar_vempty[s], (uint32_t)((lv.n / 2 - 1) & 1), dead, p.err);
+        dead = __any_sync(0xffffffffu, dead);
+        if (!dead) load(lv, &tv, stage_v(s), &bar_vfull[s]);
+      }
+    } else if (lane == 0) {
+      // the products: S(t) as soon as the softmax has read S(t - 1), then O += P V
+      // of t - 1 once its P is written; at a new piece the other way round (its Q
+      // is written when the piece before it is finished)
+      Cur c = begin();
+      int pieces = 0;
+      auto issue_pv = [&](int t, bool first_tile) {
+        // (the first of a piece overwrites O: the softmax must have read it)
+        if (first_tile && pieces > 1)
+          wait_spin(bar_ofree, (uint32_t)(pieces & 1), dead, p.err);
         wait_spin(&bar_p[t % C::NPB], (uint32_t)((t / C::NPB) & 1), dead, p.err);
         wait_spin(&bar_vfull[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
-        dead = __any_sync(0xffffffffu, dead);
-        if (lane == 0) {
-          const uint32_t v_addr = smem_addr(stage_v(t & 1));
-          tc_fence_after();
+        if (dead) return;
+        const uint32_t v_addr = smem_addr(stage_v(t & 1));
+        tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ts(tm + C::kColO, tm + C::kColP + (t % C::NPB) * (BN / 2) + 8 * kk,
-                   sw128_desc(v_addr + kk * 2048, C::kKVBox, 1024), C::kIdescO,
-                   (c.j > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&bar_o[t % C::NPB]);
-          mma_commit(&bar_vempty[t & 1]);
-        }
-        __syncwarp();
-        advance(c);
-      }
-    } else {
-      // K loads and S = Q K^T
-      for (int i = 0; i < C::NS && ld.c.ok; ++i)
-        load(ld, &tk, stage_k(ld.n & 1), &bar_kfull[ld.n & 1]);
-      for (int t = 0; c.ok && !dead; ++t) {
-        // S(t) once the softmax has read S(t - 1); a new piece's Q is then there
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_ts(tm + C::kColO, tm + C::kColP + (t % C::NPB) * (BN / 2) + 8 * kk,
+                 sw128_desc(v_addr + kk * 2048, C::kKVBox, 1024), C::kIdescO,
+                 (!first_tile || kk > 0) ? 1u : 0u);
+        mma_commit(&bar_o[t % C::NPB]);
+        mma_commit(&bar_vempty[t & 1]);
+      };
+      bool prev_first = false;  // tile t - 1 was the first of its piece
+      int t = 0;
+      for (; c.ok && !dead; ++t) {
+        const bool fresh = c.j == 0;
+        if (fresh && t > 0) issue_pv(t - 1, prev_first);
         if (t >= 1) wait_spin(bar_sfree, (uint32_t)((t - 1) & 1), dead, p.err);
-        if (c.j == 0) wait_spin(bar_q, (uint32_t)(r++ & 1), dead, p.err);
+        if (fresh) wait_spin(bar_q, (uint32_t)(pieces++ & 1), dead, p.err);
         wait_spin(&bar_kfull[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
-        if (lane == 0) {
-          const uint32_t q_addr = smem_addr(sq), k_addr = smem_addr(stage_k(t & 1));
-          tc_fence_after();
+        if (dead) break;
+        const uint32_t q_addr = smem_addr(sq), k_addr = smem_addr(stage_k(t & 1));
+        tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t qo = (uint32_t)((kk >> 2) * C::kQBox + (kk & 3) * 32);
-            const uint32_t ko = (uint32_t)((kk >> 2) * C::kKVBox + (kk & 3) * 32);
-            mma_ss(tm + C::kColS, sw128_desc(q_addr + qo, 16, 1024),
-                   sw128_desc(k_addr + ko, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(bar_s);
-          mma_commit(&bar_kempty[t & 1]);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t qo = (uint32_t)((kk >> 2) * C::kQBox + (kk & 3) * 32);
+          const uint32_t ko = (uint32_t)((kk >> 2) * C::kKVBox + (kk & 3) * 32);
+          mma_ss(tm + C::kColS, sw128_desc(q_addr + qo, 16, 1024),
+                 sw128_desc(k_addr + ko, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u);
         }
-        __syncwarp();
-        if (ld.c.ok) {  // K(t + 2) into the stage S(t) used
-          wait_spin(&bar_kempty[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
-          dead = __any_sync(0xffffffffu, dead);
-          if (!dead) load(ld, &tk, stage_k(ld.n & 1), &bar_kfull[ld.n & 1]);
-        }
-        dead = __any_sync(0xffffffffu, dead);
+        mma_commit(bar_s);
+        mma_commit(&bar_kempty[t & 1]);
+        if (!fresh) issue_pv(t - 1, prev_first);
+        prev_first = fresh;
         advance(c);
       }
+      if (t > 0 && !dead) issue_pv(t - 1, prev_first);
     }
   } else {
     // ------------------------------------------------ softmax warpgroup
@@ -761,6 +768,7 @@ __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, c
   constexpr int BN = TreePL<D>::BN, V = D / 32;
   __shared__ int scratch[16], s_before;
   const int tid = threadIdx.x, lane = tid & 31;
+  // block (x, z): item x of all, head z of its HB
   const int b = (int)blockIdx.x / g.KM, hm = (int)blockIdx.x - b * g.KM;
   // tiles before this sequence, and of all
   const int batch = (int)p.batch, per = (batch + kJoinT - 1) / kJoinT;
@@ -774,12 +782,12 @@ __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, c
   }
   __syncthreads();
   const int T = tree_tiles<BN>(p, g, tree_context(p, g, b));
-  const int share = tree_share(total, g.max_slots, g.min_tiles);
+  const int share = tree_share(total, g.groups, g.min_tiles);
   const int start = s_before + hm * T;
   const int s0 = start / share, s1 = (start + T - 1) / share;
   if (T > 0 && s0 == s1) return;  // finished by its run
   const int all_rows = p.nodes * g.G, ws_rows = min(all_rows, kTM);
-  const int h = hm / g.MT, mt = hm - h * g.MT;
+  const int hl = (int)blockIdx.z, hb = hm / g.MT, mt = hm - hb * g.MT, h = hb * g.HB + hl;
   const int row = (int)blockIdx.y * (kJoinT / 32) + (tid >> 5), R = mt * kTM + row;
   if (row >= kTM || R >= all_rows) return;
   const int64_t out = ((int64_t)b * p.nodes + R / g.G) * p.heads + h * g.G + R % g.G;
@@ -787,7 +795,9 @@ __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, c
   const float2* ws_ml =
       reinterpret_cast<const float2*>(p.ws + (int64_t)g.max_slots * 2 * ws_rows * D);
   // the item's piece in a run is its last if it begins inside the run
-  auto place = [&](int s) { return tree_part(s, s * share < start ? 1 : 0, ws_rows, row); };
+  auto place = [&](int s) { 
+    return tree_part(s * g.HB + hl, s * share < start ? 1 : 0, ws_rows, row);
+  };
   // lanes take the pieces' maxima and sums, 32 pieces at a time; their outputs
   // then come four loads at once, a piece in which the row sees nothing (it has
   // no output) with weight 0
@@ -877,7 +887,11 @@ const char* tree_tc_launch(const TreeParams& p, int d, int sms, cudaStream_t str
   g.G = p.heads / p.kv_heads;
   const int64_t rows = (int64_t)p.nodes * g.G, mt = (rows + kTM - 1) / kTM;
   g.MT = (int)mt;
-  g.KM = (int)(p.kv_heads * mt);
+  // the largest divisor of the key heads up to 16
+  g.HB = 1;
+  for (int i = 2; i <= 16; ++i)
+    if (p.kv_heads % i == 0) g.HB = i;
+  g.KM = (int)(p.kv_heads / g.HB * mt);
   g.cap = (int)(p.width * p.page);
   CUtensorMap maps[2];
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)p.kv_heads, (cuuint64_t)p.page,
@@ -892,15 +906,16 @@ const char* tree_tc_launch(const TreeParams& p, int d, int sms, cudaStream_t str
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return "tensor map encoding failed";
   g.max_slots = 2 * sms;
+  g.groups = g.max_slots / g.HB;
   TreeParams pc = p;
   void* args[] = {&maps[0], &maps[1], &pc, &g};
   if (cudaLaunchKernel(tk.main, dim3((unsigned)sms), dim3((unsigned)tk.threads), args,
                        (size_t)tk.smem, stream) != cudaSuccess)
     return "launch failed";
   void* jargs[] = {&pc, &g};
-  const int64_t items = p.batch * p.kv_heads * mt;
+  const int64_t items = p.batch * g.KM;
   const unsigned groups = (unsigned)((std::min<int64_t>(rows, kTM) + kJoinT / 32 - 1) / (kJoinT / 32));
-  if (cudaLaunchKernel(tk.join, dim3((unsigned)items, groups), dim3(kJoinT), jargs, 0, stream) !=
+  if (cudaLaunchKernel(tk.join, dim3((unsigned)items, groups, (unsigned)g.HB), dim3(kJoinT), jargs, 0, stream) !=
       cudaSuccess)
     return "join launch failed";
   return nullptr;
