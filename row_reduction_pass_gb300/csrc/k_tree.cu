@@ -120,7 +120,11 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
 }
 
 constexpr int kTM = 128;  // rows of a tile: MMA M, TMEM lanes
-constexpr int kTreeThreads = 384;
+// Two softmax warpgroups, and for each pipeline w a warp that issues S (8 + w), one
+// for O += P V (10 + w), one that loads K (12 + w) and one that loads V (14 + w): a
+// load takes its warp about 650 cycles, an issue 500-1000, and in one warp they
+// delayed one another (one loader for both pipelines: decode batch 200 -> 234 us).
+constexpr int kTreeThreads = 512;
 constexpr int kMaskStride = kTreeMaxNodes / 32 + 1;  // mask words of a row, one spare
 
 // Tiles, stages, TMEM columns (256 a pipeline: S, P buffers, O) as in k_attn.cu.
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int w = warp < 8 ? warp >> 2 : (warp - 8) & 1;  // this thread's pipeline
+  const int w = warp < 8 ? warp >> 2 : warp & 1;  // this thread's pipeline
   unsigned char* pipe = smem + w * C::kPipe;
   unsigned char* sq = pipe;
   auto stage_k = [&](int s) { return pipe + C::kQBytes + (2 * s) * C::kKVBytes; };
@@ -374,129 +378,116 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!dead) dead = !mbar_wait_bounded(bar, parity, p.err);
   };
+  // a pipeline's tiles in order: tile t0 + j of a piece
+  struct Cur {
+    TreeSeg s;
+    int j;
+    bool ok;
+  };
+  auto settle = [&](Cur& c) {  // to the next piece that has tiles
+    while (c.ok && c.s.tiles == 0) c.ok = tree_seg_next<D>(c.s, p, g);
+    c.j = 0;
+  };
+  auto advance = [&](Cur& c) {
+    if (++c.j < c.s.tiles) return;
+    c.ok = tree_seg_next<D>(c.s, p, g);
+    settle(c);
+  };
+  auto begin = [&](const TreeSeg& s) {
+    Cur c{s, 0, s.left > 0};
+    settle(c);
+    return c;
+  };
 
   if (first.left <= 0) {
     // no run for this pipeline
-  } else if (warp >= 8) {
-    // ------------------------------------------------------ the issuers
-    // the pipeline's tiles in order: tile t0 + j of a piece
-    struct Cur {
-      TreeSeg s;
-      int j;
-      bool ok;
-    };
-    auto settle = [&](Cur& c) {  // to the next piece that has tiles
-      while (c.ok && c.s.tiles == 0) c.ok = tree_seg_next<D>(c.s, p, g);
-      c.j = 0;
-    };
-    auto advance = [&](Cur& c) {
-      if (++c.j < c.s.tiles) return;
-      c.ok = tree_seg_next<D>(c.s, p, g);
-      settle(c);
-    };
-    // Tiles of K or V through the page table: lane i loads box i, whose page it
+  } else if (warp >= 12) {
+    // ------------------------------------------------------ the loaders
+    // Tiles of K or V through the page table: K(n) goes where S(n - 2) has read its
+    // keys, V(n) where O += P V of n - 2 has.  Lane i loads box i, whose page it
     // looks up one tile ahead.
-    struct Loader {
-      Cur c;
-      int n;     // tiles loaded
-      int page;  // of this lane's box of the next tile
-    };
-    auto box_pos = [&](const Cur& c) { return (c.s.t0 + c.j) * BN + lane * g.box; };
-    auto look_up = [&](Loader& ld) {
-      if (!ld.c.ok) return;
-      const int pos = box_pos(ld.c);
-      if (lane * g.box < BN && pos < ld.c.s.vis) {
-        ld.page = __ldg(p.table + (int64_t)ld.c.s.b * p.width + tree_page(p, g, pos));
-        if (ld.page < 0 || ld.page >= p.pages) ld.page = (int)p.pages;  // out of range: zeros
+    const bool isv = warp >= 14;
+    const CUtensorMap* map = isv ? &tv : &tk;
+    uint64_t* full = isv ? bar_vfull : bar_kfull;
+    uint64_t* empty = isv ? bar_vempty : bar_kempty;
+    unsigned char* stage = isv ? stage_v(0) : stage_k(0);
+    Cur c = begin(first);
+    int page = 0;
+    auto box_pos = [&]() { return (c.s.t0 + c.j) * BN + lane * g.box; };
+    auto look_up = [&]() {
+      if (!c.ok) return;
+      const int pos = box_pos();
+      if (lane * g.box < BN && pos < c.s.vis) {
+        page = __ldg(p.table + (int64_t)c.s.b * p.width + tree_page(p, g, pos));
+        if (page < 0 || page >= p.pages) page = (int)p.pages;  // out of range: zeros
       }
     };
-    auto load = [&](Loader& ld, const CUtensorMap* map, unsigned char* dst, uint64_t* bar) {
-      const int key0 = (ld.c.s.t0 + ld.c.j) * BN, pos = box_pos(ld.c);
-      const int boxes = min(BN, ld.c.s.vis - key0 + g.box - 1) >> g.box_shift;  // those that hold keys
+    look_up();
+    for (int n = 0; c.ok; ++n) {
+      const int s = n & 1;
+      if (n >= 2) wait_spin(&empty[s], (uint32_t)((n / 2 - 1) & 1), dead, p.err);
+      if (__any_sync(0xffffffffu, dead)) break;
+      const int key0 = (c.s.t0 + c.j) * BN, pos = box_pos();
+      const int boxes = min(BN, c.s.vis - key0 + g.box - 1) >> g.box_shift;  // that hold keys
       if (lane == 0)
-        mbar_arrive_expect_tx(bar, (uint32_t)(boxes * g.box * C::kBoxes * 128));
+        mbar_arrive_expect_tx(&full[s], (uint32_t)(boxes * g.box * C::kBoxes * 128));
       __syncwarp();
       if (lane < boxes) {
+        unsigned char* dst = stage + s * 2 * C::kKVBytes + lane * g.box * 128;
 #pragma unroll
         for (int b = 0; b < C::kBoxes; ++b)
-          tma_load_4d(dst + b * C::kKVBox + lane * g.box * 128, map, 64 * b, ld.c.s.h,
-                      tree_page_row(p, g, pos), ld.page, bar);
+          tma_load_4d(dst + b * C::kKVBox, map, 64 * b, c.s.h, tree_page_row(p, g, pos), page,
+                      &full[s]);
       }
-      ++ld.n;
-      advance(ld.c);
-      look_up(ld);
-    };
-    auto begin = [&]() {
-      Cur c{first, 0, true};
-      settle(c);
-      return c;
-    };
-    if (warp >= 10) {
-      // the loader: K(n) into the stage that S(n - 2) has read, V(n) into the one
-      // that O += P V of n - 2 has
-      Loader lk{begin(), 0, 0}, lv = lk;
-      look_up(lk);
-      lv.page = lk.page;
-      while (lv.c.ok && !dead) {
-        if (lk.c.ok) {
-          const int s = lk.n & 1;
-          if (lk.n >= 2) wait_spin(&bar_kempty[s], (uint32_t)((lk.n / 2 - 1) & 1), dead, p.err);
-          dead = __any_sync(0xffffffffu, dead);
-          if (!dead) load(lk, &tk, stage_k(s), &bar_kfull[s]);
-        }
-        const int s = lv.n & 1;
-        if (lv.n >= 2) wait_spin(&bar_vempty[s], (uint32_t)((lv.n / 2 - 1) & 1), dead, p.err);
-        dead = __any_sync(0xffffffffu, dead);
-        if (!dead) load(lv, &tv, stage_v(s), &bar_vfull[s]);
-      }
-    } else if (lane == 0) {
-      // the products: S(t) as soon as the softmax has read S(t - 1), then O += P V
-      // of t - 1 once its P is written; at a new piece the other way round (its Q
-      // is written when the piece before it is finished)
-      Cur c = begin();
-      int pieces = 0;
-      auto issue_pv = [&](int t, bool first_tile) {
-        // (the first of a piece overwrites O: the softmax must have read it)
-        if (first_tile && pieces > 1)
-          wait_spin(bar_ofree, (uint32_t)(pieces & 1), dead, p.err);
-        wait_spin(&bar_p[t % C::NPB], (uint32_t)((t / C::NPB) & 1), dead, p.err);
-        wait_spin(&bar_vfull[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
-        if (dead) return;
-        const uint32_t v_addr = smem_addr(stage_v(t & 1));
-        tc_fence_after();
+      advance(c);
+      look_up();
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------ the issuers
+    if (lane == 0) {
+      Cur c = begin(first);
+      int pieces = 0;  // begun
+      if (warp >= 10) {
+        // O += P V as soon as P is written (the first of a piece, which overwrites
+        // O, once the softmax has read it)
+        for (int t = 0; c.ok && !dead; ++t) {
+          if (c.j == 0 && pieces++ > 0) wait_spin(bar_ofree, (uint32_t)(pieces & 1), dead, p.err);
+          wait_spin(&bar_p[t % C::NPB], (uint32_t)((t / C::NPB) & 1), dead, p.err);
+          wait_spin(&bar_vfull[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
+          if (dead) break;
+          const uint32_t v_addr = smem_addr(stage_v(t & 1));
+          tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts(tm + C::kColO, tm + C::kColP + (t % C::NPB) * (BN / 2) + 8 * kk,
-                 sw128_desc(v_addr + kk * 2048, C::kKVBox, 1024), C::kIdescO,
-                 (!first_tile || kk > 0) ? 1u : 0u);
-        mma_commit(&bar_o[t % C::NPB]);
-        mma_commit(&bar_vempty[t & 1]);
-      };
-      bool prev_first = false;  // tile t - 1 was the first of its piece
-      int t = 0;
-      for (; c.ok && !dead; ++t) {
-        const bool fresh = c.j == 0;
-        if (fresh && t > 0) issue_pv(t - 1, prev_first);
-        if (t >= 1) wait_spin(bar_sfree, (uint32_t)((t - 1) & 1), dead, p.err);
-        if (fresh) wait_spin(bar_q, (uint32_t)(pieces++ & 1), dead, p.err);
-        wait_spin(&bar_kfull[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
-        if (dead) break;
-        const uint32_t q_addr = smem_addr(sq), k_addr = smem_addr(stage_k(t & 1));
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t qo = (uint32_t)((kk >> 2) * C::kQBox + (kk & 3) * 32);
-          const uint32_t ko = (uint32_t)((kk >> 2) * C::kKVBox + (kk & 3) * 32);
-          mma_ss(tm + C::kColS, sw128_desc(q_addr + qo, 16, 1024),
-                 sw128_desc(k_addr + ko, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(tm + C::kColO, tm + C::kColP + (t % C::NPB) * (BN / 2) + 8 * kk,
+                   sw128_desc(v_addr + kk * 2048, C::kKVBox, 1024), C::kIdescO,
+                   (c.j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&bar_o[t % C::NPB]);
+          mma_commit(&bar_vempty[t & 1]);
+          advance(c);
         }
-        mma_commit(bar_s);
-        mma_commit(&bar_kempty[t & 1]);
-        if (!fresh) issue_pv(t - 1, prev_first);
-        prev_first = fresh;
-        advance(c);
+      } else {
+        // S = Q K^T as soon as the softmax has read the S before (a new piece's Q is
+        // then there)
+        for (int t = 0; c.ok && !dead; ++t) {
+          wait_spin(&bar_kfull[t & 1], (uint32_t)((t >> 1) & 1), dead, p.err);
+          if (c.j == 0) wait_spin(bar_q, (uint32_t)(pieces++ & 1), dead, p.err);
+          if (t >= 1) wait_spin(bar_sfree, (uint32_t)((t - 1) & 1), dead, p.err);
+          if (dead) break;
+          const uint32_t q_addr = smem_addr(sq), k_addr = smem_addr(stage_k(t & 1));
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t qo = (uint32_t)((kk >> 2) * C::kQBox + (kk & 3) * 32);
+            const uint32_t ko = (uint32_t)((kk >> 2) * C::kKVBox + (kk & 3) * 32);
+            mma_ss(tm + C::kColS, sw128_desc(q_addr + qo, 16, 1024),
+                   sw128_desc(k_addr + ko, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(bar_s);
+          mma_commit(&bar_kempty[t & 1]);
+          advance(c);
+        }
       }
-      if (t > 0 && !dead) issue_pv(t - 1, prev_first);
     }
   } else {
     // ------------------------------------------------ softmax warpgroup
@@ -562,16 +553,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         for (int j = 0; j < s.tiles; ++j, ++t) {
           const int key0 = (s.t0 + j) * BN;
           const bool tail = key0 + BN > min(s.ctx, s.vis);
-          wait(bar_s, (uint32_t)(t & 1));
-          tc_fence_after();
-          uint32_t v[BN / 32][32];
-          if (wlive) {
-#pragma unroll
-            for (int c = 0; c < BN / 32; ++c) tmem_ld32_nowait(tS + 32 * c, v[c]);
-            tmem_ld_wait();
-          }
-          tc_fence_before();
-          mbar_arrive(bar_sfree);
           if (tail) {
             // V at positions nobody may see, and non-finite values at nodes: 0
             tail_seen = true;
@@ -579,33 +560,41 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const int vr = row % BN, pos = key0 + vr;
             if (pos >= s.ctx || pos >= s.vis) {
               uint4* vp = reinterpret_cast<uint4*>(stage_v(t & 1) + row / BN * C::kKVBox + vr * 128);
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < 8; ++c) {
+                uint4 x = vp[c];
                 if (pos >= s.vis) {
                   vp[c] = make_uint4(0u, 0u, 0u, 0u);
-                } else {
-                  uint4 x = vp[c];
-                  if (odd_bf16x2(x.x) || odd_bf16x2(x.y) || odd_bf16x2(x.z) || odd_bf16x2(x.w)) {
-                    for (int i = 0; i < 4; ++i) {
-                      uint32_t y = word_of(x, i);
-                      if ((y & 0x7f80u) == 0x7f80u) y &= 0xffff0000u;
-                      if ((y & 0x7f800000u) == 0x7f800000u) y &= 0xffffu;
-                      set_word(x, i, y);
-                    }
-                    vp[c] = x;
-                    *odd = piece;
+                } else if (odd_bf16x2(x.x) || odd_bf16x2(x.y) || odd_bf16x2(x.z) ||
+                           odd_bf16x2(x.w)) {
+                  for (int i = 0; i < 4; ++i) {
+                    uint32_t y = word_of(x, i);
+                    if ((y & 0x7f80u) == 0x7f80u) y &= 0xffff0000u;
+                    if ((y & 0x7f800000u) == 0x7f800000u) y &= 0xffffu;
+                    set_word(x, i, y);
                   }
+                  vp[c] = x;
+                  *odd = piece;
                 }
               }
             }
             fence_proxy_async_smem();
           }
+          wait(bar_s, (uint32_t)(t & 1));
+          tc_fence_after();
           if (wlive) {
-            if (tail || holes) {
+            // S in halves of 64 columns: at BN = 128 the first is read again for its
+            // exponentials (both at once are 128 registers, and spilled)
+            uint32_t v[2][32];
+            auto read_half = [&](int hf) {
 #pragma unroll
-              for (int c = 0; c < BN / 32; ++c) {
-                const int pos = key0 + 32 * c;   // of bit 0
-                const int nb = pos - s.ctx;      // its node
+              for (int c = 0; c < 2; ++c) tmem_ld32_nowait(tS + 64 * hf + 32 * c, v[c]);
+              tmem_ld_wait();
+              if (!tail && !holes) return;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int pos = key0 + 64 * hf + 32 * c;  // of bit 0
+                const int nb = pos - s.ctx;               // its node
                 uint32_t bits = 0xffffffffu;
                 if (p.parents != nullptr) {
                   if (nb >= 0)
@@ -630,48 +619,72 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 for (int i = 0; i < 32; ++i)
                   if (!((bits >> i) & 1)) v[c][i] = __float_as_uint(-INFINITY);
               }
+            };
+            auto max_half = [&](float mx) {
+              float x[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) x[k] = -INFINITY;
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i & 7] = fmaxf(x[i & 7], __uint_as_float(v[c][i]));
+              return fmaxf(fmaxf(mx, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]))),
+                           fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+            };
+            float mx = -INFINITY;
+            if constexpr (BN == 128) {
+              read_half(0);
+              mx = max_half(mx);
             }
-            float mx[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) mx[k] = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < BN / 32; ++c)
-#pragma unroll
-              for (int i = 0; i < 32; ++i) mx[i & 7] = fmaxf(mx[i & 7], __uint_as_float(v[c][i]));
-            const float mx0 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const float mx1 = fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+            read_half(BN / 64 - 1);
+            if constexpr (BN == 64) {
+              tc_fence_before();
+              mbar_arrive(bar_sfree);
+            }
+            mx = max_half(mx);
             // m moves only by more than 8 (k_attn.cu); a row that has seen no key
             // keeps m = -inf and takes its exponentials (all 0) from 0
-            const float mt_ = fmaxf(mx0, mx1) * sc;
+            const float mt_ = mx * sc;
             const float m_new = mt_ > m + 8.f ? mt_ : m;
             const float alpha = m_new == m ? 1.f : ex2(m - m_new);
             const float mref = m_new == -INFINITY ? 0.f : m_new;
             float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-            uint32_t pk[BN / 32][16];
+            const uint32_t tP = tm + lane_base + C::kColP + (t % C::NPB) * (BN / 2);
+            bool p_free = t < C::NPB;
+            auto exp_half = [&](int hf) {
 #pragma unroll
-            for (int c = 0; c < BN / 32; ++c)
+              for (int c = 0; c < 2; ++c) {
+                uint32_t pk[16];
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                float t0, t1, t2, t3;
-                fma2(t0, t1, __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]), sc, sc, -mref,
-                     -mref);
-                fma2(t2, t3, __uint_as_float(v[c][i + 2]), __uint_as_float(v[c][i + 3]), sc, sc,
-                     -mref, -mref);
-                const float p0 = ex2(t0), p1 = ex2(t1), p2 = ex2(t2), p3 = ex2(t3);
-                add2(l0, l1, l0, l1, p0, p1);
-                add2(l2, l3, l2, l3, p2, p3);
-                pk[c][i >> 1] = pack_bf16(p0, p1);
-                pk[c][(i >> 1) + 1] = pack_bf16(p2, p3);
+                for (int i = 0; i < 32; i += 4) {
+                  float t0, t1, t2, t3;
+                  fma2(t0, t1, __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]), sc, sc,
+                       -mref, -mref);
+                  fma2(t2, t3, __uint_as_float(v[c][i + 2]), __uint_as_float(v[c][i + 3]), sc, sc,
+                       -mref, -mref);
+                  const float p0 = ex2(t0), p1 = ex2(t1), p2 = ex2(t2), p3 = ex2(t3);
+                  add2(l0, l1, l0, l1, p0, p1);
+                  add2(l2, l3, l2, l3, p2, p3);
+                  pk[i >> 1] = pack_bf16(p0, p1);
+                  pk[(i >> 1) + 1] = pack_bf16(p2, p3);
+                }
+                if (!p_free) {  // O += P V of tile t - NPB has read this P buffer
+                  wait(&bar_o[t % C::NPB], (uint32_t)((t / C::NPB - 1) & 1));
+                  tc_fence_after();
+                  p_free = true;
+                }
+                tmem_st16(tP + 32 * hf + 16 * c, pk);
               }
+            };
+            exp_half(BN / 64 - 1);
+            if constexpr (BN == 128) {
+              read_half(0);
+              tc_fence_before();
+              mbar_arrive(bar_sfree);
+              exp_half(0);
+            }
             l = l * alpha + ((l0 + l1) + (l2 + l3));
             m = m_new;
-            if (t >= C::NPB) {
-              wait(&bar_o[t % C::NPB], (uint32_t)((t / C::NPB - 1) & 1));
-              tc_fence_after();
-            }
-            const uint32_t tP = tm + lane_base + C::kColP + (t % C::NPB) * (BN / 2);
-#pragma unroll
-            for (int c = 0; c < BN / 32; ++c) tmem_st16(tP + 16 * c, pk[c]);
             if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
               if constexpr (C::NPB > 1) {
                 wait(&bar_o[(t - 1) % C::NPB], (uint32_t)(((t - 1) / C::NPB) & 1));
@@ -693,10 +706,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               }
             }
             tmem_st_wait();
-          } else if (t >= C::NPB) {
+          } else {
+            tc_fence_before();
+            mbar_arrive(bar_sfree);
             // a warp without rows keeps pace: its arrival below must not fall into
             // the P buffer's previous phase
-            wait(&bar_o[t % C::NPB], (uint32_t)((t / C::NPB - 1) & 1));
+            if (t >= C::NPB) wait(&bar_o[t % C::NPB], (uint32_t)((t / C::NPB - 1) & 1));
           }
           tc_fence_before();
           mbar_arrive(&bar_p[t % C::NPB]);
