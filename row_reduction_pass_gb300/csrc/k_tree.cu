@@ -308,6 +308,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   int* scratch = reinterpret_cast<int*>(smem + C::kOffScan);
 
   const int slot0 = 2 * (int)blockIdx.x;
+  // the joining grid may be set up now (it waits for this one before it reads)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -796,6 +798,9 @@ __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, c
     s_before = at;
   }
   __syncthreads();
+  // Launched while the pieces are still being computed: every block waits for
+  // them here, also one without work, so that this grid ends after that one.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int T = tree_tiles<BN>(p, g, tree_context(p, g, b));
   const int share = tree_share(total, g.groups, g.min_tiles);
   const int start = s_before + hm * T;
@@ -930,9 +935,16 @@ const char* tree_tc_launch(const TreeParams& p, int d, int sms, cudaStream_t str
   void* jargs[] = {&pc, &g};
   const int64_t items = p.batch * g.KM;
   const unsigned groups = (unsigned)((std::min<int64_t>(rows, kTM) + kJoinT / 32 - 1) / (kJoinT / 32));
-  if (cudaLaunchKernel(tk.join, dim3((unsigned)items, groups, (unsigned)g.HB), dim3(kJoinT), jargs, 0, stream) !=
-      cudaSuccess)
-    return "join launch failed";
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)items, groups, (unsigned)g.HB);
+  cfg.blockDim = dim3(kJoinT);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelExC(&cfg, tk.join, jargs) != cudaSuccess) return "join launch failed";
   return nullptr;
 }
 
