@@ -281,9 +281,10 @@ struct TreeGeo {
   int32_t box_shift, page_shift;  // their logarithms (page: -1 if no power of two)
   int32_t G;          // heads per key head
   int32_t MT;         // row tiles per key head
-  int32_t HB;         // key heads side by side, one to a pipeline of a group
-  int32_t KM;         // items of a sequence: kv_heads / HB * MT
-  int32_t groups;     // of HB pipelines
+  int32_t HB, RB;     // key heads and row tiles side by side in a group of pipelines
+  int32_t side;       // HB * RB
+  int32_t KM;         // items of a sequence: kv_heads / HB * MT / RB
+  int32_t groups;     // of `side` pipelines
   int32_t cap;        // positions of the page table
   int32_t min_tiles;  // fewest key tiles of a run
   int32_t max_slots;  // pipelines
