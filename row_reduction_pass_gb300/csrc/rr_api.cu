@@ -1376,18 +1376,77 @@ rr_status distill_launch(rr::DistillParams p, rr_dtype dt, cudaStream_t stream) 
   return ok();
 }
 
+// A cluster of K blocks a sequence.  With few sequences (all their clusters on the
+// chip at once, a block per SM): the largest K, two row buffers and the noise in
+// shared memory.  With many: the largest K whose blocks are about twice what the
+// chip holds at four a SM, one buffer.  No cluster where the slices do not fit.
 rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
-  const rr::VerifyKernel vk = rr::verify_kernel(dt);
+  const rr::VerifyKernels vk = rr::verify_kernels(dt);
+  const int64_t E = dt == RR_BF16 ? 2 : 4;
+  int K = 0;
+  rr::VerifyGeo g{};
+  size_t smem = 0;
   {
     std::lock_guard<std::mutex> lock(g_mu);
     DevInfo* di = nullptr;
     rr_status st = device_info(&di);
     if (st != RR_OK) return st;
     p.err = di->err;
+    auto shape = [&](int k, bool ahead) {
+      rr::VerifyGeo t{};
+      const int64_t C = round_up(cdiv(p.cols, k), 16);
+      const int64_t row = round_up(C * E + 32, 128);
+      const int64_t buf = round_up(64 + 2 * 16 * k * (vk.cluster_threads / 32), 128);
+      const int64_t noise = buf + (ahead ? 2 : 1) * 2 * row;
+      const int64_t total = noise + (ahead ? round_up(C * 4 + 32, 128) : 0);
+      if (total > di->smem_optin) return false;
+      t.C = (int32_t)C;
+      t.row_bytes = (int32_t)row;
+      t.buf_off = (int32_t)buf;
+      t.buffers = ahead ? 2 : 1;
+      t.noise_off = ahead ? (int32_t)noise : -1;
+      g = t;
+      K = k;
+      smem = (size_t)total;
+      return true;
+    };
+    int kmax = 8;
+    while (kmax > 1 && p.cols < 512 * kmax) kmax /= 2;
+    int forced = 0, fa = -1;
+    if (const char* f = std::getenv("RR_VER_K")) std::sscanf(f, "%d:%d", &forced, &fa);
+    for (int k = kmax; k >= 1 && K == 0; k /= 2)
+      if (p.batch * k <= di->sms && (forced == 0 || forced == k)) shape(k, fa != 0);
+    for (int k = kmax; k >= 1 && K == 0; k /= 2)
+      if ((k == 1 || p.batch * k <= 8 * (int64_t)di->sms) && (forced == 0 || forced == k)) {
+        // (a shape that does not fit with few blocks may with more)
+        if (!shape(k, fa == 1)) {
+          for (int k2 = 2 * k; k2 <= kmax && K == 0; k2 *= 2) shape(k2, false);
+          break;
+        }
+      }
+    if (K > 0 && (st = set_smem(di, vk.cluster, smem)) != RR_OK) return st;
   }
-  void* args[] = {&p};
-  cudaError_t e = cudaLaunchKernel(vk.fn, dim3((unsigned)p.batch), dim3((unsigned)vk.threads),
-                                   args, 0, stream);
+  cudaError_t e;
+  if (K > 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)(p.batch * K));
+    cfg.blockDim = dim3((unsigned)vk.cluster_threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = K;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {&p, &g};
+    e = cudaLaunchKernelExC(&cfg, vk.cluster, args);
+  } else {
+    void* args[] = {&p};
+    e = cudaLaunchKernel(vk.block, dim3((unsigned)p.batch), dim3((unsigned)vk.block_threads), args,
+                         0, stream);
+  }
   if (e != cudaSuccess) return fail(RR_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
   return ok();
 }

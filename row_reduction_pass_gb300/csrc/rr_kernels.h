@@ -252,11 +252,22 @@ struct VerifyParams {
   int64_t cols;
   int32_t nodes;
 };
-struct VerifyKernel {
-  const void* fn;
-  int threads;
+// Launch geometry of the cluster kernel: columns of a block's slice, byte
+// offsets into its shared memory.
+struct VerifyGeo {
+  int32_t C;
+  int32_t row_bytes;  // of a slice, with room for its head
+  int32_t buf_off;    // [buffers][target, draft][row_bytes]
+  int32_t buffers;    // 2: the first child's rows are loaded ahead
+  int32_t noise_off;  // the noise's slice, -1: read from global memory
 };
-VerifyKernel verify_kernel(int dtype);
+struct VerifyKernels {
+  const void* block;  // a block per sequence, rows of any length
+  int block_threads;
+  const void* cluster;
+  int cluster_threads;
+};
+VerifyKernels verify_kernels(int dtype);
 
 // Attention of a tree of new tokens over a paged cache (k_tree.cu): bf16.
 struct TreeParams {
