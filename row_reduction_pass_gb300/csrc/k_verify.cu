@@ -39,7 +39,8 @@ namespace rr {
 namespace {
 
 constexpr int kVerT = 512;    // a block a sequence
-constexpr int kVerClT = 256;  // a cluster a sequence, threads per block
+constexpr int kVerOffNodes = 64 + 16 * (16 + 64);  // shared memory of the cluster kernel: tokens on
+constexpr int kVerClT = 1024;  // a cluster a sequence, most threads per block
 
 struct BestTok {
   float s;
@@ -212,23 +213,52 @@ __global__ void __launch_bounds__(kVerT) verify_kernel_t(const VerifyParams p) {
 
 
 // ------------------------------------------------------ a cluster a sequence ---
+//
+// Per node: rows landed -> each thread's maximum and sum over its share of both
+// slices -> block -> cluster (one meeting) -> the children's tests, a pass and a
+// meeting for each rejection -> next node, or the draw (a pass and a meeting).
+// Measured on one chain of 50304 bf16 columns (K = 8): first version, 256 threads
+// and an IEEE division per column in the draw, 2800 cycles for the statistics and
+// 10000 for the draw; hence the packed exponents, the chunk-wise maxima (a token
+// is only looked for in a chunk that beats the best so far) and 1024 threads.
+//
+// p = 2^(x c - fl(M c)) * ip, ip = 2^-r / Z with r the rounding residual of
+// fl(M c): one rounding in the exponent's argument.
+
+// The greatest of a chunk's W scores, and the first place it stands at.
+template <int W>
+__device__ __forceinline__ void best_chunk(BestTok& best, const float (&s)[W], int j) {
+  float m = s[0];
+#pragma unroll
+  for (int e = 1; e < W; ++e) m = fmaxf(m, s[e]);
+  // (a thread's chunks come in ascending order: an equal score later loses)
+  if (best.j < 0 ? m >= 0.f : m > best.s) {
+    int at = 0;
+#pragma unroll
+    for (int e = W - 1; e >= 0; --e) at = s[e] == m ? e : at;
+    best.s = m;
+    best.j = j + at;
+  }
+}
 
 template <int DT>
-__global__ void __launch_bounds__(kVerClT, 3) verify_cluster_kernel(const VerifyParams p,
-                                                                const VerifyGeo g) {
-  constexpr int E = DType<DT>::E, W = DType<DT>::V, NW = kVerClT / 32;
+__global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const VerifyParams p,
+                                                                   const VerifyGeo g) {
+  constexpr int E = DType<DT>::E, W = DType<DT>::V;
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int NT = blockDim.x, NW = NT >> 5;
   const int K = (int)cluster_nrank(), rank = (int)cluster_rank();
   const int64_t b = blockIdx.x / K, V = p.cols;
   const int n = p.nodes;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);       // [2] a node's rows have landed
-  uint64_t* met = full + 2;                                 // [2] partials published
+  uint64_t* met = full + 2;                                 // [2] the blocks' partials published
   uint64_t* noise_bar = full + 4;
-  float4* slots = reinterpret_cast<float4*>(smem + 64);     // [2][K * NW]
-  const int nslot = K * NW;
-  const int32_t* tok = p.tokens + b * n;
-  const int32_t* par = p.parents != nullptr ? p.parents + b * n : nullptr;
+  float4* slots = reinterpret_cast<float4*>(smem + 64);     // [2][8] the blocks' partials
+  float4* wslots = slots + 16;                              // [2][32] the warps'
+  int32_t* tok = reinterpret_cast<int32_t*>(smem + kVerOffNodes);  // [n] -1: absent
+  int32_t* par = tok + n;
+  float* uni = reinterpret_cast<float*>(par + n);
   const float T = p.temperature != nullptr ? __ldg(p.temperature + b) : 1.f;
   const bool greedy = T <= 0.f;
   const float c = kLog2e / T;
@@ -238,14 +268,23 @@ __global__ void __launch_bounds__(kVerClT, 3) verify_cluster_kernel(const Verify
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&met[i], nslot);
+      mbar_init(&met[i], K);
     }
     mbar_init(noise_bar, 1);
     fence_mbar_init();
   }
+  for (int i = tid; i < n; i += NT) {
+    const int32_t x = __ldg(p.tokens + b * n + i);
+    tok[i] = x >= 0 && x < V ? x : -1;
+    par[i] = p.parents != nullptr ? __ldg(p.parents + b * n + i) : i - 1;
+    uni[i] = __ldg(p.uniform + b * n + i);
+  }
   cluster_sync();  // peers arrive on this block's barriers
 
-  bool dead = false;  // a wait gave up: later waits are skipped (the kernel still ends)
+  // A wait gave up, in any thread of the block (the threads agree on it after every
+  // wait, since they meet at block barriers): the walk ends.
+  bool dead = false;
+  auto agree = [&](bool ok) { dead = __syncthreads_or(dead || !ok); };
   auto trow = [&](int node) { return p.target + ((b * (n + 1) + node + 1) * V) * E; };
   auto drow = [&](int node) { return p.draft + ((b * n + node + 1) * V) * E; };
   // A slice of a row in shared memory: its first element is h bytes into the buffer.
@@ -255,54 +294,58 @@ __global__ void __launch_bounds__(kVerClT, 3) verify_cluster_kernel(const Verify
   auto pbuf = [&](int s) { return smem + g.buf_off + s * 2 * g.row_bytes; };
   // the next child of `cur` from node i on, -1 if none (every warp by itself)
   auto next_child = [&](int cur, int i) {
-    if (par == nullptr) {
-      if (i > cur + 1 || cur + 1 >= n) return -1;
-      const int32_t x = __ldg(tok + cur + 1);
-      return x >= 0 && x < V ? cur + 1 : -1;
-    }
     for (int base = i & ~31; base < n; base += 32) {
       const int j = base + lane;
-      bool hit = false;
-      if (j >= i && j < n && __ldg(par + j) == cur) {
-        const int32_t x = __ldg(tok + j);
-        hit = x >= 0 && x < V;
-      }
-      const uint32_t m = __ballot_sync(0xffffffffu, hit);
+      const uint32_t m =
+          __ballot_sync(0xffffffffu, j >= i && j < n && par[j] == cur && tok[j] >= 0);
       if (m != 0) return base + __ffs(m) - 1;
     }
     return -1;
   };
   int loads[2] = {0, 0};  // of each buffer (the same count in every thread)
-  auto load_rows = [&](int node, bool with_draft, int s) {
+  // brings a node's rows to buffer s (the draft's if a child is to be tried)
+  auto load_rows = [&](int node, int child, int s) {
     ++loads[s];
     if (tid != 0 || dead) return;
     const char* t = trow(node);
     const char* d = drow(node);
+    const bool draft = child >= 0 && !greedy;
     const uint32_t tb = nc > 0 ? (uint32_t)((head(t) + nc * E + 15) & ~15) : 0;
-    const uint32_t db = with_draft && nc > 0 ? (uint32_t)((head(d) + nc * E + 15) & ~15) : 0;
+    const uint32_t db = draft && nc > 0 ? (uint32_t)((head(d) + nc * E + 15) & ~15) : 0;
     mbar_arrive_expect_tx(&full[s], tb + db);
     if (tb > 0)
       bulk_load(pbuf(s), t + c0 * E - head(t), tb, &full[s], policy_evict_first());
     if (db > 0)
       bulk_load(pbuf(s) + g.row_bytes, d + c0 * E - head(d), db, &full[s], policy_evict_first());
   };
-  auto wait_rows = [&](int s) {
-    if (!dead) dead = !mbar_wait_bounded(&full[s], (uint32_t)((loads[s] - 1) & 1), p.err);
+  // the logits of child i's token in the rows of `node`
+  auto logits_at = [&](int node, int i, float& t, float& d) {
+    if (i < 0 || greedy) return;
+    t = ld_elem<DT>(trow(node) + (int64_t)tok[i] * E);
+    d = ld_elem<DT>(drow(node) + (int64_t)tok[i] * E);
   };
-  // Puts this warp's partial into every block's slots, and waits for all of them.
+  auto wait_rows = [&](int s) {
+    agree(dead || mbar_wait_bounded(&full[s], (uint32_t)((loads[s] - 1) & 1), p.err));
+  };
+  // The warps' partials to shared memory, merged by warp 0 (lane l holds warp l's)
+  // with f, and its result to every block's slots; returns the K blocks' results.
   int meets = 0;
-  auto meet = [&](float4 v) -> const float4* {
+  auto meet = [&](float4 v, float4 none, auto&& f) -> const float4* {
     const int s = meets & 1;
     const uint32_t ph = (uint32_t)((meets >> 1) & 1);
     ++meets;
-    float4* sl = slots + s * nslot + rank * NW + warp;
-    if (lane < K) {  // lane k writes to block k
-      st_cluster_f32x4(map_to_rank(sl, lane), v.x, v.y, v.z, v.w);
-      mbar_arrive_cluster(map_to_rank(&met[s], lane));
+    if (lane == 0) wslots[32 * s + warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+      const float4 r = f(lane < NW ? wslots[32 * s + lane] : none);
+      if (lane < K) {  // lane k writes to block k
+        st_cluster_f32x4(map_to_rank(&slots[8 * s + rank], lane), r.x, r.y, r.z, r.w);
+        mbar_arrive_cluster(map_to_rank(&met[s], lane));
+      }
+      __syncwarp();
     }
-    __syncwarp();
-    if (!dead) dead = !mbar_wait_bounded_cluster(&met[s], ph, p.err);
-    return slots + s * nslot;
+    agree(dead || mbar_wait_bounded_cluster(&met[s], ph, p.err));
+    return slots + 8 * s;
   };
   auto wmax = [&](float v) {
 #pragma unroll
@@ -314,62 +357,101 @@ __global__ void __launch_bounds__(kVerClT, 3) verify_cluster_kernel(const Verify
     for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
   };
-  // f(j, x) for this thread's share of a slice's elements, whole 16-byte chunks
-  // where it can
-  auto each = [&](const unsigned char* buf, int h, auto&& f) {
-    const int lead = h == 0 ? 0 : min((16 - h) / E, nc);
-    const int chunks = (nc - lead) / W, rest = nc - lead - chunks * W;
-    const unsigned char* base = buf + h;
-    if (tid < lead) f(tid, ld_smem_elem<DT>(reinterpret_cast<const char*>(base) + tid * E));
-    for (int q = tid; q < chunks; q += kVerClT) {
-      const uint4 x = *reinterpret_cast<const uint4*>(base + (lead + q * W) * E);
-#pragma unroll
-      for (int e = 0; e < W; ++e) f(lead + q * W + e, chunk_get<DT>(x, e));
-    }
-    if (tid < rest) {
-      const int j = lead + chunks * W + tid;
-      f(j, ld_smem_elem<DT>(reinterpret_cast<const char*>(base) + j * E));
-    }
+  // (m, z) pairs: z sums exp((x - m) / T)
+  auto add_up = [&](float& m, float& z) {
+    const float M = wmax(m);
+    z = wsum(m == -INFINITY ? z : z * ex2((m - M) * c));
+    m = M;
   };
-  // f(j, x, y) over two slices
-  auto each2 = [&](const unsigned char* pb, int hp, const unsigned char* qb, int hq, auto&& f) {
-    if (hp == hq) {
-      const int lead = hp == 0 ? 0 : min((16 - hp) / E, nc);
-      const int chunks = (nc - lead) / W, rest = nc - lead - chunks * W;
-      if (tid < lead || (tid >= 32 && tid - 32 < rest)) {
-        const int j = tid < lead ? tid : lead + chunks * W + tid - 32;
-        f(j, ld_smem_elem<DT>(reinterpret_cast<const char*>(pb) + hp + j * E),
-          ld_smem_elem<DT>(reinterpret_cast<const char*>(qb) + hq + j * E));
+  // The shares of a slice of nc elements whose first is h bytes into its buffer: a
+  // lead of single elements up to a 16-byte boundary, whole chunks, a rest.
+  struct Parts {
+    int lead, chunks, rest;
+  };
+  auto parts = [&](int h) {
+    Parts q;
+    q.lead = h == 0 ? 0 : min((16 - h) / E, nc);
+    q.chunks = (nc - q.lead) / W;
+    q.rest = nc - q.lead - q.chunks * W;
+    return q;
+  };
+  // this thread's single element of the lead or the rest, -1 if none
+  auto single = [&](const Parts& q) {
+    return tid < q.lead ? tid : tid >= 32 && tid - 32 < q.rest ? q.lead + q.chunks * W + tid - 32 : -1;
+  };
+  // maximum, and sum about it, of this thread's share of a row
+  auto stats = [&](const unsigned char* buf, int h, float& m, float& z) {
+    const Parts q = parts(h);
+    const uint4* base = reinterpret_cast<const uint4*>(buf + h + q.lead * E);
+    const int j = single(q);
+    const float x = j >= 0 ? ld_smem_elem<DT>(reinterpret_cast<const char*>(buf) + h + j * E)
+                           : -INFINITY;
+    m = x;
+    if constexpr (DT == kBF16) {
+      uint32_t a = 0xff80ff80u, d = a;
+#pragma unroll 4
+      for (int k = tid; k < q.chunks; k += NT) {
+        const uint4 v = base[k];
+        a = bf16x2_max(a, bf16x2_max(v.x, v.y));
+        d = bf16x2_max(d, bf16x2_max(v.z, v.w));
       }
-      for (int q = tid; q < chunks; q += kVerClT) {
-        const int j = lead + q * W;
-        const uint4 x = *reinterpret_cast<const uint4*>(pb + hp + j * E);
-        const uint4 y = *reinterpret_cast<const uint4*>(qb + hq + j * E);
-#pragma unroll
-        for (int e = 0; e < W; ++e) f(j + e, chunk_get<DT>(x, e), chunk_get<DT>(y, e));
-      }
+      a = bf16x2_max(a, d);
+      m = fmaxf(m, fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u)));
     } else {
-      for (int j = tid; j < nc; j += kVerClT)
-        f(j, ld_smem_elem<DT>(reinterpret_cast<const char*>(pb) + hp + j * E),
-          ld_smem_elem<DT>(reinterpret_cast<const char*>(qb) + hq + j * E));
+      float a = -INFINITY;
+#pragma unroll 4
+      for (int k = tid; k < q.chunks; k += NT) {
+        const uint4 v = base[k];
+        a = fmaxf(a, fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)));
+        m = fmaxf(m, fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+      }
+      m = fmaxf(m, a);
     }
+    // (a share of -inf sums to 0; about 0 a NaN still gives NaN)
+    const float r = m == -INFINITY ? 0.f : m, mL = r * c;
+    float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll 2
+    for (int k = tid; k < q.chunks; k += NT) {
+      const uint4 v = base[k];
+#pragma unroll
+      for (int e = 0; e < W; e += 4) {
+        float t0, t1, t2, t3;
+        fma2(t0, t1, chunk_get<DT>(v, e), chunk_get<DT>(v, e + 1), c, c, -mL, -mL);
+        fma2(t2, t3, chunk_get<DT>(v, e + 2), chunk_get<DT>(v, e + 3), c, c, -mL, -mL);
+        add2(a0, a1, a0, a1, ex2(t0), ex2(t1));
+        add2(a2, a3, a2, a3, ex2(t2), ex2(t3));
+      }
+    }
+    z = (a0 + a1) + (a2 + a3);
+    if (j >= 0) z += ex2(fmaf(x, c, -mL));
+    z *= ex2(-fmaf(r, c, -mL));
   };
-  auto best_of = [&](BestTok t) {  // over the cluster
+  // softmax of a row: 2^(x c - mL) * inv
+  struct Soft {
+    float mL, inv;
+  };
+  auto soft = [&](float M, float Z) {
+    const float r = M == -INFINITY ? 0.f : M, mL = r * c;
+    return Soft{mL, Z == 0.f ? 0.f : ex2(-fmaf(r, c, -mL)) / Z};
+  };
+  auto merge = [&](BestTok t) {  // over the cluster
+    auto lanes = [&](BestTok r) {
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-      const float s = __shfl_xor_sync(0xffffffffu, t.s, off);
-      const int j = __shfl_xor_sync(0xffffffffu, t.j, off);
-      t.take(s, j);
-    }
-    const float4* sl = meet(make_float4(t.s, __int_as_float(t.j), 0.f, 0.f));
+      for (int off = 16; off >= 1; off >>= 1) {
+        const float s = __shfl_xor_sync(0xffffffffu, r.s, off);
+        const int j = __shfl_xor_sync(0xffffffffu, r.j, off);
+        r.take(s, j);
+      }
+      return r;
+    };
+    t = lanes(t);
+    const float4* sl = meet(make_float4(t.s, __int_as_float(t.j), 0.f, 0.f),
+                            make_float4(0.f, __int_as_float(-1), 0.f, 0.f), [&](float4 v) {
+                              const BestTok r = lanes(BestTok{v.x, __float_as_int(v.y)});
+                              return make_float4(r.s, __int_as_float(r.j), 0.f, 0.f);
+                            });
     BestTok r{0.f, -1};
-    for (int i = lane; i < nslot; i += 32) r.take(sl[i].x, __float_as_int(sl[i].y));
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-      const float s = __shfl_xor_sync(0xffffffffu, r.s, off);
-      const int j = __shfl_xor_sync(0xffffffffu, r.j, off);
-      r.take(s, j);
-    }
+    for (int i = 0; i < K; ++i) r.take(sl[i].x, __float_as_int(sl[i].y));
     return r;
   };
 
@@ -377,7 +459,9 @@ __global__ void __launch_bounds__(kVerClT, 3) verify_cluster_kernel(const Verify
   const int nh = (int)(reinterpret_cast<uintptr_t>(noise) & 15);
   int cur = -1, done = 0, s = 0;
   int child = next_child(-1, 0);
-  load_rows(-1, child >= 0 && !greedy, 0);
+  load_rows(-1, child, 0);
+  float tx = 0.f, dx = 0.f;  // the first child's logits
+  logits_at(-1, child, tx, dx);
   if (g.noise_off >= 0 && !greedy && tid == 0) {
     const uint32_t nb = nc > 0 ? (uint32_t)((nh + nc * 4 + 15) & ~15) : 0;
     mbar_arrive_expect_tx(noise_bar, nb);
@@ -387,114 +471,159 @@ __global__ void __launch_bounds__(kVerClT, 3) verify_cluster_kernel(const Verify
   }
   int32_t token = -1;
   for (;;) {
-    const char* tr = trow(cur);
-    const char* dr = drow(cur);
-    const int hp = head(tr), hq = head(dr);
+    const int hp = head(trow(cur)), hq = head(drow(cur));
     const unsigned char* pb = pbuf(s);
     const unsigned char* qb = pb + g.row_bytes;
-    // the first child's logits here, and (with two buffers) its rows
-    float tx = 0.f, dx = 0.f;
+    // with two buffers the first child's rows are loaded while this node is worked on
     int ahead = -1, ahead_child = -1;
-    if (child >= 0 && !greedy) {
-      const int32_t x = __ldg(tok + child);
-      tx = ld_elem<DT>(tr + (int64_t)x * E);
-      dx = ld_elem<DT>(dr + (int64_t)x * E);
-    }
+    float atx = 0.f, adx = 0.f;
     if (g.buffers == 2 && child >= 0) {
       ahead = child;
       ahead_child = next_child(child, child + 1);
-      load_rows(ahead, ahead_child >= 0 && !greedy, s ^ 1);
+      load_rows(ahead, ahead_child, s ^ 1);
+      logits_at(ahead, ahead_child, atx, adx);
     }
     wait_rows(s);
-    VerRow pr{}, qr{};
+    Soft P{}, Q{};
     BestTok top{0.f, -1};
     if (greedy) {
-      each(pb, hp, [&](int j, float v) {
-        if (v > -INFINITY) top.take(v, (int)(c0 + j));
-      });
-      top = best_of(top);
+      const Parts q = parts(hp);
+      float m = -INFINITY;
+      int at = INT32_MAX;
+      const int j1 = single(q);
+      const char* row = reinterpret_cast<const char*>(pb) + hp;
+      auto look = [&](float v, int j) {
+        if (v > m || (v == m && j < at && v > -INFINITY)) {
+          m = v;
+          at = j;
+        }
+      };
+      if (j1 >= 0) look(ld_smem_elem<DT>(row + j1 * E), j1);
+      for (int k = tid; k < q.chunks; k += NT) {
+        const int j = q.lead + k * W;
+        const uint4 v = *reinterpret_cast<const uint4*>(row + j * E);
+        float x[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) x[e] = chunk_get<DT>(v, e);
+        float cm = x[0];
+#pragma unroll
+        for (int e = 1; e < W; ++e) cm = fmaxf(cm, x[e]);
+        if (cm >= m) {
+#pragma unroll
+          for (int e = 0; e < W; ++e) look(x[e], j + e);
+        }
+      }
+      top = merge(BestTok{m, m > -INFINITY ? (int)(c0 + at) : -1});
     } else {
-      // maxima, then sums about the thread's maximum; merged with the cluster's
-      float mp = -INFINITY, mq = -INFINITY, zp = 0.f, zq = 0.f;
-      each(pb, hp, [&](int, float v) { mp = fmaxf(mp, v); });
-      if (child >= 0) each(qb, hq, [&](int, float v) { mq = fmaxf(mq, v); });
-      mp = wmax(mp);
-      mq = wmax(mq);
-      // (a row of -inf here gives 0; about 0 a NaN still gives NaN)
-      const float rp = mp == -INFINITY ? 0.f : mp, rq = mq == -INFINITY ? 0.f : mq;
-      each(pb, hp, [&](int, float v) { zp += ex2((v - rp) * c); });
-      if (child >= 0) each(qb, hq, [&](int, float v) { zq += ex2((v - rq) * c); });
-      const float4* sl = meet(make_float4(mp, wsum(zp), mq, wsum(zq)));
-      float Mp = -INFINITY, Mq = -INFINITY;
-      for (int i = lane; i < nslot; i += 32) {
+      float mp, zp, mq = -INFINITY, zq = 0.f;
+      stats(pb, hp, mp, zp);
+      if (child >= 0) stats(qb, hq, mq, zq);
+      add_up(mp, zp);
+      add_up(mq, zq);
+      const float4* sl = meet(make_float4(mp, zp, mq, zq),
+                              make_float4(-INFINITY, 0.f, -INFINITY, 0.f), [&](float4 v) {
+                                add_up(v.x, v.y);
+                                add_up(v.z, v.w);
+                                return v;
+                              });
+      float Mp = -INFINITY, Mq = -INFINITY, Zp = 0.f, Zq = 0.f;
+      for (int i = 0; i < K; ++i) {
         Mp = fmaxf(Mp, sl[i].x);
         Mq = fmaxf(Mq, sl[i].z);
       }
-      Mp = wmax(Mp);
-      Mq = wmax(Mq);
-      float Zp = 0.f, Zq = 0.f;
-      for (int i = lane; i < nslot; i += 32) {
+      for (int i = 0; i < K; ++i) {
         const float4 t = sl[i];
         Zp += t.x == -INFINITY ? t.y : t.y * ex2((t.x - Mp) * c);
         Zq += t.z == -INFINITY ? t.w : t.w * ex2((t.z - Mq) * c);
       }
-      Zp = wsum(Zp);
-      Zq = wsum(Zq);
-      pr = {nullptr, Mp, Zp == 0.f ? 0.f : 1.f / Zp};
-      qr = {nullptr, Mq, Zq == 0.f ? 0.f : 1.f / Zq};
+      P = soft(Mp, Zp);
+      Q = soft(Mq, Zq);
     }
-    auto prob = [&](const VerRow& r, float v) {
-      return v == -INFINITY ? 0.f : ex2((v - r.m) * c) * r.inv;
-    };
+    auto prob = [&](const Soft& r, float v) { return ex2(fmaf(v, c, -r.mL)) * r.inv; };
     float ratio = 0.f, mass = 1.f;
+    // max(p - ratio q, 0) of W columns
+    auto residual = [&](const uint4& x, const uint4& y, float (&w)[W]) {
+      const float rq = -ratio * Q.inv;
+#pragma unroll
+      for (int e = 0; e < W; e += 2) {
+        float t0, t1, u0, u1;
+        fma2(t0, t1, chunk_get<DT>(x, e), chunk_get<DT>(x, e + 1), c, c, -P.mL, -P.mL);
+        fma2(u0, u1, chunk_get<DT>(y, e), chunk_get<DT>(y, e + 1), c, c, -Q.mL, -Q.mL);
+        mul2(t0, t1, ex2(t0), ex2(t1), P.inv, P.inv);
+        fma2(t0, t1, ex2(u0), ex2(u1), rq, rq, t0, t1);
+        w[e] = fmaxf(t0, 0.f);
+        w[e + 1] = fmaxf(t1, 0.f);
+      }
+    };
+    auto residual1 = [&](int j) {
+      const float v = ld_smem_elem<DT>(reinterpret_cast<const char*>(pb) + hp + j * E);
+      const float u = ratio > 0.f ? ld_smem_elem<DT>(reinterpret_cast<const char*>(qb) + hq + j * E)
+                                  : -INFINITY;
+      return fmaxf(fmaf(ex2(fmaf(u, c, -Q.mL)), -ratio * Q.inv, prob(P, v)), 0.f);
+    };
     int next = -1;
     for (int i = child; i >= 0 && !dead;) {
-      const int32_t x = __ldg(tok + i);
       if (greedy) {
-        if (x == top.j) {
+        if (tok[i] == top.j) {
           next = i;
           break;
         }
       } else {
-        if (i != child) {
-          tx = ld_elem<DT>(tr + (int64_t)x * E);
-          dx = ld_elem<DT>(dr + (int64_t)x * E);
-        }
-        const float px = prob(pr, tx), qx = prob(qr, dx);
-        if (__ldg(p.uniform + b * n + i) * mass * qx < px - ratio * qx) {
+        if (i != child) logits_at(cur, i, tx, dx);
+        const float px = prob(P, tx), qx = prob(Q, dx);
+        if (uni[i] * mass * qx < px - ratio * qx) {
           next = i;
           break;
         }
         ratio += mass;
         float w = 0.f;
-        each2(pb, hp, qb, hq, [&](int, float v, float u) {
-          const float t = prob(pr, v) - ratio * prob(qr, u);
-          w += t < 0.f ? 0.f : t;
-        });
-        const float4* sl = meet(make_float4(wsum(w), 0.f, 0.f, 0.f));
+        if (hp == hq) {
+          const Parts q = parts(hp);
+          const uint4* pv = reinterpret_cast<const uint4*>(pb + hp + q.lead * E);
+          const uint4* qv = reinterpret_cast<const uint4*>(qb + hp + q.lead * E);
+          float w1 = 0.f;
+#pragma unroll 2
+          for (int k = tid; k < q.chunks; k += NT) {
+            float r[W];
+            residual(pv[k], qv[k], r);
+#pragma unroll
+            for (int e = 0; e < W; e += 2) add2(w, w1, w, w1, r[e], r[e + 1]);
+          }
+          w += w1;
+          const int j = single(q);
+          if (j >= 0) w += residual1(j);
+        } else {
+#pragma unroll 4
+          for (int j = tid; j < nc; j += NT) w += residual1(j);
+        }
+        auto sum = [&](float4 v) { return make_float4(wsum(v.x), 0.f, 0.f, 0.f); };
+        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4* sl = meet(make_float4(wsum(w), 0.f, 0.f, 0.f), none, sum);
         mass = 0.f;
-        for (int k = lane; k < nslot; k += 32) mass += sl[k].x;
-        mass = wsum(mass);
+        for (int k = 0; k < K; ++k) mass += sl[k].x;
         if (!(mass > 0.f)) break;  // nothing of the target is left
       }
       i = next_child(cur, i + 1);
     }
     if (next >= 0 && !dead) {
       if (tid == 0 && rank == 0) {
-        p.out_tokens[b * (n + 1) + done] = __ldg(tok + next);
+        p.out_tokens[b * (n + 1) + done] = tok[next];
         p.out_nodes[b * (n + 1) + done] = next;
       }
       ++done;
       cur = next;
-      // every warp of the cluster has done with this node's rows (it has met the
-      // others since it read them), so the buffers may be filled again
+      // every warp of the cluster has done with this node's rows (the blocks have met
+      // since it read them), so the buffers may be filled again
       if (next == ahead) {
         child = ahead_child;
+        tx = atx;
+        dx = adx;
         s ^= 1;
       } else {
         if (ahead >= 0) wait_rows(s ^ 1);  // the rows that were loaded in vain
         child = next_child(cur, cur + 1);
-        load_rows(cur, child >= 0 && !greedy, s);
+        load_rows(cur, child, s);
+        logits_at(cur, child, tx, dx);
       }
       continue;
     }
@@ -504,28 +633,59 @@ __global__ void __launch_bounds__(kVerClT, 3) verify_cluster_kernel(const Verify
       if (!(mass > 0.f)) ratio = 0.f;
       const float* ns = noise;
       if (g.noise_off >= 0) {
-        dead = !mbar_wait_bounded(noise_bar, 0, p.err);
+        agree(mbar_wait_bounded(noise_bar, 0, p.err));
         ns = reinterpret_cast<const float*>(smem + g.noise_off + nh);
       }
       BestTok best{0.f, -1};
-      auto bid = [&](int j, float w) {
-        if (w > 0.f) {
-          const float sc = w / ns[j];
-          if (sc >= 0.f) best.take(sc, (int)(c0 + j));
+      auto score = [&](float w, float e) { return w > 0.f ? __fdividef(w, e) : -1.f; };
+      if (ratio == 0.f || hp == hq) {
+        const Parts q = parts(hp);
+        const uint4* pv = reinterpret_cast<const uint4*>(pb + hp + q.lead * E);
+        const uint4* qv = reinterpret_cast<const uint4*>(qb + hq + q.lead * E);
+        const bool whole = ((nh + q.lead * 4) & 15) == 0;
+        const uint32_t ni = DT == kBF16 ? 0xff80ff80u : 0xff800000u;
+#pragma unroll 1
+        for (int k = tid; k < q.chunks; k += NT) {
+          const int j = q.lead + k * W;
+          float e8[W];
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < W; e += 4) {
+              const float4 t = *reinterpret_cast<const float4*>(ns + j + e);
+              e8[e] = t.x, e8[e + 1] = t.y, e8[e + 2] = t.z, e8[e + 3] = t.w;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e) e8[e] = ns[j + e];
+          }
+          float r[W];
+          residual(pv[k], ratio > 0.f ? qv[k] : make_uint4(ni, ni, ni, ni), r);
+#pragma unroll
+          for (int e = 0; e < W; ++e) r[e] = score(r[e], e8[e]);
+          best_chunk<W>(best, r, (int)c0 + j);
         }
-      };
-      if (ratio > 0.f)
-        each2(pb, hp, qb, hq,
-              [&](int j, float v, float u) { bid(j, prob(pr, v) - ratio * prob(qr, u)); });
-      else
-        each(pb, hp, [&](int j, float v) { bid(j, prob(pr, v)); });
-      token = best_of(best).j;
+        const int j = single(q);
+        if (j >= 0) {
+          const float sc = score(residual1(j), ns[j]);
+          if (sc >= 0.f) best.take(sc, (int)c0 + j);
+        }
+      } else {
+#pragma unroll 4
+        for (int j = tid; j < nc; j += NT) {
+          const float sc = score(residual1(j), ns[j]);
+          if (best.j < 0 ? sc >= 0.f : sc > best.s) {
+            best.s = sc;
+            best.j = (int)c0 + j;
+          }
+        }
+      }
+      token = merge(best).j;
     }
     if (ahead >= 0) wait_rows(s ^ 1);  // no copy outlives the block
     break;
   }
   if (rank == 0) {
-    for (int i = done + tid; i <= n; i += kVerClT) {
+    for (int i = done + tid; i <= n; i += NT) {
       p.out_tokens[b * (n + 1) + i] = i == done ? token : -1;
       p.out_nodes[b * (n + 1) + i] = -1;
     }
@@ -539,9 +699,9 @@ __global__ void __launch_bounds__(kVerClT, 3) verify_cluster_kernel(const Verify
 VerifyKernels verify_kernels(int dtype) {
   if (dtype == kBF16)
     return {(const void*)verify_kernel_t<kBF16>, kVerT, (const void*)verify_cluster_kernel<kBF16>,
-            kVerClT};
+            kVerOffNodes};
   return {(const void*)verify_kernel_t<kF32>, kVerT, (const void*)verify_cluster_kernel<kF32>,
-          kVerClT};
+          kVerOffNodes};
 }
 
 }  // namespace rr

@@ -1383,7 +1383,7 @@ rr_status distill_launch(rr::DistillParams p, rr_dtype dt, cudaStream_t stream) 
 rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
   const rr::VerifyKernels vk = rr::verify_kernels(dt);
   const int64_t E = dt == RR_BF16 ? 2 : 4;
-  int K = 0;
+  int K = 0, threads = 256;
   rr::VerifyGeo g{};
   size_t smem = 0;
   {
@@ -1396,7 +1396,7 @@ rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
       rr::VerifyGeo t{};
       const int64_t C = round_up(cdiv(p.cols, k), 16);
       const int64_t row = round_up(C * E + 32, 128);
-      const int64_t buf = round_up(64 + 2 * 16 * k * (vk.cluster_threads / 32), 128);
+      const int64_t buf = round_up(vk.nodes_off + 12 * (int64_t)p.nodes, 128);
       const int64_t noise = buf + (ahead ? 2 : 1) * 2 * row;
       const int64_t total = noise + (ahead ? round_up(C * 4 + 32, 128) : 0);
       if (total > di->smem_optin) return false;
@@ -1412,8 +1412,8 @@ rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
     };
     int kmax = 8;
     while (kmax > 1 && p.cols < 512 * kmax) kmax /= 2;
-    int forced = 0, fa = -1;
-    if (const char* f = std::getenv("RR_VER_K")) std::sscanf(f, "%d:%d", &forced, &fa);
+    int forced = 0, fa = -1, ft = 0;
+    if (const char* f = std::getenv("RR_VER_K")) std::sscanf(f, "%d:%d:%d", &forced, &fa, &ft);
     for (int k = kmax; k >= 1 && K == 0; k /= 2)
       if (p.batch * k <= di->sms && (forced == 0 || forced == k)) shape(k, fa != 0);
     for (int k = kmax; k >= 1 && K == 0; k /= 2)
@@ -1424,6 +1424,8 @@ rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
           break;
         }
       }
+    // 1024 threads an SM: shared among the blocks that fit by shared memory
+    if (ft) threads = ft;
     if (K > 0 && (st = set_smem(di, vk.cluster, smem)) != RR_OK) return st;
   }
   cudaError_t e;
@@ -1431,7 +1433,7 @@ rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3((unsigned)(p.batch * K));
-    cfg.blockDim = dim3((unsigned)vk.cluster_threads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;

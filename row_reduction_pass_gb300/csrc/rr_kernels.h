@@ -265,7 +265,7 @@ struct VerifyKernels {
   const void* block;  // a block per sequence, rows of any length
   int block_threads;
   const void* cluster;
-  int cluster_threads;
+  int nodes_off;  // cluster kernel: 12 bytes a node from this byte of shared memory on
 };
 VerifyKernels verify_kernels(int dtype);
 
