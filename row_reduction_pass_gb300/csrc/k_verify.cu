@@ -39,8 +39,7 @@ namespace rr {
 namespace {
 
 constexpr int kVerT = 512;    // a block a sequence
-constexpr int kVerOffNodes = 64 + 16 * (16 + 64);  // shared memory of the cluster kernel: tokens on
-constexpr int kVerClT = 1024;  // a cluster a sequence, most threads per block
+constexpr int kVerClT = 288;  // a cluster a sequence, threads per block
 
 struct BestTok {
   float s;
@@ -220,7 +219,9 @@ __global__ void __launch_bounds__(kVerT) verify_kernel_t(const VerifyParams p) {
 // Measured on one chain of 50304 bf16 columns (K = 8): first version, 256 threads
 // and an IEEE division per column in the draw, 2800 cycles for the statistics and
 // 10000 for the draw; hence the packed exponents, the chunk-wise maxima (a token
-// is only looked for in a chunk that beats the best so far) and 1024 threads.
+// is only looked for in a chunk that beats the best so far), and a warp of its own
+// that issues the loads (the address arithmetic and the copies held its warp up for
+// 1300 cycles a node).
 //
 // p = 2^(x c - fl(M c)) * ip, ip = 2^-r / Z with r the rounding residual of
 // fl(M c): one rounding in the exponent's argument.
@@ -242,21 +243,22 @@ __device__ __forceinline__ void best_chunk(BestTok& best, const float (&s)[W], i
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const VerifyParams p,
+__global__ void __launch_bounds__(kVerClT, 3) verify_cluster_kernel(const VerifyParams p,
                                                                    const VerifyGeo g) {
   constexpr int E = DType<DT>::E, W = DType<DT>::V;
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int NT = blockDim.x, NW = NT >> 5;
+  const int NT = blockDim.x - 32, NW = NT >> 5;  // the working warps; then the loading one
+  const bool works = warp < NW;
   const int K = (int)cluster_nrank(), rank = (int)cluster_rank();
   const int64_t b = blockIdx.x / K, V = p.cols;
   const int n = p.nodes;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);       // [2] a node's rows have landed
   uint64_t* met = full + 2;                                 // [2] the blocks' partials published
   uint64_t* noise_bar = full + 4;
-  float4* slots = reinterpret_cast<float4*>(smem + 64);     // [2][8] the blocks' partials
-  float4* wslots = slots + 16;                              // [2][32] the warps'
-  int32_t* tok = reinterpret_cast<int32_t*>(smem + kVerOffNodes);  // [n] -1: absent
+  float4* slots = reinterpret_cast<float4*>(smem + 64);     // [2][K * NW] partials
+  const int nslot = K * NW;
+  int32_t* tok = reinterpret_cast<int32_t*>(smem + g.nodes_off);  // [n] -1: absent
   int32_t* par = tok + n;
   float* uni = reinterpret_cast<float*>(par + n);
   const float T = p.temperature != nullptr ? __ldg(p.temperature + b) : 1.f;
@@ -268,12 +270,12 @@ __global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const Verify
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&met[i], K);
+      mbar_init(&met[i], nslot);
     }
     mbar_init(noise_bar, 1);
     fence_mbar_init();
   }
-  for (int i = tid; i < n; i += NT) {
+  for (int i = tid; i < n; i += blockDim.x) {
     const int32_t x = __ldg(p.tokens + b * n + i);
     tok[i] = x >= 0 && x < V ? x : -1;
     par[i] = p.parents != nullptr ? __ldg(p.parents + b * n + i) : i - 1;
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const Verify
   // brings a node's rows to buffer s (the draft's if a child is to be tried)
   auto load_rows = [&](int node, int child, int s) {
     ++loads[s];
-    if (tid != 0 || dead) return;
+    if (tid != NT || dead) return;
     const char* t = trow(node);
     const char* d = drow(node);
     const bool draft = child >= 0 && !greedy;
@@ -327,41 +329,43 @@ __global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const Verify
   auto wait_rows = [&](int s) {
     agree(dead || mbar_wait_bounded(&full[s], (uint32_t)((loads[s] - 1) & 1), p.err));
   };
-  // The warps' partials to shared memory, merged by warp 0 (lane l holds warp l's)
-  // with f, and its result to every block's slots; returns the K blocks' results.
+  // Puts this warp's partial into every block's slots, and waits for all of them.
   int meets = 0;
-  auto meet = [&](float4 v, float4 none, auto&& f) -> const float4* {
+  auto meet = [&](float4 v) -> const float4* {
     const int s = meets & 1;
     const uint32_t ph = (uint32_t)((meets >> 1) & 1);
     ++meets;
-    if (lane == 0) wslots[32 * s + warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-      const float4 r = f(lane < NW ? wslots[32 * s + lane] : none);
-      if (lane < K) {  // lane k writes to block k
-        st_cluster_f32x4(map_to_rank(&slots[8 * s + rank], lane), r.x, r.y, r.z, r.w);
-        mbar_arrive_cluster(map_to_rank(&met[s], lane));
-      }
-      __syncwarp();
+    if (works && lane < K) {  // lane k writes to block k
+      float4* sl = slots + s * nslot + rank * NW + warp;
+      st_cluster_f32x4(map_to_rank(sl, lane), v.x, v.y, v.z, v.w);
+      mbar_arrive_cluster(map_to_rank(&met[s], lane));
     }
+    __syncwarp();
     agree(dead || mbar_wait_bounded_cluster(&met[s], ph, p.err));
-    return slots + 8 * s;
-  };
-  auto wmax = [&](float v) {
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-    return v;
+    return slots + s * nslot;
   };
   auto wsum = [&](float v) {
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
   };
-  // (m, z) pairs: z sums exp((x - m) / T)
-  auto add_up = [&](float& m, float& z) {
-    const float M = wmax(m);
-    z = wsum(m == -INFINITY ? z : z * ex2((m - M) * c));
+  // two (m, z) pairs over the warp: z sums exp((x - m) / T)
+  auto add_up2 = [&](float& m, float& z, float& m2, float& z2) {
+    float M = m, M2 = m2;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      M2 = fmaxf(M2, __shfl_xor_sync(0xffffffffu, M2, off));
+    }
+    if (m != -INFINITY) z *= ex2((m - M) * c);
+    if (m2 != -INFINITY) z2 *= ex2((m2 - M2) * c);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+      z += __shfl_xor_sync(0xffffffffu, z, off);
+      z2 += __shfl_xor_sync(0xffffffffu, z2, off);
+    }
     m = M;
+    m2 = M2;
   };
   // The shares of a slice of nc elements whose first is h bytes into its buffer: a
   // lead of single elements up to a 16-byte boundary, whole chunks, a rest.
@@ -381,50 +385,51 @@ __global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const Verify
   };
   // maximum, and sum about it, of this thread's share of a row
   auto stats = [&](const unsigned char* buf, int h, float& m, float& z) {
+    constexpr uint32_t ni = DT == kBF16 ? 0xff80ff80u : 0xff800000u;
     const Parts q = parts(h);
     const uint4* base = reinterpret_cast<const uint4*>(buf + h + q.lead * E);
     const int j = single(q);
     const float x = j >= 0 ? ld_smem_elem<DT>(reinterpret_cast<const char*>(buf) + h + j * E)
                            : -INFINITY;
     m = x;
-    if constexpr (DT == kBF16) {
-      uint32_t a = 0xff80ff80u, d = a;
-#pragma unroll 4
-      for (int k = tid; k < q.chunks; k += NT) {
-        const uint4 v = base[k];
-        a = bf16x2_max(a, bf16x2_max(v.x, v.y));
-        d = bf16x2_max(d, bf16x2_max(v.z, v.w));
-      }
-      a = bf16x2_max(a, d);
-      m = fmaxf(m, fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u)));
-    } else {
-      float a = -INFINITY;
-#pragma unroll 4
-      for (int k = tid; k < q.chunks; k += NT) {
-        const uint4 v = base[k];
-        a = fmaxf(a, fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)));
-        m = fmaxf(m, fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
-      }
-      m = fmaxf(m, a);
-    }
-    // (a share of -inf sums to 0; about 0 a NaN still gives NaN)
-    const float r = m == -INFINITY ? 0.f : m, mL = r * c;
-    float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-#pragma unroll 2
-    for (int k = tid; k < q.chunks; k += NT) {
-      const uint4 v = base[k];
+    z = x == -INFINITY ? 0.f : x == x ? 1.f : x;
+    // four chunks at a time: their maximum, the sum so far rescaled to it, then
+    // their exponentials
+    for (int k = tid; k < q.chunks; k += 4 * NT) {
+      uint4 v[4];
+      float cm = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < W; e += 4) {
-        float t0, t1, t2, t3;
-        fma2(t0, t1, chunk_get<DT>(v, e), chunk_get<DT>(v, e + 1), c, c, -mL, -mL);
-        fma2(t2, t3, chunk_get<DT>(v, e + 2), chunk_get<DT>(v, e + 3), c, c, -mL, -mL);
-        add2(a0, a1, a0, a1, ex2(t0), ex2(t1));
-        add2(a2, a3, a2, a3, ex2(t2), ex2(t3));
+      for (int i = 0; i < 4; ++i) {
+        v[i] = k + i * NT < q.chunks ? base[k + i * NT] : make_uint4(ni, ni, ni, ni);
+        if constexpr (DT == kBF16) {
+          const uint32_t w = bf16x2_max(bf16x2_max(v[i].x, v[i].y), bf16x2_max(v[i].z, v[i].w));
+          cm = fmaxf(cm, fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
+        } else {
+          cm = fmaxf(fmaxf(cm, fmaxf(__uint_as_float(v[i].x), __uint_as_float(v[i].y))),
+                     fmaxf(__uint_as_float(v[i].z), __uint_as_float(v[i].w)));
+        }
       }
+      if (cm > m) {
+        z = m == -INFINITY ? z : z * ex2((m - cm) * c);
+        m = cm;
+      }
+      // (a share of -inf sums to 0; about 0 a NaN still gives NaN)
+      const float r = m == -INFINITY ? 0.f : m, mL = r * c;
+      float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (k + i * NT >= q.chunks) break;
+#pragma unroll
+        for (int e = 0; e < W; e += 4) {
+          float t0, t1, t2, t3;
+          fma2(t0, t1, chunk_get<DT>(v[i], e), chunk_get<DT>(v[i], e + 1), c, c, -mL, -mL);
+          fma2(t2, t3, chunk_get<DT>(v[i], e + 2), chunk_get<DT>(v[i], e + 3), c, c, -mL, -mL);
+          add2(a0, a1, a0, a1, ex2(t0), ex2(t1));
+          add2(a2, a3, a2, a3, ex2(t2), ex2(t3));
+        }
+      }
+      z += ((a0 + a1) + (a2 + a3)) * ex2(-fmaf(r, c, -mL));
     }
-    z = (a0 + a1) + (a2 + a3);
-    if (j >= 0) z += ex2(fmaf(x, c, -mL));
-    z *= ex2(-fmaf(r, c, -mL));
   };
   // softmax of a row: 2^(x c - mL) * inv
   struct Soft {
@@ -445,14 +450,10 @@ __global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const Verify
       return r;
     };
     t = lanes(t);
-    const float4* sl = meet(make_float4(t.s, __int_as_float(t.j), 0.f, 0.f),
-                            make_float4(0.f, __int_as_float(-1), 0.f, 0.f), [&](float4 v) {
-                              const BestTok r = lanes(BestTok{v.x, __float_as_int(v.y)});
-                              return make_float4(r.s, __int_as_float(r.j), 0.f, 0.f);
-                            });
+    const float4* sl = meet(make_float4(t.s, __int_as_float(t.j), 0.f, 0.f));
     BestTok r{0.f, -1};
-    for (int i = 0; i < K; ++i) r.take(sl[i].x, __float_as_int(sl[i].y));
-    return r;
+    for (int i = lane; i < nslot; i += 32) r.take(sl[i].x, __float_as_int(sl[i].y));
+    return lanes(r);
   };
 
   const float* noise = p.race + b * V + c0;  // this block's part
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const Verify
   load_rows(-1, child, 0);
   float tx = 0.f, dx = 0.f;  // the first child's logits
   logits_at(-1, child, tx, dx);
-  if (g.noise_off >= 0 && !greedy && tid == 0) {
+  if (g.noise_off >= 0 && !greedy && tid == NT) {
     const uint32_t nb = nc > 0 ? (uint32_t)((nh + nc * 4 + 15) & ~15) : 0;
     mbar_arrive_expect_tx(noise_bar, nb);
     if (nb > 0)
@@ -498,8 +499,8 @@ __global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const Verify
           at = j;
         }
       };
-      if (j1 >= 0) look(ld_smem_elem<DT>(row + j1 * E), j1);
-      for (int k = tid; k < q.chunks; k += NT) {
+      if (works && j1 >= 0) look(ld_smem_elem<DT>(row + j1 * E), j1);
+      for (int k = tid; works && k < q.chunks; k += NT) {
         const int j = q.lead + k * W;
         const uint4 v = *reinterpret_cast<const uint4*>(row + j * E);
         float x[W];
@@ -515,27 +516,26 @@ __global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const Verify
       }
       top = merge(BestTok{m, m > -INFINITY ? (int)(c0 + at) : -1});
     } else {
-      float mp, zp, mq = -INFINITY, zq = 0.f;
-      stats(pb, hp, mp, zp);
-      if (child >= 0) stats(qb, hq, mq, zq);
-      add_up(mp, zp);
-      add_up(mq, zq);
-      const float4* sl = meet(make_float4(mp, zp, mq, zq),
-                              make_float4(-INFINITY, 0.f, -INFINITY, 0.f), [&](float4 v) {
-                                add_up(v.x, v.y);
-                                add_up(v.z, v.w);
-                                return v;
-                              });
-      float Mp = -INFINITY, Mq = -INFINITY, Zp = 0.f, Zq = 0.f;
-      for (int i = 0; i < K; ++i) {
-        Mp = fmaxf(Mp, sl[i].x);
-        Mq = fmaxf(Mq, sl[i].z);
+      float mp = -INFINITY, zp = 0.f, mq = -INFINITY, zq = 0.f;
+      if (works) {
+        stats(pb, hp, mp, zp);
+        if (child >= 0) stats(qb, hq, mq, zq);
+        add_up2(mp, zp, mq, zq);
       }
-      for (int i = 0; i < K; ++i) {
+      const float4* sl = meet(make_float4(mp, zp, mq, zq));
+      // lane l takes slots l, l + 32, ...; every warp the same way
+      float Mp = -INFINITY, Zp = 0.f, Mq = -INFINITY, Zq = 0.f;
+      for (int i = lane; i < nslot; i += 32) {
         const float4 t = sl[i];
-        Zp += t.x == -INFINITY ? t.y : t.y * ex2((t.x - Mp) * c);
-        Zq += t.z == -INFINITY ? t.w : t.w * ex2((t.z - Mq) * c);
+        const float a = fmaxf(Mp, t.x), d = fmaxf(Mq, t.z);
+        Zp = (Mp == -INFINITY ? Zp : Zp * ex2((Mp - a) * c)) +
+             (t.x == -INFINITY ? t.y : t.y * ex2((t.x - a) * c));
+        Zq = (Mq == -INFINITY ? Zq : Zq * ex2((Mq - d) * c)) +
+             (t.z == -INFINITY ? t.w : t.w * ex2((t.z - d) * c));
+        Mp = a;
+        Mq = d;
       }
+      add_up2(Mp, Zp, Mq, Zq);
       P = soft(Mp, Zp);
       Q = soft(Mq, Zq);
     }
@@ -577,7 +577,8 @@ __global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const Verify
         }
         ratio += mass;
         float w = 0.f;
-        if (hp == hq) {
+        if (!works) {
+        } else if (hp == hq) {
           const Parts q = parts(hp);
           const uint4* pv = reinterpret_cast<const uint4*>(pb + hp + q.lead * E);
           const uint4* qv = reinterpret_cast<const uint4*>(qb + hp + q.lead * E);
@@ -596,11 +597,10 @@ __global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const Verify
 #pragma unroll 4
           for (int j = tid; j < nc; j += NT) w += residual1(j);
         }
-        auto sum = [&](float4 v) { return make_float4(wsum(v.x), 0.f, 0.f, 0.f); };
-        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4* sl = meet(make_float4(wsum(w), 0.f, 0.f, 0.f), none, sum);
+        const float4* sl = meet(make_float4(wsum(w), 0.f, 0.f, 0.f));
         mass = 0.f;
-        for (int k = 0; k < K; ++k) mass += sl[k].x;
+        for (int k = lane; k < nslot; k += 32) mass += sl[k].x;
+        mass = wsum(mass);
         if (!(mass > 0.f)) break;  // nothing of the target is left
       }
       i = next_child(cur, i + 1);
@@ -638,7 +638,8 @@ __global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const Verify
       }
       BestTok best{0.f, -1};
       auto score = [&](float w, float e) { return w > 0.f ? __fdividef(w, e) : -1.f; };
-      if (ratio == 0.f || hp == hq) {
+      if (!works) {
+      } else if (ratio == 0.f || hp == hq) {
         const Parts q = parts(hp);
         const uint4* pv = reinterpret_cast<const uint4*>(pb + hp + q.lead * E);
         const uint4* qv = reinterpret_cast<const uint4*>(qb + hq + q.lead * E);
@@ -685,7 +686,7 @@ __global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const Verify
     break;
   }
   if (rank == 0) {
-    for (int i = done + tid; i <= n; i += NT) {
+    for (int i = done + tid; i <= n; i += blockDim.x) {
       p.out_tokens[b * (n + 1) + i] = i == done ? token : -1;
       p.out_nodes[b * (n + 1) + i] = -1;
     }
@@ -698,10 +699,8 @@ __global__ void __launch_bounds__(kVerClT, 1) verify_cluster_kernel(const Verify
 
 VerifyKernels verify_kernels(int dtype) {
   if (dtype == kBF16)
-    return {(const void*)verify_kernel_t<kBF16>, kVerT, (const void*)verify_cluster_kernel<kBF16>,
-            kVerOffNodes};
-  return {(const void*)verify_kernel_t<kF32>, kVerT, (const void*)verify_cluster_kernel<kF32>,
-          kVerOffNodes};
+    return {(const void*)verify_kernel_t<kBF16>, kVerT, (const void*)verify_cluster_kernel<kBF16>};
+  return {(const void*)verify_kernel_t<kF32>, kVerT, (const void*)verify_cluster_kernel<kF32>};
 }
 
 }  // namespace rr

@@ -1396,11 +1396,13 @@ rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
       rr::VerifyGeo t{};
       const int64_t C = round_up(cdiv(p.cols, k), 16);
       const int64_t row = round_up(C * E + 32, 128);
-      const int64_t buf = round_up(vk.nodes_off + 12 * (int64_t)p.nodes, 128);
+      const int64_t nodes = 64 + 2 * 16 * k * (threads / 32);
+      const int64_t buf = round_up(nodes + 12 * (int64_t)p.nodes, 128);
       const int64_t noise = buf + (ahead ? 2 : 1) * 2 * row;
       const int64_t total = noise + (ahead ? round_up(C * 4 + 32, 128) : 0);
       if (total > di->smem_optin) return false;
       t.C = (int32_t)C;
+      t.nodes_off = (int32_t)nodes;
       t.row_bytes = (int32_t)row;
       t.buf_off = (int32_t)buf;
       t.buffers = ahead ? 2 : 1;
@@ -1414,6 +1416,7 @@ rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
     while (kmax > 1 && p.cols < 512 * kmax) kmax /= 2;
     int forced = 0, fa = -1, ft = 0;
     if (const char* f = std::getenv("RR_VER_K")) std::sscanf(f, "%d:%d:%d", &forced, &fa, &ft);
+    if (ft) threads = ft;
     for (int k = kmax; k >= 1 && K == 0; k /= 2)
       if (p.batch * k <= di->sms && (forced == 0 || forced == k)) shape(k, fa != 0);
     for (int k = kmax; k >= 1 && K == 0; k /= 2)
@@ -1425,7 +1428,6 @@ rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
         }
       }
     // 1024 threads an SM: shared among the blocks that fit by shared memory
-    if (ft) threads = ft;
     if (K > 0 && (st = set_smem(di, vk.cluster, smem)) != RR_OK) return st;
   }
   cudaError_t e;
@@ -1433,7 +1435,7 @@ rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3((unsigned)(p.batch * K));
-    cfg.blockDim = dim3((unsigned)threads);
+    cfg.blockDim = dim3((unsigned)threads + 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;

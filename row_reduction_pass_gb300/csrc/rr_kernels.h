@@ -260,12 +260,12 @@ struct VerifyGeo {
   int32_t buf_off;    // [buffers][target, draft][row_bytes]
   int32_t buffers;    // 2: the first child's rows are loaded ahead
   int32_t noise_off;  // the noise's slice, -1: read from global memory
+  int32_t nodes_off;  // tokens, parents, uniform numbers: 12 bytes a node
 };
 struct VerifyKernels {
   const void* block;  // a block per sequence, rows of any length
   int block_threads;
   const void* cluster;
-  int nodes_off;  // cluster kernel: 12 bytes a node from this byte of shared memory on
 };
 VerifyKernels verify_kernels(int dtype);
 
