@@ -39,7 +39,7 @@ namespace rr {
 namespace {
 
 constexpr int kVerT = 512;    // a block a sequence
-constexpr int kVerClT = 288;  // a cluster a sequence, threads per block
+constexpr int kVerClT = 256;  // a cluster a sequence, threads per block
 
 struct BestTok {
   float s;
@@ -243,7 +243,7 @@ __device__ __forceinline__ void best_chunk(BestTok& best, const float (&s)[W], i
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kVerClT, 3) verify_cluster_kernel(const VerifyParams p,
+__global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const VerifyParams p,
                                                                    const VerifyGeo g) {
   constexpr int E = DType<DT>::E, W = DType<DT>::V;
   extern __shared__ __align__(128) unsigned char smem[];

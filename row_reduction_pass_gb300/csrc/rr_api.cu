@@ -1383,7 +1383,7 @@ rr_status distill_launch(rr::DistillParams p, rr_dtype dt, cudaStream_t stream) 
 rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
   const rr::VerifyKernels vk = rr::verify_kernels(dt);
   const int64_t E = dt == RR_BF16 ? 2 : 4;
-  int K = 0, threads = 256;
+  int K = 0, threads = 224;
   rr::VerifyGeo g{};
   size_t smem = 0;
   {
