@@ -238,11 +238,10 @@ __device__ __forceinline__ int tree_scan(int v, int* scratch, int* total) {
   return before + x - v;
 }
 
-// Row r of a tile in the workspace: one piece of `slot`, 0 its first, 1 its last.
-__device__ __forceinline__ int64_t tree_part(int slot, int part, int rows, int r) {
-  return ((int64_t)slot * 2 + part) * rows + r;
-}
-
+// The workspace: two pieces a pipeline (its run's first and last), a piece being
+// [D / 4][rows] 16-byte chunks of the output (so that the rows of a warp write, and
+// the joining threads read, whole lines), and behind them the pieces' [rows]
+// (maximum, sum).
 __device__ __forceinline__ bool odd_bf16x2(uint32_t w) {  // an infinity or NaN in the pair
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
@@ -503,7 +502,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const float sc = p.scale_log2;
     const int slot = slot0 + w;
     const int all_rows = p.nodes * g.G, ws_rows = min(all_rows, kTM);
-    float* ws_o = p.ws;
+    uint4* ws_o = reinterpret_cast<uint4*>(p.ws);
     float2* ws_ml = reinterpret_cast<float2*>(p.ws + (int64_t)g.max_slots * 2 * ws_rows * D);
     uint32_t* mask = masks + row * kMaskStride;
     TreeSeg s = first;
@@ -522,15 +521,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       bool present = live;
       float m = -INFINITY, l = 0.f;
       if (s.tiles > 0) {
-        // Q: this thread's row into its place of the swizzled tile
-        // (zeros for the rows of a live warp beyond the last)
+        // Q into the swizzled tile, a warp its 32 rows, whole rows at a time (a row per
+        // lane would touch 32 lines an instruction); zeros for the rows of a live warp
+        // beyond the last
         if (wlive) {
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + out * D * 2);
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c)
-            *reinterpret_cast<uint4*>(sq + (c >> 3) * C::kQBox + row * 128 +
-                                      (((c & 7) ^ (row & 7)) << 4)) =
-                live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 4
+          for (int i = 0; i < D / 8; ++i) {
+            const int at = i * 32 + lane, r = at / (D / 8), c = at % (D / 8);
+            const int64_t from = __shfl_sync(0xffffffffu, out, r);
+            const bool on = __shfl_sync(0xffffffffu, (int)live, r);
+            const int qr = 32 * (warp & 3) + r;
+            *reinterpret_cast<uint4*>(sq + (c >> 3) * C::kQBox + qr * 128 +
+                                      (((c & 7) ^ (qr & 7)) << 4)) =
+                on ? __ldg(reinterpret_cast<const uint4*>(p.q + from * D * 2) + c)
+                   : make_uint4(0u, 0u, 0u, 0u);
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive(bar_q);
@@ -731,7 +736,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         const bool whole = !cut0 && !cut1;
         const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-        const int64_t at = whole ? 0 : tree_part(slot, piece > 1, ws_rows, live ? row : 0);
+        const int part = 2 * slot + (piece > 1);  // the run's first piece, or its last
         // O in 32 columns at a time (few registers: the loop above keeps the rest)
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -754,21 +759,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                   pack_bf16(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv),
                   pack_bf16(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv));
           } else if (live) {
-            uint4* dst = reinterpret_cast<uint4*>(ws_o + at * D + 32 * c);
+            uint4* dst = ws_o + ((int64_t)part * (D / 4) + 8 * c) * ws_rows + row;
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              dst[i >> 2] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              dst[(i >> 2) * ws_rows] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
         tc_fence_before();
         mbar_arrive(bar_ofree);
         if (live && whole && p.lse != nullptr)
           p.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        if (live && !whole) ws_ml[at] = make_float2(m, l);
+        if (live && !whole) ws_ml[(int64_t)part * ws_rows + row] = make_float2(m, l);
       } else if (live) {
         // nothing of these tiles is visible to the row tile
         if (cut0 || cut1)
-          ws_ml[tree_part(slot, piece > 1, ws_rows, row)] = make_float2(-INFINITY, 0.f);
+          ws_ml[(int64_t)(2 * slot + (piece > 1)) * ws_rows + row] = make_float2(-INFINITY, 0.f);
       }
     }
   }
@@ -781,13 +786,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 }
 
 // Joins the pieces of items cut by runs, and writes the rows of sequences that
-// have no tile at all.  One warp per row: a block takes 8 rows of one item.
+// have no tile at all.  A thread takes one 16-byte chunk of one row, over all
+// pieces.
 constexpr int kJoinT = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, const TreeGeo g) {
-  constexpr int BN = TreePL<D>::BN, V = D / 32;
+  constexpr int BN = TreePL<D>::BN, U = 8;  // pieces loaded at once
   __shared__ int scratch[16], s_before;
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x;
   // block (x, z): item x of all, pipeline z of its group
   const int b = (int)blockIdx.x / g.KM, hm = (int)blockIdx.x - b * g.KM;
   // tiles before this sequence, and of all
@@ -800,83 +806,64 @@ __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, c
     for (int i = b0; i < b; ++i) at += tree_tiles<BN>(p, g, tree_context(p, g, i)) * g.KM;
     s_before = at;
   }
+  const int all_rows = p.nodes * g.G, ws_rows = min(all_rows, kTM);
+  const int flat = (int)blockIdx.y * kJoinT + tid;  // of the piece's chunks
+  const int chunk = flat / ws_rows, row = flat - chunk * ws_rows;
+  const int sub = (int)blockIdx.z, mb = g.MT / g.RB, hb = hm / mb;
+  const int h = hb * g.HB + sub / g.RB, mt = (hm - hb * mb) * g.RB + sub % g.RB;
+  const int R = mt * kTM + row, node = R / g.G;
+  const int64_t out = ((int64_t)b * p.nodes + node) * p.heads + h * g.G + R - node * g.G;
+  const int T = tree_tiles<BN>(p, g, tree_context(p, g, b));
+  const int share = tree_share(total, g.groups, g.min_tiles);
   __syncthreads();
+  const int start = s_before + hm * T;
+  const int s0 = start / share, s1 = (start + T - 1) / share;
   // Launched while the pieces are still being computed: every block waits for
   // them here, also one without work, so that this grid ends after that one.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int T = tree_tiles<BN>(p, g, tree_context(p, g, b));
-  const int share = tree_share(total, g.groups, g.min_tiles);
-  const int start = s_before + hm * T;
-  const int s0 = start / share, s1 = (start + T - 1) / share;
   if (T > 0 && s0 == s1) return;  // finished by its run
-  const int all_rows = p.nodes * g.G, ws_rows = min(all_rows, kTM);
-  const int sub = (int)blockIdx.z, mb = g.MT / g.RB, hb = hm / mb;
-  const int h = hb * g.HB + sub / g.RB, mt = (hm - hb * mb) * g.RB + sub % g.RB;
-  const int row = (int)blockIdx.y * (kJoinT / 32) + (tid >> 5), R = mt * kTM + row;
-  if (row >= kTM || R >= all_rows) return;
-  const int64_t out = ((int64_t)b * p.nodes + R / g.G) * p.heads + h * g.G + R % g.G;
-  const float* ws_o = p.ws;
+  if (chunk >= D / 4 || R >= all_rows) return;
+  const float4* ws_o = reinterpret_cast<const float4*>(p.ws);
   const float2* ws_ml =
       reinterpret_cast<const float2*>(p.ws + (int64_t)g.max_slots * 2 * ws_rows * D);
-  // the item's piece in a run is its last if it begins inside the run
-  auto place = [&](int s) { 
-    return tree_part(s * g.side + sub, s * share < start ? 1 : 0, ws_rows, row);
-  };
-  // lanes take the pieces' maxima and sums, 32 pieces at a time; their outputs
-  // then come four loads at once, a piece in which the row sees nothing (it has
-  // no output) with weight 0
+  // the item's piece in a run is the run's last if it begins inside the run
+  auto part = [&](int s) { return 2 * (s * g.side + sub) + (s * share < start ? 1 : 0); };
   const int n = T > 0 ? s1 - s0 + 1 : 0;
-  float M = -INFINITY, L = 0.f, o[V];
+  float M = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += U) {
+    float2 ml[U];
+    float4 x[U];
+    float mx = M;
 #pragma unroll
-  for (int i = 0; i < V; ++i) o[i] = 0.f;
-  for (int base = 0; base < n; base += 32) {
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (base + lane < n) ml = ws_ml[place(s0 + base + lane)];
-    float mx = ml.x;
+    for (int i = 0; i < U; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + i < n) {
+        const int64_t pt = part(s0 + i0 + i);
+        ml[i] = ws_ml[pt * ws_rows + row];
+        x[i] = ws_o[(pt * (D / 4) + chunk) * ws_rows + row];
+      }
+    }
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    mx = fmaxf(mx, M);
+    for (int i = 0; i < U; ++i) mx = fmaxf(mx, ml[i].x);
     const float keep = M == mx ? 1.f : ex2(M - mx);
     M = mx;
-    const float a = ml.y == 0.f ? 0.f : ml.x == M ? 1.f : ex2(ml.x - M);
-    float sum = ml.y * a;
+    L *= keep;
+    o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    L = L * keep + sum;
-#pragma unroll
-    for (int c = 0; c < V; ++c) o[c] *= keep;
-    const uint32_t full = __ballot_sync(0xffffffffu, ml.y != 0.f);
-    const int m = min(32, n - base);
-    for (int i = 0; i < m; i += 4) {
-      float f[4][V], wt[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        wt[q] = __shfl_sync(0xffffffffu, a, i + q);
-#pragma unroll
-        for (int c = 0; c < V; ++c) f[q][c] = 0.f;
-        if ((full >> (i + q)) & 1) {
-          const float* src = ws_o + place(s0 + base + i + q) * D + lane * V;
-          if constexpr (V == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(src);
-            f[q][0] = x.x, f[q][1] = x.y, f[q][2] = x.z, f[q][3] = x.w;
-          } else {
-            const float2 x = *reinterpret_cast<const float2*>(src);
-            f[q][0] = x.x, f[q][1] = x.y;
-          }
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int c = 0; c < V; ++c) o[c] = fmaf(f[q][c], wt[q], o[c]);
+    for (int i = 0; i < U; ++i) {
+      if (ml[i].y == 0.f) continue;  // a piece in which the row sees nothing: no output there
+      const float a = ml[i].x == M ? 1.f : ex2(ml[i].x - M);
+      L = fmaf(ml[i].y, a, L);
+      o = make_float4(fmaf(x[i].x, a, o.x), fmaf(x[i].y, a, o.y), fmaf(x[i].z, a, o.z),
+                      fmaf(x[i].w, a, o.w));
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  char* dst = p.o + out * D * 2 + lane * V * 2;
-#pragma unroll
-  for (int c = 0; c < V; c += 2)
-    *reinterpret_cast<uint32_t*>(dst + 2 * c) = pack_bf16(o[c] * inv, o[c + 1] * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[out] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+  *reinterpret_cast<uint2*>(p.o + (out * D + 4 * chunk) * 2) =
+      make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  if (chunk == 0 && p.lse != nullptr) p.lse[out] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 }  // namespace
@@ -941,7 +928,8 @@ const char* tree_tc_launch(const TreeParams& p, int d, int sms, cudaStream_t str
     return "launch failed";
   void* jargs[] = {&pc, &g};
   const int64_t items = p.batch * g.KM;
-  const unsigned groups = (unsigned)((std::min<int64_t>(rows, kTM) + kJoinT / 32 - 1) / (kJoinT / 32));
+  const unsigned groups =
+      (unsigned)((std::min<int64_t>(rows, kTM) * (d / 4) + kJoinT - 1) / kJoinT);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3((unsigned)items, groups, (unsigned)g.side);
