@@ -339,18 +339,19 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     const float M = warp_max(m);
     const float a = m == -INFINITY ? 0.f : ex2((m - M) * p.c);
     d = warp_sum(d * a);
-    if (lane == 0) {
-      float4* sl = slots + (j & 3) * nslot + rank * nwp + w;
-      const float4 v = make_float4(M, d, w < nw ? d : 0.f, 0.f);
-      if constexpr (CL) {
-        for (int t = 0; t < K; ++t) {
-          st_cluster_f32x4(map_to_rank(sl, t), v.x, v.y, v.z, v.w);
-          mbar_arrive_cluster(map_to_rank(&mrg[j & 3], t));
-        }
-      } else {
-        *sl = v;
-        mbar_arrive(&mrg[j & 3]);
+    float4* sl = slots + (j & 3) * nslot + rank * nwp + w;
+    const float4 v = make_float4(M, d, w < nw ? d : 0.f, 0.f);
+    if constexpr (CL) {
+      // lane t writes to rank t (one lane after the other waited for each rank's
+      // store in turn: 5500 cycles a row for four ranks)
+      if (lane < K) {
+        st_cluster_f32x4(map_to_rank(sl, lane), v.x, v.y, v.z, v.w);
+        mbar_arrive_cluster(map_to_rank(&mrg[j & 3], lane));
       }
+      __syncwarp();
+    } else if (lane == 0) {
+      *sl = v;
+      mbar_arrive(&mrg[j & 3]);
     }
   };
   // the teacher's mass outside the list, and the weight of the student's softmax
