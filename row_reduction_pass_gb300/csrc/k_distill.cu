@@ -191,17 +191,18 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
 // One block (or a cluster of K blocks, each with a slice of S 16-byte chunks)
 // per row at a time, grid-stride over the rows; x and y share their address
 // modulo 16, so a chunk of one is a chunk of the other whatever the row's
-// alignment.  The block's last two warps, the list warps, are set apart from the
-// rest, the row warps:
-//   list warp, per row j (of its parity): waits until the row warps have
-//     published row j's statistics, prepares row j + 2's list, writes row j's
-//     loss, and, once row j + 1 is published (every chunk of row j then stored),
-//     stores row j's listed columns.
+// alignment.  The block's last three warps, a merge warp and two list warps, are
+// set apart from the rest, the row warps:
 //   row warp, per row j: waits for the row and its list, takes its chunks into
-//     registers, publishes the warp's maximum and sums to every block of the
-//     cluster, merges all the warps' when they are there (thread 0 then refills
-//     the row's buffer with row j + 2, one bulk copy), stores its chunks of
-//     dlogits.
+//     registers, publishes the warp's maximum and sum to every block of the
+//     cluster, waits for the merged statistics, stores its chunks of dlogits.
+//   merge warp, per row j: waits until every warp has published row j, refills the
+//     row's buffer with row j + 2 (one bulk copy), merges the partials and hands
+//     the row's statistics to the other warps (every warp merging for itself
+//     took 1000 cycles of a row's 10300, 2200 in a cluster of three).
+//   list warp, per row j (of its parity): waits for row j's statistics, prepares
+//     row j + 2's list, writes row j's loss, and, once row j + 1 is published (every
+//     chunk of row j then stored), stores row j's listed columns.
 // So a block meets once a row (an mbarrier of the published statistics), the
 // two latencies of a list (its entries, then the student's logits there) are a
 // row ahead of their use, and two rows are in flight while one is worked on.
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
                                                                 const DistillGeo g) {
   constexpr int E = DType<DT>::E, W = DType<DT>::V, NQ = kDistNQ;
   extern __shared__ __align__(128) unsigned char smem[];
-  const int nw = (int)(blockDim.x >> 5) - 2;  // row warps
+  const int nw = (int)(blockDim.x >> 5) - 3;  // row warps
   const int G = nw * 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int K = 1, rank = 0;
@@ -275,16 +276,15 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);  // [2] the row has landed
   uint64_t* mrg = full + 2;                            // [4] statistics published
   uint64_t* ready = full + 6;                          // [2] the list is prepared
-  DistHead* heads = reinterpret_cast<DistHead*>(smem + 64);      // [4]
-  uint4* edge = reinterpret_cast<uint4*>(smem + 128);            // [2] a row's ragged chunks
-  float4* slots = reinterpret_cast<float4*>(smem + 160);         // [4][nslot]
+  uint64_t* done = full + 8;                           // [4] statistics merged
+  DistHead* heads = reinterpret_cast<DistHead*>(smem + 96);      // [4]
+  uint4* edge = reinterpret_cast<uint4*>(smem + 160);            // [2] a row's ragged chunks
+  float4* final_ = reinterpret_cast<float4*>(smem + 192);        // [4] (M, Z, Zt) of a row
+  float4* slots = reinterpret_cast<float4*>(smem + 256);         // [4][nslot]
   DistEntry* lists = reinterpret_cast<DistEntry*>(smem + g.list_off);  // [4][k]
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + g.bits_off);     // [2][words]
-  // With a tail the list warps publish too (the listed columns' part of Z).  In a
-  // cluster they always do: a slot is written again four rows later, and every
-  // warp that reads it must have said, by publishing a later row, that it has.
-  constexpr bool kListPublishes = TAIL || CL;
-  const int nwp = nw + (kListPublishes ? 1 : 0), nslot = K * nwp;
+  // with a tail the list warps publish too (the listed columns' part of Z)
+  const int nwp = nw + (TAIL ? 1 : 0), nslot = K * nwp;
   const int64_t rowb = p.cols * E;
   const int k0 = rank * g.S;
   auto row_addr = [&](int64_t r) { return reinterpret_cast<uintptr_t>(p.x) + r * rowb; };
@@ -300,7 +300,10 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       mbar_init(&full[i], 1);
       mbar_init(&ready[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&mrg[i], nslot);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&mrg[i], nslot);
+      mbar_init(&done[i], 1);
+    }
     fence_mbar_init();
   }
   for (int i = tid; i < 2 * g.words; i += blockDim.x) bits[i] = 0;
@@ -308,31 +311,12 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
   else __syncthreads();
 
   bool dead = false;  // a wait gave up: later waits are skipped (the kernel still ends)
-  // Row j published by every warp.  (No list warp runs so late that the barrier's
-  // next phase, row j + 4, ends before it looks: that row waits for its list.)
-  auto published = [&](int64_t j) {
-    const uint32_t ph = (uint32_t)((j >> 2) & 1);
-    if (!dead) {
-      if constexpr (CL) dead = !mbar_wait_bounded_cluster(&mrg[j & 3], ph, p.err);
-      else dead = !mbar_wait_bounded(&mrg[j & 3], ph, p.err);
-    }
-  };
-  // row j's statistics, the same bits in every warp of every rank
-  auto merged = [&](int64_t j, float& M, float& d, float& dt) {
-    published(j);
-    const float4* sl = slots + (j & 3) * nslot;
-    M = -INFINITY;
-    for (int i = lane; i < nslot; i += 32) M = fmaxf(M, sl[i].x);
-    M = warp_max(M);
-    d = dt = 0.f;
-    for (int i = lane; i < nslot; i += 32) {
-      const float4 t = sl[i];
-      const float a = t.x == -INFINITY ? 0.f : ex2((t.x - M) * p.c);
-      d += t.y * a;
-      if (TAIL) dt += t.z * a;
-    }
-    d = warp_sum(d);
-    if (TAIL) dt = warp_sum(dt);
+  // Waits until row j's statistics are merged (every warp of the cluster has then
+  // published it).  No warp runs so late that the barrier's next phase, row j + 4,
+  // ends before it looks: that row waits for this block's row warps and lists.
+  auto merged = [&](int64_t j) {
+    if (!dead) dead = !mbar_wait_bounded(&done[j & 3], (uint32_t)((j >> 2) & 1), p.err);
+    return final_[j & 3];
   };
   // warp w's partial of row j, to the slots of every rank
   auto publish = [&](int64_t j, int w, float m, float d) {
@@ -374,7 +358,46 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
               &full[j & 1], policy_evict_first());
   };
 
-  if (warp >= nw) {
+  if (warp == nw) {
+    // ------------------------------------------------------ the merge warp
+    // (A slot is written again four rows later by warps that wait for the rows
+    // between, which wait for this block's row warps, which wait for this warp.)
+    if (lane == 0) {
+      load_row(0);
+      load_row(1);
+    }
+    for (int64_t j = 0; row_of(j) < p.rows; ++j) {
+      const uint32_t ph = (uint32_t)((j >> 2) & 1);
+      if (!dead) {
+        if constexpr (CL) dead = !mbar_wait_bounded_cluster(&mrg[j & 3], ph, p.err);
+        else dead = !mbar_wait_bounded(&mrg[j & 3], ph, p.err);
+      }
+      if (lane == 0) load_row(j + 2);  // every row warp has taken its chunks of row j
+      const float4* sl = slots + (j & 3) * nslot;
+      float M = -INFINITY, d = 0.f, dt = 0.f;
+      for (int i = lane; i < nslot; i += 32) M = fmaxf(M, sl[i].x);
+      M = warp_max(M);
+      for (int i = lane; i < nslot; i += 32) {
+        const float4 t = sl[i];
+        const float a = t.x == -INFINITY ? 0.f : ex2((t.x - M) * p.c);
+        d += t.y * a;
+        if (TAIL) dt += t.z * a;
+      }
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) {
+        d += __shfl_xor_sync(0xffffffffu, d, off);
+        if (TAIL) dt += __shfl_xor_sync(0xffffffffu, dt, off);
+      }
+      if (lane == 0) {
+        final_[j & 3] = make_float4(M, d, dt, 0.f);
+        mbar_arrive(&done[j & 3]);
+      }
+      __syncwarp();
+    }
+    if (dead && lane == 0)  // copies of this block still in flight end before it does
+      for (int i = 0; i < 2; ++i) mbar_wait_bounded(&full[i], 0, p.err);
+    __syncthreads();
+  } else if (warp > nw) {
     // ------------------------------------------------------ the list warps
     // the place of column c in the slice (row start h bytes into its chunk), or -1
     auto place = [&](int c, int h) {
@@ -467,15 +490,13 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     auto publish_list = [&](int64_t j) {
       const DistEntry* li = lists + (j & 3) * k;
       float m = -INFINITY, d = 0.f;
-      if (TAIL) {
+      for (int i = lane; i < k; i += 32)
+        if (li[i].place >= 0 && li[i].place < kDistAgain) m = fmaxf(m, li[i].x);
+      if (m != -INFINITY) {
+        const float mL = m * p.c;
         for (int i = lane; i < k; i += 32)
-          if (li[i].place >= 0 && li[i].place < kDistAgain) m = fmaxf(m, li[i].x);
-        if (m != -INFINITY) {
-          const float mL = m * p.c;
-          for (int i = lane; i < k; i += 32)
-            if (li[i].place >= 0 && li[i].place < kDistAgain) d += ex2(fmaf(li[i].x, p.c, -mL));
-          d *= ex2(-fmaf(m, p.c, -mL));
-        }
+          if (li[i].place >= 0 && li[i].place < kDistAgain) d += ex2(fmaf(li[i].x, p.c, -mL));
+        d *= ex2(-fmaf(m, p.c, -mL));
       }
       publish(j, nw, m, d);
     };
@@ -531,7 +552,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       }
       if (lane == 0) p.loss[row_of(j)] = l;
     };
-    int64_t j = warp - nw;
+    int64_t j = warp - nw - 1;
     load_entries(j, 0);
     load_logits(j);
     prepare(j);
@@ -540,15 +561,18 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     bool open = false;  // the block's last row: listed columns still to be stored
     for (; row_of(j) < p.rows; j += 2) {
       load_logits(j + 2);
-      if (kListPublishes) publish_list(j);
-      merged(j, M, d, dt);
+      if (TAIL) publish_list(j);
+      const float4 f = merged(j);
+      M = f.x;
+      d = f.y;
+      dt = f.z;
       clear_bits(j);
       prepare(j + 2);
       load_entries(j + 4, 0);
       if (rank == 0) write_loss(j, M, d, dt);
       open = row_of(j + 1) >= p.rows;
       if (!open) {
-        published(j + 1);
+        merged(j + 1);
         finish(j, M, d, dt);
       }
     }
@@ -556,10 +580,6 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     if (open) finish(j - 2, M, d, dt);
   } else {
     // ------------------------------------------------------- the row warps
-    if (tid == 0) {
-      load_row(0);
-      load_row(1);
-    }
     for (int64_t j = 0; row_of(j) < p.rows; ++j) {
       const int64_t r = row_of(j);
       const uintptr_t a = row_addr(r);
@@ -587,17 +607,33 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       }
       if (!dead) dead = !mbar_wait_bounded(&ready[j & 1], ph, p.err);
       uint4 v[NQ];
-      float m = -INFINITY;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         if (q >= nq) break;
         v[q] = buf[tid + q * G];
-        if (TAIL) {  // listed lanes become -inf: the list warp counts them
+      }
+      if (TAIL) {  // listed lanes become -inf: the list warp counts them
+        uint32_t listed[2] = {0u, 0u};  // a byte a chunk
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          if (q >= nq) break;
           const int c = tid + q * G;
           uint32_t b = bm[W == 8 ? c : c >> 1];
           if (W == 4) b = (c & 1) ? b >> 4 : b & 15u;
-          if (b != 0) v[q] = dist_take_out<DT>(v[q], b);
+          listed[q >> 2] |= b << (8 * (q & 3));
         }
+        if ((listed[0] | listed[1]) != 0) {
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            const uint32_t b = (listed[q >> 2] >> (8 * (q & 3))) & 255u;
+            if (b != 0) v[q] = dist_take_out<DT>(v[q], b);
+          }
+        }
+      }
+      float m = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        if (q >= nq) break;
         if constexpr (DT == kBF16) {
           const uint32_t w = bf16x2_max(bf16x2_max(v[q].x, v[q].y), bf16x2_max(v[q].z, v[q].w));
           m = fmaxf(m, fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
@@ -624,9 +660,9 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         d = (d + d1) * ex2(-fmaf(m, p.c, -mL));
       }
       publish(j, warp, m, d);
-      float M, dt;
-      merged(j, M, d, dt);
-      if (tid == 0) load_row(j + 2);  // every row warp has taken its chunks of row j
+      const float4 fin = merged(j);
+      const float M = fin.x, dt = fin.z;
+      d = fin.y;
       if (p.y == nullptr) continue;
       char* y = p.y + r * rowb - h + (int64_t)k0 * 16;
       const DistHead hd = heads[j & 3];
@@ -668,8 +704,6 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         }
       }
     }
-    if (dead && tid == 0)  // copies of this block still in flight end before it does
-      for (int i = 0; i < 2; ++i) mbar_wait_bounded(&full[i], 0, p.err);
     __syncthreads();  // every chunk stored: the last row's listed columns may be
   }
   if constexpr (CL) cluster_sync();  // no peer still writes this block's slots
