@@ -122,6 +122,20 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// The wait for this thread's tcgen05.ld, as an operation on the registers loaded, so
+// that no use of them can be moved before it.
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+
 constexpr int kTM = 128;  // rows of a tile: MMA M, TMEM lanes
 // Two softmax warpgroups, and for each pipeline w a warp that issues S (8 + w), one
 // for O += P V (10 + w), one that loads K (12 + w) and one that loads V (14 + w): a
@@ -565,7 +579,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const bool tail = key0 + BN > min(s.ctx, s.vis);
           if (tail) {
             // V at positions nobody may see, and non-finite values at nodes: 0
+            // (This barrier is not waited on at every tile, and the products may be two
+            // tiles behind: V(t - 2) may not even have landed, and the wait for V(t)'s
+            // phase would then be satisfied by the phase before V(t - 2)'s.  So first
+            // the product that reads V(t - 2).)
             tail_seen = true;
+            if (t >= 2) wait(&bar_vempty[t & 1], (uint32_t)(((t >> 1) - 1) & 1));
             wait(&bar_vfull[t & 1], (uint32_t)((t >> 1) & 1));
             const int vr = row % BN, pos = key0 + vr;
             if (pos >= s.ctx || pos >= s.vis) {
@@ -599,7 +618,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             auto read_half = [&](int hf) {
 #pragma unroll
               for (int c = 0; c < 2; ++c) tmem_ld32_nowait(tS + 64 * hf + 32 * c, v[c]);
-              tmem_ld_wait();
+              tmem_ld_done(v[0]);
+              tmem_ld_done(v[1]);
               if (!tail && !holes) return;
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
@@ -704,7 +724,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld32_nowait(tO + 32 * c, o);
-                tmem_ld_wait();
+                tmem_ld_done(o);
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
                   float a0, a1;
@@ -743,7 +763,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           if (!wlive) break;
           uint32_t o[32];
           tmem_ld32_nowait(tO + 32 * c, o);
-          tmem_ld_wait();
+          tmem_ld_done(o);
           if (l == 0.f) {  // (nothing seen: the accumulator holds nothing of this row's)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0u;

@@ -199,6 +199,45 @@ def test_tree_attention_split_sequences(D, batch, ctx):
                             True))
 
 
+@pytest.mark.parametrize("D,ps", [(128, 64), (64, 128)])
+def test_tree_attention_many_sequences_a_block(D, ps):
+    """Enough cache that memory is the bound, and sequences short enough that a
+    block works through several of them, each with the rest of a page behind its end:
+    six runs give the same bits and the float64 attention."""
+    B, H, KV = 64, 32, 8
+    g = torch.Generator("cuda").manual_seed(4)
+    lens = [500 + int(3500 * ((b * 0.618034) % 1.0)) for b in range(B)]
+    need = [(L + 1 + ps - 1) // ps for L in lens]
+    table = torch.zeros(B, max(need), dtype=torch.int32, device="cuda")
+    order = torch.randperm(sum(need), generator=g, device="cuda").int()
+    at = 0
+    for b in range(B):
+        table[b, :need[b]] = order[at:at + need[b]]
+        at += need[b]
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    q, kc, vc = rnd(B, 1, H, D), rnd(at, ps, KV, D), rnd(at, ps, KV, D)
+    ctx = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    runs = []
+    for _ in range(6):
+        o, l = torch.full_like(q, 7.0), torch.empty(B, 1, H, device="cuda")
+        rr.rr_attention_tree_fwd(q, kc, vc, table, ctx, o, lse=l)
+        runs.append((o, l))
+    torch.cuda.synchronize()
+    assert rr.rr_read_device_error(0) == 0
+    for o, l in runs[1:]:
+        assert torch.equal(o, runs[0][0]) and torch.equal(l, runs[0][1])
+    for b in range(B):
+        pages = table[b, :need[b]].long()
+        k = kc[pages].reshape(-1, KV, D)[:lens[b] + 1].double().repeat_interleave(H // KV, 1)
+        v = vc[pages].reshape(-1, KV, D)[:lens[b] + 1].double().repeat_interleave(H // KV, 1)
+        s = torch.einsum("hd,lhd->hl", q[b, 0].double(), k) / D ** 0.5
+        p = torch.softmax(s, 1)
+        compare("lse", host(runs[0][1][b, 0]), torch.logsumexp(s, 1).cpu().numpy(), 1e-5, 1e-5)
+        compare("o", host(runs[0][0][b, 0]), torch.einsum("hl,lhd->hd", p, v).cpu().numpy(), 0.0,
+                1e-6, scale=torch.einsum("hl,lhd->hd", p, v.abs()).cpu().numpy(),
+                scale_rtol=2.0 ** -7)
+
+
 def test_tree_attention_long_chain():
     """A prompt chunk: 600 new tokens, several tiles of query rows."""
     check_tree(*tree_inputs(2, 600, 2, 1, 64, [0, 77], 16, 3, False))
