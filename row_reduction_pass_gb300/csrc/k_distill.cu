@@ -213,16 +213,22 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
 // warps which lanes of a chunk to leave out of Zt (a byte or half a byte a
 // chunk, nearly always 0), and the list warp whether a column came twice.
 struct __align__(16) DistHead {
-  float g;     // upstream gradient times T
-  float st;    // sum of t_k
-  int live;    // some entry has weight
-  int dup;     // a column of this slice may be listed twice
+  float g;        // upstream gradient times T
+  float tn;       // t_k = tn * (the entries' t)
+  float st;       // sum of t_k (with a tail)
+  int live;       // some entry has weight
+  int dup;        // a column of this slice may be listed twice
+  float m, d;     // maximum of the slice's listed columns, sum of exp((x - m) / T)
+  float ref;      // the logit that a0 is relative to
+  double a0;      // sum t_k (ln t_k - (x - ref) / T)
 };
 struct __align__(16) DistEntry {
-  float t, lt, x;  // the teacher's weight (0: absent) and its logarithm, the student's logit
-  int place;       // element place in this block's slice, -1 none; + kDistAgain if listed before
+  float t, x;  // the teacher's weight (before tn; 0: absent), the student's logit
+  int place;   // element place in this block's slice, -1 none; + kDistAgain if listed before
+  int pad;
 };
 constexpr int kDistAgain = 1 << 30;
+constexpr int kDistOffSlots = 384;  // shared memory: statistics' slots on
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -278,9 +284,9 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
   uint64_t* ready = full + 6;                          // [2] the list is prepared
   uint64_t* done = full + 8;                           // [4] statistics merged
   DistHead* heads = reinterpret_cast<DistHead*>(smem + 96);      // [4]
-  uint4* edge = reinterpret_cast<uint4*>(smem + 160);            // [2] a row's ragged chunks
-  float4* final_ = reinterpret_cast<float4*>(smem + 192);        // [4] (M, Z, Zt) of a row
-  float4* slots = reinterpret_cast<float4*>(smem + 256);         // [4][nslot]
+  uint4* edge = reinterpret_cast<uint4*>(smem + 288);            // [2] a row's ragged chunks
+  float4* final_ = reinterpret_cast<float4*>(smem + 320);        // [4] (M, Z, Zt) of a row
+  float4* slots = reinterpret_cast<float4*>(smem + kDistOffSlots);  // [4][nslot]
   DistEntry* lists = reinterpret_cast<DistEntry*>(smem + g.list_off);  // [4][k]
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + g.bits_off);     // [2][words]
   // with a tail the list warps publish too (the listed columns' part of Z)
@@ -399,11 +405,6 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     __syncthreads();
   } else if (warp > nw) {
     // ------------------------------------------------------ the list warps
-    // the place of column c in the slice (row start h bytes into its chunk), or -1
-    auto place = [&](int c, int h) {
-      const int64_t e = (int64_t)c + h / E - (int64_t)k0 * W;
-      return e >= 0 && e < (int64_t)g.S * W ? (int)e : -1;
-    };
     // a / T, 1 / T in two parts
     auto over_t = [&](float a) {
       return isfinite(a) ? fmaf(a, p.inv_t, a * p.inv_t_lo) : a;
@@ -414,47 +415,50 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     int ci[4];
     float cv[4], cx[4];
     auto load_entries = [&](int64_t j, int base) {
-      const int64_t at = row_of(j) * k;
+      const int64_t at = row_of(j) * k + base + lane;
       const bool any = row_of(j) < p.rows;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int i = base + lane + 32 * q;
-        ci[q] = any && i < k ? __ldg(p.index + at + i) : -1;
-        cv[q] = any && i < k ? __ldg(p.value + at + i) : 0.f;
+        ci[q] = -1;
+        if (any && base + lane + 32 * q < k) {
+          ci[q] = __ldg(p.index + at + 32 * q);
+          cv[q] = __ldg(p.value + at + 32 * q);
+        }
       }
     };
     auto load_logits = [&](int64_t j) {
       const char* x = p.x + row_of(j) * rowb;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        cx[q] = ci[q] >= 0 && ci[q] < p.cols ? ld_elem<DT>(x + (int64_t)ci[q] * E) : 0.f;
+        if (ci[q] >= 0 && ci[q] < p.cols) cx[q] = ld_elem<DT>(x + (int64_t)ci[q] * E);
     };
+    // What a list says before the row's statistics are known: the weights t (with
+    // no tail relative to the greatest, tn brings them to sum 1), its part of the
+    // loss relative to a logit of its own, the listed columns' part of Z.  Every
+    // entry is touched once, in registers.
     auto prepare = [&](int64_t j) {
       const int64_t r = row_of(j);
       if (r >= p.rows) return;
       const int h = (int)(row_addr(r) & 15);
+      const int first = h / E - k0 * W;  // place of column 0
       DistEntry* li = lists + (j & 3) * k;
       uint32_t* bm = bits + (j & 1) * g.words;
-      float vm = -INFINITY;
-      int any = 0, dup = 0;
+      float vm = -INFINITY, ref = -INFINITY;
+      int any = 0;
+      // maxima over the list (a list of more than 128: a pass of its own)
       for (int base = 0;;) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int i = base + lane + 32 * q;
-          if (i >= k) break;
-          const bool beyond = ci[q] >= p.cols;
-          if (beyond && rank == 0 && p.bad != nullptr) atomicAdd(p.bad, 1);
-          const bool there = ci[q] >= 0 && !beyond;
-          int e = there ? place(ci[q], h) : -1;
-          if (e >= 0 && ((atomicOr(&bm[e >> 5], 1u << (e & 31)) >> (e & 31)) & 1)) {
-            dup = 1;
-            e |= kDistAgain;
+          if (base + 32 * q >= k) break;
+          if (ci[q] < 0) continue;
+          if (ci[q] >= p.cols) {
+            if (rank == 0 && p.bad != nullptr) atomicAdd(p.bad, 1);
+            ci[q] = -1;
+            continue;
           }
-          li[i] = DistEntry{0.f, there ? cv[q] : -INFINITY, cx[q], e};
-          if (there) {
-            any = 1;
-            vm = fmaxf(vm, cv[q]);
-          }
+          any = 1;
+          vm = fmaxf(vm, cv[q]);
+          ref = fmaxf(ref, cx[q]);
         }
         base += 128;
         if (base >= k) break;
@@ -462,43 +466,73 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         load_logits(j);
       }
       any = __any_sync(0xffffffffu, any);
-      vm = warp_max(vm);
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) {
+        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
+        ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, off));
+      }
+      if (ref == -INFINITY) ref = 0.f;
       const bool live = any && (TAIL || vm != -INFINITY);
-      float lnt = 0.f;
-      if (!TAIL) {
-        float z = 0.f;
-        for (int i = lane; i < k && live; i += 32) z += expf(over_t(li[i].lt - vm));
-        lnt = logf(warp_sum(z));
+      const float v0 = TAIL ? 0.f : vm, mL = ref * p.c;
+      float st = 0.f, d = 0.f, a0 = 0.f;
+      int dup = 0;
+      for (int base = 0; base < k; base += 128) {
+        if (k > 128) {
+          load_entries(j, base);
+          load_logits(j);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (base + 32 * q >= k) break;
+          const int i = base + 32 * q + lane;
+          if (i >= k) continue;
+          DistEntry en{0.f, 0.f, -1, 0};
+          if (ci[q] >= 0 && ci[q] < p.cols) {
+            const float lt = TAIL ? cv[q] : over_t(cv[q] - v0);
+            en.x = cx[q];
+            if (live) {
+              en.t = expf(lt);
+              st += en.t;
+              if (!(en.t <= 0.f)) a0 += en.t * (lt - over_t(en.x - ref));
+            }
+            const int e = ci[q] + first;
+            if (e >= 0 && e < g.S * W) {
+              en.place = e;
+              if ((atomicOr(&bm[e >> 5], 1u << (e & 31)) >> (e & 31)) & 1) {
+                dup = 1;
+                en.place |= kDistAgain;
+              } else if (TAIL) {
+                d += ex2(fmaf(en.x, p.c, -mL));
+              }
+            }
+          }
+          li[i] = en;
+        }
       }
-      float st = 0.f;
-      for (int i = lane; i < k && live; i += 32) {
-        const float lt = TAIL ? li[i].lt : over_t(li[i].lt - vm) - lnt;
-        const float t = expf(lt);
-        li[i].lt = lt;
-        li[i].t = t;
-        st += t;
-      }
-      st = warp_sum(st);
       dup = __any_sync(0xffffffffu, dup);
-      if (lane == 0)
-        heads[j & 3] = DistHead{p.temperature * (p.grad != nullptr ? __ldg(p.grad + r) : 1.f), st,
-                                live, dup};
+      double a = (double)a0;
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, off);
+        st += __shfl_xor_sync(0xffffffffu, st, off);
+        if (TAIL) d += __shfl_xor_sync(0xffffffffu, d, off);
+      }
+      if (lane == 0) {
+        DistHead hd;
+        hd.g = p.temperature * (p.grad != nullptr ? __ldg(p.grad + r) : 1.f);
+        hd.tn = TAIL ? 1.f : 1.f / st;
+        hd.st = TAIL ? st : 1.f;
+        hd.live = live;
+        hd.dup = dup;
+        hd.m = d > 0.f ? ref : d == d ? -INFINITY : ref;
+        hd.d = d * ex2(-fmaf(ref, p.c, -mL));
+        hd.ref = ref;
+        // sum t ln t has ln t_k = lt - ln(sum of t) where the list is normalised
+        hd.a0 = TAIL ? a : a / (double)st - (double)logf(st);
+        heads[j & 3] = hd;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ready[j & 1]);
-    };
-    // the maximum and sum of the slice's listed columns (each column once)
-    auto publish_list = [&](int64_t j) {
-      const DistEntry* li = lists + (j & 3) * k;
-      float m = -INFINITY, d = 0.f;
-      for (int i = lane; i < k; i += 32)
-        if (li[i].place >= 0 && li[i].place < kDistAgain) m = fmaxf(m, li[i].x);
-      if (m != -INFINITY) {
-        const float mL = m * p.c;
-        for (int i = lane; i < k; i += 32)
-          if (li[i].place >= 0 && li[i].place < kDistAgain) d += ex2(fmaf(li[i].x, p.c, -mL));
-        d *= ex2(-fmaf(m, p.c, -mL));
-      }
-      publish(j, nw, m, d);
     };
     auto clear_bits = [&](int64_t j) {
       const DistEntry* li = lists + (j & 3) * k;
@@ -516,7 +550,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       const DistEntry* li = lists + (j & 3) * k;
       float mass, tt;
       masses(hd, dt, mass, tt);
-      const float A = hd.g * (mass / d), mL = M * p.c, res = ex2(-fmaf(M, p.c, -mL));
+      const float mL = M * p.c, A = hd.g * (mass / d) * ex2(-fmaf(M, p.c, -mL)), B = hd.g * hd.tn;
       char* y = p.y + r * rowb - h + (int64_t)k0 * 16;
       for (int i = lane; i < k; i += 32) {
         const DistEntry en = li[i];
@@ -524,28 +558,23 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         float t = en.t;
         if (hd.dup)
           for (int n = 0; n < k; ++n) t += li[n].place == (en.place | kDistAgain) ? li[n].t : 0.f;
-        st_elem<DT>(y + (int64_t)en.place * E, ex2(fmaf(en.x, p.c, -mL)) * res * A - hd.g * t);
+        st_elem<DT>(y + en.place * E, fmaf(ex2(fmaf(en.x, p.c, -mL)), A, -B * t));
       }
     };
+    // The loss: a0 plus st times the distance of ref from the row's logarithm of Z,
+    // two numbers of some tens whose sum is small, hence in double (a few
+    // operations a row).
     auto write_loss = [&](int64_t j, float M, float d, float dt) {
       const DistHead hd = heads[j & 3];
       float l = 0.f;
       if (hd.live && M != -INFINITY) {
-        const DistEntry* li = lists + (j & 3) * k;
-        // ln Z in two parts, hi of a few bits: the terms below are then small
-        // differences, and ln Z brings no rounding of its own size
         const int ez = (__float_as_int(d) >> 23) - 127;
-        const float hi = ez * 0.6875f;
-        const float lo = fmaf((float)ez, 0.00564718056f,
-                              logf(__int_as_float(__float_as_int(d) - (ez << 23))));
-        for (int i = lane; i < k; i += 32) {
-          const DistEntry en = li[i];
-          if (!(en.t <= 0.f)) l += en.t * ((en.lt + hi) - over_t(en.x - M));
-        }
-        l = warp_sum(l);
+        const double lnz = (double)ez * 0.69314718055994531 +
+                           (double)logf(__int_as_float(__float_as_int(d) - (ez << 23)));
+        const double inv_t = (double)p.inv_t + (double)p.inv_t_lo;
+        l = (float)(hd.a0 + (double)hd.st * (((double)M - (double)hd.ref) * inv_t + lnz));
         float mass, tt;
         masses(hd, dt, mass, tt);
-        l += lo * (TAIL ? hd.st : 1.f);
         if (tt > 0.f) l += tt * (logf(tt) - logf(dt / d));
         l *= p.temperature * p.temperature;
         if (d != d) l = d;
@@ -561,7 +590,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     bool open = false;  // the block's last row: listed columns still to be stored
     for (; row_of(j) < p.rows; j += 2) {
       load_logits(j + 2);
-      if (TAIL) publish_list(j);
+      if (TAIL) publish(j, nw, lane == 0 ? heads[j & 3].m : -INFINITY, lane == 0 ? heads[j & 3].d : 0.f);
       const float4 f = merged(j);
       M = f.x;
       d = f.y;
@@ -607,33 +636,17 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       }
       if (!dead) dead = !mbar_wait_bounded(&ready[j & 1], ph, p.err);
       uint4 v[NQ];
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        if (q >= nq) break;
-        v[q] = buf[tid + q * G];
-      }
-      if (TAIL) {  // listed lanes become -inf: the list warp counts them
-        uint32_t listed[2] = {0u, 0u};  // a byte a chunk
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          if (q >= nq) break;
-          const int c = tid + q * G;
-          uint32_t b = bm[W == 8 ? c : c >> 1];
-          if (W == 4) b = (c & 1) ? b >> 4 : b & 15u;
-          listed[q >> 2] |= b << (8 * (q & 3));
-        }
-        if ((listed[0] | listed[1]) != 0) {
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            const uint32_t b = (listed[q >> 2] >> (8 * (q & 3))) & 255u;
-            if (b != 0) v[q] = dist_take_out<DT>(v[q], b);
-          }
-        }
-      }
       float m = -INFINITY;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         if (q >= nq) break;
+        v[q] = buf[tid + q * G];
+        if (TAIL) {  // listed lanes become -inf: the list warp counts them
+          const int c = tid + q * G;
+          uint32_t b = bm[W == 8 ? c : c >> 1];
+          if (W == 4) b = (c & 1) ? b >> 4 : b & 15u;
+          if (b != 0) v[q] = dist_take_out<DT>(v[q], b);
+        }
         if constexpr (DT == kBF16) {
           const uint32_t w = bf16x2_max(bf16x2_max(v[q].x, v[q].y), bf16x2_max(v[q].z, v[q].w));
           m = fmaxf(m, fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
@@ -727,6 +740,7 @@ DistillKernels distill_kernels(int dtype, bool tail) {
                        : (const void*)distill_stream_kernel<kF32, false, true>;
   }
   d.rows_threads = kDistT;
+  d.slots_off = kDistOffSlots;
   return d;
 }
 

@@ -1269,17 +1269,18 @@ static rr_status distill_shape(const rr::DistillKernels& dk, const rr::DistillPa
     const int64_t S = cdiv(nch_max, K);
     if (K > 1 && (K - 1) * S >= nch_min) break;  // every rank gets chunks
     if (const char* f = std::getenv("RR_DIST_K")) if (atoi(f) && atoi(f) != K) continue;
-    // 1, 5, 13 or 29 row warps: with the three others a block of 128 .. 1024
-    // threads, so that the 1024 threads an SM holds at 64 registers are whole blocks
-    int64_t nw = 1;
-    while (nw < 29 && 32 * nw * rr::kDistNQ < S) nw = 2 * nw + 3;
-    if (32 * nw * rr::kDistNQ < S) continue;
+    // the fewest row warps that hold the slice, then as many as the 32 warps an SM
+    // holds at 64 registers give each of that many blocks (three more a block are
+    // its merge and list warps)
+    int64_t nw = cdiv(S, 32 * rr::kDistNQ);
+    if (nw > 29) continue;
+    nw = 32 / (32 / (nw + 3)) - 3;
     DistillShape sh;
     sh.K = K;
     sh.T = (int)(nw + 3) * 32;
     sh.geo.S = (int32_t)S;
     sh.geo.words = (int32_t)cdiv(S * W, 32);
-    const int64_t list = 256 + 4 * 16 * K * (nw + 1);
+    const int64_t list = dk.slots_off + 4 * 16 * K * (nw + 1);
     const int64_t bits = list + 4 * 16 * (int64_t)p.k;
     const int64_t buf = round_up(bits + 8 * (int64_t)sh.geo.words, 128);
     const int64_t smem = buf + 2 * S * 16;

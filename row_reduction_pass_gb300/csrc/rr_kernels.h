@@ -220,7 +220,7 @@ struct DistillParams {
 // Launch geometry of the streaming kernel: a block (one of K of a cluster)
 // holds a slice of S 16-byte chunks of a row, at most kDistNQ a row thread;
 // byte offsets into its shared memory.
-constexpr int kDistNQ = 8;
+constexpr int kDistNQ = 7;
 struct DistillGeo {
   int32_t S;
   int32_t words;     // 32-bit words of a slice's column bits
@@ -232,6 +232,7 @@ struct DistillKernels {
   const void* rows;       // a block per row, any alignment and length
   int rows_threads;
   const void* stream[2];  // [cluster]
+  int slots_off;          // stream: byte offset of the [4][K * (row warps + 1)] slots
 };
 DistillKernels distill_kernels(int dtype, bool tail);
 
