@@ -1268,7 +1268,6 @@ static rr_status distill_shape(const rr::DistillKernels& dk, const rr::DistillPa
   for (int K = 1; K <= 8; ++K) {
     const int64_t S = cdiv(nch_max, K);
     if (K > 1 && (K - 1) * S >= nch_min) break;  // every rank gets chunks
-    if (const char* f = std::getenv("RR_DIST_K")) if (atoi(f) && atoi(f) != K) continue;
     // the fewest row warps that hold the slice, then as many as the 32 warps an SM
     // holds at 64 registers give each of that many blocks (three more a block are
     // its merge and list warps)
@@ -1379,12 +1378,16 @@ rr_status distill_launch(rr::DistillParams p, rr_dtype dt, cudaStream_t stream) 
 
 // A cluster of K blocks a sequence.  With few sequences (all their clusters on the
 // chip at once, a block per SM): the largest K, two row buffers and the noise in
-// shared memory.  With many: the largest K whose blocks are about twice what the
-// chip holds at four a SM, one buffer.  No cluster where the slices do not fit.
+// shared memory (one chain of 50304 columns: K = 8 29 us, K = 4 38, K = 2 48; 8 trees
+// 31 us against 46).  With many: the largest K whose blocks are at most twice what
+// the chip holds at four a SM, one buffer (256 chains: K = 4 107 us, K = 2 122, K = 8
+// 445; 48 of 131072 columns: K = 8 62 us, K = 4 85).  No cluster where the slices
+// do not fit.
 rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
   const rr::VerifyKernels vk = rr::verify_kernels(dt);
   const int64_t E = dt == RR_BF16 ? 2 : 4;
-  int K = 0, threads = 224;
+  int K = 0;
+  const int threads = 224;  // working ones; a block has 32 more
   rr::VerifyGeo g{};
   size_t smem = 0;
   {
@@ -1415,20 +1418,14 @@ rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
     };
     int kmax = 8;
     while (kmax > 1 && p.cols < 512 * kmax) kmax /= 2;
-    int forced = 0, fa = -1, ft = 0;
-    if (const char* f = std::getenv("RR_VER_K")) std::sscanf(f, "%d:%d:%d", &forced, &fa, &ft);
-    if (ft) threads = ft;
     for (int k = kmax; k >= 1 && K == 0; k /= 2)
-      if (p.batch * k <= di->sms && (forced == 0 || forced == k)) shape(k, fa != 0);
+      if (p.batch * k <= di->sms) shape(k, true);
     for (int k = kmax; k >= 1 && K == 0; k /= 2)
-      if ((k == 1 || p.batch * k <= 8 * (int64_t)di->sms) && (forced == 0 || forced == k)) {
-        // (a shape that does not fit with few blocks may with more)
-        if (!shape(k, fa == 1)) {
-          for (int k2 = 2 * k; k2 <= kmax && K == 0; k2 *= 2) shape(k2, false);
-          break;
-        }
+      if (k == 1 || p.batch * k <= 8 * (int64_t)di->sms) {
+        // (slices that do not fit with few blocks may with more)
+        for (int k2 = k; k2 <= kmax && K == 0; k2 *= 2) shape(k2, false);
+        break;
       }
-    // 1024 threads an SM: shared among the blocks that fit by shared memory
     if (K > 0 && (st = set_smem(di, vk.cluster, smem)) != RR_OK) return st;
   }
   cudaError_t e;

@@ -16,6 +16,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIBNAME = "librr.so"
 _lock = threading.Lock()
 _lib = None
+_torch_module = None  # imported at the first call
 
 RR_F32 = 0
 RR_BF16 = 1
@@ -109,6 +110,14 @@ def rr_status_string(status: int) -> str:
     return load_library().rr_status_string(int(status)).decode()
 
 
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
 def _check(fn: str, status: int):
     if status != 0:
         detail = load_library().rr_last_error_detail()
@@ -132,6 +141,15 @@ def _stream(stream):
     import torch
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _raw_stream(stream):
+    """The stream's handle; the current one's without building a Stream object
+    (3 us of a call's 12-17)."""
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _contig(*ts):
@@ -276,28 +294,24 @@ def _args(fn, *ts):
     """Checks (name, tensor, dtype or None, shape) tuples of one call: contiguous
     CUDA tensors of that dtype and shape on the current device (a None tensor,
     an absent argument, passes).  Returns their addresses."""
-    import torch
-    out = []
+    out, devs = [], set()
     for name, t, dtype, shape in ts:
         if t is None:
             out.append(None)
             continue
-        if dtype is not None and t.dtype != dtype:
+        if dtype is not None and t.dtype is not dtype:
             raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{fn}: {name} must be contiguous")
         out.append(t.data_ptr())
-    dev = -1
-    for name, t, _, _ in ts:
-        if t is not None:
-            if not t.is_cuda:
+        devs.add(t.get_device())
+    if len(devs) != 1 or -1 in devs or devs != {_torch().cuda.current_device()}:
+        for name, t, _, _ in ts:
+            if t is not None and not t.is_cuda:
                 raise ValueError(f"{fn}: {name} must be a CUDA tensor")
-            if dev < 0:
-                dev = torch.cuda.current_device()
-            if t.get_device() != dev:
-                raise ValueError(f"{fn}: {name} is on {t.device}, not on the current device")
+        raise ValueError(f"{fn}: the tensors must all be on the current device")
     return out
 
 
@@ -307,7 +321,7 @@ def rr_distill_fwd_bwd(logits, top_index, top_value, loss, dlogits=None, grad=No
     (top_index int32, top_value fp32, [rows, k]); tail keeps the teacher's mass
     outside the list (top_value then holds log-probabilities).  dlogits may be
     logits, or None for the loss alone; grad [rows] scales dlogits."""
-    import torch
+    torch = _torch()
     rows, cols = logits.shape
     k = top_index.shape[1]
     i32, f32 = torch.int32, torch.float32
@@ -322,7 +336,7 @@ def rr_distill_fwd_bwd(logits, top_index, top_value, loss, dlogits=None, grad=No
          None if bad_index_count is None else bad_index_count.shape))
     st = load_library().rr_distill_fwd_bwd(x, i, v, g, l, d, rows, cols, k, temperature,
                                            1 if tail else 0, bad, _dtype(logits),
-                                           _stream(stream))
+                                           _raw_stream(stream))
     if st != 0:
         _check(fn, st)
 
@@ -344,7 +358,7 @@ def rr_attention_tree_fwd(q, k_cache, v_cache, page_table, context_len, o, lse=N
 
     ``workspace`` is a uint8 CUDA tensor of at least
     ``rr_attention_tree_workspace_size`` bytes; it is allocated here if omitted."""
-    import torch
+    torch = _torch()
     b, n, h, d = q.shape
     pages, page_size, kv, _ = k_cache.shape
     width = page_table.shape[1]
@@ -366,7 +380,7 @@ def rr_attention_tree_fwd(q, k_cache, v_cache, page_table, context_len, o, lse=N
     if scale is None:
         scale = 1.0 / float(d) ** 0.5
     st = lib.rr_attention_tree_fwd(pq, pk, pv, pt, pc, pp, po, pl, pw, size, b, n, h, kv, d, pages,
-                                   page_size, width, scale, _dtype(q), _stream(stream))
+                                   page_size, width, scale, _dtype(q), _raw_stream(stream))
     if st != 0:
         _check(fn, st)
 
@@ -380,7 +394,7 @@ def rr_draft_verify(target_logits, draft_logits, tokens, uniform, race, out_toke
     tokens / parents (int32) and uniform (fp32) [batch, nodes], race [batch, cols]
     exponential noise, temperature [batch] (<= 0: greedy).  Writes out_tokens and
     out_nodes [batch, nodes + 1] and out_count [batch] (int32)."""
-    import torch
+    torch = _torch()
     b, n1, v = target_logits.shape
     n, dt, i32, f32 = n1 - 1, target_logits.dtype, torch.int32, torch.float32
     fn = "rr_draft_verify"
@@ -392,7 +406,7 @@ def rr_draft_verify(target_logits, draft_logits, tokens, uniform, race, out_toke
         ("out_tokens", out_tokens, i32, (b, n1)), ("out_nodes", out_nodes, i32, (b, n1)),
         ("out_count", out_count, i32, (b,)))
     st = load_library().rr_draft_verify(pt, pd, pk, pp, pu, pr, pT, ot, on, oc, b, n, v,
-                                        _dtype(target_logits), _stream(stream))
+                                        _dtype(target_logits), _raw_stream(stream))
     if st != 0:
         _check(fn, st)
 
