@@ -320,11 +320,12 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
     if (db > 0)
       bulk_load(pbuf(s) + g.row_bytes, d + c0 * E - head(d), db, &full[s], policy_evict_first());
   };
-  // the logits of child i's token in the rows of `node`
-  auto logits_at = [&](int node, int i, float& t, float& d) {
+  // the logits of child i's token in the rows of `node`, as they are stored (a
+  // conversion here would wait for them, 1000 cycles and more a node)
+  auto logits_at = [&](int node, int i, uint32_t& t, uint32_t& d) {
     if (i < 0 || greedy) return;
-    t = ld_elem<DT>(trow(node) + (int64_t)tok[i] * E);
-    d = ld_elem<DT>(drow(node) + (int64_t)tok[i] * E);
+    t = ld_elem_bits<DT>(trow(node) + (int64_t)tok[i] * E);
+    d = ld_elem_bits<DT>(drow(node) + (int64_t)tok[i] * E);
   };
   auto wait_rows = [&](int s) {
     agree(dead || mbar_wait_bounded(&full[s], (uint32_t)((loads[s] - 1) & 1), p.err));
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
   int cur = -1, done = 0, s = 0;
   int child = next_child(-1, 0);
   load_rows(-1, child, 0);
-  float tx = 0.f, dx = 0.f;  // the first child's logits
+  uint32_t tx = 0, dx = 0;  // the first child's logits
   logits_at(-1, child, tx, dx);
   if (g.noise_off >= 0 && !greedy && tid == NT) {
     const uint32_t nb = nc > 0 ? (uint32_t)((nh + nc * 4 + 15) & ~15) : 0;
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
     const unsigned char* qb = pb + g.row_bytes;
     // with two buffers the first child's rows are loaded while this node is worked on
     int ahead = -1, ahead_child = -1;
-    float atx = 0.f, adx = 0.f;
+    uint32_t atx = 0, adx = 0;
     if (g.buffers == 2 && child >= 0) {
       ahead = child;
       ahead_child = next_child(child, child + 1);
@@ -488,30 +489,41 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
     Soft P{}, Q{};
     BestTok top{0.f, -1};
     if (greedy) {
+      // a thread keeps its greatest chunk (the first of equal ones: its chunks come
+      // in ascending order) and looks for the place in it at the end
       const Parts q = parts(hp);
-      float m = -INFINITY;
-      int at = INT32_MAX;
-      const int j1 = single(q);
       const char* row = reinterpret_cast<const char*>(pb) + hp;
-      auto look = [&](float v, int j) {
-        if (v > m || (v == m && j < at && v > -INFINITY)) {
-          m = v;
-          at = j;
-        }
-      };
-      if (works && j1 >= 0) look(ld_smem_elem<DT>(row + j1 * E), j1);
+      const uint4* base = reinterpret_cast<const uint4*>(row + q.lead * E);
+      float m = -INFINITY;
+      int at = -1, chunk = -1;
+#pragma unroll 4
       for (int k = tid; works && k < q.chunks; k += NT) {
-        const int j = q.lead + k * W;
-        const uint4 v = *reinterpret_cast<const uint4*>(row + j * E);
-        float x[W];
+        const uint4 v = base[k];
+        float cm;
+        if constexpr (DT == kBF16) {
+          const uint32_t w = bf16x2_max(bf16x2_max(v.x, v.y), bf16x2_max(v.z, v.w));
+          cm = fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+        } else {
+          cm = fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                     fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+        }
+        if (cm > m) {
+          m = cm;
+          chunk = k;
+        }
+      }
+      if (chunk >= 0) {
+        const uint4 v = base[chunk];
 #pragma unroll
-        for (int e = 0; e < W; ++e) x[e] = chunk_get<DT>(v, e);
-        float cm = x[0];
-#pragma unroll
-        for (int e = 1; e < W; ++e) cm = fmaxf(cm, x[e]);
-        if (cm >= m) {
-#pragma unroll
-          for (int e = 0; e < W; ++e) look(x[e], j + e);
+        for (int e = W - 1; e >= 0; --e)
+          if (chunk_get<DT>(v, e) == m) at = q.lead + chunk * W + e;
+      }
+      const int j1 = works ? single(q) : -1;
+      if (j1 >= 0) {
+        const float v = ld_smem_elem<DT>(row + j1 * E);
+        if (v > m || (v == m && at >= 0 && j1 < at)) {
+          m = v;
+          at = j1;
         }
       }
       top = merge(BestTok{m, m > -INFINITY ? (int)(c0 + at) : -1});
@@ -570,7 +582,7 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
         }
       } else {
         if (i != child) logits_at(cur, i, tx, dx);
-        const float px = prob(P, tx), qx = prob(Q, dx);
+        const float px = prob(P, bits_to_f32<DT>(tx)), qx = prob(Q, bits_to_f32<DT>(dx));
         if (uni[i] * mass * qx < px - ratio * qx) {
           next = i;
           break;
