@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       mbar_init(&ready[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&mrg[i], nslot);
+      mbar_init(&mrg[i], CL ? 1 : nslot);  // (in a cluster: the bytes of the slots)
       mbar_init(&done[i], 1);
     }
     fence_mbar_init();
@@ -332,12 +332,10 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     float4* sl = slots + (j & 3) * nslot + rank * nwp + w;
     const float4 v = make_float4(M, d, w < nw ? d : 0.f, 0.f);
     if constexpr (CL) {
-      // lane t writes to rank t (one lane after the other waited for each rank's
-      // store in turn: 5500 cycles a row for four ranks)
-      if (lane < K) {
-        st_cluster_f32x4(map_to_rank(sl, lane), v.x, v.y, v.z, v.w);
-        mbar_arrive_cluster(map_to_rank(&mrg[j & 3], lane));
-      }
+      // lane t writes to rank t (one lane after the other took 5500 cycles a row for
+      // four ranks)
+      if (lane < K)
+        st_async_f32x4(map_to_rank(sl, lane), map_to_rank(&mrg[j & 3], lane), v.x, v.y, v.z, v.w);
       __syncwarp();
     } else if (lane == 0) {
       *sl = v;
@@ -374,6 +372,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     }
     for (int64_t j = 0; row_of(j) < p.rows; ++j) {
       const uint32_t ph = (uint32_t)((j >> 2) & 1);
+      if (CL && lane == 0) mbar_arrive_expect_tx(&mrg[j & 3], (uint32_t)(nslot * 16));
       if (!dead) {
         if constexpr (CL) dead = !mbar_wait_bounded_cluster(&mrg[j & 3], ph, p.err);
         else dead = !mbar_wait_bounded(&mrg[j & 3], ph, p.err);

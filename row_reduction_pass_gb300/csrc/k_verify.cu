@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&met[i], nslot);
+      mbar_init(&met[i], 1);
     }
     mbar_init(noise_bar, 1);
     fence_mbar_init();
@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
   // A wait gave up, in any thread of the block (the threads agree on it after every
   // wait, since they meet at block barriers): the walk ends.
   bool dead = false;
-  auto agree = [&](bool ok) { dead = __syncthreads_or(dead || !ok); };
+  bool late = false;  // this thread gave up since they last agreed
+  auto agree = [&](bool ok) { dead = __syncthreads_or(dead || late || !ok); };
   auto trow = [&](int node) { return p.target + ((b * (n + 1) + node + 1) * V) * E; };
   auto drow = [&](int node) { return p.draft + ((b * n + node + 1) * V) * E; };
   // A slice of a row in shared memory: its first element is h bytes into the buffer.
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
     d = ld_elem_bits<DT>(drow(node) + (int64_t)tok[i] * E);
   };
   auto wait_rows = [&](int s) {
-    agree(dead || mbar_wait_bounded(&full[s], (uint32_t)((loads[s] - 1) & 1), p.err));
+    if (!dead && !late) late = !mbar_wait_bounded(&full[s], (uint32_t)((loads[s] - 1) & 1), p.err);
   };
   // Puts this warp's partial into every block's slots, and waits for all of them.
   int meets = 0;
@@ -336,11 +337,10 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
     const int s = meets & 1;
     const uint32_t ph = (uint32_t)((meets >> 1) & 1);
     ++meets;
-    if (works && lane < K) {  // lane k writes to block k
-      float4* sl = slots + s * nslot + rank * NW + warp;
-      st_cluster_f32x4(map_to_rank(sl, lane), v.x, v.y, v.z, v.w);
-      mbar_arrive_cluster(map_to_rank(&met[s], lane));
-    }
+    if (works && lane < K)  // lane k writes to block k
+      st_async_f32x4(map_to_rank(slots + s * nslot + rank * NW + warp, lane),
+                     map_to_rank(&met[s], lane), v.x, v.y, v.z, v.w);
+    if (tid == NT) mbar_arrive_expect_tx(&met[s], (uint32_t)(nslot * 16));
     __syncwarp();
     agree(dead || mbar_wait_bounded_cluster(&met[s], ph, p.err));
     return slots + s * nslot;
@@ -536,18 +536,26 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
       }
       const float4* sl = meet(make_float4(mp, zp, mq, zq));
       // lane l takes slots l, l + 32, ...; every warp the same way
-      float Mp = -INFINITY, Zp = 0.f, Mq = -INFINITY, Zq = 0.f;
+      float Mp = -INFINITY, Mq = -INFINITY, Zp = 0.f, Zq = 0.f;
+      for (int i = lane; i < nslot; i += 32) {
+        Mp = fmaxf(Mp, sl[i].x);
+        Mq = fmaxf(Mq, sl[i].z);
+      }
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) {
+        Mp = fmaxf(Mp, __shfl_xor_sync(0xffffffffu, Mp, off));
+        Mq = fmaxf(Mq, __shfl_xor_sync(0xffffffffu, Mq, off));
+      }
       for (int i = lane; i < nslot; i += 32) {
         const float4 t = sl[i];
-        const float a = fmaxf(Mp, t.x), d = fmaxf(Mq, t.z);
-        Zp = (Mp == -INFINITY ? Zp : Zp * ex2((Mp - a) * c)) +
-             (t.x == -INFINITY ? t.y : t.y * ex2((t.x - a) * c));
-        Zq = (Mq == -INFINITY ? Zq : Zq * ex2((Mq - d) * c)) +
-             (t.z == -INFINITY ? t.w : t.w * ex2((t.z - d) * c));
-        Mp = a;
-        Mq = d;
+        Zp += t.x == -INFINITY ? t.y : t.y * ex2((t.x - Mp) * c);
+        Zq += t.z == -INFINITY ? t.w : t.w * ex2((t.z - Mq) * c);
       }
-      add_up2(Mp, Zp, Mq, Zq);
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) {
+        Zp += __shfl_xor_sync(0xffffffffu, Zp, off);
+        Zq += __shfl_xor_sync(0xffffffffu, Zq, off);
+      }
       P = soft(Mp, Zp);
       Q = soft(Mq, Zq);
     }

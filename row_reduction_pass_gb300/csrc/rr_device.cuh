@@ -336,6 +336,18 @@ __device__ __forceinline__ void st_cluster_f32x4(uint32_t cl_addr, float a, floa
                "f"(c), "f"(d)
                : "memory");
 }
+// 16 bytes to the shared memory of a CTA of this cluster that complete as many
+// transaction bytes on an mbarrier there (addresses from mapa): the data and its
+// signal in one message, where a store followed by a release arrival waits for the
+// store's way there and back first.
+__device__ __forceinline__ void st_async_f32x4(uint32_t cl_addr, uint32_t cl_bar, float a, float b,
+                                               float c, float d) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, "
+      "[%1];" ::"r"(cl_addr),
+      "r"(cl_bar), "f"(a), "f"(b), "f"(c), "f"(d)
+      : "memory");
+}
 // try_wait with acquire at cluster scope (arrivals from other CTAs of the
 // cluster).
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
