@@ -366,10 +366,11 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     // ------------------------------------------------------ the merge warp
     // (A slot is written again four rows later by warps that wait for the rows
     // between, which wait for this block's row warps, which wait for this warp.)
-    if (lane == 0) {
-      load_row(0);
-      load_row(1);
-    }
+    // (long rows: the second is asked for when the first is there, or all blocks'
+    // first rows would come at the pace of two)
+    if (lane == 0) load_row(0);
+    if (g.S >= 2048 && row_of(0) < p.rows) dead = !mbar_wait_bounded(&full[0], 0, p.err);
+    if (lane == 0) load_row(1);
     for (int64_t j = 0; row_of(j) < p.rows; ++j) {
       const uint32_t ph = (uint32_t)((j >> 2) & 1);
       if (CL && lane == 0) mbar_arrive_expect_tx(&mrg[j & 3], (uint32_t)(nslot * 16));
