@@ -157,7 +157,8 @@ struct TreePL {
   static constexpr int kKVBytes = kBoxes * kKVBox;
   static constexpr int kPipe = kQBytes + NS * 2 * kKVBytes;
   static constexpr int kOffMask = 2 * kPipe;
-  static constexpr int kOffBar = kOffMask + 2 * kTM * kMaskStride * 4;
+  static constexpr int kOffPar = kOffMask + 2 * kTM * kMaskStride * 4;  // [2][256] parents
+  static constexpr int kOffBar = kOffPar + 2 * kTreeMaxNodes * 4;
   static constexpr int kOffScan = kOffBar + 512;
   static constexpr int kSmem = kOffScan + 256 + 1024;
   static constexpr uint32_t kColS = 0, kColP = BN, kColO = 256 - D;
@@ -306,6 +307,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   auto stage_k = [&](int s) { return pipe + C::kQBytes + (2 * s) * C::kKVBytes; };
   auto stage_v = [&](int s) { return pipe + C::kQBytes + (2 * s + 1) * C::kKVBytes; };
   uint32_t* masks = reinterpret_cast<uint32_t*>(smem + C::kOffMask) + w * kTM * kMaskStride;
+  int32_t* spar = reinterpret_cast<int32_t*>(smem + C::kOffPar) + w * kTreeMaxNodes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + w * 16;
   uint64_t* bar_q = bars + 0;       // Q written, 128 arrivals
   uint64_t* bar_s = bars + 1;       // S done
@@ -535,6 +537,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       bool present = live;
       float m = -INFINITY, l = 0.f;
       if (s.tiles > 0) {
+        // The piece's loads are asked for together: parents, Q, the table's entries.
+        int up0 = 0, up1 = 0;
+        if (p.parents != nullptr) {
+          const int32_t* par = p.parents + (int64_t)s.b * p.nodes;
+          if (row < p.nodes) up0 = __ldg(par + row);
+          if (row + 128 < p.nodes) up1 = __ldg(par + row + 128);
+        }
         // Q into the swizzled tile, a warp its 32 rows, whole rows at a time (a row per
         // lane would touch 32 lines an instruction); zeros for the rows of a live warp
         // beyond the last
@@ -553,16 +562,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         fence_proxy_async_smem();
         mbar_arrive(bar_q);
-        if (p.parents != nullptr) {
-          const int32_t* par = p.parents + (int64_t)s.b * p.nodes;
-          for (int i = 0; i < kMaskStride; ++i) mask[i] = 0;
-          for (int a = node; a >= 0 && present;) {
-            mask[a >> 5] |= 1u << (a & 31);
-            const int up = __ldg(par + a);
-            if (up < -1 || up >= a) present = false;
-            a = up;
-          }
-        }
         // pages that do not exist: none in the pieces of a sound table
         bool holes = false;
         {
@@ -573,41 +572,54 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           holes = __any_sync(0xffffffffu, holes);
         }
+        if (p.parents != nullptr) {
+          // the bits of this row's node and its ancestors
+          named_bar(1 + w, 128);  // (the parents of the piece before have been used)
+          if (row < p.nodes) spar[row] = up0;
+          if (row + 128 < p.nodes) spar[row + 128] = up1;
+          for (int i = 0; i < kMaskStride; ++i) mask[i] = 0;
+          named_bar(1 + w, 128);
+          for (int a = node; a >= 0 && present;) {
+            mask[a >> 5] |= 1u << (a & 31);
+            const int up = spar[a];
+            if (up < -1 || up >= a) present = false;
+            a = up;
+          }
+        }
         bool tail_seen = false;
         for (int j = 0; j < s.tiles; ++j, ++t) {
           const int key0 = (s.t0 + j) * BN;
           const bool tail = key0 + BN > min(s.ctx, s.vis);
-          if (tail) {
-            // V at positions nobody may see, and non-finite values at nodes: 0
-            // (This barrier is not waited on at every tile, and the products may be two
-            // tiles behind: V(t - 2) may not even have landed, and the wait for V(t)'s
-            // phase would then be satisfied by the phase before V(t - 2)'s.  So first
-            // the product that reads V(t - 2).)
-            tail_seen = true;
-            if (t >= 2) wait(&bar_vempty[t & 1], (uint32_t)(((t >> 1) - 1) & 1));
-            wait(&bar_vfull[t & 1], (uint32_t)((t >> 1) & 1));
-            const int vr = row % BN, pos = key0 + vr;
-            if (pos >= s.ctx || pos >= s.vis) {
-              uint4* vp = reinterpret_cast<uint4*>(stage_v(t & 1) + row / BN * C::kKVBox + vr * 128);
-#pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
-                uint4 x = vp[c];
-                if (pos >= s.vis) {
-                  vp[c] = make_uint4(0u, 0u, 0u, 0u);
-                } else if (odd_bf16x2(x.x) || odd_bf16x2(x.y) || odd_bf16x2(x.z) ||
-                           odd_bf16x2(x.w)) {
-                  for (int i = 0; i < 4; ++i) {
-                    uint32_t y = word_of(x, i);
-                    if ((y & 0x7f80u) == 0x7f80u) y &= 0xffff0000u;
-                    if ((y & 0x7f800000u) == 0x7f800000u) y &= 0xffffu;
-                    set_word(x, i, y);
-                  }
-                  vp[c] = x;
-                  *odd = piece;
+          // which of the tile's keys this row sees, 32 to a word
+          const bool masked = tail || holes;
+          uint32_t seen[BN / 32];
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) {
+              const int pos = key0 + 32 * c;  // of bit 0
+              const int nb = pos - s.ctx;     // its node
+              uint32_t bits = 0xffffffffu;
+              if (p.parents != nullptr) {
+                if (nb >= 0)
+                  bits = nb >> 5 < kMaskStride - 1
+                             ? __funnelshift_r(mask[nb >> 5], mask[(nb >> 5) + 1], nb & 31)
+                             : 0u;
+                else if (nb > -32)
+                  bits = (mask[0] << -nb) | ((1u << -nb) - 1u);
+              }
+              const int lim = p.parents != nullptr ? s.vis : min(s.ctx + node + 1, s.vis);
+              if (lim - pos <= 0) bits = 0;
+              else if (lim - pos < 32) bits &= (1u << (lim - pos)) - 1u;
+              if (holes) {
+                for (int i = 0; i < 32; i += 16) {
+                  if (pos + i >= s.vis) break;
+                  const int page =
+                      __ldg(p.table + (int64_t)s.b * p.width + tree_page(p, g, pos + i));
+                  if (page < 0 || page >= p.pages) bits &= ~(0xffffu << i);
                 }
               }
+              seen[c] = bits;
             }
-            fence_proxy_async_smem();
           }
           wait(bar_s, (uint32_t)(t & 1));
           tc_fence_after();
@@ -620,34 +632,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               for (int c = 0; c < 2; ++c) tmem_ld32_nowait(tS + 64 * hf + 32 * c, v[c]);
               tmem_ld_done(v[0]);
               tmem_ld_done(v[1]);
-              if (!tail && !holes) return;
+              if (masked) {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const int pos = key0 + 64 * hf + 32 * c;  // of bit 0
-                const int nb = pos - s.ctx;               // its node
-                uint32_t bits = 0xffffffffu;
-                if (p.parents != nullptr) {
-                  if (nb >= 0)
-                    bits = nb >> 5 < kMaskStride - 1
-                               ? __funnelshift_r(mask[nb >> 5], mask[(nb >> 5) + 1], nb & 31)
-                               : 0u;
-                  else if (nb > -32)
-                    bits = (mask[0] << -nb) | ((1u << -nb) - 1u);
-                }
-                const int lim = p.parents != nullptr ? s.vis : min(s.ctx + node + 1, s.vis);
-                if (lim - pos <= 0) bits = 0;
-                else if (lim - pos < 32) bits &= (1u << (lim - pos)) - 1u;
-                if (holes) {
-                  for (int i = 0; i < 32; i += 16) {
-                    if (pos + i >= s.vis) break;
-                    const int page =
-                        __ldg(p.table + (int64_t)s.b * p.width + tree_page(p, g, pos + i));
-                    if (page < 0 || page >= p.pages) bits &= ~(0xffffu << i);
-                  }
-                }
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (!((bits >> i) & 1)) v[c][i] = __float_as_uint(-INFINITY);
+                  for (int i = 0; i < 32; ++i)
+                    if (!((seen[2 * hf + c] >> i) & 1)) v[c][i] = __float_as_uint(-INFINITY);
               }
             };
             auto max_half = [&](float mx) {
@@ -742,6 +732,38 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             // a warp without rows keeps pace: its arrival below must not fall into
             // the P buffer's previous phase
             if (t >= C::NPB) wait(&bar_o[t % C::NPB], (uint32_t)((t / C::NPB - 1) & 1));
+          }
+          if (tail) {
+            // V at positions nobody may see, and non-finite values at nodes: 0
+            // (This barrier is not waited on at every tile, and the products may be two
+            // tiles behind: V(t - 2) may not even have landed, and the wait for V(t)'s
+            // phase would then be satisfied by the phase before V(t - 2)'s.  So first
+            // the product that reads V(t - 2).)
+            tail_seen = true;
+            if (t >= 2) wait(&bar_vempty[t & 1], (uint32_t)(((t >> 1) - 1) & 1));
+            wait(&bar_vfull[t & 1], (uint32_t)((t >> 1) & 1));
+            const int vr = row % BN, pos = key0 + vr;
+            if (pos >= s.ctx || pos >= s.vis) {
+              uint4* vp = reinterpret_cast<uint4*>(stage_v(t & 1) + row / BN * C::kKVBox + vr * 128);
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                uint4 x = vp[c];
+                if (pos >= s.vis) {
+                  vp[c] = make_uint4(0u, 0u, 0u, 0u);
+                } else if (odd_bf16x2(x.x) || odd_bf16x2(x.y) || odd_bf16x2(x.z) ||
+                           odd_bf16x2(x.w)) {
+                  for (int i = 0; i < 4; ++i) {
+                    uint32_t y = word_of(x, i);
+                    if ((y & 0x7f80u) == 0x7f80u) y &= 0xffff0000u;
+                    if ((y & 0x7f800000u) == 0x7f800000u) y &= 0xffffu;
+                    set_word(x, i, y);
+                  }
+                  vp[c] = x;
+                  *odd = piece;
+                }
+              }
+            }
+            fence_proxy_async_smem();
           }
           tc_fence_before();
           mbar_arrive(&bar_p[t % C::NPB]);
