@@ -34,6 +34,7 @@
 // row.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "rr_device.cuh"
 #include "rr_kernels.h"
@@ -194,9 +195,92 @@ __device__ __forceinline__ int tree_page_row(const TreeParams& p, const TreeGeo&
   return g.page_shift >= 0 ? pos & (p.page - 1) : pos % p.page;
 }
 
-// The run of group `grp`: tiles [grp * share, (grp + 1) * share) of all.
-__device__ __forceinline__ int tree_share(int total, int groups, int min_tiles) {
-  return max((total + groups - 1) / groups, min_tiles);
+// How the tiles are cut into runs, one for each group of pipelines.
+//   flat: run i is tiles [i share, (i + 1) share) of all, across items.
+//   own (few items): every item is cut into pieces of at most `share` tiles of its
+//     own, a piece a run.  No run then pays for a second piece (its own queries,
+//     first products, output: about kTreePieceTiles tiles), so this is taken where
+//     its longest run is at most that much longer than the flat one: 16 sequences of
+//     1000-4100 keys, 30 nodes, head_dim 64: the slowest pipeline 42000 -> 24000
+//     cycles.
+struct TreePlan {
+  int share;
+  bool own;
+};
+constexpr int kTreePieceTiles = 3;
+constexpr int kTreeWarpSeqs = 320;  // a warp plans up to these many; more are always flat
+
+__device__ __forceinline__ int tree_cdiv(int a, int b) { return (a + b - 1) / b; }
+__device__ __forceinline__ int warp_isum(int v) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// Sequence b's tiles (0 past the last sequence).  The planning loops read the
+// lengths again each time: they stay in the first-level cache, and rolled loops keep
+// the code short, which is fetched once per call.
+template <int BN>
+__device__ __forceinline__ int tree_tiles_of(const TreeParams& p, const TreeGeo& g, int b) {
+  return b < (int)p.batch ? tree_tiles<BN>(p, g, tree_context(p, g, b)) : 0;
+}
+template <int BN>
+__device__ __forceinline__ TreePlan tree_plan(const TreeParams& p, const TreeGeo& g) {
+  const int lane = threadIdx.x & 31, batch = (int)p.batch;
+  int sum = 0, some = 0;
+#pragma unroll 1
+  for (int b = lane; b < batch; b += 32) {
+    const int T = tree_tiles_of<BN>(p, g, b);
+    sum += T;
+    some += T > 0;
+  }
+  sum = warp_isum(sum) * g.KM;
+  some = warp_isum(some) * g.KM;
+  TreePlan plan{max(tree_cdiv(sum, g.groups), g.min_tiles), false};
+  if (some > g.groups) return plan;
+  // the least share, at most kTreePieceTiles above the flat one, whose pieces are no
+  // more than the groups
+#pragma unroll 1
+  for (int share = plan.share; share <= plan.share + kTreePieceTiles; ++share) {
+    int n = 0;
+#pragma unroll 1
+    for (int b = lane; b < batch; b += 32) n += tree_cdiv(tree_tiles_of<BN>(p, g, b), share);
+    if (warp_isum(n) * g.KM <= g.groups) return TreePlan{share, true};
+  }
+  return plan;
+}
+// A sequence's units: the plan's runs if they are items' own, else its tiles.
+template <int BN>
+__device__ __forceinline__ int tree_units(const TreeParams& p, const TreeGeo& g,
+                                          const TreePlan& plan, int b) {
+  const int T = tree_tiles_of<BN>(p, g, b);
+  return (plan.own ? tree_cdiv(T, plan.share) : T) * g.KM;
+}
+// The sequence that holds unit `at`, and how many are before it in *before; -1 past
+// the end.
+template <int BN>
+__device__ __forceinline__ int tree_find(const TreeParams& p, const TreeGeo& g,
+                                         const TreePlan& plan, int64_t at, int* before) {
+  const int lane = threadIdx.x & 31;
+  int base = 0;
+#pragma unroll 1
+  for (int b = 0; b < (int)p.batch; b += 32) {
+    const int v = tree_units<BN>(p, g, plan, b + lane);
+    int x = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, base + x > at);
+    if (m != 0) {
+      const int l = __ffs(m) - 1;
+      *before = base + __shfl_sync(0xffffffffu, x - v, l);
+      return b + l;
+    }
+    base += __shfl_sync(0xffffffffu, x, 31);
+  }
+  return -1;
 }
 
 template <int D>
@@ -351,21 +435,48 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     fence_mbar_init();
     *odd = 0;
-    firsts[w].left = 0;
   }
-  // where the two pipelines' runs begin: each thread counts the tiles of some
-  // sequences, and the one that holds a run's first tile writes it down
-  {
+  // where this pipeline's run begins
+  TreeSeg first;
+  first.left = 0;
+  const int grp = (slot0 + w) / g.side, sub = slot0 + w - grp * g.side;
+  if (p.batch <= kTreeWarpSeqs) {
+    if (grp < g.groups) {
+      int before = 0;
+      const TreePlan plan = tree_plan<BN>(p, g);
+      const int64_t at = plan.own ? grp : (int64_t)grp * plan.share;
+      const int b = tree_find<BN>(p, g, plan, at, &before);
+      if (b >= 0) {
+        first.b = b;
+        first.ctx = tree_context(p, g, b);
+        first.T = tree_tiles<BN>(p, g, first.ctx);
+        const int off = (int)at - before;
+        if (plan.own) {
+          const int n = tree_cdiv(first.T, plan.share);
+          first.hm = off / n;
+          first.t0 = (off - first.hm * n) * plan.share;
+          first.left = min(plan.share, first.T - first.t0);
+        } else {
+          first.hm = off / first.T;
+          first.t0 = off - first.hm * first.T;
+          first.left = plan.share;  // (the sequences end, or the run does)
+        }
+      }
+    }
+  } else {
+    // many sequences: each thread counts the tiles of some, and the one that holds a
+    // run's first tile writes it down
     const int batch = (int)p.batch, per = (batch + kTreeThreads - 1) / kTreeThreads;
     const int b0 = tid * per, b1 = min(b0 + per, batch);
     int mine = 0, total;
+    if (tid < 2) firsts[tid].left = 0;  // (before the scan's barriers)
     for (int b = b0; b < b1; ++b) mine += tree_tiles<BN>(p, g, tree_context(p, g, b)) * g.KM;
     const int at = tree_scan(mine, scratch, &total);
-    const int share = tree_share(total, g.groups, g.min_tiles);
+    const int share = max(tree_cdiv(total, g.groups), g.min_tiles);
     for (int s = 0; s < 2; ++s) {
-      const int grp = (slot0 + s) / g.side, sub = slot0 + s - grp * g.side;
-      const int64_t start = (int64_t)grp * share;
-      if (grp >= g.groups || start < at || start >= (int64_t)at + mine) continue;
+      const int gs = (slot0 + s) / g.side;
+      const int64_t start = (int64_t)gs * share;
+      if (gs >= g.groups || start < at || start >= (int64_t)at + mine) continue;
       int off = (int)start - at;
       for (int b = b0; b < b1; ++b) {
         TreeSeg sg;
@@ -376,24 +487,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           off -= n;
           continue;
         }
-        sg.left = min(share, total - (int)start);
+        sg.left = share;
         sg.b = b;
         sg.hm = off / sg.T;
         sg.t0 = off - sg.hm * sg.T;
-        const int mb = g.MT / g.RB, hb = sg.hm / mb;
-        sg.h = hb * g.HB + sub / g.RB;
-        sg.mt = (sg.hm - hb * mb) * g.RB + sub % g.RB;
-        tree_seg_fill<D>(sg, p, g);
         firsts[s] = sg;
         break;
       }
     }
+    __syncthreads();
+    first = firsts[w];
+  }
+  if (first.left > 0) {
+    const int mb = g.MT / g.RB, hb = first.hm / mb;
+    first.h = hb * g.HB + sub / g.RB;
+    first.mt = (first.hm - hb * mb) * g.RB + sub % g.RB;
+    tree_seg_fill<D>(first, p, g);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *tslot + 256u * w;
-  const TreeSeg first = firsts[w];
   bool dead = false;  // a wait gave up: no further waits (the kernel still ends)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!dead) dead = !mbar_wait_bounded(bar, parity, p.err);
@@ -586,14 +700,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             a = up;
           }
         }
+        // Tiles wholly inside the context go through a copy of the loop's body without
+        // masks (a loop that carried them: large trees 235 -> 256 us).
         bool tail_seen = false;
-        for (int j = 0; j < s.tiles; ++j, ++t) {
+        auto tile = [&](auto masked_c, int j) {
+          constexpr bool masked = decltype(masked_c)::value;
           const int key0 = (s.t0 + j) * BN;
-          const bool tail = key0 + BN > min(s.ctx, s.vis);
+          const bool tail = masked && key0 + BN > min(s.ctx, s.vis);
           // which of the tile's keys this row sees, 32 to a word
-          const bool masked = tail || holes;
           uint32_t seen[BN / 32];
-          if (masked) {
+          if constexpr (masked) {
 #pragma unroll
             for (int c = 0; c < BN / 32; ++c) {
               const int pos = key0 + 32 * c;  // of bit 0
@@ -632,7 +748,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               for (int c = 0; c < 2; ++c) tmem_ld32_nowait(tS + 64 * hf + 32 * c, v[c]);
               tmem_ld_done(v[0]);
               tmem_ld_done(v[1]);
-              if (masked) {
+              if constexpr (masked) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -767,7 +883,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           tc_fence_before();
           mbar_arrive(&bar_p[t % C::NPB]);
-        }
+        };
+        const int inside = holes ? 0 : min(s.tiles, max(0, min(s.ctx, s.vis) / BN - s.t0));
+        int j = 0;
+        for (; j < inside; ++j, ++t) tile(std::false_type{}, j);
+        for (; j < s.tiles; ++j, ++t) tile(std::true_type{}, j);
         wait(&bar_o[(t - 1) % C::NPB], (uint32_t)(((t - 1) / C::NPB) & 1));
         tc_fence_after();
         if (tail_seen) named_bar(1 + w, 128);  // every thread's look at V
@@ -838,15 +958,42 @@ __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, c
   const int tid = threadIdx.x;
   // block (x, z): item x of all, pipeline z of its group
   const int b = (int)blockIdx.x / g.KM, hm = (int)blockIdx.x - b * g.KM;
-  // tiles before this sequence, and of all
-  const int batch = (int)p.batch, per = (batch + kJoinT - 1) / kJoinT;
-  const int b0 = tid * per, b1 = min(b0 + per, batch);
-  int mine = 0, total;
-  for (int i = b0; i < b1; ++i) mine += tree_tiles<BN>(p, g, tree_context(p, g, i)) * g.KM;
-  int at = tree_scan(mine, scratch, &total);
-  if (b >= b0 && b < b1) {
-    for (int i = b0; i < b; ++i) at += tree_tiles<BN>(p, g, tree_context(p, g, i)) * g.KM;
-    s_before = at;
+  const int tiles = tree_tiles<BN>(p, g, tree_context(p, g, b));
+  // the item's first run, the runs that hold a piece of it, the first one's piece
+  int run0 = 0, n = 0, skip = 0;
+  if (p.batch <= kTreeWarpSeqs) {
+    const TreePlan plan = tree_plan<BN>(p, g);
+    int mine = 0;  // units before this sequence
+#pragma unroll 1
+    for (int i = tid & 31; i < b; i += 32) mine += tree_units<BN>(p, g, plan, i);
+    const int before = warp_isum(mine);
+    if (tiles > 0 && plan.own) {
+      n = tree_cdiv(tiles, plan.share);
+      run0 = before + hm * n;
+    } else if (tiles > 0) {
+      const int start = before + hm * tiles;
+      run0 = start / plan.share;
+      n = (start + tiles - 1) / plan.share - run0 + 1;
+      skip = run0 * plan.share < start;
+    }
+  } else {
+    const int batch = (int)p.batch, per = (batch + kJoinT - 1) / kJoinT;
+    const int b0 = tid * per, b1 = min(b0 + per, batch);
+    int mine = 0, total;
+    for (int i = b0; i < b1; ++i) mine += tree_tiles<BN>(p, g, tree_context(p, g, i)) * g.KM;
+    int at = tree_scan(mine, scratch, &total);
+    if (b >= b0 && b < b1) {
+      for (int i = b0; i < b; ++i) at += tree_tiles<BN>(p, g, tree_context(p, g, i)) * g.KM;
+      s_before = at;
+    }
+    __syncthreads();
+    if (tiles > 0) {
+      const int share = max(tree_cdiv(total, g.groups), g.min_tiles);
+      const int start = s_before + hm * tiles;
+      run0 = start / share;
+      n = (start + tiles - 1) / share - run0 + 1;
+      skip = run0 * share < start;
+    }
   }
   const int all_rows = p.nodes * g.G, ws_rows = min(all_rows, kTM);
   const int flat = (int)blockIdx.y * kJoinT + tid;  // of the piece's chunks
@@ -855,22 +1002,16 @@ __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, c
   const int h = hb * g.HB + sub / g.RB, mt = (hm - hb * mb) * g.RB + sub % g.RB;
   const int R = mt * kTM + row, node = R / g.G;
   const int64_t out = ((int64_t)b * p.nodes + node) * p.heads + h * g.G + R - node * g.G;
-  const int T = tree_tiles<BN>(p, g, tree_context(p, g, b));
-  const int share = tree_share(total, g.groups, g.min_tiles);
-  __syncthreads();
-  const int start = s_before + hm * T;
-  const int s0 = start / share, s1 = (start + T - 1) / share;
   // Launched while the pieces are still being computed: every block waits for
   // them here, also one without work, so that this grid ends after that one.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (T > 0 && s0 == s1) return;  // finished by its run
+  if (n == 1) return;  // finished by its run
   if (chunk >= D / 4 || R >= all_rows) return;
   const float4* ws_o = reinterpret_cast<const float4*>(p.ws);
   const float2* ws_ml =
       reinterpret_cast<const float2*>(p.ws + (int64_t)g.max_slots * 2 * ws_rows * D);
-  // the item's piece in a run is the run's last if it begins inside the run
-  auto part = [&](int s) { return 2 * (s * g.side + sub) + (s * share < start ? 1 : 0); };
-  const int n = T > 0 ? s1 - s0 + 1 : 0;
+  // an item's piece in a run is the run's last if it begins inside the run: its first
+  auto part = [&](int i) { return 2 * ((run0 + i) * g.side + sub) + (i == 0 ? skip : 0); };
   float M = -INFINITY, L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = 0; i0 < n; i0 += U) {
@@ -882,7 +1023,7 @@ __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, c
       ml[i] = make_float2(-INFINITY, 0.f);
       x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i0 + i < n) {
-        const int64_t pt = part(s0 + i0 + i);
+        const int64_t pt = part(i0 + i);
         ml[i] = ws_ml[pt * ws_rows + row];
         x[i] = ws_o[(pt * (D / 4) + chunk) * ws_rows + row];
       }

@@ -192,10 +192,11 @@ def test_tree_attention_lengths(D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("batch,ctx", [(1, 6000), (3, 9001), (70, 200)])
+@pytest.mark.parametrize("batch,ctx", [(1, 6000), (3, 9001), (17, 900), (70, 200), (320, 60), (321, 60),
+                                       (700, 33)])
 def test_tree_attention_split_sequences(D, batch, ctx):
     """Long contexts shared between many blocks, and more sequences than blocks."""
-    check_tree(*tree_inputs(batch, 2, 2, 1, D, [ctx - 13 * b for b in range(batch)], 64, ctx + D,
+    check_tree(*tree_inputs(batch, 2, 2, 1, D, [max(0, ctx - 13 * b) for b in range(batch)], 64, ctx + D,
                             True))
 
 
