@@ -292,6 +292,15 @@ __device__ __forceinline__ void tree_seg_fill(TreeSeg& s, const TreeParams& p, c
   s.vis = min(s.ctx + last + 1, g.cap);
   s.tiles = max(0, min(s.t1, (s.vis + BN - 1) / BN) - s.t0);
 }
+// A run's first piece, from its item hm: head, row tile, tiles.
+template <int D>
+__device__ __forceinline__ void tree_seg_place(TreeSeg& s, const TreeParams& p, const TreeGeo& g,
+                                               int sub) {
+  const int mb = g.MT / g.RB, hb = s.hm / mb;
+  s.h = hb * g.HB + sub / g.RB;
+  s.mt = (s.hm - hb * mb) * g.RB + sub % g.RB;
+  tree_seg_fill<D>(s, p, g);
+}
 template <int D>
 __device__ __forceinline__ bool tree_seg_next(TreeSeg& s, const TreeParams& p, const TreeGeo& g) {
   s.left -= s.t1 - s.t0;
@@ -343,36 +352,6 @@ __device__ __forceinline__ int tree_scan(int v, int* scratch, int* total) {
 // (maximum, sum).
 __device__ __forceinline__ bool odd_bf16x2(uint32_t w) {  // an infinity or NaN in the pair
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-
-// Adds to columns [32 c, 32 c + 32) of a row's output the non-finite values of V
-// at the nodes of piece s that its node sees (a rare path, kept out of line).
-__device__ __noinline__ void tree_add_odd_at(const TreeParams& p, int b, int ctx, int lo, int hi,
-                                             int h, int node, const uint32_t* mask, int D, int c,
-                                             float* o) {
-  for (int pos = lo; pos < hi; ++pos) {
-    const int j = pos - ctx;
-    if (p.parents != nullptr ? !((mask[j >> 5] >> (j & 31)) & 1) : j > node) continue;
-    const int page = __ldg(p.table + (int64_t)b * p.width + pos / p.page);
-    if (page < 0 || page >= p.pages) continue;
-    const char* v = p.v + ((((int64_t)page * p.page + pos % p.page) * p.kv_heads + h) * D + 32 * c) * 2;
-    for (int i = 0; i < 32; ++i) {
-      const float f = ld_elem_cached<kBF16>(v + 2 * i);
-      if (!(fabsf(f) < INFINITY)) o[i] += f;
-    }
-  }
-}
-__device__ __forceinline__ void tree_add_odd(const TreeParams& p, const TreeSeg& s, int h,
-                                             int node, const uint32_t* mask, int D, int BN,
-                                             int c, uint32_t (&o)[32]) {
-  float f[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) f[i] = 0.f;
-  tree_add_odd_at(p, s.b, s.ctx, max(s.ctx, s.t0 * BN), min((s.t0 + s.tiles) * BN, s.vis), h,
-                  node, mask, D, c, f);
-#pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (f[i] != 0.f) o[i] = __float_as_uint(__uint_as_float(o[i]) + f[i]);
 }
 
 template <int D>
@@ -436,32 +415,37 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     fence_mbar_init();
     *odd = 0;
   }
-  // where this pipeline's run begins
-  TreeSeg first;
-  first.left = 0;
-  const int grp = (slot0 + w) / g.side, sub = slot0 + w - grp * g.side;
+  // where the pipelines' runs begin: a loading warp of each plans (the others only
+  // read the result: a plan in every warp cost the softmax loop registers)
   if (p.batch <= kTreeWarpSeqs) {
-    if (grp < g.groups) {
-      int before = 0;
-      const TreePlan plan = tree_plan<BN>(p, g);
-      const int64_t at = plan.own ? grp : (int64_t)grp * plan.share;
-      const int b = tree_find<BN>(p, g, plan, at, &before);
-      if (b >= 0) {
-        first.b = b;
-        first.ctx = tree_context(p, g, b);
-        first.T = tree_tiles<BN>(p, g, first.ctx);
-        const int off = (int)at - before;
-        if (plan.own) {
-          const int n = tree_cdiv(first.T, plan.share);
-          first.hm = off / n;
-          first.t0 = (off - first.hm * n) * plan.share;
-          first.left = min(plan.share, first.T - first.t0);
-        } else {
-          first.hm = off / first.T;
-          first.t0 = off - first.hm * first.T;
-          first.left = plan.share;  // (the sequences end, or the run does)
+    if (warp == 12 || warp == 13) {
+      TreeSeg sg;
+      sg.left = 0;
+      const int grp = (slot0 + w) / g.side;
+      if (grp < g.groups) {
+        int before = 0;
+        const TreePlan plan = tree_plan<BN>(p, g);
+        const int64_t at = plan.own ? grp : (int64_t)grp * plan.share;
+        const int b = tree_find<BN>(p, g, plan, at, &before);
+        if (b >= 0) {
+          sg.b = b;
+          sg.ctx = tree_context(p, g, b);
+          sg.T = tree_tiles<BN>(p, g, sg.ctx);
+          const int off = (int)at - before;
+          if (plan.own) {
+            const int n = tree_cdiv(sg.T, plan.share);
+            sg.hm = off / n;
+            sg.t0 = (off - sg.hm * n) * plan.share;
+            sg.left = min(plan.share, sg.T - sg.t0);
+          } else {
+            sg.hm = off / sg.T;
+            sg.t0 = off - sg.hm * sg.T;
+            sg.left = plan.share;  // (the sequences end, or the run does)
+          }
+          tree_seg_place<D>(sg, p, g, slot0 + w - grp * g.side);
         }
       }
+      if (lane == 0) firsts[w] = sg;
     }
   } else {
     // many sequences: each thread counts the tiles of some, and the one that holds a
@@ -491,23 +475,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         sg.b = b;
         sg.hm = off / sg.T;
         sg.t0 = off - sg.hm * sg.T;
+        tree_seg_place<D>(sg, p, g, slot0 + s - gs * g.side);
         firsts[s] = sg;
         break;
       }
     }
-    __syncthreads();
-    first = firsts[w];
-  }
-  if (first.left > 0) {
-    const int mb = g.MT / g.RB, hb = first.hm / mb;
-    first.h = hb * g.HB + sub / g.RB;
-    first.mt = (first.hm - hb * mb) * g.RB + sub % g.RB;
-    tree_seg_fill<D>(first, p, g);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *tslot + 256u * w;
+  const TreeSeg first = firsts[w];
   bool dead = false;  // a wait gave up: no further waits (the kernel still ends)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!dead) dead = !mbar_wait_bounded(bar, parity, p.err);
@@ -910,7 +888,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0u;
           }
-          if (fix) tree_add_odd(p, s, h, node, mask, D, BN, c, o);
+          if (fix) {
+            // Adds the non-finite values of V that this row sees (rare: rolled loops over
+            // a copy in the Q tile, which no product reads any more; a function of its own
+            // made the whole kernel 5 % slower, calls being costly to allocate around)
+            float* f = reinterpret_cast<float*>(sq) + row;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i * kTM] = __uint_as_float(o[i]);
+            const int hi = min((s.t0 + s.tiles) * BN, s.vis);
+#pragma unroll 1
+            for (int pos = max(s.ctx, s.t0 * BN); pos < hi; ++pos) {
+              const int j = pos - s.ctx;
+              if (p.parents != nullptr ? !((mask[j >> 5] >> (j & 31)) & 1) : j > node) continue;
+              const int page = __ldg(p.table + (int64_t)s.b * p.width + tree_page(p, g, pos));
+              if (page < 0 || page >= p.pages) continue;
+              const int64_t at = ((int64_t)page * p.page + tree_page_row(p, g, pos)) * p.kv_heads + h;
+              const char* v = p.v + (at * D + 32 * c) * 2;
+#pragma unroll 1
+              for (int i = 0; i < 32; ++i) {
+                const float x = ld_elem_cached<kBF16>(v + 2 * i);
+                if (!(fabsf(x) < INFINITY)) f[i * kTM] += x;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(f[i * kTM]);
+          }
           if (live && whole) {
             uint4* dst = reinterpret_cast<uint4*>(p.o + (out * D + 32 * c) * 2);
 #pragma unroll
