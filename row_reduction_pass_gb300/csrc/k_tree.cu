@@ -109,7 +109,6 @@ __global__ void __launch_bounds__(kTreeT) tree_rows_kernel_t(const TreeParams p)
     p.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 
-
 // ------------------------------------------------------------ tensor cores ---
 
 // 4-D TMA tile load [dst] <- map at {c0, c1, c2, c3}, completing bytes on bar.
@@ -346,14 +345,14 @@ __device__ __forceinline__ int tree_scan(int v, int* scratch, int* total) {
   return before + x - v;
 }
 
-// The workspace: two pieces a pipeline (its run's first and last), a piece being
-// [D / 4][rows] 16-byte chunks of the output (so that the rows of a warp write, and
-// the joining threads read, whole lines), and behind them the pieces' [rows]
-// (maximum, sum).
 __device__ __forceinline__ bool odd_bf16x2(uint32_t w) {  // an infinity or NaN in the pair
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
+// The workspace: two pieces a pipeline (its run's first and last), a piece being
+// [D / 4][rows] 16-byte chunks of the output (so that the rows of a warp write, and
+// the joining threads read, whole lines), and behind them the pieces' [rows]
+// (maximum, sum).
 template <int D>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -890,11 +889,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           if (fix) {
             // Adds the non-finite values of V that this row sees (rare: rolled loops over
-            // a copy in the Q tile, which no product reads any more; a function of its own
-            // made the whole kernel 5 % slower, calls being costly to allocate around)
-            float* f = reinterpret_cast<float*>(sq) + row;
+            // a copy in this warp's rows of the Q tile, which no product reads any more and
+            // no other warp writes; a function of its own made the whole kernel 5 % slower,
+            // calls being costly to allocate around)
+            float* f = reinterpret_cast<float*>(sq + (warp & 3) * 32 * 128) + lane;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i * kTM] = __uint_as_float(o[i]);
+            for (int i = 0; i < 32; ++i) f[i * 32] = __uint_as_float(o[i]);
             const int hi = min((s.t0 + s.tiles) * BN, s.vis);
 #pragma unroll 1
             for (int pos = max(s.ctx, s.t0 * BN); pos < hi; ++pos) {
@@ -907,12 +907,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll 1
               for (int i = 0; i < 32; ++i) {
                 const float x = ld_elem_cached<kBF16>(v + 2 * i);
-                if (!(fabsf(x) < INFINITY)) f[i * kTM] += x;
+                if (!(fabsf(x) < INFINITY)) f[i * 32] += x;
               }
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(f[i * kTM]);
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(f[i * 32]);
           }
+          __syncwarp();  // (the next piece's Q goes over f)
           if (live && whole) {
             uint4* dst = reinterpret_cast<uint4*>(p.o + (out * D + 32 * c) * 2);
 #pragma unroll
