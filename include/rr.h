@@ -365,6 +365,9 @@ size_t rr_attention_tree_workspace_size(int64_t batch, int64_t nodes, int64_t he
  *           nothing.
  *   lse : [batch x nodes x heads] float32, or NULL.
  *   head_dim 64 or 128; heads a multiple of kv_heads; scale > 0 and finite.
+ *   At most 65536 sequences, 2^20 nodes, 2^30 rows (batch x nodes x heads) and 2^30
+ *   positions in a row of the table; batch x kv_heads x ceil(nodes x heads / kv_heads
+ *   / 128) x (ceil(table positions / 64) + 1) at most 2^30.
  *   workspace : device scratch of workspace_bytes >= the size query's answer
  *           (16-byte aligned), owned by the caller; its contents on entry are
  *           ignored.  Calls that may overlap on the GPU need one each.
@@ -403,12 +406,13 @@ rr_status rr_attention_tree_fwd(const void *q, const void *k_cache, const void *
  *   uniform : [batch x nodes] float32 in [0, 1).  race : [batch x cols] float32 > 0.
  *   temperature : [batch] float32, or NULL (1).  <= 0: greedy, a child is
  *           accepted iff it is the target's largest logit (the lowest index at a
- *           tie), which is also the last token.
+ *           tie), which is also the last token.  Otherwise finite and >= 2^-120.
  *   out_tokens : [batch x (nodes + 1)] int32, the accepted tokens, the last
  *           token, then -1.  out_nodes : [batch x (nodes + 1)] int32, the nodes
  *           of the accepted tokens, then -1.  out_count : [batch] int32, how many
  *           were accepted.
- * Rows of nodes that are not reached are not looked at.  A target row without a
+ *   At most 65535 nodes; cols < 2^31.
+ * Rows of nodes that are not reached change nothing.  A target row without a
  * finite logit, or with a NaN or +inf one where it is softmaxed, ends the walk
  * with the last token -1.
  */

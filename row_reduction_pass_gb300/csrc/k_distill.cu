@@ -331,6 +331,9 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     d = warp_sum(d * a);
     float4* sl = slots + (j & 3) * nslot + rank * nwp + w;
     const float4 v = make_float4(M, d, w < nw ? d : 0.f, 0.f);
+    // (this row's predecessor is stored before its listed columns are: finish)
+    __threadfence_block();
+    __syncwarp();
     if constexpr (CL) {
       // lane t writes to rank t (one lane after the other took 5500 cycles a row for
       // four ranks)

@@ -210,7 +210,6 @@ __global__ void __launch_bounds__(kVerT) verify_kernel_t(const VerifyParams p) {
   if (tid == 0) p.out_count[b] = done;
 }
 
-
 // ------------------------------------------------------ a cluster a sequence ---
 //
 // Per node: rows landed -> each thread's maximum and sum over its share of both
@@ -256,7 +255,7 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);       // [2] a node's rows have landed
   uint64_t* met = full + 2;                                 // [2] the blocks' partials published
   uint64_t* noise_bar = full + 4;
-  float4* slots = reinterpret_cast<float4*>(smem + 64);     // [2][K * NW] partials
+  float4* slots = reinterpret_cast<float4*>(smem + 64);     // [3][K * NW] partials
   const int nslot = K * NW;
   int32_t* tok = reinterpret_cast<int32_t*>(smem + g.nodes_off);  // [n] -1: absent
   int32_t* par = tok + n;
@@ -332,18 +331,24 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
     if (!dead && !late) late = !mbar_wait_bounded(&full[s], (uint32_t)((loads[s] - 1) & 1), p.err);
   };
   // Puts this warp's partial into every block's slots, and waits for all of them.
-  int meets = 0;
+  // (Three sets of slots: a block that writes meeting m + 3's has met at m + 2, for
+  // which this block's working warps published after all its warps, the loading one
+  // too, had come to m + 1 and so read m's.  With two sets the loading warp, which
+  // publishes nothing, might still be reading.)
+  int meets = 0, set = 0;
   auto meet = [&](float4 v) -> const float4* {
     const int s = meets & 1;
     const uint32_t ph = (uint32_t)((meets >> 1) & 1);
+    float4* to = slots + set * nslot;
     ++meets;
+    set = set == 2 ? 0 : set + 1;
     if (works && lane < K)  // lane k writes to block k
-      st_async_f32x4(map_to_rank(slots + s * nslot + rank * NW + warp, lane),
-                     map_to_rank(&met[s], lane), v.x, v.y, v.z, v.w);
+      st_async_f32x4(map_to_rank(to + rank * NW + warp, lane), map_to_rank(&met[s], lane), v.x,
+                     v.y, v.z, v.w);
     if (tid == NT) mbar_arrive_expect_tx(&met[s], (uint32_t)(nslot * 16));
     __syncwarp();
     agree(dead || mbar_wait_bounded_cluster(&met[s], ph, p.err));
-    return slots + s * nslot;
+    return to;
   };
   auto wsum = [&](float v) {
 #pragma unroll
@@ -704,6 +709,11 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
     }
     if (ahead >= 0) wait_rows(s ^ 1);  // no copy outlives the block
     break;
+  }
+  if (dead && tid == NT) {  // nor after a wait gave up
+    for (int i = 0; i < 2; ++i)
+      if (loads[i] > 0) mbar_wait_bounded(&full[i], (uint32_t)((loads[i] - 1) & 1), p.err);
+    if (g.noise_off >= 0 && !greedy) mbar_wait_bounded(noise_bar, 0, p.err);
   }
   if (rank == 0) {
     for (int i = done + tid; i <= n; i += blockDim.x) {

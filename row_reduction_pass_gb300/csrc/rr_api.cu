@@ -1400,7 +1400,7 @@ rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
       rr::VerifyGeo t{};
       const int64_t C = round_up(cdiv(p.cols, k), 16);
       const int64_t row = round_up(C * E + 32, 128);
-      const int64_t nodes = 64 + 2 * 16 * k * (threads / 32);
+      const int64_t nodes = 64 + 3 * 16 * k * (threads / 32);
       const int64_t buf = round_up(nodes + 12 * (int64_t)p.nodes, 128);
       const int64_t noise = buf + (ahead ? 2 : 1) * 2 * row;
       const int64_t total = noise + (ahead ? round_up(C * 4 + 32, 128) : 0);
@@ -2249,9 +2249,11 @@ static rr_status tree_shape(int64_t batch, int64_t nodes, int64_t heads, int64_t
     return fail(RR_ERR_INVALID_ARG, "head_dim must be 64 or 128");
   if (heads < 1 || kv_heads < 1 || heads % kv_heads != 0)
     return fail(RR_ERR_INVALID_ARG, "heads must be a positive multiple of kv_heads");
-  if (heads > 65535 || nodes > (1 << 20) || batch > (1 << 20) ||
-      batch * nodes > ((int64_t)1 << 31) / heads)
-    return fail(RR_ERR_INVALID_ARG, "too many query rows");
+  // (rows are counted in 32 bits, with room for a tile more; every block looks
+  // through all sequences for its own work)
+  if (heads > 65535 || nodes > (1 << 20) || batch > 65536 ||
+      batch * nodes > ((int64_t)1 << 30) / heads)
+    return fail(RR_ERR_INVALID_ARG, "too many sequences or query rows");
   return RR_OK;
 }
 

@@ -374,7 +374,11 @@ def rr_attention_tree_fwd(q, k_cache, v_cache, page_table, context_len, o, lse=N
     if workspace is None:
         need = lib.rr_attention_tree_workspace_size(b, n, h, kv, d)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            if stream is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            else:  # of the stream that uses it
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
             pw = workspace.data_ptr()
     size = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if scale is None:

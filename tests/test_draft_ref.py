@@ -128,6 +128,10 @@ def test_attention_tree_argument_errors(lib):
     assert f(b=-1) == 1 and f(n=-1) == 1 and f(ps=0) == 1 and f(w=-1) == 1 and f(pages=-1) == 1
     assert f(n=257) == 1                                     # a tree of more than 256 nodes
     assert f(b=1 << 20, n=1 << 20, p=None) == 1
+    assert f(b=65537) == 1                                   # more sequences than are looked through
+    assert f(b=1, n=1 << 16, h=16385, kv=1, p=None) == 1     # 2^30 rows
+    assert f(b=65536, w=1 << 20) == 1                        # key tiles
+    assert f(ps=16, w=(1 << 26) + 1) == 1                    # positions
     for sc in (0.0, -1.0, float("nan"), float("inf")):
         assert f(sc=sc) == 1
     assert f(b=0) == 0 and f(n=0) == 0

@@ -126,6 +126,15 @@ def test_distill_student_sure_of_the_list():
     compare("dlogits", host(dl), rd, 2.0 ** -23, 1e-30, scale=dm, scale_rtol=64 * ref.EPS)
 
 
+@pytest.mark.parametrize("dtype,cols,k", [("f32", 50304, 1024), ("bf16", 50304, 1024),
+                                          ("f32", 207000, 300), ("f32", 262147, 1024),
+                                          ("bf16", 420001, 7)])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_long_rows_and_lists(cols, k, tail, dtype):
+    """Long lists beside long rows; the longest rows a cluster holds, and longer ones."""
+    check_distill(5, cols, k, dtype, tail, 2.0, k + cols)
+
+
 # ---------------------------------------------------------------- attention ---
 
 def tree_inputs(B, n, H, KV, D, lens, ps, seed, tree, spare=2):
@@ -192,12 +201,12 @@ def test_tree_attention_lengths(D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("batch,ctx", [(1, 6000), (3, 9001), (17, 900), (70, 200), (320, 60), (321, 60),
-                                       (700, 33)])
+@pytest.mark.parametrize("batch,ctx", [(1, 6000), (3, 9001), (17, 900), (70, 200), (320, 60),
+                                       (321, 60), (700, 33)])
 def test_tree_attention_split_sequences(D, batch, ctx):
     """Long contexts shared between many blocks, and more sequences than blocks."""
-    check_tree(*tree_inputs(batch, 2, 2, 1, D, [max(0, ctx - 13 * b) for b in range(batch)], 64, ctx + D,
-                            True))
+    lens = [max(0, ctx - 13 * b) for b in range(batch)]
+    check_tree(*tree_inputs(batch, 2, 2, 1, D, lens, 64, ctx + D, True))
 
 
 @pytest.mark.parametrize("D,ps", [(128, 64), (64, 128)])
@@ -309,6 +318,47 @@ def test_tree_attention_no_table_and_no_pages():
         assert (o == 0).all() and torch.isneginf(l).all()
 
 
+@pytest.mark.parametrize("ps", [5, 16, 64])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("tree", [False, True])
+def test_tree_attention_positions_beyond_the_table(ps, D, tree):
+    """Contexts and nodes that the table does not cover, up to the largest length."""
+    q, kc, vc, table, _, par = tree_inputs(4, 5, 4, 2, D, [300, 300, 300, 300], ps, ps + D, tree)
+    table = np.ascontiguousarray(table[:, :128 // ps])
+    edge = table.shape[1] * ps
+    check_tree(q, kc, vc, table, np.array([edge - 3, edge, edge + 40, 2 ** 31 - 1], np.int32), par)
+
+
+def test_tree_attention_sequences_share_pages():
+    """One table row for all (a common prefix): page indexes that stand many times."""
+    q, kc, vc, table, ctx, par = tree_inputs(3, 4, 8, 2, 128, [200, 200, 200], 16, 5, True)
+    table[:] = table[0]
+    table[:, 2] = table[:, 1]
+    check_tree(q, kc, vc, table, ctx, par)
+
+
+def test_tree_attention_odd_values_at_nodes_of_many_pieces():
+    """Infinities in V at nodes that all of a sequence's rows see, of several row tiles
+    and heads, in a batch where pipelines go on to other sequences: those rows and
+    columns become infinite, all others stay as they are."""
+    B, n, H, KV, D, ps = 40, 33, 32, 4, 64, 16
+    lens = [100 + 37 * b for b in range(B)]
+    q, kc, vc, table, ctx, par = tree_inputs(B, n, H, KV, D, lens, ps, 8, True)
+    par[:, 1:] = np.maximum(par[:, 1:], 0)          # all below node 0
+    a = run_tree(q, kc, vc, table, ctx, par)
+    hit = np.zeros(a[0].shape, bool)
+    inf = store(np.array([np.inf]), "bf16")[0]
+    for b in range(0, B, 3):
+        h, c = b % KV, 7 * b % D
+        vc[table[b, lens[b] // ps], lens[b] % ps, h, c] = inf
+        hit[b, :, h * (H // KV):(h + 1) * (H // KV), c] = True
+    for _ in range(3):
+        o, l = run_tree(q, kc, vc, table, ctx, par)
+        assert torch.equal(l, a[1])
+        assert (host(o)[~hit] == host(a[0])[~hit]).all()
+        assert np.isposinf(host(o)[hit]).all()
+
+
 def test_tree_attention_last_page_offsets_beyond_32_bits():
     """A pool of more than 2^31 elements (4.3 GB): the pages at its end."""
     D, KV, ps = 128, 8, 64
@@ -413,6 +463,23 @@ def test_verify_no_nodes_draws_from_the_target():
 
 def test_verify_large_batch():
     check_verify(*verify_inputs(700, 3, 64, "bf16", 2, 2))
+
+
+@pytest.mark.parametrize("V,dtype", [(300001, "f32"), (524287, "bf16")])
+@pytest.mark.parametrize("branch", [0, 2])
+def test_verify_rows_longer_than_a_cluster_holds(V, dtype, branch):
+    check_verify(*verify_inputs(3, 4, V, dtype, 77 + branch, branch, greedy=True), least=0.6)
+
+
+def test_verify_more_nodes_than_shared_memory_holds():
+    B, n, V = 2, 20000, 5
+    rng = np.random.default_rng(3)
+    t = rng.standard_normal((B, n + 1, V)).astype(np.float32)
+    d = t[:, :n] + np.float32(0.05) * rng.standard_normal((B, n, V)).astype(np.float32)
+    tok = rng.integers(0, V, (B, n)).astype(np.int32)
+    par = np.array([[max(-1, i // 8 - 1) for i in range(n)] for _ in range(B)], np.int32)
+    check_verify(t, d, tok, rng.random((B, n)).astype(np.float32),
+                 rng.exponential(size=(B, V)).astype(np.float32), par, None)
 
 
 def test_verify_absent_nodes_masked_and_undefined_rows():
@@ -545,6 +612,54 @@ def test_draft_score_verify_and_distil_together():
                                  value.cpu().numpy(), T=2.0)
     compare("loss", host(loss), rl, 0.0, 1e-30, scale=lm, scale_rtol=64 * ref.EPS)
     compare("dlogits", host(dl), rd, 2.0 ** -23, 1e-30, scale=dm, scale_rtol=64 * ref.EPS)
+
+
+def test_calls_on_two_streams_at_once():
+    """Each of the three on two streams that are not the current one, with workspaces of
+    their own (the binding's too): bit for bit what calls one after the other give."""
+    B, n, H, KV, D, ps, V, k = 9, 12, 16, 2, 128, 16, 30011, 20
+    sides = []
+    for seed in (1, 2):
+        q, kc, vc, table, ctx, par = tree_inputs(B, n, H, KV, D, [700 * b % 4001 for b in range(B)],
+                                                 ps, seed, True)
+        dev = lambda a: torch.from_numpy(a.view(np.int16)).view(torch.bfloat16).cuda()  # noqa: E731
+        a = [dev(q), dev(kc), dev(vc)] + [torch.from_numpy(x).cuda() for x in (table, ctx, par)]
+        g = torch.Generator("cuda").manual_seed(seed)
+        t = torch.randn(B, n + 1, V, device="cuda", generator=g)
+        d = t[:, :n] + 0.3 * torch.randn(B, n, V, device="cuda", generator=g)
+        v = [t, d.contiguous(), d.argmax(2).int(), torch.rand(B, n, device="cuda", generator=g),
+             torch.rand(B, V, device="cuda", generator=g) + 0.01]
+        idx = torch.randint(0, V, (B * n, k), dtype=torch.int32, device="cuda", generator=g)
+        val = torch.randn(B * n, k, device="cuda", generator=g)
+        sides.append((a, v, idx, val, torch.cuda.Stream()))
+
+    def outs():
+        i32 = dict(dtype=torch.int32, device="cuda")
+        return [torch.zeros(B, n, H, D, dtype=torch.bfloat16, device="cuda"),
+                torch.zeros(B, n, H, device="cuda"), torch.zeros(B, n + 1, **i32),
+                torch.zeros(B, n + 1, **i32), torch.zeros(B, **i32),
+                torch.zeros(B * n, device="cuda"), torch.zeros(B * n, V, device="cuda")]
+
+    def run(side, o, stream):
+        a, v, idx, val, _ = side
+        rr.rr_attention_tree_fwd(*a[:5], o[0], lse=o[1], parents=a[5], stream=stream)
+        rr.rr_draft_verify(*v, *o[2:5], parents=a[5], stream=stream)
+        rr.rr_distill_fwd_bwd(v[1].view(B * n, V), idx, val, o[5], o[6], stream=stream)
+
+    want = [outs(), outs()]
+    for side, o in zip(sides, want):
+        run(side, o, None)
+        torch.cuda.synchronize()
+    got = [[outs() for _ in range(8)] for _ in sides]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for side, o in zip(sides, got):
+            run(side, o[i], side[4])
+    torch.cuda.synchronize()
+    assert rr.rr_read_device_error(0) == 0
+    for w, o in zip(want, got):
+        for x in o:
+            assert all(torch.equal(p, r) for p, r in zip(w, x))
 
 
 def test_captured_calls_replay_on_new_inputs():
