@@ -887,7 +887,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0u;
           }
-          if (fix) {
+          if (__builtin_expect(fix, 0)) {
             // Adds the non-finite values of V that this row sees (rare: rolled loops over
             // a copy in this warp's rows of the Q tile, which no product reads any more and
             // no other warp writes; a function of its own made the whole kernel 5 % slower,
