@@ -404,9 +404,11 @@ rr_status rr_attention_tree_fwd(const void *q, const void *k_cache, const void *
  *           node (never accepted, its siblings are tried as if it were not there).
  *   parents : [batch x nodes] int32 as for rr_attention_tree_fwd, or NULL (a chain).
  *   uniform : [batch x nodes] float32 in [0, 1).  race : [batch x cols] float32 > 0.
- *   temperature : [batch] float32, or NULL (1).  <= 0: greedy, a child is
- *           accepted iff it is the target's largest logit (the lowest index at a
- *           tie), which is also the last token.  Otherwise finite and >= 2^-120.
+ *   temperature : [batch] float32, or NULL (1).  <= 0: greedy, p and q are all on
+ *           their row's largest logit (the lowest index at a tie).  So the first
+ *           child tried is accepted iff it is the target's largest, a later one iff
+ *           it is and the draft's largest is another; the last token is the
+ *           target's largest.  Otherwise finite and >= 2^-120.
  *   out_tokens : [batch x (nodes + 1)] int32, the accepted tokens, the last
  *           token, then -1.  out_nodes : [batch x (nodes + 1)] int32, the nodes
  *           of the accepted tokens, then -1.  out_count : [batch] int32, how many

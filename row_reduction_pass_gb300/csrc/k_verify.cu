@@ -15,6 +15,12 @@
 // given exponential noise e (of independent exponentials with rates w_j the
 // smallest is j's with probability w_j / sum w), the lowest index at a tie.
 //
+// A sequence at temperature <= 0 has p and q all on their largest logits (the lowest
+// index at a tie), and the same formulas: the first child tried is accepted iff it is
+// p's token; a rejected one leaves max(p - c q, 0) = p, or nothing if q's token is
+// p's.  So a later child is accepted iff it is p's token and q's is another, and q is
+// looked at only for such a child.
+//
 // Only the rows of visited nodes are read: the walk depends on the tokens
 // accepted so far.
 //
@@ -139,24 +145,32 @@ __global__ void __launch_bounds__(kVerT) verify_kernel_t(const VerifyParams p) {
     const char* tr = p.target + ((b * (n + 1) + cur + 1) * V) * E;
     const char* dr = p.draft + ((b * n + cur + 1) * V) * E;
     VerRow pr{}, qr{};
+    auto row_top = [&](const char* x) {
+      BestTok t{0.f, -1};
+      for (int64_t j = tid; j < V; j += kVerT) {
+        const float v = ld_elem<DT>(x + j * E);
+        if (v > -INFINITY) t.take(v, (int)j);
+      }
+      return ver_best(t, red);
+    };
     BestTok top{0.f, -1};
     if (greedy) {
-      for (int64_t j = tid; j < V; j += kVerT) {
-        const float v = ld_elem<DT>(tr + j * E);
-        if (v > -INFINITY) top.take(v, (int)j);
-      }
-      top = ver_best(top, red);
+      top = row_top(tr);
     } else {
       pr = ver_row<DT>(tr, V, c, red);
     }
     float ratio = 0.f, mass = 1.f;
-    bool have_q = false;
+    bool have_q = false, first = true;
     int next = -1;
     for (int i = cur + 1; i < n && next < 0; ++i) {
       const int32_t x = tok[i];
       if ((par != nullptr ? par[i] : i - 1) != cur || x < 0 || x >= V) continue;
       if (greedy) {
-        if (x == top.j) next = i;
+        if (x == top.j) {
+          if (!first && row_top(dr).j == top.j) break;  // nothing of the target is left
+          next = i;
+        }
+        first = false;
         continue;
       }
       if (!have_q) {
@@ -317,6 +331,16 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
     mbar_arrive_expect_tx(&full[s], tb + db);
     if (tb > 0)
       bulk_load(pbuf(s), t + c0 * E - head(t), tb, &full[s], policy_evict_first());
+    if (db > 0)
+      bulk_load(pbuf(s) + g.row_bytes, d + c0 * E - head(d), db, &full[s], policy_evict_first());
+  };
+  // brings only the draft's row of a node to buffer s
+  auto load_draft = [&](int node, int s) {
+    ++loads[s];
+    if (tid != NT || dead) return;
+    const char* d = drow(node);
+    const uint32_t db = nc > 0 ? (uint32_t)((head(d) + nc * E + 15) & ~15) : 0;
+    mbar_arrive_expect_tx(&full[s], db);
     if (db > 0)
       bulk_load(pbuf(s) + g.row_bytes, d + c0 * E - head(d), db, &full[s], policy_evict_first());
   };
@@ -493,11 +517,12 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
     wait_rows(s);
     Soft P{}, Q{};
     BestTok top{0.f, -1};
-    if (greedy) {
+    // a row's largest logit, over the cluster
+    auto row_top = [&](const unsigned char* buf, int h) {
       // a thread keeps its greatest chunk (the first of equal ones: its chunks come
       // in ascending order) and looks for the place in it at the end
-      const Parts q = parts(hp);
-      const char* row = reinterpret_cast<const char*>(pb) + hp;
+      const Parts q = parts(h);
+      const char* row = reinterpret_cast<const char*>(buf) + h;
       const uint4* base = reinterpret_cast<const uint4*>(row + q.lead * E);
       float m = -INFINITY;
       int at = -1, chunk = -1;
@@ -531,7 +556,10 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
           at = j1;
         }
       }
-      top = merge(BestTok{m, m > -INFINITY ? (int)(c0 + at) : -1});
+      return merge(BestTok{m, m > -INFINITY ? (int)(c0 + at) : -1});
+    };
+    if (greedy) {
+      top = row_top(pb, hp);
     } else {
       float mp = -INFINITY, zp = 0.f, mq = -INFINITY, zq = 0.f;
       if (works) {
@@ -590,6 +618,11 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
     for (int i = child; i >= 0 && !dead;) {
       if (greedy) {
         if (tok[i] == top.j) {
+          if (i != child) {
+            load_draft(cur, s);
+            wait_rows(s);
+            if (row_top(qb, hq).j == top.j) break;  // nothing of the target is left
+          }
           next = i;
           break;
         }

@@ -396,7 +396,8 @@ def rr_draft_verify(target_logits, draft_logits, tokens, uniform, race, out_toke
 
     target_logits [batch, nodes + 1, cols], draft_logits [batch, nodes, cols],
     tokens / parents (int32) and uniform (fp32) [batch, nodes], race [batch, cols]
-    exponential noise, temperature [batch] (<= 0: greedy).  Writes out_tokens and
+    exponential noise, temperature [batch] (<= 0: greedy, each distribution all on its
+    largest logit).  Writes out_tokens and
     out_nodes [batch, nodes + 1] and out_count [batch] (int32)."""
     torch = _torch()
     b, n1, v = target_logits.shape

@@ -171,14 +171,9 @@ def verify(target, draft, tokens, uniform, race, parents=None, temperature=None)
                 if up != cur or not 0 <= x < V:
                     continue
                 if q is None:
-                    q = softmax_row(f64(draft[b, cur + 1]), T) if T > 0 else rest
-                if T <= 0:  # accepted iff it is the one token of the target
-                    if rest[x] > 0:
-                        nxt = i
-                        break
-                    continue
+                    q = softmax_row(f64(draft[b, cur + 1]), T)
                 lhs, rhs = float(uniform[b, i]) * q[x], rest[x]
-                if max(lhs, rhs) > 0:
+                if T > 0 and max(lhs, rhs) > 0:
                     margin[b] = min(margin[b], abs(lhs - rhs) / max(p[x], q[x]))
                 if lhs < rhs:
                     nxt = i

@@ -444,6 +444,29 @@ def test_verify_greedy_and_sampled_sequences(V, branch):
     check_verify(*verify_inputs(30, 6, V, "bf16", V, branch, noise=0.2, greedy=True))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [3, 40, 1003, 50304, 300001])
+def test_verify_greedy_trees_of_siblings(V, dtype):
+    """All four ways: the target's largest logit is the first child's token, a later
+    child's or none's, and the draft's largest is the target's or another."""
+    B, n = 24 if V <= 1003 else 6, 7
+    rng = np.random.default_rng(V)
+    t, d, tok, u, e, par, _ = verify_inputs(B, n, V, dtype, V, 3)
+    for b in range(B):
+        for r in range(n + 1):
+            best = int(ref.f64(t[b, r]).argmax())
+            kids = [i for i in range(n) if par[b, i] == r - 1]
+            if not kids:
+                continue
+            tok[b, kids] = rng.choice([x for x in range(min(V, 50)) if x != best], len(kids))
+            way = rng.integers(0, 4)
+            if way < 3:
+                tok[b, kids[min(way, len(kids) - 1)]] = best
+            if rng.random() < 0.5:
+                d[b, r, best] = store(np.array([99.0]), dtype)[0]
+    check_verify(t, d, tok, u, e, par, np.zeros(B, np.float32), least=1.0)
+
+
 @pytest.mark.parametrize("n", [1, 2, 40])
 def test_verify_poor_and_perfect_drafts(n):
     """Drafts unlike the target (every child is rejected, the residual is
