@@ -228,7 +228,7 @@ struct __align__(16) DistEntry {
   int pad;
 };
 constexpr int kDistAgain = 1 << 30;
-constexpr int kDistOffSlots = 384;  // shared memory: statistics' slots on
+constexpr int kDistOffSlots = 416;  // shared memory: statistics' slots on
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
   uint64_t* ready = full + 6;                          // [2] the list is prepared
   uint64_t* done = full + 8;                           // [4] statistics merged
   DistHead* heads = reinterpret_cast<DistHead*>(smem + 96);      // [4]
-  uint4* edge = reinterpret_cast<uint4*>(smem + 288);            // [2] a row's ragged chunks
-  float4* final_ = reinterpret_cast<float4*>(smem + 320);        // [4] (M, Z, Zt) of a row
+  uint4* edges = reinterpret_cast<uint4*>(smem + 288);           // [2][2] a row's ragged chunks
+  float4* final_ = reinterpret_cast<float4*>(smem + 352);        // [4] (M, Z, Zt) of a row
   float4* slots = reinterpret_cast<float4*>(smem + kDistOffSlots);  // [4][nslot]
   DistEntry* lists = reinterpret_cast<DistEntry*>(smem + g.list_off);  // [4][k]
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + g.bits_off);     // [2][words]
@@ -628,6 +628,10 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       // neighbours become -inf in the buffer, by the chunk's only reader (the
       // proxy fence orders this before the copy that refills the buffer)
       const int nq = n > tid ? (n - tid + G - 1) / G : 0;
+      // (two rows' copies: a row's last chunk may be another thread's than that of the
+      // row before, which reads its copy when it stores its outputs; by row j + 2 every
+      // warp has published row j + 1, and so stored row j)
+      uint4* edge = edges + 2 * (j & 1);
       const bool head = tid == 0 && rank == 0 && h != 0;
       const bool end = tail_bytes != 16 && last < n && tid + (nq - 1) * G == last;
       if (head || end) {

@@ -126,6 +126,30 @@ def test_distill_student_sure_of_the_list():
     compare("dlogits", host(dl), rd, 2.0 ** -23, 1e-30, scale=dm, scale_rtol=64 * ref.EPS)
 
 
+@pytest.mark.parametrize("dtype,cols", [("bf16", 9733), ("bf16", 59183), ("f32", 19467),
+                                        ("f32", 40971), ("bf16", 118347)])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_rows_whose_last_chunk_moves(cols, tail, dtype):
+    """Rows that end in one chunk or the next, by where they begin, so that its thread
+    changes from row to row: right at every run, and the same bits."""
+    rows = 700 if cols < 50000 else 200
+    x, index, value, g = distill_inputs(rows, cols, 9, dtype, cols, tail, 2.0, hard=False)
+    xd, idx, val, gd = to_dev(x), to_dev(index).view(rows, 9), to_dev(value).view(rows, 9), to_dev(g)
+    outs = []
+    for _ in range(8):
+        loss, dl = empty_like_dev((rows,), "f32"), empty_like_dev(x.shape, dtype)
+        rr.rr_distill_fwd_bwd(xd, idx, val, loss, dl, grad=gd, temperature=2.0, tail=tail)
+        outs.append((loss, dl))
+    torch.cuda.synchronize()
+    check_guards()
+    for loss, dl in outs[1:]:
+        assert torch.equal(loss, outs[0][0]) and torch.equal(dl, outs[0][1])
+    rl, rd, lm, dm = ref.distill(x, index, value, g, 2.0, tail)
+    compare("distill loss", host(outs[0][0]), rl, 0.0, 1e-30, scale=lm, scale_rtol=64 * ref.EPS)
+    compare("distill dlogits", host(outs[0][1]), rd, 2.0 ** -8 if dtype == "bf16" else 2.0 ** -23,
+            1e-30, scale=dm, scale_rtol=64 * ref.EPS)
+
+
 @pytest.mark.parametrize("dtype,cols,k", [("f32", 50304, 1024), ("bf16", 50304, 1024),
                                           ("f32", 207000, 300), ("f32", 262147, 1024),
                                           ("bf16", 420001, 7)])
