@@ -209,6 +209,12 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
 // One list warp alone was the bottleneck: 8192 x 50304 bf16 took 265 us without
 // entries, 357 us with 64 a row, 451 us with 128 (54 rows a block).
 //
+// Bound: HBM (a row in, a row out), where a block has rows enough: 8192 x 50304 bf16
+// with 64 entries 252 us, 96 % of the copy bandwidth.  With a tail and 100 entries
+// (2048 x 50304, 13-14 rows a block) 89 us, 68 %: a row's chain of maximum, sum,
+// meeting and outputs, 4.4 us, is longer than its traffic.  In clusters the
+// meeting adds 1 us to that: 255 x 65537 fp32 33 us, 60 %.
+//
 // Bits of the listed columns of a slice, by place in the slice, tell the row
 // warps which lanes of a chunk to leave out of Zt (a byte or half a byte a
 // chunk, nearly always 0), and the list warp whether a column came twice.
@@ -369,10 +375,11 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     // ------------------------------------------------------ the merge warp
     // (A slot is written again four rows later by warps that wait for the rows
     // between, which wait for this block's row warps, which wait for this warp.)
-    // (long rows: the second is asked for when the first is there, or all blocks'
-    // first rows would come at the pace of two)
+    // (the second row is asked for when the first is there, or all blocks' first rows
+    // would come at the pace of two: 128 x 131072 bf16 21.2 -> 20.3 us; short rows the
+    // same either way)
     if (lane == 0) load_row(0);
-    if (g.S >= 2048 && row_of(0) < p.rows) dead = !mbar_wait_bounded(&full[0], 0, p.err);
+    if (row_of(0) < p.rows) dead = !mbar_wait_bounded(&full[0], 0, p.err);
     if (lane == 0) load_row(1);
     for (int64_t j = 0; row_of(j) < p.rows; ++j) {
       const uint32_t ph = (uint32_t)((j >> 2) & 1);
@@ -593,7 +600,8 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     bool open = false;  // the block's last row: listed columns still to be stored
     for (; row_of(j) < p.rows; j += 2) {
       load_logits(j + 2);
-      if (TAIL) publish(j, nw, lane == 0 ? heads[j & 3].m : -INFINITY, lane == 0 ? heads[j & 3].d : 0.f);
+      if (TAIL)
+        publish(j, nw, lane == 0 ? heads[j & 3].m : -INFINITY, lane == 0 ? heads[j & 3].d : 0.f);
       const float4 f = merged(j);
       M = f.x;
       d = f.y;

@@ -26,7 +26,7 @@
 //
 // A cluster of K blocks walks a sequence, each with a slice of the columns: the
 // slices of a node's two rows come to shared memory by bulk copies and stay there
-// for every pass over them (maximum, sum, the residual's mass after each rejection,
+// for every pass over them (maximum and sum, the residual's mass after each rejection,
 // the final draw), so a row is read from memory once.  After each pass every warp
 // puts its partial into a slot of every block of the cluster and arrives on its
 // mbarrier; every warp then merges all slots in the same order, so all threads of
@@ -34,7 +34,10 @@
 // sequences a walk is bound by latency (a row's 1.5-2 us, then about 0.6 us a
 // meeting), so the first child's rows are loaded while its parent's are worked
 // on; with many it is bound by memory, several clusters share an SM, and nothing
-// is loaded that the walk does not reach.  Rows that a cluster cannot hold go to
+// is loaded that the walk does not reach.  Measured (in a graph): one chain of 5 over
+// 50304 bf16 columns 20.4 us, 8 trees of 39 over 65537 fp32 columns 24.8 us, 256 chains
+// of 8 over 50304 93 us (the cluster's meetings and exponentials; reading the rows
+// visited takes 32).  Rows that a cluster cannot hold go to
 // a kernel of one block per sequence that reads them again for every pass.
 #include <cstdint>
 
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kVerT) verify_kernel_t(const VerifyParams p) {
 // meeting for each rejection -> next node, or the draw (a pass and a meeting).
 // Measured on one chain of 50304 bf16 columns (K = 8): first version, 256 threads
 // and an IEEE division per column in the draw, 2800 cycles for the statistics and
-// 10000 for the draw; hence the packed exponents, the chunk-wise maxima (a token
+// 10000 for the draw (29 us; now 20.4); hence the packed exponents, the chunk-wise maxima (a token
 // is only looked for in a chunk that beats the best so far), and a warp of its own
 // that issues the loads (the address arithmetic and the copies held its warp up for
 // 1300 cycles a node).
@@ -411,7 +414,8 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
   };
   // this thread's single element of the lead or the rest, -1 if none
   auto single = [&](const Parts& q) {
-    return tid < q.lead ? tid : tid >= 32 && tid - 32 < q.rest ? q.lead + q.chunks * W + tid - 32 : -1;
+    if (tid < q.lead) return tid;
+    return tid >= 32 && tid - 32 < q.rest ? q.lead + q.chunks * W + tid - 32 : -1;
   };
   // maximum, and sum about it, of this thread's share of a row
   auto stats = [&](const unsigned char* buf, int h, float& m, float& z) {

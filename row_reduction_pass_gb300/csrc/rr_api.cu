@@ -1250,9 +1250,9 @@ rr_status check_shape(int64_t rows, int64_t cols, rr_dtype dt) {
 // rounded up to whole warps, plus the list warp; a cluster of K blocks where one
 // block cannot hold the row twice, or where splitting rows over more SMs ends
 // earlier (few rows).  The cost of a shape is its rounds of rows times a row's
-// share of a block (chunks, plus 1024 for what a row costs whatever its length:
-// the statistics' meeting and, in a cluster, its distance).  False where no
-// shape holds the row.
+// share of a block in chunks, plus what a row costs whatever its length, the
+// meeting over its statistics (1024 chunks' time, in a cluster 1536).  K stays 0
+// where no shape holds the row.
 struct DistillShape {
   int K = 0, T = 0;
   int64_t grid = 0;
@@ -1378,11 +1378,12 @@ rr_status distill_launch(rr::DistillParams p, rr_dtype dt, cudaStream_t stream) 
 
 // A cluster of K blocks a sequence.  With few sequences (all their clusters on the
 // chip at once, a block per SM): the largest K, two row buffers and the noise in
-// shared memory (one chain of 50304 columns: K = 8 29 us, K = 4 38, K = 2 48; 8 trees
-// 31 us against 46).  With many: the largest K whose blocks are at most twice what
-// the chip holds at four a SM, one buffer (256 chains: K = 4 107 us, K = 2 122, K = 8
-// 445; 48 of 131072 columns: K = 8 62 us, K = 4 85).  No cluster where the slices
-// do not fit.
+// shared memory (one chain of 50304 bf16 columns: K = 8 20.4 us, 4 25, 2 36, 1 56; 8
+// trees of 65537 fp32 columns: K = 8 24.8 us, with one buffer 26.5, K = 4 34).  With
+// many: the largest K whose blocks are at most twice what the chip holds at four a SM,
+// one buffer (256 chains: K = 4 91 us, K = 8 117, with two buffers 154; 48 chains of
+// 131072 bf16 columns: K = 8 51 us, with two buffers 76, K = 4 67).  No cluster where
+// the slices do not fit.
 rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
   const rr::VerifyKernels vk = rr::verify_kernels(dt);
   const int64_t E = dt == RR_BF16 ? 2 : 4;
