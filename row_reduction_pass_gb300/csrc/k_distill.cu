@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
 //     took 1000 cycles of a row's 10300, 2200 in a cluster of three).
 //   list warp, per row j (of its parity): waits for row j's statistics, prepares
 //     row j + 2's list, writes row j's loss, and, once row j + 1 is published (every
-//     chunk of row j then stored), stores row j's listed columns.
+//     chunk of row j then stored), takes the listed columns out of row j + 2 (with a
+//     tail) and stores row j's listed columns.
 // So a block meets once a row (an mbarrier of the published statistics), the
 // two latencies of a list (its entries, then the student's logits there) are a
 // row ahead of their use, and two rows are in flight while one is worked on.
@@ -215,9 +216,10 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
 // meeting and outputs, 4.4 us, is longer than its traffic.  In clusters the
 // meeting adds 1 us to that: 255 x 65537 fp32 33 us, 60 %.
 //
-// Bits of the listed columns of a slice, by place in the slice, tell the row
-// warps which lanes of a chunk to leave out of Zt (a byte or half a byte a
-// chunk, nearly always 0), and the list warp whether a column came twice.
+// Bits of the listed columns of a slice, by place in the slice, tell the list warp
+// whether a column came twice.  (They also told the row warps which lanes to leave out
+// of Zt, a byte a chunk: 8192 x 50304 bf16 with a tail and 100
+// entries 372 us, and 299 us since the list warp takes them out of the landed row.)
 struct __align__(16) DistHead {
   float g;        // upstream gradient times T
   float tn;       // t_k = tn * (the entries' t)
@@ -245,20 +247,6 @@ __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
   return v;
-}
-
-// The lanes of a chunk whose bit is set become -inf.
-template <int DT>
-__device__ __forceinline__ uint4 dist_take_out(uint4 c, uint32_t b) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t m = DT == kBF16 ? ((b >> (2 * i)) & 1 ? 0xffffu : 0u) |
-                                         ((b >> (2 * i + 1)) & 1 ? 0xffff0000u : 0u)
-                                   : ((b >> i) & 1 ? 0xffffffffu : 0u);
-    w[i] = (word_of(c, i) & ~m) | ((DT == kBF16 ? 0xff80ff80u : 0xff800000u) & m);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // The lanes of a chunk outside bytes [lo, hi) become -inf.
@@ -542,6 +530,23 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         heads[j & 3] = hd;
       }
       __syncwarp();
+      if (!TAIL && lane == 0) mbar_arrive(&ready[j & 1]);
+    };
+    // With a tail: the listed columns of row j become -inf where it has landed, so that
+    // the row warps' sum is that of the unlisted ones.
+    auto take_out = [&](int64_t j) {
+      if (!TAIL || row_of(j) >= p.rows) return;
+      if (!dead) dead = !mbar_wait_bounded(&full[j & 1], (uint32_t)((j >> 1) & 1), p.err);
+      const DistEntry* li = lists + (j & 3) * k;
+      char* buf = reinterpret_cast<char*>(smem + g.buf_off + (j & 1) * g.S * 16);
+      for (int i = lane; i < k; i += 32)
+        if (li[i].place >= 0) {
+          char* at = buf + (li[i].place & (kDistAgain - 1)) * E;
+          if constexpr (DT == kBF16) *reinterpret_cast<unsigned short*>(at) = 0xff80u;
+          else *reinterpret_cast<float*>(at) = -INFINITY;
+        }
+      fence_proxy_async_smem();  // (before the copy that refills the buffer)
+      __syncwarp();
       if (lane == 0) mbar_arrive(&ready[j & 1]);
     };
     auto clear_bits = [&](int64_t j) {
@@ -595,6 +600,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     load_entries(j, 0);
     load_logits(j);
     prepare(j);
+    take_out(j);
     load_entries(j + 2, 0);
     float M = 0.f, d = 0.f, dt = 0.f;
     bool open = false;  // the block's last row: listed columns still to be stored
@@ -613,6 +619,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       open = row_of(j + 1) >= p.rows;
       if (!open) {
         merged(j + 1);
+        take_out(j + 2);
         finish(j, M, d, dt);
       }
     }
@@ -630,8 +637,8 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       const int tail_bytes = (int)(h + rowb - 16 * (nch - 1));
       const uint32_t ph = (uint32_t)((j >> 1) & 1);
       uint4* buf = reinterpret_cast<uint4*>(smem + g.buf_off + (j & 1) * g.S * 16);
-      const unsigned char* bm = reinterpret_cast<const unsigned char*>(bits + (j & 1) * g.words);
       if (!dead) dead = !mbar_wait_bounded(&full[j & 1], ph, p.err);
+      if (!dead) dead = !mbar_wait_bounded(&ready[j & 1], ph, p.err);
       // the lanes of the row's first and last chunk that belong to its
       // neighbours become -inf in the buffer, by the chunk's only reader (the
       // proxy fence orders this before the copy that refills the buffer)
@@ -649,19 +656,12 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         if (end) edge[1] = buf[last];
         fence_proxy_async_smem();
       }
-      if (!dead) dead = !mbar_wait_bounded(&ready[j & 1], ph, p.err);
       uint4 v[NQ];
       float m = -INFINITY;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         if (q >= nq) break;
         v[q] = buf[tid + q * G];
-        if (TAIL) {  // listed lanes become -inf: the list warp counts them
-          const int c = tid + q * G;
-          uint32_t b = bm[W == 8 ? c : c >> 1];
-          if (W == 4) b = (c & 1) ? b >> 4 : b & 15u;
-          if (b != 0) v[q] = dist_take_out<DT>(v[q], b);
-        }
         if constexpr (DT == kBF16) {
           const uint32_t w = bf16x2_max(bf16x2_max(v[q].x, v[q].y), bf16x2_max(v[q].z, v[q].w));
           m = fmaxf(m, fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
