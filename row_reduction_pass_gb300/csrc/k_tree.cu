@@ -361,8 +361,14 @@ __device__ __forceinline__ bool odd_bf16x2(uint32_t w) {  // an infinity or NaN 
 
 // The workspace: two pieces a pipeline (its run's first and last), a piece being
 // [D / 4][rows] 16-byte chunks of the output (so that the rows of a warp write, and
-// the joining threads read, whole lines), and behind them the pieces' [rows]
-// (maximum, sum).
+// the joining threads read, whole lines), behind them the pieces' [rows] (maximum,
+// sum), and behind those the plan: its share, whether the runs are items' own, and
+// the units before each sequence.
+template <int D>
+__device__ __forceinline__ int32_t* tree_ws_plan(const TreeParams& p, const TreeGeo& g) {
+  const int64_t rows = min(p.nodes * g.G, kTM);
+  return reinterpret_cast<int32_t*>(p.ws + (int64_t)g.max_slots * 2 * rows * (D + 2));
+}
 template <int D>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -466,6 +472,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     for (int b = b0; b < b1; ++b) mine += tree_tiles<BN>(p, g, tree_context(p, g, b)) * g.KM;
     const int at = tree_scan(mine, scratch, &total);
     const int share = max(tree_cdiv(total, g.groups), g.min_tiles);
+    if (blockIdx.x == 0) {  // the plan, for the join
+      int32_t* plan = tree_ws_plan<D>(p, g);
+      if (tid == 0) plan[0] = share, plan[1] = 0;
+      int before = at;
+      for (int b = b0; b < b1; ++b) {
+        plan[2 + b] = before;
+        before += tree_tiles<BN>(p, g, tree_context(p, g, b)) * g.KM;
+      }
+    }
     for (int s = 0; s < 2; ++s) {
       const int gs = (slot0 + s) / g.side;
       const int64_t start = (int64_t)gs * share;
@@ -955,6 +970,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
   }
 
+  // The plan, for the join (whose blocks would each make it again: 46 us of large trees'
+  // 240), by a warp that has loaded all its keys.
+  if (p.batch <= kTreeWarpSeqs && blockIdx.x == 0 && warp == 12) {
+    int32_t* out = tree_ws_plan<D>(p, g);
+    const TreePlan plan = tree_plan<BN>(p, g);
+    if (lane == 0) out[0] = plan.share, out[1] = plan.own;
+    int base = 0;
+#pragma unroll 1
+    for (int b = lane; b - lane < (int)p.batch; b += 32) {
+      const int v = tree_units<BN>(p, g, plan, b);
+      int x = v;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+      }
+      if (b < (int)p.batch) out[2 + b] = base + x - v;
+      base += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+
   tc_fence_before();
   __syncthreads();
   if (warp == 0)
@@ -969,47 +1005,10 @@ constexpr int kJoinT = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, const TreeGeo g) {
   constexpr int BN = TreePL<D>::BN, U = 8;  // pieces loaded at once
-  __shared__ int scratch[16], s_before;
   const int tid = threadIdx.x;
   // block (x, z): item x of all, pipeline z of its group
   const int b = (int)blockIdx.x / g.KM, hm = (int)blockIdx.x - b * g.KM;
   const int tiles = tree_tiles<BN>(p, g, tree_context(p, g, b));
-  // the item's first run, the runs that hold a piece of it, the first one's piece
-  int run0 = 0, n = 0, skip = 0;
-  if (p.batch <= kTreeWarpSeqs) {
-    const TreePlan plan = tree_plan<BN>(p, g);
-    int mine = 0;  // units before this sequence
-#pragma unroll 1
-    for (int i = tid & 31; i < b; i += 32) mine += tree_units<BN>(p, g, plan, i);
-    const int before = warp_isum(mine);
-    if (tiles > 0 && plan.own) {
-      n = tree_cdiv(tiles, plan.share);
-      run0 = before + hm * n;
-    } else if (tiles > 0) {
-      const int start = before + hm * tiles;
-      run0 = start / plan.share;
-      n = (start + tiles - 1) / plan.share - run0 + 1;
-      skip = run0 * plan.share < start;
-    }
-  } else {
-    const int batch = (int)p.batch, per = (batch + kJoinT - 1) / kJoinT;
-    const int b0 = tid * per, b1 = min(b0 + per, batch);
-    int mine = 0, total;
-    for (int i = b0; i < b1; ++i) mine += tree_tiles<BN>(p, g, tree_context(p, g, i)) * g.KM;
-    int at = tree_scan(mine, scratch, &total);
-    if (b >= b0 && b < b1) {
-      for (int i = b0; i < b; ++i) at += tree_tiles<BN>(p, g, tree_context(p, g, i)) * g.KM;
-      s_before = at;
-    }
-    __syncthreads();
-    if (tiles > 0) {
-      const int share = max(tree_cdiv(total, g.groups), g.min_tiles);
-      const int start = s_before + hm * tiles;
-      run0 = start / share;
-      n = (start + tiles - 1) / share - run0 + 1;
-      skip = run0 * share < start;
-    }
-  }
   const int all_rows = p.nodes * g.G, ws_rows = min(all_rows, kTM);
   const int flat = (int)blockIdx.y * kJoinT + tid;  // of the piece's chunks
   const int chunk = flat / ws_rows, row = flat - chunk * ws_rows;
@@ -1020,6 +1019,21 @@ __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, c
   // Launched while the pieces are still being computed: every block waits for
   // them here, also one without work, so that this grid ends after that one.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the item's first run, the runs that hold a piece of it, the first one's piece
+  int run0 = 0, n = 0, skip = 0;
+  if (tiles > 0) {
+    const int32_t* plan = tree_ws_plan<D>(p, g);
+    const int share = plan[0], before = plan[2 + b];
+    if (plan[1]) {
+      n = tree_cdiv(tiles, share);
+      run0 = before + hm * n;
+    } else {
+      const int start = before + hm * tiles;
+      run0 = start / share;
+      n = (start + tiles - 1) / share - run0 + 1;
+      skip = run0 * share < start;
+    }
+  }
   if (n == 1) return;  // finished by its run
   if (chunk >= D / 4 || R >= all_rows) return;
   const float4* ws_o = reinterpret_cast<const float4*>(p.ws);
@@ -1141,9 +1155,9 @@ const char* tree_tc_launch(const TreeParams& p, int d, int sms, cudaStream_t str
   return nullptr;
 }
 
-size_t tree_ws_bytes(int64_t nodes, int heads, int kv_heads, int d, int sms) {
+size_t tree_ws_bytes(int64_t batch, int64_t nodes, int heads, int kv_heads, int d, int sms) {
   const int64_t rows = std::min<int64_t>(nodes * (heads / kv_heads), kTM);
-  return (size_t)(2 * sms) * 2 * rows * (d + 2) * sizeof(float);
+  return ((size_t)(2 * sms) * 2 * rows * (d + 2) + 2 + batch) * sizeof(float);
 }
 
 }  // namespace rr

@@ -2265,7 +2265,7 @@ size_t rr_attention_tree_workspace_size(int64_t batch, int64_t nodes, int64_t he
   std::lock_guard<std::mutex> lock(g_mu);
   DevInfo* di = nullptr;
   if (device_info(&di) != RR_OK) return 0;
-  return rr::tree_ws_bytes(nodes, (int)heads, (int)kv_heads, (int)head_dim, di->sms);
+  return rr::tree_ws_bytes(batch, nodes, (int)heads, (int)kv_heads, (int)head_dim, di->sms);
 }
 
 rr_status rr_attention_tree_fwd(const void* q, const void* k_cache, const void* v_cache,

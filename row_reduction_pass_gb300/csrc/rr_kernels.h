@@ -315,7 +315,7 @@ TreeKernels tree_kernels(int d);
 // Encodes the tensor maps and launches the two kernels (`sms` blocks): null on
 // success, else a short reason.
 const char* tree_tc_launch(const TreeParams& p, int d, int sms, cudaStream_t stream);
-size_t tree_ws_bytes(int64_t nodes, int heads, int kv_heads, int d, int sms);
+size_t tree_ws_bytes(int64_t batch, int64_t nodes, int heads, int kv_heads, int d, int sms);
 
 // The column reduce's split of its 32 warps over the P partial rows: the
 // smallest power of two >= P / 16, at most 32 (the rest of the warps take
