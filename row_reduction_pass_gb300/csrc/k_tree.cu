@@ -32,13 +32,14 @@
 //
 // Measured (in a graph): 64 sequences of 500-8000 keys, one token, 32 heads over 8 of
 // 128: 172 us, 95 % of the copy bandwidth; one such sequence of 4001: 14.4 us, a
-// piece's latency and the join's; 8 trees of 62 nodes, 64 heads over 8, over 12000-20000
-// keys: 240 us, 53 % of the bf16 rate (k_attn.cu's 54 % on long causal heads): the
-// pipelines' tiles follow one another every 1570 cycles, of which the softmax works
-// 1250, and the issuers of S and P V are held 870 and 480 by the tensor pipe's queue.
-// Tried and slower there: half of Q in TMEM for less shared memory traffic (239 -> 242
-// us), Q copied asynchronously and O written in whole lines (240 -> 246 us; a
-// pipeline's prologue and epilogue are the other's tiles' time).
+// piece's latency and the join's; 16 trees of 30 nodes, 16 heads over 4 of 64, over
+// 1000-4100 keys 24.4 us, the same; 8 trees of 62 nodes, 64 heads over 8, over
+// 12000-20000 keys 229 us, 56 % of the bf16 rate (k_attn.cu's 54 % on long causal
+// heads): the pipelines' tiles follow one another every 1570 cycles, of which the
+// softmax works 1250, and the issuers of S and P V are held 870 and 480 by the tensor
+// pipe's queue.  Tried and slower there: half of Q in TMEM for less shared memory
+// traffic (239 -> 242 us), Q copied asynchronously and O written in whole lines (240 ->
+// 246 us; a pipeline's prologue and epilogue are the other's tiles' time).
 //
 // Page sizes that are not a multiple of 16 go to a kernel of one warp per query
 // row.
@@ -970,8 +971,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
   }
 
-  // The plan, for the join (whose blocks would each make it again: 46 us of large trees'
-  // 240), by a warp that has loaded all its keys.
+  // The plan, for the join (whose blocks each made it again: large trees 240 -> 229 us),
+  // by a warp that has loaded all its keys.
   if (p.batch <= kTreeWarpSeqs && blockIdx.x == 0 && warp == 12) {
     int32_t* out = tree_ws_plan<D>(p, g);
     const TreePlan plan = tree_plan<BN>(p, g);
@@ -998,13 +999,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                  : "memory");
 }
 
-// Joins the pieces of items cut by runs, and writes the rows of sequences that
+// Joins the pieces of items cut by runs (the plan says which), and writes the rows of sequences that
 // have no tile at all.  A thread takes one 16-byte chunk of one row, over all
 // pieces.
 constexpr int kJoinT = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, const TreeGeo g) {
-  constexpr int BN = TreePL<D>::BN, U = 8;  // pieces loaded at once
+  constexpr int BN = TreePL<D>::BN;
   const int tid = threadIdx.x;
   // block (x, z): item x of all, pipeline z of its group
   const int b = (int)blockIdx.x / g.KM, hm = (int)blockIdx.x - b * g.KM;
@@ -1043,7 +1044,10 @@ __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, c
   auto part = [&](int i) { return 2 * ((run0 + i) * g.side + sub) + (i == 0 ? skip : 0); };
   float M = -INFINITY, L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += U) {
+  // pieces loaded at once: 8, or 2 where there are no more (an unused place costs as
+  // much as a used one: large trees 232 -> 229 us)
+  auto add = [&](auto at_once, int i0) {
+    constexpr int U = decltype(at_once)::value;
     float2 ml[U];
     float4 x[U];
     float mx = M;
@@ -1071,7 +1075,10 @@ __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, c
       o = make_float4(fmaf(x[i].x, a, o.x), fmaf(x[i].y, a, o.y), fmaf(x[i].z, a, o.z),
                       fmaf(x[i].w, a, o.w));
     }
-  }
+  };
+  if (n == 2) add(std::integral_constant<int, 2>{}, 0);
+  else
+    for (int i0 = 0; i0 < n; i0 += 8) add(std::integral_constant<int, 8>{}, i0);
   const float inv = L == 0.f ? 0.f : 1.f / L;
   *reinterpret_cast<uint2*>(p.o + (out * D + 4 * chunk) * 2) =
       make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));

@@ -302,7 +302,8 @@ struct TreeGeo {
   int32_t max_slots;  // pipelines
 };
 // fewest key tiles a pipeline takes: a shorter run would cost more in its
-// piece's trip through the workspace than it saves
+// piece's trip through the workspace than it saves (one token over 4001 keys of 8 key
+// heads: 4 tiles 14.4 us, 3 15.3, 2 15.1; 16 trees of 30 nodes the same within 1 %)
 constexpr int kTreeMinTiles = 4;
 struct TreeKernels {
   const void* main;
