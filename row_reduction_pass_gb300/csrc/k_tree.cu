@@ -999,9 +999,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                  : "memory");
 }
 
-// Joins the pieces of items cut by runs (the plan says which), and writes the rows of sequences that
-// have no tile at all.  A thread takes one 16-byte chunk of one row, over all
-// pieces.
+// Joins the pieces of items cut by runs (the plan says which), and writes the rows
+// of sequences that have no tile at all.  A thread takes one 16-byte chunk of one
+// row, over all pieces.
 constexpr int kJoinT = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, const TreeGeo g) {
