@@ -35,8 +35,8 @@
 // meeting), so the first child's rows are loaded while its parent's are worked
 // on; with many it is bound by memory, several clusters share an SM, and nothing
 // is loaded that the walk does not reach.  Measured (in a graph): one chain of 5 over
-// 50304 bf16 columns 20.4 us, 8 trees of 39 over 65537 fp32 columns 24.8 us, 256 chains
-// of 8 over 50304 93 us (the cluster's meetings and exponentials; reading the rows
+// 50304 bf16 columns 19.6 us, 8 trees of 39 over 65537 fp32 columns 24.7 us, 256 chains
+// of 8 over 50304 88 us (the cluster's meetings and exponentials; reading the rows
 // visited takes 32).  Rows that a cluster cannot hold go to
 // a kernel of one block per sequence that reads them again for every pass.
 #include <cstdint>
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kVerT) verify_kernel_t(const VerifyParams p) {
 // meeting for each rejection -> next node, or the draw (a pass and a meeting).
 // Measured on one chain of 50304 bf16 columns (K = 8): first version, 256 threads
 // and an IEEE division per column in the draw, 2800 cycles for the statistics and
-// 10000 for the draw (29 us; now 20.4); hence the packed exponents, the chunk-wise maxima (a token
+// 10000 for the draw (29 us; now 19.6); hence the packed exponents, the chunk-wise maxima (a token
 // is only looked for in a chunk that beats the best so far), and a warp of its own
 // that issues the loads (the address arithmetic and the copies held its warp up for
 // 1300 cycles a node).
@@ -638,6 +638,8 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
           break;
         }
         ratio += mass;
+        // (W is asked for only by another child; whether it is 0 the draw tells)
+        if (next_child(cur, i + 1) < 0) break;
         float w = 0.f;
         if (!works) {
         } else if (hp == hq) {
@@ -698,51 +700,55 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
         agree(mbar_wait_bounded(noise_bar, 0, p.err));
         ns = reinterpret_cast<const float*>(smem + g.noise_off + nh);
       }
-      BestTok best{0.f, -1};
       auto score = [&](float w, float e) { return w > 0.f ? __fdividef(w, e) : -1.f; };
-      if (!works) {
-      } else if (ratio == 0.f || hp == hq) {
-        const Parts q = parts(hp);
-        const uint4* pv = reinterpret_cast<const uint4*>(pb + hp + q.lead * E);
-        const uint4* qv = reinterpret_cast<const uint4*>(qb + hq + q.lead * E);
-        const bool whole = ((nh + q.lead * 4) & 15) == 0;
-        const uint32_t ni = DT == kBF16 ? 0xff80ff80u : 0xff800000u;
 #pragma unroll 1
-        for (int k = tid; k < q.chunks; k += NT) {
-          const int j = q.lead + k * W;
-          float e8[W];
-          if (whole) {
+      for (;; ratio = 0.f) {  // from the residual; from p where it holds nothing
+        BestTok best{0.f, -1};
+        if (!works) {
+        } else if (ratio == 0.f || hp == hq) {
+          const Parts q = parts(hp);
+          const uint4* pv = reinterpret_cast<const uint4*>(pb + hp + q.lead * E);
+          const uint4* qv = reinterpret_cast<const uint4*>(qb + hq + q.lead * E);
+          const bool whole = ((nh + q.lead * 4) & 15) == 0;
+          const uint32_t ni = DT == kBF16 ? 0xff80ff80u : 0xff800000u;
+#pragma unroll 1
+          for (int k = tid; k < q.chunks; k += NT) {
+            const int j = q.lead + k * W;
+            float e8[W];
+            if (whole) {
 #pragma unroll
-            for (int e = 0; e < W; e += 4) {
-              const float4 t = *reinterpret_cast<const float4*>(ns + j + e);
-              e8[e] = t.x, e8[e + 1] = t.y, e8[e + 2] = t.z, e8[e + 3] = t.w;
+              for (int e = 0; e < W; e += 4) {
+                const float4 t = *reinterpret_cast<const float4*>(ns + j + e);
+                e8[e] = t.x, e8[e + 1] = t.y, e8[e + 2] = t.z, e8[e + 3] = t.w;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < W; ++e) e8[e] = ns[j + e];
             }
-          } else {
+            float r[W];
+            residual(pv[k], ratio > 0.f ? qv[k] : make_uint4(ni, ni, ni, ni), r);
 #pragma unroll
-            for (int e = 0; e < W; ++e) e8[e] = ns[j + e];
+            for (int e = 0; e < W; ++e) r[e] = score(r[e], e8[e]);
+            best_chunk<W>(best, r, (int)c0 + j);
           }
-          float r[W];
-          residual(pv[k], ratio > 0.f ? qv[k] : make_uint4(ni, ni, ni, ni), r);
-#pragma unroll
-          for (int e = 0; e < W; ++e) r[e] = score(r[e], e8[e]);
-          best_chunk<W>(best, r, (int)c0 + j);
-        }
-        const int j = single(q);
-        if (j >= 0) {
-          const float sc = score(residual1(j), ns[j]);
-          if (sc >= 0.f) best.take(sc, (int)c0 + j);
-        }
-      } else {
+          const int j = single(q);
+          if (j >= 0) {
+            const float sc = score(residual1(j), ns[j]);
+            if (sc >= 0.f) best.take(sc, (int)c0 + j);
+          }
+        } else {
 #pragma unroll 4
-        for (int j = tid; j < nc; j += NT) {
-          const float sc = score(residual1(j), ns[j]);
-          if (best.j < 0 ? sc >= 0.f : sc > best.s) {
-            best.s = sc;
-            best.j = (int)c0 + j;
+          for (int j = tid; j < nc; j += NT) {
+            const float sc = score(residual1(j), ns[j]);
+            if (best.j < 0 ? sc >= 0.f : sc > best.s) {
+              best.s = sc;
+              best.j = (int)c0 + j;
+            }
           }
         }
+        token = merge(best).j;
+        if (token >= 0 || ratio == 0.f) break;
       }
-      token = merge(best).j;
     }
     if (ahead >= 0) wait_rows(s ^ 1);  // no copy outlives the block
     break;
