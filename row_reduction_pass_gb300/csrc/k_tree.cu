@@ -1001,7 +1001,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
 // Joins the pieces of items cut by runs (the plan says which), and writes the rows
 // of sequences that have no tile at all.  A thread takes one 16-byte chunk of one
-// row, over all pieces.
+// row, over all pieces (eight threads, each some of the pieces: one token 14.4 -> 14.0
+// us, but 16 trees of 30 nodes 24.3 -> 24.8).
 constexpr int kJoinT = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinT) tree_join_kernel(const TreeParams p, const TreeGeo g) {
