@@ -8,9 +8,17 @@
 //   dx_j    = g T [ M s_j - [j unlisted] tt e_j / Zt - sum_{k: i_k = j} t_k ]
 // e_j = exp((x_j - max) / T), Z = sum e, Zt = its part over unlisted columns,
 // tt = the teacher's mass outside the list (0 when the list is renormalised),
-// M = sum t + tt.  Zt is summed over the unlisted columns themselves: Z less
-// the listed terms would lose every digit when the list holds nearly all of
-// the student's mass.
+// M = sum t + tt.  The student's mass is summed in two parts, Zt over the unlisted
+// and Zl over the listed columns, and Z = Zt + Zl, so that neither part is the
+// difference of two sums: Z - Zl loses every digit of Zt where the list holds nearly
+// all of the mass, and where it holds little (a list of 4 of 131072 columns at T = 4:
+// 6e-4 of it) ln tt and ln(Zt / Z), both near 0, are the logarithms of numbers near 1
+// whose rounding, 2^-24, is a thousandth of them, and they nearly cancel against the
+// list's terms.  So
+//   ln tt = log1p(-sum t),   ln(Zt / Z) = log1p(-Zl / Z) where Zl < Z / 2,
+//   M s_j - tt e_j / Zt = (e_j / Z) (sum t - tt Zl / Zt)   at an unlisted column
+// (M Zt - tt Z = sum t Zt - tt Zl).  By the first forms the loss was off by up to 1e-3
+// there (2-norm over the rows), by these 7e-6.
 //
 // A bit filter of up to 2^16 bits in shared memory holds (column mod its size)
 // of the listed columns; a column whose bit is clear is unlisted, one whose bit
@@ -46,6 +54,12 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   v = red[0];
   for (int i = 1; i < (int)(blockDim.x >> 5); ++i) v += red[i];
   return v;
+}
+
+// The tail's part of the loss, tt (ln tt - ln(Zt / Z)), with tt = 1 - st > 0.
+__device__ __forceinline__ float tail_loss(float st, float tt, float Z, float Zt, float Zl) {
+  const float lns = Zl < 0.5f * Z ? log1pf(-Zl / Z) : logf(Zt / Z);
+  return tt * (log1pf(-st) - lns);
 }
 
 // One block per row, single-element accesses: any alignment, any length.
@@ -91,7 +105,7 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
     vm = block_max(vm, red);
     const bool live = any && (p.tail || vm != -INFINITY);
     // the row's maximum and sums (online, per thread, then merged)
-    float m = -INFINITY, d = 0.f, dt = 0.f;
+    float m = -INFINITY, d = 0.f, dt = 0.f, dl = 0.f;  // d: no tail
     if (live) {
       for (int64_t j = tid; j < p.cols; j += kDistT) {
         const float v = ld_elem<DT>(x + j * E);
@@ -99,25 +113,29 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
           const float a = ex2((m - v) * p.c);
           d *= a;
           dt *= a;
+          dl *= a;
           m = v;
         }
         const float e = v == -INFINITY ? 0.f : ex2((v - m) * p.c);
-        d += e;
-        if (p.tail) {
+        if (!p.tail) {
+          d += e;
+        } else {
           const uint32_t b = (uint32_t)j & fmask;
           bool listed = (filter[b >> 5] >> (b & 31)) & 1;
           if (listed && p.filter_bits < p.cols) {
             listed = false;
             for (int i = 0; i < p.k; ++i) listed = listed || tidx[i] == (int)j;
           }
-          if (!listed) dt += e;
+          if (listed) dl += e;
+          else dt += e;
         }
       }
     }
     const float M = block_max(m, red);
     const float a = m == -INFINITY ? 0.f : ex2((m - M) * p.c);
-    const float Z = block_sum(d * a, red);
     const float Zt = p.tail ? block_sum(dt * a, red) : 0.f;
+    const float Zl = p.tail ? block_sum(dl * a, red) : 0.f;
+    const float Z = p.tail ? Zt + Zl : block_sum(d * a, red);
     const float g = p.temperature * (p.grad != nullptr ? p.grad[r] : 1.f);
     if (!live || M == -INFINITY) {  // no teacher, or nothing to learn from: zeros
       if (tid == 0) p.loss[r] = 0.f;
@@ -149,15 +167,16 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
         st = block_sum(st, red);
         tt = Zt > 0.f ? fmaxf(1.f - st, 0.f) : 0.f;
         mass = st + tt;
-        if (tt > 0.f) l += tt * (logf(tt) - (logf(Zt) - lnZ));
+        if (tt > 0.f) l += tail_loss(st, tt, Z, Zt, Zl);
       }
       if (tid == 0) p.loss[r] = p.temperature * p.temperature * l;
       if (y != nullptr) {
-        const float A = g * (mass / Z), B = tt > 0.f ? g * (tt / Zt) : 0.f;
+        const float A = g * (mass / Z);                                  // listed
+        const float U = p.tail ? g * ((st - (tt > 0.f ? tt * (Zl / Zt) : 0.f)) / Z) : A;
         for (int64_t j = tid; j < p.cols; j += kDistT) {
           const float v = ld_elem<DT>(x + j * E);
           const float e = v == -INFINITY ? 0.f : ex2((v - M) * p.c);
-          st_elem<DT>(y + j * E, e * (A - B));
+          st_elem<DT>(y + j * E, e * U);
         }
         __syncthreads();
         for (int i = tid; i < p.k; i += kDistT) {
@@ -279,7 +298,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
   uint64_t* done = full + 8;                           // [4] statistics merged
   DistHead* heads = reinterpret_cast<DistHead*>(smem + 96);      // [4]
   uint4* edges = reinterpret_cast<uint4*>(smem + 288);           // [2][2] a row's ragged chunks
-  float4* final_ = reinterpret_cast<float4*>(smem + 352);        // [4] (M, Z, Zt) of a row
+  float4* final_ = reinterpret_cast<float4*>(smem + 352);        // [4] (M, Z, Zt, Zl) of a row
   float4* slots = reinterpret_cast<float4*>(smem + kDistOffSlots);  // [4][nslot]
   DistEntry* lists = reinterpret_cast<DistEntry*>(smem + g.list_off);  // [4][k]
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + g.bits_off);     // [2][words]
@@ -324,7 +343,8 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     const float a = m == -INFINITY ? 0.f : ex2((m - M) * p.c);
     d = warp_sum(d * a);
     float4* sl = slots + (j & 3) * nslot + rank * nwp + w;
-    const float4 v = make_float4(M, d, w < nw ? d : 0.f, 0.f);
+    // (maximum, sum; with a tail the sum of unlisted, of listed columns)
+    const float4 v = make_float4(M, w < nw ? d : 0.f, w < nw ? 0.f : d, 0.f);
     // (this row's predecessor is stored before its listed columns are: finish)
     __threadfence_block();
     __syncwarp();
@@ -378,22 +398,31 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       }
       if (lane == 0) load_row(j + 2);  // every row warp has taken its chunks of row j
       const float4* sl = slots + (j & 3) * nslot;
-      float M = -INFINITY, d = 0.f, dt = 0.f;
+      float M = -INFINITY, d = 0.f, dt = 0.f, dl = 0.f;
       for (int i = lane; i < nslot; i += 32) M = fmaxf(M, sl[i].x);
       M = warp_max(M);
       for (int i = lane; i < nslot; i += 32) {
         const float4 t = sl[i];
         const float a = t.x == -INFINITY ? 0.f : ex2((t.x - M) * p.c);
-        d += t.y * a;
-        if (TAIL) dt += t.z * a;
+        if (!TAIL) {
+          d += t.y * a;
+        } else {
+          dt += t.y * a;
+          dl += t.z * a;
+        }
       }
 #pragma unroll
       for (int off = 16; off >= 1; off >>= 1) {
-        d += __shfl_xor_sync(0xffffffffu, d, off);
-        if (TAIL) dt += __shfl_xor_sync(0xffffffffu, dt, off);
+        if (!TAIL) {
+          d += __shfl_xor_sync(0xffffffffu, d, off);
+        } else {
+          dt += __shfl_xor_sync(0xffffffffu, dt, off);
+          dl += __shfl_xor_sync(0xffffffffu, dl, off);
+        }
       }
+      if (TAIL) d = dt + dl;
       if (lane == 0) {
-        final_[j & 3] = make_float4(M, d, dt, 0.f);
+        final_[j & 3] = make_float4(M, d, dt, dl);
         mbar_arrive(&done[j & 3]);
       }
       __syncwarp();
@@ -579,7 +608,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     // The loss: a0 plus st times the distance of ref from the row's logarithm of Z,
     // two numbers of some tens whose sum is small, hence in double (a few
     // operations a row).
-    auto write_loss = [&](int64_t j, float M, float d, float dt) {
+    auto write_loss = [&](int64_t j, float M, float d, float dt, float dl) {
       const DistHead hd = heads[j & 3];
       float l = 0.f;
       if (hd.live && M != -INFINITY) {
@@ -587,11 +616,11 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         const double lnz = (double)ez * 0.69314718055994531 +
                            (double)logf(__int_as_float(__float_as_int(d) - (ez << 23)));
         const double inv_t = (double)p.inv_t + (double)p.inv_t_lo;
-        l = (float)(hd.a0 + (double)hd.st * (((double)M - (double)hd.ref) * inv_t + lnz));
+        double s = hd.a0 + (double)hd.st * (((double)M - (double)hd.ref) * inv_t + lnz);
         float mass, tt;
         masses(hd, dt, mass, tt);
-        if (tt > 0.f) l += tt * (logf(tt) - logf(dt / d));
-        l *= p.temperature * p.temperature;
+        if (tt > 0.f) s += tail_loss(hd.st, tt, d, dt, dl);
+        l = (float)s * (p.temperature * p.temperature);
         if (d != d) l = d;
       }
       if (lane == 0) p.loss[row_of(j)] = l;
@@ -602,7 +631,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     prepare(j);
     take_out(j);
     load_entries(j + 2, 0);
-    float M = 0.f, d = 0.f, dt = 0.f;
+    float M = 0.f, d = 0.f, dt = 0.f, dl = 0.f;
     bool open = false;  // the block's last row: listed columns still to be stored
     for (; row_of(j) < p.rows; j += 2) {
       load_logits(j + 2);
@@ -612,10 +641,11 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       M = f.x;
       d = f.y;
       dt = f.z;
+      dl = f.w;
       clear_bits(j);
       prepare(j + 2);
       load_entries(j + 4, 0);
-      if (rank == 0) write_loss(j, M, d, dt);
+      if (rank == 0) write_loss(j, M, d, dt, dl);
       open = row_of(j + 1) >= p.rows;
       if (!open) {
         merged(j + 1);
@@ -689,7 +719,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       }
       publish(j, warp, m, d);
       const float4 fin = merged(j);
-      const float M = fin.x, dt = fin.z;
+      const float M = fin.x, dt = fin.z, dl = fin.w;
       d = fin.y;
       if (p.y == nullptr) continue;
       char* y = p.y + r * rowb - h + (int64_t)k0 * 16;
@@ -700,7 +730,9 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         float mass, tt;
         masses(hd, dt, mass, tt);
         mL = M * p.c;
-        f = (hd.g * (mass / d) - (tt > 0.f ? hd.g * (tt / dt) : 0.f)) * ex2(-fmaf(M, p.c, -mL));
+        // (of an unlisted column: the listed ones are stored again)
+        const float u = TAIL ? hd.st - (tt > 0.f ? tt * (dl / dt) : 0.f) : mass;
+        f = hd.g * (u / d) * ex2(-fmaf(M, p.c, -mL));
       }
       const float nmL = -mL;
 #pragma unroll

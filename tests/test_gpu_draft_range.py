@@ -1,0 +1,91 @@
+"""The draft model's operators at the ends of their ranges (distillation and
+verification): lists that hold little of the mass, finite mask values, low
+temperatures, NaN.  Both kernels of each operator."""
+import numpy as np
+import pytest
+import torch
+
+import draft_ref as ref
+import row_reduction_pass_gb300 as rr
+
+from parity import check_guards, compare, empty_like_dev, host, store, to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+def run_distill(x, index, value, g, dtype, T, tail, pads=(0, 0)):
+    """pads that differ take the kernel of single-element accesses."""
+    rows, k = index.shape
+    dl, loss = empty_like_dev(x.shape, dtype, pads[1]), empty_like_dev((rows,), "f32")
+    rr.rr_distill_fwd_bwd(to_dev(x, pads[0]), to_dev(index).view(rows, k),
+                          to_dev(value).view(rows, k), loss, dl, grad=to_dev(g), temperature=T,
+                          tail=tail)
+    torch.cuda.synchronize()
+    check_guards()
+    assert rr.rr_read_device_error(0) == 0
+    return host(loss), host(dl)
+
+
+def small_list(rows, cols, k, T, dtype, seed):
+    """A student's logits, and the top of a teacher's that are the student's with noise,
+    as log-probabilities at temperature T."""
+    rng = np.random.default_rng(seed)
+    x = store(3.0 * rng.standard_normal((rows, cols)), dtype)
+    t = ref.f64(x) + rng.standard_normal((rows, cols))
+    index = np.argsort(-t, axis=1)[:, :k].astype(np.int32)
+    z = t / T
+    lse = np.log(np.exp(z - z.max(1, keepdims=True)).sum(1, keepdims=True)) + z.max(1, keepdims=True)
+    value = np.take_along_axis(z - lse, index.astype(np.int64), 1).astype(np.float32)
+    return x, index, value, rng.uniform(0.5, 1.5, rows).astype(np.float32)
+
+
+def tail_bounds(x, index, value, g, T, k):
+    """What the fp32 arithmetic may be off by where list and student's list hold less
+    than half of the mass, in units of EPS (half a step, relative):
+      loss: a listed term t (lt - z + ln Z): lt, z = (x - m) / T (a difference, a product)
+        and the difference one step of their size each, the product one, the sums of the
+        list K / 32 + 6 (a lane's share one after the other, then five levels) of |lt - ref|
+        and of st ln Z; t itself 5 (expf 2 ulp and its argument), which the loss feels as
+        t (lt - ls - ln tt + ln st');
+      the tail's term: the student's list, sl, 4 |z| + 8 for the exponentials (argument
+        and ex2.approx, 2^-22, also where the parts are scaled to the row's maximum), 40
+        for the sums of Z (at most 28 terms a thread in four chains, and the meetings), and
+        two logarithms of 4 (1 ulp each of log1pf, and its argument);
+      an unlisted gradient g T e / Z (st - tt Zl / Zt): st K / 32 + 14, sl as above.
+    Each is allowed once, and half a step of the result's type."""
+    X = ref.f64(x)
+    cols = index.astype(np.int64)
+    lt, z = value.astype(np.float64), X / T
+    z = z - z.max(1, keepdims=True)
+    lnZ = np.log(np.exp(z).sum(1, keepdims=True))
+    zl = np.take_along_axis(z, cols, 1)
+    t, s = np.exp(lt), np.exp(zl - lnZ)
+    st, sl = t.sum(1, keepdims=True), s.sum(1, keepdims=True)
+    assert st.max() < 0.5 and sl.max() < 0.5
+    sums = k / 32 + 6
+    felt = np.abs(lt - zl + lnZ) + np.abs(np.log1p(-st) - np.log1p(-sl))
+    units = (t * (2 * np.abs(lt) + 3 * np.abs(zl) + sums * (np.abs(lt) + np.abs(zl) + lnZ)
+                  + 5 * felt)).sum(1)
+    units_sl = (s * (4 * np.abs(zl) + 48)).sum(1)
+    units += units_sl + 4 * (np.abs(np.log1p(-st)) + np.abs(np.log1p(-sl)))[:, 0]
+    per_unlisted = (sums + 8) * st[:, 0] + units_sl
+    # tt = 1 - st and its product are rounded relative to themselves: 2 more of sl
+    return T * T * units, (g * T * (per_unlisted + 2 * sl[:, 0]))[:, None] * np.exp(z - lnZ)
+
+
+@pytest.mark.parametrize("pads", [(0, 0), (1, 0)])
+@pytest.mark.parametrize("rows,cols,k,T,dtype", [
+    (37, 131072, 4, 4.0, "f32"), (37, 131072, 4, 4.0, "bf16"), (60, 20000, 32, 4.0, "f32"),
+    (60, 20011, 1, 4.0, "f32"), (90, 5003, 2, 8.0, "bf16"), (5, 300001, 4, 4.0, "f32")])
+def test_distill_tail_of_a_list_with_little_mass(rows, cols, k, T, dtype, pads):
+    x, index, value, g = small_list(rows, cols, k, T, dtype, cols + k)
+    loss, dl = run_distill(x, index, value, g, dtype, T, True, pads)
+    rl, rd, _, _ = ref.distill(x, index, value, g, T, True)
+    lu, du = tail_bounds(x, index, value, g, T, k)
+    compare("distill loss", loss, rl, ref.EPS, 0.0, scale=lu, scale_rtol=ref.EPS)
+    if dtype == "f32":
+        free = np.ones(x.shape, bool)
+        np.put_along_axis(free, index.astype(np.int64), False, 1)
+        # (a result's own exponential: 2 |z| + 6 steps of it, |z| at most 10 here)
+        compare("unlisted dlogits", np.where(free, dl, 0.0), np.where(free, rd, 0.0),
+                27 * ref.EPS, 0.0, scale=du, scale_rtol=ref.EPS)
