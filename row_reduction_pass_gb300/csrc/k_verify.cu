@@ -239,8 +239,11 @@ __global__ void __launch_bounds__(kVerT) verify_kernel_t(const VerifyParams p) {
 // that issues the loads (the address arithmetic and the copies held its warp up for
 // 1300 cycles a node).
 //
-// p = 2^(x c - fl(M c)) * ip, ip = 2^-r / Z with r the rounding residual of
-// fl(M c): one rounding in the exponent's argument.
+// p = 2^((x - M) c) / Z, the maximum taken off before the scaling: in the form
+// 2^(x c - fl(M c)), one packed operation less, the rounding residual of fl(M c) is
+// greater than a float32 exponent for |M| c > 2^31, which masks of -1e10 or the
+// type's lowest value reach (a thread whose columns are all masked has such a
+// maximum), and so do ordinary logits at temperatures of 1e-9 and below.
 
 // The greatest of a chunk's W scores, and the first place it stands at.
 template <int W>
@@ -417,6 +420,11 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
     if (tid < q.lead) return tid;
     return tid >= 32 && tid - 32 < q.rest ? q.lead + q.chunks * W + tid - 32 : -1;
   };
+  // (x - m) log2 e / T of two columns
+  auto scaled2 = [&](float& t0, float& t1, float x0, float x1, float m) {
+    add2(t0, t1, x0, x1, -m, -m);
+    mul2(t0, t1, t0, t1, c, c);
+  };
   // maximum, and sum about it, of this thread's share of a row
   auto stats = [&](const unsigned char* buf, int h, float& m, float& z) {
     constexpr uint32_t ni = DT == kBF16 ? 0xff80ff80u : 0xff800000u;
@@ -448,7 +456,7 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
         m = cm;
       }
       // (a share of -inf sums to 0; about 0 a NaN still gives NaN)
-      const float r = m == -INFINITY ? 0.f : m, mL = r * c;
+      const float r = m == -INFINITY ? 0.f : m;
       float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -456,22 +464,21 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
 #pragma unroll
         for (int e = 0; e < W; e += 4) {
           float t0, t1, t2, t3;
-          fma2(t0, t1, chunk_get<DT>(v[i], e), chunk_get<DT>(v[i], e + 1), c, c, -mL, -mL);
-          fma2(t2, t3, chunk_get<DT>(v[i], e + 2), chunk_get<DT>(v[i], e + 3), c, c, -mL, -mL);
+          scaled2(t0, t1, chunk_get<DT>(v[i], e), chunk_get<DT>(v[i], e + 1), r);
+          scaled2(t2, t3, chunk_get<DT>(v[i], e + 2), chunk_get<DT>(v[i], e + 3), r);
           add2(a0, a1, a0, a1, ex2(t0), ex2(t1));
           add2(a2, a3, a2, a3, ex2(t2), ex2(t3));
         }
       }
-      z += ((a0 + a1) + (a2 + a3)) * ex2(-fmaf(r, c, -mL));
+      z += (a0 + a1) + (a2 + a3);
     }
   };
-  // softmax of a row: 2^(x c - mL) * inv
+  // softmax of a row: 2^((x - m) c) * inv
   struct Soft {
-    float mL, inv;
+    float m, inv;
   };
   auto soft = [&](float M, float Z) {
-    const float r = M == -INFINITY ? 0.f : M, mL = r * c;
-    return Soft{mL, Z == 0.f ? 0.f : ex2(-fmaf(r, c, -mL)) / Z};
+    return Soft{M == -INFINITY ? 0.f : M, Z == 0.f ? 0.f : 1.f / Z};
   };
   auto merge = [&](BestTok t) {  // over the cluster
     auto lanes = [&](BestTok r) {
@@ -596,7 +603,7 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
       P = soft(Mp, Zp);
       Q = soft(Mq, Zq);
     }
-    auto prob = [&](const Soft& r, float v) { return ex2(fmaf(v, c, -r.mL)) * r.inv; };
+    auto prob = [&](const Soft& r, float v) { return ex2((v - r.m) * c) * r.inv; };
     float ratio = 0.f, mass = 1.f;
     // max(p - ratio q, 0) of W columns
     auto residual = [&](const uint4& x, const uint4& y, float (&w)[W]) {
@@ -604,8 +611,8 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
 #pragma unroll
       for (int e = 0; e < W; e += 2) {
         float t0, t1, u0, u1;
-        fma2(t0, t1, chunk_get<DT>(x, e), chunk_get<DT>(x, e + 1), c, c, -P.mL, -P.mL);
-        fma2(u0, u1, chunk_get<DT>(y, e), chunk_get<DT>(y, e + 1), c, c, -Q.mL, -Q.mL);
+        scaled2(t0, t1, chunk_get<DT>(x, e), chunk_get<DT>(x, e + 1), P.m);
+        scaled2(u0, u1, chunk_get<DT>(y, e), chunk_get<DT>(y, e + 1), Q.m);
         mul2(t0, t1, ex2(t0), ex2(t1), P.inv, P.inv);
         fma2(t0, t1, ex2(u0), ex2(u1), rq, rq, t0, t1);
         w[e] = fmaxf(t0, 0.f);
@@ -616,7 +623,7 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
       const float v = ld_smem_elem<DT>(reinterpret_cast<const char*>(pb) + hp + j * E);
       const float u = ratio > 0.f ? ld_smem_elem<DT>(reinterpret_cast<const char*>(qb) + hq + j * E)
                                   : -INFINITY;
-      return fmaxf(fmaf(ex2(fmaf(u, c, -Q.mL)), -ratio * Q.inv, prob(P, v)), 0.f);
+      return fmaxf(fmaf(ex2((u - Q.m) * c), -ratio * Q.inv, prob(P, v)), 0.f);
     };
     int next = -1;
     for (int i = child; i >= 0 && !dead;) {

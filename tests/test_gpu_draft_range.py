@@ -8,6 +8,7 @@ import torch
 import draft_ref as ref
 import row_reduction_pass_gb300 as rr
 
+from test_gpu_draft import check_verify, verify_inputs
 from parity import check_guards, compare, empty_like_dev, host, store, to_dev
 
 pytestmark = pytest.mark.gpu
@@ -89,3 +90,52 @@ def test_distill_tail_of_a_list_with_little_mass(rows, cols, k, T, dtype, pads):
         # (a result's own exponential: 2 |z| + 6 steps of it, |z| at most 10 here)
         compare("unlisted dlogits", np.where(free, dl, 0.0), np.where(free, rd, 0.0),
                 27 * ref.EPS, 0.0, scale=du, scale_rtol=ref.EPS)
+
+
+# ------------------------------------------------------------- verification ---
+
+LOWEST = {"f32": float(np.finfo(np.float32).min), "bf16": -3.3895313892515355e38}
+
+
+def redraw(d, par, T, rng):
+    """Tokens from the draft's distributions."""
+    B, n, V = d.shape
+    tok = np.zeros((B, n), np.int32)
+    for b in range(B):
+        for i in range(n):
+            up = i - 1 if par is None else par[b, i]
+            tok[b, i] = rng.choice(V, p=ref.softmax_row(ref.f64(d[b, up + 1]), float(T[b])))
+    return tok
+
+
+@pytest.mark.parametrize("fill", ["lowest", -1e30, -1e10, -1e9])
+@pytest.mark.parametrize("V,dtype", [(97, "f32"), (4097, "bf16"), (50304, "bf16"), (50304, "f32"),
+                                     (300001, "f32")])
+def test_verify_columns_masked_by_a_finite_value(V, dtype, fill):
+    """All but a run of columns and a few scattered ones hold a mask's value, as a
+    grammar's or a vocabulary's masks leave a row (300001: the one-block kernel)."""
+    B, n = (16, 6) if V < 50000 else (4, 6)
+    t, d, tok, u, e, par, T = verify_inputs(B, n, V, dtype, V, 2)
+    T[::2] = 0.3
+    rng = np.random.default_rng(V)
+    keep = np.zeros(V, bool)
+    keep[V // 3:V // 3 + V // 20 + 8] = True
+    keep[rng.choice(V, 8)] = True
+    bits = store(np.array([LOWEST[dtype] if fill == "lowest" else fill]), dtype)[0]
+    t[:, :, ~keep], d[:, :, ~keep] = bits, bits
+    tok = redraw(d, par, T, rng)
+    want = check_verify(t, d, tok, u, e, par, T)
+    assert (want[0][:, 0] >= 0).all() and want[2].max() > 0
+
+
+@pytest.mark.parametrize("T", [1e-6, 1e-9, 1e-12, 2.0 ** -120])
+@pytest.mark.parametrize("V,dtype", [(1003, "f32"), (50304, "bf16"), (300001, "f32")])
+@pytest.mark.parametrize("branch", [0, 2])
+def test_verify_low_temperatures(V, dtype, T, branch):
+    B, n = (20, 6) if V < 50000 else (4, 6)
+    t, d, tok, u, e, par, temps = verify_inputs(B, n, V, dtype, V + branch, branch, noise=0.1)
+    temps[:] = T
+    rng = np.random.default_rng(V)
+    x = store(ref.f64(t) * 3 + 7, dtype), store(ref.f64(d) * 3 + 7, dtype)
+    want = check_verify(*x, redraw(x[1], par, temps, rng), u, e, par, temps)
+    assert (want[0][:, 0] >= 0).all() and want[2].max() > 0
