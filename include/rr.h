@@ -73,6 +73,8 @@
  *     fl(m log2 e) (m the row maximum).  For |m| >= 2^30 that residual can
  *     leave the float32 exponent range, and the row's outputs can then be NaN;
  *     finite logits below 2^30 in magnitude are always in range.
+ *     rr_distill_fwd_bwd and rr_draft_verify take 2^((x - m) log2 e / T): any
+ *     finite logits are in range.
  */
 #ifndef RR_H
 #define RR_H
@@ -321,7 +323,7 @@ rr_status rr_attention_fwd(const void *q, const void *k, const void *v, void *o,
  *   grad    : [rows] float32, the upstream gradient of the row's loss, or NULL (1).
  *   loss    : [rows] float32.  dlogits : [rows x cols] dtype, may equal logits
  *           (written in place); other overlap is an error.  NULL: loss only.
- *   temperature : > 0 and finite.
+ *   temperature : 2^-120 to 2^120.
  *   bad_index_count : nullable device int32; each entry with index >= cols adds 1.
  * An entry with a negative index, or one >= cols, is absent.  An entry listed
  * twice counts with both values.  A value of -inf has weight 0 (with a tail its

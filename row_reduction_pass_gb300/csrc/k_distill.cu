@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
       if (y != nullptr)
         for (int64_t j = tid; j < p.cols; j += kDistT) st_elem<DT>(y + j * E, 0.f);
     } else {
-      // t_k and the loss
+      // t_k and the loss / T, T ln t_k - T ln s in the logits' own units
       const float lnZ = logf(Z);
       float lnt = 0.f;  // ln of the list's normaliser
       if (!p.tail) {
@@ -156,7 +156,8 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
         if (tidx[i] < 0) continue;
         const float lt = p.tail ? tval[i] : (tval[i] - vm) * p.inv_t - lnt;
         const float t = expf(lt);
-        if (t > 0.f) l += t * (lt - ((tx[i] - M) * p.inv_t - lnZ));
+        const float ltT = p.tail ? p.temperature * lt : (tval[i] - vm) - p.temperature * lnt;
+        if (t > 0.f) l += t * (ltT - ((tx[i] - M) - p.temperature * lnZ));
         else if (t != t) l = t;
         st += t;
         tval[i] = t;
@@ -167,9 +168,9 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
         st = block_sum(st, red);
         tt = Zt > 0.f ? fmaxf(1.f - st, 0.f) : 0.f;
         mass = st + tt;
-        if (tt > 0.f) l += tail_loss(st, tt, Z, Zt, Zl);
+        if (tt > 0.f) l += p.temperature * tail_loss(st, tt, Z, Zt, Zl);
       }
-      if (tid == 0) p.loss[r] = p.temperature * p.temperature * l;
+      if (tid == 0) p.loss[r] = p.temperature * l;
       if (y != nullptr) {
         const float A = g * (mass / Z);                                  // listed
         const float U = p.tail ? g * ((st - (tt > 0.f ? tt * (Zl / Zt) : 0.f)) / Z) : A;
@@ -247,7 +248,7 @@ struct __align__(16) DistHead {
   int dup;        // a column of this slice may be listed twice
   float m, d;     // maximum of the slice's listed columns, sum of exp((x - m) / T)
   float ref;      // the logit that a0 is relative to
-  double a0;      // sum t_k (ln t_k - (x - ref) / T)
+  double a0;      // sum t_k (T ln t_k - (x - ref))
 };
 struct __align__(16) DistEntry {
   float t, x;  // the teacher's weight (before tn; 0: absent), the student's logit
@@ -434,7 +435,8 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     // ------------------------------------------------------ the list warps
     // a / T, 1 / T in two parts
     auto over_t = [&](float a) {
-      return isfinite(a) ? fmaf(a, p.inv_t, a * p.inv_t_lo) : a;
+      const float q = a * p.inv_t;
+      return isfinite(q) ? fmaf(a, p.inv_t, a * p.inv_t_lo) : q;
     };
     // The list of a row passes through registers, 4 entries a lane (lists of up
     // to 128) at a time: its entries are loaded one row before the student's
@@ -462,7 +464,9 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     // What a list says before the row's statistics are known: the weights t (with
     // no tail relative to the greatest, tn brings them to sum 1), its part of the
     // loss relative to a logit of its own, the listed columns' part of Z.  Every
-    // entry is touched once, in registers.
+    // entry is touched once, in registers.  The loss is summed divided by T, in the
+    // logits' units (T ln t_k is v itself without a tail): it neither overflows nor
+    // underflows where T^2 or 1 / T would.
     auto prepare = [&](int64_t j) {
       const int64_t r = row_of(j);
       if (r >= p.rows) return;
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       }
       if (ref == -INFINITY) ref = 0.f;
       const bool live = any && (TAIL || vm != -INFINITY);
-      const float v0 = TAIL ? 0.f : vm, mL = ref * p.c;
+      const float v0 = TAIL ? 0.f : vm;
       float st = 0.f, d = 0.f, a0 = 0.f;
       int dup = 0;
       for (int base = 0; base < k; base += 128) {
@@ -515,12 +519,12 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
           if (i >= k) continue;
           DistEntry en{0.f, 0.f, -1, 0};
           if (ci[q] >= 0 && ci[q] < p.cols) {
-            const float lt = TAIL ? cv[q] : over_t(cv[q] - v0);
+            const float v = cv[q] - v0, lt = TAIL ? v : over_t(v);
             en.x = cx[q];
             if (live) {
               en.t = expf(lt);
               st += en.t;
-              if (!(en.t <= 0.f)) a0 += en.t * (lt - over_t(en.x - ref));
+              if (!(en.t <= 0.f)) a0 += en.t * ((TAIL ? p.temperature * v : v) - (en.x - ref));
             }
             const int e = ci[q] + first;
             if (e >= 0 && e < g.S * W) {
@@ -529,7 +533,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
                 dup = 1;
                 en.place |= kDistAgain;
               } else if (TAIL) {
-                d += ex2(fmaf(en.x, p.c, -mL));
+                d += ex2((en.x - ref) * p.c);
               }
             }
           }
@@ -552,10 +556,10 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         hd.live = live;
         hd.dup = dup;
         hd.m = d > 0.f ? ref : d == d ? -INFINITY : ref;
-        hd.d = d * ex2(-fmaf(ref, p.c, -mL));
+        hd.d = d;
         hd.ref = ref;
         // sum t ln t has ln t_k = lt - ln(sum of t) where the list is normalised
-        hd.a0 = TAIL ? a : a / (double)st - (double)logf(st);
+        hd.a0 = TAIL ? a : a / (double)st - (double)p.temperature * (double)logf(st);
         heads[j & 3] = hd;
       }
       __syncwarp();
@@ -594,7 +598,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       const DistEntry* li = lists + (j & 3) * k;
       float mass, tt;
       masses(hd, dt, mass, tt);
-      const float mL = M * p.c, A = hd.g * (mass / d) * ex2(-fmaf(M, p.c, -mL)), B = hd.g * hd.tn;
+      const float A = hd.g * (mass / d), B = hd.g * hd.tn;
       char* y = p.y + r * rowb - h + (int64_t)k0 * 16;
       for (int i = lane; i < k; i += 32) {
         const DistEntry en = li[i];
@@ -602,11 +606,11 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         float t = en.t;
         if (hd.dup)
           for (int n = 0; n < k; ++n) t += li[n].place == (en.place | kDistAgain) ? li[n].t : 0.f;
-        st_elem<DT>(y + en.place * E, fmaf(ex2(fmaf(en.x, p.c, -mL)), A, -B * t));
+        st_elem<DT>(y + en.place * E, fmaf(ex2((en.x - M) * p.c), A, -B * t));
       }
     };
-    // The loss: a0 plus st times the distance of ref from the row's logarithm of Z,
-    // two numbers of some tens whose sum is small, hence in double (a few
+    // The loss: a0 plus st times the distance of ref from T times the row's logarithm
+    // of Z, two numbers of some tens whose sum is small, hence in double (a few
     // operations a row).
     auto write_loss = [&](int64_t j, float M, float d, float dt, float dl) {
       const DistHead hd = heads[j & 3];
@@ -615,12 +619,12 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         const int ez = (__float_as_int(d) >> 23) - 127;
         const double lnz = (double)ez * 0.69314718055994531 +
                            (double)logf(__int_as_float(__float_as_int(d) - (ez << 23)));
-        const double inv_t = (double)p.inv_t + (double)p.inv_t_lo;
-        double s = hd.a0 + (double)hd.st * (((double)M - (double)hd.ref) * inv_t + lnz);
+        const double T = (double)p.temperature;
+        double s = hd.a0 + (double)hd.st * (((double)M - (double)hd.ref) + T * lnz);
         float mass, tt;
         masses(hd, dt, mass, tt);
-        if (tt > 0.f) s += tail_loss(hd.st, tt, d, dt, dl);
-        l = (float)s * (p.temperature * p.temperature);
+        if (tt > 0.f) s += T * (double)tail_loss(hd.st, tt, d, dt, dl);
+        l = (float)(s * T);
         if (d != d) l = d;
       }
       if (lane == 0) p.loss[row_of(j)] = l;
@@ -700,10 +704,9 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
                     fmaxf(__uint_as_float(v[q].z), __uint_as_float(v[q].w)));
         }
       }
-      // sum of 2^(x c - fl(m c))
+      // sum of 2^((x - m) c)
       float d = 0.f;
       if (m != -INFINITY) {
-        const float mL = m * p.c;
         float d1 = 0.f;
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
@@ -711,11 +714,11 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
 #pragma unroll
           for (int i = 0; i < W; i += 2) {
             float t0, t1;
-            fma2(t0, t1, chunk_get<DT>(v[q], i), chunk_get<DT>(v[q], i + 1), p.c, p.c, -mL, -mL);
+            scaled2(t0, t1, chunk_get<DT>(v[q], i), chunk_get<DT>(v[q], i + 1), m, p.c);
             add2(d, d1, d, d1, ex2(t0), ex2(t1));
           }
         }
-        d = (d + d1) * ex2(-fmaf(m, p.c, -mL));
+        d += d1;
       }
       publish(j, warp, m, d);
       const float4 fin = merged(j);
@@ -724,17 +727,15 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       if (p.y == nullptr) continue;
       char* y = p.y + r * rowb - h + (int64_t)k0 * 16;
       const DistHead hd = heads[j & 3];
-      float f = 0.f, mL = 0.f;
+      float f = 0.f;
       const bool zero = !hd.live || M == -INFINITY;
       if (!zero) {
         float mass, tt;
         masses(hd, dt, mass, tt);
-        mL = M * p.c;
         // (of an unlisted column: the listed ones are stored again)
         const float u = TAIL ? hd.st - (tt > 0.f ? tt * (dl / dt) : 0.f) : mass;
-        f = hd.g * (u / d) * ex2(-fmaf(M, p.c, -mL));
+        f = hd.g * (u / d);
       }
-      const float nmL = -mL;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         if (q >= nq || zero) break;
@@ -742,7 +743,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
 #pragma unroll
         for (int i = 0; i < W; i += 2) {
           float t0, t1;
-          fma2(t0, t1, chunk_get<DT>(v[q], i), chunk_get<DT>(v[q], i + 1), p.c, p.c, nmL, nmL);
+          scaled2(t0, t1, chunk_get<DT>(v[q], i), chunk_get<DT>(v[q], i + 1), M, p.c);
           mul2(e[i], e[i + 1], ex2(t0), ex2(t1), f, f);
         }
         if (!(head && q == 0) && !(end && q == nq - 1))
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         for (int i = lo; i < hi; i += E) {
           const float x = ld_smem_elem<DT>(reinterpret_cast<const char*>(edge + s) + i);
           st_elem<DT>(y + (s == 0 ? 0 : (int64_t)last * 16) + i,
-                      zero ? 0.f : ex2(fmaf(x, p.c, nmL)) * f);
+                      zero ? 0.f : ex2((x - M) * p.c) * f);
         }
       }
     }

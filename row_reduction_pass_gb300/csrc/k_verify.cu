@@ -420,11 +420,6 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
     if (tid < q.lead) return tid;
     return tid >= 32 && tid - 32 < q.rest ? q.lead + q.chunks * W + tid - 32 : -1;
   };
-  // (x - m) log2 e / T of two columns
-  auto scaled2 = [&](float& t0, float& t1, float x0, float x1, float m) {
-    add2(t0, t1, x0, x1, -m, -m);
-    mul2(t0, t1, t0, t1, c, c);
-  };
   // maximum, and sum about it, of this thread's share of a row
   auto stats = [&](const unsigned char* buf, int h, float& m, float& z) {
     constexpr uint32_t ni = DT == kBF16 ? 0xff80ff80u : 0xff800000u;
@@ -464,8 +459,8 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
 #pragma unroll
         for (int e = 0; e < W; e += 4) {
           float t0, t1, t2, t3;
-          scaled2(t0, t1, chunk_get<DT>(v[i], e), chunk_get<DT>(v[i], e + 1), r);
-          scaled2(t2, t3, chunk_get<DT>(v[i], e + 2), chunk_get<DT>(v[i], e + 3), r);
+          scaled2(t0, t1, chunk_get<DT>(v[i], e), chunk_get<DT>(v[i], e + 1), r, c);
+          scaled2(t2, t3, chunk_get<DT>(v[i], e + 2), chunk_get<DT>(v[i], e + 3), r, c);
           add2(a0, a1, a0, a1, ex2(t0), ex2(t1));
           add2(a2, a3, a2, a3, ex2(t2), ex2(t3));
         }
@@ -611,8 +606,8 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
 #pragma unroll
       for (int e = 0; e < W; e += 2) {
         float t0, t1, u0, u1;
-        scaled2(t0, t1, chunk_get<DT>(x, e), chunk_get<DT>(x, e + 1), P.m);
-        scaled2(u0, u1, chunk_get<DT>(y, e), chunk_get<DT>(y, e + 1), Q.m);
+        scaled2(t0, t1, chunk_get<DT>(x, e), chunk_get<DT>(x, e + 1), P.m, c);
+        scaled2(u0, u1, chunk_get<DT>(y, e), chunk_get<DT>(y, e + 1), Q.m, c);
         mul2(t0, t1, ex2(t0), ex2(t1), P.inv, P.inv);
         fma2(t0, t1, ex2(u0), ex2(u1), rq, rq, t0, t1);
         w[e] = fmaxf(t0, 0.f);

@@ -2144,8 +2144,9 @@ rr_status rr_distill_fwd_bwd(const void* logits, const int32_t* top_index, const
   if (st != RR_OK) return st;
   if (k < 0 || k > 1024) return fail(RR_ERR_INVALID_ARG, "k=%lld outside 0..1024", (long long)k);
   if (cols > INT32_MAX) return fail(RR_ERR_INVALID_ARG, "cols beyond an int32 index");
-  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature))
-    return fail(RR_ERR_INVALID_ARG, "temperature must be finite and > 0");
+  // (T ln t and (x - max) log2 e / T of ordinary values stay in a float32's range)
+  if (!(temperature >= 0x1p-120f && temperature <= 0x1p120f))
+    return fail(RR_ERR_INVALID_ARG, "temperature must be within 2^-120 .. 2^120");
   if (rows == 0) return ok();
   if (rows > ((int64_t)1 << 50) / (k + 1)) return fail(RR_ERR_INVALID_ARG, "rows*k too large");
   if (!logits || !loss || (k > 0 && (!top_index || !top_value)))

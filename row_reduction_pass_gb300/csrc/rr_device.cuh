@@ -57,6 +57,14 @@ __device__ __forceinline__ void mul2(float& dx, float& dy, float ax, float ay, f
       : "=f"(dx), "=f"(dy)
       : "f"(ax), "f"(ay), "f"(bx), "f"(by));
 }
+// (x - m) c of two values, the difference first: it is right for any finite x and m,
+// where one rounding less, x c - fl(m c), leaves a residual of fl(m c) that exceeds a
+// float32 exponent for |m| c > 2^31.
+__device__ __forceinline__ void scaled2(float& t0, float& t1, float x0, float x1, float m,
+                                        float c) {
+  add2(t0, t1, x0, x1, -m, -m);
+  mul2(t0, t1, t0, t1, c, c);
+}
 
 // ---------------------------------------------------------------- storage ---
 

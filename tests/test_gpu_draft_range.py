@@ -13,6 +13,8 @@ from parity import check_guards, compare, empty_like_dev, host, store, to_dev
 
 pytestmark = pytest.mark.gpu
 
+LOWEST = {"f32": float(np.finfo(np.float32).min), "bf16": -3.3895313892515355e38}
+
 
 def run_distill(x, index, value, g, dtype, T, tail, pads=(0, 0)):
     """pads that differ take the kernel of single-element accesses."""
@@ -92,10 +94,71 @@ def test_distill_tail_of_a_list_with_little_mass(rows, cols, k, T, dtype, pads):
                 27 * ref.EPS, 0.0, scale=du, scale_rtol=ref.EPS)
 
 
+def compare_distill(got, x, index, value, g, dtype, T, tail, atol=1e-30):
+    rl, rd, lm, dm = ref.distill(x, index, value, g, T, tail)
+    compare("distill loss", got[0], rl, 0.0, atol, scale=lm, scale_rtol=64 * ref.EPS)
+    compare("distill dlogits", got[1], rd, 2.0 ** -8 if dtype == "bf16" else 2.0 ** -23, atol,
+            scale=dm, scale_rtol=64 * ref.EPS)
+
+
+@pytest.mark.parametrize("fill", ["lowest", -1e30, -1e10, -1e9])
+@pytest.mark.parametrize("cols,dtype", [(97, "f32"), (1000, "bf16"), (4097, "bf16"), (50304, "bf16"),
+                                        (50304, "f32"), (131075, "f32"), (300001, "f32")])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_columns_masked_by_a_finite_value(cols, tail, dtype, fill):
+    """All but a run of columns and a few scattered ones hold a mask's value; some lists
+    have a masked column (300001: the kernel of single-element accesses)."""
+    rows, k, T = (24, 6, 0.3) if cols < 50000 else (6, 6, 0.3)
+    rng = np.random.default_rng(cols)
+    x = store(rng.standard_normal((rows, cols)) * 3.0, dtype)
+    keep = np.zeros(cols, bool)
+    keep[cols // 3:cols // 3 + cols // 20 + 8] = True
+    keep[rng.choice(cols, 4, replace=False)] = True
+    x[:, ~keep] = store(np.array([LOWEST[dtype] if fill == "lowest" else fill]), dtype)[0]
+    index = np.stack([rng.choice(np.flatnonzero(keep), k, replace=False) for _ in range(rows)])
+    z = rng.standard_normal((rows, k))
+    value = z - np.log(np.exp(z).sum(1, keepdims=True)) - 0.4 if tail else z
+    if fill != "lowest":
+        index[::4, 2] = np.flatnonzero(~keep)[-1]
+    index, value = index.astype(np.int32), value.astype(np.float32)
+    g = rng.uniform(0.5, 1.5, rows).astype(np.float32)
+    got = run_distill(x, index, value, g, dtype, T, tail)
+    compare_distill(got, x, index, value, g, dtype, T, tail)
+
+
+@pytest.mark.parametrize("T", [1e-6, 1e-9, 1e-12, 2.0 ** -120])
+@pytest.mark.parametrize("cols,dtype", [(97, "f32"), (4097, "bf16"), (50304, "f32"),
+                                        (131075, "f32"), (300001, "f32")])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_low_temperatures(cols, tail, dtype, T):
+    """The distributions are all on their largest logits; the loss, about T times a
+    difference of logits, keeps its digits."""
+    rows, k = 20 if cols < 50000 else 6, 5
+    rng = np.random.default_rng(cols)
+    x = store(rng.standard_normal((rows, cols)) * 6.0 + 7.0, dtype)
+    index = np.stack([rng.choice(cols, k, replace=False) for _ in range(rows)]).astype(np.int32)
+    index[::2, 0] = ref.f64(x)[::2].argmax(1)
+    z = rng.standard_normal((rows, k))
+    value = (z - np.log(np.exp(z).sum(1, keepdims=True)) - 0.4 if tail else z).astype(np.float32)
+    g = rng.uniform(0.5, 1.5, rows).astype(np.float32)
+    got = run_distill(x, index, value, g, dtype, T, tail)
+    # (T 1e-30: exponentials flushed to zero)
+    compare_distill(got, x, index, value, g, dtype, T, tail, atol=T * 1e-30)
+
+
+@pytest.mark.parametrize("T", [2.0 ** 30, 2.0 ** 60])
+@pytest.mark.parametrize("cols", [97, 300001])
+def test_distill_high_temperatures(cols, T):
+    """Without a tail (T^2 times what the list's weights leave of 1 would be the loss)."""
+    rows, k, rng = 5, 3, np.random.default_rng(cols)
+    x = rng.standard_normal((rows, cols)).astype(np.float32)
+    index = np.stack([rng.choice(cols, k, replace=False) for _ in range(rows)]).astype(np.int32)
+    value, g = rng.standard_normal((rows, k)).astype(np.float32), np.ones(rows, np.float32)
+    compare_distill(run_distill(x, index, value, g, "f32", T, False), x, index, value, g, "f32", T,
+                    False)
+
+
 # ------------------------------------------------------------- verification ---
-
-LOWEST = {"f32": float(np.finfo(np.float32).min), "bf16": -3.3895313892515355e38}
-
 
 def redraw(d, par, T, rng):
     """Tokens from the draft's distributions."""
