@@ -329,7 +329,8 @@ rr_status rr_attention_fwd(const void *q, const void *k, const void *v, void *o,
  * twice counts with both values.  A value of -inf has weight 0 (with a tail its
  * column still counts as listed).  A row with no entry present (without a tail:
  * none of finite weight), or fully masked logits, gets loss 0 and dlogits 0.
- * The tail term is left out of a row whose unlisted columns hold none of the
+ * A NaN or +inf logit, or a NaN value, makes the loss and dlogits of a row with an
+ * entry present NaN.  The tail term is left out of a row whose unlisted columns hold none of the
  * student's mass (all below 2^-126 of its largest probability).
  */
 rr_status rr_distill_fwd_bwd(const void *logits, const int32_t *top_index,

@@ -94,16 +94,17 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
       tidx[i] = j;
       tval[i] = v;
       if (j >= 0) {
-        any = 1;
+        any |= v == v ? 1 : 3;  // (a NaN is not a list without weight)
         vm = fmaxf(vm, v);
         tx[i] = ld_elem<DT>(x + (int64_t)j * E);
         const uint32_t b = (uint32_t)j & fmask;
         if (atomicOr(&filter[b >> 5], 1u << (b & 31)) & (1u << (b & 31))) s_dup = 1;
       }
     }
+    const bool undefined = __syncthreads_or(any & 2);
     any = __syncthreads_or(any);
     vm = block_max(vm, red);
-    const bool live = any && (p.tail || vm != -INFINITY);
+    const bool live = any && (p.tail || vm != -INFINITY || undefined);
     // the row's maximum and sums (online, per thread, then merged)
     float m = -INFINITY, d = 0.f, dt = 0.f, dl = 0.f;  // d: no tail
     if (live) {
@@ -137,7 +138,8 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
     const float Zl = p.tail ? block_sum(dl * a, red) : 0.f;
     const float Z = p.tail ? Zt + Zl : block_sum(d * a, red);
     const float g = p.temperature * (p.grad != nullptr ? p.grad[r] : 1.f);
-    if (!live || M == -INFINITY) {  // no teacher, or nothing to learn from: zeros
+    // (a row of NaN and -inf has a maximum of -inf too, but not a sum of 0)
+    if (!live || (M == -INFINITY && Z == 0.f)) {  // no teacher, or nothing to learn from: zeros
       if (tid == 0) p.loss[r] = 0.f;
       if (y != nullptr)
         for (int64_t j = tid; j < p.cols; j += kDistT) st_elem<DT>(y + j * E, 0.f);
@@ -163,13 +165,14 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
         tval[i] = t;
       }
       l = block_sum(l, red);
-      float mass = 1.f, tt = 0.f;
+      st = block_sum(st, red);
+      float mass = st == st ? 1.f : st, tt = 0.f;
       if (p.tail) {
-        st = block_sum(st, red);
         tt = Zt > 0.f ? fmaxf(1.f - st, 0.f) : 0.f;
         mass = st + tt;
         if (tt > 0.f) l += p.temperature * tail_loss(st, tt, Z, Zt, Zl);
       }
+      if (Z != Z) l = Z;
       if (tid == 0) p.loss[r] = p.temperature * l;
       if (y != nullptr) {
         const float A = g * (mass / Z);                                  // listed
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
 struct __align__(16) DistHead {
   float g;        // upstream gradient times T
   float tn;       // t_k = tn * (the entries' t)
-  float st;       // sum of t_k (with a tail)
+  float st;       // sum of t_k (with no tail 1, or NaN)
   int live;       // some entry has weight
   int dup;        // a column of this slice may be listed twice
   float m, d;     // maximum of the slice's listed columns, sum of exp((x - m) / T)
@@ -362,12 +365,13 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
   };
   // the teacher's mass outside the list, and the weight of the student's softmax
   auto masses = [&](const DistHead& hd, float dt, float& mass, float& tt) {
-    mass = 1.f;
-    tt = 0.f;
-    if (TAIL) {
-      if (dt > 0.f) tt = fmaxf(1.f - hd.st, 0.f);
-      mass = hd.st + tt;
-    }
+    tt = TAIL && dt > 0.f ? fmaxf(1.f - hd.st, 0.f) : 0.f;
+    mass = hd.st + tt;
+  };
+  // a row with no teacher, or nothing to learn from (a row of NaN and -inf has a maximum
+  // of -inf too, but not a sum of 0)
+  auto empty = [&](const DistHead& hd, float M, float d) {
+    return !hd.live || (M == -INFINITY && d == 0.f);
   };
 
   auto load_row = [&](int64_t j) {
@@ -487,7 +491,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
             ci[q] = -1;
             continue;
           }
-          any = 1;
+          any |= cv[q] == cv[q] ? 1 : 3;  // (a NaN is not a list without weight)
           vm = fmaxf(vm, cv[q]);
           ref = fmaxf(ref, cx[q]);
         }
@@ -496,14 +500,14 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         load_entries(j, base);
         load_logits(j);
       }
-      any = __any_sync(0xffffffffu, any);
+      any = (int)__reduce_or_sync(0xffffffffu, (unsigned)any);
 #pragma unroll
       for (int off = 16; off >= 1; off >>= 1) {
         vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
         ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, off));
       }
       if (ref == -INFINITY) ref = 0.f;
-      const bool live = any && (TAIL || vm != -INFINITY);
+      const bool live = any && (TAIL || vm != -INFINITY || any == 3);
       const float v0 = TAIL ? 0.f : vm;
       float st = 0.f, d = 0.f, a0 = 0.f;
       int dup = 0;
@@ -552,7 +556,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
         DistHead hd;
         hd.g = p.temperature * (p.grad != nullptr ? __ldg(p.grad + r) : 1.f);
         hd.tn = TAIL ? 1.f : 1.f / st;
-        hd.st = TAIL ? st : 1.f;
+        hd.st = TAIL || st != st ? st : 1.f;
         hd.live = live;
         hd.dup = dup;
         hd.m = d > 0.f ? ref : d == d ? -INFINITY : ref;
@@ -593,7 +597,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     auto finish = [&](int64_t j, float M, float d, float dt) {
       const int64_t r = row_of(j);
       const DistHead hd = heads[j & 3];
-      if (p.y == nullptr || !hd.live || M == -INFINITY) return;
+      if (p.y == nullptr || empty(hd, M, d)) return;
       const int h = (int)(row_addr(r) & 15);
       const DistEntry* li = lists + (j & 3) * k;
       float mass, tt;
@@ -615,7 +619,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     auto write_loss = [&](int64_t j, float M, float d, float dt, float dl) {
       const DistHead hd = heads[j & 3];
       float l = 0.f;
-      if (hd.live && M != -INFINITY) {
+      if (!empty(hd, M, d)) {
         const int ez = (__float_as_int(d) >> 23) - 127;
         const double lnz = (double)ez * 0.69314718055994531 +
                            (double)logf(__int_as_float(__float_as_int(d) - (ez << 23)));
@@ -704,22 +708,20 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
                     fmaxf(__uint_as_float(v[q].z), __uint_as_float(v[q].w)));
         }
       }
-      // sum of 2^((x - m) c)
-      float d = 0.f;
-      if (m != -INFINITY) {
-        float d1 = 0.f;
+      // sum of 2^((x - m) c)  (a share of -inf sums to 0; about 0 a NaN still gives NaN)
+      const float about = m == -INFINITY ? 0.f : m;
+      float d = 0.f, d1 = 0.f;
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          if (q >= nq) break;
+      for (int q = 0; q < NQ; ++q) {
+        if (q >= nq) break;
 #pragma unroll
-          for (int i = 0; i < W; i += 2) {
-            float t0, t1;
-            scaled2(t0, t1, chunk_get<DT>(v[q], i), chunk_get<DT>(v[q], i + 1), m, p.c);
-            add2(d, d1, d, d1, ex2(t0), ex2(t1));
-          }
+        for (int i = 0; i < W; i += 2) {
+          float t0, t1;
+          scaled2(t0, t1, chunk_get<DT>(v[q], i), chunk_get<DT>(v[q], i + 1), about, p.c);
+          add2(d, d1, d, d1, ex2(t0), ex2(t1));
         }
-        d += d1;
       }
+      d += d1;
       publish(j, warp, m, d);
       const float4 fin = merged(j);
       const float M = fin.x, dt = fin.z, dl = fin.w;
@@ -728,7 +730,7 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       char* y = p.y + r * rowb - h + (int64_t)k0 * 16;
       const DistHead hd = heads[j & 3];
       float f = 0.f;
-      const bool zero = !hd.live || M == -INFINITY;
+      const bool zero = empty(hd, M, d);
       if (!zero) {
         float mass, tt;
         masses(hd, dt, mass, tt);

@@ -158,6 +158,59 @@ def test_distill_high_temperatures(cols, T):
                     False)
 
 
+@pytest.mark.parametrize("cols,dtype", [(2, "f32"), (97, "f32"), (4097, "bf16"), (50304, "bf16"),
+                                        (131075, "f32"), (300001, "f32")])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_nan_and_inf_logits(cols, tail, dtype):
+    """One NaN (or +inf) anywhere in a row, listed or not, makes the row's loss and
+    dlogits NaN, and so does a row of NaN, or of NaN and -inf; the rows beside it are as
+    they would be."""
+    rng = np.random.default_rng(cols)
+    rows, k, T = 16, 2, 2.0
+    x = store(rng.standard_normal((rows, cols)) * 3.0, dtype)
+    nan, inf, ninf = store(np.array([np.nan, np.inf, -np.inf]), dtype)
+    index = np.stack([rng.choice(cols, k, replace=False) for _ in range(rows)]).astype(np.int32)
+    z = rng.standard_normal((rows, k))
+    value = (z - np.log(np.exp(z).sum(1, keepdims=True)) - 0.4 if tail else z).astype(np.float32)
+    x[1] = nan
+    x[2], x[2, cols // 2] = ninf, nan
+    x[4, 0], x[5, cols - 1], x[6, cols // 2] = nan, nan, nan
+    x[7, index[7, 1]] = nan
+    x[8, cols // 3] = inf
+    x[10, max(0, cols - 5):] = nan
+    x[11], index[11] = nan, -1                   # no entry present: zeros
+    x[13] = ninf                                 # fully masked: zeros
+    g = rng.uniform(0.5, 1.5, rows).astype(np.float32)
+    loss, dl = run_distill(x, index, value, g, dtype, T, tail)
+    bad = [1, 2, 4, 5, 6, 7, 8, 10]
+    assert np.isnan(loss[bad]).all() and np.isnan(dl[bad]).all()
+    assert loss[11] == 0 and (dl[11] == 0).all() and loss[13] == 0 and (dl[13] == 0).all()
+    good = [r for r in range(rows) if r not in bad + [11]]
+    compare_distill((loss[good], dl[good]), x[good], index[good], value[good], g[good], dtype, T,
+                    tail)
+
+
+@pytest.mark.parametrize("cols", [97, 50304, 300001])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("k", [1, 3, 200])
+def test_distill_nan_values(cols, tail, k):
+    """A NaN among the teacher's values, or all of them: no list without weight."""
+    rng = np.random.default_rng(k)
+    rows, k = 6, min(k, cols)
+    x = rng.standard_normal((rows, cols)).astype(np.float32)
+    index = np.stack([rng.choice(cols, k, replace=False) for _ in range(rows)]).astype(np.int32)
+    value = (rng.standard_normal((rows, k)) - 9.0).astype(np.float32)
+    value[1] = np.nan
+    value[2, k // 2] = np.nan
+    value[3], value[3, 0] = -np.inf, np.nan
+    g = np.ones(rows, np.float32)
+    loss, dl = run_distill(x, index, value, g, "f32", 1.0, tail)
+    assert np.isnan(loss[1:4]).all() and np.isnan(dl[1:4]).all()
+    good = [0, 4, 5]
+    compare_distill((loss[good], dl[good]), x[good], index[good], value[good], g[good], "f32", 1.0,
+                    tail)
+
+
 # ------------------------------------------------------------- verification ---
 
 def redraw(d, par, T, rng):
