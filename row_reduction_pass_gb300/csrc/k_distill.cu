@@ -374,8 +374,15 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
     return !hd.live || (M == -INFINITY && d == 0.f);
   };
 
+  int64_t asked = -1;  // the last row asked for
   auto load_row = [&](int64_t j) {
     if (row_of(j) >= p.rows || dead) return;
+    // (the row before in this buffer has landed, unless the warps that use it gave up)
+    if (j >= 2 && !mbar_wait_bounded(&full[j & 1], (uint32_t)(((j >> 1) - 1) & 1), p.err)) {
+      dead = true;
+      return;
+    }
+    asked = j;
     const uintptr_t a = row_addr(row_of(j));
     const uint32_t bytes = (uint32_t)chunks((int)(a & 15)) * 16u;
     mbar_arrive_expect_tx(&full[j & 1], bytes);
@@ -432,8 +439,10 @@ __global__ void __launch_bounds__(1024, 1) distill_stream_kernel(const DistillPa
       }
       __syncwarp();
     }
-    if (dead && lane == 0)  // copies of this block still in flight end before it does
-      for (int i = 0; i < 2; ++i) mbar_wait_bounded(&full[i], 0, p.err);
+    // Copies of this block end before it does (they have, but where a wait gave up).
+    if (lane == 0)
+      for (int64_t j = asked > 0 ? asked - 1 : 0; j <= asked; ++j)
+        mbar_wait_bounded(&full[j & 1], (uint32_t)((j >> 1) & 1), p.err);
     __syncthreads();
   } else if (warp > nw) {
     // ------------------------------------------------------ the list warps

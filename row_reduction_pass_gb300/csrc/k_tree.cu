@@ -536,6 +536,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     return c;
   };
 
+  int copies = 0;  // tiles that this loader has asked for
   if (first.left <= 0) {
     // no run for this pipeline
   } else if (warp >= 12) {
@@ -576,6 +577,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           tma_load_4d(dst + b * C::kKVBox, map, 64 * b, c.s.h, tree_page_row(p, g, pos), page,
                       &full[s]);
       }
+      copies = n + 1;
       advance(c);
       look_up();
     }
@@ -584,6 +586,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (lane == 0) {
       Cur c = begin(first);
       int pieces = 0;  // begun
+      int issued = 0;
+      // (the products end before the block does, also after a wait gave up)
+      auto finish = [&](uint64_t* bar, uint32_t parity) {
+        if (issued > 0) mbar_wait_bounded(bar, parity, p.err);
+      };
       if (warp >= 10) {
         // O += P V as soon as P is written (the first of a piece, which overwrites
         // O, once the softmax has read it)
@@ -601,8 +608,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                    (c.j > 0 || kk > 0) ? 1u : 0u);
           mma_commit(&bar_o[t % C::NPB]);
           mma_commit(&bar_vempty[t & 1]);
+          issued = t + 1;
           advance(c);
         }
+        finish(&bar_o[(issued + C::NPB - 1) % C::NPB], (uint32_t)(((issued - 1) / C::NPB) & 1));
       } else {
         // S = Q K^T as soon as the softmax has read the S before (a new piece's Q is
         // then there)
@@ -622,8 +631,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           mma_commit(bar_s);
           mma_commit(&bar_kempty[t & 1]);
+          issued = t + 1;
           advance(c);
         }
+        finish(bar_s, (uint32_t)((issued - 1) & 1));
       }
     }
   } else {
@@ -992,6 +1003,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
   }
 
+  // Copies end before the block does (they have, but where a wait gave up).
+  for (int n = max(copies - 2, 0); n < copies; ++n)
+    mbar_wait_bounded(&(warp >= 14 ? bar_vfull : bar_kfull)[n & 1], (uint32_t)((n >> 1) & 1), p.err);
   tc_fence_before();
   __syncthreads();
   if (warp == 0)
