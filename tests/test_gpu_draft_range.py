@@ -255,3 +255,20 @@ def test_verify_low_temperatures(V, dtype, T, branch):
     x = store(ref.f64(t) * 3 + 7, dtype), store(ref.f64(d) * 3 + 7, dtype)
     want = check_verify(*x, redraw(x[1], par, temps, rng), u, e, par, temps)
     assert (want[0][:, 0] >= 0).all() and want[2].max() > 0
+
+
+# ---------------------------------------------------------------- attention ---
+
+@pytest.mark.parametrize("batch", [2, 400])
+def test_tree_attention_pages_but_no_table(batch):
+    """A table of no width: nothing is seen, by either way of planning."""
+    q = torch.randn(batch, 3, 4, 64, device="cuda").bfloat16()
+    kc = torch.randn(5, 16, 2, 64, device="cuda").bfloat16()
+    table = torch.empty(batch, 0, dtype=torch.int32, device="cuda")
+    ctx = torch.full((batch,), 9, dtype=torch.int32, device="cuda")
+    for par in (None, torch.full((batch, 3), -1, dtype=torch.int32, device="cuda")):
+        o, l = torch.full_like(q, 7.0), torch.zeros(batch, 3, 4, device="cuda")
+        rr.rr_attention_tree_fwd(q, kc, kc, table, ctx, o, lse=l, parents=par)
+        torch.cuda.synchronize()
+        assert rr.rr_read_device_error(0) == 0
+        assert (o == 0).all() and torch.isneginf(l).all()
