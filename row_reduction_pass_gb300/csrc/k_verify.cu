@@ -600,9 +600,11 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
     }
     auto prob = [&](const Soft& r, float v) { return ex2((v - r.m) * c) * r.inv; };
     float ratio = 0.f, mass = 1.f;
+    // the factor of q's exponentials (0 with no ratio, also where q is not defined)
+    auto weight_q = [&]() { return ratio > 0.f ? -ratio * Q.inv : 0.f; };
     // max(p - ratio q, 0) of W columns
     auto residual = [&](const uint4& x, const uint4& y, float (&w)[W]) {
-      const float rq = -ratio * Q.inv;
+      const float rq = weight_q();
 #pragma unroll
       for (int e = 0; e < W; e += 2) {
         float t0, t1, u0, u1;
@@ -618,7 +620,7 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
       const float v = ld_smem_elem<DT>(reinterpret_cast<const char*>(pb) + hp + j * E);
       const float u = ratio > 0.f ? ld_smem_elem<DT>(reinterpret_cast<const char*>(qb) + hq + j * E)
                                   : -INFINITY;
-      return fmaxf(fmaf(ex2((u - Q.m) * c), -ratio * Q.inv, prob(P, v)), 0.f);
+      return fmaxf(fmaf(ex2((u - Q.m) * c), weight_q(), prob(P, v)), 0.f);
     };
     int next = -1;
     for (int i = child; i >= 0 && !dead;) {

@@ -8,7 +8,7 @@ import torch
 import draft_ref as ref
 import row_reduction_pass_gb300 as rr
 
-from test_gpu_draft import check_verify, verify_inputs
+from test_gpu_draft import check_verify, run_verify, verify_inputs
 from parity import check_guards, compare, empty_like_dev, host, store, to_dev
 
 pytestmark = pytest.mark.gpu
@@ -255,6 +255,20 @@ def test_verify_low_temperatures(V, dtype, T, branch):
     x = store(ref.f64(t) * 3 + 7, dtype), store(ref.f64(d) * 3 + 7, dtype)
     want = check_verify(*x, redraw(x[1], par, temps, rng), u, e, par, temps)
     assert (want[0][:, 0] >= 0).all() and want[2].max() > 0
+
+
+@pytest.mark.parametrize("V", [200, 300001])
+@pytest.mark.parametrize("branch", [0, 3])
+def test_verify_undefined_draft_rows(V, branch):
+    """A NaN or +inf in the draft's row: no child is accepted, and the token is that of a
+    sequence in which nothing was drafted."""
+    t, d, tok, u, e, par, T = verify_inputs(4, 5, V, "f32", V, branch)
+    d[0, 0, 3], d[1, 0, V - 1], d[2, 0] = np.nan, np.inf, np.nan
+    got = run_verify(t, d, tok, u, e, par, T)
+    none = run_verify(t, d, np.full_like(tok, -1), u, e, par, T)
+    for a, b in zip(got, none):
+        assert (a[:3] == b[:3]).all()
+    assert (got[0][:3, 0] >= 0).all()
 
 
 # ---------------------------------------------------------------- attention ---
