@@ -330,8 +330,8 @@ rr_status rr_attention_fwd(const void *q, const void *k, const void *v, void *o,
  * column still counts as listed).  A row with no entry present (without a tail:
  * none of finite weight), or fully masked logits, gets loss 0 and dlogits 0.
  * A NaN or +inf logit, or a NaN value, makes the loss and dlogits of a row with an
- * entry present NaN.  The tail term is left out of a row whose unlisted columns hold none of the
- * student's mass (all below 2^-126 of its largest probability).
+ * entry present NaN.  The tail term is left out of a row whose unlisted columns hold
+ * none of the student's mass (all below 2^-126 of its largest probability).
  */
 rr_status rr_distill_fwd_bwd(const void *logits, const int32_t *top_index,
                              const float *top_value, const float *grad, float *loss,
@@ -376,7 +376,10 @@ size_t rr_attention_tree_workspace_size(int64_t batch, int64_t nodes, int64_t he
  *           ignored.  Calls that may overlap on the GPU need one each.
  * A row that sees nothing gets o = 0 and lse = -inf.  Positions beyond the
  * table, or on a page outside [0, pages), are not seen.  What stands at unseen
- * positions (NaN or infinities too) changes nothing.
+ * positions (NaN or infinities too) changes nothing.  Products on the tensor cores
+ * (bf16 in, fp32 accumulate), softmax in fp32, its weights rounded to bf16 for their
+ * product with V (page sizes that are no multiple of 16: kept in fp32).  The scores
+ * scale q . k are below 2^30 in magnitude.
  */
 rr_status rr_attention_tree_fwd(const void *q, const void *k_cache, const void *v_cache,
                                 const int32_t *page_table, const int32_t *context_len,
@@ -406,12 +409,15 @@ rr_status rr_attention_tree_fwd(const void *q, const void *k_cache, const void *
  *   tokens : [batch x nodes] int32; a token outside [0, cols) marks an absent
  *           node (never accepted, its siblings are tried as if it were not there).
  *   parents : [batch x nodes] int32 as for rr_attention_tree_fwd, or NULL (a chain).
- *   uniform : [batch x nodes] float32 in [0, 1).  race : [batch x cols] float32 > 0.
+ *   uniform : [batch x nodes] float32 in [0, 1).  race : [batch x cols] float32,
+ *           2^-126 to 2^126.
  *   temperature : [batch] float32, or NULL (1).  <= 0: greedy, p and q are all on
  *           their row's largest logit (the lowest index at a tie).  So the first
  *           child tried is accepted iff it is the target's largest, a later one iff
  *           it is and the draft's largest is another; the last token is the
- *           target's largest.  Otherwise finite and >= 2^-120.
+ *           target's largest.  So list a greedy tree's siblings by the draft's logit,
+ *           the largest first: then no child that is the target's choice is refused.
+ *           Otherwise finite and >= 2^-120.
  *   out_tokens : [batch x (nodes + 1)] int32, the accepted tokens, the last
  *           token, then -1.  out_nodes : [batch x (nodes + 1)] int32, the nodes
  *           of the accepted tokens, then -1.  out_count : [batch] int32, how many
@@ -419,7 +425,10 @@ rr_status rr_attention_tree_fwd(const void *q, const void *k_cache, const void *
  *   At most 65535 nodes; cols < 2^31.
  * Rows of nodes that are not reached change nothing.  A target row without a
  * finite logit, or with a NaN or +inf one where it is softmaxed, ends the walk
- * with the last token -1.
+ * with the last token -1.  A draft row with a NaN or +inf one has no child accepted,
+ * and the last token is drawn from p.  Probabilities and quotients are float32: where
+ * two sides of a test, or two scores, are equal within their rounding (some 1e-6,
+ * relative), either answer may come, and another for rows that another kernel takes.
  */
 rr_status rr_draft_verify(const void *target_logits, const void *draft_logits,
                           const int32_t *tokens, const int32_t *parents, const float *uniform,

@@ -20,11 +20,13 @@
 // (M Zt - tt Z = sum t Zt - tt Zl).  By the first forms the loss was off by up to 1e-3
 // there (2-norm over the rows), by these 7e-6.
 //
-// A bit filter of up to 2^16 bits in shared memory holds (column mod its size)
-// of the listed columns; a column whose bit is clear is unlisted, one whose bit
-// is set is looked up in the list (only rows longer than the filter ever find
-// it is not there).  Listed columns are stored again after the row's sweep, by
-// the one thread whose entry is the first with that column.
+// Two kernels: one of rows in registers (below), and for rows whose logits and
+// gradients differ in alignment, or that a cluster cannot hold, one of single-element
+// accesses.  There a bit filter of up to 2^16 bits in shared memory holds (column mod
+// its size) of the listed columns; a column whose bit is clear is unlisted, one whose
+// bit is set is looked up in the list (only rows longer than the filter ever find it is
+// not there).  Listed columns are stored again after the row's sweep, by the one
+// thread whose entry is the first with that column.
 #include <cstdint>
 
 #include "rr_device.cuh"
@@ -234,10 +236,10 @@ __global__ void __launch_bounds__(kDistT) distill_rows_kernel(const DistillParam
 // entries, 357 us with 64 a row, 451 us with 128 (54 rows a block).
 //
 // Bound: HBM (a row in, a row out), where a block has rows enough: 8192 x 50304 bf16
-// with 64 entries 252 us, 96 % of the copy bandwidth.  With a tail and 100 entries
-// (2048 x 50304, 13-14 rows a block) 89 us, 68 %: a row's chain of maximum, sum,
-// meeting and outputs, 4.4 us, is longer than its traffic.  In clusters the
-// meeting adds 1 us to that: 255 x 65537 fp32 33 us, 60 %.
+// with 64 entries 251 us, 97 % of the copy bandwidth.  With a tail and 100 entries
+// (2048 x 50304, 13-14 rows a block) 82 us, 74 %: a row's chain of maximum, sum,
+// meeting and outputs, 5.8 us, is longer than its traffic, 4.4.  In clusters the
+// meeting adds 1 us to that: 255 x 65537 fp32 29 us, 68 %.  (Replayed in a graph.)
 //
 // Bits of the listed columns of a slice, by place in the slice, tell the list warp
 // whether a column came twice.  (They also told the row warps which lanes to leave out

@@ -30,11 +30,16 @@
 // and so are non-finite values at nodes (0 x inf would be NaN for rows that do not
 // see the node); rows that do see such a node get the values added at the end.
 //
+// The softmax weights are rounded to bf16 before P V, since both operands of that
+// product have V's type (their sum stays in fp32): o is 0.0023 off float64 (2-norm), its
+// own rounding to bf16 alone is 0.0017.  A weight split into two bf16 would double the
+// product.
+//
 // Measured (in a graph): 64 sequences of 500-8000 keys, one token, 32 heads over 8 of
-// 128: 172 us, 95 % of the copy bandwidth; one such sequence of 4001: 14.4 us, a
+// 128: 171 us, 96 % of the copy bandwidth; one such sequence of 4001: 14.5 us, a
 // piece's latency and the join's; 16 trees of 30 nodes, 16 heads over 4 of 64, over
-// 1000-4100 keys 24.4 us, the same; 8 trees of 62 nodes, 64 heads over 8, over
-// 12000-20000 keys 229 us, 56 % of the bf16 rate (k_attn.cu's 54 % on long causal
+// 1000-4100 keys 24.8 us, the same; 8 trees of 62 nodes, 64 heads over 8, over
+// 12000-20000 keys 225 us, 57 % of the bf16 rate (k_attn.cu's 54 % on long causal
 // heads): the pipelines' tiles follow one another every 1570 cycles, of which the
 // softmax works 1250, and the issuers of S and P V are held 870 and 480 by the tensor
 // pipe's queue.  Tried and slower there: half of Q in TMEM for less shared memory
@@ -42,7 +47,8 @@
 // 246 us; a pipeline's prologue and epilogue are the other's tiles' time).
 //
 // Page sizes that are not a multiple of 16 go to a kernel of one warp per query
-// row.
+// row, a key at a time: the 64 sequences above take 9.9 ms with a page size of 1, 9.7
+// with 5.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>

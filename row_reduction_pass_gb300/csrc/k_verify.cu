@@ -35,7 +35,7 @@
 // meeting), so the first child's rows are loaded while its parent's are worked
 // on; with many it is bound by memory, several clusters share an SM, and nothing
 // is loaded that the walk does not reach.  Measured (in a graph): one chain of 5 over
-// 50304 bf16 columns 19.6 us, 8 trees of 39 over 65537 fp32 columns 24.7 us, 256 chains
+// 50304 bf16 columns 19 us, 8 trees of 39 over 65537 fp32 columns 25.7 us, 256 chains
 // of 8 over 50304 88 us (the cluster's meetings and exponentials; reading the rows
 // visited takes 32).  Rows that a cluster cannot hold go to
 // a kernel of one block per sequence that reads them again for every pass.
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kVerT) verify_kernel_t(const VerifyParams p) {
 // meeting for each rejection -> next node, or the draw (a pass and a meeting).
 // Measured on one chain of 50304 bf16 columns (K = 8): first version, 256 threads
 // and an IEEE division per column in the draw, 2800 cycles for the statistics and
-// 10000 for the draw (29 us; now 19.6); hence the packed exponents, the chunk-wise maxima (a token
+// 10000 for the draw (29 us; now 19); hence the packed exponents, the chunk-wise maxima (a token
 // is only looked for in a chunk that beats the best so far), and a warp of its own
 // that issues the loads (the address arithmetic and the copies held its warp up for
 // 1300 cycles a node).
@@ -704,6 +704,7 @@ __global__ void __launch_bounds__(kVerClT, 4) verify_cluster_kernel(const Verify
         agree(mbar_wait_bounded(noise_bar, 0, p.err));
         ns = reinterpret_cast<const float*>(smem + g.noise_off + nh);
       }
+      // (a quotient within 2 steps: the weights themselves are some steps off)
       auto score = [&](float w, float e) { return w > 0.f ? __fdividef(w, e) : -1.f; };
 #pragma unroll 1
       for (;; ratio = 0.f) {  // from the residual; from p where it holds nothing

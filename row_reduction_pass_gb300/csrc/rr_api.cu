@@ -1247,11 +1247,14 @@ rr_status check_shape(int64_t rows, int64_t cols, rr_dtype dt) {
 // ------------------------------------- the draft model's operators: launch ----
 
 // The streaming kernel's launch: row threads for at most kDistNQ chunks each,
-// rounded up to whole warps, plus the list warp; a cluster of K blocks where one
-// block cannot hold the row twice, or where splitting rows over more SMs ends
-// earlier (few rows).  The cost of a shape is its rounds of rows times a row's
-// share of a block in chunks, plus what a row costs whatever its length, the
-// meeting over its statistics (1024 chunks' time, in a cluster 1536).  K stays 0
+// rounded up to whole warps, plus a merge warp and two list warps; a cluster of K
+// blocks where one block cannot hold the row twice, or where splitting rows over more
+// SMs ends earlier (few rows).  The cost of a shape is its rounds of rows times a
+// row's share of a block in chunks, plus what a row costs whatever its length, the
+// meeting over its statistics (1024 chunks' time, in a cluster 1536).  The list's
+// length is not in it: of the shapes swept its choice was the best or within 1 %, but
+// for 4096 x 32000 fp32 with full lists of 128 entries (K = 3 223 us, K = 4 200; cold
+// calls), which want the L1 cache that two blocks of 99 KB leave little of.  K stays 0
 // where no shape holds the row.
 struct DistillShape {
   int K = 0, T = 0;
@@ -1382,8 +1385,11 @@ rr_status distill_launch(rr::DistillParams p, rr_dtype dt, cudaStream_t stream) 
 // trees of 65537 fp32 columns: K = 8 24.8 us, with one buffer 26.5, K = 4 34).  With
 // many: the largest K whose blocks are at most twice what the chip holds at four a SM,
 // one buffer (256 chains: K = 4 91 us, K = 8 117, with two buffers 154; 48 chains of
-// 131072 bf16 columns: K = 8 51 us, with two buffers 76, K = 4 67).  No cluster where
-// the slices do not fit.
+// 131072 bf16 columns: K = 8 51 us, with two buffers 76, K = 4 67).  (Each group taken
+// with one state of the kernel, the first and the third before its last steps.)  Blocks
+// of long slices are fewer than four a SM, which the rule does not look at: 700 chains
+// of 5 over 50304 columns, K = 1, one block a SM, take 275 us, 3.4 times their traffic,
+// where 300 (K = 4) take 84, 2.4 times.  No cluster where the slices do not fit.
 rr_status verify_launch(rr::VerifyParams p, rr_dtype dt, cudaStream_t stream) {
   const rr::VerifyKernels vk = rr::verify_kernels(dt);
   const int64_t E = dt == RR_BF16 ? 2 : 4;
