@@ -17,12 +17,16 @@
  *   rr_distill_fwd_bwd       distillation loss and dlogits from a teacher's top entries
  *   rr_attention_tree_fwd    attention of a tree of new tokens over a paged cache
  *   rr_draft_verify          acceptance of drafted tokens against the target
+ *   rr_qk_norm_rope_fwd, rr_qk_norm_rope_bwd    norms of queries and keys with the rotation
+ *   rr_attention_packed_fwd, rr_attention_packed_bwd   causal attention, packed sequences
+ *   rr_token_logprob_fwd, rr_token_logprob_bwd  log probabilities of given tokens
  *   rr_layernorm_bwd_noalloc the LayerNorm backward without a caller workspace
  *   rr_selftest_bounded_wait, rr_read_device_error   the bounded device waits
  *
  * Common conventions
  *   - Every tensor is dense, row-major [rows x cols] with row stride = cols
- *     (per-column vectors are [cols], per-row vectors are [rows]).
+ *     (per-column vectors are [cols], per-row vectors are [rows]), but where an
+ *     argument named *_stride says how many elements lie between rows.
  *   - Every pointer is a DEVICE pointer on the current CUDA device, allocated
  *     and owned by the caller; the library allocates nothing and keeps no state
  *     beyond a per-device cache of attributes (and the fixed scratch array of
@@ -435,6 +439,177 @@ rr_status rr_draft_verify(const void *target_logits, const void *draft_logits,
                           const float *race, const float *temperature, int32_t *out_tokens,
                           int32_t *out_nodes, int32_t *out_count, int64_t batch, int64_t nodes,
                           int64_t cols, rr_dtype dtype, cudaStream_t stream);
+
+/*
+ * Norms of queries and keys, head by head, and the position rotation, in one pass
+ * (RMSNorm of rr_rmsnorm_fwd over each head; rotary position embedding, Su et al.
+ * 2021).  For each token and head, with x its head_dim values and w the weight:
+ *   u = x w / sqrt(mean(x^2) + eps),
+ *   y_a = cos u_a - sin u_b,  y_b = sin u_a + cos u_b  for the pairs p < rot_dim / 2,
+ *   (a, b) = (p, p + rot_dim / 2), or (2p, 2p + 1) if interleaved; the elements from
+ *   rot_dim on are not rotated (y = u).
+ *   q, q_out : [tokens x heads x head_dim] dtype; k, k_out : [tokens x kv_heads x
+ *           head_dim]; a token's heads are dense, tokens *_stride elements apart (views
+ *           of a fused projection).  An output may be its input (written in place);
+ *           other overlap is an error.  kv_heads == 0: k, k_out may be NULL.
+ *   q_weight, k_weight : [head_dim] dtype, or NULL (1).
+ *   cos, sin : [max_positions x rot_dim / 2] float32.
+ *   positions : [tokens] int32 row of the table, or NULL (the token's index).
+ *   bad_position_count : nullable device int32; each token with a position >=
+ *           max_positions adds 1, and its rotated elements are NaN.
+ *   head_dim even, at most 256; rot_dim even, 2 .. head_dim; at most 65535 heads;
+ *   eps >= 0 and finite.
+ * A token with a negative position (padding) gets zeros, and so does a head whose mean
+ * square is not finite, or zero with eps == 0.
+ */
+rr_status rr_qk_norm_rope_fwd(const void *q, const void *k, const void *q_weight,
+                              const void *k_weight, const float *cos, const float *sin,
+                              const int32_t *positions, void *q_out, void *k_out,
+                              int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                              int64_t rot_dim, int64_t max_positions, int64_t q_stride,
+                              int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride,
+                              float eps, int interleaved, int32_t *bad_position_count,
+                              rr_dtype dtype, cudaStream_t stream);
+
+/* Bytes of device workspace rr_qk_norm_rope_bwd needs for these sizes; 0 if none,
+ * or if the arguments are invalid.  Depends on the current device. */
+size_t rr_qk_norm_rope_bwd_workspace_size(int64_t tokens, int64_t heads, int64_t kv_heads,
+                                          int64_t head_dim);
+
+/*
+ * Gradient of rr_qk_norm_rope_fwd (its arguments have the same meaning and limits).
+ * With g the gradient of a head's output turned back by the token's angles, r the
+ * head's 1 / sqrt(mean(x^2) + eps) (computed again from q, k) and xh = x r:
+ *   dx = r (g w - xh mean(g w xh)),   dw = sum over tokens and heads of g xh.
+ *   dq_out, dk_out : gradients of q_out, k_out.  dq, dk : gradients of q, k; each may be
+ *           the gradient it comes from, or q / k (written in place); other overlap is
+ *           an error.
+ *   dq_weight, dk_weight : [head_dim] dtype, or both NULL (not computed).
+ *   workspace : device scratch of workspace_bytes >= the size query's answer (16-byte
+ *           aligned), owned by the caller; its contents on entry are ignored.  Calls
+ *           that may overlap on the GPU need one each.  Without weight gradients: NULL.
+ * Heads that the forward set to zero get dx = 0 and add nothing to dw, which is summed
+ * in a fixed order (the same bits at every run).  Positions beyond the table: NaN.
+ */
+rr_status rr_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q, const void *k,
+                              const void *q_weight, const void *k_weight, const float *cos,
+                              const float *sin, const int32_t *positions, void *dq, void *dk,
+                              void *dq_weight, void *dk_weight, void *workspace,
+                              size_t workspace_bytes, int64_t tokens, int64_t heads,
+                              int64_t kv_heads, int64_t head_dim, int64_t rot_dim,
+                              int64_t max_positions, int64_t dq_out_stride, int64_t dk_out_stride,
+                              int64_t q_stride, int64_t k_stride, int64_t dq_stride,
+                              int64_t dk_stride, float eps, int interleaved,
+                              int32_t *bad_position_count, rr_dtype dtype, cudaStream_t stream);
+
+/*
+ * Causal attention over packed sequences of differing lengths, with grouped heads: the
+ * attention of whole prompts and of training (rr_attention_tree_fwd has the form for
+ * single new tokens over a cache).  Sequence b is the tokens cu_seqlens[b] ..
+ * cu_seqlens[b + 1] - 1; for its token i and head h (key head h / (heads / kv_heads)),
+ * over the tokens j <= i of the sequence,
+ *   o = sum_j softmax(scale q_i . k_j)_j v_j,   lse = log sum_j exp(scale q_i . k_j).
+ *   q, o : [tokens x heads x head_dim] dtype; k, v : [tokens x kv_heads x head_dim]; a
+ *           token's heads are dense, tokens *_stride elements apart.  16-byte aligned
+ *           tensors whose strides and rows (head_dim) are whole 16-byte chunks.  o must
+ *           not overlap another tensor.
+ *   cu_seqlens : [batch + 1] int32, not decreasing, within 0 .. tokens (bounds outside
+ *           are taken as the nearest; of decreasing bounds the results are not
+ *           specified).  Sequences may be empty.  Rows of o and lse outside every
+ *           sequence are left as they were.
+ *   lse : [heads x tokens] float32, or NULL.
+ *   head_dim at most 256; heads a multiple of kv_heads, at most 65535; batch at most
+ *   2^20, tokens below 2^31; scale > 0 and finite.  |scale q . k| below 2^30.
+ * bf16 with head_dim 64 or 128 runs on the tensor cores (fp32 accumulate; weights rounded
+ * to bf16 for their product with v); other head dimensions and float32 on plain kernels.
+ * What stands at unseen tokens (NaN or infinities too) changes nothing.
+ */
+rr_status rr_attention_packed_fwd(const void *q, const void *k, const void *v,
+                                  const int32_t *cu_seqlens, void *o, float *lse, int64_t tokens,
+                                  int64_t batch, int64_t heads, int64_t kv_heads,
+                                  int64_t head_dim, int64_t q_stride, int64_t k_stride,
+                                  int64_t v_stride, int64_t o_stride, float scale, rr_dtype dtype,
+                                  cudaStream_t stream);
+
+/* Bytes of device workspace rr_attention_packed_bwd needs for these sizes; 0 if
+ * none, or if the arguments are invalid. */
+size_t rr_attention_packed_bwd_workspace_size(int64_t tokens, int64_t heads);
+
+/*
+ * Gradient of rr_attention_packed_fwd (arguments of the same names have the same
+ * meaning and limits).  With p = exp(scale q . k - lse), delta = dout . o and
+ * ds = p (dout . v - delta):
+ *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i,
+ * dk and dv over the tokens i of the sequence that see j and all heads of the key head.
+ *   dout : gradient of o.  o, lse : what the forward gave for these q, k, v, scale.
+ *   dq, dk, dv : gradients, of the shapes of q, k, v; they must not overlap another
+ *           tensor (three views of one fused buffer, side by side, do not).
+ *   workspace : device scratch of workspace_bytes >= the size query's answer (16-byte
+ *           aligned), owned by the caller; its contents on entry are ignored.  Calls
+ *           that may overlap on the GPU need one each.
+ * Rows outside every sequence are left as they were, and nothing there or in another
+ * sequence changes a sequence's gradients.  Every sum has a fixed order (the same bits at
+ * every run).  On the tensor cores p and ds are rounded to bf16 for their products.  A NaN
+ * or infinity in a sequence may reach any gradient of that sequence.
+ */
+rr_status rr_attention_packed_bwd(const void *dout, const void *q, const void *k, const void *v,
+                                  const void *o, const float *lse, const int32_t *cu_seqlens,
+                                  void *dq, void *dk, void *dv, void *workspace,
+                                  size_t workspace_bytes, int64_t tokens, int64_t batch,
+                                  int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                  int64_t dout_stride, int64_t q_stride, int64_t k_stride,
+                                  int64_t v_stride, int64_t o_stride, int64_t dq_stride,
+                                  int64_t dk_stride, int64_t dv_stride, float scale,
+                                  rr_dtype dtype, cudaStream_t stream);
+
+/*
+ * Log probabilities of given tokens, with what a sampler or a policy's loss wants beside
+ * them, from one pass over each row.  With z = logits / temperature, t the row's token:
+ *   logprob  = z_t - log sum_j exp z_j,
+ *   entropy  = -sum_j p_j ln p_j,  p = softmax(z),
+ *   row_max  = max_j logits_j,  log_sum = ln sum_j exp(z_j - row_max / temperature)
+ *              (both kept for rr_token_logprob_bwd; their sum, row_max / temperature +
+ *              log_sum, is the row's log-sum-exp),
+ *   rank     = how many columns are before t by (logit descending, column ascending),
+ *   top_index, top_logprob = the first k columns in that order, and their log
+ *              probabilities.
+ *   logits : [rows x cols] dtype, rows logits_stride >= cols elements apart.
+ *   tokens : [rows] int32.  A row whose token is ignore_index is not read: it gets 0 (rank
+ *           and top_index -1).
+ *   logprob : [rows] float32; entropy, row_max, log_sum ([rows] float32) and rank ([rows]
+ *           int32) may be NULL.  top_index, top_logprob : [rows x k] int32 and float32,
+ *           0 <= k <= 128 (k == 0: NULL).
+ *   temperature : 2^-120 to 2^120.
+ *   bad_token_count : nullable device int32; each token outside [0, cols) (and not
+ *           ignored) adds 1; such a row gets logprob NaN and rank -1.
+ * Columns of -inf are not listed; places of the list that are left get index -1 and
+ * -inf.  A row of nothing but -inf gets logprob, entropy and log_sum 0, row_max -inf and an
+ * empty list.  A row with a NaN or +inf gets NaN, rank -1 and top_index -1.
+ */
+rr_status rr_token_logprob_fwd(const void *logits, const int32_t *tokens, float *logprob,
+                               float *entropy, float *row_max, float *log_sum, int32_t *rank,
+                               int32_t *top_index, float *top_logprob, int64_t rows, int64_t cols,
+                               int64_t logits_stride, int64_t k, float temperature,
+                               int32_t ignore_index, int32_t *bad_token_count, rr_dtype dtype,
+                               cudaStream_t stream);
+
+/*
+ * Gradient of rr_token_logprob_fwd's logprob and entropy:
+ *   dlogits_j = [g (1_{j=t} - p_j) - h p_j (ln p_j + entropy)] / temperature.
+ *   row_max, log_sum, entropy : [rows] float32 from the forward (same temperature).
+ *   grad_logprob (g), grad_entropy (h) : [rows] float32, or NULL (0); entropy may be NULL
+ *           where grad_entropy is.
+ *   dlogits : [rows x cols] dtype, rows dlogits_stride apart; may be logits, with the
+ *           same stride (written in place); other overlap is an error.
+ * A row whose token is ignore_index, or of nothing but -inf, gets 0.  A token outside
+ * [0, cols) adds no 1_{j=t}.
+ */
+rr_status rr_token_logprob_bwd(const void *logits, const int32_t *tokens, const float *row_max,
+                               const float *log_sum, const float *entropy,
+                               const float *grad_logprob, const float *grad_entropy, void *dlogits,
+                               int64_t rows, int64_t cols, int64_t logits_stride,
+                               int64_t dlogits_stride, float temperature, int32_t ignore_index,
+                               rr_dtype dtype, cudaStream_t stream);
 
 /*
  * Self-test of the bounded device-side waits (a diagnostic of this library;

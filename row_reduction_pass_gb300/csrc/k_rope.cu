@@ -1,0 +1,348 @@
+// k_rope.cu -- norms of queries and keys, head by head, with the position rotation in
+// the same pass, and its gradient.
+//
+// A row is one head of one token, D elements.  With x its values, w the weight that all
+// heads share and (c, s) the cosine and sine of the token's angle for a pair (a, b):
+//   r = 1 / sqrt(sum x^2 / D + eps),  u = x r w,
+//   y_a = c u_a - s u_b,  y_b = s u_a + c u_b   (elements behind the rotated ones: y = u),
+// and backward, with g = the pair turned back by its angle:
+//   dw = sum over rows of g x r,  h = g w,  dx = r (h - x r mean(h x r)).
+// Nothing is saved between the two: the row is in registers anyway when r is needed.
+//
+// A lane owns a slot of a row: two chunks of W elements that hold W whole pairs (halves:
+// chunk j and the one R / 2 elements on; neighbours: two adjacent chunks), so the rotation
+// needs no exchange and the row's one sum is a butterfly over its D / 2W lanes.  A warp
+// takes 32 / G heads of one token at a time and walks over the token's heads, queries
+// then keys, with the token's cosines and sines in registers.
+#include <cstdint>
+
+#include "rr_device.cuh"
+#include "rr_kernels.h"
+
+namespace rr {
+namespace {
+
+constexpr int kThreads = 256;
+
+// What a lane keeps of the row's layout: element offsets of its slots.
+template <int W, int NS>
+struct Slots {
+  int ea[NS], eb[NS], ang[NS];
+  bool on[NS], rot[NS];
+  __device__ __forceinline__ Slots(int gl, const RopeParams& p) {
+    const int n2 = p.dim / (2 * W), nrot = p.rot / (2 * W);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int s = gl + i * p.group;
+      on[i] = s < n2;
+      rot[i] = s < nrot;
+      ang[i] = s * W;
+      if (p.interleaved) {
+        ea[i] = 2 * s * W;
+        eb[i] = ea[i] + W;
+      } else if (rot[i]) {
+        ea[i] = s * W;
+        eb[i] = p.rot / 2 + s * W;
+      } else {
+        ea[i] = p.rot + 2 * (s - nrot) * W;
+        eb[i] = ea[i] + W;
+      }
+    }
+  }
+};
+
+template <int DT, int W>
+__device__ __forceinline__ void load(float (&f)[W], const char* p) {
+  if constexpr (W == 1) {
+    f[0] = ld_elem<DT>(p);
+  } else {
+    const uint4 c = ld_chunk_stream(p);
+#pragma unroll
+    for (int i = 0; i < W; ++i) f[i] = chunk_get<DT>(c, i);
+  }
+}
+template <int DT, int W>
+__device__ __forceinline__ void load_cached(float (&f)[W], const char* p) {
+  if constexpr (W == 1) {
+    f[0] = ld_elem_cached<DT>(p);
+  } else {
+    const uint4 c = ld_chunk_cached(p);
+#pragma unroll
+    for (int i = 0; i < W; ++i) f[i] = chunk_get<DT>(c, i);
+  }
+}
+template <int DT, int W>
+__device__ __forceinline__ void store(char* p, const float (&f)[W]) {
+  if constexpr (W == 1)
+    st_elem<DT>(p, f[0]);
+  else
+    *reinterpret_cast<uint4*>(p) = chunk_pack<DT>(f);
+}
+
+// Turns the slot's pairs by (c, s).
+template <int W>
+__device__ __forceinline__ void turn(float (&a)[W], float (&b)[W], const float (&c)[W],
+                                     const float (&s)[W], bool neighbours) {
+  if (W > 1 && neighbours) {
+    float u[2 * W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) u[i] = a[i], u[W + i] = b[i];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float x = u[2 * i], y = u[2 * i + 1];
+      u[2 * i] = c[i] * x - s[i] * y;
+      u[2 * i + 1] = s[i] * x + c[i] * y;
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) a[i] = u[i], b[i] = u[W + i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float x = a[i], y = b[i];
+      a[i] = c[i] * x - s[i] * y;
+      b[i] = s[i] * x + c[i] * y;
+    }
+  }
+}
+
+__device__ __forceinline__ float group_sum(float v, int group) {
+  for (int off = group >> 1; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// The token's angles for this lane's slots; out of the table: NaN, counted once a token.
+template <int W, int NS>
+__device__ __forceinline__ void angles(float (&c)[NS][W], float (&s)[NS][W],
+                                       const Slots<W, NS>& sl, const RopeParams& p, int pos) {
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+#pragma unroll
+    for (int e = 0; e < W; ++e) c[i][e] = 1.f, s[i][e] = 0.f;
+    if (!sl.rot[i]) continue;
+    if (pos < 0 || pos >= p.positions_n) {
+#pragma unroll
+      for (int e = 0; e < W; ++e) c[i][e] = s[i][e] = __int_as_float(0x7fc00000);
+    } else {
+      const int64_t at = (int64_t)pos * (p.rot / 2) + sl.ang[i];
+      if constexpr (W == 1) {
+        c[i][0] = __ldg(p.cos + at);
+        s[i][0] = __ldg(p.sin + at);
+      } else {
+#pragma unroll
+        for (int e = 0; e < W; e += 4) {
+          const float4 cv = __ldg(reinterpret_cast<const float4*>(p.cos + at + e));
+          const float4 sv = __ldg(reinterpret_cast<const float4*>(p.sin + at + e));
+          c[i][e] = cv.x, c[i][e + 1] = cv.y, c[i][e + 2] = cv.z, c[i][e + 3] = cv.w;
+          s[i][e] = sv.x, s[i][e + 1] = sv.y, s[i][e + 2] = sv.z, s[i][e + 3] = sv.w;
+        }
+      }
+    }
+  }
+}
+
+template <int DT, int W, int NS>
+__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeParams p) {
+  constexpr int E = DType<DT>::E;
+  const int lane = threadIdx.x & 31;
+  const int gl = lane & (p.group - 1), sub = lane / p.group, per = 32 / p.group;
+  const int rows = p.heads + p.kv_heads;
+  const Slots<W, NS> sl(gl, p);
+  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+  const int64_t units = p.tokens * p.segs;
+  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < units;
+       u += warps) {
+    const int64_t t = u / p.segs;
+    const int seg = (int)(u - t * p.segs);
+    const int pos = p.positions ? __ldg(p.positions + t) : (int)t;
+    if (pos >= p.positions_n && seg == 0 && lane == 0 && p.bad) atomicAdd(p.bad, 1);
+    float c[NS][W], s[NS][W];
+    angles<W, NS>(c, s, sl, p, pos);
+    const int last = min(rows, (seg + 1) * p.seg_rows);
+    for (int r0 = seg * p.seg_rows; r0 < last; r0 += per) {
+      const int h = r0 + sub;
+      const bool live = h < last, isq = h < p.heads;
+      const int64_t in = (isq ? t * p.q_stride + (int64_t)h * p.dim
+                              : t * p.k_stride + (int64_t)(h - p.heads) * p.dim) * E;
+      const char* x = (isq ? p.q : p.k) + in;
+      float a[NS][W], b[NS][W];
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) a[i][e] = b[i][e] = 0.f;
+        if (live && sl.on[i]) {
+          load<DT, W>(a[i], x + (int64_t)sl.ea[i] * E);
+          load<DT, W>(b[i], x + (int64_t)sl.eb[i] * E);
+        }
+#pragma unroll
+        for (int e = 0; e < W; ++e) ss += a[i][e] * a[i][e] + b[i][e] * b[i][e];
+      }
+      const float ms = group_sum(ss, p.group) * p.inv_dim;
+      const bool keep = pos >= 0 && ms <= 3.402823466e38f && ms + p.eps > 0.f;
+      const float r = keep ? rsqrtf(ms + p.eps) : 0.f;
+      if (!live) continue;
+      const int64_t out = (isq ? t * p.qo_stride + (int64_t)h * p.dim
+                               : t * p.ko_stride + (int64_t)(h - p.heads) * p.dim) * E;
+      char* y = (isq ? p.qo : p.ko) + out;
+      const char* w = isq ? p.qw : p.kw;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        if (!sl.on[i]) continue;
+        if (keep) {
+          float wa[W], wb[W];
+#pragma unroll
+          for (int e = 0; e < W; ++e) wa[e] = wb[e] = 1.f;
+          if (w) {
+            load_cached<DT, W>(wa, w + sl.ea[i] * E);
+            load_cached<DT, W>(wb, w + sl.eb[i] * E);
+          }
+#pragma unroll
+          for (int e = 0; e < W; ++e) a[i][e] *= r * wa[e], b[i][e] *= r * wb[e];
+          turn<W>(a[i], b[i], c[i], s[i], p.interleaved);
+        } else {
+#pragma unroll
+          for (int e = 0; e < W; ++e) a[i][e] = b[i][e] = 0.f;
+        }
+        store<DT, W>(y + (int64_t)sl.ea[i] * E, a[i]);
+        store<DT, W>(y + (int64_t)sl.eb[i] * E, b[i]);
+      }
+    }
+  }
+}
+
+// dx of every row, and this block's sums over its rows of g x r for the two weights, in
+// workspace row blockIdx.x ([2][D] floats), which col_reduce_kernel adds up.
+template <int DT, int W, int NS>
+__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const RopeParams p) {
+  constexpr int E = DType<DT>::E;
+  extern __shared__ float part[];  // [warps][2][D]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gl = lane & (p.group - 1), sub = lane / p.group, per = 32 / p.group;
+  const int rows = p.heads + p.kv_heads;
+  const Slots<W, NS> sl(gl, p);
+  float acc[2][NS][2][W];
+#pragma unroll
+  for (int i = 0; i < 2 * NS * 2 * W; ++i) (&acc[0][0][0][0])[i] = 0.f;
+  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+  const int64_t units = p.tokens * p.segs;
+  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + warp; u < units; u += warps) {
+    const int64_t t = u / p.segs;
+    const int seg = (int)(u - t * p.segs);
+    const int pos = p.positions ? __ldg(p.positions + t) : (int)t;
+    if (pos >= p.positions_n && seg == 0 && lane == 0 && p.bad) atomicAdd(p.bad, 1);
+    float c[NS][W], s[NS][W];
+    angles<W, NS>(c, s, sl, p, pos);
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+      for (int e = 0; e < W; ++e) s[i][e] = -s[i][e];  // the turn back
+    const int last = min(rows, (seg + 1) * p.seg_rows);
+    for (int r0 = seg * p.seg_rows; r0 < last; r0 += per) {
+      const int h = r0 + sub;
+      const bool live = h < last, isq = h < p.heads;
+      const int64_t hd = (int64_t)(isq ? h : h - p.heads) * p.dim;
+      const char* x = (isq ? p.q : p.k) + (t * (isq ? p.q_stride : p.k_stride) + hd) * E;
+      const char* dy = (isq ? p.dyq : p.dyk) + (t * (isq ? p.dyq_stride : p.dyk_stride) + hd) * E;
+      const char* w = isq ? p.qw : p.kw;
+      float a[NS][W], b[NS][W], ga[NS][W], gb[NS][W];
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) a[i][e] = b[i][e] = ga[i][e] = gb[i][e] = 0.f;
+        if (live && sl.on[i]) {
+          load<DT, W>(a[i], x + (int64_t)sl.ea[i] * E);
+          load<DT, W>(b[i], x + (int64_t)sl.eb[i] * E);
+          load<DT, W>(ga[i], dy + (int64_t)sl.ea[i] * E);
+          load<DT, W>(gb[i], dy + (int64_t)sl.eb[i] * E);
+        }
+#pragma unroll
+        for (int e = 0; e < W; ++e) ss += a[i][e] * a[i][e] + b[i][e] * b[i][e];
+      }
+      const float ms = group_sum(ss, p.group) * p.inv_dim;
+      const bool keep = pos >= 0 && ms <= 3.402823466e38f && ms + p.eps > 0.f;
+      const float r = keep ? rsqrtf(ms + p.eps) : 0.f;
+      float dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        turn<W>(ga[i], gb[i], c[i], s[i], p.interleaved);
+        float wa[W], wb[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) wa[e] = wb[e] = 1.f;
+        if (w && sl.on[i]) {
+          load_cached<DT, W>(wa, w + sl.ea[i] * E);
+          load_cached<DT, W>(wb, w + sl.eb[i] * E);
+        }
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          a[i][e] *= r, b[i][e] *= r;
+          const float da = ga[i][e] * a[i][e], db = gb[i][e] * b[i][e];
+          if (keep && live) {
+            if (isq)
+              acc[0][i][0][e] += da, acc[0][i][1][e] += db;
+            else
+              acc[1][i][0][e] += da, acc[1][i][1][e] += db;
+          }
+          dot += da * wa[e] + db * wb[e];
+          ga[i][e] *= wa[e], gb[i][e] *= wb[e];
+        }
+      }
+      const float mean = group_sum(dot, p.group) * p.inv_dim;
+      if (!live) continue;
+      char* dx = (isq ? p.qo : p.ko) + (t * (isq ? p.qo_stride : p.ko_stride) + hd) * E;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        if (!sl.on[i]) continue;
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          a[i][e] = keep ? r * (ga[i][e] - a[i][e] * mean) : 0.f;
+          b[i][e] = keep ? r * (gb[i][e] - b[i][e] * mean) : 0.f;
+        }
+        store<DT, W>(dx + (int64_t)sl.ea[i] * E, a[i]);
+        store<DT, W>(dx + (int64_t)sl.eb[i] * E, b[i]);
+      }
+    }
+  }
+  if (p.ws == nullptr) return;
+  // the warp's row groups, then the block's warps, each in a fixed order
+#pragma unroll
+  for (int i = 0; i < 2 * NS * 2 * W; ++i) {
+    float v = (&acc[0][0][0][0])[i];
+    for (int off = p.group; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    (&acc[0][0][0][0])[i] = v;
+  }
+  if (sub == 0) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (sl.on[i])
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            part[(warp * 2 + k) * p.dim + sl.ea[i] + e] = acc[k][i][0][e];
+            part[(warp * 2 + k) * p.dim + sl.eb[i] + e] = acc[k][i][1][e];
+          }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * p.dim; i += kThreads) {
+    float v = 0.f;
+    for (int wv = 0; wv < kThreads / 32; ++wv) v += part[wv * 2 * p.dim + i];
+    p.ws[(int64_t)blockIdx.x * 2 * p.dim + i] = v;
+  }
+}
+
+}  // namespace
+
+RopeKernels rope_kernels(int dtype, bool vec) {
+  if (dtype == kF32)
+    return vec ? RopeKernels{(const void*)rope_fwd_kernel<kF32, 4, 1>,
+                             (const void*)rope_bwd_kernel<kF32, 4, 1>, kThreads}
+               : RopeKernels{(const void*)rope_fwd_kernel<kF32, 1, 4>,
+                             (const void*)rope_bwd_kernel<kF32, 1, 4>, kThreads};
+  return vec ? RopeKernels{(const void*)rope_fwd_kernel<kBF16, 8, 1>,
+                           (const void*)rope_bwd_kernel<kBF16, 8, 1>, kThreads}
+             : RopeKernels{(const void*)rope_fwd_kernel<kBF16, 1, 4>,
+                           (const void*)rope_bwd_kernel<kBF16, 1, 4>, kThreads};
+}
+
+}  // namespace rr

@@ -2351,6 +2351,590 @@ rr_status rr_attention_tree_fwd(const void* q, const void* k_cache, const void* 
 
 }  // extern "C"
 
+// ------------------------------------ packed sequences: norms, attention, tokens ----
+
+namespace {
+
+// A tensor of `rows` rows of `width` bytes, `stride` bytes apart.
+struct View {
+  const void* p;
+  int64_t rows, stride, width;
+};
+
+// Whether two such tensors share a byte: disjoint spans share none, nor do views side by
+// side in rows of one buffer (the same stride); anything else counts as shared.
+bool views_overlap(const View& a, const View& b) {
+  if (!a.p || !b.p || a.rows == 0 || b.rows == 0 || a.width == 0 || b.width == 0) return false;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t na = (uintptr_t)((a.rows - 1) * a.stride + a.width);
+  const uintptr_t nb = (uintptr_t)((b.rows - 1) * b.stride + b.width);
+  if (pa + na <= pb || pb + nb <= pa) return false;
+  if (a.stride != b.stride || a.stride <= 0) return true;
+  const int64_t s = a.stride;
+  const int64_t d = pb >= pa ? (int64_t)((pb - pa) % (uintptr_t)s)
+                             : (s - (int64_t)((pa - pb) % (uintptr_t)s)) % s;
+  return !(d >= a.width && d + b.width <= s);
+}
+bool same_view(const View& a, const View& b) { return a.p == b.p && a.stride == b.stride; }
+
+rr_status rope_shape(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim) {
+  if (tokens < 0) return fail(RR_ERR_INVALID_ARG, "tokens=%lld < 0", (long long)tokens);
+  if (heads < 1 || kv_heads < 0 || heads > 65535 || kv_heads > 65535)
+    return fail(RR_ERR_INVALID_ARG, "heads outside 1..65535 or kv_heads outside 0..65535");
+  if (head_dim < 2 || head_dim > 256 || head_dim % 2 != 0)
+    return fail(RR_ERR_INVALID_ARG, "head_dim must be even, 2..256");
+  if (tokens > INT32_MAX) return fail(RR_ERR_INVALID_ARG, "too many tokens");
+  return RR_OK;
+}
+
+// The checks both directions share, the kernel and the units of work.
+struct RopePlan {
+  rr::RopeKernels k;
+  bool vec;
+  int sms;
+};
+rr_status rope_plan(rr::RopeParams& p, rr_dtype dt, float eps, const int64_t* strides, int n,
+                    const void* const* tensors, RopePlan* out) {
+  const int E = dt == RR_BF16 ? 2 : 4, W = 16 / E;
+  bool vec = p.dim % (2 * W) == 0 && p.rot % (2 * W) == 0 && p.dim / (2 * W) <= 32 &&
+             aligned(p.qw, 16) && aligned(p.kw, 16) && aligned(p.cos, 16) && aligned(p.sin, 16);
+  for (int i = 0; i < n; ++i) {
+    vec = vec && aligned(tensors[i], 16) && strides[i] * E % 16 == 0;
+    if (!aligned(tensors[i], E)) return fail(RR_ERR_INVALID_ARG, "misaligned pointer");
+  }
+  DevInfo* di = nullptr;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    rr_status st = device_info(&di);
+    if (st != RR_OK) return st;
+    out->sms = di->sms;
+  }
+  out->vec = vec;
+  out->k = rr::rope_kernels(dt == RR_BF16 ? rr::kBF16 : rr::kF32, vec);
+  const int slots = vec ? p.dim / (2 * W) : std::min(32, p.dim / 2);
+  p.group = 1;
+  while (p.group < slots) p.group *= 2;
+  p.eps = eps;
+  p.inv_dim = 1.f / (float)p.dim;
+  return RR_OK;
+}
+// Cuts each token's heads into units until `warps` have one.
+void rope_units(rr::RopeParams& p, int64_t warps) {
+  const int rows = p.heads + p.kv_heads, per = 32 / p.group;
+  const int64_t its = cdiv(rows, per);
+  const int64_t segs = std::min(its, std::max<int64_t>(1, cdiv(warps, p.tokens)));
+  p.seg_rows = (int32_t)(cdiv(its, segs) * per);
+  p.segs = (int32_t)cdiv(rows, p.seg_rows);
+}
+
+constexpr int kRopeBwdBlocks = 2;  // a SM
+
+}  // namespace
+
+extern "C" {
+
+rr_status rr_qk_norm_rope_fwd(const void* q, const void* k, const void* q_weight,
+                              const void* k_weight, const float* cos, const float* sin,
+                              const int32_t* positions, void* q_out, void* k_out, int64_t tokens,
+                              int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t rot_dim,
+                              int64_t max_positions, int64_t q_stride, int64_t k_stride,
+                              int64_t q_out_stride, int64_t k_out_stride, float eps,
+                              int interleaved, int32_t* bad_position_count, rr_dtype dtype,
+                              cudaStream_t stream) {
+  if (dtype != RR_F32 && dtype != RR_BF16)
+    return fail(RR_ERR_UNSUPPORTED_DTYPE, "dtype %d", (int)dtype);
+  rr_status st = rope_shape(tokens, heads, kv_heads, head_dim);
+  if (st != RR_OK) return st;
+  if (rot_dim < 2 || rot_dim > head_dim || rot_dim % 2 != 0)
+    return fail(RR_ERR_INVALID_ARG, "rot_dim must be even, 2..head_dim");
+  if (max_positions < 0 || max_positions > INT32_MAX)
+    return fail(RR_ERR_INVALID_ARG, "max_positions outside 0..2^31-1");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(RR_ERR_INVALID_ARG, "bad eps");
+  const int64_t wq = heads * head_dim, wk = kv_heads * head_dim, cap = (int64_t)1 << 28;
+  if (q_stride < wq || q_out_stride < wq || k_stride < wk || k_out_stride < wk ||
+      q_stride > cap || q_out_stride > cap || k_stride > cap || k_out_stride > cap)
+    return fail(RR_ERR_INVALID_ARG, "a stride is shorter than a token's heads (or beyond 2^28)");
+  if (tokens == 0) return ok();
+  if (!q || !q_out || (kv_heads > 0 && (!k || !k_out)) || (max_positions > 0 && (!cos || !sin)))
+    return fail(RR_ERR_INVALID_ARG, "null pointer");
+  if (kv_heads == 0) k = nullptr, k_out = nullptr, k_weight = nullptr;
+  if (!aligned(cos, 4) || !aligned(sin, 4) || !aligned(positions, 4) ||
+      !aligned(bad_position_count, 4) || !aligned(q_weight, dtype == RR_BF16 ? 2 : 4) ||
+      !aligned(k_weight, dtype == RR_BF16 ? 2 : 4))
+    return fail(RR_ERR_INVALID_ARG, "misaligned pointer");
+  const int64_t E = dtype == RR_BF16 ? 2 : 4;
+  const View vq{q, tokens, q_stride * E, wq * E}, vk{k, tokens, k_stride * E, wk * E},
+      oq{q_out, tokens, q_out_stride * E, wq * E}, ok_{k_out, tokens, k_out_stride * E, wk * E},
+      vc{bad_position_count, 1, 4, 4};
+  const View side[] = {{q_weight, 1, 0, head_dim * E}, {k_weight, 1, 0, head_dim * E},
+                       {cos, 1, 0, max_positions * rot_dim * 2},
+                       {sin, 1, 0, max_positions * rot_dim * 2}, {positions, 1, 0, tokens * 4}};
+  if ((!same_view(oq, vq) && views_overlap(oq, vq)) || views_overlap(oq, vk) ||
+      (!same_view(ok_, vk) && views_overlap(ok_, vk)) || views_overlap(ok_, vq) ||
+      views_overlap(oq, ok_) || views_overlap(vc, oq) || views_overlap(vc, ok_) ||
+      views_overlap(vc, vq) || views_overlap(vc, vk))
+    return fail(RR_ERR_ALIASING, "an output overlaps another tensor");
+  for (const View& s : side)
+    if (views_overlap(s, oq) || views_overlap(s, ok_) || views_overlap(s, vc))
+      return fail(RR_ERR_ALIASING, "an output overlaps a weight, the table or the positions");
+  rr::RopeParams p{};
+  p.q = static_cast<const char*>(q);
+  p.k = static_cast<const char*>(k);
+  p.qw = static_cast<const char*>(q_weight);
+  p.kw = static_cast<const char*>(k_weight);
+  p.qo = static_cast<char*>(q_out);
+  p.ko = static_cast<char*>(k_out);
+  p.cos = cos;
+  p.sin = sin;
+  p.positions = positions;
+  p.bad = bad_position_count;
+  p.tokens = tokens;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.qo_stride = q_out_stride;
+  p.ko_stride = k_out_stride;
+  p.positions_n = max_positions;
+  p.heads = (int32_t)heads;
+  p.kv_heads = (int32_t)kv_heads;
+  p.dim = (int32_t)head_dim;
+  p.rot = (int32_t)rot_dim;
+  p.interleaved = interleaved ? 1 : 0;
+  const int64_t strides[] = {q_stride, q_out_stride, k_stride, k_out_stride};
+  const void* tensors[] = {q, q_out, k, k_out};
+  RopePlan pl{};
+  if ((st = rope_plan(p, dtype, eps, strides, kv_heads > 0 ? 4 : 2, tensors, &pl)) != RR_OK)
+    return st;
+  const int wpb = pl.k.threads / 32;
+  rope_units(p, (int64_t)pl.sms * 8 * wpb);
+  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * p.segs, wpb), (int64_t)pl.sms * 8);
+  void* args[] = {&p};
+  cudaError_t e = cudaLaunchKernel(pl.k.fwd, dim3((unsigned)grid), dim3((unsigned)pl.k.threads),
+                                   args, 0, stream);
+  if (e != cudaSuccess) return fail(RR_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+size_t rr_qk_norm_rope_bwd_workspace_size(int64_t tokens, int64_t heads, int64_t kv_heads,
+                                          int64_t head_dim) {
+  if (rope_shape(tokens, heads, kv_heads, head_dim) != RR_OK || tokens == 0) return 0;
+  std::lock_guard<std::mutex> lock(g_mu);
+  DevInfo* di = nullptr;
+  if (device_info(&di) != RR_OK) return 0;
+  return (size_t)di->sms * kRopeBwdBlocks * 2 * head_dim * 4;
+}
+
+rr_status rr_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                              const void* q_weight, const void* k_weight, const float* cos,
+                              const float* sin, const int32_t* positions, void* dq, void* dk,
+                              void* dq_weight, void* dk_weight, void* workspace,
+                              size_t workspace_bytes, int64_t tokens, int64_t heads,
+                              int64_t kv_heads, int64_t head_dim, int64_t rot_dim,
+                              int64_t max_positions, int64_t dq_out_stride, int64_t dk_out_stride,
+                              int64_t q_stride, int64_t k_stride, int64_t dq_stride,
+                              int64_t dk_stride, float eps, int interleaved,
+                              int32_t* bad_position_count, rr_dtype dtype, cudaStream_t stream) {
+  if (dtype != RR_F32 && dtype != RR_BF16)
+    return fail(RR_ERR_UNSUPPORTED_DTYPE, "dtype %d", (int)dtype);
+  rr_status st = rope_shape(tokens, heads, kv_heads, head_dim);
+  if (st != RR_OK) return st;
+  if (rot_dim < 2 || rot_dim > head_dim || rot_dim % 2 != 0)
+    return fail(RR_ERR_INVALID_ARG, "rot_dim must be even, 2..head_dim");
+  if (max_positions < 0 || max_positions > INT32_MAX)
+    return fail(RR_ERR_INVALID_ARG, "max_positions outside 0..2^31-1");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(RR_ERR_INVALID_ARG, "bad eps");
+  const int64_t wq = heads * head_dim, wk = kv_heads * head_dim;
+  const int64_t all[] = {q_stride, dq_out_stride, dq_stride, k_stride, dk_out_stride, dk_stride};
+  for (int i = 0; i < 6; ++i)
+    if (all[i] < (i < 3 ? wq : wk) || all[i] > ((int64_t)1 << 28))
+      return fail(RR_ERR_INVALID_ARG, "a stride is shorter than a token's heads (or beyond 2^28)");
+  if (tokens == 0) return ok();
+  if (!q || !dq_out || !dq || (kv_heads > 0 && (!k || !dk_out || !dk)) ||
+      (max_positions > 0 && (!cos || !sin)))
+    return fail(RR_ERR_INVALID_ARG, "null pointer");
+  if (kv_heads == 0) k = dk_out = dk = nullptr, k_weight = nullptr;
+  if (!dq_weight != !dk_weight)
+    return fail(RR_ERR_INVALID_ARG, "dq_weight and dk_weight: both, or neither");
+  const int64_t E = dtype == RR_BF16 ? 2 : 4;
+  if (!aligned(cos, 4) || !aligned(sin, 4) || !aligned(positions, 4) ||
+      !aligned(bad_position_count, 4) || !aligned(q_weight, E) || !aligned(k_weight, E) ||
+      !aligned(dq_weight, E) || !aligned(dk_weight, E) || !aligned(workspace, 16))
+    return fail(RR_ERR_INVALID_ARG, "misaligned pointer");
+  const size_t need =
+      dq_weight ? rr_qk_norm_rope_bwd_workspace_size(tokens, heads, kv_heads, head_dim) : 0;
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(RR_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", workspace_bytes,
+                need);
+  const View in[] = {{q, tokens, q_stride * E, wq * E}, {dq_out, tokens, dq_out_stride * E, wq * E},
+                     {k, tokens, k_stride * E, wk * E}, {dk_out, tokens, dk_out_stride * E, wk * E}};
+  const View dqv{dq, tokens, dq_stride * E, wq * E}, dkv{dk, tokens, dk_stride * E, wk * E};
+  const View small[] = {{dq_weight, 1, 0, head_dim * E}, {dk_weight, 1, 0, head_dim * E},
+                        {workspace, 1, 0, (int64_t)need}, {bad_position_count, 1, 0, 4}};
+  const View side[] = {{q_weight, 1, 0, head_dim * E}, {k_weight, 1, 0, head_dim * E},
+                       {cos, 1, 0, max_positions * rot_dim * 2},
+                       {sin, 1, 0, max_positions * rot_dim * 2}, {positions, 1, 0, tokens * 4}};
+  bool bad = views_overlap(dqv, dkv);
+  for (int i = 0; i < 4; ++i) {
+    bad = bad || (!(i < 2 && same_view(dqv, in[i])) && views_overlap(dqv, in[i]));
+    bad = bad || (!(i >= 2 && same_view(dkv, in[i])) && views_overlap(dkv, in[i]));
+  }
+  for (int i = 0; i < 4; ++i) {
+    bad = bad || views_overlap(small[i], dqv) || views_overlap(small[i], dkv);
+    for (const View& v : in) bad = bad || views_overlap(small[i], v);
+    for (const View& v : side) bad = bad || views_overlap(small[i], v);
+    for (int j = 0; j < i; ++j) bad = bad || views_overlap(small[i], small[j]);
+  }
+  for (const View& v : side) bad = bad || views_overlap(v, dqv) || views_overlap(v, dkv);
+  if (bad) return fail(RR_ERR_ALIASING, "an output or the workspace overlaps another tensor");
+  rr::RopeParams p{};
+  p.q = static_cast<const char*>(q);
+  p.k = static_cast<const char*>(k);
+  p.qw = static_cast<const char*>(q_weight);
+  p.kw = static_cast<const char*>(k_weight);
+  p.dyq = static_cast<const char*>(dq_out);
+  p.dyk = static_cast<const char*>(dk_out);
+  p.qo = static_cast<char*>(dq);
+  p.ko = static_cast<char*>(dk);
+  p.cos = cos;
+  p.sin = sin;
+  p.positions = positions;
+  p.bad = bad_position_count;
+  p.ws = dq_weight ? static_cast<float*>(workspace) : nullptr;
+  p.tokens = tokens;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.qo_stride = dq_stride;
+  p.ko_stride = dk_stride;
+  p.dyq_stride = dq_out_stride;
+  p.dyk_stride = dk_out_stride;
+  p.positions_n = max_positions;
+  p.heads = (int32_t)heads;
+  p.kv_heads = (int32_t)kv_heads;
+  p.dim = (int32_t)head_dim;
+  p.rot = (int32_t)rot_dim;
+  p.interleaved = interleaved ? 1 : 0;
+  const void* tensors[] = {q, dq_out, dq, k, dk_out, dk};
+  RopePlan pl{};
+  if ((st = rope_plan(p, dtype, eps, all, kv_heads > 0 ? 6 : 3, tensors, &pl)) != RR_OK) return st;
+  const int wpb = pl.k.threads / 32;
+  const int64_t most = (int64_t)pl.sms * kRopeBwdBlocks;
+  rope_units(p, most * wpb);
+  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * p.segs, wpb), most);
+  void* args[] = {&p};
+  cudaError_t e =
+      cudaLaunchKernel(pl.k.bwd, dim3((unsigned)grid), dim3((unsigned)pl.k.threads), args,
+                       (size_t)wpb * 2 * p.dim * 4, stream);
+  if (e != cudaSuccess) return fail(RR_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
+  if (p.ws) {
+    const void* cr =
+        dtype == RR_BF16 ? rr::col_reduce_kernel_ptr_bf16() : rr::col_reduce_kernel_ptr_f32();
+    const float* ws = p.ws;
+    int64_t P = grid, cols = head_dim, planes = 2;
+    char *dw = static_cast<char*>(dq_weight), *dk_w = static_cast<char*>(dk_weight);
+    void* cargs[] = {&ws, &P, &cols, &planes, &dw, &dk_w};
+    e = cudaLaunchKernel(cr, dim3((unsigned)cdiv(2 * cols, 32 * (32 / rr::col_reduce_split(P)))),
+                         dim3(1024), cargs, 0, stream);
+    if (e != cudaSuccess) return fail(RR_ERR_CUDA, "column reduce launch: %s", cudaGetErrorString(e));
+  }
+  return ok();
+}
+
+// ------------------------------------------------------------- attention ----
+
+static rr_status packed_check(const void* q, const void* k, const void* v, const void* o,
+                              const int32_t* cu, int64_t tokens, int64_t batch, int64_t heads,
+                              int64_t kv_heads, int64_t head_dim, float scale, rr_dtype dtype) {
+  if (dtype != RR_F32 && dtype != RR_BF16)
+    return fail(RR_ERR_UNSUPPORTED_DTYPE, "dtype %d", (int)dtype);
+  if (tokens < 0 || batch < 0) return fail(RR_ERR_INVALID_ARG, "negative size");
+  if (heads < 1 || kv_heads < 1 || heads > 65535 || heads % kv_heads != 0)
+    return fail(RR_ERR_INVALID_ARG, "heads must be a multiple of kv_heads, 1..65535");
+  const int W = dtype == RR_BF16 ? 8 : 4;
+  if (head_dim < W || head_dim > 256 || head_dim % W != 0)
+    return fail(RR_ERR_INVALID_ARG, "head_dim must be whole 16-byte chunks, at most 256");
+  if (tokens > INT32_MAX - 4096 || batch > (1 << 20) || tokens > ((int64_t)1 << 32) / heads)
+    return fail(RR_ERR_INVALID_ARG, "too many tokens, sequences or query rows");
+  if (!(scale > 0.f) || !std::isfinite(scale))
+    return fail(RR_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (tokens == 0 || batch == 0) return RR_OK;
+  if (!q || !k || !v || !o || !cu) return fail(RR_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(cu, 4)) return fail(RR_ERR_INVALID_ARG, "misaligned pointer");
+  return RR_OK;
+}
+static rr_status packed_views(const View* v, int n, int64_t E) {
+  for (int i = 0; i < n; ++i) {
+    if (v[i].stride < v[i].width || v[i].stride > ((int64_t)1 << 28) * E)
+      return fail(RR_ERR_INVALID_ARG, "a stride is shorter than a token's heads (or beyond 2^28)");
+    if (!aligned(v[i].p, 16) || v[i].stride % 16 != 0)
+      return fail(RR_ERR_INVALID_ARG, "tensors and strides must be 16-byte aligned");
+  }
+  return RR_OK;
+}
+static rr_status packed_rows_launch(const void* fn, const rr::PackedParams& p, int64_t heads,
+                                    int warps, cudaStream_t stream) {
+  void* args[] = {const_cast<rr::PackedParams*>(&p)};
+  cudaError_t e = cudaLaunchKernel(fn, dim3((unsigned)cdiv(p.tokens * heads, warps)),
+                                   dim3((unsigned)warps * 32), args, 0, stream);
+  if (e != cudaSuccess) return fail(RR_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+rr_status rr_attention_packed_fwd(const void* q, const void* k, const void* v,
+                                  const int32_t* cu_seqlens, void* o, float* lse, int64_t tokens,
+                                  int64_t batch, int64_t heads, int64_t kv_heads,
+                                  int64_t head_dim, int64_t q_stride, int64_t k_stride,
+                                  int64_t v_stride, int64_t o_stride, float scale, rr_dtype dtype,
+                                  cudaStream_t stream) {
+  rr_status st = packed_check(q, k, v, o, cu_seqlens, tokens, batch, heads, kv_heads, head_dim,
+                              scale, dtype);
+  if (st != RR_OK) return st;
+  const int64_t E = dtype == RR_BF16 ? 2 : 4, wq = heads * head_dim * E,
+                wk = kv_heads * head_dim * E;
+  const View t[] = {{q, tokens, q_stride * E, wq}, {k, tokens, k_stride * E, wk},
+                    {v, tokens, v_stride * E, wk}, {o, tokens, o_stride * E, wq}};
+  if ((st = packed_views(t, 4, E)) != RR_OK) return st;
+  if (!aligned(lse, 4)) return fail(RR_ERR_INVALID_ARG, "misaligned pointer");
+  if (tokens == 0 || batch == 0) return ok();
+  const View vl{lse, 1, 0, heads * tokens * 4}, vc{cu_seqlens, 1, 0, (batch + 1) * 4};
+  for (int i = 0; i < 4; ++i)
+    if ((i < 3 && views_overlap(t[3], t[i])) || views_overlap(vl, t[i]))
+      return fail(RR_ERR_ALIASING, "o or lse overlaps another tensor");
+  if (views_overlap(vc, t[3]) || views_overlap(vc, vl))
+    return fail(RR_ERR_ALIASING, "o or lse overlaps cu_seqlens");
+  rr::PackedParams p{};
+  p.q = static_cast<const char*>(q);
+  p.k = static_cast<const char*>(k);
+  p.v = static_cast<const char*>(v);
+  p.o = static_cast<const char*>(o);
+  p.lse = lse;
+  p.cu = cu_seqlens;
+  p.tokens = tokens;
+  p.batch = batch;
+  p.sq = q_stride;
+  p.sk = k_stride;
+  p.sv = v_stride;
+  p.so = o_stride;
+  p.heads = (int32_t)heads;
+  p.kv_heads = (int32_t)kv_heads;
+  p.dim = (int32_t)head_dim;
+  p.scale = scale;
+  p.scale_log2 = scale * rr::kLog2e;
+  const rr::PackedRowKernels rk = rr::packed_row_kernels(dtype == RR_BF16 ? rr::kBF16 : rr::kF32);
+  return packed_rows_launch(rk.fwd, p, heads, rk.warps, stream);
+}
+
+size_t rr_attention_packed_bwd_workspace_size(int64_t tokens, int64_t heads) {
+  if (tokens < 1 || heads < 1 || heads > 65535 || tokens > ((int64_t)1 << 32) / heads) return 0;
+  return (size_t)(tokens * heads) * 4;
+}
+
+rr_status rr_attention_packed_bwd(const void* dout, const void* q, const void* k, const void* v,
+                                  const void* o, const float* lse, const int32_t* cu_seqlens,
+                                  void* dq, void* dk, void* dv, void* workspace,
+                                  size_t workspace_bytes, int64_t tokens, int64_t batch,
+                                  int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                  int64_t dout_stride, int64_t q_stride, int64_t k_stride,
+                                  int64_t v_stride, int64_t o_stride, int64_t dq_stride,
+                                  int64_t dk_stride, int64_t dv_stride, float scale,
+                                  rr_dtype dtype, cudaStream_t stream) {
+  rr_status st = packed_check(q, k, v, o, cu_seqlens, tokens, batch, heads, kv_heads, head_dim,
+                              scale, dtype);
+  if (st != RR_OK) return st;
+  const int64_t E = dtype == RR_BF16 ? 2 : 4, wq = heads * head_dim * E,
+                wk = kv_heads * head_dim * E;
+  // outputs first
+  const View t[] = {{dq, tokens, dq_stride * E, wq}, {dk, tokens, dk_stride * E, wk},
+                    {dv, tokens, dv_stride * E, wk}, {dout, tokens, dout_stride * E, wq},
+                    {q, tokens, q_stride * E, wq},   {k, tokens, k_stride * E, wk},
+                    {v, tokens, v_stride * E, wk},   {o, tokens, o_stride * E, wq}};
+  if ((st = packed_views(t, 8, E)) != RR_OK) return st;
+  if (!aligned(lse, 4) || !aligned(workspace, 16))
+    return fail(RR_ERR_INVALID_ARG, "misaligned pointer");
+  if (tokens == 0 || batch == 0) return ok();
+  if (!dout || !lse || !dq || !dk || !dv) return fail(RR_ERR_INVALID_ARG, "null pointer");
+  const size_t need = rr_attention_packed_bwd_workspace_size(tokens, heads);
+  if (workspace_bytes < need || !workspace)
+    return fail(RR_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", workspace_bytes,
+                need);
+  const View vw{workspace, 1, 0, (int64_t)need}, vl{lse, 1, 0, heads * tokens * 4},
+      vc{cu_seqlens, 1, 0, (batch + 1) * 4};
+  bool bad = views_overlap(vw, vl) || views_overlap(vw, vc);
+  for (int i = 0; i < 8; ++i) {
+    bad = bad || views_overlap(vw, t[i]);
+    for (int j = 0; j < std::min(i, 3); ++j) bad = bad || views_overlap(t[i], t[j]);
+    if (i < 3) bad = bad || views_overlap(vl, t[i]) || views_overlap(vc, t[i]);
+  }
+  if (bad) return fail(RR_ERR_ALIASING, "a gradient or the workspace overlaps another tensor");
+  rr::PackedParams p{};
+  p.q = static_cast<const char*>(q);
+  p.k = static_cast<const char*>(k);
+  p.v = static_cast<const char*>(v);
+  p.o = static_cast<const char*>(o);
+  p.lse = const_cast<float*>(lse);
+  p.cu = cu_seqlens;
+  p.dout = static_cast<const char*>(dout);
+  p.dq = static_cast<const char*>(dq);
+  p.dk = static_cast<const char*>(dk);
+  p.dv = static_cast<const char*>(dv);
+  p.delta = static_cast<float*>(workspace);
+  p.tokens = tokens;
+  p.batch = batch;
+  p.sq = q_stride;
+  p.sk = k_stride;
+  p.sv = v_stride;
+  p.so = o_stride;
+  p.sdo = dout_stride;
+  p.sdq = dq_stride;
+  p.sdk = dk_stride;
+  p.sdv = dv_stride;
+  p.heads = (int32_t)heads;
+  p.kv_heads = (int32_t)kv_heads;
+  p.dim = (int32_t)head_dim;
+  p.scale = scale;
+  p.scale_log2 = scale * rr::kLog2e;
+  const rr::PackedRowKernels rk = rr::packed_row_kernels(dtype == RR_BF16 ? rr::kBF16 : rr::kF32);
+  if ((st = packed_rows_launch(rk.dq, p, heads, rk.warps, stream)) != RR_OK) return st;
+  return packed_rows_launch(rk.dkv, p, kv_heads, rk.warps, stream);
+}
+
+// ----------------------------------------------------- log probabilities ----
+
+static rr_status logprob_check(int64_t rows, int64_t cols, float temperature, rr_dtype dtype) {
+  rr_status st = check_shape(rows, cols, dtype);
+  if (st != RR_OK) return st;
+  if (cols > INT32_MAX) return fail(RR_ERR_INVALID_ARG, "cols beyond an int32 token");
+  if (!(temperature >= 0x1p-120f && temperature <= 0x1p120f))
+    return fail(RR_ERR_INVALID_ARG, "temperature must be within 2^-120 .. 2^120");
+  return RR_OK;
+}
+
+rr_status rr_token_logprob_fwd(const void* logits, const int32_t* tokens, float* logprob,
+                               float* entropy, float* row_max, float* log_sum, int32_t* rank,
+                               int32_t* top_index, float* top_logprob, int64_t rows, int64_t cols,
+                               int64_t logits_stride, int64_t k, float temperature,
+                               int32_t ignore_index, int32_t* bad_token_count, rr_dtype dtype,
+                               cudaStream_t stream) {
+  rr_status st = logprob_check(rows, cols, temperature, dtype);
+  if (st != RR_OK) return st;
+  if (k < 0 || k > rr::kLogprobMaxK)
+    return fail(RR_ERR_INVALID_ARG, "k=%lld outside 0..%d", (long long)k, rr::kLogprobMaxK);
+  if (logits_stride < cols || logits_stride > ((int64_t)1 << 60) / std::max<int64_t>(rows, 1))
+    return fail(RR_ERR_INVALID_ARG, "logits_stride shorter than cols (or too large)");
+  if (rows == 0) return ok();
+  if (rows > ((int64_t)1 << 50)) return fail(RR_ERR_INVALID_ARG, "rows too large");
+  if (!logits || !tokens || !logprob || (k > 0 && (!top_index || !top_logprob)))
+    return fail(RR_ERR_INVALID_ARG, "null pointer");
+  const int64_t E = dtype == RR_BF16 ? 2 : 4;
+  if (k == 0) top_index = nullptr, top_logprob = nullptr;
+  const void* words[] = {tokens, logprob, entropy, row_max, log_sum, rank, top_index, top_logprob,
+                         bad_token_count};
+  for (const void* w : words)
+    if (!aligned(w, 4)) return fail(RR_ERR_INVALID_ARG, "misaligned pointer");
+  if (!aligned(logits, E)) return fail(RR_ERR_INVALID_ARG, "misaligned pointer");
+  const View in[] = {{logits, rows, logits_stride * E, cols * E}, {tokens, 1, 0, rows * 4}};
+  const View out[] = {{logprob, 1, 0, rows * 4},       {entropy, 1, 0, rows * 4},
+                      {row_max, 1, 0, rows * 4},       {log_sum, 1, 0, rows * 4},
+                      {rank, 1, 0, rows * 4},          {top_index, 1, 0, rows * k * 4},
+                      {top_logprob, 1, 0, rows * k * 4}, {bad_token_count, 1, 0, 4}};
+  for (int i = 0; i < 8; ++i) {
+    bool bad = views_overlap(out[i], in[0]) || views_overlap(out[i], in[1]);
+    for (int j = 0; j < i; ++j) bad = bad || views_overlap(out[i], out[j]);
+    if (bad) return fail(RR_ERR_ALIASING, "an output overlaps another tensor");
+  }
+  rr::LogprobParams p{};
+  p.x = static_cast<const char*>(logits);
+  p.tokens = tokens;
+  p.logprob = logprob;
+  p.entropy = entropy;
+  p.row_max = row_max;
+  p.log_sum = log_sum;
+  p.rank = rank;
+  p.top_index = top_index;
+  p.top_logprob = top_logprob;
+  p.bad = bad_token_count;
+  p.rows = rows;
+  p.cols = cols;
+  p.stride = logits_stride;
+  p.k = (int32_t)k;
+  p.ignore = ignore_index;
+  p.temperature = temperature;
+  p.c = rr::kLog2e / temperature;
+  int sms = 0;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    DevInfo* di = nullptr;
+    if ((st = device_info(&di)) != RR_OK) return st;
+    sms = di->sms;
+    p.err = di->err;
+  }
+  const rr::LogprobKernels lk = rr::logprob_kernels(dtype == RR_BF16 ? rr::kBF16 : rr::kF32);
+  void* args[] = {&p};
+  cudaError_t e = cudaLaunchKernel(lk.fwd, dim3((unsigned)std::min<int64_t>(rows, 8 * (int64_t)sms)),
+                                   dim3((unsigned)lk.threads), args, 0, stream);
+  if (e != cudaSuccess) return fail(RR_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+rr_status rr_token_logprob_bwd(const void* logits, const int32_t* tokens, const float* row_max,
+                               const float* log_sum, const float* entropy,
+                               const float* grad_logprob, const float* grad_entropy, void* dlogits,
+                               int64_t rows, int64_t cols, int64_t logits_stride,
+                               int64_t dlogits_stride, float temperature, int32_t ignore_index,
+                               rr_dtype dtype, cudaStream_t stream) {
+  rr_status st = logprob_check(rows, cols, temperature, dtype);
+  if (st != RR_OK) return st;
+  const int64_t most = ((int64_t)1 << 60) / std::max<int64_t>(rows, 1);
+  if (logits_stride < cols || dlogits_stride < cols || logits_stride > most ||
+      dlogits_stride > most)
+    return fail(RR_ERR_INVALID_ARG, "a stride is shorter than cols (or too large)");
+  if (rows == 0) return ok();
+  if (!logits || !tokens || !row_max || !log_sum || !dlogits || (grad_entropy && !entropy))
+    return fail(RR_ERR_INVALID_ARG, "null pointer");
+  const int64_t E = dtype == RR_BF16 ? 2 : 4;
+  const void* words[] = {tokens, row_max, log_sum, entropy, grad_logprob, grad_entropy};
+  for (const void* w : words)
+    if (!aligned(w, 4)) return fail(RR_ERR_INVALID_ARG, "misaligned pointer");
+  if (!aligned(logits, E) || !aligned(dlogits, E))
+    return fail(RR_ERR_INVALID_ARG, "misaligned pointer");
+  const View x{logits, rows, logits_stride * E, cols * E},
+      y{dlogits, rows, dlogits_stride * E, cols * E};
+  if (!same_view(x, y) && views_overlap(x, y))
+    return fail(RR_ERR_ALIASING, "logits and dlogits partially overlap");
+  for (const void* w : words)
+    if (views_overlap(y, View{w, 1, 0, rows * 4}))
+      return fail(RR_ERR_ALIASING, "dlogits overlaps an input");
+  rr::LogprobBwdParams p{};
+  p.x = static_cast<const char*>(logits);
+  p.tokens = tokens;
+  p.row_max = row_max;
+  p.log_sum = log_sum;
+  p.entropy = entropy;
+  p.g = grad_logprob;
+  p.h = grad_entropy;
+  p.y = static_cast<char*>(dlogits);
+  p.rows = rows;
+  p.cols = cols;
+  p.x_stride = logits_stride;
+  p.y_stride = dlogits_stride;
+  p.ignore = ignore_index;
+  p.temperature = temperature;
+  p.c = rr::kLog2e / temperature;
+  const rr::LogprobKernels lk = rr::logprob_kernels(dtype == RR_BF16 ? rr::kBF16 : rr::kF32);
+  p.segs = (int32_t)cdiv(cols * E, lk.bwd_bytes);
+  if (rows > INT32_MAX / p.segs)
+    return fail(RR_ERR_INVALID_ARG, "too many rows for this many columns");
+  // chunks of both tensors start at the same columns in every row
+  const bool vec = ((reinterpret_cast<uintptr_t>(logits) ^ reinterpret_cast<uintptr_t>(dlogits)) &
+                    15) == 0 &&
+                   (logits_stride - dlogits_stride) * E % 16 == 0;
+  void* args[] = {&p};
+  cudaError_t e = cudaLaunchKernel(lk.bwd[vec], dim3((unsigned)(rows * p.segs)),
+                                   dim3((unsigned)lk.threads), args, 0, stream);
+  if (e != cudaSuccess) return fail(RR_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+}  // extern "C"
+
 namespace {
 
 // One thread arms an mbarrier for 16 transaction bytes that no copy delivers

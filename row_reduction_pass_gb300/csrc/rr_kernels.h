@@ -318,6 +318,87 @@ TreeKernels tree_kernels(int d);
 const char* tree_tc_launch(const TreeParams& p, int d, int sms, cudaStream_t stream);
 size_t tree_ws_bytes(int64_t batch, int64_t nodes, int heads, int kv_heads, int d, int sms);
 
+// Norms of queries and keys with the position rotation (k_rope.cu).  Strides are in
+// elements, from a token to the next.
+struct RopeParams {
+  const char *q, *k;          // [tokens][heads | kv_heads][dim]
+  const char *qw, *kw;        // [dim], or null (1)
+  const char *dyq, *dyk;      // backward: gradients of the outputs
+  char *qo, *ko;              // outputs; backward: dq, dk
+  const float *cos, *sin;     // [positions_n][rot / 2]
+  const int32_t* positions;   // [tokens], or null (the token's index)
+  int32_t* bad;               // counter of positions beyond the table, or null
+  float* ws;                  // backward: [blocks][2][dim] sums, or null (no weight gradients)
+  int64_t tokens, q_stride, k_stride, qo_stride, ko_stride, dyq_stride, dyk_stride;
+  int64_t positions_n;
+  int32_t heads, kv_heads, dim, rot;
+  int32_t group;              // lanes of a row, a power of two
+  int32_t segs, seg_rows;     // a token's rows are cut into segs units of seg_rows
+  int32_t interleaved;
+  float eps, inv_dim;
+};
+struct RopeKernels {
+  const void *fwd, *bwd;
+  int threads;
+};
+// vec: slots of two 16-byte chunks, a row on up to 32 lanes; else of two elements.
+RopeKernels rope_kernels(int dtype, bool vec);
+
+// Log probabilities of given tokens (k_logprob.cu).  Strides in elements.
+constexpr int kLogprobMaxK = 128;
+struct LogprobParams {
+  const char* x;          // [rows][cols] logits
+  const int32_t* tokens;  // [rows]
+  float *logprob, *entropy, *row_max, *log_sum;  // [rows]; all but the first may be null
+  int32_t* rank;          // [rows], or null
+  int32_t* top_index;     // [rows][k]
+  float* top_logprob;     // [rows][k]
+  int32_t* bad;           // counter of tokens out of range, or null
+  int* err;
+  int64_t rows, cols, stride;
+  int32_t k, ignore;
+  float temperature, c;   // c = log2 e / temperature
+};
+struct LogprobBwdParams {
+  const char* x;
+  const int32_t* tokens;
+  const float *row_max, *log_sum, *entropy;  // entropy: null without h
+  const float *g, *h;     // [rows] gradients of logprob and entropy, or null (0)
+  char* y;                // dlogits
+  int64_t rows, cols, x_stride, y_stride;
+  int32_t segs, ignore;   // blocks a row
+  float temperature, c;
+};
+struct LogprobKernels {
+  const void* fwd;
+  const void* bwd[2];     // [elements, 16-byte chunks]
+  int threads;
+  int bwd_bytes;          // of a row that a block of the backward takes
+};
+LogprobKernels logprob_kernels(int dtype);
+
+// Causal attention over packed sequences (k_packed.cu, k_packed_tc.cu).  Strides in
+// elements, from a token to the next; heads are dim apart.
+struct PackedParams {
+  const char *q, *k, *v;      // [tokens][heads | kv_heads][dim]
+  const char* o;              // the forward's output, the backward's input
+  float* lse;                 // [heads][tokens]
+  const int32_t* cu;          // [batch + 1] bounds of the sequences
+  const char* dout;           // backward: gradient of o
+  const char *dq, *dk, *dv;   // backward: outputs
+  float* delta;               // backward: [heads][tokens] sums of dout o
+  int* err;
+  int64_t tokens, batch;
+  int64_t sq, sk, sv, so, sdo, sdq, sdk, sdv;
+  int32_t heads, kv_heads, dim;
+  float scale, scale_log2;    // scale_log2 = scale log2 e
+};
+struct PackedRowKernels {
+  const void *fwd, *dq, *dkv;
+  int warps;                  // rows a block
+};
+PackedRowKernels packed_row_kernels(int dtype);
+
 // The column reduce's split of its 32 warps over the P partial rows: the
 // smallest power of two >= P / 16, at most 32 (the rest of the warps take
 // further columns), so each warp sums about 16 partials.  A block covers
