@@ -2651,7 +2651,8 @@ static rr_status packed_check(const void* q, const void* k, const void* v, const
   const int W = dtype == RR_BF16 ? 8 : 4;
   if (head_dim < W || head_dim > 256 || head_dim % W != 0)
     return fail(RR_ERR_INVALID_ARG, "head_dim must be whole 16-byte chunks, at most 256");
-  if (tokens > INT32_MAX - 4096 || batch > (1 << 20) || tokens > ((int64_t)1 << 32) / heads)
+  if (tokens > INT32_MAX - 4096 || batch > (1 << 20) || tokens > ((int64_t)1 << 32) / heads ||
+      tokens / 128 + batch > ((int64_t)1 << 31) / heads)
     return fail(RR_ERR_INVALID_ARG, "too many tokens, sequences or query rows");
   if (!(scale > 0.f) || !std::isfinite(scale))
     return fail(RR_ERR_INVALID_ARG, "scale must be finite and > 0");
@@ -2718,6 +2719,22 @@ rr_status rr_attention_packed_fwd(const void* q, const void* k, const void* v,
   p.dim = (int32_t)head_dim;
   p.scale = scale;
   p.scale_log2 = scale * rr::kLog2e;
+  const rr::PackedTcKernels tk = rr::packed_tc_kernels(dtype == RR_BF16 ? p.dim : 0);
+  if (tk.fwd) {
+    int sms = 0;
+    {
+      std::lock_guard<std::mutex> lock(g_mu);
+      DevInfo* di = nullptr;
+      if ((st = device_info(&di)) != RR_OK) return st;
+      if ((st = set_smem(di, tk.fwd, (size_t)tk.fwd_smem)) != RR_OK) return st;
+      p.err = di->err;
+      sms = di->sms;
+    }
+    if (const char* why = rr::packed_tc_fwd_launch(p, sms, stream))
+      return fail(RR_ERR_CUDA, "packed attention: %s (%s)", why,
+                  cudaGetErrorString(cudaGetLastError()));
+    return ok();
+  }
   const rr::PackedRowKernels rk = rr::packed_row_kernels(dtype == RR_BF16 ? rr::kBF16 : rr::kF32);
   return packed_rows_launch(rk.fwd, p, heads, rk.warps, stream);
 }
