@@ -173,6 +173,39 @@ struct Fwd {
   static constexpr uint32_t kIdescO = attn_idesc(kTile, D, true);
 };
 
+// 64 columns of a warp's 32 rows (lane = row, lo and hi 32 columns each) times f as bf16: as
+// one TMA store of whole lines from `box` where every row is stored, else row by row.
+__device__ __forceinline__ void put_box(const uint32_t (&lo)[32], const uint32_t (&hi)[32], float f,
+                                        unsigned char* box, const CUtensorMap* map, int col,
+                                        int head, int token, char* out, bool whole, bool mine) {
+  const int lane = threadIdx.x & 31;
+  if (whole) {
+    if (lane == 0) stores_read();  // the box's last store has read it
+    __syncwarp();
+  }
+#pragma unroll
+  for (int c2 = 0; c2 < 2; ++c2)
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+      const uint32_t* oc = c2 ? hi : lo;
+      const uint4 q4 = make_uint4(
+          pack_bf16(__uint_as_float(oc[i]) * f, __uint_as_float(oc[i + 1]) * f),
+          pack_bf16(__uint_as_float(oc[i + 2]) * f, __uint_as_float(oc[i + 3]) * f),
+          pack_bf16(__uint_as_float(oc[i + 4]) * f, __uint_as_float(oc[i + 5]) * f),
+          pack_bf16(__uint_as_float(oc[i + 6]) * f, __uint_as_float(oc[i + 7]) * f));
+      const int ch = 4 * c2 + (i >> 3);  // 16-byte chunk of the 128-byte row
+      if (whole)
+        *reinterpret_cast<uint4*>(box + lane * 128 + ((ch ^ (lane & 7)) << 4)) = q4;
+      else if (mine)
+        *reinterpret_cast<uint4*>(out + 16 * ch) = q4;
+    }
+  if (whole) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) store_box(map, box, col, head, token);
+  }
+}
+
 // Row t of head h again, in float32, from the keys that it sees: the warp's lanes take 32
 // keys' scores, then all the D columns.  sq: shared room for D floats.
 template <int D>
@@ -540,33 +573,9 @@ __global__ void __launch_bounds__(352, 1)
       const bool whole = __all_sync(0xffffffffu, live && fine);
       char* out = const_cast<char*>(p.o) + (at * p.so + (int64_t)x.head * D) * 2;
 #pragma unroll
-      for (int b = 0; b < C::kBoxes; ++b) {
-        if (whole) {
-          if (lane == 0) stores_read();  // the box's last store has read it
-          __syncwarp();
-        }
-#pragma unroll
-        for (int c2 = 0; c2 < 2; ++c2)
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            const uint32_t* oc = o[2 * b + c2];
-            const uint4 q4 = make_uint4(
-                pack_bf16(__uint_as_float(oc[i]) * inv, __uint_as_float(oc[i + 1]) * inv),
-                pack_bf16(__uint_as_float(oc[i + 2]) * inv, __uint_as_float(oc[i + 3]) * inv),
-                pack_bf16(__uint_as_float(oc[i + 4]) * inv, __uint_as_float(oc[i + 5]) * inv),
-                pack_bf16(__uint_as_float(oc[i + 6]) * inv, __uint_as_float(oc[i + 7]) * inv));
-            const int ch = 4 * c2 + (i >> 3);  // 16-byte chunk of the 128-byte row
-            if (whole)
-              *reinterpret_cast<uint4*>(box + lane * 128 + ((ch ^ (lane & 7)) << 4)) = q4;
-            else if (live && fine)
-              *reinterpret_cast<uint4*>(out + 128 * b + 16 * ch) = q4;
-          }
-        if (whole) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) store_box(&to, box, 64 * b, x.head, (int)at);
-        }
-      }
+      for (int b = 0; b < C::kBoxes; ++b)
+        put_box(o[2 * b], o[2 * b + 1], inv, box, &to, 64 * b, x.head, (int)at, out + 128 * b, whole,
+                live && fine);
       uint32_t broken = __ballot_sync(0xffffffffu, live && !fine);
       if (broken) {
         if (lane == 0) stores_read();
@@ -582,6 +591,649 @@ __global__ void __launch_bounds__(352, 1)
     if (lane == 0) stores_done();
   }
 
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+}
+
+// ------------------------------------------------------------------ backward ---
+// Two kernels, so that every sum has one owner and a fixed order (S and dP are computed in
+// both): dQ by query tiles, dK and dV by key tiles, the latter transposed, so that all three
+// are products of a weight matrix in TMEM with a tile in shared memory, as O = P V is.
+// delta = sum dO o of each row comes from a kernel before them.
+//
+// A block has eight softmax warps, two to a quarter of the 128 TMEM lanes, with 64 of the
+// tile's 128 columns each; warp 8 loads, warps 9 and 10 issue.
+//
+// dQ, a query tile against key tiles t: S(t) = Q K^T, dP(t) = dO V^T, then
+//   dS = P (dP - delta) as bf16 in one of two buffers, dQ += dS K.  S and dP of t + 1 run
+//   while the softmax works on t.
+// dK and dV, a key tile against the query tiles of all heads of its group: S^T = K Q^T, P^T
+//   over its half of S^T's columns, dV += P^T dO; dP^T = V dO^T, dS^T likewise, dK += dS^T Q.
+//   Two issuers, so that one pair's products run while the softmax works on the other pair.
+//
+// Rows of a tile beyond its sequence are masked, and where such a row is summed over (K in
+// dQ; Q and dO in dK, dV) it is set to zero in shared memory before the product, so that no
+// other sequence's NaN takes part.
+template <int D>
+struct Bwd {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTileBytes = kBoxes * kBox;
+  static constexpr int kOffStage = 6 * kTileBytes;    // dQ: 8 warps' output boxes
+  static constexpr int kOffStat = 6 * kTileBytes;     // dK, dV: [stage][-lse, -delta][128]
+  static constexpr int kStage = 32 * 128;
+  static constexpr int kOffBarQ = kOffStage + 8 * kStage, kOffBarK = kOffStat + 2048;
+  static constexpr int kSmemQ = kOffBarQ + 256 + kSorted * 8 + 1024;
+  static constexpr int kSmemK = kOffBarK + 256 + 2 * kSorted * 8 + 1024;
+  static constexpr uint32_t kIdescS = attn_idesc(kTile, kTile, false);
+  static constexpr uint32_t kIdescG = attn_idesc(kTile, D, true);
+};
+
+// The tensor maps of a backward kernel: 128-row boxes of the inputs, 32-row boxes of outputs.
+struct BwdMaps {
+  CUtensorMap q, k, v, g, out0, out1;
+};
+
+// D (+)= A B^T of two tiles in shared memory, A [128 x D], B [128 x D].
+template <int D>
+__device__ __forceinline__ void issue_tiles(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = (uint32_t)((kk >> 2) * kBox + (kk & 3) * 32);
+    mma_ss(d, sw128_desc(a + off, 16, 1024), sw128_desc(b + off, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+  }
+}
+// Rows [from, 128) of a tile in shared memory become zero (all lanes of a warp).
+template <int D>
+__device__ __forceinline__ void clear_rows(unsigned char* tile, int from) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  for (int b = 0; b < D / 64; ++b)
+    for (int i = from * 8 + lane; i < kTile * 8; i += 32)
+      *reinterpret_cast<uint4*>(tile + b * kBox + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// delta of every row of every head: a group of D / 8 lanes a row.
+template <int D>
+__global__ void __launch_bounds__(256) packed_delta_kernel(const PackedParams p) {
+  constexpr int G = D / 8, R = 32 / G;
+  const int lane = threadIdx.x & 31, gl = lane % G;
+  const int64_t rows = p.tokens * p.heads;
+  const int64_t row = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * R + lane / G;
+  const int64_t t = row / p.heads;
+  const int h = (int)(row - t * p.heads);
+  float s = 0.f;
+  if (row < rows) {
+    const uint4 a = ld_chunk_cached(p.dout + (t * p.sdo + (int64_t)h * D + gl * 8) * 2);
+    const uint4 b = ld_chunk_cached(p.o + (t * p.so + (int64_t)h * D + gl * 8) * 2);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += chunk_get<kBF16>(a, e) * chunk_get<kBF16>(b, e);
+  }
+#pragma unroll
+  for (int off = G / 2; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (row < rows && gl == 0) p.delta[(int64_t)h * p.tokens + t] = s;
+}
+
+template <int D>
+__global__ void __launch_bounds__(352, 1)
+    packed_dq_kernel(const __grid_constant__ BwdMaps maps, const PackedParams p) {
+  using C = Bwd<D>;
+  constexpr int T = C::kTileBytes;
+  constexpr uint32_t kColP = 128, kColG = 256, kColS = 384;  // dP, dQ, dS buffers
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char *sq = smem, *sg = smem + T;
+  auto sk = [&](int s) { return smem + (2 + s) * T; };
+  auto sv = [&](int s) { return smem + (4 + s) * T; };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBarQ);
+  uint64_t* bar_q = bars;           // Q and dO landed
+  uint64_t* bar_qfree = bars + 1;   // the item's last S and dP done
+  uint64_t* bar_s = bars + 2;
+  uint64_t* bar_dp = bars + 3;
+  uint64_t* bar_read = bars + 4;    // S and dP read, 256 arrivals
+  uint64_t* bar_gfree = bars + 5;   // dQ read, 256 arrivals
+  uint64_t* bar_ds = bars + 6;      // [buffer] dS written, 256 arrivals
+  uint64_t* bar_g = bars + 8;       // [buffer] dQ += dS K done
+  uint64_t* bar_kfull = bars + 10;  // [stage]
+  uint64_t* bar_vfull = bars + 12;
+  uint64_t* bar_kempty = bars + 14;
+  uint64_t* bar_vempty = bars + 16;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 18);
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tslot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 32 * 8) {
+    for (int i = 0; i < 4; ++i) mbar_init(bars + i, 1);
+    for (int i = 4; i < 8; ++i) mbar_init(bars + i, 256);
+    for (int i = 8; i < 18; ++i) mbar_init(bars + i, 1);
+    fence_mbar_init();
+  }
+  Sequences list;
+  list.init(reinterpret_cast<int2*>(smem + C::kOffBarQ + 256),
+            reinterpret_cast<int2*>(smem + C::kOffStage), p, kTile, p.heads);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  const int group = p.heads / p.kv_heads;
+  bool dead = false, more;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    int nk = 0, nv = 0, nq = 0;
+    for (int r = 0;; ++r) {
+      const Item it = list.get(r, more);
+      if (!more) break;
+      if (!it.ok || lane != 0) continue;
+      const int h = it.part, kv = h / group;
+      if (nq > 0) wait_spin(bar_qfree, (uint32_t)((nq - 1) & 1), dead, p.err);
+      if (dead) continue;
+      ++nq;
+      mbar_arrive_expect_tx(bar_q, 2 * T);
+      for (int b = 0; b < C::kBoxes; ++b) {
+        load_box(sq + b * kBox, &maps.q, 64 * b, h, it.beg + it.level * kTile, bar_q);
+        load_box(sg + b * kBox, &maps.g, 64 * b, h, it.beg + it.level * kTile, bar_q);
+      }
+      for (int t = 0; t <= it.level; ++t) {
+        const int s = nk & 1;
+        const uint32_t ph = (uint32_t)(((nk >> 1) - 1) & 1);
+        if (nk >= 2) wait_spin(&bar_kempty[s], ph, dead, p.err);
+        if (dead) break;
+        ++nk;
+        mbar_arrive_expect_tx(&bar_kfull[s], T);
+        for (int b = 0; b < C::kBoxes; ++b)
+          load_box(sk(s) + b * kBox, &maps.k, 64 * b, kv, it.beg + t * kTile, &bar_kfull[s]);
+        if (nv >= 2) wait_spin(&bar_vempty[s], ph, dead, p.err);
+        if (dead) break;
+        ++nv;
+        mbar_arrive_expect_tx(&bar_vfull[s], T);
+        for (int b = 0; b < C::kBoxes; ++b)
+          load_box(sv(s) + b * kBox, &maps.v, 64 * b, kv, it.beg + t * kTile, &bar_vfull[s]);
+      }
+    }
+    for (int n = max(nk - 2, 0); n < nk; ++n)
+      mbar_wait_bounded(&bar_kfull[n & 1], (uint32_t)((n >> 1) & 1), p.err);
+    for (int n = max(nv - 2, 0); n < nv; ++n)
+      mbar_wait_bounded(&bar_vfull[n & 1], (uint32_t)((n >> 1) & 1), p.err);
+    if (nq > 0) mbar_wait_bounded(bar_q, (uint32_t)((nq - 1) & 1), p.err);
+  } else if (warp == 9) {
+    // ----------------------------------------------------------- S and dP
+    int n = 0, items = 0;
+    for (int r = 0;; ++r) {
+      const Item it = list.get(r, more);
+      if (!more) break;
+      if (!it.ok || lane != 0) continue;
+      wait_spin(bar_q, (uint32_t)(items++ & 1), dead, p.err);
+      for (int t = 0; t <= it.level; ++t) {
+        const int s = n & 1;
+        const uint32_t ph = (uint32_t)((n >> 1) & 1);
+        wait_spin(&bar_kfull[s], ph, dead, p.err);
+        if (n > 0) wait_spin(bar_read, (uint32_t)((n - 1) & 1), dead, p.err);
+        wait_spin(&bar_vfull[s], ph, dead, p.err);
+        if (dead) break;
+        tc_fence_after();
+        issue_tiles<D>(tmem, smem_addr(sq), smem_addr(sk(s)), C::kIdescS);
+        mma_commit(bar_s);
+        issue_tiles<D>(tmem + kColP, smem_addr(sg), smem_addr(sv(s)), C::kIdescS);
+        mma_commit(bar_dp);
+        mma_commit(&bar_vempty[s]);
+        if (t == it.level) mma_commit(bar_qfree);
+        ++n;
+      }
+    }
+    if (n > 0) mbar_wait_bounded(bar_dp, (uint32_t)((n - 1) & 1), p.err);
+  } else if (warp == 10) {
+    // --------------------------------------------------------- dQ += dS K
+    int n = 0, items = 0;
+    for (int r = 0;; ++r) {
+      const Item it = list.get(r, more);
+      if (!more) break;
+      if (!it.ok) continue;
+      for (int t = 0; t <= it.level; ++t) {
+        const int s = n & 1;
+        if (lane == 0) {
+          wait_spin(&bar_kfull[s], (uint32_t)((n >> 1) & 1), dead, p.err);
+          wait_spin(&bar_ds[s], (uint32_t)((n >> 1) & 1), dead, p.err);
+          if (t == 0 && items > 0) wait_spin(bar_gfree, (uint32_t)((items - 1) & 1), dead, p.err);
+        }
+        dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
+        if (dead) break;
+        const int rest = it.len - t * kTile;
+        if (rest < kTile) clear_rows<D>(sk(s), rest);
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t k_addr = smem_addr(sk(s));
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_ts(tmem + kColG, tmem + kColS + 64 * s + 8 * kk,
+                   sw128_desc(k_addr + kk * 2048, kBox, 1024), C::kIdescG,
+                   (t > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&bar_g[s]);
+          mma_commit(&bar_kempty[s]);
+        }
+        ++n;
+      }
+      ++items;
+    }
+    if (lane == 0 && n > 0)
+      mbar_wait_bounded(&bar_g[(n - 1) & 1], (uint32_t)(((n - 1) >> 1) & 1), p.err);
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int row = tid & 127, half = warp >> 2, col0 = 64 * half;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + col0, tG = tmem + lanes + kColG;
+    const float sc = p.scale_log2;
+    unsigned char* box = smem + C::kOffStage + warp * C::kStage;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!dead) dead = !mbar_wait_bounded(bar, parity, p.err);
+    };
+    int n = 0;
+    for (int r = 0;; ++r) {
+      const Item it = list.get(r, more);
+      if (!more) break;
+      if (!it.ok) continue;
+      const int h = it.part, q0 = it.level * kTile;
+      const bool live = q0 + row < it.len;
+      const int64_t at = (int64_t)it.beg + q0 + row, stat = (int64_t)h * p.tokens + at;
+      const float nl = live ? -p.lse[stat] * kLog2e : 0.f;
+      const float nd = live ? -p.delta[stat] : 0.f;
+      for (int t = 0; t <= it.level; ++t, ++n) {
+        uint32_t v[2][32], w[2][32];
+        wait(bar_s, (uint32_t)(n & 1));
+        tc_fence_after();
+        tmem_ld32_nowait(tS, v[0]);
+        tmem_ld32_nowait(tS + 32, v[1]);
+        tmem_ld_wait();
+        wait(bar_dp, (uint32_t)(n & 1));
+        tc_fence_after();
+        tmem_ld32_nowait(tS + kColP, w[0]);
+        tmem_ld32_nowait(tS + kColP + 32, w[1]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float t0, t1;
+            fma2(t0, t1, __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]), sc, sc, nl, nl);
+            v[c][i] = __float_as_uint(ex2(t0));
+            v[c][i + 1] = __float_as_uint(ex2(t1));
+          }
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(bar_read);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float t0, t1;
+            add2(t0, t1, __uint_as_float(w[c][i]), __uint_as_float(w[c][i + 1]), nd, nd);
+            mul2(t0, t1, t0, t1, __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
+            w[c][i] = __float_as_uint(t0);
+            w[c][i + 1] = __float_as_uint(t1);
+          }
+        if (t == it.level) {  // the diagonal: keys after the row
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (col0 + 32 * c + i > row) w[c][i] = 0u;
+        }
+        uint32_t pk[2][16];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            pk[c][i >> 1] = pack_bf16(__uint_as_float(w[c][i]), __uint_as_float(w[c][i + 1]));
+        if (n >= 2) {  // the product that read this buffer is done
+          wait(&bar_g[n & 1], (uint32_t)(((n >> 1) - 1) & 1));
+          tc_fence_after();
+        }
+        const uint32_t tD = tmem + lanes + kColS + 64 * (n & 1) + 32 * half;
+        tmem_st16(tD, pk[0]);
+        tmem_st16(tD + 16, pk[1]);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bar_ds[n & 1]);
+      }
+      wait(&bar_g[(n - 1) & 1], (uint32_t)(((n - 1) >> 1) & 1));
+      tc_fence_after();
+      const int col = D == 128 ? col0 : 0;  // (head_dim 64: the first four warps store)
+      uint32_t o[2][32];
+      tmem_ld32_nowait(tG + col, o[0]);
+      tmem_ld32_nowait(tG + col + 32, o[1]);
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(bar_gfree);
+      if (D == 128 || half == 0)
+        put_box(o[0], o[1], p.scale, box, &maps.out0, col, h, (int)at,
+                const_cast<char*>(p.dq) + (at * p.sdq + (int64_t)h * D + col) * 2,
+                __all_sync(0xffffffffu, live), live);
+    }
+    if (lane == 0) stores_done();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(352, 1)
+    packed_dkv_kernel(const __grid_constant__ BwdMaps maps, const PackedParams p) {
+  using C = Bwd<D>;
+  constexpr int T = C::kTileBytes;
+  constexpr uint32_t kColP = 128, kColV = 256, kColK = 256 + D;  // dP^T, dV, dK
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char *sk = smem, *sv = smem + T;
+  auto sq = [&](int s) { return smem + (2 + s) * T; };
+  auto sg = [&](int s) { return smem + (4 + s) * T; };
+  auto stats = [&](int s) { return reinterpret_cast<float*>(smem + C::kOffStat) + 256 * s; };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBarK);
+  uint64_t* bar_kv = bars;          // K and V landed
+  uint64_t* bar_s = bars + 1;
+  uint64_t* bar_dp = bars + 2;
+  uint64_t* bar_dv = bars + 3;      // dV += P^T dO done
+  uint64_t* bar_dk = bars + 4;      // dK += dS^T Q done
+  uint64_t* bar_p = bars + 5;       // P^T written, 256 arrivals
+  uint64_t* bar_ds = bars + 6;      // dS^T written, 256 arrivals
+  uint64_t* bar_gfree = bars + 7;   // dK and dV read, 256 arrivals
+  uint64_t* bar_kvfree = bars + 8;  // the output boxes (over K and V) are read, 8 arrivals
+  uint64_t* bar_qfull = bars + 10;  // [stage]
+  uint64_t* bar_dofull = bars + 12;
+  uint64_t* bar_stat = bars + 14;   // lse and delta written
+  uint64_t* bar_empty = bars + 16;  // [stage] both products are done with it
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 18);
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tslot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 32 * 8) {
+    for (int i = 0; i < 5; ++i) mbar_init(bars + i, 1);
+    for (int i = 5; i < 8; ++i) mbar_init(bars + i, 256);
+    mbar_init(bar_kvfree, 8);
+    for (int i = 10; i < 16; ++i) mbar_init(bars + i, 1);
+    mbar_init(&bar_empty[0], 2);
+    mbar_init(&bar_empty[1], 2);
+    fence_mbar_init();
+  }
+  Sequences list;
+  list.init(reinterpret_cast<int2*>(smem + C::kOffBarK + 256),
+            reinterpret_cast<int2*>(smem + C::kOffBarK + 256) + kSorted, p, kTile, p.kv_heads);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  const int group = p.heads / p.kv_heads;
+  bool dead = false, more;
+  // Item: key tile `first` of the sequence's nt, level + 1 query tiles of each head of `part`.
+  auto first_of = [&](const Item& it) { return (it.len + kTile - 1) / kTile - 1 - it.level; };
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    int n = 0, items = 0;
+    for (int r = 0;; ++r) {
+      const Item it = list.get(r, more);
+      if (!more) break;
+      if (!it.ok) continue;
+      const int first = first_of(it);
+      if (lane == 0) {
+        if (items > 0) wait_spin(bar_kvfree, (uint32_t)((items - 1) & 1), dead, p.err);
+        if (!dead) {
+          mbar_arrive_expect_tx(bar_kv, 2 * T);
+          for (int b = 0; b < C::kBoxes; ++b) {
+            load_box(sk + b * kBox, &maps.k, 64 * b, it.part, it.beg + first * kTile, bar_kv);
+            load_box(sv + b * kBox, &maps.v, 64 * b, it.part, it.beg + first * kTile, bar_kv);
+          }
+          ++items;
+        }
+      }
+      for (int h = it.part * group; h < (it.part + 1) * group; ++h)
+        for (int i = first; i <= first + it.level; ++i) {
+          const int s = n & 1;
+          if (lane == 0) {
+            if (n >= 2) wait_spin(&bar_empty[s], (uint32_t)(((n >> 1) - 1) & 1), dead, p.err);
+            if (!dead) {
+              mbar_arrive_expect_tx(&bar_qfull[s], T);
+              for (int b = 0; b < C::kBoxes; ++b)
+                load_box(sq(s) + b * kBox, &maps.q, 64 * b, h, it.beg + i * kTile, &bar_qfull[s]);
+              mbar_arrive_expect_tx(&bar_dofull[s], T);
+              for (int b = 0; b < C::kBoxes; ++b)
+                load_box(sg(s) + b * kBox, &maps.g, 64 * b, h, it.beg + i * kTile, &bar_dofull[s]);
+            }
+          }
+          dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
+          if (dead) break;
+          float* st = stats(s);
+          float a[4], d[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int row = i * kTile + 32 * j + lane;
+            const int64_t at = (int64_t)h * p.tokens + it.beg + row;
+            a[j] = row < it.len ? -__ldg(p.lse + at) * kLog2e : 0.f;
+            d[j] = row < it.len ? -p.delta[at] : 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            st[32 * j + lane] = a[j];
+            st[128 + 32 * j + lane] = d[j];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_stat[s]);
+          ++n;
+        }
+    }
+    if (lane == 0) {
+      for (int i = max(n - 2, 0); i < n; ++i) {
+        mbar_wait_bounded(&bar_qfull[i & 1], (uint32_t)((i >> 1) & 1), p.err);
+        mbar_wait_bounded(&bar_dofull[i & 1], (uint32_t)((i >> 1) & 1), p.err);
+      }
+      if (items > 0) mbar_wait_bounded(bar_kv, (uint32_t)((items - 1) & 1), p.err);
+    }
+  } else if (warp >= 9) {
+    // warp 9: S^T = K Q^T, dV += P^T dO; warp 10: dP^T = V dO^T, dK += dS^T Q
+    const bool for_v = warp == 9;
+    const uint32_t a_addr = smem_addr(for_v ? sk : sv);
+    const uint32_t tA = tmem + (for_v ? 0u : kColP), tG = tmem + (for_v ? kColV : kColK);
+    uint64_t* bar_in = for_v ? bar_qfull : bar_dofull;   // the first product's tile
+    uint64_t* bar_sum = for_v ? bar_dofull : bar_qfull;  // the second's
+    uint64_t* bar_a = for_v ? bar_s : bar_dp;
+    uint64_t* bar_w = for_v ? bar_p : bar_ds;
+    uint64_t* bar_g = for_v ? bar_dv : bar_dk;
+    int n = 0, firsts = 0, items = 0;
+    for (int r = 0;; ++r) {
+      const Item it = list.get(r, more);
+      if (!more) break;
+      if (!it.ok) continue;
+      const int first = first_of(it), tiles = group * (it.level + 1);
+      if (lane == 0) wait_spin(bar_kv, (uint32_t)(items & 1), dead, p.err);
+      for (int t = 0, i = first; t < tiles; ++t, i = i == first + it.level ? first : i + 1) {
+        const int s = n & 1;
+        const uint32_t ph = (uint32_t)((n >> 1) & 1);
+        unsigned char* tin = for_v ? sq(s) : sg(s);
+        unsigned char* tsum = for_v ? sg(s) : sq(s);
+        if (lane == 0) {
+          wait_spin(&bar_in[s], ph, dead, p.err);
+          // the weights of the tile before stand where this product goes
+          if (n > 0) wait_spin(bar_g, (uint32_t)((n - 1) & 1), dead, p.err);
+          if (!dead) {
+            tc_fence_after();
+            issue_tiles<D>(tA, a_addr, smem_addr(tin), C::kIdescS);
+            mma_commit(bar_a);
+            ++firsts;
+          }
+          wait_spin(&bar_sum[s], ph, dead, p.err);
+          wait_spin(bar_w, (uint32_t)(n & 1), dead, p.err);
+          if (t == 0 && items > 0) wait_spin(bar_gfree, (uint32_t)((items - 1) & 1), dead, p.err);
+        }
+        dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
+        if (dead) break;
+        const int rest = it.len - i * kTile;
+        if (rest < kTile) clear_rows<D>(tsum, rest);
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t addr = smem_addr(tsum);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_ts(tG, tA + 8 * kk + (kk >= 4 ? 32 : 0), sw128_desc(addr + kk * 2048, kBox, 1024),
+                   C::kIdescG, (t > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(bar_g);
+          mma_commit(&bar_empty[s]);
+        }
+        ++n;
+      }
+      ++items;
+    }
+    if (lane == 0) {
+      if (firsts > 0) mbar_wait_bounded(bar_a, (uint32_t)((firsts - 1) & 1), p.err);
+      if (n > 0) mbar_wait_bounded(bar_g, (uint32_t)((n - 1) & 1), p.err);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int row = tid & 127, half = warp >> 2, col0 = 64 * half;  // key row, query columns
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + col0, tD = tS + kColP;
+    const float sc = p.scale_log2;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!dead) dead = !mbar_wait_bounded(bar, parity, p.err);
+    };
+    int n = 0;
+    for (int r = 0;; ++r) {
+      const Item it = list.get(r, more);
+      if (!more) break;
+      if (!it.ok) continue;
+      const int first = first_of(it), tiles = group * (it.level + 1);
+      for (int t = 0, i = first; t < tiles; ++t, ++n, i = i == first + it.level ? first : i + 1) {
+        const int s = n & 1;
+        const float4* nl = reinterpret_cast<const float4*>(stats(s) + col0);
+        const float4* nd = nl + 32;
+        uint32_t v[2][32], pk[16];
+        // columns [lo, hi) of this thread's 64 see its key
+        const int lo = i == first ? row - col0 : 0, hi = it.len - i * kTile - col0;
+        const bool edge = i == first || it.len - i * kTile < kTile;
+        wait(&bar_stat[s], (uint32_t)((n >> 1) & 1));
+        wait(bar_s, (uint32_t)(n & 1));
+        tc_fence_after();
+        tmem_ld32_nowait(tS, v[0]);
+        tmem_ld32_nowait(tS + 32, v[1]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 l = nl[8 * c + (j >> 2)];
+            float t0, t1, t2, t3;
+            fma2(t0, t1, __uint_as_float(v[c][j]), __uint_as_float(v[c][j + 1]), sc, sc, l.x, l.y);
+            fma2(t2, t3, __uint_as_float(v[c][j + 2]), __uint_as_float(v[c][j + 3]), sc, sc, l.z,
+                 l.w);
+            v[c][j] = __float_as_uint(ex2(t0));
+            v[c][j + 1] = __float_as_uint(ex2(t1));
+            v[c][j + 2] = __float_as_uint(ex2(t2));
+            v[c][j + 3] = __float_as_uint(ex2(t3));
+          }
+          if (edge) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (32 * c + j < lo || 32 * c + j >= hi) v[c][j] = 0u;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            pk[j >> 1] = pack_bf16(__uint_as_float(v[c][j]), __uint_as_float(v[c][j + 1]));
+          tmem_st16(tS + 16 * c, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar_p);
+        wait(bar_dp, (uint32_t)(n & 1));
+        tc_fence_after();
+        uint32_t w[2][32];
+        tmem_ld32_nowait(tD, w[0]);
+        tmem_ld32_nowait(tD + 32, w[1]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 d = nd[8 * c + (j >> 2)];
+            float t0, t1, t2, t3;
+            add2(t0, t1, __uint_as_float(w[c][j]), __uint_as_float(w[c][j + 1]), d.x, d.y);
+            add2(t2, t3, __uint_as_float(w[c][j + 2]), __uint_as_float(w[c][j + 3]), d.z, d.w);
+            mul2(t0, t1, t0, t1, __uint_as_float(v[c][j]), __uint_as_float(v[c][j + 1]));
+            mul2(t2, t3, t2, t3, __uint_as_float(v[c][j + 2]), __uint_as_float(v[c][j + 3]));
+            w[c][j] = __float_as_uint(t0);
+            w[c][j + 1] = __float_as_uint(t1);
+            w[c][j + 2] = __float_as_uint(t2);
+            w[c][j + 3] = __float_as_uint(t3);
+          }
+          if (edge) {  // (0 times a NaN)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (32 * c + j < lo || 32 * c + j >= hi) w[c][j] = 0u;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            pk[j >> 1] = pack_bf16(__uint_as_float(w[c][j]), __uint_as_float(w[c][j + 1]));
+          tmem_st16(tD + 16 * c, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar_ds);
+      }
+      wait(bar_dv, (uint32_t)((n - 1) & 1));
+      wait(bar_dk, (uint32_t)((n - 1) & 1));
+      tc_fence_after();
+      const bool live = first * kTile + row < it.len;
+      const bool whole = __all_sync(0xffffffffu, live);
+      const int64_t at = (int64_t)it.beg + first * kTile + row;
+      const uint32_t tV = tmem + lanes + kColV, tK = tmem + lanes + kColK;
+      char* dv = const_cast<char*>(p.dv) + (at * p.sdv + (int64_t)it.part * D) * 2;
+      char* dk = const_cast<char*>(p.dk) + (at * p.sdk + (int64_t)it.part * D) * 2;
+      uint32_t o[2][32];
+      if constexpr (D == 128) {  // 64 columns of dV and of dK each
+        uint32_t o2[2][32];
+        tmem_ld32_nowait(tV + col0, o[0]);
+        tmem_ld32_nowait(tV + col0 + 32, o[1]);
+        tmem_ld32_nowait(tK + col0, o2[0]);
+        tmem_ld32_nowait(tK + col0 + 32, o2[1]);
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(bar_gfree);
+        unsigned char* box = smem + warp * 2 * C::kStage;
+        put_box(o[0], o[1], 1.f, box, &maps.out1, col0, it.part, (int)at, dv + 2 * col0, whole,
+                live);
+        put_box(o2[0], o2[1], p.scale, box + C::kStage, &maps.out0, col0, it.part, (int)at,
+                dk + 2 * col0, whole, live);
+      } else {  // dV for one half of the warps, dK for the other
+        tmem_ld32_nowait(half ? tK : tV, o[0]);
+        tmem_ld32_nowait((half ? tK : tV) + 32, o[1]);
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(bar_gfree);
+        put_box(o[0], o[1], half ? p.scale : 1.f, smem + warp * C::kStage,
+                half ? &maps.out0 : &maps.out1, 0, it.part, (int)at, half ? dk : dv, whole, live);
+      }
+      if (lane == 0) {
+        stores_read();
+        mbar_arrive(bar_kvfree);
+      }
+    }
+    if (lane == 0) stores_done();
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 0)
@@ -606,10 +1258,14 @@ bool encode_map(CUtensorMap* map, const char* base, int64_t tokens, int heads, i
 
 }  // namespace
 
+template <int D>
+static PackedTcKernels tc_kernels() {
+  return PackedTcKernels{(const void*)packed_fwd_kernel<D>, (const void*)packed_delta_kernel<D>,
+                         (const void*)packed_dq_kernel<D>,  (const void*)packed_dkv_kernel<D>,
+                         Fwd<D>::kSmem, Bwd<D>::kSmemQ, Bwd<D>::kSmemK};
+}
 PackedTcKernels packed_tc_kernels(int d) {
-  if (d == 64) return PackedTcKernels{(const void*)packed_fwd_kernel<64>, Fwd<64>::kSmem};
-  if (d == 128) return PackedTcKernels{(const void*)packed_fwd_kernel<128>, Fwd<128>::kSmem};
-  return PackedTcKernels{nullptr, 0};
+  return d == 64 ? tc_kernels<64>() : d == 128 ? tc_kernels<128>() : PackedTcKernels{};
 }
 
 const char* packed_tc_fwd_launch(const PackedParams& p, int sms, cudaStream_t stream) {
@@ -628,6 +1284,38 @@ const char* packed_tc_fwd_launch(const PackedParams& p, int sms, cudaStream_t st
   void* args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &pc};
   if (cudaLaunchKernel(k.fwd, dim3((unsigned)std::min<int64_t>(sms, items)), dim3(352), args,
                        (size_t)k.fwd_smem, stream) != cudaSuccess)
+    return "launch failed";
+  return nullptr;
+}
+
+const char* packed_tc_bwd_launch(const PackedParams& p, int sms, cudaStream_t stream) {
+  const PackedTcKernels k = packed_tc_kernels(p.dim);
+  BwdMaps mq, mk;
+  if (!encode_map(&mq.q, p.q, p.tokens, p.heads, p.dim, p.sq, kTile) ||
+      !encode_map(&mq.g, p.dout, p.tokens, p.heads, p.dim, p.sdo, kTile) ||
+      !encode_map(&mq.k, p.k, p.tokens, p.kv_heads, p.dim, p.sk, kTile) ||
+      !encode_map(&mq.v, p.v, p.tokens, p.kv_heads, p.dim, p.sv, kTile) ||
+      !encode_map(&mq.out0, p.dq, p.tokens, p.heads, p.dim, p.sdq, 32))
+    return "tensor map encoding failed";
+  mk = mq;
+  if (!encode_map(&mk.out0, p.dk, p.tokens, p.kv_heads, p.dim, p.sdk, 32) ||
+      !encode_map(&mk.out1, p.dv, p.tokens, p.kv_heads, p.dim, p.sdv, 32))
+    return "tensor map encoding failed";
+  mq.out1 = mq.out0;
+  PackedParams pc = p;
+  const int64_t rows = p.tokens * p.heads, per = 8 * (32 / (p.dim / 8));
+  void* dargs[] = {&pc};
+  if (cudaLaunchKernel(k.delta, dim3((unsigned)((rows + per - 1) / per)), dim3(256), dargs, 0,
+                       stream) != cudaSuccess)
+    return "launch failed";
+  const int64_t levels = p.tokens / kTile + p.batch;
+  void* qargs[] = {&mq, &pc};
+  if (cudaLaunchKernel(k.dq, dim3((unsigned)std::min<int64_t>(sms, levels * p.heads)), dim3(352),
+                       qargs, (size_t)k.dq_smem, stream) != cudaSuccess)
+    return "launch failed";
+  void* kargs[] = {&mk, &pc};
+  if (cudaLaunchKernel(k.dkv, dim3((unsigned)std::min<int64_t>(sms, levels * p.kv_heads)),
+                       dim3(352), kargs, (size_t)k.dkv_smem, stream) != cudaSuccess)
     return "launch failed";
   return nullptr;
 }

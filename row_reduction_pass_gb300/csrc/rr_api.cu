@@ -2808,6 +2808,23 @@ rr_status rr_attention_packed_bwd(const void* dout, const void* q, const void* k
   p.dim = (int32_t)head_dim;
   p.scale = scale;
   p.scale_log2 = scale * rr::kLog2e;
+  const rr::PackedTcKernels tk = rr::packed_tc_kernels(dtype == RR_BF16 ? p.dim : 0);
+  if (tk.dq) {
+    int sms = 0;
+    {
+      std::lock_guard<std::mutex> lock(g_mu);
+      DevInfo* di = nullptr;
+      if ((st = device_info(&di)) != RR_OK) return st;
+      if ((st = set_smem(di, tk.dq, (size_t)tk.dq_smem)) != RR_OK) return st;
+      if ((st = set_smem(di, tk.dkv, (size_t)tk.dkv_smem)) != RR_OK) return st;
+      p.err = di->err;
+      sms = di->sms;
+    }
+    if (const char* why = rr::packed_tc_bwd_launch(p, sms, stream))
+      return fail(RR_ERR_CUDA, "packed attention: %s (%s)", why,
+                  cudaGetErrorString(cudaGetLastError()));
+    return ok();
+  }
   const rr::PackedRowKernels rk = rr::packed_row_kernels(dtype == RR_BF16 ? rr::kBF16 : rr::kF32);
   if ((st = packed_rows_launch(rk.dq, p, heads, rk.warps, stream)) != RR_OK) return st;
   return packed_rows_launch(rk.dkv, p, kv_heads, rk.warps, stream);

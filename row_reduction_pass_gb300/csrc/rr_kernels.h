@@ -399,13 +399,14 @@ struct PackedRowKernels {
 };
 PackedRowKernels packed_row_kernels(int dtype);
 struct PackedTcKernels {
-  const void* fwd;
-  int fwd_smem;
+  const void *fwd, *delta, *dq, *dkv;
+  int fwd_smem, dq_smem, dkv_smem;
 };
 // Tensor-core kernels for bf16 of this head dimension; fwd null where there are none.
 PackedTcKernels packed_tc_kernels(int d);
 // Encodes the tensor maps and launches: null on success, else a short reason.
 const char* packed_tc_fwd_launch(const PackedParams& p, int sms, cudaStream_t stream);
+const char* packed_tc_bwd_launch(const PackedParams& p, int sms, cudaStream_t stream);
 
 // The column reduce's split of its 32 warps over the P partial rows: the
 // smallest power of two >= P / 16, at most 32 (the rest of the warps take
