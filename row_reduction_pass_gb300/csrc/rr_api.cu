@@ -2892,18 +2892,41 @@ rr_status rr_token_logprob_fwd(const void* logits, const int32_t* tokens, float*
   p.ignore = ignore_index;
   p.temperature = temperature;
   p.c = rr::kLog2e / temperature;
-  int sms = 0;
+  const rr::LogprobKernels lk = rr::logprob_kernels(dtype == RR_BF16 ? rr::kBF16 : rr::kF32);
+  // Rows that leave SMs idle are cut over a cluster, as long as a block keeps 4 KB.
+  int K = 1, occ = 0;
+  const void* fn = nullptr;
+  int64_t grid = 0;
   {
     std::lock_guard<std::mutex> lock(g_mu);
     DevInfo* di = nullptr;
     if ((st = device_info(&di)) != RR_OK) return st;
-    sms = di->sms;
-    p.err = di->err;
+    while (K < 8 && rows * K * 2 <= 2 * (int64_t)di->sms && cols * E / (K * 2) >= 4096) K *= 2;
+    fn = lk.fwd[rank != nullptr][K > 1];
+    if (K == 1) {
+      int& o = di->occ[{fn, (long long)lk.threads << 32}];
+      if (o == 0) {
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, fn, lk.threads, 0);
+        if (e != cudaSuccess || o <= 0)
+          return fail(RR_ERR_CUDA, "occupancy query: %s", cudaGetErrorString(e));
+      }
+      occ = o;
+    }
+    grid = K > 1 ? rows * K : std::min<int64_t>(rows, (int64_t)di->sms * occ);
   }
-  const rr::LogprobKernels lk = rr::logprob_kernels(dtype == RR_BF16 ? rr::kBF16 : rr::kF32);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)lk.threads);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = K;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = K > 1 ? 1 : 0;
   void* args[] = {&p};
-  cudaError_t e = cudaLaunchKernel(lk.fwd, dim3((unsigned)std::min<int64_t>(rows, 8 * (int64_t)sms)),
-                                   dim3((unsigned)lk.threads), args, 0, stream);
+  cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
   if (e != cudaSuccess) return fail(RR_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
   return ok();
 }

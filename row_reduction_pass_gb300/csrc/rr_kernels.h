@@ -354,7 +354,6 @@ struct LogprobParams {
   int32_t* top_index;     // [rows][k]
   float* top_logprob;     // [rows][k]
   int32_t* bad;           // counter of tokens out of range, or null
-  int* err;
   int64_t rows, cols, stride;
   int32_t k, ignore;
   float temperature, c;   // c = log2 e / temperature
@@ -370,7 +369,7 @@ struct LogprobBwdParams {
   float temperature, c;
 };
 struct LogprobKernels {
-  const void* fwd;
+  const void* fwd[2][2];  // [rank wanted][a row on a cluster]
   const void* bwd[2];     // [elements, 16-byte chunks]
   int threads;
   int bwd_bytes;          // of a row that a block of the backward takes
