@@ -2902,11 +2902,14 @@ rr_status rr_token_logprob_fwd(const void* logits, const int32_t* tokens, float*
     DevInfo* di = nullptr;
     if ((st = device_info(&di)) != RR_OK) return st;
     while (K < 8 && rows * K * 2 <= 2 * (int64_t)di->sms && cols * E / (K * 2) >= 4096) K *= 2;
-    fn = lk.fwd[rank != nullptr][K > 1];
+    p.err = di->err;
+    fn = (K > 1 ? lk.cluster : lk.rows)[rank != nullptr];
     if (K == 1) {
-      int& o = di->occ[{fn, (long long)lk.threads << 32}];
+      if ((st = set_smem(di, fn, (size_t)lk.rows_smem)) != RR_OK) return st;
+      int& o = di->occ[{fn, (long long)lk.rows_threads << 32 | lk.rows_smem}];
       if (o == 0) {
-        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, fn, lk.threads, 0);
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, fn, lk.rows_threads,
+                                                                      (size_t)lk.rows_smem);
         if (e != cudaSuccess || o <= 0)
           return fail(RR_ERR_CUDA, "occupancy query: %s", cudaGetErrorString(e));
       }
@@ -2917,7 +2920,8 @@ rr_status rr_token_logprob_fwd(const void* logits, const int32_t* tokens, float*
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)lk.threads);
+  cfg.blockDim = dim3((unsigned)(K > 1 ? lk.threads : lk.rows_threads));
+  cfg.dynamicSmemBytes = K > 1 ? 0 : (size_t)lk.rows_smem;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = K;

@@ -230,7 +230,7 @@ struct DistillGeo {
 };
 struct DistillKernels {
   const void* rows;       // a block per row, any alignment and length
-  int rows_threads;
+  int rows_threads, rows_smem;
   const void* stream[2];  // [cluster]
   int slots_off;          // stream: byte offset of the [4][K * (row warps + 1)] slots
 };
@@ -354,6 +354,7 @@ struct LogprobParams {
   int32_t* top_index;     // [rows][k]
   float* top_logprob;     // [rows][k]
   int32_t* bad;           // counter of tokens out of range, or null
+  int* err;
   int64_t rows, cols, stride;
   int32_t k, ignore;
   float temperature, c;   // c = log2 e / temperature
@@ -369,9 +370,11 @@ struct LogprobBwdParams {
   float temperature, c;
 };
 struct LogprobKernels {
-  const void* fwd[2][2];  // [rank wanted][a row on a cluster]
-  const void* bwd[2];     // [elements, 16-byte chunks]
-  int threads;
+  const void* rows[2];     // [rank wanted] a row a block at a time
+  const void* cluster[2];  // [rank wanted] a row on a cluster of up to 8 blocks
+  const void* bwd[2];      // [elements, 16-byte chunks]
+  int threads;             // of the cluster and backward kernels
+  int rows_threads, rows_smem;
   int bwd_bytes;          // of a row that a block of the backward takes
 };
 LogprobKernels logprob_kernels(int dtype);
