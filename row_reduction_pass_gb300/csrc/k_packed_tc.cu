@@ -4,13 +4,17 @@
 // Forward.  A block, one per SM, works on two tiles of 128 query rows at once that attend
 // to the same keys (halves 0 and 1): two heads of a key head's group over the same tokens,
 // or, where the group is odd, two neighbouring tiles of one head.  Key and value tiles of
-// 128 tokens are loaded once for both.  Per half and key tile: S = Q K^T into TMEM, a
-// softmax warpgroup of four warps (thread t owns row t, TMEM lane t) turns it into bf16
-// weights in TMEM with the running maximum and sum of the online softmax, O += P V.
-// While one half is in its softmax the tensor cores work for the other.
-//   head_dim 128: a half's 256 TMEM columns are S (128), whose first half P overwrites, and
-//     O (128); S of the next tile follows O += P V of this one.
-//   head_dim 64: S (128), P (64) and O (64); S of the next tile as soon as S has been read.
+// 128 tokens are loaded once for both and used as two sub-tiles of 64.  Per half and
+// sub-tile: S = Q K^T into one of two TMEM buffers, a softmax warpgroup of four warps (thread
+// t owns row t, TMEM lane t) turns it into bf16 weights in TMEM with the running maximum and
+// sum of the online softmax, O += P V.  S of the next sub-tile is there when a softmax ends
+// (with one buffer of 128 keys each step was S, softmax and O += P V one after the other, and
+// both halves in step: 5080 cycles a tile of 128 keys, of which the products need 2200).
+//   head_dim 128: a half's 256 TMEM columns are S (2 x 64), which P overwrites, and O (128);
+//     S of u + 2 follows O += P V of u.
+//   head_dim 64: S (2 x 64), P (2 x 32) and O (64); S of u + 2 as soon as S of u is read.
+// A product alone takes 85 to 130 cycles for 128 x 128 x 16, two that do not depend on each
+// other 66 each: the halves' products have an issuing warp each.
 // Roles: warps 0-3 and 4-7 the halves' softmax, warp 8 loads (TMA), warps 9 and 10 issue the
 // halves' products.
 //
@@ -36,6 +40,7 @@ namespace {
 
 constexpr int kTile = 128;           // query rows and keys of a tile
 constexpr int kBox = kTile * 128;    // bytes of 128 rows x 64 columns
+constexpr int kSub = 64;             // keys of a sub-tile (forward)
 constexpr int kSorted = 128;         // sequences that a block sorts
 
 // TMA box [128 tokens x 1 head x 64 columns] at {column, head, token}.
@@ -168,8 +173,10 @@ struct Fwd {
   static constexpr int kOffBar = kOffStage + 8 * kStage;
   static constexpr int kOffSeq = kOffBar + 256;
   static constexpr int kSmem = kOffSeq + kSorted * 8 + 1024;
-  static constexpr uint32_t kColP = D == 128 ? 0 : 128, kColO = 256 - D;
-  static constexpr uint32_t kIdescS = attn_idesc(kTile, kTile, false);
+  // columns of a half: S buffer b at 64 b, P buffer b at kColP0 + kStepP b, O
+  static constexpr uint32_t kColP0 = D == 128 ? 0 : 128, kStepP = D == 128 ? 64 : 32;
+  static constexpr uint32_t kColO = 256 - D;
+  static constexpr uint32_t kIdescS = attn_idesc(kTile, kSub, false);
   static constexpr uint32_t kIdescO = attn_idesc(kTile, D, true);
 };
 
@@ -255,9 +262,10 @@ __device__ __noinline__ void repair_row(const PackedParams& p, int64_t begin, in
   for (int i = 0; i < D / 32; ++i) st_elem<kBF16>(o + 2 * (lane + 32 * i), acc[i] / l);
 }
 
-// A half's query tile of an item: its first row in the sequence, head and key tiles (0: none).
+// A half's query tile of an item: its first row in the sequence, head, key tiles (0: none) and
+// sub-tiles.
 struct Half {
-  int row0, head, tiles;
+  int row0, head, tiles, subs;
 };
 __device__ __forceinline__ Half half_of(const Item& it, int h, int group, bool even) {
   Half x;
@@ -267,6 +275,7 @@ __device__ __forceinline__ Half half_of(const Item& it, int h, int group, bool e
   x.head = kv * group + (even ? 2 * pair + h : pair);
   x.row0 = tile * kTile;
   x.tiles = it.ok && x.row0 < it.len ? tile + 1 : 0;
+  x.subs = x.tiles ? (min(it.len, x.row0 + kTile) + kSub - 1) / kSub : 0;
   return x;
 }
 
@@ -285,16 +294,16 @@ __global__ void __launch_bounds__(352, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* bar_q = bars;           // [half] Q landed
   uint64_t* bar_qfree = bars + 2;   // [half] the item's last S done
-  uint64_t* bar_s = bars + 4;       // [half] S done
-  uint64_t* bar_sfree = bars + 6;   // [half] S read (head_dim 64), 128 arrivals
-  uint64_t* bar_p = bars + 8;       // [half] P written, 128 arrivals
-  uint64_t* bar_o = bars + 10;      // [half] O += P V done
-  uint64_t* bar_ofree = bars + 12;  // [half] O read, 128 arrivals
-  uint64_t* bar_kfull = bars + 14;  // [stage]
-  uint64_t* bar_vfull = bars + 16;
-  uint64_t* bar_kempty = bars + 18; // [stage] both halves' S done
-  uint64_t* bar_vempty = bars + 20; // [stage] both halves' O += P V done
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 22);
+  uint64_t* bar_ofree = bars + 4;   // [half] O read, 128 arrivals
+  uint64_t* bar_kfull = bars + 6;   // [stage]
+  uint64_t* bar_vfull = bars + 8;
+  uint64_t* bar_kempty = bars + 10; // [stage] both halves' S done
+  uint64_t* bar_vempty = bars + 12; // [stage] both halves' O += P V done
+  uint64_t* bar_s = bars + 14;      // [half][buffer] S done
+  uint64_t* bar_o = bars + 18;      // [half][buffer] O += P V done
+  uint64_t* bar_sfree = bars + 22;  // [half][buffer] S read (head_dim 64), 128 arrivals
+  uint64_t* bar_p = bars + 26;      // [half][buffer] P written, 128 arrivals
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 30);
 
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -307,15 +316,17 @@ __global__ void __launch_bounds__(352, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_q[i], 1);
       mbar_init(&bar_qfree[i], 1);
-      mbar_init(&bar_s[i], 1);
-      mbar_init(&bar_sfree[i], 128);
-      mbar_init(&bar_p[i], 128);
-      mbar_init(&bar_o[i], 1);
       mbar_init(&bar_ofree[i], 128);
       mbar_init(&bar_kfull[i], 1);
       mbar_init(&bar_vfull[i], 1);
       mbar_init(&bar_kempty[i], 2);
       mbar_init(&bar_vempty[i], 2);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar_s[i], 1);
+      mbar_init(&bar_o[i], 1);
+      mbar_init(&bar_sfree[i], 128);
+      mbar_init(&bar_p[i], 128);
     }
     fence_mbar_init();
   }
@@ -382,68 +393,64 @@ __global__ void __launch_bounds__(352, 1)
     const uint32_t tm = tmem + 256u * h;
     const uint32_t q_addr = smem_addr(smem + h * C::kTileBytes);
     int kc = 0, ns = 0, no = 0, items = 0;  // key tiles loaded, products issued, items
+    bar_s += 2 * h, bar_o += 2 * h, bar_sfree += 2 * h, bar_p += 2 * h;
     auto stage = [&](int t) { return (kc + t) & 1; };
     auto phase = [&](int t) { return (uint32_t)(((kc + t) >> 1) & 1); };
-    auto issue_s = [&](int t, bool last) {
-      const uint32_t k_addr = smem_addr(smem + C::kOffK + stage(t) * C::kTileBytes);
-      wait_spin(&bar_kfull[stage(t)], phase(t), dead, p.err);
+    auto issue_s = [&](int u, int subs) {  // of sub-tile u
+      const int st = stage(u >> 1), b = ns & 1;
+      wait_spin(&bar_kfull[st], phase(u >> 1), dead, p.err);
+      if (ns >= 2)  // what is in its buffer has been used
+        wait_spin(D == 128 ? &bar_o[b] : &bar_sfree[b], (uint32_t)(((ns >> 1) - 1) & 1), dead, p.err);
       if (dead) return;
       tc_fence_after();
+      const uint32_t k_addr = smem_addr(smem + C::kOffK + st * C::kTileBytes) + (u & 1) * kSub * 128;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (uint32_t)((kk >> 2) * kBox + (kk & 3) * 32);
-        mma_ss(tm, sw128_desc(q_addr + off, 16, 1024), sw128_desc(k_addr + off, 16, 1024),
-               C::kIdescS, kk > 0 ? 1u : 0u);
+        mma_ss(tm + 64 * b, sw128_desc(q_addr + off, 16, 1024),
+               sw128_desc(k_addr + off, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u);
       }
       ++ns;
-      mma_commit(&bar_s[h]);
-      mma_commit(&bar_kempty[stage(t)]);
-      if (last) mma_commit(&bar_qfree[h]);
+      mma_commit(&bar_s[b]);
+      if ((u & 1) || u == subs - 1) mma_commit(&bar_kempty[st]);
+      if (u == subs - 1) mma_commit(&bar_qfree[h]);
     };
-    auto issue_pv = [&](int t) {
-      const uint32_t v_addr = smem_addr(smem + C::kOffV + stage(t) * C::kTileBytes);
-      wait_spin(&bar_vfull[stage(t)], phase(t), dead, p.err);
+    auto issue_pv = [&](int u, int subs) {
+      const int st = stage(u >> 1), b = no & 1;
+      wait_spin(&bar_p[b], (uint32_t)((no >> 1) & 1), dead, p.err);
+      if (u == 0 && items > 0) wait_spin(&bar_ofree[h], (uint32_t)((items - 1) & 1), dead, p.err);
+      wait_spin(&bar_vfull[st], phase(u >> 1), dead, p.err);
       if (dead) return;
       tc_fence_after();
+      const uint32_t v_addr = smem_addr(smem + C::kOffV + st * C::kTileBytes) + (u & 1) * kSub * 128;
 #pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk)
-        mma_ts(tm + C::kColO, tm + C::kColP + 8 * kk, sw128_desc(v_addr + kk * 2048, kBox, 1024),
-               C::kIdescO, (t > 0 || kk > 0) ? 1u : 0u);
+      for (int kk = 0; kk < kSub / 16; ++kk)
+        mma_ts(tm + C::kColO, tm + C::kColP0 + C::kStepP * b + 8 * kk,
+               sw128_desc(v_addr + kk * 2048, kBox, 1024), C::kIdescO, (u > 0 || kk > 0) ? 1u : 0u);
       ++no;
-      mma_commit(&bar_o[h]);
-      mma_commit(&bar_vempty[stage(t)]);
+      mma_commit(&bar_o[b]);
+      if ((u & 1) || u == subs - 1) mma_commit(&bar_vempty[st]);
     };
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
       if (!it.ok) continue;
-      const int nh = half_of(it, h, group, even).tiles;
-      const int n = max(nh, half_of(it, 1 - h, group, even).tiles);
+      const Half x = half_of(it, h, group, even);
+      const int n = max(x.tiles, half_of(it, 1 - h, group, even).tiles);
       if (lane == 0) {
-        if (nh > 0) {
+        if (x.subs > 0) {
           wait_spin(&bar_q[h], (uint32_t)(items & 1), dead, p.err);
-          if (D == 64) {
-            if (ns > 0) wait_spin(&bar_sfree[h], (uint32_t)((ns - 1) & 1), dead, p.err);
-            issue_s(0, nh == 1);
-          }
+          issue_s(0, x.subs);
+          if (x.subs > 1) issue_s(1, x.subs);
         }
-        for (int t = 0; t < nh && !dead; ++t) {
-          if (D == 128) {
-            // P of the tile before stands where S goes
-            if (no > 0) wait_spin(&bar_o[h], (uint32_t)((no - 1) & 1), dead, p.err);
-            issue_s(t, t == nh - 1);
-          } else if (t + 1 < nh) {
-            wait_spin(&bar_sfree[h], (uint32_t)(no & 1), dead, p.err);
-            issue_s(t + 1, t + 1 == nh - 1);
-          }
-          wait_spin(&bar_p[h], (uint32_t)(no & 1), dead, p.err);
-          if (t == 0 && items > 0)
-            wait_spin(&bar_ofree[h], (uint32_t)((items - 1) & 1), dead, p.err);
-          issue_pv(t);
+        for (int u = 0; u < x.subs && !dead; ++u) {
+          if (D == 64 && u + 2 < x.subs) issue_s(u + 2, x.subs);
+          issue_pv(u, x.subs);
+          if (D == 128 && u + 2 < x.subs) issue_s(u + 2, x.subs);
         }
         // the other half's tiles: a stage is given back once it has landed, so that its
         // barrier's phases keep their order
-        for (int t = nh; t < n && !dead; ++t) {
+        for (int t = x.tiles; t < n && !dead; ++t) {
           wait_spin(&bar_kfull[stage(t)], phase(t), dead, p.err);
           if (!dead) mbar_arrive(&bar_kempty[stage(t)]);
           wait_spin(&bar_vfull[stage(t)], phase(t), dead, p.err);
@@ -451,18 +458,19 @@ __global__ void __launch_bounds__(352, 1)
         }
       }
       kc += n;
-      items += nh > 0;
+      items += x.subs > 0;
     }
-    if (ns > 0) mbar_wait_bounded(&bar_s[h], (uint32_t)((ns - 1) & 1), p.err);
-    if (no > 0) mbar_wait_bounded(&bar_o[h], (uint32_t)((no - 1) & 1), p.err);
+    if (ns > 0) mbar_wait_bounded(&bar_s[(ns - 1) & 1], (uint32_t)(((ns - 1) >> 1) & 1), p.err);
+    if (no > 0) mbar_wait_bounded(&bar_o[(no - 1) & 1], (uint32_t)(((no - 1) >> 1) & 1), p.err);
   } else {
     // ------------------------------------------------- a half's softmax
     const int h = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + 256u * h + lanes, tP = tS + C::kColP, tO = tS + C::kColO;
+    const uint32_t tm = tmem + 256u * h + lanes, tO = tm + C::kColO;
     const float sc = p.scale_log2;
     unsigned char* box = smem + C::kOffStage + warp * C::kStage;
-    int th = 0;
+    int n = 0;  // sub-tiles
+    bar_s += 2 * h, bar_o += 2 * h, bar_sfree += 2 * h, bar_p += 2 * h;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!dead) dead = !mbar_wait_bounded(bar, parity, p.err);
     };
@@ -470,31 +478,33 @@ __global__ void __launch_bounds__(352, 1)
       const Item it = list.get(r, more);
       if (!more) break;
       const Half x = half_of(it, h, group, even);
-      if (x.tiles == 0) continue;
+      if (x.subs == 0) continue;
       float m = -INFINITY, l = 0.f;
-      for (int t = 0; t < x.tiles; ++t, ++th) {
-        wait(&bar_s[h], (uint32_t)(th & 1));
+      for (int u = 0; u < x.subs; ++u, ++n) {
+        const int b = n & 1;
+        wait(&bar_s[b], (uint32_t)((n >> 1) & 1));
         tc_fence_after();
-        uint32_t v[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_nowait(tS + 32 * c, v[c]);
+        uint32_t v[2][32];
+        tmem_ld32_nowait(tm + 64 * b, v[0]);
+        tmem_ld32_nowait(tm + 64 * b + 32, v[1]);
         tmem_ld_wait();
         if (D == 64) {
           tc_fence_before();
-          mbar_arrive(&bar_sfree[h]);
+          mbar_arrive(&bar_sfree[b]);
         }
-        if (t == x.tiles - 1) {  // the diagonal: keys after the row
+        if (u * kSub + kSub - 1 > x.row0) {  // the diagonal: keys after the row
+          const int last = x.row0 + row - u * kSub;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (32 * c + i > row) v[c][i] = __float_as_uint(-INFINITY);
+              if (32 * c + i > last) v[c][i] = __float_as_uint(-INFINITY);
         }
         float mx[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mx[k] = -INFINITY;
+        for (int k = 0; k < 8; ++k) mx[k] = __uint_as_float(v[0][k]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int i = 0; i < 32; ++i) mx[i & 7] = fmaxf(mx[i & 7], __uint_as_float(v[c][i]));
         const float mx0 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
@@ -506,9 +516,9 @@ __global__ void __launch_bounds__(352, 1)
         const float ref = mn == -INFINITY ? 0.f : mn;
         const float alpha = ex2(m - ref);
         float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-        uint32_t pk[4][16];
+        uint32_t pk[2][16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             float t0, t1, t2, t3;
@@ -523,35 +533,37 @@ __global__ void __launch_bounds__(352, 1)
           }
         l = l * alpha + ((l0 + l1) + (l2 + l3));
         m = mn;
-        if (D == 64 && th > 0) {  // the product before is done with P and O
-          wait(&bar_o[h], (uint32_t)((th - 1) & 1));
+        if (D == 64 && n >= 2) {  // the product before is done with the buffer
+          wait(&bar_o[b], (uint32_t)(((n >> 1) - 1) & 1));
           tc_fence_after();
         }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_st16(tP + 16 * c, pk[c]);
-        if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          uint32_t o[D / 32][32];
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) tmem_ld32_nowait(tO + 32 * c, o[c]);
-          tmem_ld_wait();
+        const uint32_t tP = tm + C::kColP0 + C::kStepP * b;
+        tmem_st16(tP, pk[0]);
+        tmem_st16(tP + 16, pk[1]);
+        if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          wait(&bar_o[b ^ 1], (uint32_t)(((n - 1) >> 1) & 1));
+          tc_fence_after();
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32_nowait(tO + 32 * c, o);
+            tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               float a0, a1;
-              mul2(a0, a1, __uint_as_float(o[c][i]), __uint_as_float(o[c][i + 1]), alpha, alpha);
-              o[c][i] = __float_as_uint(a0);
-              o[c][i + 1] = __float_as_uint(a1);
+              mul2(a0, a1, __uint_as_float(o[i]), __uint_as_float(o[i + 1]), alpha, alpha);
+              o[i] = __float_as_uint(a0);
+              o[i + 1] = __float_as_uint(a1);
             }
-            tmem_st32(tO + 32 * c, o[c]);
+            tmem_st32(tO + 32 * c, o);
           }
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&bar_p[h]);
+        mbar_arrive(&bar_p[b]);
       }
       // O / l and lse
-      wait(&bar_o[h], (uint32_t)((th - 1) & 1));
+      wait(&bar_o[(n - 1) & 1], (uint32_t)(((n - 1) >> 1) & 1));
       tc_fence_after();
       uint32_t o[D / 32][32];
 #pragma unroll

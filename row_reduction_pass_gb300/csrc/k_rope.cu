@@ -12,8 +12,8 @@
 // A lane owns a slot of a row: two chunks of W elements that hold W whole pairs (halves:
 // chunk j and the one R / 2 elements on; neighbours: two adjacent chunks), so the rotation
 // needs no exchange and the row's one sum is a butterfly over its D / 2W lanes.  A warp
-// takes 32 / G heads of one token at a time and walks over the token's heads, queries
-// then keys, with the token's cosines and sines in registers.
+// takes 32 / G heads of one token at a time and walks over the token's queries (or keys)
+// with the token's cosines and sines in registers.
 #include <cstdint>
 
 #include "rr_device.cuh"
@@ -23,6 +23,7 @@ namespace rr {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kFwdU = 2, kBwdU = 2, kFwdBlocks = 4, kBwdBlocks = 2;
 
 // What a lane keeps of the row's layout: element offsets of its slots.
 template <int W, int NS>
@@ -140,189 +141,271 @@ __device__ __forceinline__ void angles(float (&c)[NS][W], float (&s)[NS][W],
   }
 }
 
-template <int DT, int W, int NS>
-__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeParams p) {
+// A warp's share of the work: units of rows of one kind (all queries' units, then the keys'),
+// each a token's rows [first, last) of that kind.  Units of a warp are gridDim x warps apart.
+struct Unit {
+  int64_t t;
+  int first, last;
+  bool isq;
+};
+__device__ __forceinline__ Unit unit_of(const RopeParams& p, int64_t u) {
+  Unit x;
+  const int64_t nq = p.tokens * p.q_segs;
+  x.isq = u < nq;
+  const int segs = x.isq ? p.q_segs : p.k_segs, rows = x.isq ? p.q_rows : p.k_rows;
+  const int64_t v = x.isq ? u : u - nq;
+  x.t = v / segs;
+  x.first = (int)(v - x.t * segs) * rows;
+  x.last = min(x.isq ? p.heads : p.kv_heads, x.first + rows);
+  return x;
+}
+__device__ __forceinline__ int position_of(const RopeParams& p, int64_t t) {
+  return p.positions ? __ldg(p.positions + t) : (int)t;
+}
+__device__ __forceinline__ void count_bad(const RopeParams& p, const Unit& x, int pos) {
+  if (p.bad && pos >= p.positions_n && x.isq && x.first == 0 && (threadIdx.x & 31) == 0)
+    atomicAdd(p.bad, 1);
+}
+
+// A slot's two chunks as they are stored.
+template <int DT, int W>
+struct Raw {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const char* x, int ea, int eb) {
+    constexpr int E = DType<DT>::E;
+    if constexpr (W == 1) {
+      a.x = ld_elem_bits<DT>(x + ea * E);
+      b.x = ld_elem_bits<DT>(x + eb * E);
+    } else {
+      a = ld_chunk_stream(x + ea * E);
+      b = ld_chunk_stream(x + eb * E);
+    }
+  }
+  __device__ __forceinline__ void get(float (&fa)[W], float (&fb)[W]) const {
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      fa[e] = W == 1 ? bits_to_f32<DT>(a.x) : chunk_get<DT>(a, e);
+      fb[e] = W == 1 ? bits_to_f32<DT>(b.x) : chunk_get<DT>(b, e);
+    }
+  }
+};
+
+// U row groups' loads are issued before the first is needed: what bounds the kernel is how
+// many bytes are under way.
+template <int DT, int W, int NS, int U>
+__global__ void __launch_bounds__(kThreads, kFwdBlocks) rope_fwd_kernel(const RopeParams p) {
   constexpr int E = DType<DT>::E;
   const int lane = threadIdx.x & 31;
   const int gl = lane & (p.group - 1), sub = lane / p.group, per = 32 / p.group;
-  const int rows = p.heads + p.kv_heads;
   const Slots<W, NS> sl(gl, p);
   const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  const int64_t units = p.tokens * p.segs;
-  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < units;
-       u += warps) {
-    const int64_t t = u / p.segs;
-    const int seg = (int)(u - t * p.segs);
-    const int pos = p.positions ? __ldg(p.positions + t) : (int)t;
-    if (pos >= p.positions_n && seg == 0 && lane == 0 && p.bad) atomicAdd(p.bad, 1);
+  const int64_t units = p.tokens * (p.q_segs + p.k_segs);
+  int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (u >= units) return;
+  Unit x = unit_of(p, u);
+  int pos = position_of(p, x.t);
+  while (true) {
+    const Unit now = x;
+    const int at = pos;
+    u += warps;
+    if (u < units) {
+      x = unit_of(p, u);
+      pos = position_of(p, x.t);
+    }
+    const char* in = (now.isq ? p.q + now.t * p.q_stride * E : p.k + now.t * p.k_stride * E);
+    char* out = (now.isq ? p.qo + now.t * p.qo_stride * E : p.ko + now.t * p.ko_stride * E);
+    const char* w = now.isq ? p.qw : p.kw;
+    count_bad(p, now, at);
     float c[NS][W], s[NS][W];
-    angles<W, NS>(c, s, sl, p, pos);
-    const int last = min(rows, (seg + 1) * p.seg_rows);
-    for (int r0 = seg * p.seg_rows; r0 < last; r0 += per) {
-      const int h = r0 + sub;
-      const bool live = h < last, isq = h < p.heads;
-      const int64_t in = (isq ? t * p.q_stride + (int64_t)h * p.dim
-                              : t * p.k_stride + (int64_t)(h - p.heads) * p.dim) * E;
-      const char* x = (isq ? p.q : p.k) + in;
-      float a[NS][W], b[NS][W];
-      float ss = 0.f;
+    for (int r0 = now.first; r0 < now.last; r0 += U * per) {
+      Raw<DT, W> raw[U][NS];
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
+      for (int k = 0; k < U; ++k) {
+        const int h = r0 + k * per + sub;
 #pragma unroll
-        for (int e = 0; e < W; ++e) a[i][e] = b[i][e] = 0.f;
-        if (live && sl.on[i]) {
-          load<DT, W>(a[i], x + (int64_t)sl.ea[i] * E);
-          load<DT, W>(b[i], x + (int64_t)sl.eb[i] * E);
+        for (int i = 0; i < NS; ++i) {
+          raw[k][i].a = raw[k][i].b = make_uint4(0, 0, 0, 0);
+          if (h < now.last && sl.on[i]) raw[k][i].load(in + (int64_t)h * p.dim * E, sl.ea[i], sl.eb[i]);
         }
-#pragma unroll
-        for (int e = 0; e < W; ++e) ss += a[i][e] * a[i][e] + b[i][e] * b[i][e];
       }
-      const float ms = group_sum(ss, p.group) * p.inv_dim;
-      const bool keep = pos >= 0 && ms <= 3.402823466e38f && ms + p.eps > 0.f;
-      const float r = keep ? rsqrtf(ms + p.eps) : 0.f;
-      if (!live) continue;
-      const int64_t out = (isq ? t * p.qo_stride + (int64_t)h * p.dim
-                               : t * p.ko_stride + (int64_t)(h - p.heads) * p.dim) * E;
-      char* y = (isq ? p.qo : p.ko) + out;
-      const char* w = isq ? p.qw : p.kw;
+      if (r0 == now.first) angles<W, NS>(c, s, sl, p, at);
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        if (!sl.on[i]) continue;
-        if (keep) {
-          float wa[W], wb[W];
+      for (int k = 0; k < U; ++k) {
+        const int h = r0 + k * per + sub;
+        if (r0 + k * per >= now.last) break;
+        float a[NS][W], b[NS][W], ss = 0.f;
 #pragma unroll
-          for (int e = 0; e < W; ++e) wa[e] = wb[e] = 1.f;
-          if (w) {
-            load_cached<DT, W>(wa, w + sl.ea[i] * E);
-            load_cached<DT, W>(wb, w + sl.eb[i] * E);
-          }
+        for (int i = 0; i < NS; ++i) {
+          raw[k][i].get(a[i], b[i]);
 #pragma unroll
-          for (int e = 0; e < W; ++e) a[i][e] *= r * wa[e], b[i][e] *= r * wb[e];
-          turn<W>(a[i], b[i], c[i], s[i], p.interleaved);
-        } else {
-#pragma unroll
-          for (int e = 0; e < W; ++e) a[i][e] = b[i][e] = 0.f;
+          for (int e = 0; e < W; ++e) ss += a[i][e] * a[i][e] + b[i][e] * b[i][e];
         }
-        store<DT, W>(y + (int64_t)sl.ea[i] * E, a[i]);
-        store<DT, W>(y + (int64_t)sl.eb[i] * E, b[i]);
+        const float ms = group_sum(ss, p.group) * p.inv_dim;
+        const bool keep = at >= 0 && ms <= 3.402823466e38f && ms + p.eps > 0.f;
+        const float r = keep ? rsqrtf(ms + p.eps) : 0.f;
+        if (h >= now.last) continue;
+        char* y = out + (int64_t)h * p.dim * E;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          if (!sl.on[i]) continue;
+          if (keep) {
+            float wa[W], wb[W];
+#pragma unroll
+            for (int e = 0; e < W; ++e) wa[e] = wb[e] = 1.f;
+            if (w) {
+              load_cached<DT, W>(wa, w + sl.ea[i] * E);
+              load_cached<DT, W>(wb, w + sl.eb[i] * E);
+            }
+#pragma unroll
+            for (int e = 0; e < W; ++e) a[i][e] *= r * wa[e], b[i][e] *= r * wb[e];
+            turn<W>(a[i], b[i], c[i], s[i], p.interleaved);
+          } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e) a[i][e] = b[i][e] = 0.f;
+          }
+          store<DT, W>(y + sl.ea[i] * E, a[i]);
+          store<DT, W>(y + sl.eb[i] * E, b[i]);
+        }
       }
     }
+    if (u >= units) return;
   }
 }
 
 // dx of every row, and this block's sums over its rows of g x r for the two weights, in
-// workspace row blockIdx.x ([2][D] floats), which col_reduce_kernel adds up.
-template <int DT, int W, int NS>
-__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const RopeParams p) {
+// workspace row blockIdx.x ([2][D] floats), which col_reduce_kernel adds up.  A warp's rows
+// are queries first, then keys: one set of sums, put aside between the two.
+template <int DT, int W, int NS, int U>
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) rope_bwd_kernel(const RopeParams p) {
   constexpr int E = DType<DT>::E;
   extern __shared__ float part[];  // [warps][2][D]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gl = lane & (p.group - 1), sub = lane / p.group, per = 32 / p.group;
-  const int rows = p.heads + p.kv_heads;
   const Slots<W, NS> sl(gl, p);
-  float acc[2][NS][2][W];
+  float acc[NS][2][W];
 #pragma unroll
-  for (int i = 0; i < 2 * NS * 2 * W; ++i) (&acc[0][0][0][0])[i] = 0.f;
-  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  const int64_t units = p.tokens * p.segs;
-  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + warp; u < units; u += warps) {
-    const int64_t t = u / p.segs;
-    const int seg = (int)(u - t * p.segs);
-    const int pos = p.positions ? __ldg(p.positions + t) : (int)t;
-    if (pos >= p.positions_n && seg == 0 && lane == 0 && p.bad) atomicAdd(p.bad, 1);
-    float c[NS][W], s[NS][W];
-    angles<W, NS>(c, s, sl, p, pos);
+  for (int i = 0; i < NS * 2 * W; ++i) (&acc[0][0][0])[i] = 0.f;
+  // the warp's row groups, in a fixed order, to its place for queries (0) or keys (1)
+  auto put_aside = [&](int kind) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
+    for (int i = 0; i < NS * 2 * W; ++i) {
+      float v = (&acc[0][0][0])[i];
+      for (int off = p.group; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+      (&acc[0][0][0])[i] = v;
+    }
+    if (sub == 0)
 #pragma unroll
-      for (int e = 0; e < W; ++e) s[i][e] = -s[i][e];  // the turn back
-    const int last = min(rows, (seg + 1) * p.seg_rows);
-    for (int r0 = seg * p.seg_rows; r0 < last; r0 += per) {
-      const int h = r0 + sub;
-      const bool live = h < last, isq = h < p.heads;
-      const int64_t hd = (int64_t)(isq ? h : h - p.heads) * p.dim;
-      const char* x = (isq ? p.q : p.k) + (t * (isq ? p.q_stride : p.k_stride) + hd) * E;
-      const char* dy = (isq ? p.dyq : p.dyk) + (t * (isq ? p.dyq_stride : p.dyk_stride) + hd) * E;
-      const char* w = isq ? p.qw : p.kw;
-      float a[NS][W], b[NS][W], ga[NS][W], gb[NS][W];
-      float ss = 0.f;
+      for (int i = 0; i < NS; ++i)
+        if (sl.on[i])
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-#pragma unroll
-        for (int e = 0; e < W; ++e) a[i][e] = b[i][e] = ga[i][e] = gb[i][e] = 0.f;
-        if (live && sl.on[i]) {
-          load<DT, W>(a[i], x + (int64_t)sl.ea[i] * E);
-          load<DT, W>(b[i], x + (int64_t)sl.eb[i] * E);
-          load<DT, W>(ga[i], dy + (int64_t)sl.ea[i] * E);
-          load<DT, W>(gb[i], dy + (int64_t)sl.eb[i] * E);
-        }
-#pragma unroll
-        for (int e = 0; e < W; ++e) ss += a[i][e] * a[i][e] + b[i][e] * b[i][e];
-      }
-      const float ms = group_sum(ss, p.group) * p.inv_dim;
-      const bool keep = pos >= 0 && ms <= 3.402823466e38f && ms + p.eps > 0.f;
-      const float r = keep ? rsqrtf(ms + p.eps) : 0.f;
-      float dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        turn<W>(ga[i], gb[i], c[i], s[i], p.interleaved);
-        float wa[W], wb[W];
-#pragma unroll
-        for (int e = 0; e < W; ++e) wa[e] = wb[e] = 1.f;
-        if (w && sl.on[i]) {
-          load_cached<DT, W>(wa, w + sl.ea[i] * E);
-          load_cached<DT, W>(wb, w + sl.eb[i] * E);
-        }
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          a[i][e] *= r, b[i][e] *= r;
-          const float da = ga[i][e] * a[i][e], db = gb[i][e] * b[i][e];
-          if (keep && live) {
-            if (isq)
-              acc[0][i][0][e] += da, acc[0][i][1][e] += db;
-            else
-              acc[1][i][0][e] += da, acc[1][i][1][e] += db;
+          for (int e = 0; e < W; ++e) {
+            part[(warp * 2 + kind) * p.dim + sl.ea[i] + e] = acc[i][0][e];
+            part[(warp * 2 + kind) * p.dim + sl.eb[i] + e] = acc[i][1][e];
           }
-          dot += da * wa[e] + db * wb[e];
-          ga[i][e] *= wa[e], gb[i][e] *= wb[e];
+#pragma unroll
+    for (int i = 0; i < NS * 2 * W; ++i) (&acc[0][0][0])[i] = 0.f;
+  };
+  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+  const int64_t units = p.tokens * (p.q_segs + p.k_segs);
+  int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+  bool queries = true;
+  Unit x = unit_of(p, u < units ? u : 0);
+  int pos = position_of(p, x.t);
+  while (u < units) {
+    const Unit now = x;
+    const int at = pos;
+    u += warps;
+    if (u < units) {
+      x = unit_of(p, u);
+      pos = position_of(p, x.t);
+    }
+    if (queries && !now.isq) {
+      if (p.ws) put_aside(0);
+      queries = false;
+    }
+    const char* in = (now.isq ? p.q + now.t * p.q_stride * E : p.k + now.t * p.k_stride * E);
+    const char* gin = (now.isq ? p.dyq + now.t * p.dyq_stride * E : p.dyk + now.t * p.dyk_stride * E);
+    char* out = (now.isq ? p.qo + now.t * p.qo_stride * E : p.ko + now.t * p.ko_stride * E);
+    const char* w = now.isq ? p.qw : p.kw;
+    count_bad(p, now, at);
+    float c[NS][W], s[NS][W];
+    for (int r0 = now.first; r0 < now.last; r0 += U * per) {
+      Raw<DT, W> rx[U][NS], rg[U][NS];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int h = r0 + k * per + sub;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          rx[k][i].a = rx[k][i].b = rg[k][i].a = rg[k][i].b = make_uint4(0, 0, 0, 0);
+          if (h < now.last && sl.on[i]) {
+            rx[k][i].load(in + (int64_t)h * p.dim * E, sl.ea[i], sl.eb[i]);
+            rg[k][i].load(gin + (int64_t)h * p.dim * E, sl.ea[i], sl.eb[i]);
+          }
         }
       }
-      const float mean = group_sum(dot, p.group) * p.inv_dim;
-      if (!live) continue;
-      char* dx = (isq ? p.qo : p.ko) + (t * (isq ? p.qo_stride : p.ko_stride) + hd) * E;
+      if (r0 == now.first) {
+        angles<W, NS>(c, s, sl, p, at);
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        if (!sl.on[i]) continue;
+        for (int i = 0; i < NS; ++i)
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-          a[i][e] = keep ? r * (ga[i][e] - a[i][e] * mean) : 0.f;
-          b[i][e] = keep ? r * (gb[i][e] - b[i][e] * mean) : 0.f;
+          for (int e = 0; e < W; ++e) s[i][e] = -s[i][e];  // the turn back
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int h = r0 + k * per + sub;
+        if (r0 + k * per >= now.last) break;
+        const bool live = h < now.last;
+        float a[NS][W], b[NS][W], ga[NS][W], gb[NS][W], ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          rx[k][i].get(a[i], b[i]);
+#pragma unroll
+          for (int e = 0; e < W; ++e) ss += a[i][e] * a[i][e] + b[i][e] * b[i][e];
         }
-        store<DT, W>(dx + (int64_t)sl.ea[i] * E, a[i]);
-        store<DT, W>(dx + (int64_t)sl.eb[i] * E, b[i]);
+        const float ms = group_sum(ss, p.group) * p.inv_dim;
+        const bool keep = at >= 0 && ms <= 3.402823466e38f && ms + p.eps > 0.f;
+        const float r = keep ? rsqrtf(ms + p.eps) : 0.f;
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          rg[k][i].get(ga[i], gb[i]);
+          turn<W>(ga[i], gb[i], c[i], s[i], p.interleaved);
+          float wa[W], wb[W];
+#pragma unroll
+          for (int e = 0; e < W; ++e) wa[e] = wb[e] = 1.f;
+          if (w && sl.on[i]) {
+            load_cached<DT, W>(wa, w + sl.ea[i] * E);
+            load_cached<DT, W>(wb, w + sl.eb[i] * E);
+          }
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            a[i][e] *= r, b[i][e] *= r;
+            const float da = ga[i][e] * a[i][e], db = gb[i][e] * b[i][e];
+            if (keep && live) acc[i][0][e] += da, acc[i][1][e] += db;
+            dot += da * wa[e] + db * wb[e];
+            ga[i][e] *= wa[e], gb[i][e] *= wb[e];
+          }
+        }
+        const float mean = group_sum(dot, p.group) * p.inv_dim;
+        if (!live) continue;
+        char* dx = out + (int64_t)h * p.dim * E;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          if (!sl.on[i]) continue;
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            a[i][e] = keep ? r * (ga[i][e] - a[i][e] * mean) : 0.f;
+            b[i][e] = keep ? r * (gb[i][e] - b[i][e] * mean) : 0.f;
+          }
+          store<DT, W>(dx + sl.ea[i] * E, a[i]);
+          store<DT, W>(dx + sl.eb[i] * E, b[i]);
+        }
       }
     }
   }
   if (p.ws == nullptr) return;
-  // the warp's row groups, then the block's warps, each in a fixed order
-#pragma unroll
-  for (int i = 0; i < 2 * NS * 2 * W; ++i) {
-    float v = (&acc[0][0][0][0])[i];
-    for (int off = p.group; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    (&acc[0][0][0][0])[i] = v;
-  }
-  if (sub == 0) {
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-      if (sl.on[i])
-#pragma unroll
-        for (int e = 0; e < W; ++e)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            part[(warp * 2 + k) * p.dim + sl.ea[i] + e] = acc[k][i][0][e];
-            part[(warp * 2 + k) * p.dim + sl.eb[i] + e] = acc[k][i][1][e];
-          }
-  }
+  put_aside(queries ? 0 : 1);
+  if (queries) put_aside(1);  // (no keys: zeros)
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * p.dim; i += kThreads) {
     float v = 0.f;
@@ -333,16 +416,15 @@ __global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const RopeParams p) 
 
 }  // namespace
 
+template <int DT, int W>
+static RopeKernels kernels_of(bool vec) {
+  return vec ? RopeKernels{(const void*)rope_fwd_kernel<DT, W, 1, kFwdU>,
+                           (const void*)rope_bwd_kernel<DT, W, 1, kBwdU>, kThreads}
+             : RopeKernels{(const void*)rope_fwd_kernel<DT, 1, 4, 1>,
+                           (const void*)rope_bwd_kernel<DT, 1, 4, 1>, kThreads};
+}
 RopeKernels rope_kernels(int dtype, bool vec) {
-  if (dtype == kF32)
-    return vec ? RopeKernels{(const void*)rope_fwd_kernel<kF32, 4, 1>,
-                             (const void*)rope_bwd_kernel<kF32, 4, 1>, kThreads}
-               : RopeKernels{(const void*)rope_fwd_kernel<kF32, 1, 4>,
-                             (const void*)rope_bwd_kernel<kF32, 1, 4>, kThreads};
-  return vec ? RopeKernels{(const void*)rope_fwd_kernel<kBF16, 8, 1>,
-                           (const void*)rope_bwd_kernel<kBF16, 8, 1>, kThreads}
-             : RopeKernels{(const void*)rope_fwd_kernel<kBF16, 1, 4>,
-                           (const void*)rope_bwd_kernel<kBF16, 1, 4>, kThreads};
+  return dtype == kF32 ? kernels_of<kF32, 4>(vec) : kernels_of<kBF16, 8>(vec);
 }
 
 }  // namespace rr

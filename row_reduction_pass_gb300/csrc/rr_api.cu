@@ -2418,13 +2418,19 @@ rr_status rope_plan(rr::RopeParams& p, rr_dtype dt, float eps, const int64_t* st
   p.inv_dim = 1.f / (float)p.dim;
   return RR_OK;
 }
-// Cuts each token's heads into units until `warps` have one.
+// Cuts each token's queries and keys into units until `warps` have one.
 void rope_units(rr::RopeParams& p, int64_t warps) {
-  const int rows = p.heads + p.kv_heads, per = 32 / p.group;
-  const int64_t its = cdiv(rows, per);
-  const int64_t segs = std::min(its, std::max<int64_t>(1, cdiv(warps, p.tokens)));
-  p.seg_rows = (int32_t)(cdiv(its, segs) * per);
-  p.segs = (int32_t)cdiv(rows, p.seg_rows);
+  const int per = 32 / p.group;
+  const int64_t want = std::max<int64_t>(1, cdiv(warps, p.tokens));  // units a token
+  auto cut = [&](int rows, int64_t segs, int32_t* n, int32_t* each) {
+    const int64_t its = cdiv(rows, per);
+    segs = std::max<int64_t>(1, std::min(its, segs));
+    *each = (int32_t)(cdiv(its, segs) * per);
+    *n = rows == 0 ? 0 : (int32_t)cdiv(rows, *each);
+  };
+  const int64_t all = p.heads + p.kv_heads;
+  cut(p.heads, cdiv(want * p.heads, all), &p.q_segs, &p.q_rows);
+  cut(p.kv_heads, cdiv(want * p.kv_heads, all), &p.k_segs, &p.k_rows);
 }
 
 constexpr int kRopeBwdBlocks = 2;  // a SM
@@ -2506,7 +2512,7 @@ rr_status rr_qk_norm_rope_fwd(const void* q, const void* k, const void* q_weight
     return st;
   const int wpb = pl.k.threads / 32;
   rope_units(p, (int64_t)pl.sms * 8 * wpb);
-  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * p.segs, wpb), (int64_t)pl.sms * 8);
+  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * (p.q_segs + p.k_segs), wpb), (int64_t)pl.sms * 8);
   void* args[] = {&p};
   cudaError_t e = cudaLaunchKernel(pl.k.fwd, dim3((unsigned)grid), dim3((unsigned)pl.k.threads),
                                    args, 0, stream);
@@ -2618,7 +2624,7 @@ rr_status rr_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void
   const int wpb = pl.k.threads / 32;
   const int64_t most = (int64_t)pl.sms * kRopeBwdBlocks;
   rope_units(p, most * wpb);
-  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * p.segs, wpb), most);
+  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * (p.q_segs + p.k_segs), wpb), most);
   void* args[] = {&p};
   cudaError_t e =
       cudaLaunchKernel(pl.k.bwd, dim3((unsigned)grid), dim3((unsigned)pl.k.threads), args,

@@ -333,7 +333,8 @@ struct RopeParams {
   int64_t positions_n;
   int32_t heads, kv_heads, dim, rot;
   int32_t group;              // lanes of a row, a power of two
-  int32_t segs, seg_rows;     // a token's rows are cut into segs units of seg_rows
+  int32_t q_segs, q_rows;     // a token's queries are cut into q_segs units of q_rows heads
+  int32_t k_segs, k_rows;     // and its keys (none: k_segs 0)
   int32_t interleaved;
   float eps, inv_dim;
 };
