@@ -3,6 +3,8 @@
 Each translation unit compiles in its own nvcc process, in parallel; the
 objects are linked into ``row_reduction_pass_gb300/librr.so`` with the CUDA
 runtime linked statically, so the library only needs the driver at run time.
+Beside it, ``_call.c`` becomes the extension module through which Python calls some of
+its entry points.
 """
 from __future__ import annotations
 
@@ -11,12 +13,15 @@ import glob
 import hashlib
 import os
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "librr.so")
+CALL = os.path.join(HERE, "_call.c")
+CALL_LIB = os.path.join(HERE, "_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -30,7 +35,7 @@ def _nvcc() -> str:
 
 def _digest() -> str:
     h = hashlib.sha256()
-    for f in sorted(glob.glob(os.path.join(CSRC, "*")) + [os.path.join(ROOT, "include", "rr.h")]):
+    for f in sorted(glob.glob(os.path.join(CSRC, "*")) + [CALL, os.path.join(ROOT, "include", "rr.h")]):
         with open(f, "rb") as fh:
             h.update(os.path.basename(f).encode())
             h.update(fh.read())
@@ -43,7 +48,7 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
     os.makedirs(BUILD, exist_ok=True)
     stamp = os.path.join(BUILD, "librr.stamp")
     dig = _digest()
-    if not force and os.path.exists(LIB) and os.path.exists(stamp):
+    if not force and os.path.exists(LIB) and os.path.exists(CALL_LIB) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == dig:
                 return LIB
@@ -68,6 +73,13 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = CALL_LIB + f".tmp{os.getpid()}"
+    r = subprocess.run([os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I",
+                        sysconfig.get_paths()["include"], "-o", tmp, CALL],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CALL}:\n{r.stderr}")
+    os.replace(tmp, CALL_LIB)
     with open(stamp, "w") as f:
         f.write(dig)
     return LIB

@@ -434,47 +434,37 @@ def rr_draft_verify(target_logits, draft_logits, tokens, uniform, race, out_toke
         _check(fn, st)
 
 
-def _rows(fn, *ts):
-    """Checks (name, tensor, dtype, shape) tuples of tensors whose rows (all but the first
-    dimension) are dense and may lie any distance apart; a None tensor passes.  Returns
-    their addresses and the elements from a row to the next."""
-    out, dev = [], _torch().cuda.current_device()
-    for name, t, dtype, shape in ts:
-        if t is None:
-            out += (None, 0)
-            continue
-        if t.dtype is not dtype:
-            raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-        if t.get_device() != dev:
-            raise ValueError(f"{fn}: {name} must be a CUDA tensor on the current device")
-        stride, width = t.stride(), 1
-        for n, s in zip(reversed(shape[1:]), reversed(stride[1:])):
-            if s != width and n > 1:
-                raise ValueError(f"{fn}: the rows of {name} must be dense")
-            width *= n
-        out += (t.data_ptr(), stride[0] if shape[0] > 1 else width)
-    return out
+_calls = None  # the extension module of the packed-sequence operators, at the first call
 
 
-def _workspace(need, device, stream):
+def _call():
+    global _calls
+    if _calls is None:
+        lib = load_library()
+        try:
+            from . import _call as module
+        except ImportError as e:
+            raise RuntimeError("the extension module _call is missing: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        torch = _torch()
+        names = ("rr_qk_norm_rope_fwd", "rr_qk_norm_rope_bwd", "rr_attention_packed_fwd",
+                 "rr_attention_packed_bwd", "rr_token_logprob_fwd", "rr_token_logprob_bwd")
+        module.setup(torch.float32, torch.bfloat16, torch.int32, torch.cuda.current_device,
+                     torch._C._cuda_getCurrentRawStream,
+                     tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+        _calls = module
+    return _calls
+
+
+def _scratch(need, device, stream):
     """Device scratch for a call whose caller gave none, of the stream that uses it."""
+    if need == 0:
+        return None
     torch = _torch()
     if stream is None:
         return torch.empty(need, dtype=torch.uint8, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(need, dtype=torch.uint8, device=device)
-
-
-def _given(fn, workspace, need, device, stream):
-    """(tensor that must live until the launch, address, bytes) of a call's workspace."""
-    if workspace is None:
-        if need == 0:
-            return None, None, 0
-        workspace = _workspace(need, device, stream)
-    (address,) = _args(fn, ("workspace", workspace, None, workspace.shape))
-    return workspace, address, workspace.numel() * workspace.element_size()
 
 
 def rr_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps=1e-6,
@@ -486,24 +476,11 @@ def rr_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_
 
     q, k, q_out and k_out may be views whose tokens lie apart (a fused projection's), and
     q_out, k_out may be q, k.  The weights may be None (1); k and k_out may be None."""
-    torch = _torch()
-    fn = "rr_qk_norm_rope_fwd"
-    t, h, d = q.shape
-    kv = 0 if k is None else k.shape[1]
-    dt, i32, f32 = q.dtype, torch.int32, torch.float32
-    n, half = cos.shape
-    a, sa, b, sb, oa, soa, ob, sob = _rows(
-        fn, ("q", q, dt, (t, h, d)), ("k", k, dt, (t, kv, d)), ("q_out", q_out, dt, (t, h, d)),
-        ("k_out", k_out, dt, (t, kv, d)))
-    wq, wk, pc, ps, pp, bad = _args(
-        fn, ("q_weight", q_weight, dt, (d,)), ("k_weight", k_weight, dt, (d,)),
-        ("cos", cos, f32, (n, half)), ("sin", sin, f32, (n, half)),
-        ("positions", positions, i32, (t,)), ("bad_position_count", bad_position_count, i32, (1,)))
-    st = load_library().rr_qk_norm_rope_fwd(
-        a, b, wq, wk, pc, ps, pp, oa, ob, t, h, kv, d, 2 * half, n, sa, sb, soa, sob, eps,
-        1 if interleaved else 0, bad, _dtype(q), _raw_stream(stream))
+    st = (_calls or _call()).rope_fwd(
+        q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, eps, interleaved,
+        bad_position_count, None if stream is None else stream.cuda_stream)
     if st != 0:
-        _check(fn, st)
+        _check("rr_qk_norm_rope_fwd", st)
 
 
 def rr_qk_norm_rope_bwd_workspace_size(tokens: int, heads: int, kv_heads: int,
@@ -520,32 +497,17 @@ def rr_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, posi
 
     ``workspace`` is a uint8 CUDA tensor of at least
     ``rr_qk_norm_rope_bwd_workspace_size`` bytes; it is allocated here if omitted."""
-    torch = _torch()
-    fn = "rr_qk_norm_rope_bwd"
-    lib = load_library()
-    t, h, d = q.shape
-    kv = 0 if k is None else k.shape[1]
-    dt, i32, f32 = q.dtype, torch.int32, torch.float32
-    n, half = cos.shape
-    ga, sga, gb, sgb, a, sa, b, sb, oa, soa, ob, sob = _rows(
-        fn, ("dq_out", dq_out, dt, (t, h, d)), ("dk_out", dk_out, dt, (t, kv, d)),
-        ("q", q, dt, (t, h, d)), ("k", k, dt, (t, kv, d)), ("dq", dq, dt, (t, h, d)),
-        ("dk", dk, dt, (t, kv, d)))
-    wq, wk, pc, ps, pp, dwq, dwk, bad = _args(
-        fn, ("q_weight", q_weight, dt, (d,)), ("k_weight", k_weight, dt, (d,)),
-        ("cos", cos, f32, (n, half)), ("sin", sin, f32, (n, half)),
-        ("positions", positions, i32, (t,)), ("dq_weight", dq_weight, dt, (d,)),
-        ("dk_weight", dk_weight, dt, (d,)), ("bad_position_count", bad_position_count, i32, (1,)))
-    need = 0
-    if dq_weight is not None and workspace is None:
-        need = lib.rr_qk_norm_rope_bwd_workspace_size(t, h, kv, d)
-    workspace, pw, size = _given(fn, workspace, need, q.device, stream)
-    st = lib.rr_qk_norm_rope_bwd(
-        ga, gb, a, b, wq, wk, pc, ps, pp, oa, ob, dwq, dwk, pw, size, t, h, kv, d, 2 * half, n,
-        sga, sgb, sa, sb, soa, sob, eps, 1 if interleaved else 0, bad, _dtype(q),
-        _raw_stream(stream))
+    call = _calls or _call()
+    if workspace is None and dq_weight is not None:
+        t, h, d = q.shape
+        workspace = _scratch(rr_qk_norm_rope_bwd_workspace_size(
+            t, h, 0 if k is None else k.shape[1], d), q.device, stream)
+    st = call.rope_bwd(
+        dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, positions, dq, dk, dq_weight,
+        dk_weight, eps, interleaved, workspace, bad_position_count,
+        None if stream is None else stream.cuda_stream)
     if st != 0:
-        _check(fn, st)
+        _check("rr_qk_norm_rope_bwd", st)
 
 
 def rr_attention_packed_fwd(q, k, v, cu_seqlens, o, lse=None, scale=None, stream=None):
@@ -554,23 +516,11 @@ def rr_attention_packed_fwd(q, k, v, cu_seqlens, o, lse=None, scale=None, stream
     sequence b the tokens cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [batch + 1] on the
     device).  lse (fp32 [heads, tokens]) is optional; scale defaults to 1 / sqrt(head_dim).
     Rows outside every sequence are left as they were."""
-    torch = _torch()
-    fn = "rr_attention_packed_fwd"
-    t, h, d = q.shape
-    kv = k.shape[1]
-    dt = q.dtype
-    a, sa, b, sb, c, sc, po, so = _rows(
-        fn, ("q", q, dt, (t, h, d)), ("k", k, dt, (t, kv, d)), ("v", v, dt, (t, kv, d)),
-        ("o", o, dt, (t, h, d)))
-    cu, pl = _args(fn, ("cu_seqlens", cu_seqlens, torch.int32, (cu_seqlens.shape[0],)),
-                   ("lse", lse, torch.float32, (h, t)))
-    if scale is None:
-        scale = 1.0 / float(d) ** 0.5
-    st = load_library().rr_attention_packed_fwd(
-        a, b, c, cu, po, pl, t, cu_seqlens.shape[0] - 1, h, kv, d, sa, sb, sc, so, scale,
-        _dtype(q), _raw_stream(stream))
+    st = (_calls or _call()).attn_fwd(
+        q, k, v, cu_seqlens, o, lse, float(q.shape[-1]) ** -0.5 if scale is None else scale,
+        None if stream is None else stream.cuda_stream)
     if st != 0:
-        _check(fn, st)
+        _check("rr_attention_packed_fwd", st)
 
 
 def rr_attention_packed_bwd_workspace_size(tokens: int, heads: int) -> int:
@@ -584,26 +534,15 @@ def rr_attention_packed_bwd(dout, q, k, v, o, lse, cu_seqlens, dq, dk, dv, scale
 
     ``workspace`` is a uint8 CUDA tensor of at least
     ``rr_attention_packed_bwd_workspace_size`` bytes; it is allocated here if omitted."""
-    torch = _torch()
-    fn = "rr_attention_packed_bwd"
-    lib = load_library()
-    t, h, d = q.shape
-    kv = k.shape[1]
-    dt, qs, ks = q.dtype, (t, h, d), (t, kv, d)
-    pg, sg, a, sa, b, sb, c, sc, po, so, pdq, sdq, pdk, sdk, pdv, sdv = _rows(
-        fn, ("dout", dout, dt, qs), ("q", q, dt, qs), ("k", k, dt, ks), ("v", v, dt, ks),
-        ("o", o, dt, qs), ("dq", dq, dt, qs), ("dk", dk, dt, ks), ("dv", dv, dt, ks))
-    cu, pl = _args(fn, ("cu_seqlens", cu_seqlens, torch.int32, (cu_seqlens.shape[0],)),
-                   ("lse", lse, torch.float32, (h, t)))
-    need = 0 if workspace is not None else lib.rr_attention_packed_bwd_workspace_size(t, h)
-    workspace, pw, size = _given(fn, workspace, need, q.device, stream)
-    if scale is None:
-        scale = 1.0 / float(d) ** 0.5
-    st = lib.rr_attention_packed_bwd(
-        pg, a, b, c, po, pl, cu, pdq, pdk, pdv, pw, size, t, cu_seqlens.shape[0] - 1, h, kv, d,
-        sg, sa, sb, sc, so, sdq, sdk, sdv, scale, _dtype(q), _raw_stream(stream))
+    call = _calls or _call()
+    if workspace is None:
+        workspace = _scratch(rr_attention_packed_bwd_workspace_size(*q.shape[:2]), q.device, stream)
+    st = call.attn_bwd(
+        dout, q, k, v, o, lse, cu_seqlens, dq, dk, dv,
+        float(q.shape[-1]) ** -0.5 if scale is None else scale, workspace,
+        None if stream is None else stream.cuda_stream)
     if st != 0:
-        _check(fn, st)
+        _check("rr_attention_packed_bwd", st)
 
 
 def rr_token_logprob_fwd(logits, tokens, logprob, entropy=None, row_max=None, log_sum=None,
@@ -614,46 +553,22 @@ def rr_token_logprob_fwd(logits, tokens, logprob, entropy=None, row_max=None, lo
     :func:`rr_token_logprob_bwd`), the token's rank (int32) and the row's k largest columns
     with their log probabilities (top_index int32, top_logprob fp32, [rows, k]; a tie goes
     to the lower column).  logits [rows, cols] may be a view whose rows lie apart."""
-    torch = _torch()
-    fn = "rr_token_logprob_fwd"
-    rows, cols = logits.shape
-    i32, f32 = torch.int32, torch.float32
-    if (top_index is None) != (top_logprob is None):
-        raise ValueError(f"{fn}: top_index and top_logprob: both, or neither")
-    k = 0 if top_index is None else top_index.shape[1]
-    x, sx = _rows(fn, ("logits", logits, logits.dtype, (rows, cols)))
-    t, lp, en, rm, ls, rk, ti, tl, bad = _args(
-        fn, ("tokens", tokens, i32, (rows,)), ("logprob", logprob, f32, (rows,)),
-        ("entropy", entropy, f32, (rows,)), ("row_max", row_max, f32, (rows,)),
-        ("log_sum", log_sum, f32, (rows,)), ("rank", rank, i32, (rows,)),
-        ("top_index", top_index, i32, (rows, k)), ("top_logprob", top_logprob, f32, (rows, k)),
-        ("bad_token_count", bad_token_count, i32, (1,)))
-    st = load_library().rr_token_logprob_fwd(x, t, lp, en, rm, ls, rk, ti, tl, rows, cols, sx, k,
-                                             temperature, ignore_index, bad, _dtype(logits),
-                                             _raw_stream(stream))
+    st = (_calls or _call()).logprob_fwd(
+        logits, tokens, logprob, entropy, row_max, log_sum, rank, top_index, top_logprob,
+        temperature, ignore_index, bad_token_count, None if stream is None else stream.cuda_stream)
     if st != 0:
-        _check(fn, st)
+        _check("rr_token_logprob_fwd", st)
 
 
 def rr_token_logprob_bwd(logits, tokens, row_max, log_sum, grad_logprob, dlogits, entropy=None,
                          grad_entropy=None, temperature=1.0, ignore_index=-100, stream=None):
     """Gradient of :func:`rr_token_logprob_fwd`'s logprob and (grad_entropy, with the
     forward's entropy) entropy; dlogits may be logits.  grad_logprob may be None (0)."""
-    torch = _torch()
-    fn = "rr_token_logprob_bwd"
-    rows, cols = logits.shape
-    f32 = torch.float32
-    x, sx, y, sy = _rows(fn, ("logits", logits, logits.dtype, (rows, cols)),
-                         ("dlogits", dlogits, logits.dtype, (rows, cols)))
-    t, rm, ls, en, g, h = _args(
-        fn, ("tokens", tokens, torch.int32, (rows,)), ("row_max", row_max, f32, (rows,)),
-        ("log_sum", log_sum, f32, (rows,)), ("entropy", entropy, f32, (rows,)),
-        ("grad_logprob", grad_logprob, f32, (rows,)), ("grad_entropy", grad_entropy, f32, (rows,)))
-    st = load_library().rr_token_logprob_bwd(x, t, rm, ls, en, g, h, y, rows, cols, sx, sy,
-                                             temperature, ignore_index, _dtype(logits),
-                                             _raw_stream(stream))
+    st = (_calls or _call()).logprob_bwd(
+        logits, tokens, row_max, log_sum, grad_logprob, dlogits, entropy, grad_entropy,
+        temperature, ignore_index, None if stream is None else stream.cuda_stream)
     if st != 0:
-        _check(fn, st)
+        _check("rr_token_logprob_bwd", st)
 
 
 def rr_read_device_error(device: int = 0, reset: bool = True) -> int:
