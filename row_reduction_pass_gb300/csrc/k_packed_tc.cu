@@ -1,28 +1,24 @@
 // k_packed_tc.cu -- causal attention over packed sequences with grouped heads on the
 // 5th-generation tensor cores (bf16, head dimension 64 or 128).
 //
-// Forward.  A block, one per SM, works on two tiles of 128 query rows at once that attend
-// to the same keys (halves 0 and 1): two heads of a key head's group over the same tokens,
-// or, where the group is odd, two neighbouring tiles of one head.  Key and value tiles of
-// 128 tokens are loaded once for both and used as two sub-tiles of 64.  Per half and
-// sub-tile: S = Q K^T into one of two TMEM buffers, a softmax warpgroup of four warps (thread
-// t owns row t, TMEM lane t) turns it into bf16 weights in TMEM with the running maximum and
-// sum of the online softmax, O += P V.  S of the next sub-tile is there when a softmax ends
-// (with one buffer of 128 keys each step was S, softmax and O += P V one after the other, and
-// both halves in step: 5080 cycles a tile of 128 keys, of which the products need 2200).
-//   head_dim 128: a half's 256 TMEM columns are S (2 x 64), which P overwrites, and O (128);
-//     S of u + 2 follows O += P V of u.
-//   head_dim 64: S (2 x 64), P (2 x 32) and O (64); S of u + 2 as soon as S of u is read.
-// A product alone takes 85 to 130 cycles for 128 x 128 x 16, two that do not depend on each
-// other 66 each: the halves' products have an issuing warp each.
-// Roles: warps 0-3 and 4-7 the halves' softmax, warp 8 loads (TMA), warps 9 and 10 issue the
-// halves' products.
+// Forward.  A block, one per SM, works on one tile of 128 query rows of a head at a time:
+// S = Q K^T of a key tile into one of three TMEM buffers, eight softmax warps (two threads a
+// row, 64 keys each, which trade their maxima) turn it into bf16 weights in the same buffer
+// with the running maximum and sum of the online softmax, O += P V.  With S two tiles ahead
+// the softmax always finds its next tile, and the tensor cores have two products that do not
+// depend on each other: a product of 128 x 128 x 16 takes 85 to 130 cycles alone and 66 beside
+// another.  16000 tokens, 32 heads on 8, head_dim 128, one sequence: 256 us, 1370 TFLOP/s.  (Two
+// tiles of 128 rows a block, which share the loaded keys but leave TMEM for one S each, took
+// 384 us, S, softmax and O += P V one after the other; with their scores in two buffers of 64
+// keys 344 us: an S of 64 keys takes as long as one of 128.)
+//   TMEM: S (3 x 128 columns, P over the first half of each half) and O (D columns).
+// Roles: warps 0-7 softmax (two to a quarter of the lanes), warp 8 loads Q and K (TMA), warp 11
+// loads V, warps 9 and 10 issue S and O += P V.
 //
-// Work.  An item is a level of a sequence (a tile of 128 queries, or two where the group is
-// odd) with one pair of a key head; its cost is the level.  Sequence lengths are known on the
-// device only, so each block sorts the (at most 128) sequences by their length and finds its
-// items in the list of all levels, longest first, that the blocks are dealt in a zigzag.
-// More sequences are taken in their own order.
+// Work.  An item is a level of a sequence (a tile of 128 queries) with one head; its cost is the
+// level.  Sequence lengths are known on the device only, so each block sorts the (at most 128)
+// sequences by their length and finds its items in the list of all levels, longest first, that
+// the blocks are dealt in a zigzag.  More sequences are taken in their own order.
 //
 // A tile's rows beyond its sequence (the next one's, or past the buffer, which read as zero)
 // are not stored, and keys beyond a row's own are masked in S.  Their V has weight 0, which a
@@ -40,7 +36,6 @@ namespace {
 
 constexpr int kTile = 128;           // query rows and keys of a tile
 constexpr int kBox = kTile * 128;    // bytes of 128 rows x 64 columns
-constexpr int kSub = 64;             // keys of a sub-tile (forward)
 constexpr int kSorted = 128;         // sequences that a block sorts
 
 // TMA box [128 tokens x 1 head x 64 columns] at {column, head, token}.
@@ -166,17 +161,16 @@ struct Sequences {
 template <int D>
 struct Fwd {
   static constexpr int kBoxes = D / 64;
-  static constexpr int kTileBytes = kBoxes * kBox;
-  static constexpr int kOffK = 2 * kTileBytes, kOffV = 4 * kTileBytes;
-  static constexpr int kOffStage = 6 * kTileBytes;       // 8 warps' output boxes
+  static constexpr int kTileBytes = kBoxes * kBox;       // Q, then two stages of K and of V
+  static constexpr int kOffK = kTileBytes, kOffV = 3 * kTileBytes;
+  static constexpr int kOffStage = 5 * kTileBytes;       // 8 warps' output boxes
   static constexpr int kStage = 32 * 128;
-  static constexpr int kOffBar = kOffStage + 8 * kStage;
+  static constexpr int kOffTrade = kOffStage + 8 * kStage;  // [2][half][128] floats
+  static constexpr int kOffBar = kOffTrade + 2048;
   static constexpr int kOffSeq = kOffBar + 256;
   static constexpr int kSmem = kOffSeq + kSorted * 8 + 1024;
-  // columns of a half: S buffer b at 64 b, P buffer b at kColP0 + kStepP b, O
-  static constexpr uint32_t kColP0 = D == 128 ? 0 : 128, kStepP = D == 128 ? 64 : 32;
-  static constexpr uint32_t kColO = 256 - D;
-  static constexpr uint32_t kIdescS = attn_idesc(kTile, kSub, false);
+  static constexpr uint32_t kColO = 384;
+  static constexpr uint32_t kIdescS = attn_idesc(kTile, kTile, false);
   static constexpr uint32_t kIdescO = attn_idesc(kTile, D, true);
 };
 
@@ -262,48 +256,38 @@ __device__ __noinline__ void repair_row(const PackedParams& p, int64_t begin, in
   for (int i = 0; i < D / 32; ++i) st_elem<kBF16>(o + 2 * (lane + 32 * i), acc[i] / l);
 }
 
-// A half's query tile of an item: its first row in the sequence, head, key tiles (0: none) and
-// sub-tiles.
-struct Half {
-  int row0, head, tiles, subs;
-};
-__device__ __forceinline__ Half half_of(const Item& it, int h, int group, bool even) {
-  Half x;
-  const int pairs = even ? group / 2 : group;
-  const int kv = it.part / pairs, pair = it.part - kv * pairs;
-  const int tile = even ? it.level : 2 * it.level + h;
-  x.head = kv * group + (even ? 2 * pair + h : pair);
-  x.row0 = tile * kTile;
-  x.tiles = it.ok && x.row0 < it.len ? tile + 1 : 0;
-  x.subs = x.tiles ? (min(it.len, x.row0 + kTile) + kSub - 1) / kSub : 0;
-  return x;
-}
-
+// D (+)= A B^T of two tiles in shared memory, A [128 x D], B [128 x D].
 template <int D>
-__global__ void __launch_bounds__(352, 1)
+__device__ __forceinline__ void issue_tiles(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = (uint32_t)((kk >> 2) * kBox + (kk & 3) * 32);
+    mma_ss(d, sw128_desc(a + off, 16, 1024), sw128_desc(b + off, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+  }
+}
+template <int D>
+__global__ void __launch_bounds__(384, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
                       const PackedParams p) {
   using C = Fwd<D>;
+  constexpr int T = C::kTileBytes;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int group = p.heads / p.kv_heads;
-  const bool even = group % 2 == 0;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* bar_q = bars;           // [half] Q landed
-  uint64_t* bar_qfree = bars + 2;   // [half] the item's last S done
-  uint64_t* bar_ofree = bars + 4;   // [half] O read, 128 arrivals
-  uint64_t* bar_kfull = bars + 6;   // [stage]
-  uint64_t* bar_vfull = bars + 8;
-  uint64_t* bar_kempty = bars + 10; // [stage] both halves' S done
-  uint64_t* bar_vempty = bars + 12; // [stage] both halves' O += P V done
-  uint64_t* bar_s = bars + 14;      // [half][buffer] S done
-  uint64_t* bar_o = bars + 18;      // [half][buffer] O += P V done
-  uint64_t* bar_sfree = bars + 22;  // [half][buffer] S read (head_dim 64), 128 arrivals
-  uint64_t* bar_p = bars + 26;      // [half][buffer] P written, 128 arrivals
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 30);
+  uint64_t* bar_q = bars;           // Q landed
+  uint64_t* bar_qfree = bars + 1;   // the item's last S done
+  uint64_t* bar_ofree = bars + 2;   // O read, 256 arrivals
+  uint64_t* bar_kfull = bars + 3;   // [stage]
+  uint64_t* bar_vfull = bars + 5;
+  uint64_t* bar_kempty = bars + 7;
+  uint64_t* bar_vempty = bars + 9;
+  uint64_t* bar_s = bars + 11;      // [buffer] S done
+  uint64_t* bar_o = bars + 14;      // [buffer] O += P V done
+  uint64_t* bar_p = bars + 17;      // [buffer] P written, 256 arrivals
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 20);
 
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -313,192 +297,158 @@ __global__ void __launch_bounds__(352, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 32 * 8) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar_q[i], 1);
-      mbar_init(&bar_qfree[i], 1);
-      mbar_init(&bar_ofree[i], 128);
-      mbar_init(&bar_kfull[i], 1);
-      mbar_init(&bar_vfull[i], 1);
-      mbar_init(&bar_kempty[i], 2);
-      mbar_init(&bar_vempty[i], 2);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&bar_s[i], 1);
-      mbar_init(&bar_o[i], 1);
-      mbar_init(&bar_sfree[i], 128);
-      mbar_init(&bar_p[i], 128);
-    }
+    for (int i = 0; i < 17; ++i) mbar_init(bars + i, i == 2 ? 256 : 1);
+    for (int i = 17; i < 20; ++i) mbar_init(bars + i, 256);
     fence_mbar_init();
   }
   Sequences list;
   list.init(reinterpret_cast<int2*>(smem + C::kOffSeq), reinterpret_cast<int2*>(smem + C::kOffStage),
-            p, even ? kTile : 2 * kTile, (even ? group / 2 : group) * p.kv_heads);
+            p, kTile, p.heads);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
+  const int group = p.heads / p.kv_heads;
   bool dead = false, more;
+  int b = 0;        // the tile's S buffer
+  uint32_t ph = 0;  // and how often all have been used (parity)
+  auto next_buffer = [&]() {
+    if (++b == 3) b = 0, ph ^= 1;
+  };
 
   // A role whose wait gave up asks for nothing more, and what it has asked for ends before
   // the block does.
-  if (warp == 8) {
-    // ------------------------------------------------------------ loads
-    int nk = 0, nv = 0, qn[2] = {0, 0};
+  if (warp == 8 || warp == 11) {
+    // --------------------------------------------------- loads: Q and K, or V
+    const bool keys = warp == 8;
+    const CUtensorMap* map = keys ? &tk : &tv;
+    uint64_t *full = keys ? bar_kfull : bar_vfull, *empty = keys ? bar_kempty : bar_vempty;
+    unsigned char* stages = smem + (keys ? C::kOffK : C::kOffV);
+    int n = 0, items = 0;
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
       if (!it.ok || lane != 0) continue;
-      const int kv = it.part / (even ? group / 2 : group);
-      int n = 0;
-      for (int h = 0; h < 2; ++h) {
-        const Half x = half_of(it, h, group, even);
-        if (x.tiles == 0) continue;
-        n = max(n, x.tiles);
-        if (qn[h] > 0) wait_spin(&bar_qfree[h], (uint32_t)((qn[h] - 1) & 1), dead, p.err);
-        if (dead) break;
-        ++qn[h];
-        mbar_arrive_expect_tx(&bar_q[h], C::kTileBytes);
-        for (int b = 0; b < C::kBoxes; ++b)
-          load_box(smem + h * C::kTileBytes + b * kBox, &tq, 64 * b, x.head, it.beg + x.row0,
-                   &bar_q[h]);
+      const int h = it.part;
+      if (keys) {
+        if (items > 0) wait_spin(bar_qfree, (uint32_t)((items - 1) & 1), dead, p.err);
+        if (!dead) {
+          ++items;
+          mbar_arrive_expect_tx(bar_q, T);
+          for (int x = 0; x < C::kBoxes; ++x)
+            load_box(smem + x * kBox, &tq, 64 * x, h, it.beg + it.level * kTile, bar_q);
+        }
       }
-      for (int t = 0; t < n; ++t) {
-        const int s = nk & 1;
-        const uint32_t ph = (uint32_t)(((nk >> 1) - 1) & 1);
-        if (nk >= 2) wait_spin(&bar_kempty[s], ph, dead, p.err);
+      for (int t = 0; t <= it.level; ++t) {
+        const int s = n & 1;
+        if (n >= 2) wait_spin(&empty[s], (uint32_t)(((n >> 1) - 1) & 1), dead, p.err);
         if (dead) break;
-        ++nk;
-        mbar_arrive_expect_tx(&bar_kfull[s], C::kTileBytes);
-        for (int b = 0; b < C::kBoxes; ++b)
-          load_box(smem + C::kOffK + s * C::kTileBytes + b * kBox, &tk, 64 * b, kv,
-                   it.beg + t * kTile, &bar_kfull[s]);
-        if (nv >= 2) wait_spin(&bar_vempty[s], ph, dead, p.err);
-        if (dead) break;
-        ++nv;
-        mbar_arrive_expect_tx(&bar_vfull[s], C::kTileBytes);
-        for (int b = 0; b < C::kBoxes; ++b)
-          load_box(smem + C::kOffV + s * C::kTileBytes + b * kBox, &tv, 64 * b, kv,
-                   it.beg + t * kTile, &bar_vfull[s]);
+        ++n;
+        mbar_arrive_expect_tx(&full[s], T);
+        for (int x = 0; x < C::kBoxes; ++x)
+          load_box(stages + s * T + x * kBox, map, 64 * x, h / group, it.beg + t * kTile, &full[s]);
       }
     }
-    for (int n = max(nk - 2, 0); n < nk; ++n)
-      mbar_wait_bounded(&bar_kfull[n & 1], (uint32_t)((n >> 1) & 1), p.err);
-    for (int n = max(nv - 2, 0); n < nv; ++n)
-      mbar_wait_bounded(&bar_vfull[n & 1], (uint32_t)((n >> 1) & 1), p.err);
-    for (int h = 0; h < 2; ++h)
-      if (qn[h] > 0) mbar_wait_bounded(&bar_q[h], (uint32_t)((qn[h] - 1) & 1), p.err);
-  } else if (warp >= 9) {
-    // --------------------------------------------------- a half's products
-    const int h = warp - 9;
-    const uint32_t tm = tmem + 256u * h;
-    const uint32_t q_addr = smem_addr(smem + h * C::kTileBytes);
-    int kc = 0, ns = 0, no = 0, items = 0;  // key tiles loaded, products issued, items
-    bar_s += 2 * h, bar_o += 2 * h, bar_sfree += 2 * h, bar_p += 2 * h;
-    auto stage = [&](int t) { return (kc + t) & 1; };
-    auto phase = [&](int t) { return (uint32_t)(((kc + t) >> 1) & 1); };
-    auto issue_s = [&](int u, int subs) {  // of sub-tile u
-      const int st = stage(u >> 1), b = ns & 1;
-      wait_spin(&bar_kfull[st], phase(u >> 1), dead, p.err);
-      if (ns >= 2)  // what is in its buffer has been used
-        wait_spin(D == 128 ? &bar_o[b] : &bar_sfree[b], (uint32_t)(((ns >> 1) - 1) & 1), dead, p.err);
-      if (dead) return;
-      tc_fence_after();
-      const uint32_t k_addr = smem_addr(smem + C::kOffK + st * C::kTileBytes) + (u & 1) * kSub * 128;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (uint32_t)((kk >> 2) * kBox + (kk & 3) * 32);
-        mma_ss(tm + 64 * b, sw128_desc(q_addr + off, 16, 1024),
-               sw128_desc(k_addr + off, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u);
-      }
-      ++ns;
-      mma_commit(&bar_s[b]);
-      if ((u & 1) || u == subs - 1) mma_commit(&bar_kempty[st]);
-      if (u == subs - 1) mma_commit(&bar_qfree[h]);
-    };
-    auto issue_pv = [&](int u, int subs) {
-      const int st = stage(u >> 1), b = no & 1;
-      wait_spin(&bar_p[b], (uint32_t)((no >> 1) & 1), dead, p.err);
-      if (u == 0 && items > 0) wait_spin(&bar_ofree[h], (uint32_t)((items - 1) & 1), dead, p.err);
-      wait_spin(&bar_vfull[st], phase(u >> 1), dead, p.err);
-      if (dead) return;
-      tc_fence_after();
-      const uint32_t v_addr = smem_addr(smem + C::kOffV + st * C::kTileBytes) + (u & 1) * kSub * 128;
-#pragma unroll
-      for (int kk = 0; kk < kSub / 16; ++kk)
-        mma_ts(tm + C::kColO, tm + C::kColP0 + C::kStepP * b + 8 * kk,
-               sw128_desc(v_addr + kk * 2048, kBox, 1024), C::kIdescO, (u > 0 || kk > 0) ? 1u : 0u);
-      ++no;
-      mma_commit(&bar_o[b]);
-      if ((u & 1) || u == subs - 1) mma_commit(&bar_vempty[st]);
-    };
+    for (int i = max(n - 2, 0); i < n; ++i)
+      mbar_wait_bounded(&full[i & 1], (uint32_t)((i >> 1) & 1), p.err);
+    if (items > 0) mbar_wait_bounded(bar_q, (uint32_t)((items - 1) & 1), p.err);
+  } else if (warp == 9) {
+    // ----------------------------------------------------------- S = Q K^T
+    int n = 0, items = 0;
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
-      if (!it.ok) continue;
-      const Half x = half_of(it, h, group, even);
-      const int n = max(x.tiles, half_of(it, 1 - h, group, even).tiles);
-      if (lane == 0) {
-        if (x.subs > 0) {
-          wait_spin(&bar_q[h], (uint32_t)(items & 1), dead, p.err);
-          issue_s(0, x.subs);
-          if (x.subs > 1) issue_s(1, x.subs);
-        }
-        for (int u = 0; u < x.subs && !dead; ++u) {
-          if (D == 64 && u + 2 < x.subs) issue_s(u + 2, x.subs);
-          issue_pv(u, x.subs);
-          if (D == 128 && u + 2 < x.subs) issue_s(u + 2, x.subs);
-        }
-        // the other half's tiles: a stage is given back once it has landed, so that its
-        // barrier's phases keep their order
-        for (int t = x.tiles; t < n && !dead; ++t) {
-          wait_spin(&bar_kfull[stage(t)], phase(t), dead, p.err);
-          if (!dead) mbar_arrive(&bar_kempty[stage(t)]);
-          wait_spin(&bar_vfull[stage(t)], phase(t), dead, p.err);
-          if (!dead) mbar_arrive(&bar_vempty[stage(t)]);
-        }
+      if (!it.ok || lane != 0) continue;
+      wait_spin(bar_q, (uint32_t)(items++ & 1), dead, p.err);
+      for (int t = 0; t <= it.level; ++t) {
+        const int s = n & 1;
+        wait_spin(&bar_kfull[s], (uint32_t)((n >> 1) & 1), dead, p.err);
+        // O += P V of three tiles ago is done with the buffer
+        if (n >= 3) wait_spin(&bar_o[b], ph ^ 1, dead, p.err);
+        if (dead) break;
+        tc_fence_after();
+        issue_tiles<D>(tmem + 128 * b, smem_addr(smem), smem_addr(smem + C::kOffK + s * T),
+                       C::kIdescS);
+        mma_commit(&bar_s[b]);
+        mma_commit(&bar_kempty[s]);
+        if (t == it.level) mma_commit(bar_qfree);
+        ++n;
+        next_buffer();
       }
-      kc += n;
-      items += x.subs > 0;
     }
-    if (ns > 0) mbar_wait_bounded(&bar_s[(ns - 1) & 1], (uint32_t)(((ns - 1) >> 1) & 1), p.err);
-    if (no > 0) mbar_wait_bounded(&bar_o[(no - 1) & 1], (uint32_t)(((no - 1) >> 1) & 1), p.err);
+    if (n > 0) {  // (the last one's buffer, and its parity)
+      const int last = b == 0 ? 2 : b - 1;
+      mbar_wait_bounded(&bar_s[last], b == 0 ? ph ^ 1 : ph, p.err);
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ O += P V
+    int n = 0, items = 0;
+    for (int r = 0;; ++r) {
+      const Item it = list.get(r, more);
+      if (!more) break;
+      if (!it.ok || lane != 0) continue;
+      for (int t = 0; t <= it.level; ++t) {
+        const int s = n & 1;
+        wait_spin(&bar_vfull[s], (uint32_t)((n >> 1) & 1), dead, p.err);
+        if (t == 0 && items > 0) wait_spin(bar_ofree, (uint32_t)((items - 1) & 1), dead, p.err);
+        wait_spin(&bar_p[b], ph, dead, p.err);
+        if (dead) break;
+        tc_fence_after();
+        const uint32_t v_addr = smem_addr(smem + C::kOffV + s * T);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_ts(tmem + C::kColO, tmem + 128 * b + 8 * kk + (kk >= 4 ? 32 : 0),
+                 sw128_desc(v_addr + kk * 2048, kBox, 1024), C::kIdescO,
+                 (t > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(&bar_o[b]);
+        mma_commit(&bar_vempty[s]);
+        ++n;
+        next_buffer();
+      }
+      ++items;
+    }
+    if (n > 0) {
+      const int last = b == 0 ? 2 : b - 1;
+      mbar_wait_bounded(&bar_o[last], b == 0 ? ph ^ 1 : ph, p.err);
+    }
   } else {
-    // ------------------------------------------------- a half's softmax
-    const int h = warp >> 2, row = tid & 127;
+    // ------------------------------------------------------------ softmax
+    const int row = tid & 127, half = warp >> 2, col0 = 64 * half;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tm = tmem + 256u * h + lanes, tO = tm + C::kColO;
+    const uint32_t tS = tmem + lanes + col0, tO = tmem + lanes + C::kColO;
     const float sc = p.scale_log2;
     unsigned char* box = smem + C::kOffStage + warp * C::kStage;
-    int n = 0;  // sub-tiles
-    bar_s += 2 * h, bar_o += 2 * h, bar_sfree += 2 * h, bar_p += 2 * h;
+    float* trade = reinterpret_cast<float*>(smem + C::kOffTrade);
+    int swaps = 0;
+    // gives `x` to the row's other thread and takes its value
+    auto swap = [&](float x) {
+      float* at = trade + 256 * (swaps++ & 1);
+      at[128 * half + row] = x;
+      named_bar(1 + (warp & 3), 64);
+      return at[128 * (half ^ 1) + row];
+    };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!dead) dead = !mbar_wait_bounded(bar, parity, p.err);
     };
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
-      const Half x = half_of(it, h, group, even);
-      if (x.subs == 0) continue;
-      float m = -INFINITY, l = 0.f;
-      for (int u = 0; u < x.subs; ++u, ++n) {
-        const int b = n & 1;
-        wait(&bar_s[b], (uint32_t)((n >> 1) & 1));
+      if (!it.ok) continue;
+      const int h = it.part, q0 = it.level * kTile;
+      float m = -INFINITY, l = 0.f;  // of all keys; of this thread's
+      for (int t = 0; t <= it.level; ++t) {
+        wait(&bar_s[b], ph);
         tc_fence_after();
         uint32_t v[2][32];
-        tmem_ld32_nowait(tm + 64 * b, v[0]);
-        tmem_ld32_nowait(tm + 64 * b + 32, v[1]);
+        tmem_ld32_nowait(tS + 128 * b, v[0]);
+        tmem_ld32_nowait(tS + 128 * b + 32, v[1]);
         tmem_ld_wait();
-        if (D == 64) {
-          tc_fence_before();
-          mbar_arrive(&bar_sfree[b]);
-        }
-        if (u * kSub + kSub - 1 > x.row0) {  // the diagonal: keys after the row
-          const int last = x.row0 + row - u * kSub;
+        if (t == it.level) {  // the diagonal: keys after the row
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (32 * c + i > last) v[c][i] = __float_as_uint(-INFINITY);
+              if (col0 + 32 * c + i > row) v[c][i] = __float_as_uint(-INFINITY);
         }
         float mx[8];
 #pragma unroll
@@ -511,14 +461,35 @@ __global__ void __launch_bounds__(352, 1)
         const float mx1 = fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]));
         // m moves only when the tile's maximum exceeds it by more than 2^8 (P stays below
         // 2^8 otherwise, exact in its sum's float32), so O is rarely rescaled
-        const float mt = fmaxf(mx0, mx1) * sc;
+        const float mine = fmaxf(mx0, mx1);
+        const float mt = fmaxf(mine, swap(mine)) * sc;
         const float mn = mt > m + 8.f ? mt : m;
         const float ref = mn == -INFINITY ? 0.f : mn;
         const float alpha = ex2(m - ref);
-        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-        uint32_t pk[2][16];
+        if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          const int before = b == 0 ? 2 : b - 1;
+          wait(&bar_o[before], b == 0 ? ph ^ 1 : ph);
+          tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t o[32];
+            const uint32_t at = tO + D / 2 * half + 32 * c;
+            tmem_ld32_nowait(at, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float a0, a1;
+              mul2(a0, a1, __uint_as_float(o[i]), __uint_as_float(o[i + 1]), alpha, alpha);
+              o[i] = __float_as_uint(a0);
+              o[i + 1] = __float_as_uint(a1);
+            }
+            tmem_st32(at, o);
+          }
+        }
+        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             float t0, t1, t2, t3;
@@ -528,74 +499,55 @@ __global__ void __launch_bounds__(352, 1)
             const float p0 = ex2(t0), p1 = ex2(t1), p2 = ex2(t2), p3 = ex2(t3);
             add2(l0, l1, l0, l1, p0, p1);
             add2(l2, l3, l2, l3, p2, p3);
-            pk[c][i >> 1] = pack_bf16(p0, p1);
-            pk[c][(i >> 1) + 1] = pack_bf16(p2, p3);
+            pk[i >> 1] = pack_bf16(p0, p1);
+            pk[(i >> 1) + 1] = pack_bf16(p2, p3);
           }
+          tmem_st16(tS + 128 * b + 16 * c, pk);  // (over columns of its own)
+        }
         l = l * alpha + ((l0 + l1) + (l2 + l3));
         m = mn;
-        if (D == 64 && n >= 2) {  // the product before is done with the buffer
-          wait(&bar_o[b], (uint32_t)(((n >> 1) - 1) & 1));
-          tc_fence_after();
-        }
-        const uint32_t tP = tm + C::kColP0 + C::kStepP * b;
-        tmem_st16(tP, pk[0]);
-        tmem_st16(tP + 16, pk[1]);
-        if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          wait(&bar_o[b ^ 1], (uint32_t)(((n - 1) >> 1) & 1));
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32_nowait(tO + 32 * c, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float a0, a1;
-              mul2(a0, a1, __uint_as_float(o[i]), __uint_as_float(o[i + 1]), alpha, alpha);
-              o[i] = __float_as_uint(a0);
-              o[i + 1] = __float_as_uint(a1);
-            }
-            tmem_st32(tO + 32 * c, o);
-          }
-        }
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bar_p[b]);
+        next_buffer();
       }
       // O / l and lse
-      wait(&bar_o[(n - 1) & 1], (uint32_t)(((n - 1) >> 1) & 1));
+      const int last = b == 0 ? 2 : b - 1;
+      wait(&bar_o[last], b == 0 ? ph ^ 1 : ph);
       tc_fence_after();
-      uint32_t o[D / 32][32];
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) tmem_ld32_nowait(tO + 32 * c, o[c]);
+      const int col = D == 128 ? col0 : 0;  // (head_dim 64: the first four warps store)
+      uint32_t o[2][32];
+      tmem_ld32_nowait(tO + col, o[0]);
+      tmem_ld32_nowait(tO + col + 32, o[1]);
       tmem_ld_wait();
       tc_fence_before();
-      mbar_arrive(&bar_ofree[h]);
+      mbar_arrive(bar_ofree);
+      l += swap(l);
       const float inv = 1.f / l;
-      const bool live = x.row0 + row < it.len;
-      const int64_t at = (int64_t)it.beg + x.row0 + row;
-      if (p.lse != nullptr && live) p.lse[(int64_t)x.head * p.tokens + at] = (m + __log2f(l)) * kLn2;
+      const bool live = q0 + row < it.len;
+      const int64_t at = (int64_t)it.beg + q0 + row;
+      if (p.lse != nullptr && live && half == 0)
+        p.lse[(int64_t)h * p.tokens + at] = (m + __log2f(l)) * kLn2;
       float f0 = 0.f, f1 = 0.f;  // NaN if any value is NaN or infinite
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c)
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int i = 0; i < 32; i += 2)
           fma2(f0, f1, __uint_as_float(o[c][i]), __uint_as_float(o[c][i + 1]), 0.f, 0.f, f0, f1);
-      const bool fine = f0 + f1 == 0.f;
-      const bool whole = __all_sync(0xffffffffu, live && fine);
-      char* out = const_cast<char*>(p.o) + (at * p.so + (int64_t)x.head * D) * 2;
-#pragma unroll
-      for (int b = 0; b < C::kBoxes; ++b)
-        put_box(o[2 * b], o[2 * b + 1], inv, box, &to, 64 * b, x.head, (int)at, out + 128 * b, whole,
-                live && fine);
-      uint32_t broken = __ballot_sync(0xffffffffu, live && !fine);
+      f0 += f1;
+      const bool fine = f0 + swap(f0) == 0.f;
+      char* out = const_cast<char*>(p.o) + (at * p.so + (int64_t)h * D + col) * 2;
+      if (D == 128 || half == 0)
+        put_box(o[0], o[1], inv, box, &to, col, h, (int)at, out,
+                __all_sync(0xffffffffu, live && fine), live && fine);
+      uint32_t broken = half == 0 ? __ballot_sync(0xffffffffu, live && !fine) : 0;
       if (broken) {
         if (lane == 0) stores_read();
         __syncwarp();
         while (broken) {
           const int who = __ffs(broken) - 1;
           broken &= broken - 1;
-          repair_row<D>(p, it.beg, __shfl_sync(0xffffffffu, at, who), x.head,
+          repair_row<D>(p, it.beg, __shfl_sync(0xffffffffu, at, who), h,
                         reinterpret_cast<float*>(box));
         }
       }
@@ -648,15 +600,6 @@ struct BwdMaps {
   CUtensorMap q, k, v, g, out0, out1;
 };
 
-// D (+)= A B^T of two tiles in shared memory, A [128 x D], B [128 x D].
-template <int D>
-__device__ __forceinline__ void issue_tiles(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
-#pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off = (uint32_t)((kk >> 2) * kBox + (kk & 3) * 32);
-    mma_ss(d, sw128_desc(a + off, 16, 1024), sw128_desc(b + off, 16, 1024), idesc, kk > 0 ? 1u : 0u);
-  }
-}
 // Rows [from, 128) of a tile in shared memory become zero (all lanes of a warp).
 template <int D>
 __device__ __forceinline__ void clear_rows(unsigned char* tile, int from) {
@@ -1288,13 +1231,10 @@ const char* packed_tc_fwd_launch(const PackedParams& p, int sms, cudaStream_t st
       !encode_map(&maps[2], p.v, p.tokens, p.kv_heads, p.dim, p.sv, kTile) ||
       !encode_map(&maps[3], p.o, p.tokens, p.heads, p.dim, p.so, 32))
     return "tensor map encoding failed";
-  const int group = p.heads / p.kv_heads;
-  const int64_t rows = group % 2 == 0 ? kTile : 2 * kTile;
-  const int64_t parts = (int64_t)(group % 2 == 0 ? group / 2 : group) * p.kv_heads;
-  const int64_t items = (p.tokens / rows + p.batch) * parts;
+  const int64_t items = (p.tokens / kTile + p.batch) * p.heads;
   PackedParams pc = p;
   void* args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &pc};
-  if (cudaLaunchKernel(k.fwd, dim3((unsigned)std::min<int64_t>(sms, items)), dim3(352), args,
+  if (cudaLaunchKernel(k.fwd, dim3((unsigned)std::min<int64_t>(sms, items)), dim3(384), args,
                        (size_t)k.fwd_smem, stream) != cudaSuccess)
     return "launch failed";
   return nullptr;
