@@ -572,8 +572,8 @@ __global__ void __launch_bounds__(384, 1)
 // tile's 128 columns each; warp 8 loads, warps 9 and 10 issue.
 //
 // dQ, a query tile against key tiles t: S(t) = Q K^T, dP(t) = dO V^T, then
-//   dS = P (dP - delta) as bf16 in one of two buffers, dQ += dS K.  S and dP of t + 1 run
-//   while the softmax works on t.
+//   dS = P (dP - delta) as bf16 over S, dQ += dS K.  S has two buffers, so that S and dP of
+//   t + 1 run while the softmax works on t.
 // dK and dV, a key tile against the query tiles of all heads of its group: S^T = K Q^T, P^T
 //   over its half of S^T's columns, dV += P^T dO; dP^T = V dO^T, dS^T likewise, dK += dS^T Q.
 //   Two issuers, so that one pair's products run while the softmax works on the other pair.
@@ -588,7 +588,8 @@ struct Bwd {
   static constexpr int kOffStage = 6 * kTileBytes;    // dQ: 8 warps' output boxes
   static constexpr int kOffStat = 6 * kTileBytes;     // dK, dV: [stage][-lse, -delta][128]
   static constexpr int kStage = 32 * 128;
-  static constexpr int kOffBarQ = kOffStage + 8 * kStage, kOffBarK = kOffStat + 2048;
+  static constexpr int kOffTrade = kOffStage + 8 * kStage;  // dQ: [128] floats
+  static constexpr int kOffBarQ = kOffTrade + 512, kOffBarK = kOffStat + 2048;
   static constexpr int kSmemQ = kOffBarQ + 256 + kSorted * 8 + 1024;
   static constexpr int kSmemK = kOffBarK + 256 + 2 * kSorted * 8 + 1024;
   static constexpr uint32_t kIdescS = attn_idesc(kTile, kTile, false);
@@ -634,11 +635,11 @@ __global__ void __launch_bounds__(256) packed_delta_kernel(const PackedParams p)
 }
 
 template <int D>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(384, 1)
     packed_dq_kernel(const __grid_constant__ BwdMaps maps, const PackedParams p) {
   using C = Bwd<D>;
   constexpr int T = C::kTileBytes;
-  constexpr uint32_t kColP = 128, kColG = 256, kColS = 384;  // dP, dQ, dS buffers
+  constexpr uint32_t kColP = 256, kColG = 384;  // dP, dQ after S's two buffers
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -649,17 +650,17 @@ __global__ void __launch_bounds__(352, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBarQ);
   uint64_t* bar_q = bars;           // Q and dO landed
   uint64_t* bar_qfree = bars + 1;   // the item's last S and dP done
-  uint64_t* bar_s = bars + 2;
-  uint64_t* bar_dp = bars + 3;
-  uint64_t* bar_read = bars + 4;    // S and dP read, 256 arrivals
-  uint64_t* bar_gfree = bars + 5;   // dQ read, 256 arrivals
-  uint64_t* bar_ds = bars + 6;      // [buffer] dS written, 256 arrivals
-  uint64_t* bar_g = bars + 8;       // [buffer] dQ += dS K done
-  uint64_t* bar_kfull = bars + 10;  // [stage]
-  uint64_t* bar_vfull = bars + 12;
-  uint64_t* bar_kempty = bars + 14;
-  uint64_t* bar_vempty = bars + 16;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 18);
+  uint64_t* bar_dp = bars + 2;
+  uint64_t* bar_read = bars + 3;    // dP read, 256 arrivals
+  uint64_t* bar_gfree = bars + 4;   // dQ read, 256 arrivals
+  uint64_t* bar_ds = bars + 5;      // [buffer] dS written, 256 arrivals
+  uint64_t* bar_s = bars + 7;       // [buffer] S done
+  uint64_t* bar_g = bars + 9;       // [buffer] dQ += dS K done
+  uint64_t* bar_kfull = bars + 11;  // [stage]
+  uint64_t* bar_vfull = bars + 13;
+  uint64_t* bar_kempty = bars + 15;
+  uint64_t* bar_vempty = bars + 17;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 19);
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(tslot)),
@@ -668,9 +669,7 @@ __global__ void __launch_bounds__(352, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 32 * 8) {
-    for (int i = 0; i < 4; ++i) mbar_init(bars + i, 1);
-    for (int i = 4; i < 8; ++i) mbar_init(bars + i, 256);
-    for (int i = 8; i < 18; ++i) mbar_init(bars + i, 1);
+    for (int i = 0; i < 19; ++i) mbar_init(bars + i, i >= 3 && i < 7 ? 256 : 1);
     fence_mbar_init();
   }
   Sequences list;
@@ -683,47 +682,45 @@ __global__ void __launch_bounds__(352, 1)
   const int group = p.heads / p.kv_heads;
   bool dead = false, more;
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ loads
-    int nk = 0, nv = 0, nq = 0;
+  if (warp == 8 || warp == 11) {
+    // ------------------------------------------ loads: Q, dO and K, or V
+    const bool keys = warp == 8;
+    const CUtensorMap* map = keys ? &maps.k : &maps.v;
+    uint64_t *full = keys ? bar_kfull : bar_vfull, *empty = keys ? bar_kempty : bar_vempty;
+    int n = 0, items = 0;
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
       if (!it.ok || lane != 0) continue;
-      const int h = it.part, kv = h / group;
-      if (nq > 0) wait_spin(bar_qfree, (uint32_t)((nq - 1) & 1), dead, p.err);
-      if (dead) continue;
-      ++nq;
-      mbar_arrive_expect_tx(bar_q, 2 * T);
-      for (int b = 0; b < C::kBoxes; ++b) {
-        load_box(sq + b * kBox, &maps.q, 64 * b, h, it.beg + it.level * kTile, bar_q);
-        load_box(sg + b * kBox, &maps.g, 64 * b, h, it.beg + it.level * kTile, bar_q);
+      const int h = it.part;
+      if (keys) {
+        if (items > 0) wait_spin(bar_qfree, (uint32_t)((items - 1) & 1), dead, p.err);
+        if (!dead) {
+          ++items;
+          mbar_arrive_expect_tx(bar_q, 2 * T);
+          for (int b = 0; b < C::kBoxes; ++b) {
+            load_box(sq + b * kBox, &maps.q, 64 * b, h, it.beg + it.level * kTile, bar_q);
+            load_box(sg + b * kBox, &maps.g, 64 * b, h, it.beg + it.level * kTile, bar_q);
+          }
+        }
       }
       for (int t = 0; t <= it.level; ++t) {
-        const int s = nk & 1;
-        const uint32_t ph = (uint32_t)(((nk >> 1) - 1) & 1);
-        if (nk >= 2) wait_spin(&bar_kempty[s], ph, dead, p.err);
+        const int s = n & 1;
+        if (n >= 2) wait_spin(&empty[s], (uint32_t)(((n >> 1) - 1) & 1), dead, p.err);
         if (dead) break;
-        ++nk;
-        mbar_arrive_expect_tx(&bar_kfull[s], T);
+        ++n;
+        mbar_arrive_expect_tx(&full[s], T);
         for (int b = 0; b < C::kBoxes; ++b)
-          load_box(sk(s) + b * kBox, &maps.k, 64 * b, kv, it.beg + t * kTile, &bar_kfull[s]);
-        if (nv >= 2) wait_spin(&bar_vempty[s], ph, dead, p.err);
-        if (dead) break;
-        ++nv;
-        mbar_arrive_expect_tx(&bar_vfull[s], T);
-        for (int b = 0; b < C::kBoxes; ++b)
-          load_box(sv(s) + b * kBox, &maps.v, 64 * b, kv, it.beg + t * kTile, &bar_vfull[s]);
+          load_box((keys ? sk(s) : sv(s)) + b * kBox, map, 64 * b, h / group, it.beg + t * kTile,
+                   &full[s]);
       }
     }
-    for (int n = max(nk - 2, 0); n < nk; ++n)
-      mbar_wait_bounded(&bar_kfull[n & 1], (uint32_t)((n >> 1) & 1), p.err);
-    for (int n = max(nv - 2, 0); n < nv; ++n)
-      mbar_wait_bounded(&bar_vfull[n & 1], (uint32_t)((n >> 1) & 1), p.err);
-    if (nq > 0) mbar_wait_bounded(bar_q, (uint32_t)((nq - 1) & 1), p.err);
+    for (int i = max(n - 2, 0); i < n; ++i)
+      mbar_wait_bounded(&full[i & 1], (uint32_t)((i >> 1) & 1), p.err);
+    if (items > 0) mbar_wait_bounded(bar_q, (uint32_t)((items - 1) & 1), p.err);
   } else if (warp == 9) {
     // ----------------------------------------------------------- S and dP
-    int n = 0, items = 0;
+    int ns = 0, n = 0, items = 0;
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
@@ -733,12 +730,17 @@ __global__ void __launch_bounds__(352, 1)
         const int s = n & 1;
         const uint32_t ph = (uint32_t)((n >> 1) & 1);
         wait_spin(&bar_kfull[s], ph, dead, p.err);
-        if (n > 0) wait_spin(bar_read, (uint32_t)((n - 1) & 1), dead, p.err);
-        wait_spin(&bar_vfull[s], ph, dead, p.err);
+        // dQ += dS K of two tiles ago is done with the buffer
+        if (n >= 2) wait_spin(&bar_g[s], ph ^ 1, dead, p.err);
         if (dead) break;
         tc_fence_after();
-        issue_tiles<D>(tmem, smem_addr(sq), smem_addr(sk(s)), C::kIdescS);
-        mma_commit(bar_s);
+        issue_tiles<D>(tmem + 128 * s, smem_addr(sq), smem_addr(sk(s)), C::kIdescS);
+        mma_commit(&bar_s[s]);
+        ++ns;
+        wait_spin(&bar_vfull[s], ph, dead, p.err);
+        if (n > 0) wait_spin(bar_read, (uint32_t)((n - 1) & 1), dead, p.err);
+        if (dead) break;
+        tc_fence_after();
         issue_tiles<D>(tmem + kColP, smem_addr(sg), smem_addr(sv(s)), C::kIdescS);
         mma_commit(bar_dp);
         mma_commit(&bar_vempty[s]);
@@ -746,6 +748,7 @@ __global__ void __launch_bounds__(352, 1)
         ++n;
       }
     }
+    if (ns > 0) mbar_wait_bounded(&bar_s[(ns - 1) & 1], (uint32_t)(((ns - 1) >> 1) & 1), p.err);
     if (n > 0) mbar_wait_bounded(bar_dp, (uint32_t)((n - 1) & 1), p.err);
   } else if (warp == 10) {
     // --------------------------------------------------------- dQ += dS K
@@ -770,7 +773,7 @@ __global__ void __launch_bounds__(352, 1)
           const uint32_t k_addr = smem_addr(sk(s));
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_ts(tmem + kColG, tmem + kColS + 64 * s + 8 * kk,
+            mma_ts(tmem + kColG, tmem + 128 * s + 8 * kk + (kk >= 4 ? 32 : 0),
                    sw128_desc(k_addr + kk * 2048, kBox, 1024), C::kIdescG,
                    (t > 0 || kk > 0) ? 1u : 0u);
           mma_commit(&bar_g[s]);
@@ -789,6 +792,7 @@ __global__ void __launch_bounds__(352, 1)
     const uint32_t tS = tmem + lanes + col0, tG = tmem + lanes + kColG;
     const float sc = p.scale_log2;
     unsigned char* box = smem + C::kOffStage + warp * C::kStage;
+    float* trade = reinterpret_cast<float*>(smem + C::kOffTrade);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!dead) dead = !mbar_wait_bounded(bar, parity, p.err);
     };
@@ -801,18 +805,16 @@ __global__ void __launch_bounds__(352, 1)
       const bool live = q0 + row < it.len;
       const int64_t at = (int64_t)it.beg + q0 + row, stat = (int64_t)h * p.tokens + at;
       const float nl = live ? -p.lse[stat] * kLog2e : 0.f;
-      const float nd = live ? -p.delta[stat] : 0.f;
+      float nd = live ? -p.delta[stat] : 0.f;
       for (int t = 0; t <= it.level; ++t, ++n) {
         uint32_t v[2][32], w[2][32];
-        wait(bar_s, (uint32_t)(n & 1));
+        const int s = n & 1;
+        const uint32_t tB = tS + 128 * s;
+        wait(&bar_s[s], (uint32_t)((n >> 1) & 1));
         tc_fence_after();
-        tmem_ld32_nowait(tS, v[0]);
-        tmem_ld32_nowait(tS + 32, v[1]);
+        tmem_ld32_nowait(tB, v[0]);
+        tmem_ld32_nowait(tB + 32, v[1]);
         tmem_ld_wait();
-        wait(bar_dp, (uint32_t)(n & 1));
-        tc_fence_after();
-        tmem_ld32_nowait(tS + kColP, w[0]);
-        tmem_ld32_nowait(tS + kColP + 32, w[1]);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -822,9 +824,31 @@ __global__ void __launch_bounds__(352, 1)
             v[c][i] = __float_as_uint(ex2(t0));
             v[c][i + 1] = __float_as_uint(ex2(t1));
           }
+        wait(bar_dp, (uint32_t)(n & 1));
+        tc_fence_after();
+        tmem_ld32_nowait(tS + kColP, w[0]);
+        tmem_ld32_nowait(tS + kColP + 32, w[1]);
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(bar_read);
+        if (it.level == 0) {
+          // One key tile: delta = sum P dP, without the rounding of o, is at hand.  It counts
+          // most in these rows, whose few large weights all but cancel in dP - delta.
+          float d = 0.f;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (col0 + 32 * c + i <= row)
+                d = fmaf(__uint_as_float(v[c][i]), __uint_as_float(w[c][i]), d);
+          if (half == 1) trade[row] = d;
+          named_bar(1 + (warp & 3), 64);
+          if (half == 0) trade[row] = d += trade[row];
+          named_bar(1 + (warp & 3), 64);
+          if (half == 1) d = trade[row];
+          nd = -d;
+          if (live && half == 0) p.delta[stat] = d;
+        }
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -842,22 +866,17 @@ __global__ void __launch_bounds__(352, 1)
             for (int i = 0; i < 32; ++i)
               if (col0 + 32 * c + i > row) w[c][i] = 0u;
         }
-        uint32_t pk[2][16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 2)
-            pk[c][i >> 1] = pack_bf16(__uint_as_float(w[c][i]), __uint_as_float(w[c][i + 1]));
-        if (n >= 2) {  // the product that read this buffer is done
-          wait(&bar_g[n & 1], (uint32_t)(((n >> 1) - 1) & 1));
-          tc_fence_after();
+            pk[i >> 1] = pack_bf16(__uint_as_float(w[c][i]), __uint_as_float(w[c][i + 1]));
+          tmem_st16(tB + 16 * c, pk);  // (over columns of its own)
         }
-        const uint32_t tD = tmem + lanes + kColS + 64 * (n & 1) + 32 * half;
-        tmem_st16(tD, pk[0]);
-        tmem_st16(tD + 16, pk[1]);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&bar_ds[n & 1]);
+        mbar_arrive(&bar_ds[s]);
       }
       wait(&bar_g[(n - 1) & 1], (uint32_t)(((n - 1) >> 1) & 1));
       tc_fence_after();
@@ -1262,7 +1281,7 @@ const char* packed_tc_bwd_launch(const PackedParams& p, int sms, cudaStream_t st
     return "launch failed";
   const int64_t levels = p.tokens / kTile + p.batch;
   void* qargs[] = {&mq, &pc};
-  if (cudaLaunchKernel(k.dq, dim3((unsigned)std::min<int64_t>(sms, levels * p.heads)), dim3(352),
+  if (cudaLaunchKernel(k.dq, dim3((unsigned)std::min<int64_t>(sms, levels * p.heads)), dim3(384),
                        qargs, (size_t)k.dq_smem, stream) != cudaSuccess)
     return "launch failed";
   void* kargs[] = {&mk, &pc};
