@@ -574,9 +574,11 @@ __global__ void __launch_bounds__(384, 1)
 // dQ, a query tile against key tiles t: S(t) = Q K^T, dP(t) = dO V^T, then
 //   dS = P (dP - delta) as bf16 over S, dQ += dS K.  S has two buffers, so that S and dP of
 //   t + 1 run while the softmax works on t.
-// dK and dV, a key tile against the query tiles of all heads of its group: S^T = K Q^T, P^T
-//   over its half of S^T's columns, dV += P^T dO; dP^T = V dO^T, dS^T likewise, dK += dS^T Q.
-//   Two issuers, so that one pair's products run while the softmax works on the other pair.
+// dK and dV, a key tile against the query tiles of all heads of its group, in two TMEM buffers
+//   X and Y that change places with each tile: S^T = K Q^T in X, dP^T = V dO^T in Y; P^T and
+//   dS^T, bf16, over S^T in X; dV += P^T dO, dK += dS^T Q.  Y is free once dP^T is read, so S^T
+//   of the next tile and dV run while the softmax goes on to dS^T; the next dP^T, into X, while
+//   it works on the next P^T.
 //
 // Rows of a tile beyond its sequence are masked, and where such a row is summed over (K in
 // dQ; Q and dO in dK, dV) it is set to zero in shared memory before the product, so that no
@@ -906,7 +908,7 @@ __global__ void __launch_bounds__(352, 1)
     packed_dkv_kernel(const __grid_constant__ BwdMaps maps, const PackedParams p) {
   using C = Bwd<D>;
   constexpr int T = C::kTileBytes;
-  constexpr uint32_t kColP = 128, kColV = 256, kColK = 256 + D;  // dP^T, dV, dK
+  constexpr uint32_t kColV = 256, kColK = 256 + D;  // dV, dK, after two buffers
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -919,16 +921,16 @@ __global__ void __launch_bounds__(352, 1)
   uint64_t* bar_kv = bars;          // K and V landed
   uint64_t* bar_s = bars + 1;
   uint64_t* bar_dp = bars + 2;
-  uint64_t* bar_dv = bars + 3;      // dV += P^T dO done
-  uint64_t* bar_dk = bars + 4;      // dK += dS^T Q done
-  uint64_t* bar_p = bars + 5;       // P^T written, 256 arrivals
-  uint64_t* bar_ds = bars + 6;      // dS^T written, 256 arrivals
-  uint64_t* bar_gfree = bars + 7;   // dK and dV read, 256 arrivals
-  uint64_t* bar_kvfree = bars + 8;  // the output boxes (over K and V) are read, 8 arrivals
-  uint64_t* bar_qfull = bars + 10;  // [stage]
-  uint64_t* bar_dofull = bars + 12;
-  uint64_t* bar_stat = bars + 14;   // lse and delta written
-  uint64_t* bar_empty = bars + 16;  // [stage] both products are done with it
+  uint64_t* bar_g = bars + 3;       // dV += P^T dO and dK += dS^T Q done
+  uint64_t* bar_qfull = bars + 4;   // [stage]
+  uint64_t* bar_dofull = bars + 6;
+  uint64_t* bar_stat = bars + 8;    // lse and delta written
+  uint64_t* bar_empty = bars + 10;  // [stage] dV and dK are done with it
+  uint64_t* bar_read = bars + 12;   // dP^T read, 256 arrivals
+  uint64_t* bar_p = bars + 13;      // [buffer] P^T written, 256 arrivals
+  uint64_t* bar_ds = bars + 15;     // dS^T written, 256 arrivals
+  uint64_t* bar_gfree = bars + 16;  // dK and dV read, 256 arrivals
+  uint64_t* bar_kvfree = bars + 17; // the output boxes (over K and V) are read, 8 arrivals
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 18);
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -938,12 +940,7 @@ __global__ void __launch_bounds__(352, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 32 * 8) {
-    for (int i = 0; i < 5; ++i) mbar_init(bars + i, 1);
-    for (int i = 5; i < 8; ++i) mbar_init(bars + i, 256);
-    mbar_init(bar_kvfree, 8);
-    for (int i = 10; i < 16; ++i) mbar_init(bars + i, 1);
-    mbar_init(&bar_empty[0], 2);
-    mbar_init(&bar_empty[1], 2);
+    for (int i = 0; i < 18; ++i) mbar_init(bars + i, i < 12 ? 1 : i < 17 ? 256 : 8);
     fence_mbar_init();
   }
   Sequences list;
@@ -1019,69 +1016,96 @@ __global__ void __launch_bounds__(352, 1)
       }
       if (items > 0) mbar_wait_bounded(bar_kv, (uint32_t)((items - 1) & 1), p.err);
     }
-  } else if (warp >= 9) {
-    // warp 9: S^T = K Q^T, dV += P^T dO; warp 10: dP^T = V dO^T, dK += dS^T Q
-    const bool for_v = warp == 9;
-    const uint32_t a_addr = smem_addr(for_v ? sk : sv);
-    const uint32_t tA = tmem + (for_v ? 0u : kColP), tG = tmem + (for_v ? kColV : kColK);
-    uint64_t* bar_in = for_v ? bar_qfull : bar_dofull;   // the first product's tile
-    uint64_t* bar_sum = for_v ? bar_dofull : bar_qfull;  // the second's
-    uint64_t* bar_a = for_v ? bar_s : bar_dp;
-    uint64_t* bar_w = for_v ? bar_p : bar_ds;
-    uint64_t* bar_g = for_v ? bar_dv : bar_dk;
-    int n = 0, firsts = 0, items = 0;
+  } else if (warp == 9) {
+    // ------------------------------------------- S^T = K Q^T, dP^T = V dO^T
+    int ns = 0, n = 0, items = 0;
+    for (int r = 0;; ++r) {
+      const Item it = list.get(r, more);
+      if (!more) break;
+      if (!it.ok || lane != 0) continue;
+      const int tiles = group * (it.level + 1);
+      wait_spin(bar_kv, (uint32_t)(items++ & 1), dead, p.err);
+      for (int t = 0; t < tiles; ++t) {
+        const int s = n & 1;
+        const uint32_t ph = (uint32_t)((n >> 1) & 1), before = (uint32_t)((n - 1) & 1);
+        wait_spin(&bar_qfull[s], ph, dead, p.err);
+        if (n > 0) wait_spin(bar_read, before, dead, p.err);  // this buffer had dP^T
+        if (dead) break;
+        tc_fence_after();
+        issue_tiles<D>(tmem + 128 * s, smem_addr(sk), smem_addr(sq(s)), C::kIdescS);
+        mma_commit(bar_s);
+        ++ns;
+        wait_spin(&bar_dofull[s], ph, dead, p.err);
+        if (n > 0) wait_spin(bar_g, before, dead, p.err);  // this one the weights
+        if (dead) break;
+        tc_fence_after();
+        issue_tiles<D>(tmem + 128 * (s ^ 1), smem_addr(sv), smem_addr(sg(s)), C::kIdescS);
+        mma_commit(bar_dp);
+        ++n;
+      }
+    }
+    if (ns > 0) mbar_wait_bounded(bar_s, (uint32_t)((ns - 1) & 1), p.err);
+    if (n > 0) mbar_wait_bounded(bar_dp, (uint32_t)((n - 1) & 1), p.err);
+  } else if (warp == 10) {
+    // ---------------------------------------- dV += P^T dO, dK += dS^T Q
+    int n = 0, items = 0;
+    bool open = false;  // dV of a tile is issued, its dK is not
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
       if (!it.ok) continue;
       const int first = first_of(it), tiles = group * (it.level + 1);
-      if (lane == 0) wait_spin(bar_kv, (uint32_t)(items & 1), dead, p.err);
       for (int t = 0, i = first; t < tiles; ++t, i = i == first + it.level ? first : i + 1) {
-        const int s = n & 1;
-        const uint32_t ph = (uint32_t)((n >> 1) & 1);
-        unsigned char* tin = for_v ? sq(s) : sg(s);
-        unsigned char* tsum = for_v ? sg(s) : sq(s);
+        const int s = n & 1, rest = it.len - i * kTile;
+        const uint32_t ph = (uint32_t)((n >> 1) & 1), tW = tmem + 128 * s;
+        auto sum = [&](uint32_t to, uint32_t weights, const unsigned char* tile) {
+          tc_fence_after();
+          const uint32_t addr = smem_addr(tile);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_ts(tmem + to, weights + 8 * kk + (kk >= 4 ? 32 : 0),
+                   sw128_desc(addr + kk * 2048, kBox, 1024), C::kIdescG,
+                   (t > 0 || kk > 0) ? 1u : 0u);
+        };
         if (lane == 0) {
-          wait_spin(&bar_in[s], ph, dead, p.err);
-          // the weights of the tile before stand where this product goes
-          if (n > 0) wait_spin(bar_g, (uint32_t)((n - 1) & 1), dead, p.err);
-          if (!dead) {
-            tc_fence_after();
-            issue_tiles<D>(tA, a_addr, smem_addr(tin), C::kIdescS);
-            mma_commit(bar_a);
-            ++firsts;
-          }
-          wait_spin(&bar_sum[s], ph, dead, p.err);
-          wait_spin(bar_w, (uint32_t)(n & 1), dead, p.err);
+          wait_spin(&bar_dofull[s], ph, dead, p.err);
+          wait_spin(&bar_qfull[s], ph, dead, p.err);
+          wait_spin(&bar_p[s], ph, dead, p.err);
           if (t == 0 && items > 0) wait_spin(bar_gfree, (uint32_t)((items - 1) & 1), dead, p.err);
         }
         dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
         if (dead) break;
-        const int rest = it.len - i * kTile;
-        if (rest < kTile) clear_rows<D>(tsum, rest);
+        if (rest < kTile) clear_rows<D>(sg(s), rest);
+        open = true;
         if (lane == 0) {
-          tc_fence_after();
-          const uint32_t addr = smem_addr(tsum);
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_ts(tG, tA + 8 * kk + (kk >= 4 ? 32 : 0), sw128_desc(addr + kk * 2048, kBox, 1024),
-                   C::kIdescG, (t > 0 || kk > 0) ? 1u : 0u);
+          sum(kColV, tW, sg(s));
+          wait_spin(bar_ds, (uint32_t)(n & 1), dead, p.err);
+        }
+        dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
+        if (dead) break;
+        if (rest < kTile) clear_rows<D>(sq(s), rest);
+        if (lane == 0) {
+          sum(kColK, tW + 32, sq(s));
           mma_commit(bar_g);
           mma_commit(&bar_empty[s]);
         }
+        open = false;
         ++n;
       }
       ++items;
     }
     if (lane == 0) {
-      if (firsts > 0) mbar_wait_bounded(bar_a, (uint32_t)((firsts - 1) & 1), p.err);
+      if (open) {  // (nobody waits for it any more)
+        mma_commit(bar_g);
+        ++n;
+      }
       if (n > 0) mbar_wait_bounded(bar_g, (uint32_t)((n - 1) & 1), p.err);
     }
   } else {
     // ------------------------------------------------------------ softmax
     const int row = tid & 127, half = warp >> 2, col0 = 64 * half;  // key row, query columns
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + col0, tD = tS + kColP;
+    const uint32_t tS = tmem + lanes + col0;
     const float sc = p.scale_log2;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!dead) dead = !mbar_wait_bounded(bar, parity, p.err);
@@ -1096,6 +1120,7 @@ __global__ void __launch_bounds__(352, 1)
         const int s = n & 1;
         const float4* nl = reinterpret_cast<const float4*>(stats(s) + col0);
         const float4* nd = nl + 32;
+        const uint32_t tX = tS + 128 * s, tY = tS + 128 * (s ^ 1);
         uint32_t v[2][32], pk[16];
         // columns [lo, hi) of this thread's 64 see its key
         const int lo = i == first ? row - col0 : 0, hi = it.len - i * kTile - col0;
@@ -1103,8 +1128,8 @@ __global__ void __launch_bounds__(352, 1)
         wait(&bar_stat[s], (uint32_t)((n >> 1) & 1));
         wait(bar_s, (uint32_t)(n & 1));
         tc_fence_after();
-        tmem_ld32_nowait(tS, v[0]);
-        tmem_ld32_nowait(tS + 32, v[1]);
+        tmem_ld32_nowait(tX, v[0]);
+        tmem_ld32_nowait(tX + 32, v[1]);
         tmem_ld_wait();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -1128,17 +1153,19 @@ __global__ void __launch_bounds__(352, 1)
 #pragma unroll
           for (int j = 0; j < 32; j += 2)
             pk[j >> 1] = pack_bf16(__uint_as_float(v[c][j]), __uint_as_float(v[c][j + 1]));
-          tmem_st16(tS + 16 * c, pk);
+          tmem_st16(tX + 16 * c, pk);  // (over columns of its own)
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar_p);
+        mbar_arrive(&bar_p[s]);
         wait(bar_dp, (uint32_t)(n & 1));
         tc_fence_after();
         uint32_t w[2][32];
-        tmem_ld32_nowait(tD, w[0]);
-        tmem_ld32_nowait(tD + 32, w[1]);
+        tmem_ld32_nowait(tY, w[0]);
+        tmem_ld32_nowait(tY + 32, w[1]);
         tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(bar_read);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -1162,14 +1189,13 @@ __global__ void __launch_bounds__(352, 1)
 #pragma unroll
           for (int j = 0; j < 32; j += 2)
             pk[j >> 1] = pack_bf16(__uint_as_float(w[c][j]), __uint_as_float(w[c][j + 1]));
-          tmem_st16(tD + 16 * c, pk);
+          tmem_st16(tX + 32 + 16 * c, pk);
         }
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bar_ds);
       }
-      wait(bar_dv, (uint32_t)((n - 1) & 1));
-      wait(bar_dk, (uint32_t)((n - 1) & 1));
+      wait(bar_g, (uint32_t)((n - 1) & 1));
       tc_fence_after();
       const bool live = first * kTile + row < it.len;
       const bool whole = __all_sync(0xffffffffu, live);
