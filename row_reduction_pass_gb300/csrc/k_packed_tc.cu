@@ -47,6 +47,14 @@ __device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(head), "r"(token), "r"(smem_addr(bar))
       : "memory");
 }
+// The same box on its way into L2.
+__device__ __forceinline__ void prefetch_box(const CUtensorMap* map, int col, int head,
+                                             int token) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(col), "r"(head), "r"(token)
+               : "memory");
+}
 __device__ __forceinline__ void store_box(const CUtensorMap* map, const void* src, int col,
                                           int head, int token) {
   asm volatile(
@@ -204,6 +212,41 @@ __device__ __forceinline__ void put_box(const uint32_t (&lo)[32], const uint32_t
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) store_box(map, box, col, head, token);
+  }
+}
+
+// 64 columns of a warp's 32 rows (lane = row, lo and hi 32 columns each) times f as bf16, for
+// the rows of `rows` (a bit each).  Eight lanes trade their 16-byte chunks, so that each of
+// them stores one chunk of eight rows and a store covers whole lines of 128 bytes.  out: this
+// column of the warp's first row, rows `stride` bytes apart.
+__device__ __forceinline__ void put_rows(const uint32_t (&lo)[32], const uint32_t (&hi)[32],
+                                         float f, char* out, int64_t stride, uint32_t rows) {
+  const int lane = threadIdx.x & 31, at = lane & 7;
+  uint32_t x[8][4];
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t* o = (c < 4 ? lo : hi) + 8 * (c & 3) + 2 * k;
+      x[c][k] = pack_bf16(__uint_as_float(o[0]) * f, __uint_as_float(o[1]) * f);
+    }
+#pragma unroll
+  for (int bit = 1; bit < 8; bit *= 2)
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if ((c & bit) == 0)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool up = (at & bit) != 0;
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[c][k] : x[c | bit][k], bit);
+          (up ? x[c][k] : x[c | bit][k]) = got;
+        }
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const int row = (lane & ~7) + c;
+    if (rows >> row & 1)
+      *reinterpret_cast<uint4*>(out + row * stride + 16 * at) =
+          make_uint4(x[c][0], x[c][1], x[c][2], x[c][3]);
   }
 }
 
@@ -587,10 +630,9 @@ template <int D>
 struct Bwd {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kBoxes * kBox;
-  static constexpr int kOffStage = 6 * kTileBytes;    // dQ: 8 warps' output boxes
   static constexpr int kOffStat = 6 * kTileBytes;     // dK, dV: [stage][-lse, -delta][128]
   static constexpr int kStage = 32 * 128;
-  static constexpr int kOffTrade = kOffStage + 8 * kStage;  // dQ: [128] floats
+  static constexpr int kOffTrade = 7 * kTileBytes;    // dQ: [128] floats
   static constexpr int kOffBarQ = kOffTrade + 512, kOffBarK = kOffStat + 2048;
   static constexpr int kSmemQ = kOffBarQ + 256 + kSorted * 8 + 1024;
   static constexpr int kSmemK = kOffBarK + 256 + 2 * kSorted * 8 + 1024;
@@ -647,7 +689,7 @@ __global__ void __launch_bounds__(384, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char *sq = smem, *sg = smem + T;
   auto sk = [&](int s) { return smem + (2 + s) * T; };
-  auto sv = [&](int s) { return smem + (4 + s) * T; };
+  auto sv = [&](int s) { return smem + (5 + s) * T; };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBarQ);
   uint64_t* bar_q = bars;           // Q and dO landed
@@ -658,11 +700,11 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* bar_ds = bars + 5;      // [buffer] dS written, 256 arrivals
   uint64_t* bar_s = bars + 7;       // [buffer] S done
   uint64_t* bar_g = bars + 9;       // [buffer] dQ += dS K done
-  uint64_t* bar_kfull = bars + 11;  // [stage]
-  uint64_t* bar_vfull = bars + 13;
-  uint64_t* bar_kempty = bars + 15;
-  uint64_t* bar_vempty = bars + 17;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 19);
+  uint64_t* bar_kfull = bars + 11;  // [stage of 3]
+  uint64_t* bar_kempty = bars + 14;
+  uint64_t* bar_vfull = bars + 17;  // [stage of 2]
+  uint64_t* bar_vempty = bars + 19;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 21);
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(tslot)),
@@ -671,12 +713,13 @@ __global__ void __launch_bounds__(384, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 32 * 8) {
-    for (int i = 0; i < 19; ++i) mbar_init(bars + i, i >= 3 && i < 7 ? 256 : 1);
+    for (int i = 0; i < 21; ++i) mbar_init(bars + i, i >= 3 && i < 7 ? 256 : 1);
     fence_mbar_init();
   }
   Sequences list;
   list.init(reinterpret_cast<int2*>(smem + C::kOffBarQ + 256),
-            reinterpret_cast<int2*>(smem + C::kOffStage), p, kTile, p.heads);
+            reinterpret_cast<int2*>(smem), p, kTile, p.heads);
+  fence_proxy_async_smem();  // (the list's scratch lies where copies will land)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -689,10 +732,13 @@ __global__ void __launch_bounds__(384, 1)
     const bool keys = warp == 8;
     const CUtensorMap* map = keys ? &maps.k : &maps.v;
     uint64_t *full = keys ? bar_kfull : bar_vfull, *empty = keys ? bar_kempty : bar_vempty;
-    int n = 0, items = 0;
-    for (int r = 0;; ++r) {
-      const Item it = list.get(r, more);
-      if (!more) break;
+    const int ring = keys ? 3 : 2;
+    int s = 0, n = 0, items = 0;
+    uint32_t ph = 0;
+    Item nx = list.get(0, more);
+    for (int r = 1; more; ++r) {
+      const Item it = nx;
+      nx = list.get(r, more);
       if (!it.ok || lane != 0) continue;
       const int h = it.part;
       if (keys) {
@@ -704,41 +750,51 @@ __global__ void __launch_bounds__(384, 1)
             load_box(sq + b * kBox, &maps.q, 64 * b, h, it.beg + it.level * kTile, bar_q);
             load_box(sg + b * kBox, &maps.g, 64 * b, h, it.beg + it.level * kTile, bar_q);
           }
+          if (nx.ok)  // (the next item's are loaded only when this one's last S and dP are done)
+            for (int b = 0; b < C::kBoxes; ++b) {
+              prefetch_box(&maps.q, 64 * b, nx.part, nx.beg + nx.level * kTile);
+              prefetch_box(&maps.g, 64 * b, nx.part, nx.beg + nx.level * kTile);
+            }
         }
       }
       for (int t = 0; t <= it.level; ++t) {
-        const int s = n & 1;
-        if (n >= 2) wait_spin(&empty[s], (uint32_t)(((n >> 1) - 1) & 1), dead, p.err);
+        if (n >= ring) wait_spin(&empty[s], ph ^ 1, dead, p.err);
         if (dead) break;
         ++n;
         mbar_arrive_expect_tx(&full[s], T);
         for (int b = 0; b < C::kBoxes; ++b)
           load_box((keys ? sk(s) : sv(s)) + b * kBox, map, 64 * b, h / group, it.beg + t * kTile,
                    &full[s]);
+        if (++s == ring) s = 0, ph ^= 1;
       }
     }
-    for (int i = max(n - 2, 0); i < n; ++i)
-      mbar_wait_bounded(&full[i & 1], (uint32_t)((i >> 1) & 1), p.err);
+    for (int i = min(n, ring); i > 0; --i) {
+      if (--s < 0) s = ring - 1, ph ^= 1;
+      mbar_wait_bounded(&full[s], ph, p.err);
+    }
     if (items > 0) mbar_wait_bounded(bar_q, (uint32_t)((items - 1) & 1), p.err);
   } else if (warp == 9) {
     // ----------------------------------------------------------- S and dP
-    int ns = 0, n = 0, items = 0;
-    for (int r = 0;; ++r) {
-      const Item it = list.get(r, more);
-      if (!more) break;
+    int ns = 0, n = 0, items = 0, ks = 0;
+    uint32_t kph = 0;
+    Item nx = list.get(0, more);
+    for (int r = 1; more; ++r) {
+      const Item it = nx;
+      nx = list.get(r, more);
       if (!it.ok || lane != 0) continue;
       wait_spin(bar_q, (uint32_t)(items++ & 1), dead, p.err);
       for (int t = 0; t <= it.level; ++t) {
         const int s = n & 1;
         const uint32_t ph = (uint32_t)((n >> 1) & 1);
-        wait_spin(&bar_kfull[s], ph, dead, p.err);
+        wait_spin(&bar_kfull[ks], kph, dead, p.err);
         // dQ += dS K of two tiles ago is done with the buffer
         if (n >= 2) wait_spin(&bar_g[s], ph ^ 1, dead, p.err);
         if (dead) break;
         tc_fence_after();
-        issue_tiles<D>(tmem + 128 * s, smem_addr(sq), smem_addr(sk(s)), C::kIdescS);
+        issue_tiles<D>(tmem + 128 * s, smem_addr(sq), smem_addr(sk(ks)), C::kIdescS);
         mma_commit(&bar_s[s]);
         ++ns;
+        if (++ks == 3) ks = 0, kph ^= 1;
         wait_spin(&bar_vfull[s], ph, dead, p.err);
         if (n > 0) wait_spin(bar_read, (uint32_t)((n - 1) & 1), dead, p.err);
         if (dead) break;
@@ -754,33 +810,41 @@ __global__ void __launch_bounds__(384, 1)
     if (n > 0) mbar_wait_bounded(bar_dp, (uint32_t)((n - 1) & 1), p.err);
   } else if (warp == 10) {
     // --------------------------------------------------------- dQ += dS K
-    int n = 0, items = 0;
-    for (int r = 0;; ++r) {
-      const Item it = list.get(r, more);
-      if (!more) break;
+    int n = 0, items = 0, ks = 0;
+    uint32_t kph = 0;
+    Item nx = list.get(0, more);
+    for (int r = 1; more; ++r) {
+      const Item it = nx;
+      nx = list.get(r, more);
       if (!it.ok) continue;
       for (int t = 0; t <= it.level; ++t) {
-        const int s = n & 1;
+        const int s = n & 1, rest = it.len - t * kTile;
+        if (lane == 0) wait_spin(&bar_kfull[ks], kph, dead, p.err);
+        if (rest < kTile) {
+          // (S is done with the rows: their columns of it are masked)
+          if (lane == 0) wait_spin(&bar_s[s], (uint32_t)((n >> 1) & 1), dead, p.err);
+          dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
+          if (dead) break;
+          clear_rows<D>(sk(ks), rest);
+        }
         if (lane == 0) {
-          wait_spin(&bar_kfull[s], (uint32_t)((n >> 1) & 1), dead, p.err);
           wait_spin(&bar_ds[s], (uint32_t)((n >> 1) & 1), dead, p.err);
           if (t == 0 && items > 0) wait_spin(bar_gfree, (uint32_t)((items - 1) & 1), dead, p.err);
         }
         dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
         if (dead) break;
-        const int rest = it.len - t * kTile;
-        if (rest < kTile) clear_rows<D>(sk(s), rest);
         if (lane == 0) {
           tc_fence_after();
-          const uint32_t k_addr = smem_addr(sk(s));
+          const uint32_t k_addr = smem_addr(sk(ks));
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
             mma_ts(tmem + kColG, tmem + 128 * s + 8 * kk + (kk >= 4 ? 32 : 0),
                    sw128_desc(k_addr + kk * 2048, kBox, 1024), C::kIdescG,
                    (t > 0 || kk > 0) ? 1u : 0u);
           mma_commit(&bar_g[s]);
-          mma_commit(&bar_kempty[s]);
+          mma_commit(&bar_kempty[ks]);
         }
+        if (++ks == 3) ks = 0, kph ^= 1;
         ++n;
       }
       ++items;
@@ -793,21 +857,48 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + col0, tG = tmem + lanes + kColG;
     const float sc = p.scale_log2;
-    unsigned char* box = smem + C::kOffStage + warp * C::kStage;
     float* trade = reinterpret_cast<float*>(smem + C::kOffTrade);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!dead) dead = !mbar_wait_bounded(bar, parity, p.err);
     };
     int n = 0;
-    for (int r = 0;; ++r) {
-      const Item it = list.get(r, more);
-      if (!more) break;
+    // An item's dQ is read and stored after the next one's first tile, during which its last
+    // product runs.
+    int old_first = 0, old_rows = 0, old_head = 0;  // of this warp's rows: the first, how many
+    auto store = [&]() {
+      const int last = n - 1;  // (called before the next tile is counted)
+      wait(&bar_g[last & 1], (uint32_t)((last >> 1) & 1));
+      tc_fence_after();
+      const int col = D == 128 ? col0 : 0;  // (head_dim 64: the first four warps store)
+      uint32_t o[2][32];
+      tmem_ld32_nowait(tG + col, o[0]);
+      tmem_ld32_nowait(tG + col + 32, o[1]);
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(bar_gfree);
+      if (D == 128 || half == 0)
+        put_rows(o[0], o[1], p.scale,
+                 const_cast<char*>(p.dq) +
+                     ((int64_t)old_first * p.sdq + (int64_t)old_head * D + col) * 2,
+                 p.sdq * 2, __ballot_sync(0xffffffffu, lane < old_rows));
+    };
+    float nl_next = 0.f, nd_next = 0.f;
+    auto load_stats = [&](const Item& it) {
+      const int q = it.level * kTile + row;
+      const int64_t stat = (int64_t)it.part * p.tokens + it.beg + q;
+      const bool live = it.ok && q < it.len;
+      nl_next = live ? -p.lse[stat] * kLog2e : 0.f;
+      nd_next = live ? -p.delta[stat] : 0.f;
+    };
+    Item nx = list.get(0, more);
+    load_stats(nx);
+    for (int r = 1; more; ++r) {
+      const Item it = nx;
+      const float nl = nl_next;
+      float nd = nd_next;
+      nx = list.get(r, more);
+      load_stats(nx);
       if (!it.ok) continue;
-      const int h = it.part, q0 = it.level * kTile;
-      const bool live = q0 + row < it.len;
-      const int64_t at = (int64_t)it.beg + q0 + row, stat = (int64_t)h * p.tokens + at;
-      const float nl = live ? -p.lse[stat] * kLog2e : 0.f;
-      float nd = live ? -p.delta[stat] : 0.f;
       for (int t = 0; t <= it.level; ++t, ++n) {
         uint32_t v[2][32], w[2][32];
         const int s = n & 1;
@@ -849,7 +940,7 @@ __global__ void __launch_bounds__(384, 1)
           named_bar(1 + (warp & 3), 64);
           if (half == 1) d = trade[row];
           nd = -d;
-          if (live && half == 0) p.delta[stat] = d;
+          if (half == 0 && row < it.len) p.delta[(int64_t)it.part * p.tokens + it.beg + row] = d;
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -879,22 +970,13 @@ __global__ void __launch_bounds__(384, 1)
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bar_ds[s]);
+        if (t == 0 && n > 0) store();
       }
-      wait(&bar_g[(n - 1) & 1], (uint32_t)(((n - 1) >> 1) & 1));
-      tc_fence_after();
-      const int col = D == 128 ? col0 : 0;  // (head_dim 64: the first four warps store)
-      uint32_t o[2][32];
-      tmem_ld32_nowait(tG + col, o[0]);
-      tmem_ld32_nowait(tG + col + 32, o[1]);
-      tmem_ld_wait();
-      tc_fence_before();
-      mbar_arrive(bar_gfree);
-      if (D == 128 || half == 0)
-        put_box(o[0], o[1], p.scale, box, &maps.out0, col, h, (int)at,
-                const_cast<char*>(p.dq) + (at * p.sdq + (int64_t)h * D + col) * 2,
-                __all_sync(0xffffffffu, live), live);
+      old_first = it.beg + it.level * kTile + 32 * (warp & 3);
+      old_rows = it.beg + it.len - old_first;
+      old_head = it.part;
     }
-    if (lane == 0) stores_done();
+    if (n > 0) store();
   }
   tc_fence_before();
   __syncthreads();
