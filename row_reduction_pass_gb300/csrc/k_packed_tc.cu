@@ -645,6 +645,11 @@ struct BwdMaps {
   CUtensorMap q, k, v, g, out0, out1;
 };
 
+// Bits n to 31 (all for n <= 0, none for n >= 32).
+__device__ __forceinline__ uint32_t bits_from(int n) {
+  return n >= 32 ? 0u : 0xffffffffu << max(n, 0);
+}
+
 // Rows [from, 128) of a tile in shared memory become zero (all lanes of a warp).
 template <int D>
 __device__ __forceinline__ void clear_rows(unsigned char* tile, int from) {
@@ -1152,12 +1157,20 @@ __global__ void __launch_bounds__(352, 1)
         if (lane == 0) {
           wait_spin(&bar_dofull[s], ph, dead, p.err);
           wait_spin(&bar_qfull[s], ph, dead, p.err);
+        }
+        if (rest < kTile) {
+          // (S^T and dP^T may be reading them: the columns that they give are masked)
+          dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
+          if (dead) break;
+          clear_rows<D>(sg(s), rest);
+          clear_rows<D>(sq(s), rest);
+        }
+        if (lane == 0) {
           wait_spin(&bar_p[s], ph, dead, p.err);
           if (t == 0 && items > 0) wait_spin(bar_gfree, (uint32_t)((items - 1) & 1), dead, p.err);
         }
         dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
         if (dead) break;
-        if (rest < kTile) clear_rows<D>(sg(s), rest);
         open = true;
         if (lane == 0) {
           sum(kColV, tW, sg(s));
@@ -1165,7 +1178,6 @@ __global__ void __launch_bounds__(352, 1)
         }
         dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
         if (dead) break;
-        if (rest < kTile) clear_rows<D>(sq(s), rest);
         if (lane == 0) {
           sum(kColK, tW + 32, sq(s));
           mma_commit(bar_g);
@@ -1207,6 +1219,10 @@ __global__ void __launch_bounds__(352, 1)
         // columns [lo, hi) of this thread's 64 see its key
         const int lo = i == first ? row - col0 : 0, hi = it.len - i * kTile - col0;
         const bool edge = i == first || it.len - i * kTile < kTile;
+        uint32_t sees[2];  // a bit for each
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          sees[c] = bits_from(lo - 32 * c) & ~bits_from(hi - 32 * c);
         wait(&bar_stat[s], (uint32_t)((n >> 1) & 1));
         wait(bar_s, (uint32_t)(n & 1));
         tc_fence_after();
@@ -1230,7 +1246,7 @@ __global__ void __launch_bounds__(352, 1)
           if (edge) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (32 * c + j < lo || 32 * c + j >= hi) v[c][j] = 0u;
+              if (!(sees[c] >> j & 1)) v[c][j] = 0u;
           }
 #pragma unroll
           for (int j = 0; j < 32; j += 2)
@@ -1266,7 +1282,7 @@ __global__ void __launch_bounds__(352, 1)
           if (edge) {  // (0 times a NaN)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (32 * c + j < lo || 32 * c + j >= hi) w[c][j] = 0u;
+              if (!(sees[c] >> j & 1)) w[c][j] = 0u;
           }
 #pragma unroll
           for (int j = 0; j < 32; j += 2)
