@@ -299,6 +299,11 @@ __device__ __noinline__ void repair_row(const PackedParams& p, int64_t begin, in
   for (int i = 0; i < D / 32; ++i) st_elem<kBF16>(o + 2 * (lane + 32 * i), acc[i] / l);
 }
 
+// Bits n to 31 (all for n <= 0, none for n >= 32).
+__device__ __forceinline__ uint32_t bits_from(int n) {
+  return n >= 32 ? 0u : 0xffffffffu << max(n, 0);
+}
+
 // D (+)= A B^T of two tiles in shared memory, A [128 x D], B [128 x D].
 template <int D>
 __device__ __forceinline__ void issue_tiles(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
@@ -460,6 +465,8 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + col0, tO = tmem + lanes + C::kColO;
     const float sc = p.scale_log2;
+    // the diagonal: a bit for each of this thread's keys that its row sees
+    const uint32_t sees[2] = {~bits_from(row + 1 - col0), ~bits_from(row - 31 - col0)};
     unsigned char* box = smem + C::kOffStage + warp * C::kStage;
     float* trade = reinterpret_cast<float*>(smem + C::kOffTrade);
     int swaps = 0;
@@ -491,7 +498,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (col0 + 32 * c + i > row) v[c][i] = __float_as_uint(-INFINITY);
+              if (!(sees[c] >> i & 1)) v[c][i] = __float_as_uint(-INFINITY);
         }
         float mx[8];
 #pragma unroll
@@ -644,11 +651,6 @@ struct Bwd {
 struct BwdMaps {
   CUtensorMap q, k, v, g, out0, out1;
 };
-
-// Bits n to 31 (all for n <= 0, none for n >= 32).
-__device__ __forceinline__ uint32_t bits_from(int n) {
-  return n >= 32 ? 0u : 0xffffffffu << max(n, 0);
-}
 
 // Rows [from, 128) of a tile in shared memory become zero (all lanes of a warp).
 template <int D>
@@ -826,8 +828,7 @@ __global__ void __launch_bounds__(384, 1)
         const int s = n & 1, rest = it.len - t * kTile;
         if (lane == 0) wait_spin(&bar_kfull[ks], kph, dead, p.err);
         if (rest < kTile) {
-          // (S is done with the rows: their columns of it are masked)
-          if (lane == 0) wait_spin(&bar_s[s], (uint32_t)((n >> 1) & 1), dead, p.err);
+          // (S may be reading them: the columns that they give are masked)
           dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
           if (dead) break;
           clear_rows<D>(sk(ks), rest);
@@ -862,6 +863,8 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + col0, tG = tmem + lanes + kColG;
     const float sc = p.scale_log2;
+    // the diagonal: a bit for each of this thread's keys that its row sees
+    const uint32_t sees[2] = {~bits_from(row + 1 - col0), ~bits_from(row - 31 - col0)};
     float* trade = reinterpret_cast<float*>(smem + C::kOffTrade);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!dead) dead = !mbar_wait_bounded(bar, parity, p.err);
@@ -937,7 +940,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (col0 + 32 * c + i <= row)
+              if (sees[c] >> i & 1)
                 d = fmaf(__uint_as_float(v[c][i]), __uint_as_float(w[c][i]), d);
           if (half == 1) trade[row] = d;
           named_bar(1 + (warp & 3), 64);
@@ -962,7 +965,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (col0 + 32 * c + i > row) w[c][i] = 0u;
+              if (!(sees[c] >> i & 1)) w[c][i] = 0u;
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
