@@ -7,7 +7,8 @@
 // with the running maximum and sum of the online softmax, O += P V.  With S two tiles ahead
 // the softmax always finds its next tile, and the tensor cores have two products that do not
 // depend on each other: a product of 128 x 128 x 16 takes 85 to 130 cycles alone and 66 beside
-// another.  16000 tokens, 32 heads on 8, head_dim 128, one sequence: 256 us, 1370 TFLOP/s.  (Two
+// another.  16000 tokens in 4 sequences, 32 heads on 8, head_dim 128:
+// 249 us, 1405 TFLOP/s.  (Two
 // tiles of 128 rows a block, which share the loaded keys but leave TMEM for one S each, took
 // 384 us, S, softmax and O += P V one after the other; with their scores in two buffers of 64
 // keys 344 us: an S of 64 keys takes as long as one of 128.)
@@ -613,22 +614,35 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 // ------------------------------------------------------------------ backward ---
-// Two kernels, so that every sum has one owner and a fixed order (S and dP are computed in
-// both): dQ by query tiles, dK and dV by key tiles, the latter transposed, so that all three
-// are products of a weight matrix in TMEM with a tile in shared memory, as O = P V is.
-// delta = sum dO o of each row comes from a kernel before them.
+// Three kernels, so that every sum has one owner and a fixed order (S and dP are computed in
+// both of the last two): delta = sum dO o of each row; dQ by query tiles; dK and dV by key
+// tiles, transposed, so that all three are products of a weight matrix in TMEM with a tile in
+// shared memory, as O = P V is.
 //
-// A block has eight softmax warps, two to a quarter of the 128 TMEM lanes, with 64 of the
-// tile's 128 columns each; warp 8 loads, warps 9 and 10 issue.
+// A block of the two has eight softmax warps, two to a quarter of the 128 TMEM lanes, with 64
+// of the tile's 128 columns each; warp 8 loads (V in dQ: warp 11),
+// warps 9 and 10 issue.
 //
 // dQ, a query tile against key tiles t: S(t) = Q K^T, dP(t) = dO V^T, then
-//   dS = P (dP - delta) as bf16 over S, dQ += dS K.  S has two buffers, so that S and dP of
-//   t + 1 run while the softmax works on t.
+//   dS = P (dP - delta) as bf16 over S, dQ += dS K.  S has two buffers and K three stages, so
+//   that S and dP of t + 1 run while the softmax works on t.  dQ is read and stored after the
+//   next item's first tile, while which its last product runs.
 // dK and dV, a key tile against the query tiles of all heads of its group, in two TMEM buffers
 //   X and Y that change places with each tile: S^T = K Q^T in X, dP^T = V dO^T in Y; P^T and
 //   dS^T, bf16, over S^T in X; dV += P^T dO, dK += dS^T Q.  Y is free once dP^T is read, so S^T
 //   of the next tile and dV run while the softmax goes on to dS^T; the next dP^T, into X, while
 //   it works on the next P^T.
+//
+// What bounds them: the chain from one tile's weights over the product that reads them to the
+// next tile's scores.  A product of 128 x 128 x 128 takes 690 cycles with both operands in
+// shared memory and 1090 with one in TMEM when it runs alone, 530 in company; the two kernels
+// come to 2450 and 3200 cycles a tile of three and four products.  8192 tokens in 5 sequences,
+// 32 heads on 8, head_dim 128: 24 + 110 + 171 us, 669 TFLOP/s of the five products' counted
+// work (dQ, dK, dV, S, dP); 4097 tokens in 12, 12 on 4, head_dim 64: 3 + 17 + 33 us.  Tried
+// and no faster: delta's sums of dO o inside its kernel (from a tile of o: 144 us
+// instead of 24 + 110); lse and delta as further terms of the products instead of 32 loads
+// from shared memory a tile (201 instead of 190 us then); sixteen softmax warps (172); a buffer
+// more for dP^T with head_dim 64 (32 of 33 us).
 //
 // Rows of a tile beyond its sequence are masked, and where such a row is summed over (K in
 // dQ; Q and dO in dK, dV) it is set to zero in shared memory before the product, so that no

@@ -355,7 +355,6 @@ struct LogprobParams {
   int32_t* top_index;     // [rows][k]
   float* top_logprob;     // [rows][k]
   int32_t* bad;           // counter of tokens out of range, or null
-  int* err;
   int64_t rows, cols, stride;
   int32_t k, ignore;
   float temperature, c;   // c = log2 e / temperature

@@ -221,7 +221,7 @@ def check_attention(lens, H, KV, D, dtype, seed=0, first=0, tail=0, scale=None, 
     G = H // KV
     for name, b, w, m, terms in (("dq", dq, wq, mq, n), ("dk", dk, wk, mk, n * G),
                                  ("dv", dv, wv, mv, n * G)):
-        # (a row's dP and delta are sums of D terms of magnitude |dout v| <= mag / EPS-free part)
+        # (S, dP and delta are sums of D terms each, rounded by EPS a term and exponential)
         rel = 8 * (D * (worst + 4) + 64 + terms) * EPS + HALF[dt] if fine else 2.0 ** -7
         close(name, b.view[inside.cuda()], w[inside], m[inside], rel, HALF[dt], floor=1e-6)
         assert bool((b.view[out.cuda()] == 7.0).all()), name
@@ -423,6 +423,13 @@ def test_logprob_temperatures(T, dtype):
     close("logprob", lp, want["logprob"], 1 + want["log_sum"], 64 * EPS, EPS)
     assert bool(torch.isfinite(ent).all())
     close("entropy", ent, want["entropy"], 1 + want["ent"], 256 * EPS, EPS)
+
+
+@pytest.mark.parametrize("rows,cols,dtype,k,gap,pad", [
+    (12, 33000, "bf16", 128, 0, 0), (200, 33001, "bf16", 20, 3, 1), (14, 40001, "f32", 5, 3, 1),
+    (9, 270001, "f32", 33, 5, 3), (12, 270000, "bf16", 100, 0, 1), (13, 262144, "bf16", 0, 8, 0)])
+def test_logprob_rows_over_several_blocks(rows, cols, dtype, k, gap, pad):
+    check_logprob(rows, cols, dtype, k, T=0.9, seed=rows, gap=gap, pad=pad)
 
 
 def test_logprob_more_rows_than_blocks():
