@@ -264,6 +264,13 @@ def test_attention_many_sequences(D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+def test_attention_more_tiles_than_blocks(D):
+    """Several tiles a block, of differing lengths: forward, dq and dk, dv."""
+    check_attention([700, 333, 129, 257, 90, 1, 0, 128], 32, 32, D, "bf16", seed=7)
+    check_attention([37 * i % 300 for i in range(140)], 4, 2, D, "bf16", seed=8)
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_attention_unseen_values_change_nothing(D):
     """NaN and infinities in the keys and values of later tokens, and of the sequences
     beside it, leave a token's output as it is."""
