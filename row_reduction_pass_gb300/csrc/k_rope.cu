@@ -23,7 +23,13 @@ namespace rr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFwdU = 2, kBwdU = 2, kFwdBlocks = 4, kBwdBlocks = 2;
+// Row groups in flight a warp, and blocks an SM.  Memory bounds both kernels (the forward reads
+// and writes each row once, the backward reads two and writes one); what they lack is bytes
+// under way, which cost registers.  16384 tokens, bf16, 32 + 8 heads of 128 read and written by
+// the forward: 60 us with 2 and 3, 5690 GB/s (2 and 4: 70, 3 and 3: 66, 1 and 5: 87; each row's
+// loads issued before the one before it is worked on, 83); backward 105 us, 4870 GB/s, with 2
+// and 2 (2 and 3: 137, 3 and 2: 113; likewise 149).
+constexpr int kFwdU = 2, kBwdU = 2, kFwdBlocks = 3, kBwdBlocks = 2;
 
 // What a lane keeps of the row's layout: element offsets of its slots.
 template <int W, int NS>
@@ -80,6 +86,56 @@ __device__ __forceinline__ void store(char* p, const float (&f)[W]) {
     *reinterpret_cast<uint4*>(p) = chunk_pack<DT>(f);
 }
 
+// Element by element, two at a time where there are two (half of the kernels' instructions
+// are these): x *= y, x *= f, d += the sum of x y, d += x y, d += x f.
+template <int W>
+__device__ __forceinline__ void times(float (&x)[W], const float (&y)[W]) {
+  if constexpr (W == 1) {
+    x[0] *= y[0];
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; e += 2) mul2(x[e], x[e + 1], x[e], x[e + 1], y[e], y[e + 1]);
+  }
+}
+template <int W>
+__device__ __forceinline__ void times(float (&x)[W], float f) {
+  if constexpr (W == 1) {
+    x[0] *= f;
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; e += 2) mul2(x[e], x[e + 1], x[e], x[e + 1], f, f);
+  }
+}
+template <int W>
+__device__ __forceinline__ void add_to(float (&d)[2], const float (&x)[W], const float (&y)[W]) {
+  if constexpr (W == 1) {
+    d[0] += x[0] * y[0];
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; e += 2)
+      fma2(d[0], d[1], x[e], x[e + 1], y[e], y[e + 1], d[0], d[1]);
+  }
+}
+template <int W>
+__device__ __forceinline__ void add_each(float (&d)[W], const float (&x)[W], const float (&y)[W]) {
+  if constexpr (W == 1) {
+    d[0] += x[0] * y[0];
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; e += 2)
+      fma2(d[e], d[e + 1], x[e], x[e + 1], y[e], y[e + 1], d[e], d[e + 1]);
+  }
+}
+template <int W>
+__device__ __forceinline__ void plus(float (&d)[W], const float (&x)[W], float f) {
+  if constexpr (W == 1) {
+    d[0] += x[0] * f;
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; e += 2) fma2(d[e], d[e + 1], x[e], x[e + 1], f, f, d[e], d[e + 1]);
+  }
+}
+
 // Turns the slot's pairs by (c, s).
 template <int W>
 __device__ __forceinline__ void turn(float (&a)[W], float (&b)[W], const float (&c)[W],
@@ -96,12 +152,18 @@ __device__ __forceinline__ void turn(float (&a)[W], float (&b)[W], const float (
     }
 #pragma unroll
     for (int i = 0; i < W; ++i) a[i] = u[i], b[i] = u[W + i];
+  } else if constexpr (W == 1) {
+    const float x = a[0], y = b[0];
+    a[0] = c[0] * x - s[0] * y;
+    b[0] = s[0] * x + c[0] * y;
   } else {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float x = a[i], y = b[i];
-      a[i] = c[i] * x - s[i] * y;
-      b[i] = s[i] * x + c[i] * y;
+    for (int i = 0; i < W; i += 2) {
+      float t0, t1, u0, u1;
+      mul2(t0, t1, s[i], s[i + 1], b[i], b[i + 1]);
+      mul2(u0, u1, s[i], s[i + 1], a[i], a[i + 1]);
+      fma2(a[i], a[i + 1], c[i], c[i + 1], a[i], a[i + 1], -t0, -t1);
+      fma2(b[i], b[i + 1], c[i], c[i + 1], b[i], b[i + 1], u0, u1);
     }
   }
 }
@@ -154,7 +216,7 @@ __device__ __forceinline__ Unit unit_of(const RopeParams& p, int64_t u) {
   x.isq = u < nq;
   const int segs = x.isq ? p.q_segs : p.k_segs, rows = x.isq ? p.q_rows : p.k_rows;
   const int64_t v = x.isq ? u : u - nq;
-  x.t = v / segs;
+  x.t = v <= 0xffffffffll ? (uint32_t)v / (uint32_t)segs : v / segs;
   x.first = (int)(v - x.t * segs) * rows;
   x.last = min(x.isq ? p.heads : p.kv_heads, x.first + rows);
   return x;
@@ -233,14 +295,14 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks) rope_fwd_kernel(const Ro
       for (int k = 0; k < U; ++k) {
         const int h = r0 + k * per + sub;
         if (r0 + k * per >= now.last) break;
-        float a[NS][W], b[NS][W], ss = 0.f;
+        float a[NS][W], b[NS][W], ss[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           raw[k][i].get(a[i], b[i]);
-#pragma unroll
-          for (int e = 0; e < W; ++e) ss += a[i][e] * a[i][e] + b[i][e] * b[i][e];
+          add_to<W>(ss, a[i], a[i]);
+          add_to<W>(ss, b[i], b[i]);
         }
-        const float ms = group_sum(ss, p.group) * p.inv_dim;
+        const float ms = group_sum(ss[0] + ss[1], p.group) * p.inv_dim;
         const bool keep = at >= 0 && ms <= 3.402823466e38f && ms + p.eps > 0.f;
         const float r = keep ? rsqrtf(ms + p.eps) : 0.f;
         if (h >= now.last) continue;
@@ -249,15 +311,15 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks) rope_fwd_kernel(const Ro
         for (int i = 0; i < NS; ++i) {
           if (!sl.on[i]) continue;
           if (keep) {
-            float wa[W], wb[W];
-#pragma unroll
-            for (int e = 0; e < W; ++e) wa[e] = wb[e] = 1.f;
+            times<W>(a[i], r);
+            times<W>(b[i], r);
             if (w) {
-              load_cached<DT, W>(wa, w + sl.ea[i] * E);
-              load_cached<DT, W>(wb, w + sl.eb[i] * E);
+              float wi[W];
+              load_cached<DT, W>(wi, w + sl.ea[i] * E);
+              times<W>(a[i], wi);
+              load_cached<DT, W>(wi, w + sl.eb[i] * E);
+              times<W>(b[i], wi);
             }
-#pragma unroll
-            for (int e = 0; e < W; ++e) a[i][e] *= r * wa[e], b[i][e] *= r * wb[e];
             turn<W>(a[i], b[i], c[i], s[i], p.interleaved);
           } else {
 #pragma unroll
@@ -355,17 +417,16 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) rope_bwd_kernel(const Ro
         const int h = r0 + k * per + sub;
         if (r0 + k * per >= now.last) break;
         const bool live = h < now.last;
-        float a[NS][W], b[NS][W], ga[NS][W], gb[NS][W], ss = 0.f;
+        float a[NS][W], b[NS][W], ga[NS][W], gb[NS][W], ss[2] = {0.f, 0.f}, dot[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           rx[k][i].get(a[i], b[i]);
-#pragma unroll
-          for (int e = 0; e < W; ++e) ss += a[i][e] * a[i][e] + b[i][e] * b[i][e];
+          add_to<W>(ss, a[i], a[i]);
+          add_to<W>(ss, b[i], b[i]);
         }
-        const float ms = group_sum(ss, p.group) * p.inv_dim;
+        const float ms = group_sum(ss[0] + ss[1], p.group) * p.inv_dim;
         const bool keep = at >= 0 && ms <= 3.402823466e38f && ms + p.eps > 0.f;
         const float r = keep ? rsqrtf(ms + p.eps) : 0.f;
-        float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           rg[k][i].get(ga[i], gb[i]);
@@ -377,28 +438,34 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) rope_bwd_kernel(const Ro
             load_cached<DT, W>(wa, w + sl.ea[i] * E);
             load_cached<DT, W>(wb, w + sl.eb[i] * E);
           }
-#pragma unroll
-          for (int e = 0; e < W; ++e) {
-            a[i][e] *= r, b[i][e] *= r;
-            const float da = ga[i][e] * a[i][e], db = gb[i][e] * b[i][e];
-            if (keep && live) acc[i][0][e] += da, acc[i][1][e] += db;
-            dot += da * wa[e] + db * wb[e];
-            ga[i][e] *= wa[e], gb[i][e] *= wb[e];
+          times<W>(a[i], r);
+          times<W>(b[i], r);
+          if (keep && live) {
+            add_each<W>(acc[i][0], ga[i], a[i]);
+            add_each<W>(acc[i][1], gb[i], b[i]);
           }
+          times<W>(ga[i], wa);
+          times<W>(gb[i], wb);
+          add_to<W>(dot, ga[i], a[i]);
+          add_to<W>(dot, gb[i], b[i]);
         }
-        const float mean = group_sum(dot, p.group) * p.inv_dim;
+        const float mean = group_sum(dot[0] + dot[1], p.group) * p.inv_dim;
         if (!live) continue;
         char* dx = out + (int64_t)h * p.dim * E;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           if (!sl.on[i]) continue;
+          if (keep) {
+            plus<W>(ga[i], a[i], -mean);
+            plus<W>(gb[i], b[i], -mean);
+            times<W>(ga[i], r);
+            times<W>(gb[i], r);
+          } else {
 #pragma unroll
-          for (int e = 0; e < W; ++e) {
-            a[i][e] = keep ? r * (ga[i][e] - a[i][e] * mean) : 0.f;
-            b[i][e] = keep ? r * (gb[i][e] - b[i][e] * mean) : 0.f;
+            for (int e = 0; e < W; ++e) ga[i][e] = gb[i][e] = 0.f;
           }
-          store<DT, W>(dx + sl.ea[i] * E, a[i]);
-          store<DT, W>(dx + sl.eb[i] * E, b[i]);
+          store<DT, W>(dx + sl.ea[i] * E, ga[i]);
+          store<DT, W>(dx + sl.eb[i] * E, gb[i]);
         }
       }
     }

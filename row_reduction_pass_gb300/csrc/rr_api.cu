@@ -2433,7 +2433,7 @@ void rope_units(rr::RopeParams& p, int64_t warps) {
   cut(p.kv_heads, cdiv(want * p.kv_heads, all), &p.k_segs, &p.k_rows);
 }
 
-constexpr int kRopeBwdBlocks = 2;  // a SM
+constexpr int kRopeFwdBlocks = 3, kRopeBwdBlocks = 2;  // a SM
 
 }  // namespace
 
@@ -2511,8 +2511,8 @@ rr_status rr_qk_norm_rope_fwd(const void* q, const void* k, const void* q_weight
   if ((st = rope_plan(p, dtype, eps, strides, kv_heads > 0 ? 4 : 2, tensors, &pl)) != RR_OK)
     return st;
   const int wpb = pl.k.threads / 32;
-  rope_units(p, (int64_t)pl.sms * 8 * wpb);
-  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * (p.q_segs + p.k_segs), wpb), (int64_t)pl.sms * 8);
+  rope_units(p, (int64_t)pl.sms * kRopeFwdBlocks * wpb);
+  const int64_t grid = std::min<int64_t>(cdiv(p.tokens * (p.q_segs + p.k_segs), wpb), (int64_t)pl.sms * kRopeFwdBlocks);
   void* args[] = {&p};
   cudaError_t e = cudaLaunchKernel(pl.k.fwd, dim3((unsigned)grid), dim3((unsigned)pl.k.threads),
                                    args, 0, stream);
