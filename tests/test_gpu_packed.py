@@ -10,8 +10,9 @@ storage type, relative):
   attention, float32 kernels: a score's error is dim EPS times scale sum |q k| (the plain form
     returns the largest of a row), a weight's relative error that plus 16 EPS, and a sum over
     n keys adds n EPS; on the tensor cores (bf16): products are exact, weights and ds are
-    rounded (2^-9), and so is the result (2^-9); delta carries the rounding of o (2^-9 of
-    sum |dout o|).  Twice these sums is allowed, as the float32 errors are far below them.
+    rounded (at most 2^-8 each), and so is the result (2^-8); delta carries the rounding of o
+    (2^-8 of sum |dout o|).  2^-7 of the magnitudes is allowed beside the result's own
+    rounding, as the float32 errors are far below.
   log probabilities: an exponential carries (|z| + 4) EPS, sums over a row some tens, the
     logarithm as much: 64 EPS of the magnitudes that the plain form returns.
 Whole numbers are equal.
