@@ -7,11 +7,10 @@
 // with the running maximum and sum of the online softmax, O += P V.  With S two tiles ahead
 // the softmax always finds its next tile, and the tensor cores have two products that do not
 // depend on each other: a product of 128 x 128 x 16 takes 85 to 130 cycles alone and 66 beside
-// another.  16000 tokens in 4 sequences, 32 heads on 8, head_dim 128:
-// 249 us, 1405 TFLOP/s.  (Two
-// tiles of 128 rows a block, which share the loaded keys but leave TMEM for one S each, took
-// 384 us, S, softmax and O += P V one after the other; with their scores in two buffers of 64
-// keys 344 us: an S of 64 keys takes as long as one of 128.)
+// another.  Sequences of 5117, 0, 1 and 4077 tokens, 32 heads on 8, head_dim 128: 249 us, 1405
+// TFLOP/s.  (Two tiles of 128 rows a block, which share the loaded keys but leave TMEM for one S
+// each, took 384 us, S, softmax and O += P V one after the other; with their scores in two
+// buffers of 64 keys 344 us: an S of 64 keys takes as long as one of 128.)
 //   TMEM: S (3 x 128 columns, P over the first half of each half) and O (D columns).
 // Roles: warps 0-7 softmax (two to a quarter of the lanes), warp 8 loads Q and K (TMA), warp 11
 // loads V, warps 9 and 10 issue S and O += P V.
@@ -636,13 +635,12 @@ __global__ void __launch_bounds__(384, 1)
 // What bounds them: the chain from one tile's weights over the product that reads them to the
 // next tile's scores.  A product of 128 x 128 x 128 takes 690 cycles with both operands in
 // shared memory and 1090 with one in TMEM when it runs alone, 530 in company; the two kernels
-// come to 2450 and 3200 cycles a tile of three and four products.  8192 tokens in 5 sequences,
-// 32 heads on 8, head_dim 128: 24 + 110 + 171 us, 669 TFLOP/s of the five products' counted
-// work (dQ, dK, dV, S, dP); 4097 tokens in 12, 12 on 4, head_dim 64: 3 + 17 + 33 us.  Tried
-// and no faster: delta's sums of dO o inside its kernel (from a tile of o: 144 us
-// instead of 24 + 110); lse and delta as further terms of the products instead of 32 loads
-// from shared memory a tile (201 instead of 190 us then); sixteen softmax warps (172); a buffer
-// more for dP^T with head_dim 64 (32 of 33 us).
+// come to 2450 and 3200 cycles a tile of three and four products.  Sequences of 2414, 0, 1,
+// 1924 and 639 tokens, 32 heads on 8, head_dim 128: 15 + 110 + 171 us; twelve of 0 to 603
+// tokens, 12 heads on 4, head_dim 64: 3 + 17 + 33 us.  Tried and no faster: delta inside dQ's
+// kernel, from a tile of o (144 us instead of 24 + 110); lse and delta as further terms of the
+// products instead of 32 loads from shared memory a tile (201 instead of 190 us then); sixteen
+// softmax warps (172); a buffer more for dP^T with head_dim 64 (32 of 33 us).
 //
 // Rows of a tile beyond its sequence are masked, and where such a row is summed over (K in
 // dQ; Q and dO in dK, dV) it is set to zero in shared memory before the product, so that no
@@ -678,25 +676,35 @@ __device__ __forceinline__ void clear_rows(unsigned char* tile, int from) {
   __syncwarp();
 }
 
-// delta of every row of every head: a group of D / 8 lanes a row.
+// delta of the rows within the sequences: a warp a token, D / 8 lanes a head, four heads of
+// each under way.
 template <int D>
 __global__ void __launch_bounds__(256) packed_delta_kernel(const PackedParams p) {
-  constexpr int G = D / 8, R = 32 / G;
-  const int lane = threadIdx.x & 31, gl = lane % G;
-  const int64_t rows = p.tokens * p.heads;
-  const int64_t row = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * R + lane / G;
-  const int64_t t = row / p.heads;
-  const int h = (int)(row - t * p.heads);
-  float s = 0.f;
-  if (row < rows) {
-    const uint4 a = ld_chunk_cached(p.dout + (t * p.sdo + (int64_t)h * D + gl * 8) * 2);
-    const uint4 b = ld_chunk_cached(p.o + (t * p.so + (int64_t)h * D + gl * 8) * 2);
+  constexpr int G = D / 8, R = 32 / G, U = 4;
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t >= p.tokens || t < __ldg(p.cu) || t >= __ldg(p.cu + p.batch)) return;
+  const char* g = p.dout + (t * p.sdo + lane % G * 8) * 2;
+  const char* o = p.o + (t * p.so + lane % G * 8) * 2;
+  for (int h0 = lane / G; h0 - lane / G < p.heads; h0 += R * U) {
+    uint4 a[U], b[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s += chunk_get<kBF16>(a, e) * chunk_get<kBF16>(b, e);
+    for (int k = 0; k < U; ++k) {
+      const int h = min(h0 + k * R, p.heads - 1);
+      a[k] = ld_chunk_cached(g + (int64_t)h * D * 2);
+      b[k] = ld_chunk_cached(o + (int64_t)h * D * 2);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += chunk_get<kBF16>(a[k], e) * chunk_get<kBF16>(b[k], e);
+#pragma unroll
+      for (int off = G / 2; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+      const int h = h0 + k * R;
+      if (h < p.heads && lane % G == 0) p.delta[(int64_t)h * p.tokens + t] = s;
+    }
   }
-#pragma unroll
-  for (int off = G / 2; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  if (row < rows && gl == 0) p.delta[(int64_t)h * p.tokens + t] = s;
 }
 
 template <int D>
@@ -1415,9 +1423,8 @@ const char* packed_tc_bwd_launch(const PackedParams& p, int sms, cudaStream_t st
     return "tensor map encoding failed";
   mq.out1 = mq.out0;
   PackedParams pc = p;
-  const int64_t rows = p.tokens * p.heads, per = 8 * (32 / (p.dim / 8));
   void* dargs[] = {&pc};
-  if (cudaLaunchKernel(k.delta, dim3((unsigned)((rows + per - 1) / per)), dim3(256), dargs, 0,
+  if (cudaLaunchKernel(k.delta, dim3((unsigned)((p.tokens + 7) / 8)), dim3(256), dargs, 0,
                        stream) != cudaSuccess)
     return "launch failed";
   const int64_t levels = p.tokens / kTile + p.batch;
