@@ -27,7 +27,7 @@ constexpr int kThreads = 256;
 // and writes each row once, the backward reads two and writes one); what they lack is bytes
 // under way, which cost registers.  16384 tokens, bf16, 32 + 8 heads of 128 read and written by
 // the forward: 60 us with 2 and 3, 5690 GB/s (2 and 4: 70, 3 and 3: 66, 1 and 5: 87; each row's
-// loads issued before the one before it is worked on, 83); backward 105 us, 4870 GB/s, with 2
+// loads issued before the one before it is worked on, 83); backward 103 us, 4960 GB/s, with 2
 // and 2 (2 and 3: 137, 3 and 2: 113; likewise 149).
 constexpr int kFwdU = 2, kBwdU = 2, kFwdBlocks = 3, kBwdBlocks = 2;
 
@@ -335,12 +335,13 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks) rope_fwd_kernel(const Ro
 }
 
 // dx of every row, and this block's sums over its rows of g x r for the two weights, in
-// workspace row blockIdx.x ([2][D] floats), which col_reduce_kernel adds up.  A warp's rows
+// workspace row blockIdx.x ([2][D] floats), which rope_join_kernel adds up.  A warp's rows
 // are queries first, then keys: one set of sums, put aside between the two.
 template <int DT, int W, int NS, int U>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks) rope_bwd_kernel(const RopeParams p) {
   constexpr int E = DType<DT>::E;
   extern __shared__ float part[];  // [warps][2][D]
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the join may come)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gl = lane & (p.group - 1), sub = lane / p.group, per = 32 / p.group;
   const Slots<W, NS> sl(gl, p);
@@ -481,14 +482,45 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) rope_bwd_kernel(const Ro
   }
 }
 
+// The weights' gradients: column k of the `rows` sums, a warp a slice of the rows for 32
+// columns, the slices in order.  Launched beside the kernel above, whose end it waits for (1999
+// tokens, fp32, 16 + 4 heads of 64: 10.9 us in all; 12.0 as a launch after it).
+template <int DT>
+__global__ void __launch_bounds__(1024) rope_join_kernel(const float* ws, int rows, int dim,
+                                                         char* dqw, char* dkw) {
+  __shared__ float part[32][33];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, k = blockIdx.x * 32 + lane;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float s = 0.f;
+  if (k < 2 * dim) {
+    int r = slice;
+    for (; r + 128 < rows; r += 160) {
+      float a[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) a[i] = __ldcs(ws + (int64_t)(r + 32 * i) * 2 * dim + k);
+#pragma unroll
+      for (int i = 0; i < 5; ++i) s += a[i];
+    }
+    for (; r < rows; r += 32) s += __ldcs(ws + (int64_t)r * 2 * dim + k);
+  }
+  part[slice][lane] = s;
+  __syncthreads();
+  if (slice > 0 || k >= 2 * dim) return;
+  float t = part[0][lane];
+  for (int i = 1; i < 32; ++i) t += part[i][lane];
+  st_elem<DT>((k < dim ? dqw : dkw - (int64_t)dim * DType<DT>::E) + (int64_t)k * DType<DT>::E, t);
+}
+
 }  // namespace
 
 template <int DT, int W>
 static RopeKernels kernels_of(bool vec) {
   return vec ? RopeKernels{(const void*)rope_fwd_kernel<DT, W, 1, kFwdU>,
-                           (const void*)rope_bwd_kernel<DT, W, 1, kBwdU>, kThreads}
+                           (const void*)rope_bwd_kernel<DT, W, 1, kBwdU>,
+                           (const void*)rope_join_kernel<DT>, kThreads}
              : RopeKernels{(const void*)rope_fwd_kernel<DT, 1, 4, 1>,
-                           (const void*)rope_bwd_kernel<DT, 1, 4, 1>, kThreads};
+                           (const void*)rope_bwd_kernel<DT, 1, 4, 1>,
+                           (const void*)rope_join_kernel<DT>, kThreads};
 }
 RopeKernels rope_kernels(int dtype, bool vec) {
   return dtype == kF32 ? kernels_of<kF32, 4>(vec) : kernels_of<kBF16, 8>(vec);

@@ -2631,15 +2631,21 @@ rr_status rr_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void
                        (size_t)wpb * 2 * p.dim * 4, stream);
   if (e != cudaSuccess) return fail(RR_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
   if (p.ws) {
-    const void* cr =
-        dtype == RR_BF16 ? rr::col_reduce_kernel_ptr_bf16() : rr::col_reduce_kernel_ptr_f32();
     const float* ws = p.ws;
-    int64_t P = grid, cols = head_dim, planes = 2;
-    char *dw = static_cast<char*>(dq_weight), *dk_w = static_cast<char*>(dk_weight);
-    void* cargs[] = {&ws, &P, &cols, &planes, &dw, &dk_w};
-    e = cudaLaunchKernel(cr, dim3((unsigned)cdiv(2 * cols, 32 * (32 / rr::col_reduce_split(P)))),
-                         dim3(1024), cargs, 0, stream);
-    if (e != cudaSuccess) return fail(RR_ERR_CUDA, "column reduce launch: %s", cudaGetErrorString(e));
+    int rows = (int)grid, dim = p.dim;
+    char *dqw = static_cast<char*>(dq_weight), *dkw = static_cast<char*>(dk_weight);
+    void* jargs[] = {&ws, &rows, &dim, &dqw, &dkw};
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)cdiv(2 * dim, 32));
+    cfg.blockDim = dim3(1024);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelExC(&cfg, pl.k.join, jargs);
+    if (e != cudaSuccess) return fail(RR_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
   }
   return ok();
 }

@@ -339,8 +339,8 @@ struct RopeParams {
   float eps, inv_dim;
 };
 struct RopeKernels {
-  const void *fwd, *bwd;
-  int threads;
+  const void *fwd, *bwd, *join;  // join: (sums, their rows, dim, two outputs), 32 columns a block
+  int threads;                   // of the first two
 };
 // vec: slots of two 16-byte chunks, a row on up to 32 lanes; else of two elements.
 RopeKernels rope_kernels(int dtype, bool vec);
