@@ -549,8 +549,9 @@ size_t rr_attention_packed_bwd_workspace_size(int64_t tokens, int64_t heads);
  *           that may overlap on the GPU need one each.
  * Rows outside every sequence are left as they were, and nothing there or in another
  * sequence changes a sequence's gradients.  Every sum has a fixed order (the same bits at
- * every run).  On the tensor cores p and ds are rounded to bf16 for their products.  A NaN
- * or infinity in a sequence may reach any gradient of that sequence.
+ * every run).  On the tensor cores p and ds are rounded to bf16 for their products, and delta
+ * of a sequence's first 128 tokens is sum_j p (dout . v_j), the same number without o's
+ * rounding.  A NaN or infinity in a sequence may reach any gradient of that sequence.
  */
 rr_status rr_attention_packed_bwd(const void *dout, const void *q, const void *k, const void *v,
                                   const void *o, const float *lse, const int32_t *cu_seqlens,
