@@ -143,11 +143,16 @@ static int truth(Call *c, PyObject *o) {
     if (v < 0) c->bad = 1;
     return v;
 }
-static int64_t whole(Call *c, PyObject *o) {
+static int32_t whole(Call *c, const char *name, PyObject *o) {
     if (c->bad) return 0;
     const int64_t v = PyLong_AsLongLong(o);
-    if (v == -1 && PyErr_Occurred()) c->bad = 1;
-    return v;
+    if (v == -1 && PyErr_Occurred()) {
+        c->bad = 1;
+    } else if (v < INT32_MIN || v > INT32_MAX) {
+        PyErr_Format(PyExc_ValueError, "%s: %s must fit 32 bits", c->fn, name);
+        c->bad = 1;
+    }
+    return (int32_t)v;
 }
 /* A workspace: its address and bytes (numel x element_size; uint8 in practice). */
 static void *workspace(Call *c, PyObject *t, size_t *bytes) {
@@ -342,7 +347,7 @@ static PyObject *logprob_fwd(PyObject *self, PyObject *const *a, Py_ssize_t na) 
         return NULL;
     }
     const float T = (float)number(&c, a[9]);
-    const int32_t ignore = (int32_t)whole(&c, a[10]);
+    const int32_t ignore = whole(&c, "ignore_index", a[10]);
     const Tensor bad = tensor(&c, "bad_token_count", a[11], i32, 1, one, 0);
     void *s = stream_of(&c, a[12]);
     if (c.bad) return NULL;
@@ -370,7 +375,7 @@ static PyObject *logprob_bwd(PyObject *self, PyObject *const *a, Py_ssize_t na) 
     const Tensor en = tensor(&c, "entropy", a[6], f32, 1, n, 0);
     const Tensor h = tensor(&c, "grad_entropy", a[7], f32, 1, n, 0);
     const float T = (float)number(&c, a[8]);
-    const int32_t ignore = (int32_t)whole(&c, a[9]);
+    const int32_t ignore = whole(&c, "ignore_index", a[9]);
     void *s = stream_of(&c, a[10]);
     if (c.bad) return NULL;
     const int r = ((int (*)(void *, void *, void *, void *, void *, void *, void *, void *, int64_t,

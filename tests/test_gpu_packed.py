@@ -576,3 +576,13 @@ def test_binding_refusals():
                                                                 device="cuda"))
     with pytest.raises(rr.RRError):
         rr.rr_token_logprob_fwd(x, t, lp, temperature=0.0)
+
+
+@pytest.mark.parametrize("index", [2 ** 31, -2 ** 31 - 1, 2 ** 32 - 100])
+def test_binding_refuses_an_ignore_index_beyond_32_bits(index):
+    x, t = torch.zeros(2, 9, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    f = [torch.zeros(2, device="cuda") for _ in range(3)]
+    with pytest.raises(ValueError):
+        rr.rr_token_logprob_fwd(x, t, f[0], ignore_index=index)
+    with pytest.raises(ValueError):
+        rr.rr_token_logprob_bwd(x, t, *f, x, ignore_index=index)
