@@ -80,7 +80,7 @@ struct Item {
 struct Sequences {
   int2* seq;       // shared: (begin, length) of the live sequences, longest first
   const int* cu;
-  int n, batch, tokens, rows, parts, entries;
+  int n, batch, tokens, rows, parts, entries, me;
   int lv[kSorted / 32];  // levels of sequences lane, lane + 32, ...
   bool sorted;
 
@@ -97,6 +97,7 @@ struct Sequences {
     tokens = (int)p.tokens;
     rows = rows_;
     parts = parts_;
+    me = (int)blockIdx.x;
     sorted = batch <= kSorted;
     const int tid = threadIdx.x, lane = tid & 31;
     int2 mine = make_int2(0, 0);
@@ -131,7 +132,7 @@ struct Sequences {
   }
   // The r-th item of this block (all lanes of a warp); more: whether r is within the list.
   __device__ __forceinline__ Item get(int r, bool& more) const {
-    const int nb = (int)gridDim.x, me = (int)blockIdx.x;
+    const int nb = (int)gridDim.x;
     const int64_t i = (int64_t)r * nb + ((r & 1) ? nb - 1 - me : me);
     const int64_t u64 = i / parts;
     Item it{0, 0, 0, (int)(i - u64 * parts), false};
@@ -613,14 +614,15 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 // ------------------------------------------------------------------ backward ---
-// Three kernels, so that every sum has one owner and a fixed order (S and dP are computed in
-// both of the last two): delta = sum dO o of each row; dQ by query tiles; dK and dV by key
-// tiles, transposed, so that all three are products of a weight matrix in TMEM with a tile in
-// shared memory, as O = P V is.
+// A kernel for delta = sum dO o of each row, then one whose blocks take tiles of dK and dV and
+// then tiles of dQ (S and dP are computed for both, so that every sum has one owner and a fixed
+// order).  dK and dV are computed transposed, so that all three are products of a weight matrix
+// in TMEM with a tile in shared memory, as O = P V is.  Their items are long and uneven: blocks
+// with the longest of them get the shortest of dQ's (in two kernels 296 instead of 293 us, and 53
+// instead of 47 us for the second sizes below).
 //
-// A block of the two has eight softmax warps, two to a quarter of the 128 TMEM lanes, with 64
-// of the tile's 128 columns each; warp 8 loads (V in dQ: warp 11),
-// warps 9 and 10 issue.
+// A block has eight softmax warps, two to a quarter of the 128 TMEM lanes, with 64 of the
+// tile's 128 columns each; warp 8 loads (V in dQ: warp 11), warps 9 and 10 issue.
 //
 // dQ, a query tile against key tiles t: S(t) = Q K^T, dP(t) = dO V^T, then
 //   dS = P (dP - delta) as bf16 over S, dQ += dS K.  S has two buffers and K three stages, so
@@ -634,13 +636,14 @@ __global__ void __launch_bounds__(384, 1)
 //
 // What bounds them: the chain from one tile's weights over the product that reads them to the
 // next tile's scores.  A product of 128 x 128 x 128 takes 690 cycles with both operands in
-// shared memory and 1090 with one in TMEM when it runs alone, 530 in company; the two kernels
+// shared memory and 1090 with one in TMEM when it runs alone, 530 in company; the two parts
 // come to 2450 and 3200 cycles a tile of three and four products.  Sequences of 2414, 0, 1,
-// 1924 and 639 tokens, 32 heads on 8, head_dim 128: 15 + 110 + 171 us; twelve of 0 to 603
-// tokens, 12 heads on 4, head_dim 64: 3 + 17 + 33 us.  Tried and no faster: delta inside dQ's
-// kernel, from a tile of o (144 us instead of 24 + 110); lse and delta as further terms of the
-// products instead of 32 loads from shared memory a tile (201 instead of 190 us then); sixteen
-// softmax warps (172); a buffer more for dP^T with head_dim 64 (32 of 33 us).
+// 1924 and 639 tokens, 32 heads on 8, head_dim 128: 16 us for delta and 277; twelve of 0 to 603
+// tokens, 12 heads on 4, head_dim 64: 3 and 44 us.  Tried and no faster, as kernels of their own:
+// delta inside dQ's, from a tile of o (144 us instead of 24 + 110); lse and delta as further
+// terms of the products instead of 32 loads from shared memory a tile (201 instead of 190 us for
+// dK, dV then); sixteen softmax warps (172 of 171); a buffer more for dP^T with head_dim 64 (32
+// of 33 us).
 //
 // Rows of a tile beyond its sequence are masked, and where such a row is summed over (K in
 // dQ; Q and dO in dK, dV) it is set to zero in shared memory before the product, so that no
@@ -650,11 +653,11 @@ struct Bwd {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kBoxes * kBox;
   static constexpr int kOffStat = 6 * kTileBytes;     // dK, dV: [stage][-lse, -delta][128]
-  static constexpr int kStage = 32 * 128;
   static constexpr int kOffTrade = 7 * kTileBytes;    // dQ: [128] floats
-  static constexpr int kOffBarQ = kOffTrade + 512, kOffBarK = kOffStat + 2048;
-  static constexpr int kSmemQ = kOffBarQ + 256 + kSorted * 8 + 1024;
-  static constexpr int kSmemK = kOffBarK + 256 + 2 * kSorted * 8 + 1024;
+  static constexpr int kOffBarQ = kOffTrade + 512, kOffBarK = kOffBarQ + 256;
+  static constexpr int kStage = 32 * 128;
+  static constexpr int kOffSeq = kOffBarK + 256;
+  static constexpr int kSmem = kOffSeq + kSorted * 8 + 1024;
   static constexpr uint32_t kIdescS = attn_idesc(kTile, kTile, false);
   static constexpr uint32_t kIdescG = attn_idesc(kTile, D, true);
 };
@@ -708,14 +711,12 @@ __global__ void __launch_bounds__(256) packed_delta_kernel(const PackedParams p)
 }
 
 template <int D>
-__global__ void __launch_bounds__(384, 1)
-    packed_dq_kernel(const __grid_constant__ BwdMaps maps, const PackedParams p) {
+__device__ __forceinline__ void dq_part(const BwdMaps& maps, const PackedParams& p,
+                                        const Sequences& list, unsigned char* smem,
+                                        uint32_t tmem) {
   using C = Bwd<D>;
   constexpr int T = C::kTileBytes;
   constexpr uint32_t kColP = 256, kColG = 384;  // dP, dQ after S's two buffers
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char *sq = smem, *sg = smem + T;
   auto sk = [&](int s) { return smem + (2 + s) * T; };
   auto sv = [&](int s) { return smem + (5 + s) * T; };
@@ -733,26 +734,6 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* bar_kempty = bars + 14;
   uint64_t* bar_vfull = bars + 17;  // [stage of 2]
   uint64_t* bar_vempty = bars + 19;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 21);
-  if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(tslot)),
-                 "r"(512u)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  if (tid == 32 * 8) {
-    for (int i = 0; i < 21; ++i) mbar_init(bars + i, i >= 3 && i < 7 ? 256 : 1);
-    fence_mbar_init();
-  }
-  Sequences list;
-  list.init(reinterpret_cast<int2*>(smem + C::kOffBarQ + 256),
-            reinterpret_cast<int2*>(smem), p, kTile, p.heads);
-  fence_proxy_async_smem();  // (the list's scratch lies where copies will land)
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tslot;
   const int group = p.heads / p.kv_heads;
   bool dead = false, more;
 
@@ -970,7 +951,6 @@ __global__ void __launch_bounds__(384, 1)
           named_bar(1 + (warp & 3), 64);
           if (half == 1) d = trade[row];
           nd = -d;
-          if (half == 0 && row < it.len) p.delta[(int64_t)it.part * p.tokens + it.beg + row] = d;
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -1008,22 +988,15 @@ __global__ void __launch_bounds__(384, 1)
     }
     if (n > 0) store();
   }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 0)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
-                 : "memory");
 }
 
 template <int D>
-__global__ void __launch_bounds__(352, 1)
-    packed_dkv_kernel(const __grid_constant__ BwdMaps maps, const PackedParams p) {
+__device__ __forceinline__ void dkv_part(const BwdMaps& maps, const PackedParams& p,
+                                         const Sequences& list, unsigned char* smem,
+                                         uint32_t tmem) {
   using C = Bwd<D>;
   constexpr int T = C::kTileBytes;
   constexpr uint32_t kColV = 256, kColK = 256 + D;  // dV, dK, after two buffers
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char *sk = smem, *sv = smem + T;
   auto sq = [&](int s) { return smem + (2 + s) * T; };
   auto sg = [&](int s) { return smem + (4 + s) * T; };
@@ -1043,25 +1016,6 @@ __global__ void __launch_bounds__(352, 1)
   uint64_t* bar_ds = bars + 15;     // dS^T written, 256 arrivals
   uint64_t* bar_gfree = bars + 16;  // dK and dV read, 256 arrivals
   uint64_t* bar_kvfree = bars + 17; // the output boxes (over K and V) are read, 8 arrivals
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 18);
-  if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(tslot)),
-                 "r"(512u)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  if (tid == 32 * 8) {
-    for (int i = 0; i < 18; ++i) mbar_init(bars + i, i < 12 ? 1 : i < 17 ? 256 : 8);
-    fence_mbar_init();
-  }
-  Sequences list;
-  list.init(reinterpret_cast<int2*>(smem + C::kOffBarK + 256),
-            reinterpret_cast<int2*>(smem + C::kOffBarK + 256) + kSorted, p, kTile, p.kv_heads);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tslot;
   const int group = p.heads / p.kv_heads;
   bool dead = false, more;
   // Item: key tile `first` of the sequence's nt, level + 1 query tiles of each head of `part`.
@@ -1220,7 +1174,7 @@ __global__ void __launch_bounds__(352, 1)
       }
       if (n > 0) mbar_wait_bounded(bar_g, (uint32_t)((n - 1) & 1), p.err);
     }
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ softmax
     const int row = tid & 127, half = warp >> 2, col0 = 64 * half;  // key row, query columns
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -1283,6 +1237,36 @@ __global__ void __launch_bounds__(352, 1)
         mbar_arrive(&bar_p[s]);
         wait(bar_dp, (uint32_t)(n & 1));
         tc_fence_after();
+        if (first == 0 && i == 0) {
+          // The sequence's first rows see this key tile alone: as in dQ, delta = sum P dP, over
+          // a column's 32 lanes by halving, then over the four warps of the column.
+          float* part = reinterpret_cast<float*>(smem + C::kOffStat + 2048);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t y[32];
+            float x[32];
+            tmem_ld32_nowait(tY + 32 * c, y);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              x[j] = sees[c] >> j & 1 ? __uint_as_float(v[c][j]) * __uint_as_float(y[j]) : 0.f;
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1)
+#pragma unroll
+              for (int j = 0; j < off; ++j) {
+                const bool up = (lane & off) != 0;
+                const float give = up ? x[j] : x[j + off], keep = up ? x[j + off] : x[j];
+                x[j] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+              }
+            part[128 * (warp & 3) + col0 + 32 * c + lane] = x[0];
+          }
+          named_bar(5 + half, 128);
+          if (row < 64) {
+            const float* at = part + col0 + row;
+            stats(s)[128 + col0 + row] = -((at[0] + at[128]) + (at[256] + at[384]));
+          }
+          named_bar(5 + half, 128);
+        }
         uint32_t w[2][32];
         tmem_ld32_nowait(tY, w[0]);
         tmem_ld32_nowait(tY + 32, w[1]);
@@ -1357,6 +1341,48 @@ __global__ void __launch_bounds__(352, 1)
     }
     if (lane == 0) stores_done();
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(384, 1)
+    packed_bwd_kernel(const __grid_constant__ BwdMaps mk, const __grid_constant__ BwdMaps mq,
+                      const PackedParams p) {
+  using C = Bwd<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5;
+  uint64_t* bars_q = reinterpret_cast<uint64_t*>(smem + C::kOffBarQ);
+  uint64_t* bars_k = reinterpret_cast<uint64_t*>(smem + C::kOffBarK);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars_k + 18);
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tslot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 32 * 8) {
+    for (int i = 0; i < 18; ++i) mbar_init(bars_k + i, i < 12 ? 1 : i < 17 ? 256 : 8);
+    for (int i = 0; i < 21; ++i) mbar_init(bars_q + i, i >= 3 && i < 7 ? 256 : 1);
+    fence_mbar_init();
+  }
+  Sequences list;
+  list.init(reinterpret_cast<int2*>(smem + C::kOffSeq), reinterpret_cast<int2*>(smem), p, kTile,
+            p.kv_heads);
+  fence_proxy_async_smem();  // (the list's scratch lies where copies will land)
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  dkv_part<D>(mk, p, list, smem, tmem);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  list.parts = p.heads;
+  list.me = (int)(gridDim.x - 1 - blockIdx.x);  // (the first blocks had the longest items)
+  dq_part<D>(mq, p, list, smem, tmem);
   tc_fence_before();
   __syncthreads();
   if (warp == 0)
@@ -1384,8 +1410,7 @@ bool encode_map(CUtensorMap* map, const char* base, int64_t tokens, int heads, i
 template <int D>
 static PackedTcKernels tc_kernels() {
   return PackedTcKernels{(const void*)packed_fwd_kernel<D>, (const void*)packed_delta_kernel<D>,
-                         (const void*)packed_dq_kernel<D>,  (const void*)packed_dkv_kernel<D>,
-                         Fwd<D>::kSmem, Bwd<D>::kSmemQ, Bwd<D>::kSmemK};
+                         (const void*)packed_bwd_kernel<D>, Fwd<D>::kSmem, Bwd<D>::kSmem};
 }
 PackedTcKernels packed_tc_kernels(int d) {
   return d == 64 ? tc_kernels<64>() : d == 128 ? tc_kernels<128>() : PackedTcKernels{};
@@ -1428,13 +1453,9 @@ const char* packed_tc_bwd_launch(const PackedParams& p, int sms, cudaStream_t st
                        stream) != cudaSuccess)
     return "launch failed";
   const int64_t levels = p.tokens / kTile + p.batch;
-  void* qargs[] = {&mq, &pc};
-  if (cudaLaunchKernel(k.dq, dim3((unsigned)std::min<int64_t>(sms, levels * p.heads)), dim3(384),
-                       qargs, (size_t)k.dq_smem, stream) != cudaSuccess)
-    return "launch failed";
-  void* kargs[] = {&mk, &pc};
-  if (cudaLaunchKernel(k.dkv, dim3((unsigned)std::min<int64_t>(sms, levels * p.kv_heads)),
-                       dim3(352), kargs, (size_t)k.dkv_smem, stream) != cudaSuccess)
+  void* args[] = {&mk, &mq, &pc};
+  if (cudaLaunchKernel(k.bwd, dim3((unsigned)std::min<int64_t>(sms, levels * p.heads)), dim3(384),
+                       args, (size_t)k.bwd_smem, stream) != cudaSuccess)
     return "launch failed";
   return nullptr;
 }

@@ -2821,14 +2821,13 @@ rr_status rr_attention_packed_bwd(const void* dout, const void* q, const void* k
   p.scale = scale;
   p.scale_log2 = scale * rr::kLog2e;
   const rr::PackedTcKernels tk = rr::packed_tc_kernels(dtype == RR_BF16 ? p.dim : 0);
-  if (tk.dq) {
+  if (tk.bwd) {
     int sms = 0;
     {
       std::lock_guard<std::mutex> lock(g_mu);
       DevInfo* di = nullptr;
       if ((st = device_info(&di)) != RR_OK) return st;
-      if ((st = set_smem(di, tk.dq, (size_t)tk.dq_smem)) != RR_OK) return st;
-      if ((st = set_smem(di, tk.dkv, (size_t)tk.dkv_smem)) != RR_OK) return st;
+      if ((st = set_smem(di, tk.bwd, (size_t)tk.bwd_smem)) != RR_OK) return st;
       p.err = di->err;
       sms = di->sms;
     }

@@ -401,8 +401,8 @@ struct PackedRowKernels {
 };
 PackedRowKernels packed_row_kernels(int dtype);
 struct PackedTcKernels {
-  const void *fwd, *delta, *dq, *dkv;
-  int fwd_smem, dq_smem, dkv_smem;
+  const void *fwd, *delta, *bwd;
+  int fwd_smem, bwd_smem;
 };
 // Tensor-core kernels for bf16 of this head dimension; fwd null where there are none.
 PackedTcKernels packed_tc_kernels(int d);
