@@ -22,8 +22,12 @@
 //
 // A tile's rows beyond its sequence (the next one's, or past the buffer, which read as zero)
 // are not stored, and keys beyond a row's own are masked in S.  Their V has weight 0, which a
-// NaN or infinity there would turn into NaN: a row that ends with one is computed again from
-// the keys that it sees (repair_row).
+// NaN or infinity there would turn into NaN.  V's rows behind a sequence are set to zero in shared
+// memory before their product.  Those of the sequence's own later tokens are not looked at
+// (testing the one tile an item that has some took the long prompts from 255 to 270 us or more):
+// a block notes the items in which a row ended as NaN or infinite, and when all its roles have
+// ended it reads their last tiles of V and computes the rows again that an unseen value reached
+// (repair_items).  A value that a row does see stays, and costs the reading of that tile.
 #include <algorithm>
 #include <cstdint>
 
@@ -167,6 +171,10 @@ struct Sequences {
   }
 };
 
+// A block's items that have a row which is not finite: a bit for each of the first kFlagged - 1,
+// one for all others.  flags[kFlagged / 32]: whether there are any.
+constexpr int kFlagged = 4096;
+
 template <int D>
 struct Fwd {
   static constexpr int kBoxes = D / 64;
@@ -177,7 +185,8 @@ struct Fwd {
   static constexpr int kOffTrade = kOffStage + 8 * kStage;  // [2][half][128] floats
   static constexpr int kOffBar = kOffTrade + 2048;
   static constexpr int kOffSeq = kOffBar + 256;
-  static constexpr int kSmem = kOffSeq + kSorted * 8 + 1024;
+  static constexpr int kOffFlags = kOffSeq + kSorted * 8;
+  static constexpr int kSmem = kOffFlags + kFlagged / 8 + 16 + 1024;
   static constexpr uint32_t kColO = 384;
   static constexpr uint32_t kIdescS = attn_idesc(kTile, kTile, false);
   static constexpr uint32_t kIdescO = attn_idesc(kTile, D, true);
@@ -251,6 +260,12 @@ __device__ __forceinline__ void put_rows(const uint32_t (&lo)[32], const uint32_
   }
 }
 
+// Zeros in `bytes` of shared memory, by one thread (visible to later tensor products of it).
+__device__ __forceinline__ void zero_smem(void* at, int bytes) {
+  asm volatile("st.bulk.weak.shared::cta [%0], %1, 0;" ::"r"(smem_addr(at)), "l"((int64_t)bytes)
+               : "memory");
+}
+
 // Row t of head h again, in float32, from the keys that it sees: the warp's lanes take 32
 // keys' scores, then all the D columns.  sq: shared room for D floats.
 template <int D>
@@ -298,6 +313,75 @@ __device__ __noinline__ void repair_row(const PackedParams& p, int64_t begin, in
   char* o = const_cast<char*>(p.o) + (t * p.so + (int64_t)h * D) * 2;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) st_elem<kBF16>(o + 2 * (lane + 32 * i), acc[i] / l);
+}
+
+// How many of an item's rows, its first ones, a NaN or infinity of V reached that they do not see
+// (a warp; D / 32 columns a lane).  In a column, the rows before its last such value, but from
+// its first NaN on a row is NaN by what it sees.
+template <int D>
+__device__ __forceinline__ int reached_rows(const PackedParams& p, const Item& it) {
+  const int lane = threadIdx.x & 31, q0 = it.level * kTile, n = min(kTile, it.len - q0);
+  const char* v = p.v + ((int64_t)(it.beg + q0) * p.sv +
+                         (int64_t)(it.part / (p.heads / p.kv_heads)) * D + lane * (D / 32)) * 2;
+  int last[D / 32] = {}, nan[D / 32];
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) nan[c] = kTile;
+#pragma unroll 1
+  for (int j0 = 0; j0 < n; j0 += 32) {
+    uint32_t x[32][D / 64], odd = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k)
+        x[j][k] = j0 + j < n
+                      ? __ldg(reinterpret_cast<const uint32_t*>(v + (j0 + j) * p.sv * 2) + k) : 0u;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k) odd |= (x[j][k] & 0x7f807f80u) + 0x00800080u;
+    if ((odd & 0x80008000u) == 0) continue;  // no exponent of ones
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        const uint32_t bits = (x[j][c >> 1] >> 16 * (c & 1)) & 0x7fffu;
+        if (bits >= 0x7f80u) last[c] = j0 + j;
+        if (bits > 0x7f80u) nan[c] = min(nan[c], j0 + j);
+      }
+  }
+  int rows = 0;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) rows = max(rows, min(last[c], nan[c]));
+  return __reduce_max_sync(0xffffffffu, rows);
+}
+
+// All threads of the block, when its roles have ended and what they stored is in place.
+template <int D>
+__device__ __noinline__ void repair_items(const PackedParams& p, const uint32_t* flags,
+                                          unsigned char* smem) {
+  constexpr int NW = 12;
+  __shared__ int rows[NW];
+  const int warp = threadIdx.x >> 5;
+  float* sq = reinterpret_cast<float*>(smem) + warp * D;
+  Sequences list;
+  list.init(reinterpret_cast<int2*>(smem + NW * D * 4),
+            reinterpret_cast<int2*>(smem + NW * D * 4) + kSorted, p, kTile, p.heads);
+  for (int r0 = 0;; r0 += NW) {  // a warp an item
+    bool more;
+    const int bit = min(r0 + warp, kFlagged - 1);
+    const Item mine = list.get(r0 + warp, more);
+    const bool last = warp == NW - 1 && !more;
+    rows[warp] = mine.ok && (flags[bit >> 5] >> (bit & 31) & 1) ? reached_rows<D>(p, mine) : 0;
+    __syncthreads();
+    for (int k = 0; k < NW; ++k) {  // then all warps the rows of each
+      if (rows[k] == 0) continue;
+      bool is;
+      const Item it = list.get(r0 + k, is);
+      const int64_t first = (int64_t)it.beg + it.level * kTile;
+      for (int i = warp; i < rows[k]; i += NW) repair_row<D>(p, it.beg, first + i, it.part, sq);
+    }
+    if (__syncthreads_or(last)) return;
+  }
 }
 
 // Bits n to 31 (all for n <= 0, none for n >= 32).
@@ -350,6 +434,8 @@ __global__ void __launch_bounds__(384, 1)
     for (int i = 17; i < 20; ++i) mbar_init(bars + i, 256);
     fence_mbar_init();
   }
+  uint32_t* flags = reinterpret_cast<uint32_t*>(smem + C::kOffFlags);
+  if (tid <= kFlagged / 32) flags[tid] = 0;
   Sequences list;
   list.init(reinterpret_cast<int2*>(smem + C::kOffSeq), reinterpret_cast<int2*>(smem + C::kOffStage),
             p, kTile, p.heads);
@@ -439,6 +525,12 @@ __global__ void __launch_bounds__(384, 1)
       for (int t = 0; t <= it.level; ++t) {
         const int s = n & 1;
         wait_spin(&bar_vfull[s], (uint32_t)((n >> 1) & 1), dead, p.err);
+        const int rest = it.len - t * kTile;
+        if (rest < kTile && !dead) {  // rows behind the sequence
+          for (int x = 0; x < C::kBoxes; ++x)
+            zero_smem(smem + C::kOffV + s * T + x * kBox + rest * 128, (kTile - rest) * 128);
+          fence_proxy_async_smem();
+        }
         if (t == 0 && items > 0) wait_spin(bar_ofree, (uint32_t)((items - 1) & 1), dead, p.err);
         wait_spin(&bar_p[b], ph, dead, p.err);
         if (dead) break;
@@ -486,7 +578,7 @@ __global__ void __launch_bounds__(384, 1)
       if (!more) break;
       if (!it.ok) continue;
       const int h = it.part, q0 = it.level * kTile;
-      float m = -INFINITY, l = 0.f;  // of all keys; of this thread's
+      float m = -INFINITY, l = 0.f;  // for all keys; of this thread's
       for (int t = 0; t <= it.level; ++t) {
         wait(&bar_s[b], ph);
         tc_fence_after();
@@ -510,11 +602,12 @@ __global__ void __launch_bounds__(384, 1)
           for (int i = 0; i < 32; ++i) mx[i & 7] = fmaxf(mx[i & 7], __uint_as_float(v[c][i]));
         const float mx0 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const float mx1 = fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-        // m moves only when the tile's maximum exceeds it by more than 2^8 (P stays below
-        // 2^8 otherwise, exact in its sum's float32), so O is rarely rescaled
+        // m, the sums' reference, moves only when the tile's maximum exceeds it, and then to
+        // 2^8 above, so O is rarely rescaled.  P is at most 1: O overflows only where a sum of
+        // that many v does.
         const float mine = fmaxf(mx0, mx1);
         const float mt = fmaxf(mine, swap(mine)) * sc;
-        const float mn = mt > m + 8.f ? mt : m;
+        const float mn = mt > m ? mt + 8.f : m;
         const float ref = mn == -INFINITY ? 0.f : mn;
         const float alpha = ex2(m - ref);
         if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -590,17 +683,10 @@ __global__ void __launch_bounds__(384, 1)
       char* out = const_cast<char*>(p.o) + (at * p.so + (int64_t)h * D + col) * 2;
       if (D == 128 || half == 0)
         put_box(o[0], o[1], inv, box, &to, col, h, (int)at, out,
-                __all_sync(0xffffffffu, live && fine), live && fine);
-      uint32_t broken = half == 0 ? __ballot_sync(0xffffffffu, live && !fine) : 0;
-      if (broken) {
-        if (lane == 0) stores_read();
-        __syncwarp();
-        while (broken) {
-          const int who = __ffs(broken) - 1;
-          broken &= broken - 1;
-          repair_row<D>(p, it.beg, __shfl_sync(0xffffffffu, at, who), h,
-                        reinterpret_cast<float*>(box));
-        }
+                __all_sync(0xffffffffu, live), live);
+      if (half == 0 && __any_sync(0xffffffffu, live && !fine) && lane == 0) {
+        atomicOr(flags + (min(r, kFlagged - 1) >> 5), 1u << (min(r, kFlagged - 1) & 31));
+        flags[kFlagged / 32] = 1;
       }
     }
     if (lane == 0) stores_done();
@@ -611,6 +697,7 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
                  : "memory");
+  if (flags[kFlagged / 32]) repair_items<D>(p, flags, smem + C::kOffStage);
 }
 
 // ------------------------------------------------------------------ backward ---

@@ -1,0 +1,171 @@
+"""The packed-sequence operators at the edges of what they accept: values that are not finite
+where a token does not see them, long sequences, extreme magnitudes."""
+import math
+
+import pytest
+import torch
+
+import packed_ref as ref
+import row_reduction_pass_gb300 as rr
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def rnd(seed, *shape, dtype=torch.float32):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype)
+
+
+def i32(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+def attend(q, k, v, cu, **kw):
+    o, lse = torch.full_like(q, 7.0), torch.full((q.shape[1], q.shape[0]), 7.0, device="cuda")
+    rr.rr_attention_packed_fwd(q, k, v, cu, o, lse=lse, **kw)
+    return o, lse
+
+
+# ---------------------------------------------------------------- attention ---
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_rows_of_no_sequence_leave_the_same_bits(bad, D):
+    """Whatever stands between, behind and in the sequences beside it: a sequence's rows come out
+    the same to the bit, with lengths that end a tile early, at its end and a row after."""
+    lens, H, KV = [70, 128, 129, 1, 255, 300], 4, 2
+    T = 5 + sum(lens) + 40
+    q, k, v = (rnd(i, T, n, D, dtype=BF).cuda() for i, n in enumerate((H, KV, KV)))
+    ends = [5]
+    for n in lens:
+        ends.append(ends[-1] + n)
+    want, wlse = attend(q, k, v, i32(ends))
+    for b, n in enumerate(lens):
+        mine = slice(ends[b], ends[b + 1])
+        t = [x.clone() for x in (q, k, v)]
+        for x in t:
+            x[:mine.start] = bad
+            x[mine.stop:] = bad
+        o, lse = attend(*t, i32(ends))
+        assert torch.equal(o[mine], want[mine]) and torch.equal(lse[:, mine], wlse[:, mine])
+    assert rr.rr_read_device_error(0) == 0
+
+
+def near(got, want, q, k, v, cu):
+    """Two results with their own roundings, of the weights and of themselves (2^-8 each): 2^-6 of
+    sum p |v|, which an attention over |v| gives to a few of these roundings."""
+    mag = attend(q, k, v.abs(), cu)[0].float()
+    return bool(((got.float() - want.float()).abs() <= 2.0 ** -6 * 1.05 * mag).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("first", [0, 130])
+@pytest.mark.parametrize("at", [[0], [127], [128], [5, 6, 127, 200], [31, 32, 63, 64, 299], [40, 41]])
+def test_single_values_reach_the_rows_and_columns_that_see_them(at, first, D):
+    """A NaN or an infinity in one element of v: of the rows from its own on that column is NaN or
+    infinite, and everything else is as with a zero in its place: to the bit, but in the rows of
+    its tile before it."""
+    T, H, KV = first + 301, 4, 2
+    q, k, v = (rnd(i + 9, T, n, D, dtype=BF).cuda() for i, n in enumerate((H, KV, KV)))
+    cu, bad = i32([0, first, T]), (math.inf, math.nan, -math.inf, math.inf)
+    zeroed, add = v.clone(), torch.zeros(T, KV, D, device="cuda")
+    same = torch.ones(T, dtype=torch.bool, device="cuda")
+    for i, j in enumerate(at):
+        same[first + j // 128 * 128:first + j] = False
+        for kv in range(KV):
+            c = 3 if at == [40, 41] else (17 * i + 5 * kv) % D  # (one column: inf, then -inf)
+            f = (math.inf, -math.inf)[i] if at == [40, 41] else bad[(i + kv) % 4]
+            v[first + j, kv, c], zeroed[first + j, kv, c] = f, 0.0
+            add[first + j:, kv, c] += f
+    base, wlse = attend(q, k, zeroed, cu)
+    want = (base.float() + add.repeat_interleave(H // KV, 1)).to(BF)
+    o, lse = attend(q, k, v, cu)
+    assert torch.equal(lse, wlse) and not bool(torch.isfinite(want).all())
+    assert torch.equal(torch.isnan(o), torch.isnan(want))
+    assert torch.equal(torch.isinf(o), torch.isinf(want))
+    assert torch.equal(torch.nan_to_num(o[same], nan=3.0), torch.nan_to_num(want[same], nan=3.0))
+    fine = torch.isfinite(want)
+    assert near(torch.where(fine, o, base), base, q, k, zeroed, cu)
+    assert torch.equal(o[torch.isinf(want)], want[torch.isinf(want)])
+    assert rr.rr_read_device_error(0) == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_long_sequence_with_values_that_are_not_finite_beside_it(D):
+    """Sequences of 100 001 tokens and fewer: NaN behind the last, at the long one's end, early and
+    late in it change neither the others nor the rows before, and no wait runs out."""
+    lens, H = [90, 100001, 513], 2
+    T = sum(lens) + 100
+    q, k, v = (rnd(i, T, n, D, dtype=BF).cuda() for i, n in enumerate((H, 1, 1)))
+    ends = [0, 90, 90 + 100001, sum(lens)]
+    cu = i32(ends)
+    want, wlse = attend(q, k, v, cu)
+    for row in (ends[2] - 1, ends[1] + 50, ends[1] + 60000):
+        bad = v.clone()
+        bad[row] = math.nan
+        bad[ends[3]:] = math.nan
+        o, lse = attend(q, k, bad, cu)
+        assert rr.rr_read_device_error(0) == 0
+        kept = torch.ones(T, dtype=torch.bool, device="cuda")
+        kept[row:ends[2]] = False
+        assert torch.equal(lse, wlse) and bool(torch.isnan(o[~kept]).all())
+        o[~kept] = want[~kept]
+        assert near(o, want, q, k, v, cu)
+        kept[ends[1] + (row - ends[1]) // 128 * 128:row] = False  # (that tile's rows before it)
+        assert torch.equal(o[kept], want[kept])
+    bad = torch.full_like(v, math.nan)
+    o, _ = attend(q, k, bad, cu)
+    assert rr.rr_read_device_error(0) == 0 and bool(torch.isnan(o[:ends[3]]).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_more_tiles_a_block_than_have_a_bit_of_their_own(D):
+    """Sequences of one tile, some thousands for each block, every seventh with a NaN in it."""
+    n, H = 128, 4 * 160
+    T = 1100 * n
+    q, k, v = (rnd(i, T, 1, D, dtype=BF).cuda() for i in range(3))
+    q = q.expand(T, H, D).contiguous()
+    cu = torch.arange(0, T + 1, n, dtype=torch.int32, device="cuda")
+    want = torch.empty_like(q)
+    rr.rr_attention_packed_fwd(q, k, v, cu, want)
+    bad = v.clone()
+    bad[100::7 * n] = math.nan
+    o = torch.empty_like(q)
+    rr.rr_attention_packed_fwd(q, k, bad, cu, o)
+    same = torch.ones(T, dtype=torch.bool, device="cuda")
+    for b in range(0, 1100, 7):
+        same[b * n:(b + 1) * n] = False
+        assert bool(torch.isnan(o[b * n + 100:(b + 1) * n]).all())
+        assert float((o[b * n:b * n + 100] - want[b * n:b * n + 100]).float().abs().max()) < 0.05
+    assert torch.equal(o[same], want[same]) and rr.rr_read_device_error(0) == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_great_values(D):
+    """200 values of 2^120, whose sum still is a float32, under scores that rise by 7 powers of
+    two from the first tile to the second: the result is 2^120 (within its rounding and the
+    weights', 2^-8 each)."""
+    T = 200
+    q = torch.zeros(T, 1, D, dtype=BF, device="cuda")
+    q[..., 0] = 1.0
+    k = torch.zeros_like(q)
+    k[128:, 0, 0] = 7.0 * math.log(2.0)
+    v = torch.full_like(q, 2.0 ** 120)
+    o, _ = attend(q, k, v, i32([0, T]), scale=1.0)
+    assert float(((o.double() / 2.0 ** 120) - 1.0).abs().max()) <= 2.0 ** -7
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_before_a_nan_against_the_plain_form(D):
+    """Weights and the result are rounded to bf16 (2^-8 each): 2^-7 of sum p |v|."""
+    T, H, KV = 333, 4, 2
+    q, k, v = (rnd(i, T, n, D, dtype=BF) for i, n in enumerate((H, KV, KV)))
+    cu = [0, 70, 333]
+    want, wlse, mag, _ = ref.attention(q, k, v, cu, 1.0 / math.sqrt(D))
+    v[300] = math.nan
+    v[310:, :, 7] = math.inf
+    o, lse = attend(q.cuda(), k.cuda(), v.cuda(), i32(cu))
+    off = (o.double().cpu() - want).abs() - 2.0 ** -7 * mag
+    assert float(off[:300].max()) <= 0.0
+    assert float((lse.double().cpu() - wlse).abs().max()) <= 1e-5 * (1.0 + float(wlse.abs().max()))
