@@ -9,7 +9,7 @@
 // are kept apart (not their sum) for the gradient: x - m is exact near the maximum, however
 // large the logits are.
 //   dlogits_j = [g (1_{j=t} - p_j) - h p_j (ln p_j + entropy)] / T
-//             = p_j (A + B log2 p_j) + 1_{j=t} g / T  with two numbers A, B a row.
+//             = [p_j A + (p_j log2 p_j) B + 1_{j=t} g] / T  with two numbers A, B a row.
 // Both are bound by memory: the forward reads the row once, the backward reads and writes it.
 //
 // The alternatives cost no second pass over the row: each thread's own maximum is known from
@@ -888,13 +888,14 @@ __global__ void __launch_bounds__(kT) logprob_bwd_kernel(const LogprobBwdParams 
   const float g = p.g ? __ldg(p.g + r) : 0.f, h = p.h ? __ldg(p.h + r) : 0.f;
   const float ent = p.h ? __ldg(p.entropy + r) : 0.f;
   const float inv = 1.f / p.temperature, c = p.c;
-  const float A = -(g + h * ent) * inv, B = -h * kLn2 * inv, G = g * inv;
+  // (the power first and 1 / T last: where p is 0 no factor of a low temperature overflows)
+  const float A = -(g + h * ent), B = -h * kLn2;
   const float ls = __ldg(p.log_sum + r) * kLog2e;
   auto grad = [&](float x, int64_t j) {
     if (zero) return 0.f;
     const float a = max_nan((x - m) * c - ls, kLow);
-    const float v = ex2(a) * (A + B * a);
-    return j == t ? v + G : v;
+    const float e = ex2(a), v = fmaf(e * a, B, e * A);
+    return (j == t ? v + g : v) * inv;
   };
   if constexpr (kV) {
     for (int u = 0; u < kU; ++u) {

@@ -7,6 +7,7 @@ import torch
 
 import packed_ref as ref
 import row_reduction_pass_gb300 as rr
+from packed_ref import EPS, HALF
 
 pytestmark = pytest.mark.gpu
 
@@ -169,3 +170,37 @@ def test_rows_before_a_nan_against_the_plain_form(D):
     off = (o.double().cpu() - want).abs() - 2.0 ** -7 * mag
     assert float(off[:300].max()) <= 0.0
     assert float((lse.double().cpu() - wlse).abs().max()) <= 1e-5 * (1.0 + float(wlse.abs().max()))
+
+
+# -------------------------------------------------------- log probabilities ---
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("T", [2.0 ** -120, 2.0 ** -60, 0.01, 2.0 ** 60, 2.0 ** 120])
+def test_logprob_gradient_at_extreme_temperatures(T, dtype):
+    """Gradients of log probability and entropy, masked columns (-infinity, the type's lowest, a
+    finite -1e9) among them.  At a low temperature a column below the maximum has probability 0
+    and gets 0; a row of two equal maxima has 1/2 for both.  The plain form in float64, within
+    64 EPS of its magnitudes and the result's rounding, as at other temperatures.  A result below
+    2^-126 may be 0, and so may a probability, whose factor is at most h 126 ln 2 < 2^9, over T."""
+    rows, cols = 12, 999
+    x = 3.0 * rnd(3, rows, cols).to(dtype)
+    x[1, :40], x[2, :40], x[3, :40] = -math.inf, torch.finfo(dtype).min, -1e9
+    x[4, 7] = x[4, 700] = 50.0
+    x[5] = 1.5
+    tok = x.float().argmax(1)
+    tok[6:9] = torch.tensor([3, 400, -100])
+    g, h = 0.5 + rnd(4, rows).abs(), rnd(5, rows)
+    f = {n: torch.empty(rows, device="cuda") for n in ("logprob", "entropy", "row_max", "log_sum")}
+    xd, td = x.cuda(), tok.int().cuda()
+    rr.rr_token_logprob_fwd(xd, td, temperature=T, **f)
+    for gl, gh in ((g, h), (None, h), (g, None)):
+        d = torch.empty_like(xd)
+        rr.rr_token_logprob_bwd(xd, td, f["row_max"], f["log_sum"],
+                                None if gl is None else gl.cuda(), d,
+                                entropy=None if gh is None else f["entropy"],
+                                grad_entropy=None if gh is None else gh.cuda(), temperature=T)
+        want, mag = ref.logprob_bwd(x, tok, gl, gh, T)
+        # (a token's own term cancels with its probability: both carry the logarithms' error)
+        close = (d.double().cpu() - want).abs() <= (64 * EPS * mag + HALF[dtype] * want.abs()
+                                                    + 2.0 ** -126 + 2.0 ** -117 / T)
+        assert bool(close.all()), (int((~close).sum()), d.cpu()[~close][:4], want[~close][:4])
