@@ -679,7 +679,8 @@ __global__ void __launch_bounds__(kT, 4) logprob_cluster_kernel(const LogprobPar
   __shared__ uint32_t s_key[kT], s_thr;
   __shared__ unsigned short s_owner[kT];
   __shared__ unsigned long long s_cand[kCand];
-  __shared__ float s_part[kMost][4];
+  __shared__ float4 s_part[kMost];
+  static_assert(alignof(decltype(s_part)) >= 16, "written 16 bytes at a time by other blocks");
   __shared__ unsigned long long s_list[kMost * kLogprobMaxK];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = (int)cluster_nrank(), me = (int)cluster_rank();
@@ -837,7 +838,7 @@ __global__ void __launch_bounds__(kT, 4) logprob_cluster_kernel(const LogprobPar
     // to the first block: statistics, and the k largest in order (0: no column)
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (tid == 0)
-      st_cluster_f32x4(map_to_rank(s_part[me], 0), st.m, st.d, st.n, __int_as_float(ranks));
+      st_cluster_f32x4(map_to_rank(&s_part[me], 0), st.m, st.d, st.n, __int_as_float(ranks));
     const uint32_t list = map_to_rank(s_list, 0) + me * p.k * 8;
     for (int q = found + tid; q < p.k; q += kT) st_cluster_u64(list + q * 8, 0ull);
     for (int q = tid; q < found; q += kT) {
@@ -848,11 +849,11 @@ __global__ void __launch_bounds__(kT, 4) logprob_cluster_kernel(const LogprobPar
     }
     cluster_sync();
     if (me != 0) return;
-    st = Stat{s_part[0][0], s_part[0][1], s_part[0][2]};
-    ranks = __float_as_int(s_part[0][3]);
+    st = Stat{s_part[0].x, s_part[0].y, s_part[0].z};
+    ranks = __float_as_int(s_part[0].w);
     for (int w = 1; w < K; ++w) {
-      st = merge(st, Stat{s_part[w][0], s_part[w][1], s_part[w][2]}, c);
-      ranks += __float_as_int(s_part[w][3]);
+      st = merge(st, Stat{s_part[w].x, s_part[w].y, s_part[w].z}, c);
+      ranks += __float_as_int(s_part[w].w);
     }
     found = K * p.k;
   }
