@@ -2,7 +2,8 @@
  * (type, shape, layout, device), takes their addresses and calls the C entry point of librr.so.
  * The same checks written in Python cost a call 8 of its 14 microseconds, more than most of
  * these kernels take on a decoding step's sizes.  Plain CPython API; torch's tensors are asked
- * through their methods. */
+ * through their methods.  The entry points run without the interpreter's lock: a launch waits
+ * while a stream's queue is full, perhaps for a host callback that needs the lock. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
@@ -213,11 +214,14 @@ static PyObject *rope_fwd(PyObject *self, PyObject *const *a, Py_ssize_t na) {
     const Tensor bad = tensor(&c, "bad_position_count", a[11], i32, 1, one, 0);
     void *s = stream_of(&c, a[12]);
     if (c.bad) return NULL;
-    const int r = ((int (*)(void *, void *, void *, void *, void *, void *, void *, void *, void *,
-                            int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
-                            int64_t, int64_t, float, int, void *, int, void *))entry[ROPE_FWD])(
+    int r;
+    Py_BEGIN_ALLOW_THREADS
+    r = ((int (*)(void *, void *, void *, void *, void *, void *, void *, void *, void *,
+                  int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
+                  int64_t, int64_t, float, int, void *, int, void *))entry[ROPE_FWD])(
         x.p, y.p, qw.p, kw.p, cos.p, sin.p, pos.p, qo.p, ko.p, q[0], q[1], k[1], q[2], 2 * tab[1],
         tab[0], x.row, y.row, qo.row, ko.row, eps, inter, bad.p, st, s);
+    Py_END_ALLOW_THREADS
     return PyLong_FromLong(r);
 }
 
@@ -249,13 +253,16 @@ static PyObject *rope_bwd(PyObject *self, PyObject *const *a, Py_ssize_t na) {
     const Tensor bad = tensor(&c, "bad_position_count", a[16], i32, 1, one, 0);
     void *s = stream_of(&c, a[17]);
     if (c.bad) return NULL;
-    const int r = ((int (*)(void *, void *, void *, void *, void *, void *, void *, void *, void *,
-                            void *, void *, void *, void *, void *, size_t, int64_t, int64_t,
-                            int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
-                            int64_t, int64_t, float, int, void *, int, void *))entry[ROPE_BWD])(
+    int r;
+    Py_BEGIN_ALLOW_THREADS
+    r = ((int (*)(void *, void *, void *, void *, void *, void *, void *, void *, void *,
+                  void *, void *, void *, void *, void *, size_t, int64_t, int64_t,
+                  int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
+                  int64_t, int64_t, float, int, void *, int, void *))entry[ROPE_BWD])(
         gq.p, gk.p, x.p, y.p, qw.p, kw.p, cos.p, sin.p, pos.p, dq.p, dk.p, dqw.p, dkw.p, ws, bytes,
         q[0], q[1], k[1], q[2], 2 * tab[1], tab[0], gq.row, gk.row, x.row, y.row, dq.row, dk.row,
         eps, inter, bad.p, st, s);
+    Py_END_ALLOW_THREADS
     return PyLong_FromLong(r);
 }
 
@@ -287,11 +294,14 @@ static PyObject *attn_fwd(PyObject *self, PyObject *const *a, Py_ssize_t na) {
     const float scale = (float)number(&c, a[6]);
     void *s = stream_of(&c, a[7]);
     if (c.bad) return NULL;
-    const int r = ((int (*)(void *, void *, void *, void *, void *, void *, int64_t, int64_t,
-                            int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, float,
-                            int, void *))entry[ATTN_FWD])(
+    int r;
+    Py_BEGIN_ALLOW_THREADS
+    r = ((int (*)(void *, void *, void *, void *, void *, void *, int64_t, int64_t,
+                  int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, float,
+                  int, void *))entry[ATTN_FWD])(
         x.p, y.p, z.p, cu, o.p, lse.p, q[0], batch, q[1], k[1], q[2], x.row, y.row, z.row, o.row,
         scale, st, s);
+    Py_END_ALLOW_THREADS
     return PyLong_FromLong(r);
 }
 
@@ -317,12 +327,15 @@ static PyObject *attn_bwd(PyObject *self, PyObject *const *a, Py_ssize_t na) {
     void *ws = workspace(&c, a[11], &bytes);
     void *s = stream_of(&c, a[12]);
     if (c.bad) return NULL;
-    const int r = ((int (*)(void *, void *, void *, void *, void *, void *, void *, void *, void *,
-                            void *, void *, size_t, int64_t, int64_t, int64_t, int64_t, int64_t,
-                            int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
-                            float, int, void *))entry[ATTN_BWD])(
+    int r;
+    Py_BEGIN_ALLOW_THREADS
+    r = ((int (*)(void *, void *, void *, void *, void *, void *, void *, void *, void *,
+                  void *, void *, size_t, int64_t, int64_t, int64_t, int64_t, int64_t,
+                  int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
+                  float, int, void *))entry[ATTN_BWD])(
         g.p, x.p, y.p, z.p, o.p, lse.p, cu, dq.p, dk.p, dv.p, ws, bytes, q[0], batch, q[1], k[1],
         q[2], g.row, x.row, y.row, z.row, o.row, dq.row, dk.row, dv.row, scale, st, s);
+    Py_END_ALLOW_THREADS
     return PyLong_FromLong(r);
 }
 
@@ -351,11 +364,14 @@ static PyObject *logprob_fwd(PyObject *self, PyObject *const *a, Py_ssize_t na) 
     const Tensor bad = tensor(&c, "bad_token_count", a[11], i32, 1, one, 0);
     void *s = stream_of(&c, a[12]);
     if (c.bad) return NULL;
-    const int r = ((int (*)(void *, void *, void *, void *, void *, void *, void *, void *, void *,
-                            int64_t, int64_t, int64_t, int64_t, float, int32_t, void *, int,
-                            void *))entry[LOGP_FWD])(
+    int r;
+    Py_BEGIN_ALLOW_THREADS
+    r = ((int (*)(void *, void *, void *, void *, void *, void *, void *, void *, void *,
+                  int64_t, int64_t, int64_t, int64_t, float, int32_t, void *, int,
+                  void *))entry[LOGP_FWD])(
         lg.p, t.p, lp.p, en.p, rm.p, ls.p, rk.p, ti.p, tl.p, x[0], x[1], lg.row,
         top[1] < 0 ? 0 : top[1], T, ignore, bad.p, st, s);
+    Py_END_ALLOW_THREADS
     return PyLong_FromLong(r);
 }
 
@@ -378,9 +394,12 @@ static PyObject *logprob_bwd(PyObject *self, PyObject *const *a, Py_ssize_t na) 
     const int32_t ignore = whole(&c, "ignore_index", a[9]);
     void *s = stream_of(&c, a[10]);
     if (c.bad) return NULL;
-    const int r = ((int (*)(void *, void *, void *, void *, void *, void *, void *, void *, int64_t,
-                            int64_t, int64_t, int64_t, float, int32_t, int, void *))entry[LOGP_BWD])(
+    int r;
+    Py_BEGIN_ALLOW_THREADS
+    r = ((int (*)(void *, void *, void *, void *, void *, void *, void *, void *, int64_t,
+                  int64_t, int64_t, int64_t, float, int32_t, int, void *))entry[LOGP_BWD])(
         lg.p, t.p, rm.p, ls.p, en.p, g.p, h.p, dl.p, x[0], x[1], lg.row, dl.row, T, ignore, st, s);
+    Py_END_ALLOW_THREADS
     return PyLong_FromLong(r);
 }
 
