@@ -230,7 +230,7 @@ struct DistillGeo {
 };
 struct DistillKernels {
   const void* rows;       // a block per row, any alignment and length
-  int rows_threads, rows_smem;
+  int rows_threads;
   const void* stream[2];  // [cluster]
   int slots_off;          // stream: byte offset of the [4][K * (row warps + 1)] slots
 };
