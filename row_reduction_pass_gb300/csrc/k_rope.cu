@@ -59,16 +59,6 @@ struct Slots {
 };
 
 template <int DT, int W>
-__device__ __forceinline__ void load(float (&f)[W], const char* p) {
-  if constexpr (W == 1) {
-    f[0] = ld_elem<DT>(p);
-  } else {
-    const uint4 c = ld_chunk_stream(p);
-#pragma unroll
-    for (int i = 0; i < W; ++i) f[i] = chunk_get<DT>(c, i);
-  }
-}
-template <int DT, int W>
 __device__ __forceinline__ void load_cached(float (&f)[W], const char* p) {
   if constexpr (W == 1) {
     f[0] = ld_elem_cached<DT>(p);
