@@ -749,9 +749,10 @@ struct Bwd {
   static constexpr uint32_t kIdescG = attn_idesc(kTile, D, true);
 };
 
-// The tensor maps of a backward kernel: 128-row boxes of the inputs, 32-row boxes of outputs.
+// The tensor maps of the backward kernel: 128-row boxes of q, k, v and dO, 32-row boxes of dK and
+// dV (dQ is stored row by row).
 struct BwdMaps {
-  CUtensorMap q, k, v, g, out0, out1;
+  CUtensorMap q, k, v, g, dk, dv;
 };
 
 // Rows [from, 128) of a tile in shared memory become zero (all lanes of a warp).
@@ -1408,9 +1409,9 @@ __device__ __forceinline__ void dkv_part(const BwdMaps& maps, const PackedParams
         tc_fence_before();
         mbar_arrive(bar_gfree);
         unsigned char* box = smem + warp * 2 * C::kStage;
-        put_box(o[0], o[1], 1.f, box, &maps.out1, col0, it.part, (int)at, dv + 2 * col0, whole,
+        put_box(o[0], o[1], 1.f, box, &maps.dv, col0, it.part, (int)at, dv + 2 * col0, whole,
                 live);
-        put_box(o2[0], o2[1], p.scale, box + C::kStage, &maps.out0, col0, it.part, (int)at,
+        put_box(o2[0], o2[1], p.scale, box + C::kStage, &maps.dk, col0, it.part, (int)at,
                 dk + 2 * col0, whole, live);
       } else {  // dV for one half of the warps, dK for the other
         tmem_ld32_nowait(half ? tK : tV, o[0]);
@@ -1419,7 +1420,7 @@ __device__ __forceinline__ void dkv_part(const BwdMaps& maps, const PackedParams
         tc_fence_before();
         mbar_arrive(bar_gfree);
         put_box(o[0], o[1], half ? p.scale : 1.f, smem + warp * C::kStage,
-                half ? &maps.out0 : &maps.out1, 0, it.part, (int)at, half ? dk : dv, whole, live);
+                half ? &maps.dk : &maps.dv, 0, it.part, (int)at, half ? dk : dv, whole, live);
       }
       if (lane == 0) {
         stores_read();
@@ -1432,8 +1433,7 @@ __device__ __forceinline__ void dkv_part(const BwdMaps& maps, const PackedParams
 
 template <int D>
 __global__ void __launch_bounds__(384, 1)
-    packed_bwd_kernel(const __grid_constant__ BwdMaps mk, const __grid_constant__ BwdMaps mq,
-                      const PackedParams p) {
+    packed_bwd_kernel(const __grid_constant__ BwdMaps maps, const PackedParams p) {
   using C = Bwd<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -1462,14 +1462,14 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  dkv_part<D>(mk, p, list, smem, tmem);
+  dkv_part<D>(maps, p, list, smem, tmem);
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   list.parts = p.heads;
   list.me = (int)(gridDim.x - 1 - blockIdx.x);  // (the first blocks had the longest items)
-  dq_part<D>(mq, p, list, smem, tmem);
+  dq_part<D>(maps, p, list, smem, tmem);
   tc_fence_before();
   __syncthreads();
   if (warp == 0)
@@ -1522,25 +1522,21 @@ const char* packed_tc_fwd_launch(const PackedParams& p, int sms, cudaStream_t st
 
 const char* packed_tc_bwd_launch(const PackedParams& p, int sms, cudaStream_t stream) {
   const PackedTcKernels k = packed_tc_kernels(p.dim);
-  BwdMaps mq, mk;
-  if (!encode_map(&mq.q, p.q, p.tokens, p.heads, p.dim, p.sq, kTile) ||
-      !encode_map(&mq.g, p.dout, p.tokens, p.heads, p.dim, p.sdo, kTile) ||
-      !encode_map(&mq.k, p.k, p.tokens, p.kv_heads, p.dim, p.sk, kTile) ||
-      !encode_map(&mq.v, p.v, p.tokens, p.kv_heads, p.dim, p.sv, kTile) ||
-      !encode_map(&mq.out0, p.dq, p.tokens, p.heads, p.dim, p.sdq, 32))
+  BwdMaps maps;
+  if (!encode_map(&maps.q, p.q, p.tokens, p.heads, p.dim, p.sq, kTile) ||
+      !encode_map(&maps.k, p.k, p.tokens, p.kv_heads, p.dim, p.sk, kTile) ||
+      !encode_map(&maps.v, p.v, p.tokens, p.kv_heads, p.dim, p.sv, kTile) ||
+      !encode_map(&maps.g, p.dout, p.tokens, p.heads, p.dim, p.sdo, kTile) ||
+      !encode_map(&maps.dk, p.dk, p.tokens, p.kv_heads, p.dim, p.sdk, 32) ||
+      !encode_map(&maps.dv, p.dv, p.tokens, p.kv_heads, p.dim, p.sdv, 32))
     return "tensor map encoding failed";
-  mk = mq;
-  if (!encode_map(&mk.out0, p.dk, p.tokens, p.kv_heads, p.dim, p.sdk, 32) ||
-      !encode_map(&mk.out1, p.dv, p.tokens, p.kv_heads, p.dim, p.sdv, 32))
-    return "tensor map encoding failed";
-  mq.out1 = mq.out0;
   PackedParams pc = p;
   void* dargs[] = {&pc};
   if (cudaLaunchKernel(k.delta, dim3((unsigned)((p.tokens + 7) / 8)), dim3(256), dargs, 0,
                        stream) != cudaSuccess)
     return "launch failed";
   const int64_t levels = p.tokens / kTile + p.batch;
-  void* args[] = {&mk, &mq, &pc};
+  void* args[] = {&maps, &pc};
   if (cudaLaunchKernel(k.bwd, dim3((unsigned)std::min<int64_t>(sms, levels * p.heads)), dim3(384),
                        args, (size_t)k.bwd_smem, stream) != cudaSuccess)
     return "launch failed";
