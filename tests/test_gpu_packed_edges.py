@@ -171,6 +171,61 @@ def test_rows_before_a_nan_against_the_plain_form(D):
     assert float(off[:300].max()) <= 0.0
     assert float((lse.double().cpu() - wlse).abs().max()) <= 1e-5 * (1.0 + float(wlse.abs().max()))
 
+def gradients_with_exact_delta(q, k, v, g, o, G, scale):
+    """dq and dk of one sequence in float64, the bounds of their errors when delta is the weights'
+    sum, and the gradients that delta = dout . o with the rounded o would give.  Relative error
+    of a weight: a score of D products, lse, an exponential.  ds: that, dout . v and delta's sum of
+    such products, and its own rounding to bf16 (2^-8, as the result's).  Beside a row whose
+    one great weight all but cancels in dout . v - delta, o's rounding stands far above these."""
+    D, n = q.shape[2], q.shape[0]
+    q, k, v, g, o = (t.double() for t in (q, k, v, g, o))
+    zero = [torch.zeros_like(q), torch.zeros_like(k)]
+    out = [[t.clone() for t in zero] for _ in range(3)]
+    hide = torch.ones(n, n, dtype=torch.bool).triu(1)
+    for h in range(q.shape[1]):
+        kv = h // G
+        s = scale * (q[:, h] @ k[:, kv].T)
+        lse = torch.logsumexp(s.masked_fill(hide, -math.inf), 1, keepdim=True)
+        p = torch.exp(s - lse).masked_fill(hide, 0.0)
+        dp, gm = g[:, h] @ v[:, kv].T, g[:, h].abs() @ v[:, kv].abs().T
+        delta = (p * dp).sum(1, keepdim=True)
+        rel = EPS * (D * scale * (q[:, h].abs() @ k[:, kv].abs().T) + lse.abs() + 16)
+        ds = p * (dp - delta)
+        e_delta = (p * (D * EPS * gm + dp.abs() * (rel + n * EPS))).sum(1, keepdim=True)
+        e_ds = p * (D * EPS * gm + e_delta + (dp - delta).abs() * rel) + (2.0 ** -8 + n * EPS) * ds.abs()
+        rounded = p * (dp - (g[:, h] * o[:, h]).sum(1, keepdim=True))
+        for to, x, kk, qq in ((out[0], ds, k, q), (out[1], e_ds, k.abs(), q.abs()),
+                              (out[2], rounded, k, q)):
+            to[0][:, h] = scale * (x @ kk[:, kv])
+            to[1][:, kv] += scale * (x.T @ qq[:, h])
+    return out
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[37], [128], [3, 100, 0, 127]])
+def test_gradients_of_first_rows_take_delta_from_the_weights(lens, D):
+    H, KV, T = 4, 2, sum(lens)
+    scale = 1.0 / math.sqrt(D)
+    q, k, v, g = (rnd(i + 20, T, n, D).mul(3.0 if i < 2 else 1.0).to(BF)
+                  for i, n in enumerate((H, KV, KV, H)))
+    ends = [0]
+    for n in lens:
+        ends.append(ends[-1] + n)
+    want, wlse, _, _ = ref.attention(q, k, v, ends, scale)
+    o = want.to(BF)
+    dq, dk, dv = (torch.empty(T, n, D, dtype=BF, device="cuda") for n in (H, KV, KV))
+    rr.rr_attention_packed_bwd(g.cuda(), q.cuda(), k.cuda(), v.cuda(), o.cuda(),
+                               wlse.float().cuda(), i32(ends), dq, dk, dv)
+    seen = [False, False]
+    for a, b in ref.spans(ends, T):
+        exact, bound, rounded = gradients_with_exact_delta(q[a:b], k[a:b], v[a:b], g[a:b], o[a:b],
+                                                           H // KV, scale)
+        for i, got in enumerate((dq, dk)):
+            most = bound[i] + 2.0 ** -8 * exact[i].abs() + 1e-30
+            assert float(((got[a:b].double().cpu() - exact[i]).abs() / most).max()) <= 1.0
+            seen[i] |= bool(((rounded[i] - exact[i]).abs() > 2.0 * most).any())
+    assert seen == [True, True]  # o's rounding would show in either
+
 
 # -------------------------------------------------------- log probabilities ---
 
