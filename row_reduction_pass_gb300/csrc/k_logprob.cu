@@ -9,7 +9,7 @@
 // are kept apart (not their sum) for the gradient: x - m is exact near the maximum, however
 // large the logits are.
 //   dlogits_j = [g (1_{j=t} - p_j) - h p_j (ln p_j + entropy)] / T
-//             = [p_j A + (p_j log2 p_j) B + 1_{j=t} g] / T  with two numbers A, B a row.
+//             = [p_j (A + B log2 p_j) + 1_{j=t} g] / T  with two numbers A, B a row.
 // Both are bound by memory: the forward reads the row once, the backward reads and writes it.
 //
 // The alternatives cost no second pass over the row: each thread's own maximum is known from
@@ -889,14 +889,29 @@ __global__ void __launch_bounds__(kT) logprob_bwd_kernel(const LogprobBwdParams 
   const float g = p.g ? __ldg(p.g + r) : 0.f, h = p.h ? __ldg(p.h + r) : 0.f;
   const float ent = p.h ? __ldg(p.entropy + r) : 0.f;
   const float inv = 1.f / p.temperature, c = p.c;
-  // (the power first and 1 / T last: where p is 0 no factor of a low temperature overflows)
+  // (1 / T comes last: at a low temperature A and B over T may overflow where p is 0)
   const float A = -(g + h * ent), B = -h * kLn2;
   const float ls = __ldg(p.log_sum + r) * kLog2e;
-  auto grad = [&](float x, int64_t j) {
-    if (zero) return 0.f;
-    const float a = max_nan((x - m) * c - ls, kLow);
-    const float e = ex2(a), v = fmaf(e * a, B, e * A);
-    return (j == t ? v + g : v) * inv;
+  // of two neighbours' logits, in place
+  auto grad = [&](float& x0, float& x1, int64_t j) {
+    if (zero) {
+      x0 = x1 = 0.f;
+      return;
+    }
+    float a0, a1, v0, v1;
+    add2(a0, a1, x0, x1, -m, -m);
+    fma2(a0, a1, a0, a1, c, c, -ls, -ls);
+    a0 = max_nan(a0, kLow), a1 = max_nan(a1, kLow);
+    fma2(v0, v1, a0, a1, B, B, A, A);
+    mul2(v0, v1, v0, v1, ex2(a0), ex2(a1));
+    if (j == t) v0 += g;
+    if (j + 1 == t) v1 += g;
+    mul2(x0, x1, v0, v1, inv, inv);
+  };
+  auto grad1 = [&](float x, int64_t j) {
+    float none = m;
+    grad(x, none, j);
+    return x;
   };
   if constexpr (kV) {
     for (int u = 0; u < kU; ++u) {
@@ -906,16 +921,20 @@ __global__ void __launch_bounds__(kT) logprob_bwd_kernel(const LogprobBwdParams 
       if (!zero) v = ld_chunk_stream(cut.chunk(i));
       float f[W];
 #pragma unroll
-      for (int e = 0; e < W; ++e) f[e] = grad(chunk_get<DT>(v, e), cut.head + i * W + e);
+      for (int e = 0; e < W; e += 2) {
+        f[e] = chunk_get<DT>(v, e);
+        f[e + 1] = chunk_get<DT>(v, e + 1);
+        grad(f[e], f[e + 1], cut.head + i * W + e);
+      }
       st_chunk_stream(out + (int64_t)cut.head * E + i * 16, chunk_pack<DT>(f));
     }
     if (seg == 0)
-      each_ragged<DT>(cut, tid, [&](float x, int64_t j) { st_elem<DT>(out + j * E, grad(x, j)); });
+      each_ragged<DT>(cut, tid, [&](float x, int64_t j) { st_elem<DT>(out + j * E, grad1(x, j)); });
   } else {
     for (int u = 0; u < kU * W; ++u) {
       const int64_t j = ((int64_t)seg * kU * W + u) * kT + tid;
       if (j >= p.cols) break;
-      st_elem<DT>(out + j * E, grad(zero ? 0.f : ld_elem<DT>(cut.row + j * E), j));
+      st_elem<DT>(out + j * E, grad1(zero ? 0.f : ld_elem<DT>(cut.row + j * E), j));
     }
   }
 }

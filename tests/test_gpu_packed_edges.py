@@ -259,3 +259,23 @@ def test_logprob_gradient_at_extreme_temperatures(T, dtype):
         close = (d.double().cpu() - want).abs() <= (64 * EPS * mag + HALF[dtype] * want.abs()
                                                     + 2.0 ** -126 + 2.0 ** -117 / T)
         assert bool(close.all()), (int((~close).sum()), d.cpu()[~close][:4], want[~close][:4])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_logprob_gradient_of_tokens_out_of_range_adds_nothing_anywhere(pad, dtype):
+    """Tokens just below 0 and from the row's end on, with ragged rows and an output that starts at
+    another alignment: only the probabilities' part."""
+    rows, cols = 8, 133
+    x = rnd(6, rows, cols).to(dtype)
+    tok = torch.tensor([-1, -2, -3, -2 ** 31, cols, cols + 1, 2 ** 31 - 1, 132])
+    g, h = rnd(7, rows), rnd(8, rows)
+    f = {n: torch.empty(rows, device="cuda") for n in ("logprob", "entropy", "row_max", "log_sum")}
+    xd, td = x.cuda(), tok.int().cuda()
+    rr.rr_token_logprob_fwd(xd, td, **f)
+    d = torch.empty(pad + rows * cols, dtype=dtype, device="cuda")[pad:].view(rows, cols)
+    rr.rr_token_logprob_bwd(xd, td, f["row_max"], f["log_sum"], g.cuda(), d, entropy=f["entropy"],
+                            grad_entropy=h.cuda())
+    want, mag = ref.logprob_bwd(x, tok, g, h, 1.0)
+    assert bool(((d.double().cpu() - want).abs() <= 64 * EPS * mag + HALF[dtype] * want.abs()
+                 + 1e-30).all())
