@@ -457,8 +457,8 @@ rr_status rr_draft_verify(const void *target_logits, const void *draft_logits,
  *   positions : [tokens] int32 row of the table, or NULL (the token's index).
  *   bad_position_count : nullable device int32; each token with a position >=
  *           max_positions adds 1, and its rotated elements are NaN.
- *   head_dim even, at most 256; rot_dim even, 2 .. head_dim; at most 65535 heads;
- *   eps >= 0 and finite.
+ *   head_dim even, at most 256; rot_dim even, 2 .. head_dim; at most 65535 heads; tokens
+ *   below 2^31, strides at most 2^28 elements; eps >= 0 and finite.
  * A token with a negative position (padding) gets zeros, and so does a head whose mean
  * square is not finite, or zero with eps == 0.
  */
@@ -519,10 +519,15 @@ rr_status rr_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void
  *           sequence are left as they were.
  *   lse : [heads x tokens] float32, or NULL.
  *   head_dim at most 256; heads a multiple of kv_heads, at most 65535; batch at most
- *   2^20, tokens below 2^31; scale > 0 and finite.  |scale q . k| below 2^30.
+ *   2^20, tokens below 2^31 - 4096, tokens x heads at most 2^32, (tokens / 128 + batch) x
+ *   heads at most 2^31, strides at most 2^28 elements; scale > 0 and finite.
+ *   |scale q . k| below 2^30, and the sum of a sequence's |v| within float32.
  * bf16 with head_dim 64 or 128 runs on the tensor cores (fp32 accumulate; weights rounded
  * to bf16 for their product with v); other head dimensions and float32 on plain kernels.
- * What stands at unseen tokens (NaN or infinities too) changes nothing.
+ * What stands at unseen tokens (NaN or infinities too) changes nothing; a NaN or infinity that
+ * a token sees makes its output's element such.  Neither costs time in rows of no sequence; a
+ * NaN in a sequence costs its tiles' reading again, and up to 127 tokens before it are computed
+ * again by the slower arithmetic of the plain kernels.
  */
 rr_status rr_attention_packed_fwd(const void *q, const void *k, const void *v,
                                   const int32_t *cu_seqlens, void *o, float *lse, int64_t tokens,
@@ -585,7 +590,9 @@ rr_status rr_attention_packed_bwd(const void *dout, const void *q, const void *k
  *           ignored) adds 1; such a row gets logprob NaN and rank -1.
  * Columns of -inf are not listed; places of the list that are left get index -1 and
  * -inf.  A row of nothing but -inf gets logprob, entropy and log_sum 0, row_max -inf and an
- * empty list.  A row with a NaN or +inf gets NaN, rank -1 and top_index -1.
+ * empty list.  A row with a NaN or +inf gets NaN, rank -1 and top_index -1.  A row whose list
+ * ends among hundreds of equal columns (a vocabulary masked with a finite value that leaves
+ * fewer than k columns) takes k more passes over it: mask with -inf.
  */
 rr_status rr_token_logprob_fwd(const void *logits, const int32_t *tokens, float *logprob,
                                float *entropy, float *row_max, float *log_sum, int32_t *rank,
@@ -603,7 +610,7 @@ rr_status rr_token_logprob_fwd(const void *logits, const int32_t *tokens, float 
  *   dlogits : [rows x cols] dtype, rows dlogits_stride apart; may be logits, with the
  *           same stride (written in place); other overlap is an error.
  * A row whose token is ignore_index, or of nothing but -inf, gets 0.  A token outside
- * [0, cols) adds no 1_{j=t}.
+ * [0, cols) adds no 1_{j=t}.  rows x ceil(a row's bytes / 16384) below 2^31.
  */
 rr_status rr_token_logprob_bwd(const void *logits, const int32_t *tokens, const float *row_max,
                                const float *log_sum, const float *entropy,

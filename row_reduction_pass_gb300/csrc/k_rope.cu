@@ -28,7 +28,8 @@ constexpr int kThreads = 256;
 // under way, which cost registers.  16384 tokens, bf16, 32 + 8 heads of 128 read and written by
 // the forward: 60 us with 2 and 3, 5690 GB/s (2 and 4: 70, 3 and 3: 66, 1 and 5: 87; each row's
 // loads issued before the one before it is worked on, 83); backward 103 us, 4960 GB/s, with 2
-// and 2 (2 and 3: 137, 3 and 2: 113; likewise 149).
+// and 2 (2 and 3: 137, 3 and 2: 113; likewise 149).  The bf16 kernels as they are keep 44 and 58
+// bytes a thread in local memory; copies into shared memory were not tried.
 constexpr int kFwdU = 2, kBwdU = 2, kFwdBlocks = 3, kBwdBlocks = 2;
 
 // What a lane keeps of the row's layout: element offsets of its slots.

@@ -2393,6 +2393,11 @@ struct RopePlan {
   bool vec;
   int sms;
 };
+// Two chunks of 16 bytes a lane where the rotated elements and the others are whole pairs of
+// chunks and everything is aligned; else element by element.  16384 tokens, 32 + 8 heads, flushed
+// cache: bf16, head_dim 128 68 us by chunks, 224 by elements (rows an odd number of elements
+// apart), gradient 112 and 517; head_dim 80, all or (elements) 40 of it rotated, 61 and 226,
+// gradient 104 and 470; fp32, 128, 118 and 226, gradient 176 and 390.
 rr_status rope_plan(rr::RopeParams& p, rr_dtype dt, float eps, const int64_t* strides, int n,
                     const void* const* tensors, RopePlan* out) {
   const int E = dt == RR_BF16 ? 2 : 4, W = 16 / E;
@@ -2418,7 +2423,9 @@ rr_status rope_plan(rr::RopeParams& p, rr_dtype dt, float eps, const int64_t* st
   p.inv_dim = 1.f / (float)p.dim;
   return RR_OK;
 }
-// Cuts each token's queries and keys into units until `warps` have one.
+// Cuts each token's queries and keys into units until `warps` have one.  32 + 8 heads of 128 bf16,
+// flushed cache: 16 tokens 9.4 us, whole tokens 13.5 (gradient 13.5 and 19.6); 400 tokens 11.4 and
+// 13.5 (17.6 and 20.6); 1000 tokens 14.5 either way.
 void rope_units(rr::RopeParams& p, int64_t warps) {
   const int per = 32 / p.group;
   const int64_t want = std::max<int64_t>(1, cdiv(warps, p.tokens));  // units a token
@@ -2998,7 +3005,8 @@ rr_status rr_token_logprob_bwd(const void* logits, const int32_t* tokens, const 
   p.segs = (int32_t)cdiv(cols * E, lk.bwd_bytes);
   if (rows > INT32_MAX / p.segs)
     return fail(RR_ERR_INVALID_ARG, "too many rows for this many columns");
-  // chunks of both tensors start at the same columns in every row
+  // chunks of both tensors start at the same columns in every row; else element by element (8192 x
+  // 50304 bf16, flushed cache: 298 and 765 us; 4096 x 50304 fp32: 276 and 433)
   const bool vec = ((reinterpret_cast<uintptr_t>(logits) ^ reinterpret_cast<uintptr_t>(dlogits)) &
                     15) == 0 &&
                    (logits_stride - dlogits_stride) * E % 16 == 0;
