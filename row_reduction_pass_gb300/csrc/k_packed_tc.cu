@@ -16,12 +16,17 @@
 // loads V, warps 9 and 10 issue S and O += P V.
 //
 // Work.  An item is a level of a sequence (a tile of 128 queries) with one head; its cost is the
-// level.  Sequence lengths are known on the device only, so each block sorts the (at most 128)
+// level.  Sequence lengths are known on the device only, so each block sorts the (at most 128 live)
 // sequences by their length and finds its items in the list of all levels, longest first, that
-// the blocks are dealt in a zigzag.  More sequences are taken in their own order, each item
-// found by a search of the bounds in global memory: 128 sequences of 50 tokens 87 us, with an
-// empty one more 113 (gradient 274, 308); of 8 to 1200 tokens 278 and 335 (922, 1252); 120 of 60
-// before 8 of 3000 568 and 599 (2052, 2202); 32 heads on 8, head_dim 128, flushed caches.
+// the blocks are dealt in a zigzag.  More are taken in their own order, each item found by a
+// search of the bounds in global memory: 128 sequences of 50 tokens 79 us, with one of one token
+// more 110 (gradient 265, 310); of 8 to 1200 tokens 261 and 325 (904, 1320); 120 of 60 before 8 of
+// 3000 558 and 597 (2046, 2259); 32 heads on 8, head_dim 128, flushed caches.  Batches of up to 128
+// sequences have kernels of their own, without that search (247 instead of 253 us above).  Batches
+// padded with empty ones: the live ones among up to kLooked are gathered and sorted (10 of 200
+// tokens 26 us, with 1000 empty ones 30, with 4000 34; by skipping them 37 to 42 and 38 to 48, with
+// 16000 40 to 56), else a lookup that finds none goes on over half or more of those that follow
+// (60000: 42 to 56; one lookup each: 16000).
 //
 // A tile's rows beyond its sequence (the next one's, or past the buffer, which read as zero)
 // are not stored, and keys beyond a row's own are masked in S.  Their V has weight 0, which a
@@ -43,7 +48,8 @@ namespace {
 
 constexpr int kTile = 128;           // query rows and keys of a tile
 constexpr int kBox = kTile * 128;    // bytes of 128 rows x 64 columns
-constexpr int kSorted = 128;         // sequences that a block sorts
+constexpr int kSorted = 128;         // live sequences that a block sorts
+constexpr int kLooked = 8192;        // sequences among which it looks for them
 
 // TMA box [128 tokens x 1 head x 64 columns] at {column, head, token}.
 __device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int col, int head,
@@ -84,18 +90,21 @@ struct Item {
   int level, part;
   bool ok;
 };
+// kMany: more than kSorted sequences, some of which may be empty.
+template <bool kMany>
 struct Sequences {
   int2* seq;       // shared: (begin, length) of the live sequences, longest first
   const int* cu;
   int n, batch, tokens, rows, parts, entries, me;
   int lv[kSorted / 32];  // levels of sequences lane, lane + 32, ...
-  bool sorted;
+  bool sorted_;
 
+  __device__ __forceinline__ bool sorted() const { return !kMany || sorted_; }
   __device__ __forceinline__ int2 bounds(int b) const {
     const int a = min(max(__ldg(cu + b), 0), tokens), e = min(max(__ldg(cu + b + 1), 0), tokens);
     return make_int2(a, max(e - a, 0));
   }
-  // All threads of the block; `tmp` is shared room for kSorted int2.
+  // All threads of the block; `tmp` is shared room for kSorted int2 and a word a warp.
   __device__ __forceinline__ void init(int2* s, int2* tmp, const PackedParams& p, int rows_,
                                        int parts_) {
     seq = s;
@@ -105,15 +114,39 @@ struct Sequences {
     rows = rows_;
     parts = parts_;
     me = (int)blockIdx.x;
-    sorted = batch <= kSorted;
     const int tid = threadIdx.x, lane = tid & 31;
     int2 mine = make_int2(0, 0);
-    if (sorted && tid < batch) tmp[tid] = mine = bounds(tid);
-    n = __syncthreads_count(mine.y > 0);
-    if (sorted && mine.y > 0) {
+    int room = batch;  // of tmp
+    if constexpr (!kMany) {
+      if (tid < batch) tmp[tid] = mine = bounds(tid);
+      n = __syncthreads_count(mine.y > 0);
+    } else if (batch <= kLooked) {  // the live ones, in order, as long as there is room
+      int* counts = reinterpret_cast<int*>(tmp + kSorted);
+      n = 0;
+      for (int b0 = 0; b0 < batch && n <= kSorted; b0 += (int)blockDim.x) {
+        const int2 s = b0 + tid < batch ? bounds(b0 + tid) : make_int2(0, 0);
+        const uint32_t live = __ballot_sync(0xffffffffu, s.y > 0);
+        if (lane == 0) counts[tid >> 5] = __popc(live);
+        __syncthreads();
+        int at = n + __popc(live & ((1u << lane) - 1u));
+        for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+          const int c = counts[w];
+          at += w < tid >> 5 ? c : 0;
+          n += c;
+        }
+        if (s.y > 0 && at < kSorted) tmp[at] = s;
+        __syncthreads();
+      }
+      room = n;
+      if (tid < min(n, kSorted)) mine = tmp[tid];
+    } else {
+      n = kSorted + 1;
+    }
+    sorted_ = n <= kSorted;
+    if (sorted() && mine.y > 0) {
       const int l = (mine.y + rows - 1) / rows;
       int at = 0;
-      for (int b = 0; b < batch; ++b) {
+      for (int b = 0; b < room; ++b) {
         const int o = (tmp[b].y + rows - 1) / rows;
         at += o > l || (o == l && b < tid);
       }
@@ -124,11 +157,11 @@ struct Sequences {
 #pragma unroll
     for (int k = 0; k < kSorted / 32; ++k) {
       const int b = lane + 32 * k;
-      lv[k] = sorted && b < n ? (seq[b].y + rows - 1) / rows : 0;
+      lv[k] = sorted() && b < n ? (seq[b].y + rows - 1) / rows : 0;
       sum += lv[k];
     }
     // unsorted: entry floor(begin / rows) + b + level, some of which are none
-    entries = sorted ? __reduce_add_sync(0xffffffffu, sum) : tokens / rows + batch;
+    entries = sorted() ? __reduce_add_sync(0xffffffffu, sum) : tokens / rows + batch;
   }
   // levels at or above l, over all sequences
   __device__ __forceinline__ int above(int l) const {
@@ -137,16 +170,15 @@ struct Sequences {
     for (int k = 0; k < kSorted / 32; ++k) s += max(lv[k] - l, 0);
     return __reduce_add_sync(0xffffffffu, s);
   }
-  // The r-th item of this block (all lanes of a warp); more: whether r is within the list.
+  // The r-th item of this block (all lanes of a warp); more: whether r is within the list.  Where it
+  // is none (unsorted only), the next one is not before place `part`.
   __device__ __forceinline__ Item get(int r, bool& more) const {
-    const int nb = (int)gridDim.x;
-    const int64_t i = (int64_t)r * nb + ((r & 1) ? nb - 1 - me : me);
-    const int64_t u64 = i / parts;
-    Item it{0, 0, 0, (int)(i - u64 * parts), false};
-    more = u64 < entries;
+    const uint32_t nb = gridDim.x, i = r * nb + ((r & 1) ? nb - 1 - me : me);  // (entries x parts <=
+    const int u = (int)(i / (uint32_t)parts);                                  // 2^31)
+    Item it{0, 0, 0, (int)(i - (uint32_t)u * parts), false};
+    more = u < entries;
     if (!more) return it;
-    const int u = (int)u64;
-    if (sorted) {
+    if (sorted()) {
       int lo = 0, hi = (seq[0].y + rows - 1) / rows;  // above(lo) > u >= above(hi)
       int at_hi = 0;
       while (hi - lo > 1) {
@@ -169,6 +201,15 @@ struct Sequences {
       const int2 s = bounds(lo);
       it.beg = s.x, it.len = s.y, it.level = u - s.x / rows - lo;
       it.ok = it.level >= 0 && it.level * rows < it.len;
+      if (!it.ok) {
+        // none: on over half or more of the empty sequences that follow (those before a bound that
+        // is this one's end), a lane looking 2^lane of them ahead
+        const int b = min(lo + 1 + (1 << min((int)threadIdx.x & 31, 21)), batch);  // (batch <= 2^20)
+        const bool same = min(max(__ldg(cu + b), 0), tokens) <= s.x + s.y;
+        const int far = __popc(__ballot_sync(0xffffffffu, same));
+        const int next = min(lo + 1 + (far ? 1 << min(far - 1, 21) : 0), batch);
+        it.part = (int)((uint32_t)((s.x + s.y) / rows + next) * parts / nb);
+      }
     }
     return it;
   }
@@ -359,14 +400,14 @@ __device__ __forceinline__ int reached_rows(const PackedParams& p, const Item& i
 }
 
 // All threads of the block, when its roles have ended and what they stored is in place.
-template <int D>
+template <int D, bool kMany>
 __device__ __noinline__ void repair_items(const PackedParams& p, const uint32_t* flags,
                                           unsigned char* smem) {
   constexpr int NW = 12;
   __shared__ int rows[NW];
   const int warp = threadIdx.x >> 5;
   float* sq = reinterpret_cast<float*>(smem) + warp * D;
-  Sequences list;
+  Sequences<kMany> list;
   list.init(reinterpret_cast<int2*>(smem + NW * D * 4),
             reinterpret_cast<int2*>(smem + NW * D * 4) + kSorted, p, kTile, p.heads);
   for (int r0 = 0;; r0 += NW) {  // a warp an item
@@ -401,7 +442,7 @@ __device__ __forceinline__ void issue_tiles(uint32_t d, uint32_t a, uint32_t b, 
     mma_ss(d, sw128_desc(a + off, 16, 1024), sw128_desc(b + off, 16, 1024), idesc, kk > 0 ? 1u : 0u);
   }
 }
-template <int D>
+template <int D, bool kMany>
 __global__ void __launch_bounds__(384, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
@@ -439,7 +480,7 @@ __global__ void __launch_bounds__(384, 1)
   }
   uint32_t* flags = reinterpret_cast<uint32_t*>(smem + C::kOffFlags);
   if (tid <= kFlagged / 32) flags[tid] = 0;
-  Sequences list;
+  Sequences<kMany> list;
   list.init(reinterpret_cast<int2*>(smem + C::kOffSeq), reinterpret_cast<int2*>(smem + C::kOffStage),
             p, kTile, p.heads);
   tc_fence_before();
@@ -466,6 +507,7 @@ __global__ void __launch_bounds__(384, 1)
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
+      if (!it.ok) r = max(r, it.part - 1);
       if (!it.ok || lane != 0) continue;
       const int h = it.part;
       if (keys) {
@@ -496,6 +538,7 @@ __global__ void __launch_bounds__(384, 1)
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
+      if (!it.ok) r = max(r, it.part - 1);
       if (!it.ok || lane != 0) continue;
       wait_spin(bar_q, (uint32_t)(items++ & 1), dead, p.err);
       for (int t = 0; t <= it.level; ++t) {
@@ -524,6 +567,7 @@ __global__ void __launch_bounds__(384, 1)
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
+      if (!it.ok) r = max(r, it.part - 1);
       if (!it.ok || lane != 0) continue;
       for (int t = 0; t <= it.level; ++t) {
         const int s = n & 1;
@@ -579,7 +623,10 @@ __global__ void __launch_bounds__(384, 1)
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
-      if (!it.ok) continue;
+      if (!it.ok) {
+        r = max(r, it.part - 1);
+        continue;
+      }
       const int h = it.part, q0 = it.level * kTile;
       float m = -INFINITY, l = 0.f;  // for all keys; of this thread's
       for (int t = 0; t <= it.level; ++t) {
@@ -700,7 +747,7 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
                  : "memory");
-  if (flags[kFlagged / 32]) repair_items<D>(p, flags, smem + C::kOffStage);
+  if (flags[kFlagged / 32]) repair_items<D, kMany>(p, flags, smem + C::kOffStage);
 }
 
 // ------------------------------------------------------------------ backward ---
@@ -801,9 +848,9 @@ __global__ void __launch_bounds__(256) packed_delta_kernel(const PackedParams p)
   }
 }
 
-template <int D>
+template <int D, class List>
 __device__ __forceinline__ void dq_part(const BwdMaps& maps, const PackedParams& p,
-                                        const Sequences& list, unsigned char* smem,
+                                        const List& list, unsigned char* smem,
                                         uint32_t tmem) {
   using C = Bwd<D>;
   constexpr int T = C::kTileBytes;
@@ -840,6 +887,7 @@ __device__ __forceinline__ void dq_part(const BwdMaps& maps, const PackedParams&
     for (int r = 1; more; ++r) {
       const Item it = nx;
       nx = list.get(r, more);
+      if (!it.ok) r = max(r, it.part - 1);
       if (!it.ok || lane != 0) continue;
       const int h = it.part;
       if (keys) {
@@ -882,6 +930,7 @@ __device__ __forceinline__ void dq_part(const BwdMaps& maps, const PackedParams&
     for (int r = 1; more; ++r) {
       const Item it = nx;
       nx = list.get(r, more);
+      if (!it.ok) r = max(r, it.part - 1);
       if (!it.ok || lane != 0) continue;
       wait_spin(bar_q, (uint32_t)(items++ & 1), dead, p.err);
       for (int t = 0; t <= it.level; ++t) {
@@ -917,7 +966,10 @@ __device__ __forceinline__ void dq_part(const BwdMaps& maps, const PackedParams&
     for (int r = 1; more; ++r) {
       const Item it = nx;
       nx = list.get(r, more);
-      if (!it.ok) continue;
+      if (!it.ok) {
+        r = max(r, it.part - 1);
+        continue;
+      }
       for (int t = 0; t <= it.level; ++t) {
         const int s = n & 1, rest = it.len - t * kTile;
         if (lane == 0) wait_spin(&bar_kfull[ks], kph, dead, p.err);
@@ -1000,7 +1052,10 @@ __device__ __forceinline__ void dq_part(const BwdMaps& maps, const PackedParams&
       float nd = nd_next;
       nx = list.get(r, more);
       load_stats(nx);
-      if (!it.ok) continue;
+      if (!it.ok) {
+        r = max(r, it.part - 1);
+        continue;
+      }
       for (int t = 0; t <= it.level; ++t, ++n) {
         uint32_t v[2][32], w[2][32];
         const int s = n & 1;
@@ -1081,9 +1136,9 @@ __device__ __forceinline__ void dq_part(const BwdMaps& maps, const PackedParams&
   }
 }
 
-template <int D>
+template <int D, class List>
 __device__ __forceinline__ void dkv_part(const BwdMaps& maps, const PackedParams& p,
-                                         const Sequences& list, unsigned char* smem,
+                                         const List& list, unsigned char* smem,
                                          uint32_t tmem) {
   using C = Bwd<D>;
   constexpr int T = C::kTileBytes;
@@ -1118,7 +1173,10 @@ __device__ __forceinline__ void dkv_part(const BwdMaps& maps, const PackedParams
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
-      if (!it.ok) continue;
+      if (!it.ok) {
+        r = max(r, it.part - 1);
+        continue;
+      }
       const int first = first_of(it);
       if (lane == 0) {
         if (items > 0) wait_spin(bar_kvfree, (uint32_t)((items - 1) & 1), dead, p.err);
@@ -1179,6 +1237,7 @@ __device__ __forceinline__ void dkv_part(const BwdMaps& maps, const PackedParams
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
+      if (!it.ok) r = max(r, it.part - 1);
       if (!it.ok || lane != 0) continue;
       const int tiles = group * (it.level + 1);
       wait_spin(bar_kv, (uint32_t)(items++ & 1), dead, p.err);
@@ -1210,7 +1269,10 @@ __device__ __forceinline__ void dkv_part(const BwdMaps& maps, const PackedParams
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
-      if (!it.ok) continue;
+      if (!it.ok) {
+        r = max(r, it.part - 1);
+        continue;
+      }
       const int first = first_of(it), tiles = group * (it.level + 1);
       for (int t = 0, i = first; t < tiles; ++t, i = i == first + it.level ? first : i + 1) {
         const int s = n & 1, rest = it.len - i * kTile;
@@ -1278,7 +1340,10 @@ __device__ __forceinline__ void dkv_part(const BwdMaps& maps, const PackedParams
     for (int r = 0;; ++r) {
       const Item it = list.get(r, more);
       if (!more) break;
-      if (!it.ok) continue;
+      if (!it.ok) {
+        r = max(r, it.part - 1);
+        continue;
+      }
       const int first = first_of(it), tiles = group * (it.level + 1);
       for (int t = 0, i = first; t < tiles; ++t, ++n, i = i == first + it.level ? first : i + 1) {
         const int s = n & 1;
@@ -1434,7 +1499,7 @@ __device__ __forceinline__ void dkv_part(const BwdMaps& maps, const PackedParams
   }
 }
 
-template <int D>
+template <int D, bool kMany>
 __global__ void __launch_bounds__(384, 1)
     packed_bwd_kernel(const __grid_constant__ BwdMaps maps, const PackedParams p) {
   using C = Bwd<D>;
@@ -1457,7 +1522,7 @@ __global__ void __launch_bounds__(384, 1)
     for (int i = 0; i < 21; ++i) mbar_init(bars_q + i, i >= 3 && i < 7 ? 256 : 1);
     fence_mbar_init();
   }
-  Sequences list;
+  Sequences<kMany> list;
   list.init(reinterpret_cast<int2*>(smem + C::kOffSeq), reinterpret_cast<int2*>(smem), p, kTile,
             p.kv_heads);
   fence_proxy_async_smem();  // (the list's scratch lies where copies will land)
@@ -1497,17 +1562,21 @@ bool encode_map(CUtensorMap* map, const char* base, int64_t tokens, int heads, i
 
 }  // namespace
 
-template <int D>
+template <int D, bool kMany>
 static PackedTcKernels tc_kernels() {
-  return PackedTcKernels{(const void*)packed_fwd_kernel<D>, (const void*)packed_delta_kernel<D>,
-                         (const void*)packed_bwd_kernel<D>, Fwd<D>::kSmem, Bwd<D>::kSmem};
+  return PackedTcKernels{(const void*)packed_fwd_kernel<D, kMany>,
+                         (const void*)packed_delta_kernel<D>,
+                         (const void*)packed_bwd_kernel<D, kMany>, Fwd<D>::kSmem, Bwd<D>::kSmem};
 }
-PackedTcKernels packed_tc_kernels(int d) {
-  return d == 64 ? tc_kernels<64>() : d == 128 ? tc_kernels<128>() : PackedTcKernels{};
+PackedTcKernels packed_tc_kernels(int d, int64_t batch) {
+  const bool many = batch > kSorted;
+  return d == 64    ? many ? tc_kernels<64, true>() : tc_kernels<64, false>()
+         : d == 128 ? many ? tc_kernels<128, true>() : tc_kernels<128, false>()
+                    : PackedTcKernels{};
 }
 
 const char* packed_tc_fwd_launch(const PackedParams& p, int sms, cudaStream_t stream) {
-  const PackedTcKernels k = packed_tc_kernels(p.dim);
+  const PackedTcKernels k = packed_tc_kernels(p.dim, p.batch);
   CUtensorMap maps[4];
   if (!encode_map(&maps[0], p.q, p.tokens, p.heads, p.dim, p.sq, kTile) ||
       !encode_map(&maps[1], p.k, p.tokens, p.kv_heads, p.dim, p.sk, kTile) ||
@@ -1524,7 +1593,7 @@ const char* packed_tc_fwd_launch(const PackedParams& p, int sms, cudaStream_t st
 }
 
 const char* packed_tc_bwd_launch(const PackedParams& p, int sms, cudaStream_t stream) {
-  const PackedTcKernels k = packed_tc_kernels(p.dim);
+  const PackedTcKernels k = packed_tc_kernels(p.dim, p.batch);
   BwdMaps maps;
   if (!encode_map(&maps.q, p.q, p.tokens, p.heads, p.dim, p.sq, kTile) ||
       !encode_map(&maps.k, p.k, p.tokens, p.kv_heads, p.dim, p.sk, kTile) ||

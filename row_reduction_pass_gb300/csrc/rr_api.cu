@@ -2738,7 +2738,7 @@ rr_status rr_attention_packed_fwd(const void* q, const void* k, const void* v,
   p.dim = (int32_t)head_dim;
   p.scale = scale;
   p.scale_log2 = scale * rr::kLog2e;
-  const rr::PackedTcKernels tk = rr::packed_tc_kernels(dtype == RR_BF16 ? p.dim : 0);
+  const rr::PackedTcKernels tk = rr::packed_tc_kernels(dtype == RR_BF16 ? p.dim : 0, batch);
   if (tk.fwd) {
     int sms = 0;
     {
@@ -2827,7 +2827,7 @@ rr_status rr_attention_packed_bwd(const void* dout, const void* q, const void* k
   p.dim = (int32_t)head_dim;
   p.scale = scale;
   p.scale_log2 = scale * rr::kLog2e;
-  const rr::PackedTcKernels tk = rr::packed_tc_kernels(dtype == RR_BF16 ? p.dim : 0);
+  const rr::PackedTcKernels tk = rr::packed_tc_kernels(dtype == RR_BF16 ? p.dim : 0, batch);
   if (tk.bwd) {
     int sms = 0;
     {

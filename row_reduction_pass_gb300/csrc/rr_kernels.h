@@ -405,7 +405,7 @@ struct PackedTcKernels {
   int fwd_smem, bwd_smem;
 };
 // Tensor-core kernels for bf16 of this head dimension; fwd null where there are none.
-PackedTcKernels packed_tc_kernels(int d);
+PackedTcKernels packed_tc_kernels(int d, int64_t batch);
 // Encodes the tensor maps and launches: null on success, else a short reason.
 const char* packed_tc_fwd_launch(const PackedParams& p, int sms, cudaStream_t stream);
 const char* packed_tc_bwd_launch(const PackedParams& p, int sms, cudaStream_t stream);

@@ -279,3 +279,48 @@ def test_logprob_gradient_of_tokens_out_of_range_adds_nothing_anywhere(pad, dtyp
     want, mag = ref.logprob_bwd(x, tok, g, h, 1.0)
     assert bool(((d.double().cpu() - want).abs() <= 64 * EPS * mag + HALF[dtype] * want.abs()
                  + 1e-30).all())
+
+
+# --------------------------------------------------- batches padded with empty ones ---
+
+def padded(lens, place, empty):
+    """`empty` sequences of no tokens among `lens`: before, between or behind them."""
+    if place == "behind":
+        return lens + [0] * empty
+    if place == "before":
+        return [0] * empty + lens
+    each = empty // len(lens)
+    return sum(([n] + [0] * each for n in lens), [])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("place", ["behind", "before", "between"])
+@pytest.mark.parametrize("live,empty", [(1, 128), (7, 3000), (128, 1280), (129, 1290), (200, 20000),
+                                        (3, 30000)])
+def test_empty_sequences_change_nothing(live, empty, place, D):
+    """Any number of empty sequences anywhere: the same bits."""
+    lens = [1 + (37 * i + 11 * live) % 290 for i in range(live)]
+    T, H, KV = sum(lens), 4, 2
+    q, k, v, g = (rnd(i, T, n, D, dtype=BF).cuda() for i, n in enumerate((H, KV, KV, H)))
+    got = []
+    for pad in (lens, padded(lens, place, empty)):
+        cu = torch.zeros(len(pad) + 1, dtype=torch.int32)
+        cu[1:] = torch.tensor(pad).cumsum(0)
+        o, lse = attend(q, k, v, cu.cuda())
+        d = [torch.full_like(x, 7.0) for x in (q, k, v)]
+        rr.rr_attention_packed_bwd(g, q, k, v, o, lse, cu.cuda(), *d)
+        got.append([o, lse] + d)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert rr.rr_read_device_error(0) == 0
+
+
+def test_nothing_but_empty_sequences():
+    q = torch.zeros(5, 2, 64, dtype=BF, device="cuda")
+    for batch in (1, 128, 129, 400, 20000):
+        o, lse = attend(q, q, q, torch.full((batch + 1,), 3, dtype=torch.int32, device="cuda"))
+        d = [torch.full_like(q, 7.0) for _ in range(3)]
+        rr.rr_attention_packed_bwd(q, q, q, q, o, lse,
+                                   torch.full((batch + 1,), 5, dtype=torch.int32, device="cuda"), *d)
+        assert bool((o == 7.0).all()) and bool((lse == 7.0).all())
+        assert all(bool((x == 7.0).all()) for x in d)
+    assert rr.rr_read_device_error(0) == 0
