@@ -161,7 +161,10 @@ struct Sequences {
       sum += lv[k];
     }
     // unsorted: entry floor(begin / rows) + b + level, some of which are none
-    entries = sorted() ? __reduce_add_sync(0xffffffffu, sum) : tokens / rows + batch;
+    // (not more than 2^31 items, which 32 bits count: of bounds that decrease there could be)
+    entries = sorted() ? (int)min((uint32_t)__reduce_add_sync(0xffffffffu, sum),
+                                  0x80000000u / (uint32_t)p.heads)
+                       : tokens / rows + batch;
   }
   // levels at or above l, over all sequences
   __device__ __forceinline__ int above(int l) const {
@@ -173,8 +176,8 @@ struct Sequences {
   // The r-th item of this block (all lanes of a warp); more: whether r is within the list.  Where it
   // is none (unsorted only), the next one is not before place `part`.
   __device__ __forceinline__ Item get(int r, bool& more) const {
-    const uint32_t nb = gridDim.x, i = r * nb + ((r & 1) ? nb - 1 - me : me);  // (entries x parts <=
-    const int u = (int)(i / (uint32_t)parts);                                  // 2^31)
+    const uint32_t nb = gridDim.x, i = r * nb + ((r & 1) ? nb - 1 - me : me);
+    const int u = (int)(i / (uint32_t)parts);
     Item it{0, 0, 0, (int)(i - (uint32_t)u * parts), false};
     more = u < entries;
     if (!more) return it;

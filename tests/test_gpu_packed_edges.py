@@ -324,3 +324,21 @@ def test_nothing_but_empty_sequences():
         assert bool((o == 7.0).all()) and bool((lse == 7.0).all())
         assert all(bool((x == 7.0).all()) for x in d)
     assert rr.rr_read_device_error(0) == 0
+
+
+@pytest.mark.parametrize("batch", [100, 300])
+def test_decreasing_bounds_end_and_stay_inside(batch):
+    """Results are not specified, but the calls end, and nothing around the tensors is written."""
+    g = torch.Generator().manual_seed(batch)
+    T, H = 500, 2
+    cu = torch.randint(-20, 600, (batch + 1,), generator=g).int().cuda()
+    raw = [torch.full((T + 200, H, 64), 7.0, dtype=BF, device="cuda") for _ in range(5)]
+    q, o, dq, dk, dv = (t[100:100 + T] for t in raw)
+    q.copy_(rnd(1, T, H, 64, dtype=BF))
+    lse = torch.zeros(H, T, device="cuda")
+    rr.rr_attention_packed_fwd(q, q, q, cu, o, lse=lse)
+    rr.rr_attention_packed_bwd(q, q, q, q, o, lse, cu, dq, dk, dv)
+    torch.cuda.synchronize()
+    for t in raw:
+        assert bool((t[:100] == 7.0).all()) and bool((t[100 + T:] == 7.0).all())
+    assert rr.rr_read_device_error(0) == 0
